@@ -26,6 +26,13 @@
  * KV cache layout (both K and V): [num_blocks][num_kv_heads][block_size][head_dim]
  * of kv_dtype.  Slot s addresses token row s % block_size of physical block
  * s / block_size (Lecture 33 §2.2: base + block * block_stride + offset * token_stride).
+ *
+ * 4-bit KV cache (kv_dtype PKV_FP4_E2M1): [num_blocks][num_kv_heads][block_size / 16][tile], a
+ * tile being 16 rows in 9 * head_dim bytes.  First the codes, [16][head_dim / 2] bytes: element
+ * 2j of a row is the low nibble of its byte j, element 2j + 1 the high one.  Then the scales,
+ * [16][head_dim / 16] bytes: one e4m3 scale for every 16 elements of a row.  An element's value
+ * is code * scale of its 16 * k_scale[kv_head] (v_scale for V); code * scale is exact in fp16.
+ * head_dim and block_size are multiples of 16.
  */
 #ifndef PKV_H_
 #define PKV_H_
@@ -59,7 +66,9 @@ typedef enum {
 typedef enum {
   PKV_F16 = 0,
   PKV_BF16 = 1,
-  PKV_FP8_E4M3 = 2           /* e4m3 "fn": bias 7, max 448, no inf; value = code * scale[kv_head] */
+  PKV_FP8_E4M3 = 2,          /* e4m3 "fn": bias 7, max 448, no inf; value = code * scale[kv_head] */
+  PKV_FP4_E2M1 = 3           /* caches only: e2m1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and negatives), one e4m3
+                                scale per 16 elements, and scale[kv_head]; layout above */
 } pkv_dtype;
 
 /* Device error word bits (pkv_get_device_error). */
@@ -69,7 +78,7 @@ enum {
   PKV_DEVERR_SLOT = 1u << 2,          /* a slot was >= num_blocks * block_size */
   PKV_DEVERR_COPY_PAIR = 1u << 3,     /* a copy pair was out of range or its dst is also a src */
   PKV_DEVERR_TIMEOUT = 1u << 4,       /* a bounded wait on an async copy / MMA gave up */
-  PKV_DEVERR_CHUNK = 1u << 5          /* a prefill chunk's cu_q_lens / q_start_pos were inconsistent */
+  PKV_DEVERR_CHUNK = 1u << 5          /* cu_q_lens, cu_k_lens, cu_lens or q_start_pos were inconsistent */
 };
 
 /* The paged pool (Lecture 33 §2.2, "physical KV block pool"): K and V are two such tensors. */
@@ -79,8 +88,8 @@ typedef struct {
   int block_size;            /* tokens per block: 16, or 32 (the attention kernels read it as two 16-row tiles) */
   int head_dim;              /* 64 or 128 */
   pkv_dtype kv_dtype;
-  const float* k_scale;      /* (device) [num_kv_heads] fp32, e4m3 caches only, else NULL */
-  const float* v_scale;      /* (device) [num_kv_heads] fp32, e4m3 caches only, else NULL */
+  const float* k_scale;      /* (device) [num_kv_heads] fp32, e4m3 caches; 4-bit caches: may be NULL (1); else NULL */
+  const float* v_scale;      /* (device) [num_kv_heads] fp32, e4m3 caches; 4-bit caches: may be NULL (1); else NULL */
 } pkv_cache_desc;
 
 PKV_API const char* pkv_status_string(pkv_status s);
@@ -97,7 +106,13 @@ PKV_API int pkv_version(void);       /* (major << 16) | minor */
  *   k_cache[s / B][h][s % B][:] = k_new[t][h][:]   (same for V)
  * in_dtype == kv_dtype copies bytes.  in_dtype f16/bf16 into an e4m3 cache quantises
  * x / scale[h] (fp32 divide) to e4m3, round-to-nearest-even, saturating at ±448.
- * Slots that repeat within one call: one of the writers wins (unspecified which).
+ * f16/bf16 into a 4-bit cache quantises each 16 elements of a row together: with u = x / scale[h]
+ * (fp32 divide; u = x without scales), s = max|u| / 6 (fp32 divide) rounded to e4m3 (to nearest
+ * even, at least 2^-9, at most 448) and code = u / s rounded to e2m1 (to nearest even, saturating
+ * at +-6).  A NaN among the 16 makes s NaN and so all 16 values.  Rows that are 4-bit already are
+ * not taken (PKV_ERR_UNSUPPORTED).
+ * Slots that repeat within one call: one of the writers wins (unspecified which); in a 4-bit cache
+ * such a row may mix the writers' codes and scales.
  * Launch order (kv_write and copy_blocks alike): launched as a programmatic dependent of
  * the previous kernel on `stream`; the kernel touches no memory before that kernel has
  * completed, so stream order holds as for a plain launch.
@@ -105,6 +120,28 @@ PKV_API int pkv_version(void);       /* (major << 16) | minor */
 PKV_API pkv_status pkv_kv_write(const void* k_new, const void* v_new, pkv_dtype in_dtype, int num_tokens,
                         const int64_t* slot_mapping, void* k_cache, void* v_cache,
                         const pkv_cache_desc* cache, pkv_stream_t stream);
+
+/*
+ * kv_read: a sequence's cached rows out of their blocks, in order and dequantised; the way back of
+ * kv_write.  A quantised history becomes plain rows, for instance for the attention of a chunk
+ * that follows it (pkv_prompt_attention).
+ *   k_out, v_out   (device) [total_tokens][num_kv_heads][head_dim] of out_dtype (f16 or bf16; for a
+ *                  16-bit cache its own type)
+ *   cu_lens        (device) int32 [num_seqs + 1], cu_lens[0] = 0, ascending, the last at most
+ *                  total_tokens
+ *   block_tables   (device) int32 [num_seqs][max_blocks_per_seq]
+ * Output row cu_lens[i] + j becomes position j of sequence i, for K and for V:
+ *   out[cu_lens[i] + j][h][:] = cache[T_i[j / B]][h][j % B][:]  (its value, rounded once to out_dtype)
+ * Rows from cu_lens[num_seqs] on are left as they were.  A block id outside the pool leaves its rows
+ * as they were and is flagged PKV_DEVERR_BLOCK_ID; so are rows of a sequence longer than its table
+ * and, as far as the inconsistency reaches, rows under cu_lens that are not ascending from 0 or pass
+ * total_tokens (PKV_DEVERR_CHUNK).
+ * Launched like kv_write (programmatic dependent, waits before touching memory).
+ */
+PKV_API pkv_status pkv_kv_read(void* k_out, void* v_out, pkv_dtype out_dtype, int total_tokens,
+                               const int32_t* cu_lens, int num_seqs, const int32_t* block_tables,
+                               int max_blocks_per_seq, const void* k_cache, const void* v_cache,
+                               const pkv_cache_desc* cache, pkv_stream_t stream);
 
 /*
  * copy_blocks: the copy step of copy-on-write (Lecture 33 §2.4: the writer gets a new
@@ -172,8 +209,8 @@ PKV_API size_t pkv_decode_workspace_bytes(int num_seqs, int num_heads, int num_k
  * cudaHostRegister, reachable through unified addressing): the kernels then read and write
  * them in place over the host link, so a serving loop needs no separate copies.  The caches
  * and the workspace must be device memory.
- * Supported: kv f16/bf16 with the same q dtype, or e4m3 kv with f16/bf16 q (the e4m3
- * path computes in fp16, so |q| must stay below 65504); head_dim 64/128; block_size 16 or 32;
+ * Supported: kv f16/bf16 with the same q dtype, or e4m3 (head_dim 128) or 4-bit kv with f16/bf16 q
+ * (both compute in fp16, so |q| must stay below 65504); head_dim 64/128; block_size 16 or 32;
  * num_heads / num_kv_heads in 1..8; num_kv_heads * num_seqs * ceil(L_max / 16) < 2^31, where
  * L_max = min(max_context_len, max_blocks_per_seq * block_size) (else PKV_ERR_UNSUPPORTED).
  * Launch order: the decode kernel is launched as a programmatic dependent of the previous
@@ -195,8 +232,7 @@ PKV_API pkv_status pkv_paged_decode(void* out, const void* q, pkv_dtype q_dtype,
  * pkv_paged_decode (PagedAttention §3.3: each new token fills its sequence's last block).
  * For every sequence i with L = context_lens[i] >= 1, the new rows k_new[i] and v_new[i] are
  * stored at position L - 1, i.e. slot block_tables[i][(L - 1) / B] * B + (L - 1) % B, quantised
- * to e4m3 with k_scale / v_scale for an e4m3 cache exactly as pkv_kv_write does, and the decode
- * then attends positions 0 .. L - 1, the new one included.  Caches and out are bit-identical to
+ * for an e4m3 or 4-bit cache exactly as pkv_kv_write does, and the decode then attends positions 0 .. L - 1, the new one included.  Caches and out are bit-identical to
  * pkv_kv_write (with those slots) followed by pkv_paged_decode.
  *   k_new, v_new  (device, or pinned host memory as for q) [num_seqs][num_kv_heads][head_dim]
  *                 of q_dtype, 16-byte aligned
@@ -292,6 +328,90 @@ PKV_API pkv_status pkv_paged_prefill_chunk(void* out, const void* q, pkv_dtype q
                                    const void* k_cache, const void* v_cache, const pkv_cache_desc* cache,
                                    const int32_t* block_tables, int max_blocks_per_seq, float scale,
                                    pkv_stream_t stream);
+
+/*
+ * prompt_attention: causal attention of packed prompts over keys and values that need not be in a
+ * cache (the fresh rows of a prompt, or a history from pkv_kv_read with the chunk's own rows behind
+ * it).  Sequence i holds query rows cu_q_lens[i] .. cu_q_lens[i+1]-1 and key rows cu_k_lens[i] ..
+ * cu_k_lens[i+1]-1, Lq and Lk of them; its query rows are the last Lq positions.  Row r attends the
+ * sequence's keys 0 .. r + Lk - Lq:
+ *   out[r][h] = sum_j softmax_j(scale * q[r][h] . k[j][g]) v[j][g],  g = h / (num_heads / num_kv_heads)
+ * A row without keys (r + Lk - Lq < 0, or Lk == 0) gives zeros.
+ *   out, q         (device) [total_q] rows of [num_heads][head_dim] of dtype (f16 or bf16)
+ *   k, v           (device) [total_k] rows of [num_kv_heads][head_dim] of dtype
+ *   *_stride       elements from one row to the next (at least heads * head_dim, a multiple of 8), so
+ *                  that q, k and v may be parts of one packed projection
+ *   cu_q_lens, cu_k_lens (device) int32 [num_seqs + 1], from 0, ascending, the last at most total_q
+ *                  (total_k); output rows from cu_q_lens[num_seqs] on are left as they were
+ *   max_q_len      host upper bound of Lq (sizes the grid); a longer sequence sets PKV_DEVERR_CHUNK and
+ *                  its rows past max_q_len stay unwritten
+ * out must not overlap q, k or v.  Keys and values of a sequence's own rows must be finite wherever a
+ * row attends them or they share a 128-key tile with one that does; rows outside the sequences may
+ * hold anything.  cu_q_lens or cu_k_lens that are not ascending from 0 or pass the totals set
+ * PKV_DEVERR_CHUNK and leave that sequence's rows unwritten.
+ * Supported: head_dim 64 or 128, scale > 0, num_heads a multiple of num_kv_heads, num_seqs and
+ * num_heads up to 65535.  P is rounded to dtype before its product with V, as the tensor cores take
+ * it; sums and outputs are fp32 until the last rounding.  q, k and v must be device memory of the
+ * current GPU (as for pkv_paged_prefill_chunk).  Launch order as pkv_paged_prefill_chunk.
+ */
+PKV_API pkv_status pkv_prompt_attention(void* out, const void* q, const void* k, const void* v, pkv_dtype dtype,
+                                        const int32_t* cu_q_lens, const int32_t* cu_k_lens, int num_seqs,
+                                        int total_q, int total_k, int max_q_len, int num_heads, int num_kv_heads,
+                                        int head_dim, int64_t out_stride, int64_t q_stride, int64_t k_stride,
+                                        int64_t v_stride, float scale, pkv_stream_t stream);
+
+/* Rotary positions.  Pair i of a head (0 <= i < rotary_dim / 2) turns by position * f_i. */
+typedef enum {
+  PKV_ROPE_HALF = 0,         /* pair i is elements i and i + rotary_dim / 2 */
+  PKV_ROPE_INTERLEAVED = 1   /* pair i is elements 2i and 2i + 1 */
+} pkv_rope_layout;
+
+typedef enum {               /* how f_i = base^(-2i / rotary_dim) is scaled for contexts past original_context */
+  PKV_ROPE_NONE = 0,
+  PKV_ROPE_LINEAR = 1,       /* f_i / factor: positions are interpolated */
+  PKV_ROPE_NTK = 2,          /* base * factor^(rotary_dim / (rotary_dim - 2)) in the place of base */
+  PKV_ROPE_PARTS = 3         /* with r = original_context * f_i / (2 pi), the turns over the original context:
+                                f_i where r >= beta, f_i / factor where r <= alpha, between them the blend
+                                w f_i + (1 - w) f_i / factor, w = (r - alpha) / (beta - alpha) */
+} pkv_rope_scaling;
+
+/*
+ * Frequencies for pkv_qk_rotary: table[i] (host memory, rotary_dim / 2 entries; copy it to the device
+ * once) = f_i / (2 pi) turns per position in units of 2^-64 turns.  A position times an entry, modulo
+ * 2^64, is the angle modulo one turn, so far positions lose nothing.  base > 1; factor >= 1 (not
+ * read for PKV_ROPE_NONE); original_context > 0 and alpha < beta for PKV_ROPE_PARTS;
+ * rotary_dim >= 4 for PKV_ROPE_NTK.
+ */
+PKV_API pkv_status pkv_rope_table(uint64_t* table, int rotary_dim, double base, pkv_rope_scaling scaling,
+                                  double factor, double original_context, double alpha, double beta);
+
+/*
+ * qk_rotary: what a step does to its queries and keys between the projection and kv_write /
+ * attention: an RMS norm of each head (optional) and its rotation by the token's position, in one
+ * pass.  For each row x of head_dim elements, in fp32:
+ *   y = x * rsqrt(mean(x^2) + eps) * weight     (y = x when the weight is NULL)
+ *   (a, b) of pair i become magnitude * (a cos t - b sin t), magnitude * (b cos t + a sin t),
+ *   t = position * f_i; elements from rotary_dim on stay y; one rounding to dtype.
+ *   q_out, q       (device) [num_tokens] rows of [num_heads][head_dim] of dtype (f16 or bf16)
+ *   k_out, k       (device) [num_tokens] rows of [num_kv_heads][head_dim] of dtype
+ *   *_stride       elements from one token's row to the next, a multiple of 8 and at least
+ *                  heads * head_dim; q_out == q and k_out == k with equal strides work in place, other
+ *                  overlaps do not
+ *   positions      (device) int32 [num_tokens]; a negative position marks a padding token, whose rows
+ *                  in q_out and k_out are left as they were
+ *   table          (device) uint64 [rotary_dim / 2], from pkv_rope_table
+ *   q_weight, k_weight (device) [head_dim] of dtype, or NULL: no norm
+ *   magnitude      factor on the rotated elements (1 if the context is not scaled)
+ * num_heads or num_kv_heads may be 0 (its pointers are then not read).  Supported: head_dim a
+ * multiple of 16 up to 256, rotary_dim a multiple of 16 up to head_dim.
+ * Launched like kv_write (programmatic dependent, waits before touching memory).
+ */
+PKV_API pkv_status pkv_qk_rotary(void* q_out, const void* q, void* k_out, const void* k, pkv_dtype dtype,
+                                 int num_tokens, int num_heads, int num_kv_heads, int head_dim,
+                                 int64_t q_out_stride, int64_t q_stride, int64_t k_out_stride, int64_t k_stride,
+                                 const int32_t* positions, const uint64_t* table, int rotary_dim,
+                                 pkv_rope_layout layout, float magnitude, const void* q_weight,
+                                 const void* k_weight, float eps, pkv_stream_t stream);
 
 /*
  * Waits for `stream`, then reads and clears the library's device error word on the

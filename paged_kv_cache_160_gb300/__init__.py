@@ -11,11 +11,14 @@ from ._binding import (  # noqa: F401
     PkvError,
     DEVERR,
     cache_desc,
+    cache_desc_fp4,
+    fp4_cache_shape,
     lib,
     pkv_check_bounded_wait,
     pkv_copy_blocks,
     pkv_decode_workspace_bytes,
     pkv_get_device_error,
+    pkv_kv_read,
     pkv_kv_write,
     pkv_paged_decode,
     pkv_paged_decode_append,
@@ -24,6 +27,9 @@ from ._binding import (  # noqa: F401
     pkv_get_decode_sm_budget,
     pkv_set_decode_sm_budget,
     pkv_paged_prefill_chunk,
+    pkv_prompt_attention,
+    pkv_qk_rotary,
+    pkv_rope_table,
     pkv_stream_tiles,
     pkv_swap_blocks,
 )

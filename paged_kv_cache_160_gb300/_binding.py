@@ -9,7 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, c_float, c_int, c_int32, c_int64, c_size_t, c_void_p
+from ctypes import POINTER, c_double, c_float, c_int, c_int32, c_int64, c_size_t, c_void_p
 from typing import List, Optional, Sequence, Tuple
 
 import torch
@@ -19,7 +19,9 @@ _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libpkv.so"
 PKV_OK = 0
 STATUS_NAMES = {0: "PKV_OK", 1: "PKV_ERR_INVALID_ARG", 2: "PKV_ERR_UNSUPPORTED", 3: "PKV_ERR_WORKSPACE",
                 4: "PKV_ERR_CUDA", 5: "PKV_ERR_NO_BLOCKS", 6: "PKV_ERR_DEVICE_CHECK"}
-PKV_F16, PKV_BF16, PKV_FP8_E4M3 = 0, 1, 2
+PKV_F16, PKV_BF16, PKV_FP8_E4M3, PKV_FP4_E2M1 = 0, 1, 2, 3
+ROPE_LAYOUT = {"half": 0, "interleaved": 1}
+ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "parts": 3}
 DEVERR = {"block_id": 1, "context_len": 2, "slot": 4, "copy_pair": 8, "timeout": 16, "chunk": 32}
 
 
@@ -82,6 +84,19 @@ def _load() -> ctypes.CDLL:
     lib.pkv_paged_prefill_chunk.argtypes = [c_void_p, c_void_p, c_int, c_void_p, c_void_p, c_int, c_int, c_int,
                                             c_int, c_void_p, c_void_p, POINTER(CacheDesc), c_void_p, c_int,
                                             c_float, c_void_p]
+    lib.pkv_kv_read.restype = S
+    lib.pkv_kv_read.argtypes = [c_void_p, c_void_p, c_int, c_int, c_void_p, c_int, c_void_p, c_int, c_void_p,
+                                c_void_p, POINTER(CacheDesc), c_void_p]
+    lib.pkv_prompt_attention.restype = S
+    lib.pkv_prompt_attention.argtypes = [c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_void_p, c_void_p, c_int,
+                                         c_int, c_int, c_int, c_int, c_int, c_int, c_int64, c_int64, c_int64,
+                                         c_int64, c_float, c_void_p]
+    lib.pkv_rope_table.restype = S
+    lib.pkv_rope_table.argtypes = [c_void_p, c_int, c_double, c_int, c_double, c_double, c_double, c_double]
+    lib.pkv_qk_rotary.restype = S
+    lib.pkv_qk_rotary.argtypes = [c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_int, c_int, c_int, c_int, c_int64,
+                                  c_int64, c_int64, c_int64, c_void_p, c_void_p, c_int, c_int, c_float, c_void_p,
+                                  c_void_p, c_float, c_void_p]
     lib.pkv_get_device_error.restype = S
     lib.pkv_get_device_error.argtypes = [POINTER(c_int), c_void_p]
     # block manager
@@ -188,12 +203,48 @@ def cache_desc(k_cache: torch.Tensor, k_scale: Optional[torch.Tensor] = None,
     return desc
 
 
+def fp4_cache_shape(num_blocks: int, num_kv_heads: int, block_size: int, head_dim: int) -> Tuple[int, int, int, int]:
+    """Shape of a 4-bit pool tensor (uint8): 9 * head_dim bytes for each 16 rows of a kv head."""
+    if head_dim % 16 or block_size % 16:
+        raise ValueError("a 4-bit cache needs head_dim and block_size in multiples of 16")
+    return num_blocks, num_kv_heads, block_size // 16, 9 * head_dim
+
+
+def cache_desc_fp4(k_cache: torch.Tensor, k_scale: Optional[torch.Tensor] = None,
+                   v_scale: Optional[torch.Tensor] = None) -> CacheDesc:
+    """Descriptor of a 4-bit pool tensor of ``fp4_cache_shape``; the scales (float32, one per kv head)
+    are optional.  Like ``cache_desc`` it keeps the scale tensors alive."""
+    if k_cache.dtype != torch.uint8 or k_cache.dim() != 4 or k_cache.shape[3] % 144:
+        raise ValueError("a 4-bit pool is uint8 [num_blocks, num_kv_heads, block_size / 16, 9 * head_dim]")
+    nb, hkv, tiles, nbytes = k_cache.shape
+    for t in (k_scale, v_scale):
+        if t is not None and (t.dtype != torch.float32 or t.numel() != hkv):
+            raise ValueError("scales are float32 [num_kv_heads]")
+    desc = CacheDesc(nb, hkv, 16 * tiles, nbytes // 9, PKV_FP4_E2M1, _dev(k_scale, "k_scale") or None,
+                     _dev(v_scale, "v_scale") or None)
+    desc._keep = (k_scale, v_scale)
+    return desc
+
+
 def pkv_kv_write(k_new: torch.Tensor, v_new: torch.Tensor, slot_mapping: torch.Tensor, k_cache: torch.Tensor,
                  v_cache: torch.Tensor, desc: CacheDesc, stream=None) -> None:
     assert slot_mapping.dtype == torch.int64
     _check(lib.pkv_kv_write(_dev(k_new, "k_new"), _dev(v_new, "v_new"), pkv_dtype_of(k_new), k_new.shape[0],
                             _dev(slot_mapping, "slot_mapping"), _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"),
                             ctypes.byref(desc), _stream(stream)), "pkv_kv_write")
+
+
+def pkv_kv_read(k_out: torch.Tensor, v_out: torch.Tensor, cu_lens: torch.Tensor, block_tables: torch.Tensor,
+                k_cache: torch.Tensor, v_cache: torch.Tensor, desc: CacheDesc, stream=None) -> None:
+    """The cached rows of each sequence, dequantised, in order: rows cu_lens[i] .. cu_lens[i+1]-1 of k_out
+    and v_out ([total_tokens, num_kv_heads, head_dim]) become positions 0 .. of sequence i."""
+    assert cu_lens.dtype == torch.int32 and block_tables.dtype == torch.int32
+    assert k_out.dtype == v_out.dtype and k_out.shape == v_out.shape
+    assert tuple(k_out.shape[1:]) == (desc.num_kv_heads, desc.head_dim) and block_tables.shape[0] == cu_lens.numel() - 1
+    _check(lib.pkv_kv_read(_dev(k_out, "k_out"), _dev(v_out, "v_out"), pkv_dtype_of(k_out), k_out.shape[0],
+                           _dev(cu_lens, "cu_lens"), cu_lens.numel() - 1, _dev(block_tables, "block_tables"),
+                           block_tables.shape[1], _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"),
+                           ctypes.byref(desc), _stream(stream)), "pkv_kv_read")
 
 
 def pkv_copy_blocks(k_cache: torch.Tensor, v_cache: torch.Tensor, desc: CacheDesc, block_pairs: torch.Tensor,
@@ -315,6 +366,61 @@ def pkv_paged_prefill_chunk(out: torch.Tensor, q: torch.Tensor, cu_q_lens: torch
                                        _dev(v_cache, "v_cache"), ctypes.byref(desc),
                                        _dev(block_tables, "block_tables"), block_tables.shape[1], float(scale),
                                        _stream(stream)), "pkv_paged_prefill_chunk")
+
+
+def _rows(t: torch.Tensor, name: str) -> Tuple[int, int]:
+    """(address, elements from row to row) of a CUDA tensor [rows, heads, head_dim] with dense rows."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (libpkv has no CPU path)")
+    rows, heads, dim = t.shape
+    stride = t.stride()
+    if (dim > 1 and stride[2] != 1) or (heads > 1 and stride[1] != dim):
+        raise ValueError(f"{name}: the heads of a row must lie next to each other")
+    return t.data_ptr(), (stride[0] if rows > 1 else max(heads * dim, 8))
+
+
+def pkv_prompt_attention(out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q_lens: torch.Tensor,
+                         cu_k_lens: torch.Tensor, max_q_len: int, scale: float, stream=None) -> None:
+    """Causal attention of packed prompts: q and out [total_q, num_heads, head_dim], k and v [total_k,
+    num_kv_heads, head_dim] (any row stride, such as parts of a packed projection).  The query rows of
+    sequence i are its last positions; a row without keys gives zeros."""
+    assert cu_q_lens.dtype == torch.int32 and cu_k_lens.dtype == torch.int32
+    assert cu_q_lens.numel() == cu_k_lens.numel() and out.shape == q.shape and k.shape == v.shape
+    assert q.dtype == k.dtype == v.dtype == out.dtype and q.shape[2] == k.shape[2]
+    (po, so), (pq, sq), (pk, sk), (pv, sv) = _rows(out, "out"), _rows(q, "q"), _rows(k, "k"), _rows(v, "v")
+    _check(lib.pkv_prompt_attention(po, pq, pk, pv, pkv_dtype_of(q), _dev(cu_q_lens, "cu_q_lens"),
+                                    _dev(cu_k_lens, "cu_k_lens"), cu_q_lens.numel() - 1, q.shape[0], k.shape[0],
+                                    int(max_q_len), q.shape[1], k.shape[1], q.shape[2], so, sq, sk, sv, float(scale),
+                                    _stream(stream)), "pkv_prompt_attention")
+
+
+def pkv_rope_table(rotary_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                   original_context: float = 0.0, alpha: float = 1.0, beta: float = 32.0) -> torch.Tensor:
+    """Frequencies for pkv_qk_rotary (int64 [rotary_dim / 2] on the host; move it to the device once).
+    scaling: "none", "linear", "ntk" or "parts" (see include/pkv.h for the formulas)."""
+    table = torch.empty(max(rotary_dim // 2, 0), dtype=torch.int64)
+    _check(lib.pkv_rope_table(table.data_ptr(), int(rotary_dim), float(base), ROPE_SCALING[scaling], float(factor),
+                              float(original_context), float(alpha), float(beta)), "pkv_rope_table")
+    return table
+
+
+def pkv_qk_rotary(q_out: torch.Tensor, q: torch.Tensor, k_out: torch.Tensor, k: torch.Tensor, positions: torch.Tensor,
+                  table: torch.Tensor, layout: str = "half", magnitude: float = 1.0,
+                  q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                  stream=None) -> None:
+    """Per-head RMS norm (with weights) and rotation by position of q [tokens, num_heads, head_dim] and k
+    [tokens, num_kv_heads, head_dim] (any row stride); q_out is q and k_out is k works in place."""
+    assert positions.dtype == torch.int32 and table.dtype == torch.int64
+    assert q_out.shape == q.shape and k_out.shape == k.shape and q.shape[0] == k.shape[0] == positions.numel()
+    assert q.dtype == k.dtype == q_out.dtype == k_out.dtype and q.shape[2] == k.shape[2]
+    for w in (q_weight, k_weight):
+        assert w is None or (w.dtype == q.dtype and w.numel() == q.shape[2])
+    (qo, qos), (qi, qis), (ko, kos), (ki, kis) = (_rows(q_out, "q_out"), _rows(q, "q"), _rows(k_out, "k_out"),
+                                                  _rows(k, "k"))
+    _check(lib.pkv_qk_rotary(qo, qi, ko, ki, pkv_dtype_of(q), q.shape[0], q.shape[1], k.shape[1], q.shape[2], qos, qis,
+                             kos, kis, _dev(positions, "positions"), _dev(table, "table"), 2 * table.numel(),
+                             ROPE_LAYOUT[layout], float(magnitude), _dev(q_weight, "q_weight"),
+                             _dev(k_weight, "k_weight"), float(eps), _stream(stream)), "pkv_qk_rotary")
 
 
 def pkv_get_device_error(stream=None) -> int:

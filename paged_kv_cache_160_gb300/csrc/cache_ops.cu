@@ -1,6 +1,7 @@
-// kv_write (scatter of the step's new K/V rows into their slots) and copy_blocks (the copy
-// step of copy-on-write).  Both move bytes with 16-byte vector loads/stores; both are
-// bound by HBM traffic and, at serving sizes, by launch latency.
+// kv_write (scatter of the step's new K/V rows into their slots), kv_read (a sequence's rows back
+// out of its blocks, dequantised) and copy_blocks (the copy step of copy-on-write).  All move
+// bytes with 16-byte vector loads/stores where the layout allows; all are bound by HBM traffic
+// and, at serving sizes, by launch latency.
 //
 // Sources: "PagedAttention: manage the KV cache like virtual memory" §3.3 (each new token
 // fills its sequence's last block); "Lecture 33 — KV Cache management" §2.2 (slot =
@@ -90,6 +91,160 @@ __global__ void __launch_bounds__(kThreads) kv_write_quant_kernel(
     }
     k_cache[dst] = make_uint4(kw[0], kw[1], kw[2], kw[3]);
     v_cache[dst] = make_uint4(vw[0], vw[1], vw[2], vw[3]);
+  }
+}
+
+// f16/bf16 rows into a 4-bit cache; 16 elements (one scale) of K and of V per thread.
+template <bool kBF16>
+__global__ void __launch_bounds__(kThreads) kv_write_fp4_kernel(
+    const uint4* __restrict__ k_new, const uint4* __restrict__ v_new, const int64_t* __restrict__ slots,
+    uint8_t* __restrict__ k_cache, uint8_t* __restrict__ v_cache, const float* __restrict__ k_scale,
+    const float* __restrict__ v_scale, int num_tokens, int num_kv_heads, int groups, int block_size,
+    int64_t num_slots, unsigned* err) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int64_t total = int64_t(num_tokens) * num_kv_heads * groups;
+  for (int64_t i = blockIdx.x * int64_t(blockDim.x) + threadIdx.x; i < total; i += int64_t(gridDim.x) * blockDim.x) {
+    const int c = int(i % groups);
+    const int64_t r = i / groups;
+    const int h = int(r % num_kv_heads);
+    const int64_t t = r / num_kv_heads;
+    const int64_t slot = slots[t];
+    if (slot < 0) continue;
+    if (slot >= num_slots) {
+      if (c == 0 && h == 0) set_error(err, PKV_DEVERR_SLOT);
+      continue;
+    }
+    const int64_t blk = slot / block_size, off = slot % block_size;
+    const int64_t tile = ((blk * num_kv_heads + h) * block_size + off) / 16;
+    const int row = int(off % 16);
+    const int64_t base = tile * 144 * groups;                      // 9 * head_dim bytes per tile
+    const int64_t at = base + (row * groups + c) * 8, sat = base + 128 * groups + row * groups + c;
+    uint32_t sc;
+    const uint2 kc = quant16_e2m1<kBF16>(__ldg(k_new + 2 * i), __ldg(k_new + 2 * i + 1), k_scale ? k_scale[h] : 1.f,
+                                         k_scale != nullptr, sc);
+    *reinterpret_cast<uint2*>(k_cache + at) = kc;
+    k_cache[sat] = uint8_t(sc);
+    const uint2 vc = quant16_e2m1<kBF16>(__ldg(v_new + 2 * i), __ldg(v_new + 2 * i + 1), v_scale ? v_scale[h] : 1.f,
+                                         v_scale != nullptr, sc);
+    *reinterpret_cast<uint2*>(v_cache + at) = vc;
+    v_cache[sat] = uint8_t(sc);
+  }
+}
+
+// ---------------------------------------------------------------------------------------
+// kv_read
+// ---------------------------------------------------------------------------------------
+struct ReadParams {
+  uint8_t* k_out;
+  uint8_t* v_out;
+  const int32_t* cu_lens;
+  const int32_t* block_tables;
+  const uint8_t* k_cache;
+  const uint8_t* v_cache;
+  const float* k_scale;
+  const float* v_scale;
+  int total_tokens;
+  int num_seqs;
+  int max_blocks;
+  int num_blocks;
+  int num_kv_heads;
+  int block_size;
+  int head_dim;
+  unsigned* err;
+};
+
+constexpr int kReadRows = 32;    // output rows per CTA
+
+// Sixteen output elements from their stored bytes.
+template <pkv_dtype KV, bool kBF16>
+__device__ __forceinline__ void read16(const ReadParams& p, const uint8_t* cache, uint8_t* out, const float* scales,
+                                       int64_t row, int h, int g, int64_t orow) {
+  const int D = p.head_dim;
+  uint4* dst = reinterpret_cast<uint4*>(out + ((orow * p.num_kv_heads + h) * D + 16 * g) * 2);
+  if constexpr (KV == PKV_F16 || KV == PKV_BF16) {
+    const uint4* src = reinterpret_cast<const uint4*>(cache + (row * D + 16 * g) * 2);
+    const uint4 a = __ldg(src), b = __ldg(src + 1);
+    dst[0] = a;
+    dst[1] = b;
+  } else {
+    const float hs = scales ? __ldg(scales + h) : 1.f;
+    uint32_t half[8];                                      // 16 fp16 values, exact
+    if constexpr (KV == PKV_FP8_E4M3) {
+      const uint4 c = __ldg(reinterpret_cast<const uint4*>(cache + row * D + 16 * g));
+      const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        half[2 * k] = e4m3x2_to_f16x2(w[k]);
+        half[2 * k + 1] = e4m3x2_to_f16x2(w[k] >> 16);
+      }
+    } else {
+      const uint8_t* tile = cache + (row >> 4) * 9 * D;
+      const int rr = int(row & 15);
+      const uint2 c = __ldg(reinterpret_cast<const uint2*>(tile + rr * (D / 2) + 8 * g));
+      const uint32_t s2 = e4m3x2_to_f16x2(uint32_t(__ldg(tile + 8 * D + rr * (D / 16) + g)) * 0x101u);
+      uint32_t x[4], y[4];
+      e2m1x8_to_f16x8(c.x, x);
+      e2m1x8_to_f16x8(c.y, y);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        half[k] = hmul2(x[k], s2);
+        half[4 + k] = hmul2(y[k], s2);
+      }
+    }
+    uint32_t o[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float2 f = unpack2<false>(half[k]);
+      o[k] = pack2<kBF16>(f.x * hs, f.y * hs);
+    }
+    dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+    dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+  }
+}
+
+// A CTA takes kReadRows output rows: one thread per row finds its sequence and pool row, then all
+// threads move 16 elements each, group fastest, so that stores are runs of whole rows.
+template <pkv_dtype KV, bool kBF16>
+__global__ void __launch_bounds__(kThreads) kv_read_kernel(const ReadParams p) {
+  __shared__ int64_t src_row[kReadRows];                   // row of kv head 0 in the pool, -1: leave the row
+  griddep_launch_dependents();
+  griddep_wait();
+  const int t0 = blockIdx.x * kReadRows;
+  if (blockIdx.x == 0) {                                   // cu_lens ascends from 0 to at most total_tokens
+    bool bad = threadIdx.x == 0 && (p.cu_lens[0] != 0 || p.cu_lens[p.num_seqs] > p.total_tokens);
+    for (int i = threadIdx.x; i < p.num_seqs; i += blockDim.x) bad |= p.cu_lens[i + 1] < p.cu_lens[i];
+    if (bad) set_error(p.err, PKV_DEVERR_CHUNK);
+  }
+  if (threadIdx.x < kReadRows) {
+    const int t = t0 + threadIdx.x;
+    int64_t row = -1;
+    const int last = p.cu_lens[p.num_seqs];
+    if (t < p.total_tokens && t < last) {
+      int lo = 0, hi = p.num_seqs;                         // the largest i with cu_lens[i] <= t
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (p.cu_lens[mid] <= t) lo = mid; else hi = mid;
+      }
+      const int j = t - p.cu_lens[lo];
+      if (j < 0 || t >= p.cu_lens[lo + 1] || j / p.block_size >= p.max_blocks) {
+        set_error(p.err, PKV_DEVERR_CHUNK);
+      } else {
+        const int blk = p.block_tables[int64_t(lo) * p.max_blocks + j / p.block_size];
+        if (blk < 0 || blk >= p.num_blocks) set_error(p.err, PKV_DEVERR_BLOCK_ID);
+        else row = int64_t(blk) * p.num_kv_heads * p.block_size + j % p.block_size;
+      }
+    }
+    src_row[threadIdx.x] = row;
+  }
+  __syncthreads();
+  const int groups = p.head_dim / 16, per_row = p.num_kv_heads * groups;
+  for (int i = threadIdx.x; i < kReadRows * per_row; i += blockDim.x) {
+    const int r = i / per_row, c = i - r * per_row, h = c / groups, g = c - h * groups;
+    if (src_row[r] < 0) continue;
+    const int64_t row = src_row[r] + int64_t(h) * p.block_size;
+    read16<KV, kBF16>(p, p.k_cache, p.k_out, p.k_scale, row, h, g, t0 + r);
+    read16<KV, kBF16>(p, p.v_cache, p.v_out, p.v_scale, row, h, g, t0 + r);
   }
 }
 
@@ -183,6 +338,7 @@ pkv_status pkv_kv_write(const void* k_new, const void* v_new, pkv_dtype in_dtype
   if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(k_cache) || !aligned16(v_cache) ||
       (reinterpret_cast<uintptr_t>(slot_mapping) & 7u))
     return PKV_ERR_INVALID_ARG;
+  if (in_dtype == PKV_FP4_E2M1) return PKV_ERR_UNSUPPORTED;
   if (in_dtype != PKV_F16 && in_dtype != PKV_BF16 && in_dtype != PKV_FP8_E4M3) return PKV_ERR_INVALID_ARG;
   unsigned* err = error_word_ptr();
   if (!err) return PKV_ERR_CUDA;
@@ -205,10 +361,68 @@ pkv_status pkv_kv_write(const void* k_new, const void* v_new, pkv_dtype in_dtype
                    static_cast<uint4*>(v_cache), cache->k_scale, cache->v_scale, num_tokens, cache->num_kv_heads,
                    chunks, cache->block_size, num_slots, err) != cudaSuccess)
       return PKV_ERR_CUDA;
+  } else if (cache->kv_dtype == PKV_FP4_E2M1 && (in_dtype == PKV_F16 || in_dtype == PKV_BF16)) {
+    const int groups = cache->head_dim / 16;
+    const int64_t work = int64_t(num_tokens) * cache->num_kv_heads * groups;
+    auto kern = in_dtype == PKV_BF16 ? kv_write_fp4_kernel<true> : kv_write_fp4_kernel<false>;
+    if (launch_pdl(kern, dim3(grid_for(work)), dim3(kThreads), 0, s, static_cast<const uint4*>(k_new),
+                   static_cast<const uint4*>(v_new), slot_mapping, static_cast<uint8_t*>(k_cache),
+                   static_cast<uint8_t*>(v_cache), cache->k_scale, cache->v_scale, num_tokens, cache->num_kv_heads,
+                   groups, cache->block_size, num_slots, err) != cudaSuccess)
+      return PKV_ERR_CUDA;
   } else {
     return PKV_ERR_UNSUPPORTED;
   }
   return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+pkv_status pkv_kv_read(void* k_out, void* v_out, pkv_dtype out_dtype, int total_tokens, const int32_t* cu_lens,
+                       int num_seqs, const int32_t* block_tables, int max_blocks_per_seq, const void* k_cache,
+                       const void* v_cache, const pkv_cache_desc* cache, pkv_stream_t stream) {
+  using namespace pkv;
+  pkv_status st = check_cache_desc(cache);
+  if (st != PKV_OK) return st;
+  if (total_tokens < 0 || num_seqs < 0 || max_blocks_per_seq < 0) return PKV_ERR_INVALID_ARG;
+  if (out_dtype != PKV_F16 && out_dtype != PKV_BF16) return PKV_ERR_INVALID_ARG;
+  const bool wide = cache->kv_dtype == PKV_F16 || cache->kv_dtype == PKV_BF16;
+  if (wide && out_dtype != cache->kv_dtype) return PKV_ERR_UNSUPPORTED;
+  if (cache->head_dim % 16) return PKV_ERR_UNSUPPORTED;
+  if (total_tokens == 0 || num_seqs == 0) return PKV_OK;
+  if (!k_out || !v_out || !cu_lens || !block_tables || !k_cache || !v_cache || max_blocks_per_seq == 0)
+    return PKV_ERR_INVALID_ARG;
+  if (!aligned16(k_out) || !aligned16(v_out) || !aligned16(k_cache) || !aligned16(v_cache) ||
+      (reinterpret_cast<uintptr_t>(cu_lens) & 3u) || (reinterpret_cast<uintptr_t>(block_tables) & 3u))
+    return PKV_ERR_INVALID_ARG;
+  if (int64_t(cache->num_kv_heads) * cache->head_dim * kReadRows / 16 >= (int64_t(1) << 31))
+    return PKV_ERR_UNSUPPORTED;              // the rows of one CTA are indexed in 32 bits
+  unsigned* err = error_word_ptr();
+  if (!err) return PKV_ERR_CUDA;
+  ReadParams prm;
+  prm.k_out = static_cast<uint8_t*>(k_out);
+  prm.v_out = static_cast<uint8_t*>(v_out);
+  prm.cu_lens = cu_lens;
+  prm.block_tables = block_tables;
+  prm.k_cache = static_cast<const uint8_t*>(k_cache);
+  prm.v_cache = static_cast<const uint8_t*>(v_cache);
+  prm.k_scale = cache->k_scale;
+  prm.v_scale = cache->v_scale;
+  prm.total_tokens = total_tokens;
+  prm.num_seqs = num_seqs;
+  prm.max_blocks = max_blocks_per_seq;
+  prm.num_blocks = cache->num_blocks;
+  prm.num_kv_heads = cache->num_kv_heads;
+  prm.block_size = cache->block_size;
+  prm.head_dim = cache->head_dim;
+  prm.err = err;
+  const bool bf = out_dtype == PKV_BF16;
+  auto kern = wide ? (bf ? kv_read_kernel<PKV_BF16, true> : kv_read_kernel<PKV_F16, false>)
+              : cache->kv_dtype == PKV_FP8_E4M3
+                  ? (bf ? kv_read_kernel<PKV_FP8_E4M3, true> : kv_read_kernel<PKV_FP8_E4M3, false>)
+                  : (bf ? kv_read_kernel<PKV_FP4_E2M1, true> : kv_read_kernel<PKV_FP4_E2M1, false>);
+  const int grid = (total_tokens - 1) / kReadRows + 1;
+  return launch_pdl(kern, dim3(grid), dim3(kThreads), 0, reinterpret_cast<cudaStream_t>(stream), prm) == cudaSuccess
+             ? PKV_OK
+             : PKV_ERR_CUDA;
 }
 
 pkv_status pkv_copy_blocks(void* k_cache, void* v_cache, const pkv_cache_desc* cache, const int32_t* block_pairs,
@@ -224,9 +438,7 @@ pkv_status pkv_copy_blocks(void* k_cache, void* v_cache, const pkv_cache_desc* c
   if (num_pairs > 65535) return PKV_ERR_UNSUPPORTED;
   unsigned* err = error_word_ptr();
   if (!err) return PKV_ERR_CUDA;
-  const int64_t block_bytes =
-      int64_t(cache->num_kv_heads) * cache->block_size * cache->head_dim * dtype_bytes(cache->kv_dtype);
-  const int64_t chunks = block_bytes / 16;
+  const int64_t chunks = cache_block_bytes(cache) / 16;
   dim3 grid(num_pairs, 2);
   if (launch_pdl(copy_blocks_kernel, grid, dim3(kThreads), 0, reinterpret_cast<cudaStream_t>(stream),
                  static_cast<uint4*>(k_cache), static_cast<uint4*>(v_cache), block_pairs, num_pairs,
@@ -250,8 +462,7 @@ pkv_status pkv_swap_blocks(void* dst_k, void* dst_v, int dst_num_blocks, const v
   if (num_pairs > 65535) return PKV_ERR_UNSUPPORTED;
   unsigned* err = error_word_ptr();
   if (!err) return PKV_ERR_CUDA;
-  const int64_t block_bytes =
-      int64_t(layout->num_kv_heads) * layout->block_size * layout->head_dim * dtype_bytes(layout->kv_dtype);
+  const int64_t block_bytes = cache_block_bytes(layout);
   if (launch_pdl(swap_blocks_kernel, dim3(num_pairs, 2), dim3(kThreads), 0, reinterpret_cast<cudaStream_t>(stream),
                  static_cast<uint4*>(dst_k), static_cast<uint4*>(dst_v), static_cast<const uint4*>(src_k),
                  static_cast<const uint4*>(src_v), block_pairs, num_pairs, src_num_blocks, dst_num_blocks,

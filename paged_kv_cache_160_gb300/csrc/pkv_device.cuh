@@ -149,6 +149,15 @@ __device__ __forceinline__ void tma_load_3d_mc(void* smem_dst, const CUtensorMap
       : "memory");
 }
 
+// Untiled copy of `bytes` (a multiple of 16; both addresses on 16 bytes) into shared memory.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar, uint64_t pol) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::
+          "r"(smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(pol)
+      : "memory");
+}
+
 __device__ __forceinline__ void prefetch_tensormap(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
@@ -178,6 +187,27 @@ __device__ __forceinline__ void ldsm_x4_trans(uint32_t addr, uint32_t& r0, uint3
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
   return v;
 }
 
@@ -243,6 +273,73 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two_codes) {
   return out;
 }
 
+// Eight e2m1 codes, two per byte (low nibble first), to four pairs of fp16 values; exact.
+__device__ __forceinline__ void e2m1x8_to_f16x8(uint32_t codes, uint32_t (&out)[4]) {
+  asm("{\n\t.reg .b8 c0, c1, c2, c3;\n\t"
+      "mov.b32 {c0, c1, c2, c3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, c0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, c1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, c3;\n\t}"
+      : "=r"(out[0]), "=r"(out[1]), "=r"(out[2]), "=r"(out[3])
+      : "r"(codes));
+}
+
+// Eight fp32 values to eight e2m1 codes (round to nearest even, saturate to +-6), v[0] in the
+// lowest nibble.
+__device__ __forceinline__ uint32_t f32x8_to_e2m1x8(const float (&v)[8]) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 c0, c1, c2, c3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c2, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c3, %8, %7;\n\t"
+      "mov.b32 %0, {c0, c1, c2, c3};\n\t}"
+      : "=r"(r)
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+  return r;
+}
+
+template <bool kBF16>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  if constexpr (kBF16) return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
+  else return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+
+// 16 f16/bf16 values (a: elements 0-7, b: 8-15) to the 16 codes of a 4-bit cache (8 bytes, element
+// order) and their e4m3 scale: u = x / head_scale, s = max|u| / 6 in e4m3, code = u / s in e2m1.
+// All divisions are correctly rounded fp32.  u / s rounded to fp32 falls on a border between two
+// codes only if the exact quotient does: an fp32 u next to s * border (itself an fp32 value) is
+// at least half an ulp of the border away after the division.  So every writer agrees with the
+// definition bit for bit.
+template <bool kBF16>
+__device__ __forceinline__ uint2 quant16_e2m1(const uint4 a, const uint4 b, float head_scale, bool scaled,
+                                              uint32_t& scale_code) {
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  float u[16];
+  float mx = 0.f;
+  bool nan = false;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const float2 f = unpack2<kBF16>(w[k]);
+    u[2 * k] = scaled ? __fdiv_rn(f.x, head_scale) : f.x;
+    u[2 * k + 1] = scaled ? __fdiv_rn(f.y, head_scale) : f.y;
+    mx = fmaxf(mx, fmaxf(fabsf(u[2 * k]), fabsf(u[2 * k + 1])));
+    nan |= u[2 * k] != u[2 * k] || u[2 * k + 1] != u[2 * k + 1];
+  }
+  const float want = fmaxf(__fdiv_rn(mx, 6.f), 0.001953125f);   // 2^-9, the smallest e4m3 value
+  scale_code = f32x2_to_e4m3x2(want, 0.f) & 0xFFu;
+  const float s = unpack2<false>(e4m3x2_to_f16x2(scale_code)).x;
+  if (nan) scale_code = 0x7Fu;
+  float lo[8], hi[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    lo[k] = __fdiv_rn(u[k], s);
+    hi[k] = __fdiv_rn(u[8 + k], s);
+  }
+  return make_uint2(f32x8_to_e2m1x8(lo), f32x8_to_e2m1x8(hi));
+}
+
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
   uint32_t r;
   asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
@@ -258,6 +355,13 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<uint32_t*>(&v);
   }
+}
+
+// Product of two pairs of fp16 values.
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
 }
 
 __device__ __forceinline__ float fast_exp2(float x) {

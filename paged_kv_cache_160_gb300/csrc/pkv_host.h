@@ -37,7 +37,13 @@ inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 // query fails.  The runtime's error state is left clear.
 bool on_current_device(const void* p);
 
-inline int dtype_bytes(pkv_dtype d) { return d == PKV_FP8_E4M3 ? 1 : 2; }
+inline int dtype_bytes(pkv_dtype d) { return d == PKV_FP8_E4M3 ? 1 : 2; }   // not the 4-bit caches
+
+// Bytes of one pool block of K (or V): every kv head's rows, and their scales in a 4-bit cache.
+inline int64_t cache_block_bytes(const pkv_cache_desc* c) {
+  const int64_t elems = int64_t(c->num_kv_heads) * c->block_size * c->head_dim;
+  return c->kv_dtype == PKV_FP4_E2M1 ? elems / 16 * 9 : elems * dtype_bytes(c->kv_dtype);
+}
 
 // Shared checks of a cache descriptor; returns PKV_OK or the failing status.
 pkv_status check_cache_desc(const pkv_cache_desc* c);

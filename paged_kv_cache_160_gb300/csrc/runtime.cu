@@ -112,6 +112,8 @@ pkv_status check_cache_desc(const pkv_cache_desc* c) {
   if (!c) return PKV_ERR_INVALID_ARG;
   if (c->num_blocks <= 0 || c->num_kv_heads <= 0 || c->block_size <= 0 || c->head_dim <= 0)
     return PKV_ERR_INVALID_ARG;
+  if (c->kv_dtype == PKV_FP4_E2M1)           // tiles of 16 rows, scales of 16 elements
+    return c->head_dim % 16 || c->block_size % 16 ? PKV_ERR_UNSUPPORTED : PKV_OK;
   if (c->kv_dtype != PKV_F16 && c->kv_dtype != PKV_BF16 && c->kv_dtype != PKV_FP8_E4M3) return PKV_ERR_INVALID_ARG;
   if (c->kv_dtype == PKV_FP8_E4M3 && (!c->k_scale || !c->v_scale)) return PKV_ERR_INVALID_ARG;
   if (int64_t(c->head_dim) * dtype_bytes(c->kv_dtype) % 16 != 0) return PKV_ERR_INVALID_ARG;
@@ -135,7 +137,7 @@ const char* pkv_status_string(pkv_status s) {
   return "unknown status";
 }
 
-int pkv_version(void) { return (0 << 16) | 2; }
+int pkv_version(void) { return (0 << 16) | 3; }
 
 pkv_status pkv_get_device_error(int* code, pkv_stream_t stream) {
   if (!code) return PKV_ERR_INVALID_ARG;

@@ -19,14 +19,6 @@ constexpr int kWarps = 12;
 constexpr int kStages = 2;
 constexpr int kRows = 16;
 
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar, uint64_t pol) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::
-          "r"(smem_u32(dst)),
-      "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(pol)
-      : "memory");
-}
-
 struct StreamParams {
   const uint8_t* k;
   const uint8_t* v;
@@ -106,6 +98,7 @@ extern "C" pkv_status pkv_stream_tiles(const void* k_cache, const void* v_cache,
   if (!k_cache || !v_cache || !tile_rows || !checksum || !aligned16(k_cache) || !aligned16(v_cache) ||
       (reinterpret_cast<uintptr_t>(tile_rows) & 3u) || (reinterpret_cast<uintptr_t>(checksum) & 3u))
     return PKV_ERR_INVALID_ARG;
+  if (cache->kv_dtype == PKV_FP4_E2M1) return PKV_ERR_UNSUPPORTED;   // its rows are not 16-byte runs
   const int tile_bytes = kRows * cache->head_dim * dtype_bytes(cache->kv_dtype);
   const size_t smem = size_t(kWarps) * kStages * 2 * tile_bytes;
   if (smem > 200 * 1024) return PKV_ERR_UNSUPPORTED;

@@ -1,0 +1,389 @@
+"""GPU parity of the 4-bit cache: written bytes, rows read back, decode over it (plain, fused append,
+no-alloc), block copies, against the float64 oracle (oracle/fp4.py).
+
+Written bytes match the definition bit for bit.  A row read back is code * scale (exact) times the head's
+scale (one fp32 rounding), rounded once: |err| <= u |v| (1 + 2^-12) + 2^-25 (fp16 subnormals), u = finfo.eps / 2.
+
+Decode, with A = sum_j p_j |v_j|: P is rounded to fp16 (2^-11); scores are fp32 sums of exact fp16 products of
+at most 128 terms, scaled: an error of the exponent below 2^-24 * 128 * scale * sum |q k|, under 2^-12 for the
+inputs here (scale * sum |q k| < 32); exp2 and the fp32 sums add less than 2^-14; partials merge in fp32.  So
+|err| <= 2^-10 A + u |out| + 2^-25.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import fp4, prompt
+from oracle.formats import e4m3_table
+
+pytestmark = pytest.mark.gpu
+DT = {"bf16": torch.bfloat16, "f16": torch.float16}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+
+
+def _tables(rng, lens, block, num_blocks, extra=1):
+    need = [-(-n // block) for n in lens]
+    ids = list(rng.permutation(num_blocks)[: sum(need)])
+    width = max(need + [1]) + extra
+    t = np.full((len(lens), width), -1, dtype=np.int32)
+    for i, n in enumerate(need):
+        t[i, :n] = [ids.pop() for _ in range(n)]
+    return t
+
+
+def _pool(rng, num_blocks, heads, block, dim):
+    if num_blocks > 2000:                                      # codes and scales as they come
+        return (rng.integers(0, 16, (num_blocks, heads, block, dim)).astype(np.uint8),
+                rng.integers(0x28, 0x34, (num_blocks, heads, block, dim // 16)).astype(np.uint8))
+    x = rng.standard_normal((num_blocks, heads, block, dim)) * np.exp(0.3 * rng.standard_normal((num_blocks, heads, 1, 1)))
+    return fp4.quantise(x)
+
+
+def _rows(codes, sc, table, length, block, scale):
+    """float64 [length, heads, D] of one sequence."""
+    pos = np.arange(length)
+    at = (table[pos // block], slice(None), pos % block)
+    r = fp4.values(codes[at], sc[at])
+    return r if scale is None else r * scale.astype(np.float64)[:, None]
+
+
+def _close(got, ref, bound):
+    err = np.abs(got.double().cpu().numpy() - ref)
+    assert (err <= bound).all(), (float(np.nanmax(err / bound)), np.argwhere(~(err <= bound))[:3])
+
+
+# ---------------------------------------------------------------------------------------
+# write
+# ---------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("dim,heads,block,scaled", [(128, 4, 16, True), (128, 3, 32, False), (64, 5, 16, False),
+                                                    (64, 1, 32, True), (96, 2, 48, True), (16, 2, 16, False)])
+def test_written_bytes_are_the_definitions(dtype, dim, heads, block, scaled):
+    import paged_kv_cache_160_gb300 as pkv
+    rng = np.random.default_rng(dim + heads)
+    nb, tokens = 9, 61
+    pool = [rng.integers(0, 256, pkv.fp4_cache_shape(nb, heads, block, dim)).astype(np.uint8) for _ in range(2)]
+    x = [torch.from_numpy(rng.standard_normal((tokens, heads, dim)) * np.exp(2 * rng.standard_normal((tokens, heads, 1))))
+         .to(DT[dtype]) for _ in range(2)]
+    x[0][0, 0, :5] = torch.tensor([1e30, -1e30, float("inf"), -float("inf"), 0.0])
+    x[0][1, 0, 7] = float("nan")
+    x[1][2, 0] = 0.0
+    x[1][3, 0] = 2.0 ** -14
+    x[1][4, 0, 3] = -0.0
+    # quotients on the borders between codes: with a 6 in the group and no head scale, u / s = u
+    x[0][5, 0, :8] = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0])
+    x[0][5, 0, 8:16] = -x[0][5, 0, :8]
+    slots = rng.permutation(nb * block)[:tokens].astype(np.int64)
+    slots[[10, 20]] = -1
+    scales = [(0.3 + 2 * rng.random(heads)).astype(np.float32) if scaled else None for _ in range(2)]
+    dev = [torch.from_numpy(p).cuda() for p in pool]
+    desc = pkv.cache_desc_fp4(dev[0], *(torch.from_numpy(s).cuda() if scaled else None for s in scales))
+    pkv.pkv_kv_write(x[0].cuda(), x[1].cuda(), torch.from_numpy(slots).cuda(), *dev, desc)
+    assert pkv.pkv_get_device_error() == 0
+    live = slots >= 0
+    for xs, p, got, hs in zip(x, pool, dev, scales):
+        codes, sc = fp4.unpack(p)
+        want_c, want_s = fp4.quantise(xs.double().numpy(), hs)
+        nan = (want_s == 0x7F)[..., None] & np.ones(16, bool)
+        blk, off = slots[live] // block, slots[live] % block
+        codes[blk, :, off], sc[blk, :, off] = want_c[live], want_s[live]
+        gc, gs = fp4.unpack(got.cpu().numpy())
+        assert np.array_equal(gs, sc)
+        # the codes of a NaN group stand for nothing
+        hole = np.zeros(codes.shape, bool)
+        hole[blk, :, off] = nan.reshape(want_c.shape)[live]
+        assert np.array_equal(gc[~hole], codes[~hole])
+
+
+def test_many_tokens_and_a_bad_slot():
+    import paged_kv_cache_160_gb300 as pkv
+    rng = np.random.default_rng(1)
+    heads, dim, block, nb = 2, 128, 16, 400
+    x = torch.randn((6000, heads, dim), generator=torch.Generator().manual_seed(1)).to(torch.bfloat16)
+    slots = torch.from_numpy(rng.permutation(nb * block)[:6000].astype(np.int64))
+    slots[77] = nb * block
+    k = torch.zeros(pkv.fp4_cache_shape(nb, heads, block, dim), dtype=torch.uint8, device="cuda")
+    v = torch.zeros_like(k)
+    pkv.pkv_kv_write(x.cuda(), x.flip(0).contiguous().cuda(), slots.cuda(), k, v, pkv.cache_desc_fp4(k))
+    assert pkv.pkv_get_device_error() == pkv.DEVERR["slot"]
+    keep = np.arange(6000) != 77
+    blk, off = slots.numpy()[keep] // block, slots.numpy()[keep] % block
+    for got, xs in ((k, x), (v, x.flip(0))):
+        gc, gs = fp4.unpack(got.cpu().numpy())
+        wc, ws = fp4.quantise(xs.double().numpy()[keep])
+        assert np.array_equal(gc[blk, :, off], wc) and np.array_equal(gs[blk, :, off], ws)
+
+
+# ---------------------------------------------------------------------------------------
+# read
+# ---------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("out", ["bf16", "f16"])
+@pytest.mark.parametrize("dim,heads,block,scaled", [(128, 4, 16, True), (64, 3, 32, False), (96, 2, 16, True)])
+@pytest.mark.parametrize("lens", [[1], [0, 17, 0, 16, 300, 1], [33, 64, 5]])
+def test_read_back(lens, dim, heads, block, scaled, out):
+    import paged_kv_cache_160_gb300 as pkv
+    rng = np.random.default_rng(sum(lens) + dim)
+    nb = sum(-(-n // block) for n in lens) + 3
+    table = _tables(rng, lens, block, nb)
+    pools = [_pool(rng, nb, heads, block, dim) for _ in range(2)]
+    scales = [(0.3 + 2 * rng.random(heads)).astype(np.float32) if scaled else None for _ in range(2)]
+    dev = [torch.from_numpy(fp4.pack(*p)).cuda() for p in pools]
+    desc = pkv.cache_desc_fp4(dev[0], *(torch.from_numpy(s).cuda() if scaled else None for s in scales))
+    total = sum(lens)
+    outs = [torch.full((total + 5, heads, dim), 9.0, dtype=DT[out], device="cuda") for _ in range(2)]
+    pkv.pkv_kv_read(*outs, torch.tensor(np.cumsum([0] + lens), dtype=torch.int32, device="cuda"),
+                    torch.from_numpy(table).cuda(), *dev, desc)
+    assert pkv.pkv_get_device_error() == 0
+    u = torch.finfo(DT[out]).eps / 2
+    for o, p, hs in zip(outs, pools, scales):
+        assert (o[total:] == 9.0).all()
+        ref = np.concatenate([_rows(*p, table[i], n, block, hs) for i, n in enumerate(lens)])
+        _close(o[:total], ref, u * np.abs(ref) * (1 + 2.0 ** -12) + 2.0 ** -25)
+
+
+def test_read_back_of_16_bit_and_e4m3_caches():
+    import paged_kv_cache_160_gb300 as pkv
+    rng = np.random.default_rng(8)
+    lens, block, heads, dim = [20, 1, 47], 16, 3, 128
+    table = _tables(rng, lens, block, 9)
+    cu = torch.tensor(np.cumsum([0] + lens), dtype=torch.int32, device="cuda")
+    pos = np.concatenate([np.arange(n) for n in lens])
+    blk = np.concatenate([table[i, np.arange(n) // block] for i, n in enumerate(lens)])
+    for dt in (torch.bfloat16, torch.float16):
+        k = torch.randn((9, heads, block, dim), generator=torch.Generator().manual_seed(2)).to(dt)
+        v = k.flip(0).contiguous()
+        ko, vo = (torch.empty((sum(lens), heads, dim), dtype=dt, device="cuda") for _ in range(2))
+        kc = k.cuda()
+        pkv.pkv_kv_read(ko, vo, cu, torch.from_numpy(table).cuda(), kc, v.cuda(), pkv.cache_desc(kc))
+        assert torch.equal(ko.cpu(), k[blk, :, pos % block]) and torch.equal(vo.cpu(), v[blk, :, pos % block])
+    codes = rng.integers(0, 256, (2, 9, heads, block, dim)).astype(np.uint8)
+    codes[(codes & 0x7F) == 0x7F] = 0
+    hs = (0.5 + rng.random((2, heads))).astype(np.float32)
+    kc, vc = (torch.from_numpy(c).cuda() for c in codes)
+    desc = pkv.cache_desc(kc, *(torch.from_numpy(s).cuda() for s in hs))
+    for dt in (torch.bfloat16, torch.float16):
+        outs = [torch.empty((sum(lens), heads, dim), dtype=dt, device="cuda") for _ in range(2)]
+        pkv.pkv_kv_read(*outs, cu, torch.from_numpy(table).cuda(), kc, vc, desc)
+        for o, c, s in zip(outs, codes, hs):
+            ref = e4m3_table()[c][blk, :, pos % block] * s.astype(np.float64)[:, None]
+            _close(o, ref, torch.finfo(dt).eps / 2 * np.abs(ref) * (1 + 2.0 ** -12) + 2.0 ** -25)
+    assert pkv.pkv_get_device_error() == 0
+
+
+def test_read_back_reports_bad_blocks_and_lengths():
+    import paged_kv_cache_160_gb300 as pkv
+    heads, dim = 2, 64
+    k = torch.zeros(pkv.fp4_cache_shape(4, heads, 16, dim), dtype=torch.uint8, device="cuda")
+    desc = pkv.cache_desc_fp4(k)
+
+    def read(cu, table, total=40):
+        o = torch.full((total, heads, dim), 3.0, dtype=torch.bfloat16, device="cuda")
+        v = o.clone()
+        pkv.pkv_kv_read(o, v, torch.tensor(cu, dtype=torch.int32, device="cuda"),
+                        torch.tensor(table, dtype=torch.int32, device="cuda"), k, k, desc)
+        err = pkv.pkv_get_device_error()
+        assert torch.equal(o, v)
+        return (o[:, 0, 0] == 3.0).tolist(), err
+
+    left, err = read([0, 20, 40], [[0, 4], [1, 2]])           # block 4 does not exist: rows 16 .. 19
+    assert err == pkv.DEVERR["block_id"] and left == [16 <= i < 20 for i in range(40)]
+    left, err = read([0, 40], [[0, 1]])                       # two blocks hold 32 rows
+    assert err == pkv.DEVERR["chunk"] and left == [i >= 32 for i in range(40)]
+    left, err = read([0, 20, 10, 30], [[0, 1], [1, 2], [2, 3]])
+    assert err & pkv.DEVERR["chunk"] and left[30:] == [True] * 10
+    left, err = read([0, 50], [[0, 1, 2, 3]])                 # more rows than the output has
+    assert err == pkv.DEVERR["chunk"] and not any(left)
+    left, err = read([0, 40], [[0, -1, 1]])
+    assert err == pkv.DEVERR["block_id"] and left == [16 <= i < 32 for i in range(40)]
+
+
+# ---------------------------------------------------------------------------------------
+# decode
+# ---------------------------------------------------------------------------------------
+
+def _decode_case(seed, lens, hq, hkv, dim, block, scaled, nan_rest=True):
+    rng = np.random.default_rng(seed)
+    nb = sum(-(-n // block) for n in lens) + 3
+    table = _tables(rng, lens, block, nb)
+    pools = [_pool(rng, nb, hkv, block, dim) for _ in range(2)]
+    if nan_rest:                                               # rows that hold no token are NaN
+        used = np.zeros((nb, block), bool)
+        for i, n in enumerate(lens):
+            pos = np.arange(n)
+            used[table[i, pos // block], pos % block] = True
+        for codes, sc in pools:
+            sc[~used[:, None, :].repeat(hkv, 1)] = 0x7F
+    scales = [(0.5 + rng.random(hkv)).astype(np.float32) if scaled else None for _ in range(2)]
+    return rng, table, pools, scales
+
+
+def _bound(out, size, dtype):
+    return 2.0 ** -10 * size + torch.finfo(dtype).eps / 2 * np.abs(out) + 2.0 ** -25
+
+
+def _run_decode(lens, hq, hkv, dim, dtype, block=16, part=0, scaled=True, seed=0, entry="plain", max_len=None, clip=None):
+    import paged_kv_cache_160_gb300 as pkv
+    rng, table, pools, scales = _decode_case(seed, lens, hq, hkv, dim, block, scaled)
+    dev = [torch.from_numpy(fp4.pack(*p)).cuda() for p in pools]
+    desc = pkv.cache_desc_fp4(dev[0], *(torch.from_numpy(s).cuda() if scaled else None for s in scales))
+    q = torch.from_numpy(rng.standard_normal((len(lens), hq, dim))).to(DT[dtype])
+    out = torch.full(q.shape, float("nan"), dtype=DT[dtype], device="cuda")
+    longest = max_len if max_len is not None else max(lens + [1])
+    ws = torch.full((pkv.pkv_decode_workspace_bytes(len(lens), hq, hkv, dim, block, longest, part),), 0xFF,
+                    dtype=torch.uint8, device="cuda")
+    args = (out, q.cuda(), *dev, desc, torch.from_numpy(table).cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"),
+            longest, dim ** -0.5, part)
+    if entry == "noalloc":
+        pkv.pkv_paged_decode_noalloc(*args)
+    else:
+        pkv.pkv_paged_decode(*args, ws)
+    assert pkv.pkv_get_device_error() == 0
+    k, v = (np.concatenate([_rows(*p, table[i], n, block, s) for i, n in enumerate(lens)]) for p, s in zip(pools, scales))
+    ref, size = prompt.prompt_attention(q.double().numpy(), k, v, [1] * len(lens), lens, dim ** -0.5)
+    _close(out, ref, _bound(ref, size, DT[dtype]))
+    return out
+
+
+RAGGED = [1, 15, 16, 17, 31, 32, 33, 255, 700]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("hq,hkv", [(4, 4), (8, 1), (6, 2), (28, 4), (5, 1), (10, 5)])
+def test_decode_groups(hq, hkv, dim, dtype):
+    _run_decode(RAGGED, hq, hkv, dim, dtype, seed=hq + dim)
+
+
+@pytest.mark.parametrize("block", [16, 32])
+@pytest.mark.parametrize("part", [0, 16, 48, 512])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_decode_blocks_and_partitions(dim, part, block):
+    _run_decode(RAGGED + [2049], 8, 2, dim, "bf16", block=block, part=part, scaled=part % 32 == 0, seed=part)
+
+
+@pytest.mark.parametrize("lens", [[1], [16], [0], [0, 5, 0], [4000], [3, 9000], [1] * 300, [40] * 65])
+def test_decode_lengths(lens):
+    _run_decode(lens, 7, 1, 128, "f16", seed=len(lens))
+
+
+def test_decode_large_batch_takes_the_four_warp_layout():
+    """12 prefix bytes per sequence next to 12 warps' stages: past about 9,900 sequences four warps run."""
+    rng = np.random.default_rng(4)
+    _run_decode([int(n) for n in rng.integers(1, 20, 11000)], 1, 1, 128, "bf16", seed=5)
+
+
+def test_decode_no_alloc_is_bit_identical():
+    a = _run_decode(RAGGED, 8, 2, 128, "bf16", seed=9)
+    b = _run_decode(RAGGED, 8, 2, 128, "bf16", seed=9, entry="noalloc")
+    assert torch.equal(a, b)
+
+
+def test_decode_under_an_sm_budget():
+    import paged_kv_cache_160_gb300 as pkv
+    try:
+        for n in (1, 7, 66):
+            pkv.pkv_set_decode_sm_budget(n)
+            _run_decode(RAGGED, 8, 2, 128, "f16", seed=10)
+    finally:
+        pkv.pkv_set_decode_sm_budget(0)
+
+
+def test_decode_reports_bad_blocks_and_lengths():
+    import paged_kv_cache_160_gb300 as pkv
+    k = torch.zeros(pkv.fp4_cache_shape(4, 1, 16, 64), dtype=torch.uint8, device="cuda")
+    desc = pkv.cache_desc_fp4(k)
+    q = torch.ones((2, 1, 64), dtype=torch.float16, device="cuda")
+    out = torch.empty_like(q)
+    ws = torch.empty(pkv.pkv_decode_workspace_bytes(2, 1, 1, 64, 16, 64, 0), dtype=torch.uint8, device="cuda")
+    for table, lens, bit in (([[0, 4], [1, 2]], [20, 20], "block_id"), ([[0, 1], [2, 3]], [33, 5], "context_len")):
+        pkv.pkv_paged_decode(out, q, k, k, desc, torch.tensor(table, dtype=torch.int32, device="cuda"),
+                             torch.tensor(lens, dtype=torch.int32, device="cuda"), 64, 0.125, 0, ws)
+        assert pkv.pkv_get_device_error() == pkv.DEVERR[bit]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("dim,block,scaled", [(128, 16, True), (128, 32, False), (64, 16, False), (64, 32, True)])
+def test_append_equals_write_then_decode(dim, block, scaled, dtype):
+    import paged_kv_cache_160_gb300 as pkv
+    lens, hq, hkv = [1, 16, 17, 32, 33, 500, 0, 2048], 8, 2
+    rng, table, pools, scales = _decode_case(3, lens, hq, hkv, dim, block, scaled)
+    host = [torch.from_numpy(fp4.pack(*p)) for p in pools]
+    sc = [torch.from_numpy(s).cuda() if scaled else None for s in scales]
+    q, kn, vn = (torch.from_numpy(rng.standard_normal((len(lens), h, dim)) * 2).to(DT[dtype]).cuda() for h in (hq, hkv, hkv))
+    slots = torch.tensor([int(table[i, (n - 1) // block]) * block + (n - 1) % block if n else -1
+                          for i, n in enumerate(lens)], device="cuda")
+    tab, ln = torch.from_numpy(table).cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda")
+    ws = torch.empty(pkv.pkv_decode_workspace_bytes(len(lens), hq, hkv, dim, block, 2048, 0), dtype=torch.uint8, device="cuda")
+    got = []
+    for fused in (False, True):
+        k, v = host[0].cuda(), host[1].cuda()
+        desc = pkv.cache_desc_fp4(k, *sc)
+        out = torch.empty_like(q)
+        tail = (tab, ln, 2048, dim ** -0.5, 0, ws)
+        if fused:
+            pkv.pkv_paged_decode_append(out, q, kn, vn, k, v, desc, *tail)
+        else:
+            pkv.pkv_kv_write(kn, vn, slots, k, v, desc)
+            pkv.pkv_paged_decode(out, q, k, v, desc, *tail)
+        assert pkv.pkv_get_device_error() == 0
+        got.append((out, k, v))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    assert torch.isfinite(got[0][0]).all()
+
+
+def test_copies_and_swaps_move_whole_4_bit_blocks():
+    import paged_kv_cache_160_gb300 as pkv
+    rng = np.random.default_rng(12)
+    shape = pkv.fp4_cache_shape(8, 3, 32, 64)
+    k, v = (torch.from_numpy(rng.integers(0, 256, shape).astype(np.uint8)) for _ in range(2))
+    dk, dv = k.cuda(), v.cuda()
+    desc = pkv.cache_desc_fp4(dk)
+    pkv.pkv_copy_blocks(dk, dv, desc, torch.tensor([[0, 5], [7, 2]], dtype=torch.int32, device="cuda"))
+    wk, wv = k.clone(), v.clone()
+    for t in (wk, wv):
+        t[5], t[2] = t[0].clone(), t[7].clone()
+    assert torch.equal(dk.cpu(), wk) and torch.equal(dv.cpu(), wv)
+    hk, hv = torch.zeros((2,) + shape[1:], dtype=torch.uint8).pin_memory(), torch.zeros((2,) + shape[1:], dtype=torch.uint8).pin_memory()
+    pkv.pkv_swap_blocks(hk, hv, dk, dv, desc, torch.tensor([[3, 0], [5, 1]], dtype=torch.int32, device="cuda"))
+    assert pkv.pkv_get_device_error() == 0
+    assert torch.equal(hk, wk[[3, 5]]) and torch.equal(hv, wv[[3, 5]])
+
+
+def test_write_read_decode_captured_and_replayed():
+    import paged_kv_cache_160_gb300 as pkv
+    rng, table, pools, _ = _decode_case(21, [100, 40], 4, 2, 128, 16, False)
+    k, v = (torch.from_numpy(fp4.pack(*p)).cuda() for p in pools)
+    desc = pkv.cache_desc_fp4(k)
+    q, kn, vn = (torch.from_numpy(rng.standard_normal((2, h, 128))).to(torch.bfloat16).cuda() for h in (4, 2, 2))
+    tab, lens = torch.from_numpy(table).cuda(), torch.tensor([100, 40], dtype=torch.int32, device="cuda")
+    slots = torch.tensor([int(table[0, 6]) * 16 + 3, int(table[1, 2]) * 16 + 7], device="cuda")
+    cu = torch.tensor([0, 100, 140], dtype=torch.int32, device="cuda")
+    out, ko, vo = torch.empty_like(q), *(torch.empty((140, 2, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    ws = torch.empty(pkv.pkv_decode_workspace_bytes(2, 4, 2, 128, 16, 100, 0), dtype=torch.uint8, device="cuda")
+
+    def step():
+        pkv.pkv_kv_write(kn, vn, slots, k, v, desc)
+        pkv.pkv_kv_read(ko, vo, cu, tab, k, v, desc)
+        pkv.pkv_paged_decode(out, q, k, v, desc, tab, lens, 100, 0.09, 0, ws)
+
+    step()
+    torch.cuda.synchronize()
+    eager = [t.clone() for t in (out, ko, vo)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(3):
+        for t in (out, ko, vo):
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip((out, ko, vo), eager))
+    assert pkv.pkv_get_device_error() == 0

@@ -1,0 +1,186 @@
+"""GPU parity of pkv_prompt_attention against float64.
+
+With A = sum_j p_j |v_j| and u = finfo.eps / 2 of the type: P is rounded to the type (u A); scores are fp32 sums of
+at most 128 exact products, an error of the exponent below 2^-24 * 128 * scale * sum |q k| (under 2^-12 here); the
+row maximum may trail by 2^8, which costs nothing in floating point; exp2 and the fp32 sums add less than 2^-13.
+So |err| <= (u + 2^-11) A + u |out| + 2^-25.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import prompt
+
+pytestmark = pytest.mark.gpu
+DT = {"bf16": torch.bfloat16, "f16": torch.float16}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+
+
+def _run(q_lens, k_lens, hq, hkv, dim, dtype, packed=False, seed=0, pad=0, scale=None, spread=1.0):
+    import paged_kv_cache_160_gb300 as pkv
+    dt = DT[dtype]
+    g = torch.Generator().manual_seed(seed + sum(q_lens))
+    tq, tk = sum(q_lens), sum(k_lens)
+    scale = dim ** -0.5 if scale is None else scale
+    if packed:
+        assert q_lens == k_lens
+        qkv = (spread * torch.randn((tq + pad, hq + 2 * hkv, dim), generator=g)).to(dt)
+        qkv[tq:] = float("nan")
+        dev = qkv.cuda().split([hq, hkv, hkv], 1)
+        q, k, v = (t[:tq] for t in qkv.split([hq, hkv, hkv], 1))
+    else:
+        q, k, v = ((spread * torch.randn((n + pad, h, dim), generator=g)).to(dt)
+                   for n, h in ((tq, hq), (tk, hkv), (tk, hkv)))
+        q[tq:] = float("nan")
+        k[tk:] = float("nan")
+        v[tk:] = float("inf")
+        dev = [t.cuda() for t in (q, k, v)]
+        q, k, v = q[:tq], k[:tk], v[:tk]
+    out = torch.full((tq + pad, hq, dim), 5.0, dtype=dt, device="cuda")
+    cu = [torch.tensor(np.cumsum([0] + n), dtype=torch.int32, device="cuda") for n in (q_lens, k_lens)]
+    pkv.pkv_prompt_attention(out, *dev, *cu, max(q_lens + [1]), scale)
+    assert pkv.pkv_get_device_error() == 0
+    assert (out[tq:] == 5.0).all()
+    ref, size = prompt.prompt_attention(*(t.double().numpy() for t in (q, k, v)), q_lens, k_lens, scale)
+    u = torch.finfo(dt).eps / 2
+    err = np.abs(out[:tq].double().cpu().numpy() - ref)
+    bound = (u + 2.0 ** -11) * size + u * np.abs(ref) + 2.0 ** -25
+    assert (err <= bound).all(), (float(np.nanmax(err / bound)), np.argwhere(~(err <= bound))[:3])
+    return out
+
+
+@pytest.mark.parametrize("n", [1, 2, 127, 128, 129, 255, 256, 257, 400])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_one_prompt(n, dim):
+    _run([n], [n], 4, 2, dim, "bf16", pad=3)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (2, 1), (3, 1), (4, 4), (7, 1), (6, 2), (9, 3)])
+def test_groups(hq, hkv, dim, dtype):
+    _run([300, 1, 129], [300, 1, 129], hq, hkv, dim, dtype, packed=True, seed=hq)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_packed_sequences_with_empty_ones(dtype):
+    lens = [0, 5, 0, 0, 130, 64, 1, 200, 0]
+    _run(lens, lens, 3, 1, 128, dtype, pad=70)
+    _run(lens, lens, 4, 2, 64, dtype, packed=True, pad=200)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("q_lens,k_lens", [([1], [1000]), ([7], [300]), ([128, 3], [256, 131]), ([140], [500]),
+                                           ([1, 1, 1], [1, 128, 129]), ([200], [201])])
+def test_chunks_after_a_history(q_lens, k_lens, dim):
+    _run(q_lens, k_lens, 6, 2, dim, "bf16", pad=9)
+    _run(q_lens, k_lens, 3, 3, dim, "f16")
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_rows_without_keys_are_zero(dim):
+    out = _run([10, 300, 4], [3, 40, 0], 2, 1, dim, "bf16")
+    assert (out[:7] == 0).all() and (out[10:270] == 0).all() and (out[310:] == 0).all()
+    out = _run([300, 150], [40, 0], 1, 1, dim, "f16")
+    assert (out[:260] == 0).all() and (out[300:] == 0).all()
+
+
+def test_no_keys_at_all():
+    _run([5, 0], [0, 0], 4, 2, 128, "bf16")
+
+
+def test_large_scores_and_growing_maxima():
+    """Rows whose maximum rises tile after tile (every rescaling path), and scores of several hundred."""
+    import paged_kv_cache_160_gb300 as pkv
+    n, dim = 700, 128
+    q = torch.ones((n, 2, dim))
+    k = (torch.arange(n).view(n, 1, 1) / 64.0 + 0.125 * torch.randn((n, 1, dim), generator=torch.Generator().manual_seed(3)))
+    v = torch.randn((n, 1, dim), generator=torch.Generator().manual_seed(4))
+    q, k, v = (t.to(torch.bfloat16).contiguous() for t in (q, k, v))
+    ref, size = prompt.prompt_attention(*(t.double().numpy() for t in (q, k, v)), [n], [n], 0.25)
+    out = torch.empty((n, 2, dim), dtype=torch.bfloat16, device="cuda")
+    cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    pkv.pkv_prompt_attention(out, q.cuda(), k.cuda(), v.cuda(), cu, cu, n, 0.25)
+    assert pkv.pkv_get_device_error() == 0
+    # the exponent's error: 2^-24 * 128 * 0.25 * 128 * 11 (the largest |q k| sums) < 2^-8.5
+    u = torch.finfo(torch.bfloat16).eps / 2
+    err = np.abs(out.double().cpu().numpy() - ref)
+    assert (err <= (u + 2.0 ** -8) * size + u * np.abs(ref)).all()
+
+
+def test_a_rows_result_does_not_depend_on_its_neighbours():
+    """A sequence alone, and between others in one batch, bit for bit; and twice the same."""
+    import paged_kv_cache_160_gb300 as pkv
+    g = torch.Generator().manual_seed(9)
+    lens = [77, 333, 260]
+    q, k, v = (torch.randn((sum(lens), h, 128), generator=g).to(torch.bfloat16).cuda() for h in (4, 2, 2))
+
+    def run(a, b):
+        n = [x for x in lens[a:b]]
+        s, e = sum(lens[:a]), sum(lens[:b])
+        cu = torch.tensor(np.cumsum([0] + n), dtype=torch.int32, device="cuda")
+        out = torch.empty_like(q[s:e])
+        pkv.pkv_prompt_attention(out, q[s:e], k[s:e], v[s:e], cu, cu, max(n), 0.1)
+        return out
+
+    whole = run(0, 3)
+    assert torch.equal(whole, run(0, 3))
+    assert torch.equal(whole[77:410], run(1, 2)) and torch.equal(whole[410:], run(2, 3))
+
+
+def test_inconsistent_lengths_are_flagged():
+    import paged_kv_cache_160_gb300 as pkv
+    q = torch.randn((300, 2, 64), generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).cuda()
+    k = q[:, :1].contiguous()
+
+    def run(cu_q, cu_k, max_q=300):
+        out = torch.full_like(q, 4.0)
+        pkv.pkv_prompt_attention(out, q, k, k, *(torch.tensor(c, dtype=torch.int32, device="cuda") for c in (cu_q, cu_k)),
+                                 max_q, 0.125)
+        return (out[:, 0, 0] != 4.0).tolist(), pkv.pkv_get_device_error()
+
+    good, err = run([0, 100, 300], [0, 100, 300])
+    assert err == 0 and all(good)
+    wrote, err = run([0, 100, 301], [0, 100, 300])             # past total_q: that sequence is left
+    assert err == pkv.DEVERR["chunk"] and wrote == [i < 100 for i in range(300)]
+    wrote, err = run([0, 100, 300], [0, 100, 50])
+    assert err == pkv.DEVERR["chunk"] and wrote == [i < 100 for i in range(300)]
+    wrote, err = run([0, 300], [0, 300], max_q=128)            # rows past the promised bound stay unwritten
+    assert err == pkv.DEVERR["chunk"] and wrote == [i < 128 for i in range(300)]
+
+
+def test_host_memory_is_refused():
+    import paged_kv_cache_160_gb300 as pkv
+    q = torch.zeros((4, 1, 64), dtype=torch.bfloat16, device="cuda")
+    h = torch.zeros((4, 1, 64), dtype=torch.bfloat16).pin_memory()
+    cu = torch.tensor([0, 4], dtype=torch.int32, device="cuda")
+    a = (1, cu.data_ptr(), cu.data_ptr(), 1, 4, 4, 4, 1, 1, 64, 64, 64, 64, 64, 0.1, 0)
+    L = pkv.lib.pkv_prompt_attention
+    assert L(q.data_ptr(), h.data_ptr(), q.data_ptr(), q.data_ptr(), *a) == 1
+    assert L(q.data_ptr(), q.data_ptr(), h.data_ptr(), q.data_ptr(), *a) == 1
+    assert L(q.data_ptr(), q.data_ptr(), q.data_ptr(), h.data_ptr(), *a) == 1
+
+
+def test_captured_and_replayed():
+    import paged_kv_cache_160_gb300 as pkv
+    g = torch.Generator().manual_seed(11)
+    lens = [200, 64, 391]
+    q, k, v = (torch.randn((sum(lens), h, 128), generator=g).half().cuda() for h in (6, 2, 2))
+    cu = torch.tensor(np.cumsum([0] + lens), dtype=torch.int32, device="cuda")
+    out = torch.empty_like(q)
+    pkv.pkv_prompt_attention(out, q, k, v, cu, cu, 391, 0.09)
+    torch.cuda.synchronize()
+    eager, graph = out.clone(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(2):
+            pkv.pkv_prompt_attention(out, q, k, v, cu, cu, 391, 0.09)
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, eager)

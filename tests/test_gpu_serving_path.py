@@ -1,0 +1,113 @@
+"""The operators together, as a server runs them over a 4-bit cache: a prompt (rotation and norms, attention
+over its own rows, write), a second chunk (its history read back, attention over both), then decode steps with
+the fused append.  Each stage's result is compared with float64 on the inputs that stage had, and the cache with
+the bytes the definition gives.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import fp4, prompt, rotary
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+
+
+def _close(got, ref, bound):
+    err = np.abs(got.double().cpu().numpy() - ref)
+    assert (err <= bound).all(), float(np.nanmax(err / bound))
+
+
+@pytest.mark.parametrize("dim,hq,hkv,block,dtype", [(128, 4, 2, 16, torch.bfloat16), (64, 3, 1, 32, torch.float16)])
+def test_prompt_chunk_and_decode_steps(dim, hq, hkv, block, dtype):
+    import paged_kv_cache_160_gb300 as pkv
+    u = torch.finfo(dtype).eps / 2
+    g = torch.Generator().manual_seed(dim)
+    scale, base, rot = dim ** -0.5, 10000.0, dim // 2
+    freq = rotary.frequencies(rot, base)
+    table = pkv.pkv_rope_table(rot, base).cuda()
+    wq, wk = ((1 + 0.2 * torch.randn(dim, generator=g)).to(dtype) for _ in range(2))
+    prompts, chunks = [37, 130], [65, 9]
+    bm = pkv.BlockManager(64, block)
+    k_cache = torch.full(pkv.fp4_cache_shape(64, hkv, block, dim), 0x7F, dtype=torch.uint8, device="cuda")
+    v_cache = torch.full_like(k_cache, 0x7F)
+    hs = [torch.tensor([0.7 + 0.4 * h for h in range(hkv)], device="cuda") for _ in range(2)]
+    desc = pkv.cache_desc_fp4(k_cache, *hs)
+    width = 16
+    stored = [[], []]                                  # the rows each sequence got, per sequence: (k, v) tensors
+
+    def project(n, starts):
+        """A packed projection of n[i] rows of each sequence, rotated: q, k (normed, rotated), v."""
+        qkv = torch.randn((sum(n), hq + 2 * hkv, dim), generator=g).to(dtype).cuda()
+        pos = np.concatenate([np.arange(s, s + m) for s, m in zip(starts, n)])
+        q, k, v = qkv.split([hq, hkv, hkv], 1)
+        q0, k0 = q.double().cpu().numpy(), k.double().cpu().numpy()
+        pkv.pkv_qk_rotary(q, q, k, k, torch.tensor(pos, dtype=torch.int32, device="cuda"), table, "half", 1.0,
+                          wq.cuda(), wk.cuda(), 1e-6)
+        for got, x, w in ((q, q0, wq), (k, k0, wk)):
+            ref, size = rotary.rotate(rotary.rms_norm(x, w.double().numpy(), 1e-6), pos, freq, "half")
+            _close(got, ref, u * np.abs(ref) + 2.0 ** -18 * size + 2.0 ** -25)
+        return q, k, v.contiguous()
+
+    def attend(q, k, v, q_lens, k_lens):
+        out = torch.empty((sum(q_lens), hq, dim), dtype=dtype, device="cuda")
+        cu = [torch.tensor(np.cumsum([0] + n), dtype=torch.int32, device="cuda") for n in (q_lens, k_lens)]
+        pkv.pkv_prompt_attention(out, q, k, v, *cu, max(q_lens), scale)
+        ref, size = prompt.prompt_attention(*(t.double().cpu().numpy() for t in (q, k, v)), q_lens, k_lens, scale)
+        _close(out, ref, (u + 2.0 ** -11) * size + u * np.abs(ref) + 2.0 ** -25)
+
+    def write(k, v, n):
+        slots = np.concatenate([bm.append_slots(i, m)[0] for i, m in enumerate(n)])
+        pkv.pkv_kv_write(k.contiguous(), v, torch.tensor(slots, dtype=torch.int64, device="cuda"), k_cache, v_cache, desc)
+        at = 0
+        for i, m in enumerate(n):
+            stored[i].append((k[at:at + m].cpu(), v[at:at + m].cpu()))
+            at += m
+
+    def history(i):
+        """float64 values of what sequence i's cache has to hold."""
+        return [fp4.values(*fp4.quantise(torch.cat(part).double().numpy(), s.cpu().numpy()))
+                * s.double().cpu().numpy()[:, None] for part, s in zip(zip(*stored[i]), hs)]
+
+    # the prompts attend their own fresh rows, which then go into the cache
+    for i in range(2):
+        bm.allocate(i, 0)
+    q, k, v = project(prompts, [0, 0])
+    attend(q, k, v, prompts, prompts)
+    write(k, v, prompts)
+    # a chunk behind each: its history comes back from the cache and takes the chunk's rows behind it
+    tables, lens = bm.export([0, 1], width)
+    assert lens == prompts
+    q, k, v = project(chunks, prompts)
+    hist = [torch.empty((sum(prompts), hkv, dim), dtype=dtype, device="cuda") for _ in range(2)]
+    pkv.pkv_kv_read(*hist, torch.tensor(np.cumsum([0] + prompts), dtype=torch.int32, device="cuda"),
+                    torch.tensor(tables, dtype=torch.int32, device="cuda"), k_cache, v_cache, desc)
+    for got, refs in zip(hist, zip(history(0), history(1))):
+        ref = np.concatenate(refs)
+        _close(got, ref, u * np.abs(ref) * (1 + 2.0 ** -12) + 2.0 ** -25)
+    both = [torch.cat([h[:37], x[:65], h[37:], x[65:]]) for h, x in zip(hist, (k, v))]
+    attend(q, *both, chunks, [p + c for p, c in zip(prompts, chunks)])
+    write(k, v, chunks)
+    # decode steps
+    ws = torch.empty(pkv.pkv_decode_workspace_bytes(2, hq, hkv, dim, block, 512, 0), dtype=torch.uint8, device="cuda")
+    for step in range(3):
+        _, _, tables, lens = bm.step_decode([0, 1], width)
+        q, k, v = project([1, 1], [n - 1 for n in lens])
+        out = torch.empty((2, hq, dim), dtype=dtype, device="cuda")
+        q = q.contiguous()
+        pkv.pkv_paged_decode_append(out, q, k.contiguous(), v, k_cache, v_cache, desc,
+                                    torch.tensor(tables, dtype=torch.int32, device="cuda"),
+                                    torch.tensor(lens, dtype=torch.int32, device="cuda"), 512, scale, 0, ws)
+        for i in range(2):
+            stored[i].append((k[i:i + 1].cpu(), v[i:i + 1].cpu()))
+        kk, vv = (np.concatenate(t) for t in zip(*(history(i) for i in range(2))))
+        assert len(kk) == sum(lens)
+        ref, size = prompt.prompt_attention(q.double().cpu().numpy(), kk, vv, [1, 1], lens, scale)
+        # scores of normed rows: scale * sum |q k| < 32, as for the decode's own tests
+        _close(out, ref, 2.0 ** -10 * size + u * np.abs(ref) + 2.0 ** -25)
+    assert pkv.pkv_get_device_error() == 0
