@@ -24,8 +24,8 @@ LIB = os.path.join(PKG, "libpkv.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
               "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]
-SOURCES = ["runtime.cu", "cache_ops.cu", "paged_decode.cu", "paged_decode_noalloc.cu", "prefill_chunk.cu",
-           "prompt_attention.cu", "rotary.cu", "stream_tiles.cu", "block_manager.cpp"]
+SOURCES = ["runtime.cu", "cache_ops.cu", "paged_decode.cu", "paged_decode_fp4.cu",
+           "paged_decode_noalloc.cu", "prefill_chunk.cu", "prompt_attention.cu", "rotary.cu", "stream_tiles.cu", "block_manager.cpp"]
 
 
 def nvcc() -> str:

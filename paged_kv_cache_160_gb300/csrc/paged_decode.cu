@@ -39,110 +39,27 @@
 #include <atomic>
 #include <utility>
 
+#include "decode_split.cuh"
 #include "pkv_device.cuh"
 #include "pkv_host.h"
 
 namespace pkv {
 namespace {
 
-enum { KV_F16 = 0, KV_BF16 = 1, KV_E4M3 = 2, KV_E2M1 = 3 };
-
-constexpr int kBS = 16;        // tokens per tile: a 16-token block, or half of a 32-token one
-constexpr int kMaxWarps = 12;  // worker warps per CTA (3 per SM sub-partition)
-constexpr int kMaxGroup = 8;   // query heads per kv head handled by one n=8 MMA tile
-
 template <int KV, int D>
 struct Cfg {
-  static constexpr bool kFp4 = KV == KV_E2M1;
-  static constexpr bool kQuant = KV == KV_E4M3 || kFp4;          // scaled codes, computed in fp16
-  static constexpr int kElt = KV == KV_E4M3 ? 1 : 2;             // (not for 4-bit tiles)
+  static constexpr int kElt = KV == KV_E4M3 ? 1 : 2;
   static constexpr int kRowBytes = D * kElt;
-  static constexpr int kNBox = kFp4 ? 0 : kRowBytes / 128;       // 128-byte-wide TMA boxes per row
-  // One 16-row K (or V) tile; a 4-bit one holds 16 x D/2 bytes of codes, then 16 x D/16 of scales.
-  static constexpr int kTileBytes = kFp4 ? 9 * D : kBS * kRowBytes;
+  static constexpr int kNBox = kRowBytes / 128;       // 128-byte-wide TMA boxes per row
+  static constexpr int kRowChunks = kRowBytes / 16;   // 16-byte chunks per cache row
+  static constexpr int kTileBytes = kBS * kRowBytes;  // one 16-row K (or V) tile
   static constexpr int kStageBytes = 2 * kTileBytes;
-  // A row's pieces in the fused append, one per lane: 16 bytes of the cache, or 16 elements of a
-  // 4-bit row.
-  static constexpr int kRowChunks = kFp4 ? D / 16 : kRowBytes / 16;
   static constexpr int kKSteps = D / 16;
   static constexpr int kMTiles = D / 16;
-  static constexpr bool kBF16 = KV == KV_BF16;                   // MMA input type (scaled codes compute in fp16)
-  static constexpr int kStages = kFp4 ? 4 : 2;                   // tiles in flight per warp
-  static_assert(kFp4 || kRowBytes == kNBox * 128, "rows must span whole 128-byte swizzle atoms");
+  static constexpr bool kBF16 = KV == KV_BF16;        // MMA input type (e4m3 computes in fp16)
+  static_assert(kRowBytes % 128 == 0, "rows must span whole 128-byte swizzle atoms");
   static_assert(KV != KV_E4M3 || D == 128, "e4m3 path is written for head_dim 128");
 };
-
-// Token of the tile that score row r (0..15) stands for.  The 4-bit path reads V rows t and 7 - t
-// per thread quad instead of 2t and 2t + 1, which spreads a warp's row reads over all banks; the
-// scores have to use the same order.
-template <int KV>
-__device__ __forceinline__ int row_token(int r) {
-  if constexpr (KV == KV_E2M1) return (r & 8) | ((r & 1) ? 7 - ((r & 7) >> 1) : (r & 7) >> 1);
-  else return r;
-}
-
-struct DecodeParams {
-  void* out;
-  const void* q;
-  const int32_t* block_tables;
-  const int32_t* context_lens;
-  const float* k_scale;
-  const float* v_scale;
-  int num_seqs;
-  int num_kv_heads;
-  int group;
-  int max_blocks;
-  int max_len;            // min(max_blocks * block_size, max_context_len): lengths are clamped to it
-  int num_blocks;
-  int block_size;         // tokens per pool block: 16 or 32 (1 or 2 tiles)
-  int tile_shift;         // log2(block_size / 16)
-  int part_blocks;        // tiles per partition; 0 = balanced split
-  int num_workers;        // gridDim.x * worker warps per CTA
-  int defer_dependents;   // 1: the merge kernel launches when this grid completes, not at its start
-  float scale_log2;       // softmax scale * log2(e)
-  float2* ml;             // [slots][group] (running max in log2 units, sum of exponentials)
-  float* po;              // [slots][group][D] unnormalised partial outputs
-  unsigned* err;
-  // Fused append (null k_new: plain decode): each sequence's new K/V row, [num_seqs][num_kv_heads][D]
-  // in the q dtype, belongs at position context_len - 1; it is written to the caches and attended.
-  const void* k_new;
-  const void* v_new;
-  void* k_cache;
-  void* v_cache;
-};
-
-struct Tile {
-  int s, h, b, nb, len;
-};
-
-// Largest s in [lo, hi] with mult * cum[s] <= t, given mult * cum[lo] <= t.  cum is a
-// non-decreasing prefix array whose scaled entries stay below 2^31 (checked on the host).
-__device__ __forceinline__ int find_seq(const int* cum, int lo, int hi, int t, int mult) {
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (mult * cum[mid] <= t) lo = mid; else hi = mid - 1;
-  }
-  return lo;
-}
-
-// The same search over [0, S) done by a whole warp for one t: each round the 32 lanes probe
-// 32 evenly spaced candidates and a ballot keeps the chunk holding the answer, so S entries
-// take ceil(log32 S) rounds instead of log2 S dependent probes.
-__device__ __forceinline__ int find_seq_warp(const int* cum, int S, int t, int mult, int lane) {
-  int lo = 0, n = S;                         // the answer lies in [lo, lo + n); mult * cum[lo] <= t
-  while (n > 1) {
-    const int step = (n + 31) >> 5;
-    const int pos = lo + lane * step;
-    const bool ok = lane * step < n && mult * cum[pos] <= t;
-    const unsigned b = __ballot_sync(0xffffffffu, ok);   // lane 0 always holds: b != 0
-    const int k = 31 - __clz(b);
-    lo += k * step;
-    n = min(step, n - k * step);
-  }
-  return lo;
-}
-
-__device__ __forceinline__ int clamp_len(int L, int max_len) { return min(max(L, 0), max_len); }
 
 template <int QT>
 __device__ __forceinline__ float2 q_pair(const void* q, int64_t elem) {
@@ -163,9 +80,9 @@ __device__ __forceinline__ void store_out(void* out, int64_t elem, float v) {
 }
 
 // head_dim index held by accumulator row `r` (0: row g, 1: row g + 8) of m-tile i.
-template <int KV, int D>
+template <int KV>
 __device__ __forceinline__ int out_dim(int i, int r, int g) {
-  if constexpr (KV == KV_E4M3 || KV == KV_E2M1) return D / 8 * g + 2 * i + r;
+  if constexpr (KV == KV_E4M3) return 16 * g + 2 * i + r;
   else return 16 * i + g + 8 * r;
 }
 
@@ -190,7 +107,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gq = lane >> 2, tq = lane & 3;
 
-  if (!C::kFp4 && threadIdx.x == 0) {
+  if (threadIdx.x == 0) {
     prefetch_tensormap(&tmk);
     prefetch_tensormap(&tmv);
   }
@@ -358,11 +275,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     valid |= 1u << st;
     mbar_arrive_expect_tx(bar, C::kStageBytes);
     uint8_t* kdst = my_stages + st * C::kStageBytes;
-    if constexpr (C::kFp4) {
-      const int64_t off = int64_t(y / kBS) * C::kTileBytes;      // y is a multiple of 16
-      bulk_load(kdst, static_cast<const uint8_t*>(p.k_cache) + off, C::kTileBytes, bar, pol);
-      bulk_load(kdst + C::kTileBytes, static_cast<const uint8_t*>(p.v_cache) + off, C::kTileBytes, bar, pol);
-    } else if constexpr (C::kNBox == 2) {
+    if constexpr (C::kNBox == 2) {
       // One 3-D box brings both 128-byte halves of the 16 rows: [half 0: 16 x 128 B][half 1].
       tma_load_3d(kdst, &tmk, bar, 0, y, 0, pol);
       tma_load_3d(kdst + C::kTileBytes, &tmv, bar, 0, y, 0, pol);
@@ -433,14 +346,14 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       l0 = l1 = 0.f;
 #pragma unroll
       for (int mt = 0; mt < C::kMTiles; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.f;
-      sl = p.scale_log2 * (C::kQuant && p.k_scale ? p.k_scale[tl.h] : 1.f);
+      sl = p.scale_log2 * (KV == KV_E4M3 ? p.k_scale[tl.h] : 1.f);
       const bool live = gq < G;
       const int64_t qrow = (int64_t(tl.s) * Hkv * G + int64_t(tl.h) * G + gq) * D;
 #pragma unroll
       for (int j = 0; j < C::kKSteps; ++j) {
-        if constexpr (C::kQuant) {
-          float2 a = live ? q_pair<QT>(p.q, qrow + D / 4 * tq + 4 * j) : make_float2(0.f, 0.f);
-          float2 b = live ? q_pair<QT>(p.q, qrow + D / 4 * tq + 4 * j + 2) : make_float2(0.f, 0.f);
+        if constexpr (KV == KV_E4M3) {
+          float2 a = live ? q_pair<QT>(p.q, qrow + 32 * tq + 4 * j) : make_float2(0.f, 0.f);
+          float2 b = live ? q_pair<QT>(p.q, qrow + 32 * tq + 4 * j + 2) : make_float2(0.f, 0.f);
           qf[j][0] = pack2<false>(a.x, a.y);
           qf[j][1] = pack2<false>(b.x, b.y);
         } else {
@@ -463,9 +376,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       if (lane < 2 * C::kRowChunks) {
         const int c = lane % C::kRowChunks;
         const uint4* src = static_cast<const uint4*>(lane < C::kRowChunks ? p.k_new : p.v_new) +
-                           ((int64_t(tl.s) * Hkv + tl.h) * D * 2) / 16 + c * (C::kQuant ? 2 : 1);
+                           ((int64_t(tl.s) * Hkv + tl.h) * D * 2) / 16 + c * (KV == KV_E4M3 ? 2 : 1);
         na = src[0];
-        if constexpr (C::kQuant) nb2 = src[1];
+        if constexpr (KV == KV_E4M3) nb2 = src[1];
       }
     }
 
@@ -484,28 +397,14 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         const bool isv = lane >= C::kRowChunks;
         const int c = lane % C::kRowChunks;
         const int r = (tl.len - 1) & (kBS - 1);
+        uint4 v = na;
+        if constexpr (KV == KV_E4M3) v = quant16_e4m3<QT == KV_BF16>(na, nb2, (isv ? p.v_scale : p.k_scale)[tl.h]);
+        const uint32_t tbase = smem_u32(my_stages + st * C::kStageBytes) + (isv ? C::kTileBytes : 0);
+        const uint32_t a = C::kNBox == 2 ? tbase + (c >> 3) * 2048 + swz128(r, c & 7) : tbase + swz128(r, c);
+        sts128(a, v.x, v.y, v.z, v.w);
+        fence_proxy_async_smem();                // orders this write before the stage's next TMA fill
         const int64_t row = (int64_t(apb) * Hkv + tl.h) * p.block_size + ((tl.len - 1) & (p.block_size - 1));
-        if constexpr (C::kFp4) {
-          const float* hs = isv ? p.v_scale : p.k_scale;
-          uint32_t sc;
-          const uint2 v = quant16_e2m1<QT == KV_BF16>(na, nb2, hs ? hs[tl.h] : 1.f, hs != nullptr, sc);
-          const int at = r * (D / 2) + 8 * c, sat = 8 * D + r * (D / 16) + c;
-          uint8_t* st_tile = my_stages + st * C::kStageBytes + (isv ? C::kTileBytes : 0);
-          *reinterpret_cast<uint2*>(st_tile + at) = v;
-          st_tile[sat] = uint8_t(sc);
-          fence_proxy_async_smem();              // orders these writes before the stage's next fill
-          uint8_t* pool_tile = static_cast<uint8_t*>(isv ? p.v_cache : p.k_cache) + row / kBS * C::kTileBytes;
-          *reinterpret_cast<uint2*>(pool_tile + at) = v;
-          pool_tile[sat] = uint8_t(sc);
-        } else {
-          uint4 v = na;
-          if constexpr (KV == KV_E4M3) v = quant16_e4m3<QT == KV_BF16>(na, nb2, (isv ? p.v_scale : p.k_scale)[tl.h]);
-          const uint32_t tbase = smem_u32(my_stages + st * C::kStageBytes) + (isv ? C::kTileBytes : 0);
-          const uint32_t a = C::kNBox == 2 ? tbase + (c >> 3) * 2048 + swz128(r, c & 7) : tbase + swz128(r, c);
-          sts128(a, v.x, v.y, v.z, v.w);
-          fence_proxy_async_smem();              // orders this write before the stage's next TMA fill
-          static_cast<uint4*>(isv ? p.v_cache : p.k_cache)[row * C::kRowChunks + c] = v;
-        }
+        static_cast<uint4*>(isv ? p.v_cache : p.k_cache)[row * C::kRowChunks + c] = v;
       }
       __syncwarp();
     }
@@ -515,40 +414,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       const uint32_t vbase = kbase + C::kTileBytes;
       // ---- S^T = K Q^T -------------------------------------------------------------
       float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
-      if constexpr (C::kFp4) {
-        // Thread (g, t) holds elements D/4 * t .. of rows g and g + 8; a k step takes 4 of them.
-        uint32_t kw[2][D / 32], ks[2][2];
-#pragma unroll
-        for (int rr = 0; rr < 2; ++rr) {
-          const int row = row_token<KV>(gq) + 8 * rr;
-          if constexpr (D == 128) {
-            const uint4 c = lds128(kbase + row * 64 + 16 * tq);
-            kw[rr][0] = c.x; kw[rr][1] = c.y; kw[rr][2] = c.z; kw[rr][3] = c.w;
-            const uint32_t s2 = e4m3x2_to_f16x2(lds16(kbase + 8 * D + row * 8 + 2 * tq));
-            ks[rr][0] = prmt(s2, s2, 0x1010u);
-            ks[rr][1] = prmt(s2, s2, 0x3232u);
-          } else {
-            const uint2 c = lds64(kbase + row * 32 + 8 * tq);
-            kw[rr][0] = c.x; kw[rr][1] = c.y;
-            ks[rr][0] = ks[rr][1] = e4m3x2_to_f16x2(lds8(kbase + 8 * D + row * 4 + tq) * 0x101u);
-          }
-        }
-#pragma unroll
-        for (int w = 0; w < D / 32; ++w) {                 // 8 elements of each row: two k steps
-          uint32_t x[4], y[4];
-          e2m1x8_to_f16x8(kw[0][w], x);
-          e2m1x8_to_f16x8(kw[1][w], y);
-          const int g2 = D == 128 ? w >> 1 : 0;
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const uint32_t a[4] = {hmul2(x[2 * e], ks[0][g2]), hmul2(y[2 * e], ks[1][g2]),
-                                   hmul2(x[2 * e + 1], ks[0][g2]), hmul2(y[2 * e + 1], ks[1][g2])};
-            const int j = 2 * w + e;
-            if (e) mma16816<false>(sb, a, qf[j][0], qf[j][1]);
-            else mma16816<false>(sa, a, qf[j][0], qf[j][1]);
-          }
-        }
-      } else if constexpr (KV == KV_E4M3) {
+      if constexpr (KV == KV_E4M3) {
         uint32_t kr[2][8];
 #pragma unroll
         for (int rr = 0; rr < 2; ++rr) {
@@ -584,8 +450,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       float x[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) x[e] = (sa[e] + sb[e]) * sl;
-      const int tok = row_token<KV>(gq);
-      const bool v0 = tok < nv, v8 = tok + 8 < nv;
+      const bool v0 = gq < nv, v8 = gq + 8 < nv;
       if (!v0) { x[0] = -INFINITY; x[1] = -INFINITY; }
       if (!v8) { x[2] = -INFINITY; x[3] = -INFINITY; }
       // ---- online softmax over the tile's 16 tokens ----------------------------------
@@ -615,40 +480,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       const uint32_t pb0 = movmatrix_trans(pack2<kPB>(p0, p1));
       const uint32_t pb1 = movmatrix_trans(pack2<kPB>(p2, p3));
       // ---- O^T += V^T P^T -----------------------------------------------------------
-      if constexpr (C::kFp4) {
-        // Thread (g, t): elements D/8 * g .. of the tokens of score rows 2t, 2t + 1, 2t + 8, 2t + 9.
-        // Rows past the sequence end contribute code 0 and scale 0, whatever their bytes are.
-        uint32_t vw[4][D / 64], sc[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int vt = row_token<KV>(2 * tq + (k & 1) + 8 * (k >> 1));
-          const bool in = vt < nv;
-          if constexpr (D == 128) {
-            const uint2 c = lds64(vbase + vt * 64 + 8 * gq);
-            vw[k][0] = in ? c.x : 0u;
-            vw[k][1] = in ? c.y : 0u;
-            sc[k] = in ? lds8(vbase + 8 * D + vt * 8 + gq) : 0u;
-          } else {
-            vw[k][0] = in ? lds32(vbase + vt * 32 + 4 * gq) : 0u;
-            sc[k] = in ? lds8(vbase + 8 * D + vt * 4 + (gq >> 1)) : 0u;
-          }
-        }
-        const uint32_t s01 = e4m3x2_to_f16x2(sc[0] | (sc[1] << 8)), s89 = e4m3x2_to_f16x2(sc[2] | (sc[3] << 8));
-#pragma unroll
-        for (int w = 0; w < D / 64; ++w) {                 // 8 elements: four m-tiles
-          // Byte m of ev/od: element 2m / 2m + 1 of the pair's first token (low nibble) and second.
-          uint32_t e01[4], o01[4], e89[4], o89[4];
-          e2m1x8_to_f16x8((vw[0][w] & 0x0F0F0F0Fu) | ((vw[1][w] << 4) & 0xF0F0F0F0u), e01);
-          e2m1x8_to_f16x8(((vw[0][w] >> 4) & 0x0F0F0F0Fu) | (vw[1][w] & 0xF0F0F0F0u), o01);
-          e2m1x8_to_f16x8((vw[2][w] & 0x0F0F0F0Fu) | ((vw[3][w] << 4) & 0xF0F0F0F0u), e89);
-          e2m1x8_to_f16x8(((vw[2][w] >> 4) & 0x0F0F0F0Fu) | (vw[3][w] & 0xF0F0F0F0u), o89);
-#pragma unroll
-          for (int m = 0; m < 4; ++m) {
-            const uint32_t a[4] = {hmul2(e01[m], s01), hmul2(o01[m], s01), hmul2(e89[m], s89), hmul2(o89[m], s89)};
-            mma16816<false>(o[4 * w + m], a, pb0, pb1);
-          }
-        }
-      } else if constexpr (KV == KV_E4M3) {
+      if constexpr (KV == KV_E4M3) {
         uint4 vr[4];   // tokens 2t, 2t+1, 2t+8, 2t+9; bytes 16g .. 16g+15
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -709,7 +541,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       ls0 += __shfl_xor_sync(0xffffffffu, ls0, off);
       ls1 += __shfl_xor_sync(0xffffffffu, ls1, off);
     }
-    const float vs = C::kQuant && p.v_scale ? p.v_scale[tl.h] : 1.f;
+    const float vs = KV == KV_E4M3 ? p.v_scale[tl.h] : 1.f;
     const int h0 = 2 * tq, h1 = 2 * tq + 1;
     const int Hq = Hkv * G;
     const int64_t seg_t0 = int64_t(Hkv) * cum_nb[tl.s] + int64_t(tl.h) * tl.nb;
@@ -726,7 +558,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       for (int mt = 0; mt < C::kMTiles; ++mt) {
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const int d = out_dim<KV, D>(mt, r, gq);
+          const int d = out_dim<KV>(mt, r, gq);
           if (h0 < G) store_out<QT>(p.out, base + int64_t(h0) * D + d, o[mt][2 * r] * inv0);
           if (h1 < G) store_out<QT>(p.out, base + int64_t(h1) * D + d, o[mt][2 * r + 1] * inv1);
         }
@@ -740,7 +572,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     for (int mt = 0; mt < C::kMTiles; ++mt) {
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const int d = out_dim<KV, D>(mt, r, gq);
+        const int d = out_dim<KV>(mt, r, gq);
         if (h0 < G) po[h0 * D + d] = o[mt][2 * r] * vs;
         if (h1 < G) po[h1 * D + d] = o[mt][2 * r + 1] * vs;
       }
@@ -904,18 +736,29 @@ Layout layout(int group, int head_dim, int64_t slots) {
   return l;
 }
 
-// Dynamic shared memory a launch of `kern` may request: the device's per-CTA opt-in limit
-// less the kernel's static arrays.
-template <typename K>
-size_t dynamic_smem_limit(K kern) {
-  int dev = 0, optin = 0;
-  cudaFuncAttributes fa = {};
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess ||
-      cudaFuncGetAttributes(&fa, kern) != cudaSuccess || size_t(optin) <= fa.sharedSizeBytes)
-    return 0;
-  return size_t(optin) - fa.sharedSizeBytes;
+}  // namespace
+
+pkv_status launch_merge(const DecodeParams& prm, bool q_bf16, int head_dim, cudaStream_t stream) {
+  MergeParams mp;
+  mp.out = prm.out;
+  mp.ml = prm.ml;
+  mp.po = prm.po;
+  mp.context_lens = prm.context_lens;
+  mp.num_seqs = prm.num_seqs;
+  mp.num_kv_heads = prm.num_kv_heads;
+  mp.num_segments = prm.num_seqs * prm.num_kv_heads;
+  mp.group = prm.group;
+  mp.max_len = prm.max_len;
+  mp.part_blocks = prm.part_blocks;
+  mp.num_workers = prm.num_workers;
+  const int64_t items = int64_t(mp.num_segments) * mp.group;
+  const int mgrid = int((items + kMergeWarps - 1) / kMergeWarps);
+  auto kern = q_bf16 ? (head_dim == 128 ? split_kv_merge_kernel<KV_BF16, 128> : split_kv_merge_kernel<KV_BF16, 64>)
+                     : (head_dim == 128 ? split_kv_merge_kernel<KV_F16, 128> : split_kv_merge_kernel<KV_F16, 64>);
+  return launch_pdl(kern, dim3(mgrid), dim3(kMergeWarps * 32), 0, stream, mp) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
+
+namespace {
 
 template <int KV, int D, int NW, int NS>
 size_t smem_bytes(int num_seqs) {
@@ -931,43 +774,26 @@ pkv_status launch_cfg(DecodeParams prm, const CUtensorMap& tk, const CUtensorMap
     return PKV_ERR_CUDA;
   prm.num_workers = grid * NW;
   if (launch_pdl(kern, dim3(grid), dim3(NW * 32), smem, stream, tk, tv, prm) != cudaSuccess) return PKV_ERR_CUDA;
-  MergeParams mp;
-  mp.out = prm.out;
-  mp.ml = prm.ml;
-  mp.po = prm.po;
-  mp.context_lens = prm.context_lens;
-  mp.num_seqs = prm.num_seqs;
-  mp.num_kv_heads = prm.num_kv_heads;
-  mp.num_segments = prm.num_seqs * prm.num_kv_heads;
-  mp.group = prm.group;
-  mp.max_len = prm.max_len;
-  mp.part_blocks = prm.part_blocks;
-  mp.num_workers = prm.num_workers;
-  const int64_t items = int64_t(mp.num_segments) * mp.group;
-  const int mgrid = int((items + kMergeWarps - 1) / kMergeWarps);
-  if (launch_pdl(split_kv_merge_kernel<QT, D>, dim3(mgrid), dim3(kMergeWarps * 32), 0, stream, mp) != cudaSuccess)
-    return PKV_ERR_CUDA;
-  return PKV_OK;
+  return launch_merge(prm, QT == KV_BF16, D, stream);
 }
 
-// 12 worker warps when the per-sequence prefix arrays fit next to their stages, else 4 warps
-// (very large batches).
+// 12 worker warps with 2 stages each when the per-sequence prefix arrays fit next to the
+// stages, else 4 warps with 2 stages (very large batches).
 template <int KV, int QT, int D>
 pkv_status launch(const DecodeParams& prm, const CUtensorMap& tk, const CUtensorMap& tv, int grid,
                   cudaStream_t stream) {
-  constexpr int NS = Cfg<KV, D>::kStages;
   static thread_local int cached_dev = -1;
   static thread_local size_t lim12 = 0, lim4 = 0;
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess) return PKV_ERR_CUDA;
   if (dev != cached_dev) {                   // looked up once per device and thread
-    lim12 = dynamic_smem_limit(paged_decode_kernel<KV, QT, D, kMaxWarps, NS>);
-    lim4 = dynamic_smem_limit(paged_decode_kernel<KV, QT, D, 4, NS>);
+    lim12 = dynamic_smem_limit(paged_decode_kernel<KV, QT, D, kMaxWarps, 2>);
+    lim4 = dynamic_smem_limit(paged_decode_kernel<KV, QT, D, 4, 2>);
     cached_dev = dev;
   }
-  if (smem_bytes<KV, D, kMaxWarps, NS>(prm.num_seqs) <= lim12)
-    return launch_cfg<KV, QT, D, kMaxWarps, NS>(prm, tk, tv, grid, stream);
-  if (smem_bytes<KV, D, 4, NS>(prm.num_seqs) <= lim4) return launch_cfg<KV, QT, D, 4, NS>(prm, tk, tv, grid, stream);
+  if (smem_bytes<KV, D, kMaxWarps, 2>(prm.num_seqs) <= lim12)
+    return launch_cfg<KV, QT, D, kMaxWarps, 2>(prm, tk, tv, grid, stream);
+  if (smem_bytes<KV, D, 4, 2>(prm.num_seqs) <= lim4) return launch_cfg<KV, QT, D, 4, 2>(prm, tk, tv, grid, stream);
   return PKV_ERR_UNSUPPORTED;
 }
 
@@ -1073,27 +899,6 @@ pkv_status decode_impl(void* out, const void* q, pkv_dtype q_dtype, int num_seqs
   unsigned* err = error_word_ptr();
   if (!err) return PKV_ERR_CUDA;
 
-  // Tensor maps: the pool as rows of head_dim elements; a box is one 16-row tile of a (block,
-  // kv head).  Rows of 128 bytes are one 2-D box; rows of 256 bytes (2-byte, head_dim 128) are
-  // viewed as (64 elements, rows, 2 halves) so one 3-D box lands as two swizzled halves.
-  // 4-bit tiles are contiguous runs, copied without a map.
-  CUtensorMap tk = {}, tv = {};
-  const bool fp4 = cache->kv_dtype == PKV_FP4_E2M1;
-  const bool fp8 = cache->kv_dtype == PKV_FP8_E4M3;
-  const CUtensorMapDataType dt = fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16;
-  const uint64_t rows = uint64_t(cache->num_blocks) * cache->num_kv_heads * cache->block_size;
-  const uint64_t row_bytes = uint64_t(D) * dtype_bytes(cache->kv_dtype);
-  bool enc = true;
-  if (fp4) {
-  } else if (row_bytes == 256) {
-    enc = encode_tmap_3d(&tk, dt, k_cache, 64, rows, 2, 256, 128, 64, kBS, 2, CU_TENSOR_MAP_SWIZZLE_128B) &&
-          encode_tmap_3d(&tv, dt, v_cache, 64, rows, 2, 256, 128, 64, kBS, 2, CU_TENSOR_MAP_SWIZZLE_128B);
-  } else {
-    enc = encode_tmap_2d(&tk, dt, k_cache, D, rows, row_bytes, uint32_t(D), kBS, CU_TENSOR_MAP_SWIZZLE_128B) &&
-          encode_tmap_2d(&tv, dt, v_cache, D, rows, row_bytes, uint32_t(D), kBS, CU_TENSOR_MAP_SWIZZLE_128B);
-  }
-  if (!enc) return PKV_ERR_CUDA;
-
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   DecodeParams prm;
   prm.out = out;
@@ -1123,6 +928,26 @@ pkv_status decode_impl(void* out, const void* q, pkv_dtype q_dtype, int num_seqs
 
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool qbf = q_dtype == PKV_BF16;
+  if (cache->kv_dtype == PKV_FP4_E2M1) return launch_decode_fp4(prm, qbf, D, grid, s);
+
+  // Tensor maps: the pool as rows of head_dim elements; a box is one 16-row tile of a (block,
+  // kv head).  Rows of 128 bytes are one 2-D box; rows of 256 bytes (2-byte, head_dim 128) are
+  // viewed as (64 elements, rows, 2 halves) so one 3-D box lands as two swizzled halves.
+  CUtensorMap tk, tv;
+  const bool fp8 = cache->kv_dtype == PKV_FP8_E4M3;
+  const CUtensorMapDataType dt = fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16;
+  const uint64_t rows = uint64_t(cache->num_blocks) * cache->num_kv_heads * cache->block_size;
+  const uint64_t row_bytes = uint64_t(D) * dtype_bytes(cache->kv_dtype);
+  bool enc;
+  if (row_bytes == 256) {
+    enc = encode_tmap_3d(&tk, dt, k_cache, 64, rows, 2, 256, 128, 64, kBS, 2, CU_TENSOR_MAP_SWIZZLE_128B) &&
+          encode_tmap_3d(&tv, dt, v_cache, 64, rows, 2, 256, 128, 64, kBS, 2, CU_TENSOR_MAP_SWIZZLE_128B);
+  } else {
+    enc = encode_tmap_2d(&tk, dt, k_cache, D, rows, row_bytes, uint32_t(D), kBS, CU_TENSOR_MAP_SWIZZLE_128B) &&
+          encode_tmap_2d(&tv, dt, v_cache, D, rows, row_bytes, uint32_t(D), kBS, CU_TENSOR_MAP_SWIZZLE_128B);
+  }
+  if (!enc) return PKV_ERR_CUDA;
+
   switch (cache->kv_dtype) {
     case PKV_BF16:
       return D == 128 ? launch<KV_BF16, KV_BF16, 128>(prm, tk, tv, grid, s)
@@ -1134,11 +959,7 @@ pkv_status decode_impl(void* out, const void* q, pkv_dtype q_dtype, int num_seqs
       return qbf ? launch<KV_E4M3, KV_BF16, 128>(prm, tk, tv, grid, s)
                  : launch<KV_E4M3, KV_F16, 128>(prm, tk, tv, grid, s);
     case PKV_FP4_E2M1:
-      if (D == 128)
-        return qbf ? launch<KV_E2M1, KV_BF16, 128>(prm, tk, tv, grid, s)
-                   : launch<KV_E2M1, KV_F16, 128>(prm, tk, tv, grid, s);
-      return qbf ? launch<KV_E2M1, KV_BF16, 64>(prm, tk, tv, grid, s)
-                 : launch<KV_E2M1, KV_F16, 64>(prm, tk, tv, grid, s);
+      break;                                 // above
   }
   return PKV_ERR_UNSUPPORTED;
 }
