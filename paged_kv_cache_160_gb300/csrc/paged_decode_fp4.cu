@@ -27,6 +27,7 @@
 #include <type_traits>
 
 #include "decode_split.cuh"
+#include "f32x2.cuh"
 
 namespace pkv {
 namespace {
@@ -46,6 +47,40 @@ struct Fp4Cfg {
 // Token of the tile that score row r (0..15) stands for.
 __device__ __forceinline__ int row_token(int r) {
   return (r & 8) | ((r & 1) ? 7 - ((r & 7) >> 1) : (r & 7) >> 1);
+}
+
+// D += A * B (m16n8k16, fp16 in, fp32 out).  Not volatile, as the loads below are plain ones: the
+// compiler may interleave the fragments of different tiles.
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// The same with D = A * B: the zero accumulator costs no registers to clear.
+__device__ __forceinline__ void mma_f16_zero(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// Two e4m3 codes (low byte -> low half) to two fp16 values; exact.
+__device__ __forceinline__ uint32_t scales_f16x2(uint32_t two_codes) {
+  uint32_t out;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(out) : "h"(static_cast<unsigned short>(two_codes)));
+  return out;
+}
+
+// A pair of fp16 values times the low (high) half of s.
+__device__ __forceinline__ uint32_t mul_lo(uint32_t x, uint32_t s) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&x), __low2half2(*reinterpret_cast<const __half2*>(&s)));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t mul_hi(uint32_t x, uint32_t s) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&x), __high2half2(*reinterpret_cast<const __half2*>(&s)));
+  return *reinterpret_cast<const uint32_t*>(&r);
 }
 
 // Elements e0 .. e0 + 7 of a 16-bit row as four fp16 pairs.
@@ -310,15 +345,19 @@ __global__ void __launch_bounds__(kWarps * 32, 1) paged_decode_fp4_kernel(const 
 #pragma unroll
       for (int mt = 0; mt < C::kMTiles; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.f;
       sl = p.scale_log2 * (p.k_scale ? p.k_scale[tl.h] : 1.f);
+      // The softmax takes max(s) * sl and -inf * sl, so sl has to be positive: its sign goes to the
+      // queries, and 0 becomes the least normal number.
+      const uint32_t flip = sl < 0.f ? 0x80008000u : 0u;
+      sl = fmaxf(fabsf(sl), 1.17549435e-38f);
       const int64_t qrow = (int64_t(tl.s) * Hkv * G + int64_t(tl.h) * G + gq) * D + D / 4 * tq;
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {     // 8 elements: two k steps
         uint32_t v[4] = {0u, 0u, 0u, 0u};
         if (gq < G) q8<kQBF16>(p.q, qrow + 8 * c, v);
-        qf[2 * c][0] = v[0];
-        qf[2 * c][1] = v[1];
-        qf[2 * c + 1][0] = v[2];
-        qf[2 * c + 1][1] = v[3];
+        qf[2 * c][0] = v[0] ^ flip;
+        qf[2 * c][1] = v[1] ^ flip;
+        qf[2 * c + 1][0] = v[2] ^ flip;
+        qf[2 * c + 1][1] = v[3] ^ flip;
       }
     }
     const bool ends = tl.b + k == tl.nb;     // the step holds the segment's last tile
@@ -372,62 +411,56 @@ __global__ void __launch_bounds__(kWarps * 32, 1) paged_decode_fp4_kernel(const 
     }
 
     // ---- the step's tokens ------------------------------------------------------------------
-    const uint32_t base = smem_u32(stage);
     // Tokens of tile u that are attended (0: the tile is not part of the step, or did not come).
     auto tokens = [&](int u) -> int {
       return u < k && (have >> u & 1u) ? min(kBS, tl.len - (tl.b + u) * kBS) : 0;
     };
     // S^T = K Q^T of tile u: s[0]: (row g, head 2t)  s[1]: (row g, head 2t+1)  s[2]/s[3]: row g + 8.
     auto scores = [&](int u, float (&s)[4]) {
-      const uint32_t kb = base + u * 2 * C::kTileBytes;
-      uint32_t kw[2][D / 32], ks[2][2];
+      const uint8_t* kb = stage + u * 2 * C::kTileBytes;
+      uint32_t kw[2][D / 32], ks[2];         // codes; scales of the row's two groups here (D = 64: one)
 #pragma unroll
       for (int rr = 0; rr < 2; ++rr) {
         const int row = rt + 8 * rr;
         if constexpr (D == 128) {
-          const uint4 c = lds128(kb + row * 64 + 16 * tq);
+          const uint4 c = *reinterpret_cast<const uint4*>(kb + row * 64 + 16 * tq);
           kw[rr][0] = c.x; kw[rr][1] = c.y; kw[rr][2] = c.z; kw[rr][3] = c.w;
-          const uint32_t s2 = e4m3x2_to_f16x2(lds16(kb + 8 * D + row * 8 + 2 * tq));
-          ks[rr][0] = prmt(s2, s2, 0x1010u);
-          ks[rr][1] = prmt(s2, s2, 0x3232u);
+          ks[rr] = scales_f16x2(*reinterpret_cast<const uint16_t*>(kb + 8 * D + row * 8 + 2 * tq));
         } else {
-          const uint2 c = lds64(kb + row * 32 + 8 * tq);
+          const uint2 c = *reinterpret_cast<const uint2*>(kb + row * 32 + 8 * tq);
           kw[rr][0] = c.x; kw[rr][1] = c.y;
-          ks[rr][0] = ks[rr][1] = e4m3x2_to_f16x2(lds8(kb + 8 * D + row * 4 + tq) * 0x101u);
+          ks[rr] = scales_f16x2(kb[8 * D + row * 4 + tq]);
         }
       }
-      float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {     // 8 elements of each row: two k steps
         uint32_t x[4], y[4];
         e2m1x8_to_f16x8(kw[0][c], x);
         e2m1x8_to_f16x8(kw[1][c], y);
-        const int g2 = D == 128 ? c >> 1 : 0;
-        const uint32_t a[4] = {hmul2(x[0], ks[0][g2]), hmul2(y[0], ks[1][g2]), hmul2(x[1], ks[0][g2]),
-                               hmul2(y[1], ks[1][g2])};
-        mma16816<false>(sa, a, qf[2 * c][0], qf[2 * c][1]);
-        const uint32_t b[4] = {hmul2(x[2], ks[0][g2]), hmul2(y[2], ks[1][g2]), hmul2(x[3], ks[0][g2]),
-                               hmul2(y[3], ks[1][g2])};
-        mma16816<false>(sb, b, qf[2 * c + 1][0], qf[2 * c + 1][1]);
+        const bool hi = D == 128 && c >= 2;
+        auto mul = [&](uint32_t v, uint32_t sc) { return hi ? mul_hi(v, sc) : mul_lo(v, sc); };
+        const uint32_t a[4] = {mul(x[0], ks[0]), mul(y[0], ks[1]), mul(x[1], ks[0]), mul(y[1], ks[1])};
+        if (c == 0) mma_f16_zero(s, a, qf[0][0], qf[0][1]);
+        else mma_f16(s, a, qf[2 * c][0], qf[2 * c][1]);
+        const uint32_t b[4] = {mul(x[2], ks[0]), mul(y[2], ks[1]), mul(x[3], ks[0]), mul(y[3], ks[1])};
+        mma_f16(s, b, qf[2 * c + 1][0], qf[2 * c + 1][1]);
       }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s[e] = (sa[e] + sb[e]) * sl;
     };
     // O^T += V^T P^T of tile u.  Tokens past nv contribute code 0 and scale 0, whatever their bytes.
     auto values = [&](int u, int nv, uint32_t pb0, uint32_t pb1, auto full) {
-      const uint32_t vb = base + (u * 2 + 1) * C::kTileBytes;
+      const uint8_t* vb = stage + (u * 2 + 1) * C::kTileBytes;
       uint32_t vw[4][D / 64], sc[4];
 #pragma unroll
       for (int x = 0; x < 4; ++x) {          // tokens of score rows 2t, 2t + 1, 2t + 8, 2t + 9
         const int vt = (x & 2 ? 8 : 0) + (x & 1 ? 7 - tq : tq);
         if constexpr (D == 128) {
-          const uint2 c = lds64(vb + vt * 64 + 8 * gq);
+          const uint2 c = *reinterpret_cast<const uint2*>(vb + vt * 64 + 8 * gq);
           vw[x][0] = c.x;
           vw[x][1] = c.y;
-          sc[x] = lds8(vb + 8 * D + vt * 8 + gq);
+          sc[x] = vb[8 * D + vt * 8 + gq];
         } else {
-          vw[x][0] = lds32(vb + vt * 32 + 4 * gq);
-          sc[x] = lds8(vb + 8 * D + vt * 4 + (gq >> 1));
+          vw[x][0] = *reinterpret_cast<const uint32_t*>(vb + vt * 32 + 4 * gq);
+          sc[x] = vb[8 * D + vt * 4 + (gq >> 1)];
         }
         if (!decltype(full)::value && vt >= nv) {
 #pragma unroll
@@ -435,7 +468,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) paged_decode_fp4_kernel(const 
           sc[x] = 0u;
         }
       }
-      const uint32_t s01 = e4m3x2_to_f16x2(sc[0] | (sc[1] << 8)), s89 = e4m3x2_to_f16x2(sc[2] | (sc[3] << 8));
+      const uint32_t s01 = scales_f16x2(sc[0] | (sc[1] << 8)), s89 = scales_f16x2(sc[2] | (sc[3] << 8));
 #pragma unroll
       for (int c = 0; c < D / 64; ++c) {     // 8 elements: four m-tiles
         // Byte m: element 2m (e) / 2m + 1 (o) of the pair's first token (low nibble) and second.
@@ -447,7 +480,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) paged_decode_fp4_kernel(const 
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
           const uint32_t a[4] = {hmul2(e01[m], s01), hmul2(o01[m], s01), hmul2(e89[m], s89), hmul2(o89[m], s89)};
-          mma16816<false>(o[4 * c + m], a, pb0, pb1);
+          mma_f16(o[4 * c + m], a, pb0, pb1);
         }
       }
     };
@@ -478,24 +511,27 @@ __global__ void __launch_bounds__(kWarps * 32, 1) paged_decode_fp4_kernel(const 
         mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, off));
         mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
       }
-      const float mn0 = fmaxf(m0, mx0), mn1 = fmaxf(m1, mx1);
+      const float mn0 = fmaxf(m0, mx0 * sl), mn1 = fmaxf(m1, mx1 * sl);
       const bool grew = mn0 > m0 || mn1 > m1;
       const float al0 = fast_exp2(m0 - mn0), al1 = fast_exp2(m1 - mn1);
       m0 = mn0;
       m1 = mn1;
-      l0 *= al0;
-      l1 *= al1;
+      uint64_t l2 = pack_f32x2(l0 * al0, l1 * al1);
+      const uint64_t sl2 = pack_f32x2(sl, sl), nm2 = pack_f32x2(-mn0, -mn1);
       uint32_t pb[kSub][2];
 #pragma unroll
       for (int u = 0; u < kSub; ++u) {
-        const float p0 = fast_exp2(x[u][0] - mn0), p1 = fast_exp2(x[u][1] - mn1);
-        const float p2 = fast_exp2(x[u][2] - mn0), p3 = fast_exp2(x[u][3] - mn1);
-        l0 += p0 + p2;
-        l1 += p1 + p3;
+        const uint64_t ya = fma_f32x2(pack_f32x2(x[u][0], x[u][1]), sl2, nm2);
+        const uint64_t yb = fma_f32x2(pack_f32x2(x[u][2], x[u][3]), sl2, nm2);
+        const float p0 = fast_exp2(lo_f32(ya)), p1 = fast_exp2(hi_f32(ya));
+        const float p2 = fast_exp2(lo_f32(yb)), p3 = fast_exp2(hi_f32(yb));
+        l2 = add_f32x2(l2, add_f32x2(pack_f32x2(p0, p1), pack_f32x2(p2, p3)));
         // P^T as the B operand: lane (g, t) needs head g, score rows {2t, 2t+1} and {2t+8, 2t+9}.
         pb[u][0] = movmatrix_trans(pack2<false>(p0, p1));
         pb[u][1] = movmatrix_trans(pack2<false>(p2, p3));
       }
+      l0 = lo_f32(l2);
+      l1 = hi_f32(l2);
       if (__any_sync(0xffffffffu, grew)) {   // the running max moved: rescale O
 #pragma unroll
         for (int mt = 0; mt < C::kMTiles; ++mt) {

@@ -228,25 +228,26 @@ def _bound(out, size, dtype):
     return 2.0 ** -10 * size + torch.finfo(dtype).eps / 2 * np.abs(out) + 2.0 ** -25
 
 
-def _run_decode(lens, hq, hkv, dim, dtype, block=16, part=0, scaled=True, seed=0, entry="plain", max_len=None, clip=None):
+def _run_decode(lens, hq, hkv, dim, dtype, block=16, part=0, scaled=True, seed=0, entry="plain", scale=None):
     import paged_kv_cache_160_gb300 as pkv
     rng, table, pools, scales = _decode_case(seed, lens, hq, hkv, dim, block, scaled)
     dev = [torch.from_numpy(fp4.pack(*p)).cuda() for p in pools]
     desc = pkv.cache_desc_fp4(dev[0], *(torch.from_numpy(s).cuda() if scaled else None for s in scales))
     q = torch.from_numpy(rng.standard_normal((len(lens), hq, dim))).to(DT[dtype])
     out = torch.full(q.shape, float("nan"), dtype=DT[dtype], device="cuda")
-    longest = max_len if max_len is not None else max(lens + [1])
+    longest = max(lens + [1])
+    scale = dim ** -0.5 if scale is None else scale
     ws = torch.full((pkv.pkv_decode_workspace_bytes(len(lens), hq, hkv, dim, block, longest, part),), 0xFF,
                     dtype=torch.uint8, device="cuda")
     args = (out, q.cuda(), *dev, desc, torch.from_numpy(table).cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"),
-            longest, dim ** -0.5, part)
+            longest, scale, part)
     if entry == "noalloc":
         pkv.pkv_paged_decode_noalloc(*args)
     else:
         pkv.pkv_paged_decode(*args, ws)
     assert pkv.pkv_get_device_error() == 0
     k, v = (np.concatenate([_rows(*p, table[i], n, block, s) for i, n in enumerate(lens)]) for p, s in zip(pools, scales))
-    ref, size = prompt.prompt_attention(q.double().numpy(), k, v, [1] * len(lens), lens, dim ** -0.5)
+    ref, size = prompt.prompt_attention(q.double().numpy(), k, v, [1] * len(lens), lens, scale)
     _close(out, ref, _bound(ref, size, DT[dtype]))
     return out
 
@@ -271,6 +272,11 @@ def test_decode_blocks_and_partitions(dim, part, block):
 @pytest.mark.parametrize("lens", [[1], [16], [0], [0, 5, 0], [4000], [3, 9000], [1] * 300, [40] * 65])
 def test_decode_lengths(lens):
     _run_decode(lens, 7, 1, 128, "f16", seed=len(lens))
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.1])
+def test_decode_with_a_zero_or_negative_scale(scale):
+    _run_decode(RAGGED, 8, 2, 128, "bf16", seed=8, scale=scale)
 
 
 def test_decode_large_batch_takes_the_four_warp_layout():
