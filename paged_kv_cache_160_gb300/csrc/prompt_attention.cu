@@ -87,22 +87,94 @@ __device__ __forceinline__ uint32_t elect_one() {
   return r;
 }
 
+// Asks for a CTA of the grid that has not started: the hardware cancels its launch and writes its index
+// (or that there is none) to 16 bytes at `response`, completing 16 bytes on `bar`.
+__device__ __forceinline__ void ask_for_cta(void* response, uint64_t* bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                   smem_u32(response)),
+               "r"(smem_u32(bar))
+               : "memory");
+}
+// The answer: whether there was one, and its block index.
+__device__ __forceinline__ bool read_cta(const void* response, int& x, int& y, int& z) {
+  uint32_t got, a, b, c;
+  asm volatile(
+      "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\t"
+      "mov.u32 %0, 0;\n\tmov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\t"
+      "ld.shared.b128 r, [%4];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+      "selp.u32 %3, 1, 0, p;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%0, %1, %2, _}, r;\n\t}\n"
+      : "=&r"(a), "=&r"(b), "=&r"(c), "=&r"(got)
+      : "r"(smem_u32(response))
+      : "memory");
+  x = int(a);
+  y = int(b);
+  z = int(c);
+  return got != 0;
+}
+
 // ---------------------------------------------------------------------------------------
-// A CTA holds two row blocks A and B of 128 query rows that read the same keys.
-//   warp 0   : TMA producer of Q, K and V
-//   warp 1   : TMEM owner and MMA issuer, in the order S_A(0) S_B(0) | PV_A(t) S_A(t+1) PV_B(t) S_B(t+1) | ...
-//              so that one block's softmax overlaps the other's products
-//   warps 2-9: softmax of block A, warps 10-17: of block B; two threads per query row, one for each half
-//              of the tile's keys.  A tile's way from its scores to its product with V is a chain that
-//              only the other block's products cover, so the softmax is spread over twice the threads:
-//              one thread per row took 390 us for a prompt of 8192 tokens.
+// A CTA works on items: two row blocks A and B of 128 query rows that read the same keys.  The grid
+// has a CTA for every possible item; the ones that the GPU can hold take over the items of those that
+// have not started (ask_for_cta), so that barriers and TMEM are set up once per SM, the next item's
+// loads and first products run while the last rows of this one are written, and an SM that is done
+// early takes the next item.  (A CTA per item spent 7 us outside the tile loop.)
+//   warp 0    : TMA producer of Q, K and V; asks for the next item
+//   warp 1    : TMEM owner and MMA issuer, in the order S_A(0) S_B(0) | PV_A(t) S_A(t+1) PV_B(t) S_B(t+1) | ...
+//               so that one block's softmax overlaps the other's products
+//   warps 2-9 : softmax of block A, warps 10-17: of block B; two threads per query row, one for each half
+//               of the tile's keys.  A tile's way from its scores to its product with V is a chain that
+//               only the other block's products cover (3200 cycles for both blocks, about 2400 of them
+//               products), so the softmax is spread over twice the threads: one thread per row took
+//               390 us for a prompt of 8192 tokens where two take 381.
+// Every barrier's phases are counted over all items by each of its users.
 // ---------------------------------------------------------------------------------------
 template <int D>
 struct Cfg {
   static constexpr int kTileBytes = D / 64 * kHalfBytes;          // 128 rows of Q, K or V
   static constexpr int kStages = D == 128 ? 2 : 4;                // K and V tiles in flight
-  static constexpr int kSmem = (2 + 2 * kStages) * kTileBytes;
+  static constexpr int kStageRows = 8;                            // half rows of output that a warp stages at a time
+  static constexpr int kOutBytes = kStageRows * D;                // (16-bit half rows)
+  static constexpr int kSmem = (2 + 2 * kStages) * kTileBytes + 16 * kOutBytes;
 };
+
+struct Item {
+  int h;                  // kv head
+  int q0, k0, Lq, Lk;     // the sequence's first rows and lengths
+  int rows;               // query rows to compute (at most max_q_len)
+  int e0;                 // block A is row block e0 of the (sequence, kv head), B the next one
+  int na, nb, n;          // key tiles that A and B walk, and the larger
+  bool live;              // there is something to do
+};
+
+// The item of block index (x, y, z).  A sequence's row blocks of a kv head are numbered query tile by
+// query tile, its query heads inside a tile; an item takes the next two.  The hardware starts CTAs with
+// x fastest and z slowest: the last tiles, which walk the most keys, come first.
+__device__ __forceinline__ Item item_of(const PromptParams& p, int x, int y, int z, int nz) {
+  Item it;
+  it.h = x;
+  it.q0 = p.cu_q[y];
+  it.k0 = p.cu_k[y];
+  it.Lq = p.cu_q[y + 1] - it.q0;
+  it.Lk = p.cu_k[y + 1] - it.k0;
+  const bool bad = it.q0 < 0 || it.k0 < 0 || it.Lq < 0 || it.Lk < 0 || it.Lq > p.total_q - it.q0 || it.Lk > p.total_k - it.k0;
+  it.rows = bad ? 0 : min(it.Lq, p.max_q_len);
+  const int G = p.num_heads / p.num_kv_heads;
+  it.e0 = 2 * (nz - 1 - z);
+  it.live = it.e0 < (it.rows + kTile - 1) / kTile * G;
+  // Key tiles that the rows of block e attend (0: none, or no such rows).
+  auto tiles_of = [&](int e) -> int {
+    const int r0 = e / G * kTile;
+    if (r0 >= it.rows) return 0;
+    const int keys = min(it.Lq, r0 + kTile) + it.Lk - it.Lq;
+    return keys > 0 ? (keys + kTile - 1) / kTile : 0;
+  };
+  it.na = it.live ? tiles_of(it.e0) : 0;
+  it.nb = it.live ? tiles_of(it.e0 + 1) : 0;
+  it.n = max(it.na, it.nb);
+  return it;
+}
 
 template <bool kBF16, int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -111,59 +183,43 @@ __global__ void __launch_bounds__(kThreads, 1)
   using C = Cfg<D>;
   constexpr int kStages = C::kStages;
   extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ __align__(8) uint64_t bar_q, bar_k_full[kStages], bar_k_empty[kStages], bar_v_full[kStages],
-      bar_v_empty[kStages], bar_s_full[2], bar_p_full[2], bar_pv_done[2];
+  __shared__ __align__(16) uint4 response[2];                // ask_for_cta's answers, in turn
+  __shared__ __align__(8) uint64_t bar_next[2], bar_read[2]; // an answer has come / every warp has read it
+  // Q landed / no product reads it any more; K, V tiles likewise; S_x ready; P_x ready; PV_x done; O_x read.
+  __shared__ __align__(8) uint64_t bar_q, bar_q_empty, bar_k_full[kStages], bar_k_empty[kStages], bar_v_full[kStages],
+      bar_v_empty[kStages], bar_s_full[2], bar_p_full[2], bar_pv_done[2], bar_o_free[2];
   __shared__ uint32_t tmem_base_sh;
-  __shared__ float exchange[2][2][2][kTile];                 // [block][tile parity][key half][row]
+  __shared__ float exchange[2][2][2][kTile];                 // [block][step parity][key half][row]
+  __shared__ uint32_t fine[2][2][2][4];                      // [block][step parity][key half][row quarter]: the warp goes on
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // uniform in the warp
 
-  griddep_wait();
-  // ---- the row blocks --------------------------------------------------------------------
-  // A sequence's blocks of a kv head are numbered query tile by query tile, its query heads inside a
-  // tile; a CTA takes the next two of them.  The hardware starts CTAs with x fastest and
-  // z slowest: the last tiles, which walk the most keys, come first.
-  const int seq = blockIdx.y, group = gridDim.z - 1 - blockIdx.z, h = blockIdx.x;
-  const int G = p.num_heads / p.num_kv_heads;
-  const int q0 = p.cu_q[seq], k0 = p.cu_k[seq];
-  const int Lq = p.cu_q[seq + 1] - q0, Lk = p.cu_k[seq + 1] - k0;
-  const bool bad = q0 < 0 || k0 < 0 || Lq < 0 || Lk < 0 || Lq > p.total_q - q0 || Lk > p.total_k - k0;
-  if (threadIdx.x == 0 && blockIdx.z == 0 && blockIdx.x == 0 &&
-      (bad || Lq > p.max_q_len || (seq == 0 && (q0 != 0 || k0 != 0))))
-    set_error(p.err, PKV_DEVERR_CHUNK);
-  const int rows = min(Lq, p.max_q_len);                     // rows past the promised bound stay unwritten
-  if (bad || group * 2 >= (rows + kTile - 1) / kTile * G || (smem_u32(smem) & 1023u)) {
-    if ((smem_u32(smem) & 1023u) && threadIdx.x == 0) set_error(p.err, PKV_DEVERR_CHUNK);
-    griddep_launch_dependents();
+  if (smem_u32(smem) & 1023u) {                              // the 128-byte swizzle needs 1 KB alignment
+    if (threadIdx.x == 0) set_error(p.err, PKV_DEVERR_CHUNK);
     return;
   }
-  const int shift = Lk - Lq;
-  // First row and head of block e, and the key tiles its rows attend (0: none, or no such rows).
-  auto first_row = [&](int e) -> int { return e / G * kTile; };
-  auto head_of = [&](int e) -> int { return h * G + e % G; };
-  auto tiles_of = [&](int e) -> int {
-    const int r0 = first_row(e);
-    if (r0 >= rows) return 0;
-    const int keys = min(Lq, r0 + kTile) + shift;
-    return keys > 0 ? (keys + kTile - 1) / kTile : 0;
-  };
-  const int e0 = 2 * group;                                  // A is block e0, B the next one
-  const int na = tiles_of(e0), nb = tiles_of(e0 + 1), n = max(na, nb);
-
   uint8_t* sQ = smem;                                        // [block][64-dim half][128 rows]
   uint8_t* sK = smem + 2 * C::kTileBytes;                    // [stage][64-dim half][128 rows]
   uint8_t* sV = sK + kStages * C::kTileBytes;
+  uint8_t* sOut = sV + kStages * C::kTileBytes;              // [softmax warp][kStageRows][half a row]
   if (threadIdx.x == 0) {
+    prefetch_tensormap(&tmq);
+    prefetch_tensormap(&tmk);
+    prefetch_tensormap(&tmv);
     mbar_init(&bar_q, 1);
+    mbar_init(&bar_q_empty, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar_next[i], 1);
+      mbar_init(&bar_read[i], kThreads / 32);                // every warp, the asking one too
+      mbar_init(&bar_s_full[i], 1);
+      mbar_init(&bar_p_full[i], 8);                          // one arrival per softmax warp
+      mbar_init(&bar_pv_done[i], 1);
+      mbar_init(&bar_o_free[i], 8);
+    }
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&bar_k_full[i], 1);
       mbar_init(&bar_k_empty[i], 1);
       mbar_init(&bar_v_full[i], 1);
       mbar_init(&bar_v_empty[i], 1);
-    }
-    for (int x = 0; x < 2; ++x) {
-      mbar_init(&bar_s_full[x], 1);
-      mbar_init(&bar_p_full[x], 8);                          // one arrival per softmax warp
-      mbar_init(&bar_pv_done[x], 1);
     }
     fence_mbar_init();
   }
@@ -176,45 +232,85 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = tmem_base_sh;
 
-  if (warp == 0 && lane == 0) {
+  // Only the set-up above may run before the previous kernel on the stream has finished.
+  griddep_wait();
+  const int G = p.num_heads / p.num_kv_heads;
+  auto all = [](bool v) -> bool { return __all_sync(0xffffffffu, v); };
+  // The next item's block index, for a whole warp: false when there is none, or (ok false) no answer.
+  auto next_item = [&](uint32_t i, int& bx, int& by, int& bz, bool& ok) -> bool {
+    ok = all(ok && mbar_wait(&bar_next[i & 1], (i >> 1) & 1u));
+    if (!ok) return false;
+    const bool got = read_cta(&response[i & 1], bx, by, bz);
+    fence_proxy_async_smem();                                // the slot's next answer comes after this read
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bar_read[i & 1]);
+    return got;
+  };
+  int bx = blockIdx.x, by = blockIdx.y, bz = blockIdx.z;
+
+  if (warp == 0) {
     // ---------------- TMA producer ----------------
     const uint64_t pol_q = l2_policy_evict_first();
     const uint64_t pol_kv = l2_policy_evict_last();          // re-read by the other heads and query tiles
-    bool ok = true;
-    if (n > 0) {
-      mbar_arrive_expect_tx(&bar_q, 2 * C::kTileBytes);
-      for (int x = 0; x < 2; ++x) {
-        // A block past the sequence's end reads rows that nobody stores: its own first ones.
-        const int e = e0 + x, r0 = first_row(e) < rows ? first_row(e) : 0;
-        for (int d = 0; d < D / 64; ++d)
-          tma_load_3d(sQ + x * C::kTileBytes + d * kHalfBytes, &tmq, &bar_q, 64 * d, head_of(e), q0 + r0, pol_q);
+    bool ok = true, more = true;
+    uint32_t kt = 0, qi = 0;                                 // K/V tiles and items with keys so far
+    for (uint32_t i = 0; more && ok; ++i) {
+      // Ask for the item after this one.
+      ok = all(i < 2 || mbar_wait(&bar_read[i & 1], ((i >> 1) - 1) & 1u));
+      if (ok && lane == 0) {
+        mbar_arrive_expect_tx(&bar_next[i & 1], 16);
+        ask_for_cta(&response[i & 1], &bar_next[i & 1]);
       }
-    }
-    int t = 0;
-    for (; ok && t < n; ++t) {
-      const int st = t % kStages;
-      const uint32_t par = uint32_t(t / kStages - 1) & 1u;
-      if (t >= kStages && !(ok = mbar_wait(&bar_k_empty[st], par))) break;
-      mbar_arrive_expect_tx(&bar_k_full[st], C::kTileBytes);
-      for (int d = 0; d < D / 64; ++d)
-        tma_load_3d(sK + st * C::kTileBytes + d * kHalfBytes, &tmk, &bar_k_full[st], 64 * d, h, k0 + t * kTile, pol_kv);
-      if (t >= kStages && !(ok = mbar_wait(&bar_v_empty[st], par))) {
-        (void)mbar_wait(&bar_k_full[st], uint32_t(t / kStages) & 1u);   // the K tile just started
-        break;
+      const Item it = item_of(p, bx, by, bz, gridDim.z);
+      if (lane == 0 && bz == 0 && bx == 0) {                 // one item of every sequence looks at the lengths
+        const int Lq = p.cu_q[by + 1] - p.cu_q[by];
+        if ((it.rows == 0 && Lq != 0) || Lq > p.max_q_len || it.Lk < 0 || it.k0 < 0 || it.Lk > p.total_k - it.k0 ||
+            (by == 0 && (it.q0 != 0 || it.k0 != 0)))
+          set_error(p.err, PKV_DEVERR_CHUNK);
       }
-      mbar_arrive_expect_tx(&bar_v_full[st], C::kTileBytes);
-      for (int d = 0; d < D / 64; ++d)
-        tma_load_3d(sV + st * C::kTileBytes + d * kHalfBytes, &tmv, &bar_v_full[st], 64 * d, h, k0 + t * kTile, pol_kv);
+      if (ok && it.n > 0) {
+        ok = all(qi == 0 || mbar_wait(&bar_q_empty, (qi - 1) & 1u));
+        if (ok && lane == 0) {
+          mbar_arrive_expect_tx(&bar_q, 2 * C::kTileBytes);
+          for (int x = 0; x < 2; ++x) {
+            // A block past the sequence's end reads rows that nobody stores: its own first ones.
+            const int e = it.e0 + x, r0 = e / G * kTile < it.rows ? e / G * kTile : 0;
+            for (int d = 0; d < D / 64; ++d)
+              tma_load_3d(sQ + x * C::kTileBytes + d * kHalfBytes, &tmq, &bar_q, 64 * d, it.h * G + e % G, it.q0 + r0, pol_q);
+          }
+        }
+        ++qi;
+      }
+      for (int t = 0; ok && t < it.n; ++t, ++kt) {
+        const uint32_t st = kt % kStages, par = (kt / kStages - 1) & 1u;
+        ok = all(kt < uint32_t(kStages) || mbar_wait(&bar_k_empty[st], par));
+        if (ok && lane == 0) {
+          mbar_arrive_expect_tx(&bar_k_full[st], C::kTileBytes);
+          for (int d = 0; d < D / 64; ++d)
+            tma_load_3d(sK + st * C::kTileBytes + d * kHalfBytes, &tmk, &bar_k_full[st], 64 * d, it.h, it.k0 + t * kTile, pol_kv);
+        }
+        const bool v_ok = ok && all(kt < uint32_t(kStages) || mbar_wait(&bar_v_empty[st], par));
+        if (ok && !v_ok) (void)mbar_wait(&bar_k_full[st], (kt / kStages) & 1u);   // the K tile just started
+        ok = v_ok;
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&bar_v_full[st], C::kTileBytes);
+          for (int d = 0; d < D / 64; ++d)
+            tma_load_3d(sV + st * C::kTileBytes + d * kHalfBytes, &tmv, &bar_v_full[st], 64 * d, it.h, it.k0 + t * kTile, pol_kv);
+        }
+      }
+      // Also after a wait gave up: no answer may still be on its way when the CTA leaves.
+      bool came = true;
+      more = next_item(i, bx, by, bz, came);
+      ok = ok && came;
     }
-    // Drain: the last loads of each stage have landed and the commits that release the stages have
-    // arrived before the CTA may leave (each wait bounded).
-    if (!ok) {
-      set_error(p.err, PKV_DEVERR_TIMEOUT);
-      (void)mbar_wait(&bar_q, 0);
-    }
-    for (int u = max(0, t - kStages); u < t; ++u) {
-      const int st = u % kStages;
-      const uint32_t par = uint32_t(u / kStages) & 1u;
+    // Drain: the last loads of each stage have landed and the commits that release the stages and Q
+    // have arrived before the CTA may leave (each wait bounded).
+    if (!ok && lane == 0) set_error(p.err, PKV_DEVERR_TIMEOUT);
+    if (qi > 0) (void)mbar_wait(&bar_q, (qi - 1) & 1u);
+    if (ok && qi > 0) ok = mbar_wait(&bar_q_empty, (qi - 1) & 1u);
+    for (uint32_t u = kt < uint32_t(kStages) ? 0 : kt - kStages; u < kt; ++u) {
+      const uint32_t st = u % kStages, par = (u / kStages) & 1u;
       (void)mbar_wait(&bar_k_full[st], par);
       (void)mbar_wait(&bar_v_full[st], par);
       if (ok) ok = mbar_wait(&bar_k_empty[st], par) && mbar_wait(&bar_v_empty[st], par);
@@ -226,206 +322,233 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t idesc_o = umma_idesc_f16(kBF16, 128, D, false, true);
     const uint64_t dQ = umma_sdesc_sw128(smem_u32(sQ), 16, 1024), dK = umma_sdesc_sw128(smem_u32(sK), 16, 1024);
     const uint64_t dV = umma_sdesc_sw128(smem_u32(sV), kHalfBytes, 1024);
-    auto all = [](bool v) -> bool { return __all_sync(0xffffffffu, v); };
-    bool ok = n == 0 || all(mbar_wait(&bar_q, 0));
-    auto landed = [&](uint64_t* bar, int t) -> bool { return all(mbar_wait(bar, uint32_t(t / kStages) & 1u)); };
+    bool ok = true, more = true;
+    uint32_t kt = 0, qi = 0, s_of[2] = {0, 0}, o_of[2] = {0, 0};   // tiles; items with keys; steps and items of A, B
     // S_x(t) = Q_x K_t^T into TMEM columns 128x .. 128x + 127.  A descriptor advances by bytes / 16.
-    auto issue_s = [&](int x, int t) -> bool {
-      const int st = t % kStages;
-      if (!landed(&bar_k_full[st], t)) return false;
+    auto issue_s = [&](int x, uint32_t tile) -> bool {
+      const uint32_t st = tile % kStages;
+      if (!all(mbar_wait(&bar_k_full[st], (tile / kStages) & 1u))) return false;
       tc_fence_after();
       const uint64_t a = dQ + uint32_t(x * C::kTileBytes / 16), b = dK + uint32_t(st * C::kTileBytes / 16);
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk)
         mma_ss(lead, tmem + 128 * x, a + ((kk >> 2) * kHalfBytes + (kk & 3) * 32) / 16,
-                      b + ((kk >> 2) * kHalfBytes + (kk & 3) * 32) / 16, idesc_s, kk > 0);
+               b + ((kk >> 2) * kHalfBytes + (kk & 3) * 32) / 16, idesc_s, kk > 0);
       commit(lead, &bar_s_full[x]);
       return true;
     };
     // O_x += P_x(t) V_t; P_x of each half of the keys in the first 32 columns of that half's scores.
-    auto issue_pv = [&](int x, int t) -> bool {
-      const int st = t % kStages;
-      if (!landed(&bar_v_full[st], t)) return false;         // (long before P)
-      if (!all(mbar_wait(&bar_p_full[x], uint32_t(t) & 1u))) return false;
+    auto issue_pv = [&](int x, uint32_t tile, bool first) -> bool {
+      const uint32_t st = tile % kStages;
+      if (!all(mbar_wait(&bar_v_full[st], (tile / kStages) & 1u))) return false;   // (long before P)
+      if (first && o_of[x] > 0 && !all(mbar_wait(&bar_o_free[x], (o_of[x] - 1) & 1u))) return false;
+      if (!all(mbar_wait(&bar_p_full[x], s_of[x] & 1u))) return false;
+      ++s_of[x];
       tc_fence_after();
       const uint64_t b = dV + uint32_t(st * C::kTileBytes / 16);
 #pragma unroll
       for (int kk = 0; kk < kTile / 16; ++kk)
-        mma_ts(lead, tmem + 256 + 128 * x, tmem + 128 * x + (kk >> 2) * 64 + (kk & 3) * 8, b + kk * 2048 / 16, idesc_o, t > 0 || kk > 0);
+        mma_ts(lead, tmem + 256 + 128 * x, tmem + 128 * x + (kk >> 2) * 64 + (kk & 3) * 8, b + kk * 2048 / 16, idesc_o,
+               !first || kk > 0);
       commit(lead, &bar_pv_done[x]);
       return true;
     };
-    // One block may walk fewer tiles than the other.  A stage is released once both have read it.
-    if (ok && n > 0) {
-      ok = (na == 0 || issue_s(0, 0)) && (nb == 0 || issue_s(1, 0));
-      commit(lead, &bar_k_empty[0]);
-    }
-    for (int t = 0; ok && t < n; ++t) {
-      if (t < na) ok = issue_pv(0, t);
-      if (ok && t + 1 < na) ok = issue_s(0, t + 1);
-      if (ok && t < nb) ok = issue_pv(1, t);
-      commit(lead, &bar_v_empty[t % kStages]);
-      if (ok && t + 1 < nb) ok = issue_s(1, t + 1);
-      if (t + 1 < n) commit(lead, &bar_k_empty[(t + 1) % kStages]);
+    for (uint32_t i = 0; more && ok; ++i) {
+      const Item it = item_of(p, bx, by, bz, gridDim.z);
+      if (it.n > 0) {
+        ok = all(mbar_wait(&bar_q, qi & 1u));
+        ++qi;
+        // One block may walk fewer tiles than the other.  A stage is released once both have read it.
+        ok = ok && (it.na == 0 || issue_s(0, kt)) && (it.nb == 0 || issue_s(1, kt));
+        commit(lead, &bar_k_empty[kt % kStages]);
+        if (it.n == 1) commit(lead, &bar_q_empty);
+        for (int t = 0; ok && t < it.n; ++t, ++kt) {
+          if (t < it.na) ok = issue_pv(0, kt, t == 0);
+          if (ok && t + 1 < it.na) ok = issue_s(0, kt + 1);
+          if (ok && t < it.nb) ok = issue_pv(1, kt, t == 0);
+          commit(lead, &bar_v_empty[kt % kStages]);
+          if (ok && t + 1 < it.nb) ok = issue_s(1, kt + 1);
+          if (t + 1 < it.n) commit(lead, &bar_k_empty[(kt + 1) % kStages]);
+          if (t + 2 == it.n) commit(lead, &bar_q_empty);     // the item's last scores are on their way
+        }
+        o_of[0] += it.na > 0;
+        o_of[1] += it.nb > 0;
+      }
+      bool came = true;
+      more = next_item(i, bx, by, bz, came);
+      ok = ok && came;
     }
     if (!ok && lane == 0) set_error(p.err, PKV_DEVERR_TIMEOUT);
-  } else if (warp >= 2) {
+  } else {
     // ---------------- softmax: two threads per query row ----------------
     const int x = (warp - 2) >> 3, hf = ((warp - 2) >> 2) & 1;   // row block; half of the keys (and of O)
     const int quarter = warp & 3, r = 32 * quarter + lane;   // TMEM lane == row of the block
     const uint32_t lane_off = uint32_t(32 * quarter) << 16;
-    const int e = e0 + x;
-    const int row = first_row(e) + r;
-    const int nx = x == 0 ? na : nb;
     constexpr int kKeys = kTile / 2, kODims = D / 2;
     const float slog = p.scale_log2;                         // > 0, so max(s) * slog = max(s * slog)
     const uint32_t tS = tmem + 128 * x + lane_off + kKeys * hf;   // scores, and P over them
     const uint32_t tO = tmem + 256 + 128 * x + lane_off + kODims * hf;
-    // The two warps of a row quarter meet here, once per tile and once at the end, also after a wait
-    // gave up: then they only walk on, so that neither is left waiting for the other.
-    auto meet = [&]() {
-      asm volatile("bar.sync %0, 64;" ::"r"(1 + 4 * x + quarter) : "memory");
-    };
-    float m = -INFINITY, l = 0.f;                            // m of the row, l of this thread's keys
-    bool ok = true;
-    for (int t = 0; t < nx; ++t) {
-      // Waiting for PV(t - 1) on every tile keeps that barrier at most one phase ahead of this wait.
-      ok = __all_sync(0xffffffffu, ok && mbar_wait(&bar_s_full[x], uint32_t(t) & 1u) &&
-                                       (t == 0 || mbar_wait(&bar_pv_done[x], uint32_t(t - 1) & 1u)));
-      if (!ok) {
-        meet();
-        continue;
-      }
-      tc_fence_after();
-      const int lim = min(row + shift + 1, Lk) - t * kTile - kKeys * hf;   // keys 0 .. lim - 1 are attended
-      float s[kKeys];
+    uint8_t* out_stage = sOut + (warp - 2) * C::kOutBytes;
+    // The two warps of a row quarter meet here, once per tile and once per item, also after a wait
+    // gave up: then they only walk on to the item's end, so that neither is left waiting for the other.
+    auto meet = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + 4 * x + quarter) : "memory"); };
+    bool ok = true, more = true;
+    uint32_t kt = 0, steps = 0, meets = 0;                   // tiles; this block's steps; meetings
+    for (uint32_t i = 0; more && ok; ++i) {
+      const Item it = item_of(p, bx, by, bz, gridDim.z);
+      const int e = it.e0 + x, row = e / G * kTile + r;
+      const int nx = x == 0 ? it.na : it.nb;
+      float m = -INFINITY, l = 0.f;                          // m of the row, l of this thread's keys
+      for (int t = 0; t < nx; ++t, ++meets) {
+        // Waiting for PV(t - 1) on every tile keeps that barrier at most one phase ahead of this wait.
+        ok = all(ok && mbar_wait(&bar_s_full[x], (steps + t) & 1u) &&
+                 (t == 0 || mbar_wait(&bar_pv_done[x], (steps + t - 1) & 1u)));
+        if (!ok) {
+          meet();
+          continue;
+        }
+        tc_fence_after();
+        const int lim = min(row + it.Lk - it.Lq + 1, it.Lk) - t * kTile - kKeys * hf;   // keys 0 .. lim - 1 are attended
+        float s[kKeys];
 #pragma unroll
-      for (int cc = 0; cc < kKeys / 32; ++cc) tmem_ld32(tS + 32 * cc, *reinterpret_cast<float(*)[32]>(s + 32 * cc));
-      tmem_wait_ld();
-      if (lim < kKeys) {
+        for (int cc = 0; cc < kKeys / 32; ++cc) tmem_ld32(tS + 32 * cc, *reinterpret_cast<float(*)[32]>(s + 32 * cc));
+        tmem_wait_ld();
+        if (lim < kKeys) {
 #pragma unroll
-        for (int i = 0; i < kKeys; ++i) s[i] = i < lim ? s[i] : -INFINITY;
-      }
-      float mine;
-      {
+          for (int c = 0; c < kKeys; ++c) s[c] = c < lim ? s[c] : -INFINITY;
+        }
         float c4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-        for (int i = 4; i < kKeys; i += 8) {
+        for (int c = 4; c < kKeys; c += 8) {
 #pragma unroll
           for (int u = 0; u < 4; ++u)
-            if (i + 2 * u + 1 < kKeys) c4[u] = fmax3(c4[u], s[i + 2 * u], s[i + 2 * u + 1]);
+            if (c + 2 * u + 1 < kKeys) c4[u] = fmax3(c4[u], s[c + 2 * u], s[c + 2 * u + 1]);
         }
-        mine = fmaxf(fmaxf(c4[0], c4[1]), fmaxf(c4[2], c4[3]));
+        const float mine = fmaxf(fmaxf(c4[0], c4[1]), fmaxf(c4[2], c4[3]));
+        float* xm = &exchange[x][meets & 1][0][r];
+        xm[kTile * hf] = mine;
+        meet();
+        const float mt = fmaxf(mine, xm[kTile * (hf ^ 1)]) * slog;
+        const bool grow = mt > m + kRescaleThreshold;        // also true for the first tile
+        const float m_prev = m;
+        if (grow) m = mt;
+        // The sequence's last tile may reach past its keys: zero those V rows, so that 0 * whatever
+        // the rows behind hold cannot turn into NaN (both blocks write the same zeros).
+        const int kb = t * kTile;
+        if (kb + kTile > it.Lk) {
+          const uint32_t st = (kt + t) % kStages;
+          ok = all(mbar_wait(&bar_v_full[st], ((kt + t) / kStages) & 1u));
+          if (!ok) continue;
+          if (kb + r >= it.Lk) {
+            const uint32_t vrow = smem_u32(sV + st * C::kTileBytes) + r * 128;
+#pragma unroll
+            for (int d = 0; d < D / 64; ++d)
+#pragma unroll
+              for (int cc = 0; cc < 4; ++cc) sts128(vrow + d * kHalfBytes + (4 * hf + cc) * 16, 0u, 0u, 0u, 0u);
+          }
+        }
+        // P over S (keys 2e, 2e + 1 in column e).  A row without keys so far has m = -inf and every
+        // s = -inf: m = 0 then gives P = 0.
+        const float mu = m == -INFINITY ? 0.f : m;
+        const uint64_t sl2 = pack_f32x2(slog, slog), nm2 = pack_f32x2(-mu, -mu);
+        uint64_t acc0 = pack_f32x2(0.f, 0.f), acc1 = acc0;
+#pragma unroll
+        for (int hb = 0; hb < kKeys / 32; ++hb) {
+          uint32_t w[16];
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            const int c0 = 32 * hb + 2 * c;
+            const uint64_t x2 = fma_f32x2(pack_f32x2(s[c0], s[c0 + 1]), sl2, nm2);
+            const float pa = fast_exp2(lo_f32(x2)), pb = fast_exp2(hi_f32(x2));
+            const uint64_t p2 = pack_f32x2(pa, pb);
+            if (c & 1) acc1 = add_f32x2(acc1, p2);
+            else acc0 = add_f32x2(acc0, p2);
+            w[c] = pack2<kBF16>(pa, pb);
+          }
+          tmem_st16u(tS + 16 * hb, w);
+        }
+        if (__any_sync(0xffffffffu, grow && t >= 1)) {       // rescale this thread's half of O
+          const float alpha = (grow && m_prev != -INFINITY) ? fast_exp2(m_prev - m) : 1.f;
+#pragma unroll
+          for (int cc = 0; cc < kODims / 32; ++cc) {
+            float v[32];
+            tmem_ld32(tO + 32 * cc, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 32; ++c) v[c] *= alpha;
+            tmem_st32(tO + 32 * cc, v);
+          }
+          if (grow) l *= alpha;
+        }
+        tmem_wait_st();
+        if (kb + kTile > it.Lk) fence_proxy_async_smem();    // the zeroed V rows, to the tensor cores
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar_p_full[x]);
+        const uint64_t acc = add_f32x2(acc0, acc1);
+        l += lo_f32(acc) + hi_f32(acc);
       }
-      float* xm = &exchange[x][t & 1][0][r];
-      xm[kTile * hf] = mine;
+      steps += nx;
+      kt += it.n;
+      // ---------------- output ----------------
+      ok = all(ok && (nx == 0 || mbar_wait(&bar_pv_done[x], (steps - 1) & 1u)));
+      tc_fence_after();
+      more = next_item(i, bx, by, bz, ok);
+      float* xl = &exchange[x][meets & 1][0][r];
+      xl[kTile * hf] = l;
+      if (lane == 0) fine[x][meets & 1][hf][quarter] = ok;
       meet();
-      const float mt = fmaxf(mine, xm[kTile * (hf ^ 1)]) * slog;
-      const bool grow = mt > m + kRescaleThreshold;          // also true for the first tile
-      const float m_prev = m;
-      if (grow) m = mt;
-      // The sequence's last tile may reach past its keys: zero those V rows, so that 0 * whatever
-      // the rows behind hold cannot turn into NaN (both blocks write the same zeros).
-      const int kb = t * kTile;
-      if (kb + kTile > Lk) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&bar_v_full[t % kStages], uint32_t(t / kStages) & 1u));
-        if (!ok) continue;
-        if (kb + r >= Lk) {
-          const uint32_t vrow = smem_u32(sV + (t % kStages) * C::kTileBytes) + r * 128;
-#pragma unroll
-          for (int d = 0; d < D / 64; ++d)
-#pragma unroll
-            for (int cc = 0; cc < 4; ++cc) sts128(vrow + d * kHalfBytes + (4 * hf + cc) * 16, 0u, 0u, 0u, 0u);
-        }
-      }
-      // P over S (keys 2e, 2e + 1 in column e).  A row without keys so far has m = -inf and every
-      // s = -inf: m = 0 then gives P = 0.
-      const float mu = m == -INFINITY ? 0.f : m;
-      const uint64_t sl2 = pack_f32x2(slog, slog), nm2 = pack_f32x2(-mu, -mu);
-      uint64_t acc0 = pack_f32x2(0.f, 0.f), acc1 = acc0;
-#pragma unroll
-      for (int hb = 0; hb < kKeys / 32; ++hb) {
-        uint32_t w[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int c0 = 32 * hb + 2 * i;
-          const uint64_t x2 = fma_f32x2(pack_f32x2(s[c0], s[c0 + 1]), sl2, nm2);
-          const float pa = fast_exp2(lo_f32(x2)), pb = fast_exp2(hi_f32(x2));
-          const uint64_t p2 = pack_f32x2(pa, pb);
-          if (i & 1) acc1 = add_f32x2(acc1, p2);
-          else acc0 = add_f32x2(acc0, p2);
-          w[i] = pack2<kBF16>(pa, pb);
-        }
-        tmem_st16u(tS + 16 * hb, w);
-      }
-      const uint64_t acc = add_f32x2(acc0, acc1);
-      const float lsum = lo_f32(acc) + hi_f32(acc);
-      if (__any_sync(0xffffffffu, grow && t >= 1)) {         // rescale this thread's half of O
-        const float alpha = (grow && m_prev != -INFINITY) ? fast_exp2(m_prev - m) : 1.f;
+      l += xl[kTile * (hf ^ 1)];
+      ok = ok && fine[x][meets & 1][hf ^ 1][quarter] != 0;   // both warps go on, or none
+      ++meets;
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      // Half rows of 16-bit values, kStageRows at a time, through the warp's own staging area (16-byte
+      // chunk c of row rr at c ^ rr against bank conflicts), so that the warp writes whole runs.
+      uint32_t o[kODims / 2];
+      if (nx > 0 && ok) {
 #pragma unroll
         for (int cc = 0; cc < kODims / 32; ++cc) {
           float v[32];
           tmem_ld32(tO + 32 * cc, v);
           tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] *= alpha;
-          tmem_st32(tO + 32 * cc, v);
+          for (int c = 0; c < 16; ++c)
+            o[16 * cc + c] = l > 0.f ? pack2<kBF16>(v[2 * c] * inv, v[2 * c + 1] * inv) : 0u;
         }
-        if (grow) l *= alpha;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar_o_free[x]);          // the next item may overwrite O
+      } else {
+#pragma unroll
+        for (int c = 0; c < kODims / 2; ++c) o[c] = 0u;
       }
-      tmem_wait_st();
-      l += lsum;
-      if (kb + kTile > Lk) fence_proxy_async_smem();         // the zeroed V rows, to the tensor cores
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar_p_full[x]);
+      const int row0 = e / G * kTile + 32 * quarter;
+      if (ok && it.live && row0 < it.rows) {
+        constexpr int kChunks = D / 16, kRowBytes = D;       // of a half row
+        const uint32_t stage = smem_u32(out_stage);
+        uint8_t* dst = p.out + (int64_t(it.q0) * p.out_stride + int64_t(it.h * G + e % G) * D + kODims * hf) * 2;
+#pragma unroll
+        for (int k = 0; k < 32 / C::kStageRows; ++k) {
+          if (lane / C::kStageRows == k) {
+            const int rr = lane % C::kStageRows;
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c)
+              sts128(stage + rr * kRowBytes + ((c ^ (rr & (kChunks - 1))) << 4), o[4 * c], o[4 * c + 1], o[4 * c + 2],
+                     o[4 * c + 3]);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int c0 = 0; c0 < C::kStageRows * kChunks; c0 += 32) {
+            const int c = (c0 + lane) % kChunks, rr = (c0 + lane) / kChunks, orow = row0 + C::kStageRows * k + rr;
+            if (orow < it.rows)
+              reinterpret_cast<uint4*>(dst + orow * p.out_stride * 2)[c] =
+                  lds128(stage + rr * kRowBytes + ((c ^ (rr & (kChunks - 1))) << 4));
+          }
+          __syncwarp();
+        }
+      }
     }
-    if (ok && nx > 0) ok = mbar_wait(&bar_pv_done[x], uint32_t(nx - 1) & 1u);
-    if (nx == 0 && n > 0) ok = mbar_wait(&bar_q, 0);         // the output is staged where Q lands
-    ok = __all_sync(0xffffffffu, ok);
     if (!ok && lane == 0) set_error(p.err, PKV_DEVERR_TIMEOUT);
-    tc_fence_after();
-    // ---------------- output ----------------
-    // Every product that reads this block's Q is done: its area stages the warp's 32 half rows of
-    // 16-bit values, 16-byte chunk c of a row at c ^ (row mod chunks) against bank conflicts, and the
-    // warp writes runs of whole half rows.
-    exchange[x][nx & 1][hf][r] = l;                          // tile nx - 1 used the other parity
-    meet();
-    if (ok && first_row(e) + 32 * quarter < rows) {
-      constexpr int kRowBytes = D, kChunks = D / 16;         // of a half row
-      l += exchange[x][nx & 1][hf ^ 1][r];
-      const float inv = l > 0.f ? 1.f / l : 0.f;
-      const uint32_t stage = smem_u32(sQ) + x * C::kTileBytes + (hf * 4 + quarter) * 32 * kRowBytes;
-#pragma unroll
-      for (int cc = 0; cc < kODims / 32; ++cc) {
-        float v[32];
-        if (nx > 0) {
-          tmem_ld32(tO + 32 * cc, v);
-          tmem_wait_ld();
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int c = 4 * cc + i;
-          const uint32_t at = stage + lane * kRowBytes + ((c ^ (lane & (kChunks - 1))) << 4);
-          if (l > 0.f)
-            sts128(at, pack2<kBF16>(v[8 * i] * inv, v[8 * i + 1] * inv),
-                   pack2<kBF16>(v[8 * i + 2] * inv, v[8 * i + 3] * inv),
-                   pack2<kBF16>(v[8 * i + 4] * inv, v[8 * i + 5] * inv),
-                   pack2<kBF16>(v[8 * i + 6] * inv, v[8 * i + 7] * inv));
-          else
-            sts128(at, 0u, 0u, 0u, 0u);
-        }
-      }
-      __syncwarp();
-      uint8_t* dst = p.out + (int64_t(q0) * p.out_stride + int64_t(head_of(e)) * D + kODims * hf) * 2;
-#pragma unroll
-      for (int k = 0; k < kChunks; ++k) {
-        const int i = 32 * k + lane, rr = i / kChunks, c = i % kChunks;
-        const uint4 val = lds128(stage + rr * kRowBytes + ((c ^ (rr & (kChunks - 1))) << 4));
-        const int orow = first_row(e) + 32 * quarter + rr;
-        if (orow < rows) reinterpret_cast<uint4*>(dst + orow * p.out_stride * 2)[c] = val;
-      }
-    }
   }
   tc_fence_before();
   __syncthreads();
