@@ -144,7 +144,8 @@ struct Item {
   int q0, k0, Lq, Lk;     // the sequence's first rows and lengths
   int rows;               // query rows to compute (at most max_q_len)
   int e0;                 // block A is row block e0 of the (sequence, kv head), B the next one
-  int na, nb, n;          // key tiles that A and B walk, and the larger
+  int t0;                 // first key tile
+  int na, nb, n;          // key tiles that A and B walk from there, and the larger
   bool live;              // there is something to do
 };
 
@@ -173,10 +174,39 @@ __device__ __forceinline__ Item item_of(const PromptParams& p, int x, int y, int
   it.na = it.live ? tiles_of(it.e0) : 0;
   it.nb = it.live ? tiles_of(it.e0 + 1) : 0;
   it.n = max(it.na, it.nb);
+  it.t0 = 0;
   return it;
 }
 
-template <bool kBF16, int D>
+// Part `part` of `parts` of an item's key tiles.
+__device__ __forceinline__ void take_part(Item& it, int part, int parts) {
+  const int t1 = int(int64_t(it.n) * (part + 1) / parts);
+  it.t0 = int(int64_t(it.n) * part / parts);
+  it.na = max(0, min(it.na, t1) - it.t0);
+  it.nb = max(0, min(it.nb, t1) - it.t0);
+  it.n = max(it.na, it.nb);
+}
+
+// The shared::cluster address of this CTA's shared address `addr` in the CTA of the given rank.
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+// Copies `bytes` (a multiple of 16) from this CTA's shared memory to another CTA's of the cluster,
+// completing on that CTA's mbarrier; dst and bar are shared::cluster addresses.
+__device__ __forceinline__ void copy_to_cta(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "r"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
+// kSplit: a cluster of 2 or 4 CTAs works on one item, each on a part of the key tiles (taken when there
+// are fewer items than SMs; see launch).  Each CTA finishes an equal share of the rows: one of the two
+// blocks, or 64 rows of one.  The others send it those rows, unnormalised, with their maxima and sums, by
+// bulk copies from their idle K/V stages to its idle Q area (and the place of its own rows).  Reading
+// them from the other CTA's shared memory with loads took 14 us instead.
+template <bool kBF16, int D, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                   const __grid_constant__ CUtensorMap tmv, const PromptParams p) {
@@ -190,6 +220,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       bar_v_empty[kStages], bar_s_full[2], bar_p_full[2], bar_pv_done[2], bar_o_free[2];
   __shared__ uint32_t tmem_base_sh;
   __shared__ float exchange[2][2][2][kTile];                 // [block][step parity][key half][row]
+  __shared__ __align__(16) float2 part_ml[2][kSplit ? kTile : 1];   // [block][row]: maximum and sum over this CTA's keys
+  __shared__ __align__(16) float2 recv_ml[3][kSplit ? kTile : 1];   // [sender][row of this CTA's share]
+  __shared__ __align__(8) uint64_t bar_recv;
   __shared__ uint32_t fine[2][2][2][4];                      // [block][step parity][key half][row quarter]: the warp goes on
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // uniform in the warp
 
@@ -207,6 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tensormap(&tmv);
     mbar_init(&bar_q, 1);
     mbar_init(&bar_q_empty, 1);
+    mbar_init(&bar_recv, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar_next[i], 1);
       mbar_init(&bar_read[i], kThreads / 32);                // every warp, the asking one too
@@ -238,6 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto all = [](bool v) -> bool { return __all_sync(0xffffffffu, v); };
   // The next item's block index, for a whole warp: false when there is none, or (ok false) no answer.
   auto next_item = [&](uint32_t i, int& bx, int& by, int& bz, bool& ok) -> bool {
+    if constexpr (kSplit) return false;
     ok = all(ok && mbar_wait(&bar_next[i & 1], (i >> 1) & 1u));
     if (!ok) return false;
     const bool got = read_cta(&response[i & 1], bx, by, bz);
@@ -246,7 +281,47 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) mbar_arrive(&bar_read[i & 1]);
     return got;
   };
+  // Writes a warp's 32 half rows of block e, one per lane as 16-bit pairs: kStageRows at a time through
+  // the warp's own staging area (16-byte chunk c of row rr at c ^ rr against bank conflicts), so that the
+  // warp writes whole runs.
+  auto write_rows = [&](const Item& it, int e, int hf, int quarter, uint8_t* area, const uint32_t (&o)[D / 4]) {
+    const int row0 = e / G * kTile + 32 * quarter;
+    if (row0 >= it.rows) return;
+    constexpr int kChunks = D / 16, kRowBytes = D;           // of a half row
+    const uint32_t stage = smem_u32(area);
+    uint8_t* dst = p.out + (int64_t(it.q0) * p.out_stride + int64_t(it.h * G + e % G) * D + D / 2 * hf) * 2;
+#pragma unroll
+    for (int k = 0; k < 32 / C::kStageRows; ++k) {
+      if (lane / C::kStageRows == k) {
+        const int rr = lane % C::kStageRows;
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c)
+          sts128(stage + rr * kRowBytes + ((c ^ (rr & (kChunks - 1))) << 4), o[4 * c], o[4 * c + 1], o[4 * c + 2],
+                 o[4 * c + 3]);
+      }
+      __syncwarp();
+#pragma unroll
+      for (int c0 = 0; c0 < C::kStageRows * kChunks; c0 += 32) {
+        const int c = (c0 + lane) % kChunks, rr = (c0 + lane) / kChunks, orow = row0 + C::kStageRows * k + rr;
+        if (orow < it.rows)
+          reinterpret_cast<uint4*>(dst + orow * p.out_stride * 2)[c] =
+              lds128(stage + rr * kRowBytes + ((c ^ (rr & (kChunks - 1))) << 4));
+      }
+      __syncwarp();
+    }
+  };
   int bx = blockIdx.x, by = blockIdx.y, bz = blockIdx.z;
+  int part = 0, parts = 1;
+  if constexpr (kSplit) {
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(parts));
+    part = int(cluster_ctarank());
+    bx /= parts;
+  }
+  auto this_item = [&]() -> Item {
+    Item it = item_of(p, bx, by, bz, gridDim.z);
+    if constexpr (kSplit) take_part(it, part, parts);
+    return it;
+  };
 
   if (warp == 0) {
     // ---------------- TMA producer ----------------
@@ -257,12 +332,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (uint32_t i = 0; more && ok; ++i) {
       // Ask for the item after this one.
       ok = all(i < 2 || mbar_wait(&bar_read[i & 1], ((i >> 1) - 1) & 1u));
-      if (ok && lane == 0) {
+      if (!kSplit && ok && lane == 0) {
         mbar_arrive_expect_tx(&bar_next[i & 1], 16);
         ask_for_cta(&response[i & 1], &bar_next[i & 1]);
       }
-      const Item it = item_of(p, bx, by, bz, gridDim.z);
-      if (lane == 0 && bz == 0 && bx == 0) {                 // one item of every sequence looks at the lengths
+      const Item it = this_item();
+      if (lane == 0 && bz == 0 && bx == 0 && part == 0) {                 // one item of every sequence looks at the lengths
         const int Lq = p.cu_q[by + 1] - p.cu_q[by];
         if ((it.rows == 0 && Lq != 0) || Lq > p.max_q_len || it.Lk < 0 || it.k0 < 0 || it.Lk > p.total_k - it.k0 ||
             (by == 0 && (it.q0 != 0 || it.k0 != 0)))
@@ -287,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok && lane == 0) {
           mbar_arrive_expect_tx(&bar_k_full[st], C::kTileBytes);
           for (int d = 0; d < D / 64; ++d)
-            tma_load_3d(sK + st * C::kTileBytes + d * kHalfBytes, &tmk, &bar_k_full[st], 64 * d, it.h, it.k0 + t * kTile, pol_kv);
+            tma_load_3d(sK + st * C::kTileBytes + d * kHalfBytes, &tmk, &bar_k_full[st], 64 * d, it.h, it.k0 + (it.t0 + t) * kTile, pol_kv);
         }
         const bool v_ok = ok && all(kt < uint32_t(kStages) || mbar_wait(&bar_v_empty[st], par));
         if (ok && !v_ok) (void)mbar_wait(&bar_k_full[st], (kt / kStages) & 1u);   // the K tile just started
@@ -296,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
           mbar_arrive_expect_tx(&bar_v_full[st], C::kTileBytes);
           for (int d = 0; d < D / 64; ++d)
-            tma_load_3d(sV + st * C::kTileBytes + d * kHalfBytes, &tmv, &bar_v_full[st], 64 * d, it.h, it.k0 + t * kTile, pol_kv);
+            tma_load_3d(sV + st * C::kTileBytes + d * kHalfBytes, &tmv, &bar_v_full[st], 64 * d, it.h, it.k0 + (it.t0 + t) * kTile, pol_kv);
         }
       }
       // Also after a wait gave up: no answer may still be on its way when the CTA leaves.
@@ -354,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       return true;
     };
     for (uint32_t i = 0; more && ok; ++i) {
-      const Item it = item_of(p, bx, by, bz, gridDim.z);
+      const Item it = this_item();
       if (it.n > 0) {
         ok = all(mbar_wait(&bar_q, qi & 1u));
         ++qi;
@@ -395,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true, more = true;
     uint32_t kt = 0, steps = 0, meets = 0;                   // tiles; this block's steps; meetings
     for (uint32_t i = 0; more && ok; ++i) {
-      const Item it = item_of(p, bx, by, bz, gridDim.z);
+      const Item it = this_item();
       const int e = it.e0 + x, row = e / G * kTile + r;
       const int nx = x == 0 ? it.na : it.nb;
       float m = -INFINITY, l = 0.f;                          // m of the row, l of this thread's keys
@@ -408,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           continue;
         }
         tc_fence_after();
-        const int lim = min(row + it.Lk - it.Lq + 1, it.Lk) - t * kTile - kKeys * hf;   // keys 0 .. lim - 1 are attended
+        const int lim = min(row + it.Lk - it.Lq + 1, it.Lk) - (it.t0 + t) * kTile - kKeys * hf;   // keys 0 .. lim - 1 are attended
         float s[kKeys];
 #pragma unroll
         for (int cc = 0; cc < kKeys / 32; ++cc) tmem_ld32(tS + 32 * cc, *reinterpret_cast<float(*)[32]>(s + 32 * cc));
@@ -434,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (grow) m = mt;
         // The sequence's last tile may reach past its keys: zero those V rows, so that 0 * whatever
         // the rows behind hold cannot turn into NaN (both blocks write the same zeros).
-        const int kb = t * kTile;
+        const int kb = (it.t0 + t) * kTile;
         if (kb + kTile > it.Lk) {
           const uint32_t st = (kt + t) % kStages;
           ok = all(mbar_wait(&bar_v_full[st], ((kt + t) / kStages) & 1u));
@@ -502,8 +577,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = ok && fine[x][meets & 1][hf ^ 1][quarter] != 0;   // both warps go on, or none
       ++meets;
       const float inv = l > 0.f ? 1.f / l : 0.f;
-      // Half rows of 16-bit values, kStageRows at a time, through the warp's own staging area (16-byte
-      // chunk c of row rr at c ^ rr against bank conflicts), so that the warp writes whole runs.
+      if constexpr (kSplit) {                                // the rows are finished below
+        if (hf == 0) part_ml[x][r] = make_float2(nx > 0 ? m : -INFINITY, nx > 0 ? l : 0.f);
+        break;
+      }
       uint32_t o[kODims / 2];
       if (nx > 0 && ok) {
 #pragma unroll
@@ -522,36 +599,128 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < kODims / 2; ++c) o[c] = 0u;
       }
-      const int row0 = e / G * kTile + 32 * quarter;
-      if (ok && it.live && row0 < it.rows) {
-        constexpr int kChunks = D / 16, kRowBytes = D;       // of a half row
-        const uint32_t stage = smem_u32(out_stage);
-        uint8_t* dst = p.out + (int64_t(it.q0) * p.out_stride + int64_t(it.h * G + e % G) * D + kODims * hf) * 2;
-#pragma unroll
-        for (int k = 0; k < 32 / C::kStageRows; ++k) {
-          if (lane / C::kStageRows == k) {
-            const int rr = lane % C::kStageRows;
-#pragma unroll
-            for (int c = 0; c < kChunks; ++c)
-              sts128(stage + rr * kRowBytes + ((c ^ (rr & (kChunks - 1))) << 4), o[4 * c], o[4 * c + 1], o[4 * c + 2],
-                     o[4 * c + 3]);
-          }
-          __syncwarp();
-#pragma unroll
-          for (int c0 = 0; c0 < C::kStageRows * kChunks; c0 += 32) {
-            const int c = (c0 + lane) % kChunks, rr = (c0 + lane) / kChunks, orow = row0 + C::kStageRows * k + rr;
-            if (orow < it.rows)
-              reinterpret_cast<uint4*>(dst + orow * p.out_stride * 2)[c] =
-                  lds128(stage + rr * kRowBytes + ((c ^ (rr & (kChunks - 1))) << 4));
-          }
-          __syncwarp();
-        }
-      }
+      if (ok) write_rows(it, e, hf, quarter, out_stage, o);
     }
     if (!ok && lane == 0) set_error(p.err, PKV_DEVERR_TIMEOUT);
   }
   tc_fence_before();
-  __syncthreads();
+  if constexpr (!kSplit) {
+    __syncthreads();
+  } else {
+    // ---------------- combine the parts ----------------
+    // Shares: `regions` rows of a block each, in the order (block 0 rows, block 1 rows).  Half a row is
+    // kHalf bytes of fp32, 16-byte chunk c of row r at c ^ (r mod 8) against bank conflicts.
+    const Item it = this_item();                             // (read again: uniform over the cluster)
+    constexpr int kHalf = 2 * D;
+    const int share = 2 * kTile / parts;                     // 128 or 64 rows
+    auto rows_in = [&](int owner) -> int {                   // rows of a share that exist
+      const int e = it.e0 + owner * share / kTile, first = e / G * kTile + owner * share % kTile;
+      return min(share, max(0, it.rows - first));
+    };
+    if (threadIdx.x == 0)
+      mbar_arrive_expect_tx(&bar_recv, (parts - 1) * (rows_in(part) * 2 * kHalf + share * int(sizeof(float2))));
+    __syncwarp();
+    cluster_sync();                                          // every CTA's products are done: stages and Q are free
+    tc_fence_after();
+    if (warp >= 2) {
+      const int x = (warp - 2) >> 3, hf = ((warp - 2) >> 2) & 1, quarter = warp & 3, r = 32 * quarter + lane;
+      constexpr int kODims = D / 2;                          // elements of half a row
+      static_assert(2 * kTile * 2 * kHalf <= 2 * kStages * C::kTileBytes, "all rows fit in the K/V stages");
+      static_assert(kTile * 2 * kHalf <= 2 * C::kTileBytes, "a share of 128 rows, or two of 64, fit in the Q area");
+      const int owner = (x * kTile + 32 * quarter) / share, rr = (x * kTile + r) % share;   // rr: row of the share
+      const bool any = (x == 0 ? it.na : it.nb) > 0;
+      const uint32_t tO = tmem + (uint32_t(32 * quarter) << 16) + 256 + 128 * x + kODims * hf;
+      // Share s of this CTA's rows: [hf][row][kHalf], at 2 * share * kHalf * s in the stages.  What CTA
+      // `from` sends to CTA `to` lands in its slot (from - to - 1) mod parts: slots 0 (and 1) in the Q area,
+      // slot 2 in the place of its own share.
+      auto slot_base = [&](int slot, int to) -> uint32_t {
+        return slot < 2 ? smem_u32(sQ) + slot * 2 * share * kHalf : smem_u32(sK) + to * 2 * share * kHalf;
+      };
+      const uint32_t in_share = (hf * share + rr) * kHalf;   // this thread's half row in any share
+      if (owner != part) {
+        // ---- send: this warp's 32 half rows as soon as they are staged ----
+        const bool have = any && part_ml[x][r].x != -INFINITY;   // else O holds nothing, or was never written
+        const uint32_t row = smem_u32(sK) + owner * 2 * share * kHalf + in_share;
+#pragma unroll
+        for (int cc = 0; cc < kODims / 32; ++cc) {
+          float v[32];
+          if (any) {
+            tmem_ld32(tO + 32 * cc, v);
+            tmem_wait_ld();
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t at = row + (((8 * cc + i) ^ (r & 7)) << 4);
+            if (have)
+              sts128(at, __float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]),
+                     __float_as_uint(v[4 * i + 3]));
+            else
+              sts128(at, 0u, 0u, 0u, 0u);
+          }
+        }
+        fence_proxy_async_smem();                            // the staged rows, to the copies
+        __syncwarp();
+        if (lane == 0) {
+          const int slot = (part - owner - 1 + parts) % parts, rr0 = rr, n32 = min(32, max(0, rows_in(owner) - rr0));
+          const uint32_t bar = cluster_addr(smem_u32(&bar_recv), owner);
+          if (n32 > 0)
+            copy_to_cta(cluster_addr(slot_base(slot, owner) + in_share, owner), row, n32 * kHalf, bar);
+          if (hf == 0)
+            copy_to_cta(cluster_addr(smem_u32(&recv_ml[slot][rr0]), owner), smem_u32(&part_ml[x][32 * quarter]),
+                        32 * sizeof(float2), bar);
+        }
+      } else {
+        // ---- finish: this thread's half row from all parts ----
+        const bool got = __all_sync(0xffffffffu, mbar_wait(&bar_recv, 0));
+        if (!got && lane == 0) set_error(p.err, PKV_DEVERR_TIMEOUT);
+        float2 ml[4];
+        ml[3] = part_ml[x][r];
+        float mx = ml[3].x;
+#pragma unroll
+        for (int s = 0; s < 3; ++s) {
+          ml[s] = s + 1 < parts ? recv_ml[s][rr] : make_float2(-INFINITY, 0.f);
+          mx = fmaxf(mx, ml[s].x);
+        }
+        float w[4], den = 0.f;
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          w[s] = ml[s].x == -INFINITY ? 0.f : fast_exp2(ml[s].x - mx);
+          den += w[s] * ml[s].y;
+        }
+        const float inv = den > 0.f ? 1.f / den : 0.f;
+        uint32_t o[kODims / 2];
+#pragma unroll
+        for (int cc = 0; cc < kODims / 32; ++cc) {
+          float v[32];
+          if (any) {
+            tmem_ld32(tO + 32 * cc, v);
+            tmem_wait_ld();
+          }
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = any && w[3] > 0.f ? v[i] * (w[3] * inv) : 0.f;
+#pragma unroll
+          for (int s = 0; s < 3; ++s) {
+            if (s + 1 >= parts || !got) break;
+            const uint32_t row = slot_base(s, part) + in_share;
+            const float ws = w[s] * inv;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const uint4 q = lds128(row + (((8 * cc + i) ^ (r & 7)) << 4));
+              v[4 * i] += ws * __uint_as_float(q.x);
+              v[4 * i + 1] += ws * __uint_as_float(q.y);
+              v[4 * i + 2] += ws * __uint_as_float(q.z);
+              v[4 * i + 3] += ws * __uint_as_float(q.w);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[16 * cc + i] = pack2<kBF16>(v[2 * i], v[2 * i + 1]);
+        }
+        if (got) write_rows(it, it.e0 + x, hf, quarter, sOut + (warp - 2) * C::kOutBytes, o);
+      }
+    }
+    __syncwarp();
+    cluster_sync();                                          // every copy out of this CTA has arrived
+  }
   griddep_launch_dependents();
   if (warp == 1) {
     __syncwarp();
@@ -560,17 +729,67 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// Clusters of `parts` CTAs of the split kernel that the current device holds at once (0 on failure).
+template <bool kBF16, int D>
+int clusters_at_once(int parts) {
+  static thread_local int cached_dev = -1;
+  static thread_local int cached[2];                         // parts 2 and 4
+  const int dev = current_device();
+  if (dev < 0) return 0;
+  if (dev != cached_dev) {                                   // looked up once per device and thread
+    auto kern = prompt_kernel<kBF16, D, true>;
+    for (int i = 0; i < 2; ++i) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(2 << i);
+      cfg.blockDim = dim3(kThreads);
+      cfg.dynamicSmemBytes = Cfg<D>::kSmem;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = 2 << i;
+      attr[0].val.clusterDim.y = 1;
+      attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem) != cudaSuccess ||
+          cudaOccupancyMaxActiveClusters(&cached[i], kern, &cfg) != cudaSuccess)
+        return 0;
+    }
+    cached_dev = dev;
+  }
+  return cached[parts == 2 ? 0 : 1];
+}
+
+// One item walks its keys alone unless there are so few items that clusters of 2 or 4 CTAs for each still
+// run at once and every part has two key tiles or more (by the sequences' mean length).  A chunk of 512
+// rows after 3584 keys (56 items): 49.5 us alone, 35.8 us in clusters of 2; one row of 32 heads over 4096
+// keys (16 items): 48.1 us alone, 21.7 us in clusters of 4.
 template <bool kBF16, int D>
 pkv_status launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PromptParams& prm,
                   int num_seqs, int max_q_len, cudaStream_t stream) {
   using C = Cfg<D>;
-  auto kern = prompt_kernel<kBF16, D>;
+  const unsigned groups = (unsigned((max_q_len - 1) / kTile + 1) * unsigned(prm.num_heads / prm.num_kv_heads) + 1) / 2;
+  const int64_t items = int64_t(groups) * num_seqs * prm.num_kv_heads;
+  const int64_t mean_tiles = (int64_t(prm.total_k) / num_seqs + kTile - 1) / kTile;
+  int parts = 1;
+  while (parts < 4 && mean_tiles >= 4 * parts && items <= clusters_at_once<kBF16, D>(2 * parts)) parts *= 2;
+  auto kern = parts > 1 ? prompt_kernel<kBF16, D, true> : prompt_kernel<kBF16, D, false>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
     return PKV_ERR_CUDA;
-  const unsigned groups = (unsigned((max_q_len - 1) / kTile + 1) * unsigned(prm.num_heads / prm.num_kv_heads) + 1) / 2;
-  const dim3 grid(prm.num_kv_heads, num_seqs, groups);
-  return launch_pdl(kern, grid, dim3(kThreads), C::kSmem, stream, tq, tk, tv, prm) == cudaSuccess ? PKV_OK
-                                                                                                  : PKV_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(prm.num_kv_heads) * parts, num_seqs, groups);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = unsigned(parts);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, tq, tk, tv, prm) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
 }  // namespace

@@ -82,6 +82,24 @@ def test_chunks_after_a_history(q_lens, k_lens, dim):
     _run(q_lens, k_lens, 3, 3, dim, "f16")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("q_lens,k_lens,hq,hkv", [([1], [2100], 8, 1), ([1], [700], 4, 4), ([130], [1500], 3, 1),
+                                                  ([5, 0, 40], [2300, 2500, 1], 4, 2), ([300], [1900], 2, 2),
+                                                  ([2, 150], [2600, 1300], 1, 1)])
+def test_few_rows_over_many_keys(q_lens, k_lens, hq, hkv, dim, dtype):
+    """Few enough items that clusters of 2, 4 or 8 CTAs share the keys of each."""
+    _run(q_lens, k_lens, hq, hkv, dim, dtype, pad=5)
+
+
+def test_split_keys_with_a_block_that_has_none():
+    # 200 rows over 2100 keys and 2 rows over none: some parts and some blocks are empty
+    out = _run([200, 2], [4100, 0], 1, 1, 128, "bf16")
+    assert (out[200:] == 0).all()
+    out = _run([2400], [2100], 1, 1, 64, "f16")                # the first 300 rows see nothing
+    assert (out[:300] == 0).all()
+
+
 @pytest.mark.parametrize("dim", [64, 128])
 def test_rows_without_keys_are_zero(dim):
     out = _run([10, 300, 4], [3, 40, 0], 2, 1, dim, "bf16")
