@@ -6,6 +6,8 @@
 // Sources: "PagedAttention: manage the KV cache like virtual memory" §3.3 (each new token
 // fills its sequence's last block); "Lecture 33 — KV Cache management" §2.2 (slot =
 // block * block_size + offset) and §2.4 (copy-on-write copies the shared block).
+#include <algorithm>
+
 #include "pkv_device.cuh"
 #include "pkv_host.h"
 
@@ -94,39 +96,47 @@ __global__ void __launch_bounds__(kThreads) kv_write_quant_kernel(
   }
 }
 
-// f16/bf16 rows into a 4-bit cache; 16 elements (one scale) of K and of V per thread.
+// f16/bf16 rows into a 4-bit cache; 16 elements (one scale) of K and of V per thread.  A CTA takes
+// `tokens` tokens, whose places in the pool one thread each works out; the rest is 32-bit arithmetic.
 template <bool kBF16>
 __global__ void __launch_bounds__(kThreads) kv_write_fp4_kernel(
     const uint4* __restrict__ k_new, const uint4* __restrict__ v_new, const int64_t* __restrict__ slots,
     uint8_t* __restrict__ k_cache, uint8_t* __restrict__ v_cache, const float* __restrict__ k_scale,
-    const float* __restrict__ v_scale, int num_tokens, int num_kv_heads, int groups, int block_size,
+    const float* __restrict__ v_scale, int num_tokens, int num_kv_heads, int groups, int block_size, int tokens,
     int64_t num_slots, unsigned* err) {
+  __shared__ int64_t place[kThreads];                              // tile of kv head 0 * 16 + row; -1: skip
   griddep_launch_dependents();
   griddep_wait();
-  const int64_t total = int64_t(num_tokens) * num_kv_heads * groups;
-  for (int64_t i = blockIdx.x * int64_t(blockDim.x) + threadIdx.x; i < total; i += int64_t(gridDim.x) * blockDim.x) {
-    const int c = int(i % groups);
-    const int64_t r = i / groups;
-    const int h = int(r % num_kv_heads);
-    const int64_t t = r / num_kv_heads;
-    const int64_t slot = slots[t];
-    if (slot < 0) continue;
+  const int t0 = blockIdx.x * tokens, n = min(tokens, num_tokens - t0);
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    const int64_t slot = slots[t0 + i];
+    int64_t at = -1;                                               // slot < 0: padding token
     if (slot >= num_slots) {
-      if (c == 0 && h == 0) set_error(err, PKV_DEVERR_SLOT);
-      continue;
+      set_error(err, PKV_DEVERR_SLOT);
+    } else if (slot >= 0) {
+      const int64_t blk = slot / block_size;
+      at = blk * num_kv_heads * block_size + (slot - blk * block_size);
     }
-    const int64_t blk = slot / block_size, off = slot % block_size;
-    const int64_t tile = ((blk * num_kv_heads + h) * block_size + off) / 16;
-    const int row = int(off % 16);
-    const int64_t base = tile * 144 * groups;                      // 9 * head_dim bytes per tile
-    const int64_t at = base + (row * groups + c) * 8, sat = base + 128 * groups + row * groups + c;
+    place[i] = at;
+  }
+  __syncthreads();
+  const int per_token = num_kv_heads * groups;
+  for (int i = threadIdx.x; i < n * per_token; i += blockDim.x) {
+    const int r = i / per_token, c = i - r * per_token, h = c / groups, g = c - h * groups;
+    const int64_t at0 = place[r];
+    if (at0 < 0) continue;
+    const int64_t row = at0 + int64_t(h) * block_size;
+    const int64_t base = (row >> 4) * 144 * groups;                // 9 * head_dim bytes per tile
+    const int rr = int(row & 15);
+    const int64_t at = base + (rr * groups + g) * 8, sat = base + 128 * groups + rr * groups + g;
+    const int64_t src = 2 * ((int64_t(t0) + r) * per_token + c);
+    const uint4 k0 = __ldg(k_new + src), k1 = __ldg(k_new + src + 1);
+    const uint4 v0 = __ldg(v_new + src), v1 = __ldg(v_new + src + 1);
     uint32_t sc;
-    const uint2 kc = quant16_e2m1<kBF16>(__ldg(k_new + 2 * i), __ldg(k_new + 2 * i + 1), k_scale ? k_scale[h] : 1.f,
-                                         k_scale != nullptr, sc);
+    const uint2 kc = quant16_e2m1<kBF16>(k0, k1, k_scale ? k_scale[h] : 1.f, k_scale != nullptr, sc);
     *reinterpret_cast<uint2*>(k_cache + at) = kc;
     k_cache[sat] = uint8_t(sc);
-    const uint2 vc = quant16_e2m1<kBF16>(__ldg(v_new + 2 * i), __ldg(v_new + 2 * i + 1), v_scale ? v_scale[h] : 1.f,
-                                         v_scale != nullptr, sc);
+    const uint2 vc = quant16_e2m1<kBF16>(v0, v1, v_scale ? v_scale[h] : 1.f, v_scale != nullptr, sc);
     *reinterpret_cast<uint2*>(v_cache + at) = vc;
     v_cache[sat] = uint8_t(sc);
   }
@@ -155,56 +165,43 @@ struct ReadParams {
 };
 
 constexpr int kReadRows = 32;    // output rows per CTA
+constexpr int kReadAhead = 2;    // 16-byte chunks of K and of V in flight per thread
 
-// Sixteen output elements from their stored bytes.
+// Eight output elements (16 bytes; elements 8 c .. of a row) from their stored bytes.  Eight and not
+// sixteen, so that a warp's stores are runs of whole sectors.
 template <pkv_dtype KV, bool kBF16>
-__device__ __forceinline__ void read16(const ReadParams& p, const uint8_t* cache, uint8_t* out, const float* scales,
-                                       int64_t row, int h, int g, int64_t orow) {
-  const int D = p.head_dim;
-  uint4* dst = reinterpret_cast<uint4*>(out + ((orow * p.num_kv_heads + h) * D + 16 * g) * 2);
+__device__ __forceinline__ uint4 read8(const uint8_t* cache, float head_scale, int D, int64_t row, int c) {
   if constexpr (KV == PKV_F16 || KV == PKV_BF16) {
-    const uint4* src = reinterpret_cast<const uint4*>(cache + (row * D + 16 * g) * 2);
-    const uint4 a = __ldg(src), b = __ldg(src + 1);
-    dst[0] = a;
-    dst[1] = b;
+    return __ldg(reinterpret_cast<const uint4*>(cache + (row * D + 8 * c) * 2));
   } else {
-    const float hs = scales ? __ldg(scales + h) : 1.f;
-    uint32_t half[8];                                      // 16 fp16 values, exact
+    uint32_t half[4];                                      // fp16 pairs, exact
     if constexpr (KV == PKV_FP8_E4M3) {
-      const uint4 c = __ldg(reinterpret_cast<const uint4*>(cache + row * D + 16 * g));
-      const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        half[2 * k] = e4m3x2_to_f16x2(w[k]);
-        half[2 * k + 1] = e4m3x2_to_f16x2(w[k] >> 16);
-      }
+      const uint2 w = __ldg(reinterpret_cast<const uint2*>(cache + row * D + 8 * c));
+      half[0] = e4m3x2_to_f16x2(w.x);
+      half[1] = e4m3x2_to_f16x2(w.x >> 16);
+      half[2] = e4m3x2_to_f16x2(w.y);
+      half[3] = e4m3x2_to_f16x2(w.y >> 16);
     } else {
       const uint8_t* tile = cache + (row >> 4) * 9 * D;
       const int rr = int(row & 15);
-      const uint2 c = __ldg(reinterpret_cast<const uint2*>(tile + rr * (D / 2) + 8 * g));
-      const uint32_t s2 = e4m3x2_to_f16x2(uint32_t(__ldg(tile + 8 * D + rr * (D / 16) + g)) * 0x101u);
-      uint32_t x[4], y[4];
-      e2m1x8_to_f16x8(c.x, x);
-      e2m1x8_to_f16x8(c.y, y);
+      const uint32_t codes = __ldg(reinterpret_cast<const uint32_t*>(tile + rr * (D / 2) + 4 * c));
+      const uint32_t s2 = e4m3x2_to_f16x2(uint32_t(__ldg(tile + 8 * D + rr * (D / 16) + (c >> 1))) * 0x101u);
+      e2m1x8_to_f16x8(codes, half);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        half[k] = hmul2(x[k], s2);
-        half[4 + k] = hmul2(y[k], s2);
-      }
+      for (int k = 0; k < 4; ++k) half[k] = hmul2(half[k], s2);
     }
-    uint32_t o[8];
+    uint32_t o[4];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < 4; ++k) {
       const float2 f = unpack2<false>(half[k]);
-      o[k] = pack2<kBF16>(f.x * hs, f.y * hs);
+      o[k] = pack2<kBF16>(f.x * head_scale, f.y * head_scale);
     }
-    dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-    dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    return make_uint4(o[0], o[1], o[2], o[3]);
   }
 }
 
 // A CTA takes kReadRows output rows: one thread per row finds its sequence and pool row, then all
-// threads move 16 elements each, group fastest, so that stores are runs of whole rows.
+// threads move 8 elements each of K and of V, kReadAhead of them on their way at once.
 template <pkv_dtype KV, bool kBF16>
 __global__ void __launch_bounds__(kThreads) kv_read_kernel(const ReadParams p) {
   __shared__ int64_t src_row[kReadRows];                   // row of kv head 0 in the pool, -1: leave the row
@@ -238,13 +235,29 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const ReadParams p) {
     src_row[threadIdx.x] = row;
   }
   __syncthreads();
-  const int groups = p.head_dim / 16, per_row = p.num_kv_heads * groups;
-  for (int i = threadIdx.x; i < kReadRows * per_row; i += blockDim.x) {
-    const int r = i / per_row, c = i - r * per_row, h = c / groups, g = c - h * groups;
-    if (src_row[r] < 0) continue;
-    const int64_t row = src_row[r] + int64_t(h) * p.block_size;
-    read16<KV, kBF16>(p, p.k_cache, p.k_out, p.k_scale, row, h, g, t0 + r);
-    read16<KV, kBF16>(p, p.v_cache, p.v_out, p.v_scale, row, h, g, t0 + r);
+  const int D = p.head_dim, chunks = D / 8, per_row = p.num_kv_heads * chunks, total = kReadRows * per_row;
+  for (int i0 = threadIdx.x; i0 < total; i0 += kReadAhead * blockDim.x) {
+    uint4 kv[kReadAhead], vv[kReadAhead];
+    int64_t to[kReadAhead];
+#pragma unroll
+    for (int u = 0; u < kReadAhead; ++u) {
+      const int i = i0 + u * blockDim.x;
+      to[u] = -1;
+      if (i >= total) continue;
+      const int r = i / per_row, c = i - r * per_row, h = c / chunks;
+      if (src_row[r] < 0) continue;
+      const int64_t row = src_row[r] + int64_t(h) * p.block_size;
+      const float ks = p.k_scale ? __ldg(p.k_scale + h) : 1.f, vs = p.v_scale ? __ldg(p.v_scale + h) : 1.f;
+      kv[u] = read8<KV, kBF16>(p.k_cache, ks, D, row, c - h * chunks);
+      vv[u] = read8<KV, kBF16>(p.v_cache, vs, D, row, c - h * chunks);
+      to[u] = (int64_t(t0) + r) * per_row + c;
+    }
+#pragma unroll
+    for (int u = 0; u < kReadAhead; ++u) {
+      if (to[u] < 0) continue;
+      reinterpret_cast<uint4*>(p.k_out)[to[u]] = kv[u];
+      reinterpret_cast<uint4*>(p.v_out)[to[u]] = vv[u];
+    }
   }
 }
 
@@ -363,12 +376,14 @@ pkv_status pkv_kv_write(const void* k_new, const void* v_new, pkv_dtype in_dtype
       return PKV_ERR_CUDA;
   } else if (cache->kv_dtype == PKV_FP4_E2M1 && (in_dtype == PKV_F16 || in_dtype == PKV_BF16)) {
     const int groups = cache->head_dim / 16;
-    const int64_t work = int64_t(num_tokens) * cache->num_kv_heads * groups;
+    if (int64_t(cache->num_kv_heads) * groups >= (int64_t(1) << 22)) return PKV_ERR_UNSUPPORTED;
+    // One thread per 16 elements of K and V, at least a token per CTA.
+    const int tokens = std::max(1, kThreads / (cache->num_kv_heads * groups));
     auto kern = in_dtype == PKV_BF16 ? kv_write_fp4_kernel<true> : kv_write_fp4_kernel<false>;
-    if (launch_pdl(kern, dim3(grid_for(work)), dim3(kThreads), 0, s, static_cast<const uint4*>(k_new),
+    if (launch_pdl(kern, dim3((num_tokens - 1) / tokens + 1), dim3(kThreads), 0, s, static_cast<const uint4*>(k_new),
                    static_cast<const uint4*>(v_new), slot_mapping, static_cast<uint8_t*>(k_cache),
                    static_cast<uint8_t*>(v_cache), cache->k_scale, cache->v_scale, num_tokens, cache->num_kv_heads,
-                   groups, cache->block_size, num_slots, err) != cudaSuccess)
+                   groups, cache->block_size, tokens, num_slots, err) != cudaSuccess)
       return PKV_ERR_CUDA;
   } else {
     return PKV_ERR_UNSUPPORTED;
@@ -393,7 +408,7 @@ pkv_status pkv_kv_read(void* k_out, void* v_out, pkv_dtype out_dtype, int total_
   if (!aligned16(k_out) || !aligned16(v_out) || !aligned16(k_cache) || !aligned16(v_cache) ||
       (reinterpret_cast<uintptr_t>(cu_lens) & 3u) || (reinterpret_cast<uintptr_t>(block_tables) & 3u))
     return PKV_ERR_INVALID_ARG;
-  if (int64_t(cache->num_kv_heads) * cache->head_dim * kReadRows / 16 >= (int64_t(1) << 31))
+  if (int64_t(cache->num_kv_heads) * cache->head_dim >= (int64_t(1) << 24))
     return PKV_ERR_UNSUPPORTED;              // the rows of one CTA are indexed in 32 bits
   unsigned* err = error_word_ptr();
   if (!err) return PKV_ERR_CUDA;

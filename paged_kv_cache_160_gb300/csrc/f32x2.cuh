@@ -3,6 +3,8 @@
 
 #include <stdint.h>
 
+#include <cuda_runtime.h>
+
 namespace pkv {
 
 // Two fp32 values in one 64-bit register pair, for the packed fp32 instructions.
@@ -16,6 +18,11 @@ __device__ __forceinline__ float hi_f32(uint64_t v) { return __uint_as_float(uin
 __device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t d;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
 __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {

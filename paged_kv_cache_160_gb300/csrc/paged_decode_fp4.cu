@@ -27,7 +27,6 @@
 #include <type_traits>
 
 #include "decode_split.cuh"
-#include "f32x2.cuh"
 
 namespace pkv {
 namespace {

@@ -7,7 +7,6 @@
 // GB300 design: a CTA holds two row blocks of 128 query rows that read the same keys, so every K/V
 // tile feeds 256 rows.  S = Q K^T and O += P V run on tcgen05 with S, P and O in tensor memory; Q, K
 // and V arrive by TMA straight from the packed rows (any row stride).
-#include "f32x2.cuh"
 #include "pkv_device.cuh"
 #include "pkv_host.h"
 

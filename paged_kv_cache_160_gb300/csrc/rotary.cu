@@ -9,8 +9,8 @@
 //
 // Bound by HBM: 2 * (Hq + Hkv) * D * 2 bytes per token are moved, a few operations per element.  A
 // CTA takes one token, so that its rot / 2 angles are computed once for all heads: each thread holds
-// the sines and cosines of its 8 elements in registers while it walks the heads, and its first rows
-// are on their way while it computes them.
+// the sines and cosines of its 8 elements in registers while it walks the heads.  Its rows are on their
+// way, kBatch at a time, while it waits for the position and computes the angles.
 #include <math.h>
 
 #include "pkv_device.cuh"
@@ -21,6 +21,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxDim = 256;
+constexpr int kBatch = 4;                // rows in flight per thread
 
 struct RotaryParams {
   uint8_t* q_out;
@@ -58,8 +59,6 @@ __global__ void __launch_bounds__(kThreads) qk_rotary_kernel(const RotaryParams 
   griddep_launch_dependents();
   griddep_wait();
   const int64_t t = blockIdx.x;
-  const int position = p.positions[t];
-  if (position < 0) return;                                 // padding token
   constexpr int kRowsAtOnce = kThreads / kLanes;
   const int sub = threadIdx.x % kLanes, e0 = 8 * sub;
   const bool live = e0 < p.head_dim;
@@ -71,9 +70,18 @@ __global__ void __launch_bounds__(kThreads) qk_rotary_kernel(const RotaryParams 
                             : t * p.q_stride + int64_t(r) * p.head_dim;
     return reinterpret_cast<const uint4*>((isk ? p.k : p.q) + 2 * (off + e0));
   };
-  int r = threadIdx.x / kLanes;
-  const uint4 none = make_uint4(0u, 0u, 0u, 0u);
-  uint4 next = live && r < rows ? *src(r) : none;
+  int r0 = threadIdx.x / kLanes;                            // the batch's first row
+  uint4 batch[kBatch];
+  auto load_batch = [&]() {
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int r = r0 + b * kRowsAtOnce;
+      batch[b] = live && r < rows ? *src(r) : make_uint4(0u, 0u, 0u, 0u);
+    }
+  };
+  load_batch();
+  const int position = p.positions[t];
+  if (position < 0) return;                                 // padding token
 
   if (threadIdx.x < half) {
     const uint64_t phase = uint64_t(int64_t(position)) * p.table[threadIdx.x];
@@ -100,25 +108,24 @@ __global__ void __launch_bounds__(kThreads) qk_rotary_kernel(const RotaryParams 
 
   // Every thread of a warp walks the same number of rows: the norm and the partner's elements come
   // by shuffles.
-  const int steps = (rows + kRowsAtOnce - 1) / kRowsAtOnce;
-  for (int s = 0; s < steps; ++s, r += kRowsAtOnce) {
+  auto rotate = [&](int r, const uint4 in) {
     float x[8];
-    unpack8<kBF16>(next, x);
-    next = live && r + kRowsAtOnce < rows ? *src(r + kRowsAtOnce) : none;
+    unpack8<kBF16>(in, x);
     const bool isk = r >= p.num_heads;
     const void* wp = isk ? p.k_weight : p.q_weight;
-    // Uniform over the call unless only one of the weights is given; the shuffles stay outside.
-    float ss = 0.f;
+    if (p.q_weight || p.k_weight) {                         // uniform: the shuffles need the whole warp
+      float ss = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss += x[i] * x[i];
+      for (int i = 0; i < 8; ++i) ss += x[i] * x[i];
 #pragma unroll
-    for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if (wp && live) {
-      const float inv = rsqrtf(ss / float(p.head_dim) + p.eps);
-      float w[8];
-      unpack8<kBF16>(__ldg(reinterpret_cast<const uint4*>(wp) + sub), w);
+      for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      if (wp && live) {
+        const float inv = rsqrtf(ss / float(p.head_dim) + p.eps);
+        float w[8];
+        unpack8<kBF16>(__ldg(reinterpret_cast<const uint4*>(wp) + sub), w);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = x[i] * inv * w[i];
+        for (int i = 0; i < 8; ++i) x[i] = x[i] * inv * w[i];
+      }
     }
     float y[8];
 #pragma unroll
@@ -132,6 +139,15 @@ __global__ void __launch_bounds__(kThreads) qk_rotary_kernel(const RotaryParams 
       *reinterpret_cast<uint4*>((isk ? p.k_out : p.q_out) + 2 * (off + e0)) =
           make_uint4(pack2<kBF16>(y[0], y[1]), pack2<kBF16>(y[2], y[3]), pack2<kBF16>(y[4], y[5]),
                      pack2<kBF16>(y[6], y[7]));
+    }
+  };
+  const int last = (rows - 1) / kRowsAtOnce * kRowsAtOnce;  // first row of the last step
+  for (int s = 0; s <= last; s += kBatch * kRowsAtOnce, r0 += kBatch * kRowsAtOnce) {
+    if (s > 0) load_batch();
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      if (s + b * kRowsAtOnce > last) break;                // uniform over the CTA
+      rotate(r0 + b * kRowsAtOnce, batch[b]);
     }
   }
 }

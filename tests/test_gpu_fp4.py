@@ -101,6 +101,54 @@ def test_written_bytes_are_the_definitions(dtype, dim, heads, block, scaled):
         assert np.array_equal(gc[~hole], codes[~hole])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("head_scale", [None, 1.0, 0.3, -1.7, 1e-3, 3e4])
+def test_elements_on_and_next_to_the_borders_between_codes(head_scale, dtype):
+    """Every scale of the format; elements on each border times the scale, and their neighbours in the type."""
+    import paged_kv_cache_160_gb300 as pkv
+    dt = DT[dtype]
+    hs = 1.0 if head_scale is None else np.float64(np.float32(head_scale))
+    s = e4m3_table()[1:0x7F]
+    s = s[(6 * s * abs(hs) < 6e4) & (s * abs(hs) > 1e-3)]      # well inside fp16
+    borders = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0])
+    x = torch.zeros((len(s), 32), dtype=dt)
+    x[:, 0] = x[:, 16] = torch.from_numpy(6 * s * hs).to(dt)
+    mid = torch.from_numpy(s[:, None] * borders * hs).to(dt)
+    step = torch.finfo(dt).eps * mid.float().abs()
+    x[:, 1:8], x[:, 8:15], x[:, 17:24], x[:, 24:31] = mid, -(mid.float() + step).to(dt), (mid.float() - step).to(dt), -mid
+    n = len(s)
+    k = torch.zeros(pkv.fp4_cache_shape(-(-n // 16), 1, 16, 32), dtype=torch.uint8, device="cuda")
+    v = torch.zeros_like(k)
+    scale = None if head_scale is None else torch.tensor([head_scale], dtype=torch.float32, device="cuda")
+    xx = x.view(n, 1, 32)
+    pkv.pkv_kv_write(xx.cuda(), xx.flip(0).contiguous().cuda(), torch.arange(n, device="cuda"), k, v,
+                     pkv.cache_desc_fp4(k, scale, scale))
+    for got, src in ((k, xx), (v, xx.flip(0))):
+        gc, gs = fp4.unpack(got.cpu().numpy())
+        wc, ws = fp4.quantise(src.double().numpy(), None if head_scale is None else [head_scale])
+        at = np.arange(n)
+        assert np.array_equal(gs[at // 16, :, at % 16], ws) and np.array_equal(gc[at // 16, :, at % 16], wc)
+
+
+@pytest.mark.parametrize("head_scale", [0.0, float("inf"), float("nan"), 1e-38, 1e38, -3e-31])
+def test_odd_head_scales(head_scale):
+    import paged_kv_cache_160_gb300 as pkv
+    g = torch.Generator().manual_seed(3)
+    x = torch.randn((16, 1, 64), generator=g).to(torch.bfloat16)
+    x[3, 0, 5] = float("inf")
+    x[4, 0, :20] = 0.0
+    x[5] *= 1e-30
+    x[6] *= 1e30
+    k = torch.zeros(pkv.fp4_cache_shape(1, 1, 16, 64), dtype=torch.uint8, device="cuda")
+    scale = torch.tensor([head_scale], dtype=torch.float32, device="cuda")
+    pkv.pkv_kv_write(x.cuda(), x.cuda(), torch.arange(16, device="cuda"), k, k.clone(), pkv.cache_desc_fp4(k, scale, scale))
+    gc, gs = fp4.unpack(k.cpu().numpy())
+    wc, ws = fp4.quantise(x.double().numpy(), [head_scale])
+    assert np.array_equal(gs[0].transpose(1, 0, 2), ws)
+    live = np.repeat(ws != 0x7F, 16, -1)
+    assert np.array_equal(gc[0].transpose(1, 0, 2)[live], wc[live])
+
+
 def test_many_tokens_and_a_bad_slot():
     import paged_kv_cache_160_gb300 as pkv
     rng = np.random.default_rng(1)
