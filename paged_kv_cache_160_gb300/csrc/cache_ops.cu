@@ -96,50 +96,41 @@ __global__ void __launch_bounds__(kThreads) kv_write_quant_kernel(
   }
 }
 
-// f16/bf16 rows into a 4-bit cache; 16 elements (one scale) of K and of V per thread.  A CTA takes
-// `tokens` tokens, whose places in the pool one thread each works out; the rest is 32-bit arithmetic.
+// f16/bf16 rows into a 4-bit cache; 16 elements (one scale) of K and of V per thread, whose loads are on
+// their way before the token's slot is looked up.
 template <bool kBF16>
 __global__ void __launch_bounds__(kThreads) kv_write_fp4_kernel(
     const uint4* __restrict__ k_new, const uint4* __restrict__ v_new, const int64_t* __restrict__ slots,
     uint8_t* __restrict__ k_cache, uint8_t* __restrict__ v_cache, const float* __restrict__ k_scale,
-    const float* __restrict__ v_scale, int num_tokens, int num_kv_heads, int groups, int block_size, int tokens,
-    int64_t num_slots, unsigned* err) {
-  __shared__ int64_t place[kThreads];                              // tile of kv head 0 * 16 + row; -1: skip
+    const float* __restrict__ v_scale, int64_t total, int num_kv_heads, int groups, int block_size, int64_t num_slots,
+    unsigned* err) {
   griddep_launch_dependents();
   griddep_wait();
-  const int t0 = blockIdx.x * tokens, n = min(tokens, num_tokens - t0);
-  for (int i = threadIdx.x; i < n; i += blockDim.x) {
-    const int64_t slot = slots[t0 + i];
-    int64_t at = -1;                                               // slot < 0: padding token
-    if (slot >= num_slots) {
-      set_error(err, PKV_DEVERR_SLOT);
-    } else if (slot >= 0) {
-      const int64_t blk = slot / block_size;
-      at = blk * num_kv_heads * block_size + (slot - blk * block_size);
-    }
-    place[i] = at;
-  }
-  __syncthreads();
+  const int64_t i = blockIdx.x * int64_t(kThreads) + threadIdx.x;
+  if (i >= total) return;
+  const uint4 k0 = __ldg(k_new + 2 * i), k1 = __ldg(k_new + 2 * i + 1);
+  const uint4 v0 = __ldg(v_new + 2 * i), v1 = __ldg(v_new + 2 * i + 1);
   const int per_token = num_kv_heads * groups;
-  for (int i = threadIdx.x; i < n * per_token; i += blockDim.x) {
-    const int r = i / per_token, c = i - r * per_token, h = c / groups, g = c - h * groups;
-    const int64_t at0 = place[r];
-    if (at0 < 0) continue;
-    const int64_t row = at0 + int64_t(h) * block_size;
-    const int64_t base = (row >> 4) * 144 * groups;                // 9 * head_dim bytes per tile
-    const int rr = int(row & 15);
-    const int64_t at = base + (rr * groups + g) * 8, sat = base + 128 * groups + rr * groups + g;
-    const int64_t src = 2 * ((int64_t(t0) + r) * per_token + c);
-    const uint4 k0 = __ldg(k_new + src), k1 = __ldg(k_new + src + 1);
-    const uint4 v0 = __ldg(v_new + src), v1 = __ldg(v_new + src + 1);
-    uint32_t sc;
-    const uint2 kc = quant16_e2m1<kBF16>(k0, k1, k_scale ? k_scale[h] : 1.f, k_scale != nullptr, sc);
-    *reinterpret_cast<uint2*>(k_cache + at) = kc;
-    k_cache[sat] = uint8_t(sc);
-    const uint2 vc = quant16_e2m1<kBF16>(v0, v1, v_scale ? v_scale[h] : 1.f, v_scale != nullptr, sc);
-    *reinterpret_cast<uint2*>(v_cache + at) = vc;
-    v_cache[sat] = uint8_t(sc);
+  const int64_t t = total <= 0x7fffffff ? int64_t(unsigned(i) / unsigned(per_token)) : i / per_token;
+  const int c = int(i - t * per_token), h = c / groups, g = c - h * groups;
+  const int64_t slot = slots[t];
+  if (slot < 0) return;                                            // padding token
+  if (slot >= num_slots) {
+    if (c == 0) set_error(err, PKV_DEVERR_SLOT);
+    return;
   }
+  const int64_t blk = num_slots <= 0x7fffffff ? int64_t(unsigned(slot) / unsigned(block_size)) : slot / block_size;
+  const int64_t row = (blk * num_kv_heads + h) * block_size + (slot - blk * block_size);
+  const int64_t base = (row >> 4) * 144 * groups;                  // 9 * head_dim bytes per tile
+  const int rr = int(row & 15);
+  const int64_t at = base + (rr * groups + g) * 8, sat = base + 128 * groups + rr * groups + g;
+  uint32_t sc;
+  const uint2 kc = quant16_e2m1<kBF16>(k0, k1, HeadScale(k_scale, h), sc);
+  *reinterpret_cast<uint2*>(k_cache + at) = kc;
+  k_cache[sat] = uint8_t(sc);
+  const uint2 vc = quant16_e2m1<kBF16>(v0, v1, HeadScale(v_scale, h), sc);
+  *reinterpret_cast<uint2*>(v_cache + at) = vc;
+  v_cache[sat] = uint8_t(sc);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -165,66 +156,94 @@ struct ReadParams {
 };
 
 constexpr int kReadRows = 32;    // output rows per CTA
-constexpr int kReadAhead = 2;    // 16-byte chunks of K and of V in flight per thread
 
-// Eight output elements (16 bytes; elements 8 c .. of a row) from their stored bytes.  Eight and not
-// sixteen, so that a warp's stores are runs of whole sectors.
-template <pkv_dtype KV, bool kBF16>
-__device__ __forceinline__ uint4 read8(const uint8_t* cache, float head_scale, int D, int64_t row, int c) {
-  if constexpr (KV == PKV_F16 || KV == PKV_BF16) {
-    return __ldg(reinterpret_cast<const uint4*>(cache + (row * D + 8 * c) * 2));
-  } else {
-    uint32_t half[4];                                      // fp16 pairs, exact
-    if constexpr (KV == PKV_FP8_E4M3) {
-      const uint2 w = __ldg(reinterpret_cast<const uint2*>(cache + row * D + 8 * c));
-      half[0] = e4m3x2_to_f16x2(w.x);
-      half[1] = e4m3x2_to_f16x2(w.x >> 16);
-      half[2] = e4m3x2_to_f16x2(w.y);
-      half[3] = e4m3x2_to_f16x2(w.y >> 16);
-    } else {
+// Eight elements (8 c .. of a row) as stored, and as 16 output bytes.  Eight and not more, so that a
+// warp's stores are runs of whole sectors.
+template <pkv_dtype KV>
+struct Stored8 {
+  static constexpr int kWords = KV == PKV_FP4_E2M1 ? 1 : KV == PKV_FP8_E4M3 ? 2 : 4;
+  uint32_t w[kWords];
+  uint32_t scale;         // 4-bit: the e4m3 code
+
+  __device__ __forceinline__ void load(const uint8_t* cache, int D, int64_t row, int c) {
+    if constexpr (KV == PKV_FP4_E2M1) {
       const uint8_t* tile = cache + (row >> 4) * 9 * D;
       const int rr = int(row & 15);
-      const uint32_t codes = __ldg(reinterpret_cast<const uint32_t*>(tile + rr * (D / 2) + 4 * c));
-      const uint32_t s2 = e4m3x2_to_f16x2(uint32_t(__ldg(tile + 8 * D + rr * (D / 16) + (c >> 1))) * 0x101u);
-      e2m1x8_to_f16x8(codes, half);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) half[k] = hmul2(half[k], s2);
+      w[0] = __ldg(reinterpret_cast<const uint32_t*>(tile + rr * (D / 2) + 4 * c));
+      scale = __ldg(tile + 8 * D + rr * (D / 16) + (c >> 1));
+    } else if constexpr (KV == PKV_FP8_E4M3) {
+      const uint2 v = __ldg(reinterpret_cast<const uint2*>(cache + row * D + 8 * c));
+      w[0] = v.x;
+      w[1] = v.y;
+    } else {
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(cache + (row * D + 8 * c) * 2));
+      w[0] = v.x;
+      w[1] = v.y;
+      w[2] = v.z;
+      w[3] = v.w;
     }
-    uint32_t o[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float2 f = unpack2<false>(half[k]);
-      o[k] = pack2<kBF16>(f.x * head_scale, f.y * head_scale);
-    }
-    return make_uint4(o[0], o[1], o[2], o[3]);
   }
-}
+  template <bool kBF16>
+  __device__ __forceinline__ uint4 value(float head_scale) const {
+    if constexpr (KV == PKV_F16 || KV == PKV_BF16) {
+      return make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+      uint32_t half[4];                                    // fp16 pairs, exact
+      if constexpr (KV == PKV_FP8_E4M3) {
+        half[0] = e4m3x2_to_f16x2(w[0]);
+        half[1] = e4m3x2_to_f16x2(w[0] >> 16);
+        half[2] = e4m3x2_to_f16x2(w[1]);
+        half[3] = e4m3x2_to_f16x2(w[1] >> 16);
+      } else {
+        const uint32_t s2 = e4m3x2_to_f16x2(scale * 0x101u);
+        e2m1x8_to_f16x8(w[0], half);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) half[k] = hmul2(half[k], s2);
+      }
+      uint32_t o[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 f = unpack2<false>(half[k]);
+        o[k] = pack2<kBF16>(f.x * head_scale, f.y * head_scale);
+      }
+      return make_uint4(o[0], o[1], o[2], o[3]);
+    }
+  }
+};
 
-// A CTA takes kReadRows output rows: one thread per row finds its sequence and pool row, then all
-// threads move 8 elements each of K and of V, kReadAhead of them on their way at once.
+// A CTA takes kReadRows output rows: the first warp finds each one's sequence and pool row, then all
+// threads move 8 elements of K and of V at a time, kAhead of them on their way at once as stored.  The host
+// picks a number of threads that whole rows of all kv heads divide, so that a thread keeps its place in
+// the row.
 template <pkv_dtype KV, bool kBF16>
-__global__ void __launch_bounds__(kThreads) kv_read_kernel(const ReadParams p) {
+__global__ void __launch_bounds__(1024) kv_read_kernel(const ReadParams p) {
   __shared__ int64_t src_row[kReadRows];                   // row of kv head 0 in the pool, -1: leave the row
   griddep_launch_dependents();
   griddep_wait();
-  const int t0 = blockIdx.x * kReadRows;
+  const int t0 = blockIdx.x * kReadRows, S = p.num_seqs;
   if (blockIdx.x == 0) {                                   // cu_lens ascends from 0 to at most total_tokens
-    bool bad = threadIdx.x == 0 && (p.cu_lens[0] != 0 || p.cu_lens[p.num_seqs] > p.total_tokens);
-    for (int i = threadIdx.x; i < p.num_seqs; i += blockDim.x) bad |= p.cu_lens[i + 1] < p.cu_lens[i];
+    bool bad = threadIdx.x == 0 && (p.cu_lens[0] != 0 || p.cu_lens[S] > p.total_tokens);
+    for (int i = threadIdx.x; i < S; i += blockDim.x) bad |= p.cu_lens[i + 1] < p.cu_lens[i];
     if (bad) set_error(p.err, PKV_DEVERR_CHUNK);
   }
-  if (threadIdx.x < kReadRows) {
-    const int t = t0 + threadIdx.x;
+  if (threadIdx.x < 32) {
+    static_assert(kReadRows == 32, "a row per lane");
+    const int lane = threadIdx.x, t = t0 + lane;
+    // The largest i with cu_lens[i] <= t0, 32 probes a round; then each lane walks on to its own row's.
+    int lo = 0, n = S;
+    while (n > 1) {
+      const int step = (n + 31) >> 5, at = lane * step;
+      const unsigned b = __ballot_sync(0xffffffffu, at < n && p.cu_lens[lo + at] <= t0);
+      const int k = b ? 31 - __clz(b) : 0;
+      lo += k * step;
+      n = min(step, n - k * step);
+    }
     int64_t row = -1;
-    const int last = p.cu_lens[p.num_seqs];
-    if (t < p.total_tokens && t < last) {
-      int lo = 0, hi = p.num_seqs;                         // the largest i with cu_lens[i] <= t
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (p.cu_lens[mid] <= t) lo = mid; else hi = mid;
-      }
+    if (t < p.total_tokens && t < p.cu_lens[S]) {
+      int end = p.cu_lens[lo + 1];
+      while (t >= end && lo + 1 < S) end = p.cu_lens[++lo + 1];
       const int j = t - p.cu_lens[lo];
-      if (j < 0 || t >= p.cu_lens[lo + 1] || j / p.block_size >= p.max_blocks) {
+      if (j < 0 || t >= end || j / p.block_size >= p.max_blocks) {
         set_error(p.err, PKV_DEVERR_CHUNK);
       } else {
         const int blk = p.block_tables[int64_t(lo) * p.max_blocks + j / p.block_size];
@@ -232,31 +251,36 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const ReadParams p) {
         else row = int64_t(blk) * p.num_kv_heads * p.block_size + j % p.block_size;
       }
     }
-    src_row[threadIdx.x] = row;
+    src_row[lane] = row;
   }
   __syncthreads();
-  const int D = p.head_dim, chunks = D / 8, per_row = p.num_kv_heads * chunks, total = kReadRows * per_row;
-  for (int i0 = threadIdx.x; i0 < total; i0 += kReadAhead * blockDim.x) {
-    uint4 kv[kReadAhead], vv[kReadAhead];
-    int64_t to[kReadAhead];
+  constexpr int kAhead = KV == PKV_F16 || KV == PKV_BF16 ? 2 : 8;
+  const int D = p.head_dim, chunks = D / 8, per_row = p.num_kv_heads * chunks;
+  const int at_once = max(1, int(blockDim.x) / per_row);   // rows per pass
+  const int r0 = threadIdx.x / per_row;
+  if (r0 >= at_once) return;
+  for (int c = threadIdx.x - r0 * per_row; c < per_row; c += blockDim.x) {   // (once, unless a row is longer than the CTA)
+    const int h = c / chunks, chunk = c - h * chunks;
+    const float ks = p.k_scale ? __ldg(p.k_scale + h) : 1.f, vs = p.v_scale ? __ldg(p.v_scale + h) : 1.f;
+    uint4* ko = reinterpret_cast<uint4*>(p.k_out) + int64_t(t0) * per_row + c;
+    uint4* vo = reinterpret_cast<uint4*>(p.v_out) + int64_t(t0) * per_row + c;
+    for (int r = r0; r < kReadRows; r += kAhead * at_once) {
+      Stored8<KV> k[kAhead], v[kAhead];
 #pragma unroll
-    for (int u = 0; u < kReadAhead; ++u) {
-      const int i = i0 + u * blockDim.x;
-      to[u] = -1;
-      if (i >= total) continue;
-      const int r = i / per_row, c = i - r * per_row, h = c / chunks;
-      if (src_row[r] < 0) continue;
-      const int64_t row = src_row[r] + int64_t(h) * p.block_size;
-      const float ks = p.k_scale ? __ldg(p.k_scale + h) : 1.f, vs = p.v_scale ? __ldg(p.v_scale + h) : 1.f;
-      kv[u] = read8<KV, kBF16>(p.k_cache, ks, D, row, c - h * chunks);
-      vv[u] = read8<KV, kBF16>(p.v_cache, vs, D, row, c - h * chunks);
-      to[u] = (int64_t(t0) + r) * per_row + c;
-    }
+      for (int u = 0; u < kAhead; ++u) {
+        const int ru = r + u * at_once;
+        if (ru >= kReadRows || src_row[ru] < 0) continue;
+        const int64_t row = src_row[ru] + int64_t(h) * p.block_size;
+        k[u].load(p.k_cache, D, row, chunk);
+        v[u].load(p.v_cache, D, row, chunk);
+      }
 #pragma unroll
-    for (int u = 0; u < kReadAhead; ++u) {
-      if (to[u] < 0) continue;
-      reinterpret_cast<uint4*>(p.k_out)[to[u]] = kv[u];
-      reinterpret_cast<uint4*>(p.v_out)[to[u]] = vv[u];
+      for (int u = 0; u < kAhead; ++u) {
+        const int ru = r + u * at_once;
+        if (ru >= kReadRows || src_row[ru] < 0) continue;
+        ko[int64_t(ru) * per_row] = k[u].template value<kBF16>(ks);
+        vo[int64_t(ru) * per_row] = v[u].template value<kBF16>(vs);
+      }
     }
   }
 }
@@ -376,14 +400,13 @@ pkv_status pkv_kv_write(const void* k_new, const void* v_new, pkv_dtype in_dtype
       return PKV_ERR_CUDA;
   } else if (cache->kv_dtype == PKV_FP4_E2M1 && (in_dtype == PKV_F16 || in_dtype == PKV_BF16)) {
     const int groups = cache->head_dim / 16;
-    if (int64_t(cache->num_kv_heads) * groups >= (int64_t(1) << 22)) return PKV_ERR_UNSUPPORTED;
-    // One thread per 16 elements of K and V, at least a token per CTA.
-    const int tokens = std::max(1, kThreads / (cache->num_kv_heads * groups));
+    const int64_t work = int64_t(num_tokens) * cache->num_kv_heads * groups, ctas = (work - 1) / kThreads + 1;
+    if (int64_t(cache->num_kv_heads) * groups >= (int64_t(1) << 24) || ctas > 0x7fffffff) return PKV_ERR_UNSUPPORTED;
     auto kern = in_dtype == PKV_BF16 ? kv_write_fp4_kernel<true> : kv_write_fp4_kernel<false>;
-    if (launch_pdl(kern, dim3((num_tokens - 1) / tokens + 1), dim3(kThreads), 0, s, static_cast<const uint4*>(k_new),
+    if (launch_pdl(kern, dim3(unsigned(ctas)), dim3(kThreads), 0, s, static_cast<const uint4*>(k_new),
                    static_cast<const uint4*>(v_new), slot_mapping, static_cast<uint8_t*>(k_cache),
-                   static_cast<uint8_t*>(v_cache), cache->k_scale, cache->v_scale, num_tokens, cache->num_kv_heads,
-                   groups, cache->block_size, tokens, num_slots, err) != cudaSuccess)
+                   static_cast<uint8_t*>(v_cache), cache->k_scale, cache->v_scale, work, cache->num_kv_heads, groups,
+                   cache->block_size, num_slots, err) != cudaSuccess)
       return PKV_ERR_CUDA;
   } else {
     return PKV_ERR_UNSUPPORTED;
@@ -435,7 +458,10 @@ pkv_status pkv_kv_read(void* k_out, void* v_out, pkv_dtype out_dtype, int total_
                   ? (bf ? kv_read_kernel<PKV_FP8_E4M3, true> : kv_read_kernel<PKV_FP8_E4M3, false>)
                   : (bf ? kv_read_kernel<PKV_FP4_E2M1, true> : kv_read_kernel<PKV_FP4_E2M1, false>);
   const int grid = (total_tokens - 1) / kReadRows + 1;
-  return launch_pdl(kern, dim3(grid), dim3(kThreads), 0, reinterpret_cast<cudaStream_t>(stream), prm) == cudaSuccess
+  // Whole rows of all kv heads, 256 threads or more, in full warps; longer rows are walked.
+  const int per_row = cache->num_kv_heads * (cache->head_dim / 8);
+  const int threads = per_row >= 1024 ? 1024 : std::min(1024, (per_row * std::max(1, kThreads / per_row) + 31) / 32 * 32);
+  return launch_pdl(kern, dim3(grid), dim3(threads), 0, reinterpret_cast<cudaStream_t>(stream), prm) == cudaSuccess
              ? PKV_OK
              : PKV_ERR_CUDA;
 }

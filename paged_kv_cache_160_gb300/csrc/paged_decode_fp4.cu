@@ -393,9 +393,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) paged_decode_fp4_kernel(const 
       if (lane < 2 * C::kGroups) {
         const bool isv = lane >= C::kGroups;
         const int c = lane % C::kGroups, r = (tl.len - 1) & (kBS - 1);
-        const float* hs = isv ? p.v_scale : p.k_scale;
         uint32_t sc;
-        const uint2 v = quant16_e2m1<kQBF16>(na, nb2, hs ? hs[tl.h] : 1.f, hs != nullptr, sc);
+        const uint2 v = quant16_e2m1<kQBF16>(na, nb2, HeadScale(isv ? p.v_scale : p.k_scale, tl.h), sc);
         const int at = r * (D / 2) + 8 * c, sat = 8 * D + r * C::kGroups + c;
         uint8_t* tile = stage + ((k - 1) * 2 + (isv ? 1 : 0)) * C::kTileBytes;
         *reinterpret_cast<uint2*>(tile + at) = v;

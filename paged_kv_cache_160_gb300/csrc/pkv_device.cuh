@@ -286,85 +286,111 @@ __device__ __forceinline__ float2 unpack2(uint32_t w) {
   else return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 
-// a / b for both halves, given y = 1 / b correctly rounded: a quotient estimate corrected by its exact
-// residual, kSteps times.  After the second step it is the correctly rounded quotient (Markstein,
-// "Computation of elementary functions on the IBM RISC System/6000 processor", 1990: the first makes
-// the estimate faithful), barring overflow and underflow.
+// -a / b for both halves, given y close to 1 / b: an estimate of the quotient corrected by its exact
+// residual, kSteps times.  With y = 1 / b correctly rounded the second step gives the correctly rounded
+// quotient (Markstein, "Computation of elementary functions on the IBM RISC System/6000 processor", 1990:
+// the first makes the estimate faithful), barring overflow and underflow.  Negated, because
+// a + (-a / b) b keeps the sign of a zero and a - (a / b) b does not.
 template <int kSteps>
-__device__ __forceinline__ uint64_t div_f32x2(uint64_t a, uint64_t minus_b, uint64_t y) {
-  uint64_t q = mul_f32x2(a, y);
+__device__ __forceinline__ uint64_t minus_div_f32x2(uint64_t a, uint64_t b, uint64_t minus_y) {
+  uint64_t q = mul_f32x2(a, minus_y);
 #pragma unroll
-  for (int i = 0; i < kSteps; ++i) q = fma_f32x2(fma_f32x2(q, minus_b, a), y, q);
+  for (int i = 0; i < kSteps; ++i) q = fma_f32x2(fma_f32x2(q, b, a), minus_y, q);
   return q;
 }
+// The same for one value, not negated (a >= 0, two steps).
+__device__ __forceinline__ float div_by(float a, float b, float y) {
+  float q = a * y;
+  q = fmaf(fmaf(-q, b, a), y, q);
+  return fmaf(fmaf(-q, b, a), y, q);
+}
+
+// What quant16_e2m1 needs of a head's scale.
+struct HeadScale {
+  float scale, y;         // scale, 1 / scale correctly rounded
+  bool given, ordinary;   // there is one; within 2^-100 .. 2^100 in absolute value
+  __device__ __forceinline__ HeadScale(const float* scales, int h) {
+    given = scales != nullptr;
+    scale = given ? __ldg(scales + h) : 1.f;
+    y = __frcp_rn(scale);
+    ordinary = fabsf(scale) > 0x1p-100f && fabsf(scale) < 0x1p100f;
+  }
+};
 
 // 16 f16/bf16 values (a: elements 0-7, b: 8-15) to the 16 codes of a 4-bit cache (8 bytes, element
-// order) and their e4m3 scale: u = x / head_scale, s = max|u| / 6 in e4m3, code = u / s in e2m1, all
+// order) and their e4m3 scale: u = x / head scale, s = max|u| / 6 in e4m3, code = u / s in e2m1, all
 // quotients correctly rounded fp32 by definition.  Every writer of the cache takes this function.
 //   max|u| is the quotient of max|x|, rounding being monotonic.
 //   u / s needs no correct rounding, only the right side of every border between codes (0.25, 0.75,
-// 1.25, 1.75, 2.5, 3.5, 5; a tie has to stay one).  One correction leaves an error below half an ulp and
-// 2^-23 ulp: on a tie u = s * border it gives the border itself; off it, u is an fp32 value next to s *
-// border or further (an fp32 value too: s has 4 bits), so the quotient is at least 0.53 ulp away (s's
-// significand is at most 1.875).
+// 1.25, 1.75, 2.5, 3.5, 5; a tie has to stay one).  With 1 / s to 1 ulp the estimate is within 3 ulp, and
+// one correction leaves an error below half an ulp and 3 * 2^-22 ulp: on a tie u = s * border it gives the
+// border itself; off it, u is an fp32 value next to s * border or further (an fp32 value too: s has 4
+// bits), so the quotient is at least 0.53 ulp away (s's significand is at most 1.875).
 //   Elements too small for an exact residual become code 0 with any rounding; huge ones and odd head
 // scales take the division instruction.
 template <bool kBF16>
-__device__ __forceinline__ uint2 quant16_e2m1(const uint4 a, const uint4 b, float head_scale, bool scaled,
-                                              uint32_t& scale_code) {
+__device__ __forceinline__ uint2 quant16_e2m1(const uint4 a, const uint4 b, const HeadScale& hs, uint32_t& scale_code) {
   const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-  float mx = 0.f;
-  bool nan = false;
-  uint64_t u[8];
+  uint32_t m = w[0] & 0x7fff7fffu;                           // max|x| of the low and the high halves, NaN if any is
+#pragma unroll
+  for (int k = 1; k < 8; ++k) {
+    const uint32_t v = w[k] & 0x7fff7fffu;
+    if constexpr (kBF16) asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(v));
+    else asm("max.NaN.f16x2 %0, %0, %1;" : "+r"(m) : "r"(v));
+  }
+  const float2 mm = unpack2<kBF16>(m);
+  bool nan = mm.x != mm.x || mm.y != mm.y;
+  float mx = fmaxf(mm.x, mm.y);
+  uint64_t u[8];                                             // x, or -x / head scale
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     const float2 f = unpack2<kBF16>(w[k]);
     u[k] = pack_f32x2(f.x, f.y);
-    mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
-    nan |= f.x != f.x || f.y != f.y;
   }
-  const float big = 1.2676506e30f, tiny = 1.f / big;         // 2^100
-  if (scaled) {
-    const float hs = fabsf(head_scale);
-    const float um = __fdiv_rn(mx, hs);
-    nan |= head_scale != head_scale || um != um;             // 0 / 0, inf / inf
-    if (hs > tiny && hs < big && um < big) {
-      const float y = __frcp_rn(head_scale);
+  if (nan) {                                                 // the maximum of the others, for the scale's definition
+    mx = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) mx = fmaxf(mx, fmaxf(fabsf(lo_f32(u[k])), fabsf(hi_f32(u[k]))));
+  }
+  if (hs.given) {
+    if (hs.ordinary && mx < 0x1p100f && div_by(mx, fabsf(hs.scale), fabsf(hs.y)) < 0x1p100f) {
+      mx = mx < 0x1p-100f ? 0.f : div_by(mx, fabsf(hs.scale), fabsf(hs.y));
 #pragma unroll
       for (int k = 0; k < 8; ++k)
-        u[k] = div_f32x2<2>(u[k], pack_f32x2(-head_scale, -head_scale), pack_f32x2(y, y));
+        u[k] = minus_div_f32x2<2>(u[k], pack_f32x2(hs.scale, hs.scale), pack_f32x2(-hs.y, -hs.y));
     } else {
+      mx = __fdiv_rn(mx, fabsf(hs.scale));
+      nan |= mx != mx;
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const float lo = __fdiv_rn(lo_f32(u[k]), head_scale), hi = __fdiv_rn(hi_f32(u[k]), head_scale);
+        const float lo = __fdiv_rn(lo_f32(u[k]), hs.scale), hi = __fdiv_rn(hi_f32(u[k]), hs.scale);
         nan |= lo != lo || hi != hi;
-        u[k] = pack_f32x2(lo, hi);
+        u[k] = pack_f32x2(-lo, -hi);
       }
     }
-    mx = um;
   }
-  const float want = fmaxf(__fdiv_rn(mx, 6.f), 0.001953125f);   // 2^-9, the smallest e4m3 value
-  scale_code = f32x2_to_e4m3x2(want, 0.f) & 0xFFu;
+  const float want = mx < 0x1p100f ? div_by(mx, 6.f, 1.f / 6.f) : 448.f;
+  scale_code = f32x2_to_e4m3x2(fmaxf(want, 0x1p-9f), 0.f) & 0xFFu;   // 2^-9: the smallest e4m3 value
   const float s = unpack2<false>(e4m3x2_to_f16x2(scale_code)).x;
   if (nan) scale_code = 0x7Fu;
-  if (!(mx < big)) {                                         // past 6 s in any case; keeps the residuals finite
+  if (!(mx < 0x1p100f)) {                                    // past 6 s in any case; keeps the residuals finite
 #pragma unroll
     for (int k = 0; k < 8; ++k)
-      u[k] = pack_f32x2(fminf(fmaxf(lo_f32(u[k]), -big), big), fminf(fmaxf(hi_f32(u[k]), -big), big));
+      u[k] = pack_f32x2(fminf(fmaxf(lo_f32(u[k]), -0x1p100f), 0x1p100f), fminf(fmaxf(hi_f32(u[k]), -0x1p100f), 0x1p100f));
   }
-  const float y = __frcp_rn(s);
-  const uint32_t flip = scaled ? __float_as_uint(head_scale) & 0x80000000u : 0u;
-  float q[16];
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(s));
+  float q[16];                                               // -x / s, or x / head scale / s
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    const uint64_t c = div_f32x2<1>(u[k], pack_f32x2(-s, -s), pack_f32x2(y, y));
-    // The residual step loses the sign of -0: take all signs from the inputs.
-    q[2 * k] = __uint_as_float((__float_as_uint(lo_f32(c)) & 0x7fffffffu) | (((w[k] << 16) & 0x80000000u) ^ flip));
-    q[2 * k + 1] = __uint_as_float((__float_as_uint(hi_f32(c)) & 0x7fffffffu) | ((w[k] & 0x80000000u) ^ flip));
+    const uint64_t c = minus_div_f32x2<1>(u[k], pack_f32x2(s, s), pack_f32x2(-y, -y));
+    q[2 * k] = lo_f32(c);
+    q[2 * k + 1] = hi_f32(c);
   }
   const float lo[8] = {q[0], q[1], q[2], q[3], q[4], q[5], q[6], q[7]};
   const float hi[8] = {q[8], q[9], q[10], q[11], q[12], q[13], q[14], q[15]};
-  return make_uint2(f32x8_to_e2m1x8(lo), f32x8_to_e2m1x8(hi));
+  const uint32_t flip = hs.given ? 0u : 0x88888888u;         // the codes' sign bits
+  return make_uint2(f32x8_to_e2m1x8(lo) ^ flip, f32x8_to_e2m1x8(hi) ^ flip);
 }
 
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {

@@ -8,9 +8,11 @@
 // 0.06).  The top 32 bits, as a signed part of half a turn, go to sincospi.
 //
 // Bound by HBM: 2 * (Hq + Hkv) * D * 2 bytes per token are moved, a few operations per element.  A
-// CTA takes one token, so that its rot / 2 angles are computed once for all heads: each thread holds
-// the sines and cosines of its 8 elements in registers while it walks the heads.  Its rows are on their
-// way, kBatch at a time, while it waits for the position and computes the angles.
+// CTA takes one token at a time, so that its rot / 2 angles are computed once for all heads: each thread
+// holds the sines and cosines of its 8 elements in registers while it walks the heads.  CTAs stay for the
+// next token, whose rows (kBatch of them per thread) and position are on their way while this one's are
+// turned.  16,381 tokens x 40 heads of 128: 83.6 us with a row in flight per thread, 70.4 with four,
+// 58.5 across tokens (5.7 TB/s, 0.85 of the measured copy).
 #include <math.h>
 
 #include "pkv_device.cuh"
@@ -22,6 +24,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMaxDim = 256;
 constexpr int kBatch = 4;                // rows in flight per thread
+constexpr int kCtasPerSm = 3;
 
 struct RotaryParams {
   uint8_t* q_out;
@@ -33,6 +36,7 @@ struct RotaryParams {
   const uint64_t* table;
   const void* q_weight;
   const void* k_weight;
+  int num_tokens;
   int num_heads;
   int num_kv_heads;
   int head_dim;
@@ -54,61 +58,51 @@ __device__ __forceinline__ void unpack8(const uint4 v, float (&f)[8]) {
 
 // kLanes threads share a row, 8 consecutive elements each (lanes past head_dim / 8 idle).
 template <bool kBF16, bool kInterleaved, int kLanes>
-__global__ void __launch_bounds__(kThreads) qk_rotary_kernel(const RotaryParams p) {
-  __shared__ float2 turn[kMaxDim / 2];                      // magnitude * (cos, sin) of each frequency
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) qk_rotary_kernel(const RotaryParams p) {
+  __shared__ float2 turn[2][kMaxDim / 2];                   // [token parity] magnitude * (cos, sin) of each frequency
   griddep_launch_dependents();
   griddep_wait();
-  const int64_t t = blockIdx.x;
-  constexpr int kRowsAtOnce = kThreads / kLanes;
-  const int sub = threadIdx.x % kLanes, e0 = 8 * sub;
+  constexpr int kRowsAtOnce = kThreads / kLanes, kRowsPerBatch = kBatch * kRowsAtOnce;
+  const int sub = threadIdx.x % kLanes, e0 = 8 * sub, row_in_step = threadIdx.x / kLanes;
   const bool live = e0 < p.head_dim;
   const int rows = p.num_heads + p.num_kv_heads, half = p.rotary_dim / 2;
-
-  auto src = [&](int r) -> const uint4* {
-    const bool isk = r >= p.num_heads;
-    const int64_t off = isk ? t * p.k_stride + int64_t(r - p.num_heads) * p.head_dim
-                            : t * p.q_stride + int64_t(r) * p.head_dim;
-    return reinterpret_cast<const uint4*>((isk ? p.k : p.q) + 2 * (off + e0));
-  };
-  int r0 = threadIdx.x / kLanes;                            // the batch's first row
-  uint4 batch[kBatch];
-  auto load_batch = [&]() {
-#pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      const int r = r0 + b * kRowsAtOnce;
-      batch[b] = live && r < rows ? *src(r) : make_uint4(0u, 0u, 0u, 0u);
-    }
-  };
-  load_batch();
-  const int position = p.positions[t];
-  if (position < 0) return;                                 // padding token
-
-  if (threadIdx.x < half) {
-    const uint64_t phase = uint64_t(int64_t(position)) * p.table[threadIdx.x];
-    float sn, cs;
-    sincospif(float(int32_t(phase >> 32)) * 4.656612873077393e-10f, &sn, &cs);   // 2^-31: half turns
-    turn[threadIdx.x] = make_float2(cs * p.magnitude, sn * p.magnitude);
-  }
-  __syncthreads();
-  // This thread's rotation: element e of the half layout belongs to frequency e mod half, of the
-  // interleaved one to e / 2.  Outside the rotated part: cos 1, sin 0.
   const bool rotated = live && e0 < p.rotary_dim;
-  float cs[8], sn[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int e = e0 + i;
-    float2 cssn = make_float2(1.f, 0.f);
-    if (rotated) cssn = turn[kInterleaved ? e >> 1 : (e < half ? e : e - half)];
-    const bool first = kInterleaved ? (i & 1) == 0 : e < half;
-    cs[i] = cssn.x;
-    sn[i] = first ? -cssn.y : cssn.y;
-  }
   const int lane = threadIdx.x & 31;
   const int partner = kInterleaved || !rotated ? lane : (e0 < half ? lane + half / 8 : lane - half / 8);
 
+  // Row r of token t in the inputs and outputs: byte r * head_dim * 2 behind the token's q (k: the row
+  // before its first head would be there).
+  const int row_bytes = 2 * p.head_dim;
+  const int64_t k_back = int64_t(p.num_heads) * row_bytes;
+  auto load_batch = [&](int64_t t, int s, uint4 (&batch)[kBatch]) {   // rows s .. of token t
+    const uint8_t* q = p.q + 2 * (t * p.q_stride + e0);
+    const uint8_t* k = p.k + 2 * (t * p.k_stride + e0) - k_back;
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int r = s + row_in_step + b * kRowsAtOnce;
+      batch[b] = live && r < rows ? *reinterpret_cast<const uint4*>((r < p.num_heads ? q : k) + int64_t(r) * row_bytes)
+                                  : make_uint4(0u, 0u, 0u, 0u);
+    }
+  };
+  int64_t t = blockIdx.x;
+  uint4 batch[kBatch];
+  load_batch(t, 0, batch);
+  int position = p.positions[t];
+  const uint64_t freq = threadIdx.x < half ? p.table[threadIdx.x] : 0;
+  auto angles = [&](int at, float2* tn) {
+    if (threadIdx.x < half) {
+      const uint64_t phase = uint64_t(int64_t(at)) * freq;
+      float sine, cosine;
+      sincospif(float(int32_t(phase >> 32)) * 4.656612873077393e-10f, &sine, &cosine);   // 2^-31: half turns
+      tn[threadIdx.x] = make_float2(cosine * p.magnitude, sine * p.magnitude);
+    }
+  };
+  angles(position, turn[0]);
+  float cs[8], sn[8];
+
   // Every thread of a warp walks the same number of rows: the norm and the partner's elements come
   // by shuffles.
-  auto rotate = [&](int r, const uint4 in) {
+  auto rotate = [&](uint8_t* q_to, uint8_t* k_to, int r, const uint4 in) {
     float x[8];
     unpack8<kBF16>(in, x);
     const bool isk = r >= p.num_heads;
@@ -134,27 +128,61 @@ __global__ void __launch_bounds__(kThreads) qk_rotary_kernel(const RotaryParams 
       y[i] = rotated ? x[i] * cs[i] + other * sn[i] : x[i];
     }
     if (live && r < rows) {
-      const int64_t off = isk ? t * p.k_out_stride + int64_t(r - p.num_heads) * p.head_dim
-                              : t * p.q_out_stride + int64_t(r) * p.head_dim;
-      *reinterpret_cast<uint4*>((isk ? p.k_out : p.q_out) + 2 * (off + e0)) =
+      *reinterpret_cast<uint4*>((isk ? k_to : q_to) + int64_t(r) * row_bytes) =
           make_uint4(pack2<kBF16>(y[0], y[1]), pack2<kBF16>(y[2], y[3]), pack2<kBF16>(y[4], y[5]),
                      pack2<kBF16>(y[6], y[7]));
     }
   };
-  const int last = (rows - 1) / kRowsAtOnce * kRowsAtOnce;  // first row of the last step
-  for (int s = 0; s <= last; s += kBatch * kRowsAtOnce, r0 += kBatch * kRowsAtOnce) {
-    if (s > 0) load_batch();
-#pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      if (s + b * kRowsAtOnce > last) break;                // uniform over the CTA
-      rotate(r0 + b * kRowsAtOnce, batch[b]);
+  for (int n = 0, s = 0;;) {
+    // The next batch: of this token, or the first of the CTA's next one.
+    const bool token_ends = s + kRowsPerBatch >= rows;
+    const int64_t t_next = token_ends ? t + gridDim.x : t;
+    const int s_next = token_ends ? 0 : s + kRowsPerBatch;
+    const bool more = t_next < p.num_tokens;
+    uint4 next[kBatch];
+    int position_next = position;
+    if (more) {
+      load_batch(t_next, s_next, next);
+      if (token_ends) position_next = p.positions[t_next];
     }
+    if (s == 0) {                                           // a token starts
+      __syncthreads();                                      // its angles are there; the token before last is done with
+      const float2* tn = turn[n & 1];
+      // This thread's rotation: element e of the half layout belongs to frequency e mod half, of the
+      // interleaved one to e / 2.
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int e = e0 + i;
+        const float2 cssn = rotated ? tn[kInterleaved ? e >> 1 : (e < half ? e : e - half)] : make_float2(1.f, 0.f);
+        const bool first = kInterleaved ? (i & 1) == 0 : e < half;
+        cs[i] = cssn.x;
+        sn[i] = first ? -cssn.y : cssn.y;
+      }
+    }
+    if (position >= 0) {                                    // else a padding token
+      uint8_t* q_to = p.q_out + 2 * (t * p.q_out_stride + e0);
+      uint8_t* k_to = p.k_out + 2 * (t * p.k_out_stride + e0) - k_back;
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        if (s + b * kRowsAtOnce >= rows) break;             // uniform over the CTA
+        rotate(q_to, k_to, s + row_in_step + b * kRowsAtOnce, batch[b]);
+      }
+    }
+    if (token_ends && more) angles(position_next, turn[(n + 1) & 1]);
+    if (!more) break;
+    n += token_ends;
+    t = t_next;
+    s = s_next;
+    position = position_next;
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) batch[b] = next[b];
   }
 }
 
 template <bool kBF16, bool kInterleaved>
-cudaError_t launch(const RotaryParams& p, int num_tokens, cudaStream_t s) {
-  const dim3 grid(num_tokens), block(kThreads);
+cudaError_t launch(const RotaryParams& p, cudaStream_t s) {
+  const int most = num_sms() > 0 ? num_sms() * kCtasPerSm : 1024;
+  const dim3 grid(p.num_tokens < most ? p.num_tokens : most), block(kThreads);
   if (p.head_dim <= 64) return launch_pdl(qk_rotary_kernel<kBF16, kInterleaved, 8>, grid, block, 0, s, p);
   if (p.head_dim <= 128) return launch_pdl(qk_rotary_kernel<kBF16, kInterleaved, 16>, grid, block, 0, s, p);
   return launch_pdl(qk_rotary_kernel<kBF16, kInterleaved, 32>, grid, block, 0, s, p);
@@ -230,6 +258,7 @@ pkv_status pkv_qk_rotary(void* q_out, const void* q, void* k_out, const void* k,
   p.table = table;
   p.q_weight = q_weight;
   p.k_weight = k_weight;
+  p.num_tokens = num_tokens;
   p.num_heads = num_heads;
   p.num_kv_heads = num_kv_heads;
   p.head_dim = head_dim;
@@ -239,8 +268,8 @@ pkv_status pkv_qk_rotary(void* q_out, const void* q, void* k_out, const void* k,
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool inter = layout == PKV_ROPE_INTERLEAVED;
   const cudaError_t e = dtype == PKV_BF16
-                            ? (inter ? launch<true, true>(p, num_tokens, s) : launch<true, false>(p, num_tokens, s))
-                            : (inter ? launch<false, true>(p, num_tokens, s) : launch<false, false>(p, num_tokens, s));
+                            ? (inter ? launch<true, true>(p, s) : launch<true, false>(p, s))
+                            : (inter ? launch<false, true>(p, s) : launch<false, false>(p, s));
   return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
