@@ -345,9 +345,8 @@ PKV_API pkv_status pkv_paged_prefill_chunk(void* out, const void* q, pkv_dtype q
  *                  (total_k); output rows from cu_q_lens[num_seqs] on are left as they were
  *   max_q_len      host upper bound of Lq (sizes the grid); a longer sequence sets PKV_DEVERR_CHUNK and
  *                  its rows past max_q_len stay unwritten
- * out must not overlap q, k or v.  Keys and values of a sequence's own rows must be finite wherever a
- * row attends them or they share a 128-key tile with one that does; rows outside the sequences may
- * hold anything.  cu_q_lens or cu_k_lens that are not ascending from 0 or pass the totals set
+ * out must not overlap q, k or v.  Only what a row attends reaches it: infinities and NaN in other
+ * rows' keys and values, and behind the sequences, do not.  cu_q_lens or cu_k_lens that are not ascending from 0 or pass the totals set
  * PKV_DEVERR_CHUNK and leave that sequence's rows unwritten.
  * Supported: head_dim 64 or 128, scale > 0, num_heads a multiple of num_kv_heads, num_seqs and
  * num_heads up to 65535.  P is rounded to dtype before its product with V, as the tensor cores take

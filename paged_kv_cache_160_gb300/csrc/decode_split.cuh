@@ -92,7 +92,8 @@ size_t dynamic_smem_limit(K kern) {
 }
 
 // Launches the split-KV merge behind a decode kernel that ran with prm.num_workers worker warps.
-pkv_status launch_merge(const DecodeParams& prm, bool q_bf16, int head_dim, cudaStream_t stream);
+// nan_through: a head whose sum of exponentials is NaN gives NaN (else zeros).
+pkv_status launch_merge(const DecodeParams& prm, bool q_bf16, int head_dim, bool nan_through, cudaStream_t stream);
 
 // The decode kernel over 4-bit caches, with its merge.
 pkv_status launch_decode_fp4(DecodeParams prm, bool q_bf16, int head_dim, int grid, cudaStream_t stream);

@@ -596,6 +596,7 @@ struct MergeParams {
   int max_len;            // the decode call's length clamp
   int part_blocks;        // the decode call's tiles per partition (0: balanced split)
   int num_workers;        // the decode call's worker warps
+  int nan_through;        // a NaN sum gives NaN, not zeros
 };
 
 constexpr int kMergeWarps = 8;
@@ -710,7 +711,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 2) split_kv_merge_kernel(con
     }
   }
   if (rsub == 0) {
-    const float inv = den > 0.f ? 1.f / den : 0.f;
+    const float inv = den > 0.f || (p.nan_through && den != den) ? 1.f / den : 0.f;
     const int64_t obase = (int64_t(seg) * G + hh) * D + dof;   // out[s][h * G + hh][:]
 #pragma unroll
     for (int e = 0; e < 4; ++e) store_out<QT>(p.out, obase + e, acc[e] * inv);
@@ -738,7 +739,7 @@ Layout layout(int group, int head_dim, int64_t slots) {
 
 }  // namespace
 
-pkv_status launch_merge(const DecodeParams& prm, bool q_bf16, int head_dim, cudaStream_t stream) {
+pkv_status launch_merge(const DecodeParams& prm, bool q_bf16, int head_dim, bool nan_through, cudaStream_t stream) {
   MergeParams mp;
   mp.out = prm.out;
   mp.ml = prm.ml;
@@ -751,6 +752,7 @@ pkv_status launch_merge(const DecodeParams& prm, bool q_bf16, int head_dim, cuda
   mp.max_len = prm.max_len;
   mp.part_blocks = prm.part_blocks;
   mp.num_workers = prm.num_workers;
+  mp.nan_through = nan_through;
   const int64_t items = int64_t(mp.num_segments) * mp.group;
   const int mgrid = int((items + kMergeWarps - 1) / kMergeWarps);
   auto kern = q_bf16 ? (head_dim == 128 ? split_kv_merge_kernel<KV_BF16, 128> : split_kv_merge_kernel<KV_BF16, 64>)
@@ -774,7 +776,7 @@ pkv_status launch_cfg(DecodeParams prm, const CUtensorMap& tk, const CUtensorMap
     return PKV_ERR_CUDA;
   prm.num_workers = grid * NW;
   if (launch_pdl(kern, dim3(grid), dim3(NW * 32), smem, stream, tk, tv, prm) != cudaSuccess) return PKV_ERR_CUDA;
-  return launch_merge(prm, QT == KV_BF16, D, stream);
+  return launch_merge(prm, QT == KV_BF16, D, false, stream);
 }
 
 // 12 worker warps with 2 stages each when the per-sequence prefix arrays fit next to the

@@ -572,7 +572,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) paged_decode_fp4_kernel(const 
     const int64_t seg_t0 = int64_t(Hkv) * cum_nb[tl.s] + int64_t(tl.h) * tl.nb;
     // Where the piece's result goes, by the rules that paged_decode.cu and the merge share.
     const bool complete = piece_b0 == 0 && ends;
-    const float f0 = complete ? (ls0 > 0.f ? vs / ls0 : 0.f) : vs, f1 = complete ? (ls1 > 0.f ? vs / ls1 : 0.f) : vs;
+    const float f0 = complete ? (ls0 == 0.f ? 0.f : vs / ls0) : vs, f1 = complete ? (ls1 == 0.f ? 0.f : vs / ls1) : vs;
     const int64_t slot = 2 * int64_t(w) + (seg_t0 + piece_b0 == t_begin ? 0 : 1);
     // Thread (g, t) holds elements D/8 g .. + D/8 - 1 of heads 2t and 2t + 1: element 2 mt + r is
     // o[mt][2 r] (head 2t) and o[mt][2 r + 1].
@@ -616,7 +616,7 @@ pkv_status launch_cfg(DecodeParams prm, int grid, cudaStream_t stream) {
     return PKV_ERR_CUDA;
   prm.num_workers = grid * NW;
   if (launch_pdl(kern, dim3(grid), dim3(NW * 32), smem, stream, prm) != cudaSuccess) return PKV_ERR_CUDA;
-  return launch_merge(prm, kQBF16, D, stream);
+  return launch_merge(prm, kQBF16, D, true, stream);
 }
 
 // 12 worker warps when the per-sequence prefix arrays fit next to their stages (up to about 900

@@ -308,12 +308,12 @@ __device__ __forceinline__ float div_by(float a, float b, float y) {
 // What quant16_e2m1 needs of a head's scale.
 struct HeadScale {
   float scale, y;         // scale, 1 / scale correctly rounded
-  bool given, ordinary;   // there is one; within 2^-100 .. 2^100 in absolute value
+  bool given, ordinary;   // there is one; within 2^-80 .. 2^100 in absolute value
   __device__ __forceinline__ HeadScale(const float* scales, int h) {
     given = scales != nullptr;
     scale = given ? __ldg(scales + h) : 1.f;
     y = __frcp_rn(scale);
-    ordinary = fabsf(scale) > 0x1p-100f && fabsf(scale) < 0x1p100f;
+    ordinary = fabsf(scale) > 0x1p-80f && fabsf(scale) < 0x1p100f;
   }
 };
 
@@ -326,8 +326,9 @@ struct HeadScale {
 // one correction leaves an error below half an ulp and 3 * 2^-22 ulp: on a tie u = s * border it gives the
 // border itself; off it, u is an fp32 value next to s * border or further (an fp32 value too: s has 4
 // bits), so the quotient is at least 0.53 ulp away (s's significand is at most 1.875).
-//   Elements too small for an exact residual become code 0 with any rounding; huge ones and odd head
-// scales take the division instruction.
+//   Elements too small for an exact residual (below 2^-100) become code 0 with any rounding, as the head
+// scale is above 2^-80 and s at least 2^-9; huge elements and other head scales take the division
+// instruction.
 template <bool kBF16>
 __device__ __forceinline__ uint2 quant16_e2m1(const uint4 a, const uint4 b, const HeadScale& hs, uint32_t& scale_code) {
   const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};

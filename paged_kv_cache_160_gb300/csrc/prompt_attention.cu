@@ -14,7 +14,7 @@ namespace pkv {
 namespace {
 
 constexpr int kTile = 128;                    // query rows of a block, keys of a tile
-constexpr int kThreads = 576;
+constexpr int kThreads = 640;
 constexpr uint32_t kTmemCols = 512;           // S_A | S_B | O_A | O_B, 128 columns each
 constexpr int kHalfBytes = kTile * 128;       // [128 rows][64 elements] of 2 bytes
 constexpr float kRescaleThreshold = 8.f;      // log2 units
@@ -24,6 +24,10 @@ struct PromptParams {
   const int32_t* cu_q;
   const int32_t* cu_k;
   int64_t out_stride;     // elements
+  const uint8_t* v;
+  int64_t v_stride;       // elements
+  int num_seqs;
+  int compact;            // items are numbered sequence by sequence (see item_of)
   int total_q;
   int total_k;
   int max_q_len;
@@ -119,14 +123,17 @@ __device__ __forceinline__ bool read_cta(const void* response, int& x, int& y, i
 // have not started (ask_for_cta), so that barriers and TMEM are set up once per SM, the next item's
 // loads and first products run while the last rows of this one are written, and an SM that is done
 // early takes the next item.  (A CTA per item spent 7 us outside the tile loop.)
-//   warp 0    : TMA producer of Q, K and V; asks for the next item
-//   warp 1    : TMEM owner and MMA issuer, in the order S_A(0) S_B(0) | PV_A(t) S_A(t+1) PV_B(t) S_B(t+1) | ...
-//               so that one block's softmax overlaps the other's products
-//   warps 2-9 : softmax of block A, warps 10-17: of block B; two threads per query row, one for each half
+//   warps 0-7 : softmax of block A, warps 8-15: of block B; two threads per query row, one for each half
 //               of the tile's keys.  A tile's way from its scores to its product with V is a chain that
 //               only the other block's products cover (3200 cycles for both blocks, about 2400 of them
 //               products), so the softmax is spread over twice the threads: one thread per row took
 //               390 us for a prompt of 8192 tokens where two take 381.
+//   warp 16   : TMA producer of Q, K and V; asks for the next item
+//   warp 17   : TMEM owner and MMA issuer, in the order S_A(0) S_B(0) | PV_A(t) S_A(t+1) PV_B(t) S_B(t+1) | ...
+//               so that one block's softmax overlaps the other's products
+//   warps 18-19: pass every V tile on to warp 17, having looked at those that some rows see only in part (from
+//               Item::masked on): 0 * V must not turn the rows' other keys into NaN.  V rows past the sequence's
+//               end become zeros, and so do non-finite values, which the rows that do see them get back at the end.
 // Every barrier's phases are counted over all items by each of its users.
 // ---------------------------------------------------------------------------------------
 template <int D>
@@ -144,25 +151,41 @@ struct Item {
   int rows;               // query rows to compute (at most max_q_len)
   int e0;                 // block A is row block e0 of the (sequence, kv head), B the next one
   int t0;                 // first key tile
+  int masked;             // key tiles from here on are seen only in part by some rows (tile index of the sequence)
   int na, nb, n;          // key tiles that A and B walk from there, and the larger
   bool live;              // there is something to do
 };
 
-// The item of block index (x, y, z).  A sequence's row blocks of a kv head are numbered query tile by
-// query tile, its query heads inside a tile; an item takes the next two.  The hardware starts CTAs with
-// x fastest and z slowest: the last tiles, which walk the most keys, come first.
-__device__ __forceinline__ Item item_of(const PromptParams& p, int x, int y, int z, int nz) {
-  Item it;
-  it.h = x;
-  it.q0 = p.cu_q[y];
-  it.k0 = p.cu_k[y];
-  it.Lq = p.cu_q[y + 1] - it.q0;
-  it.Lk = p.cu_k[y + 1] - it.k0;
-  const bool bad = it.q0 < 0 || it.k0 < 0 || it.Lq < 0 || it.Lk < 0 || it.Lq > p.total_q - it.q0 || it.Lk > p.total_k - it.k0;
-  it.rows = bad ? 0 : min(it.Lq, p.max_q_len);
+// A sequence: its rows, or none of them where the lengths are inconsistent.
+struct Seq {
+  int q0, k0, Lq, Lk, rows;
+  bool bad;
+  __device__ __forceinline__ Seq(const PromptParams& p, int s) {
+    q0 = p.cu_q[s];
+    k0 = p.cu_k[s];
+    Lq = p.cu_q[s + 1] - q0;
+    Lk = p.cu_k[s + 1] - k0;
+    bad = q0 < 0 || k0 < 0 || Lq < 0 || Lk < 0 || Lq > p.total_q - q0 || Lk > p.total_k - k0;
+    rows = bad ? 0 : min(Lq, p.max_q_len);
+  }
+  // Items of one of its kv heads: two row blocks each.
+  __device__ __forceinline__ int items(int G) const { return ((rows + kTile - 1) / kTile * G + 1) / 2; }
+};
+
+// The item of a sequence's kv head h with row blocks 2 * level and 2 * level + 1.  The blocks of a
+// (sequence, kv head) are numbered query tile by query tile, its query heads inside a tile.
+__device__ __forceinline__ Item item_at(const PromptParams& p, int h, int s, int level) {
+  const Seq q(p, s);
   const int G = p.num_heads / p.num_kv_heads;
-  it.e0 = 2 * (nz - 1 - z);
-  it.live = it.e0 < (it.rows + kTile - 1) / kTile * G;
+  Item it;
+  it.h = h;
+  it.q0 = q.q0;
+  it.k0 = q.k0;
+  it.Lq = q.Lq;
+  it.Lk = q.Lk;
+  it.rows = q.rows;
+  it.e0 = 2 * level;
+  it.live = unsigned(level) < unsigned(q.items(G));
   // Key tiles that the rows of block e attend (0: none, or no such rows).
   auto tiles_of = [&](int e) -> int {
     const int r0 = e / G * kTile;
@@ -174,7 +197,68 @@ __device__ __forceinline__ Item item_of(const PromptParams& p, int x, int y, int
   it.nb = it.live ? tiles_of(it.e0 + 1) : 0;
   it.n = max(it.na, it.nb);
   it.t0 = 0;
+  it.masked = max(0, it.e0 / G * kTile + it.Lk - it.Lq + 1) / kTile;   // the earlier block's first row decides
   return it;
+}
+
+// In both halves of m: the value of larger magnitude of m and w, NaN if either is; its sign means nothing.
+template <bool kBF16>
+__device__ __forceinline__ void max_magnitudes(uint32_t& m, uint32_t w) {
+  if constexpr (kBF16) asm("max.NaN.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w));
+  else asm("max.NaN.xorsign.abs.f16x2 %0, %0, %1;" : "+r"(m) : "r"(w));
+}
+
+// Adds to v the non-finite values among V[j][d .. d + 31], d counting the elements of the packed row, of keys
+// j0 .. j1 - 1.
+template <bool kBF16>
+__device__ __forceinline__ void add_non_finite(const PromptParams& p, int k0, int j0, int j1, int d, float (&v)[32]) {
+  for (int j = j0; j < j1; ++j) {
+    const uint4* row = reinterpret_cast<const uint4*>(p.v + ((int64_t(k0) + j) * p.v_stride + d) * 2);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const uint4 u = row[c];
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 f = unpack2<kBF16>(w[k]);
+        if (!(fabsf(f.x) < INFINITY)) v[8 * c + 2 * k] += f.x;
+        if (!(fabsf(f.y) < INFINITY)) v[8 * c + 2 * k + 1] += f.y;
+      }
+    }
+  }
+}
+
+constexpr int kMaxSeqs = 65535;
+constexpr int kSeqChunk = 32;                                // sequences per entry of the compact numbering's table
+
+// The item of block index (x, y, z), for a whole warp.
+//   Level by level (compact 0): x is the kv head, y the sequence, z counts the levels of the longest
+// sequence down.  The hardware starts CTAs with x fastest and z slowest: the items that walk the most
+// keys come first.  Shorter sequences' indexes have nothing to do.
+//   Sequence by sequence (compact 1), where those would be too many: x counts kv heads, then a sequence's
+// levels down, then sequences; `first` holds the number of every kSeqChunk-th sequence's first item.
+__device__ __forceinline__ Item item_of(const PromptParams& p, int x, int y, int z, int nz, const int* first, int lane) {
+  if (!p.compact) return item_at(p, x, y, nz - 1 - z);
+  const int h = x % p.num_kv_heads, j = x / p.num_kv_heads, G = p.num_heads / p.num_kv_heads;
+  int lo = 0, hi = (p.num_seqs + kSeqChunk - 1) / kSeqChunk; // the chunk of item j: first[lo] <= j < first[hi]
+  if (j >= first[hi]) return Item{};
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (first[mid] <= j) lo = mid; else hi = mid;
+  }
+  const int s = lo * kSeqChunk + lane, mine = s < p.num_seqs ? Seq(p, s).items(G) : 0;
+  int sum = mine;                                            // inclusive scan over the chunk
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += v;
+  }
+  const int rest = j - first[lo];
+  const unsigned past = __ballot_sync(0xffffffffu, sum > rest);
+  if (past == 0) return Item{};                              // (lengths that contradict one another)
+  const int l = __ffs(past) - 1;
+  const int before = __shfl_sync(0xffffffffu, sum - mine, l), count = __shfl_sync(0xffffffffu, mine, l);
+  return item_at(p, h, lo * kSeqChunk + l, count - 1 - (rest - before));
 }
 
 // Part `part` of `parts` of an item's key tiles.
@@ -216,9 +300,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ __align__(8) uint64_t bar_next[2], bar_read[2]; // an answer has come / every warp has read it
   // Q landed / no product reads it any more; K, V tiles likewise; S_x ready; P_x ready; PV_x done; O_x read.
   __shared__ __align__(8) uint64_t bar_q, bar_q_empty, bar_k_full[kStages], bar_k_empty[kStages], bar_v_full[kStages],
-      bar_v_empty[kStages], bar_s_full[2], bar_p_full[2], bar_pv_done[2], bar_o_free[2];
+      bar_v_empty[kStages], bar_s_full[2], bar_p_full[2], bar_pv_done[2], bar_o_free[2],
+      bar_v_seen[kStages];                                   // V landed and, from tile `masked` on, was looked at
   __shared__ uint32_t tmem_base_sh;
   __shared__ float exchange[2][2][2][kTile];                 // [block][step parity][key half][row]
+  __shared__ int first_item[kSplit ? 1 : (kMaxSeqs + kSeqChunk - 1) / kSeqChunk + 1];
+  __shared__ int masked_item[4];                             // by item number mod 4: non-finite values were taken out (+ 1)
   __shared__ __align__(16) float2 part_ml[2][kSplit ? kTile : 1];   // [block][row]: maximum and sum over this CTA's keys
   __shared__ __align__(16) float2 recv_ml[3][kSplit ? kTile : 1];   // [sender][row of this CTA's share]
   __shared__ __align__(8) uint64_t bar_recv;
@@ -240,6 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&bar_q, 1);
     mbar_init(&bar_q_empty, 1);
     mbar_init(&bar_recv, 1);
+    for (int i = 0; i < 4; ++i) masked_item[i] = 0;
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar_next[i], 1);
       mbar_init(&bar_read[i], kThreads / 32);                // every warp, the asking one too
@@ -253,10 +341,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bar_k_empty[i], 1);
       mbar_init(&bar_v_full[i], 1);
       mbar_init(&bar_v_empty[i], 1);
+      mbar_init(&bar_v_seen[i], 2);
     }
     fence_mbar_init();
   }
-  if (warp == 1) {
+  if (warp == 17) {
     tmem_alloc(&tmem_base_sh, kTmemCols);
     tmem_relinquish();
   }
@@ -309,6 +398,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     }
   };
+  // What a row gets back of element c of its half row in place of the non-finite values taken out of V.
+  auto give_back = [&](const Item& it, int row, int hf, int c, float (&v)[32]) {
+    add_non_finite<kBF16>(p, it.k0, max(it.masked, it.t0) * kTile,
+                          min(min(row + it.Lk - it.Lq + 1, it.Lk), (it.t0 + it.n) * kTile),
+                          it.h * D + D / 2 * hf + c, v);
+  };
   int bx = blockIdx.x, by = blockIdx.y, bz = blockIdx.z;
   int part = 0, parts = 1;
   if constexpr (kSplit) {
@@ -316,153 +411,49 @@ __global__ void __launch_bounds__(kThreads, 1)
     part = int(cluster_ctarank());
     bx /= parts;
   }
+  if constexpr (!kSplit) {
+    if (p.compact) {                                         // the table of the sequences' first items
+      const int chunks = (p.num_seqs + kSeqChunk - 1) / kSeqChunk;
+      for (int c = threadIdx.x; c < chunks; c += kThreads) {
+        int sum = 0;
+        for (int s = c * kSeqChunk; s < min(p.num_seqs, (c + 1) * kSeqChunk); ++s) sum += Seq(p, s).items(G);
+        first_item[c + 1] = sum;
+      }
+      __syncthreads();
+      if (warp == 0) {
+        int total = 0;
+        for (int c0 = 0; c0 < chunks; c0 += 32) {
+          int v = c0 + lane < chunks ? first_item[c0 + lane + 1] : 0;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int w = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += w;
+          }
+          if (c0 + lane < chunks) first_item[c0 + lane + 1] = total + v;
+          total += __shfl_sync(0xffffffffu, v, 31);
+        }
+        if (lane == 0) first_item[0] = 0;
+      }
+      __syncthreads();
+    }
+  }
   auto this_item = [&]() -> Item {
-    Item it = item_of(p, bx, by, bz, gridDim.z);
+    Item it = item_of(p, bx, by, bz, gridDim.z, first_item, lane);
     if constexpr (kSplit) take_part(it, part, parts);
     return it;
   };
 
-  if (warp == 0) {
-    // ---------------- TMA producer ----------------
-    const uint64_t pol_q = l2_policy_evict_first();
-    const uint64_t pol_kv = l2_policy_evict_last();          // re-read by the other heads and query tiles
-    bool ok = true, more = true;
-    uint32_t kt = 0, qi = 0;                                 // K/V tiles and items with keys so far
-    for (uint32_t i = 0; more && ok; ++i) {
-      // Ask for the item after this one.
-      ok = all(i < 2 || mbar_wait(&bar_read[i & 1], ((i >> 1) - 1) & 1u));
-      if (!kSplit && ok && lane == 0) {
-        mbar_arrive_expect_tx(&bar_next[i & 1], 16);
-        ask_for_cta(&response[i & 1], &bar_next[i & 1]);
-      }
-      const Item it = this_item();
-      if (lane == 0 && bz == 0 && bx == 0 && part == 0) {                 // one item of every sequence looks at the lengths
-        const int Lq = p.cu_q[by + 1] - p.cu_q[by];
-        if ((it.rows == 0 && Lq != 0) || Lq > p.max_q_len || it.Lk < 0 || it.k0 < 0 || it.Lk > p.total_k - it.k0 ||
-            (by == 0 && (it.q0 != 0 || it.k0 != 0)))
-          set_error(p.err, PKV_DEVERR_CHUNK);
-      }
-      if (ok && it.n > 0) {
-        ok = all(qi == 0 || mbar_wait(&bar_q_empty, (qi - 1) & 1u));
-        if (ok && lane == 0) {
-          mbar_arrive_expect_tx(&bar_q, 2 * C::kTileBytes);
-          for (int x = 0; x < 2; ++x) {
-            // A block past the sequence's end reads rows that nobody stores: its own first ones.
-            const int e = it.e0 + x, r0 = e / G * kTile < it.rows ? e / G * kTile : 0;
-            for (int d = 0; d < D / 64; ++d)
-              tma_load_3d(sQ + x * C::kTileBytes + d * kHalfBytes, &tmq, &bar_q, 64 * d, it.h * G + e % G, it.q0 + r0, pol_q);
-          }
-        }
-        ++qi;
-      }
-      for (int t = 0; ok && t < it.n; ++t, ++kt) {
-        const uint32_t st = kt % kStages, par = (kt / kStages - 1) & 1u;
-        ok = all(kt < uint32_t(kStages) || mbar_wait(&bar_k_empty[st], par));
-        if (ok && lane == 0) {
-          mbar_arrive_expect_tx(&bar_k_full[st], C::kTileBytes);
-          for (int d = 0; d < D / 64; ++d)
-            tma_load_3d(sK + st * C::kTileBytes + d * kHalfBytes, &tmk, &bar_k_full[st], 64 * d, it.h, it.k0 + (it.t0 + t) * kTile, pol_kv);
-        }
-        const bool v_ok = ok && all(kt < uint32_t(kStages) || mbar_wait(&bar_v_empty[st], par));
-        if (ok && !v_ok) (void)mbar_wait(&bar_k_full[st], (kt / kStages) & 1u);   // the K tile just started
-        ok = v_ok;
-        if (!ok) break;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&bar_v_full[st], C::kTileBytes);
-          for (int d = 0; d < D / 64; ++d)
-            tma_load_3d(sV + st * C::kTileBytes + d * kHalfBytes, &tmv, &bar_v_full[st], 64 * d, it.h, it.k0 + (it.t0 + t) * kTile, pol_kv);
-        }
-      }
-      // Also after a wait gave up: no answer may still be on its way when the CTA leaves.
-      bool came = true;
-      more = next_item(i, bx, by, bz, came);
-      ok = ok && came;
-    }
-    // Drain: the last loads of each stage have landed and the commits that release the stages and Q
-    // have arrived before the CTA may leave (each wait bounded).
-    if (!ok && lane == 0) set_error(p.err, PKV_DEVERR_TIMEOUT);
-    if (qi > 0) (void)mbar_wait(&bar_q, (qi - 1) & 1u);
-    if (ok && qi > 0) ok = mbar_wait(&bar_q_empty, (qi - 1) & 1u);
-    for (uint32_t u = kt < uint32_t(kStages) ? 0 : kt - kStages; u < kt; ++u) {
-      const uint32_t st = u % kStages, par = (u / kStages) & 1u;
-      (void)mbar_wait(&bar_k_full[st], par);
-      (void)mbar_wait(&bar_v_full[st], par);
-      if (ok) ok = mbar_wait(&bar_k_empty[st], par) && mbar_wait(&bar_v_empty[st], par);
-    }
-  } else if (warp == 1) {
-    // ---------------- MMA issuer (the whole warp; see mma_ss) ----------------
-    const uint32_t lead = elect_one();
-    const uint32_t idesc_s = umma_idesc_f16(kBF16, 128, 128, false, false);
-    const uint32_t idesc_o = umma_idesc_f16(kBF16, 128, D, false, true);
-    const uint64_t dQ = umma_sdesc_sw128(smem_u32(sQ), 16, 1024), dK = umma_sdesc_sw128(smem_u32(sK), 16, 1024);
-    const uint64_t dV = umma_sdesc_sw128(smem_u32(sV), kHalfBytes, 1024);
-    bool ok = true, more = true;
-    uint32_t kt = 0, qi = 0, s_of[2] = {0, 0}, o_of[2] = {0, 0};   // tiles; items with keys; steps and items of A, B
-    // S_x(t) = Q_x K_t^T into TMEM columns 128x .. 128x + 127.  A descriptor advances by bytes / 16.
-    auto issue_s = [&](int x, uint32_t tile) -> bool {
-      const uint32_t st = tile % kStages;
-      if (!all(mbar_wait(&bar_k_full[st], (tile / kStages) & 1u))) return false;
-      tc_fence_after();
-      const uint64_t a = dQ + uint32_t(x * C::kTileBytes / 16), b = dK + uint32_t(st * C::kTileBytes / 16);
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk)
-        mma_ss(lead, tmem + 128 * x, a + ((kk >> 2) * kHalfBytes + (kk & 3) * 32) / 16,
-               b + ((kk >> 2) * kHalfBytes + (kk & 3) * 32) / 16, idesc_s, kk > 0);
-      commit(lead, &bar_s_full[x]);
-      return true;
-    };
-    // O_x += P_x(t) V_t; P_x of each half of the keys in the first 32 columns of that half's scores.
-    auto issue_pv = [&](int x, uint32_t tile, bool first) -> bool {
-      const uint32_t st = tile % kStages;
-      if (!all(mbar_wait(&bar_v_full[st], (tile / kStages) & 1u))) return false;   // (long before P)
-      if (first && o_of[x] > 0 && !all(mbar_wait(&bar_o_free[x], (o_of[x] - 1) & 1u))) return false;
-      if (!all(mbar_wait(&bar_p_full[x], s_of[x] & 1u))) return false;
-      ++s_of[x];
-      tc_fence_after();
-      const uint64_t b = dV + uint32_t(st * C::kTileBytes / 16);
-#pragma unroll
-      for (int kk = 0; kk < kTile / 16; ++kk)
-        mma_ts(lead, tmem + 256 + 128 * x, tmem + 128 * x + (kk >> 2) * 64 + (kk & 3) * 8, b + kk * 2048 / 16, idesc_o,
-               !first || kk > 0);
-      commit(lead, &bar_pv_done[x]);
-      return true;
-    };
-    for (uint32_t i = 0; more && ok; ++i) {
-      const Item it = this_item();
-      if (it.n > 0) {
-        ok = all(mbar_wait(&bar_q, qi & 1u));
-        ++qi;
-        // One block may walk fewer tiles than the other.  A stage is released once both have read it.
-        ok = ok && (it.na == 0 || issue_s(0, kt)) && (it.nb == 0 || issue_s(1, kt));
-        commit(lead, &bar_k_empty[kt % kStages]);
-        if (it.n == 1) commit(lead, &bar_q_empty);
-        for (int t = 0; ok && t < it.n; ++t, ++kt) {
-          if (t < it.na) ok = issue_pv(0, kt, t == 0);
-          if (ok && t + 1 < it.na) ok = issue_s(0, kt + 1);
-          if (ok && t < it.nb) ok = issue_pv(1, kt, t == 0);
-          commit(lead, &bar_v_empty[kt % kStages]);
-          if (ok && t + 1 < it.nb) ok = issue_s(1, kt + 1);
-          if (t + 1 < it.n) commit(lead, &bar_k_empty[(kt + 1) % kStages]);
-          if (t + 2 == it.n) commit(lead, &bar_q_empty);     // the item's last scores are on their way
-        }
-        o_of[0] += it.na > 0;
-        o_of[1] += it.nb > 0;
-      }
-      bool came = true;
-      more = next_item(i, bx, by, bz, came);
-      ok = ok && came;
-    }
-    if (!ok && lane == 0) set_error(p.err, PKV_DEVERR_TIMEOUT);
-  } else {
+  if (warp < 16) {
+    if constexpr (!kSplit) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");   // 512 * 104 + 128 * 64 = 640 * 96
     // ---------------- softmax: two threads per query row ----------------
-    const int x = (warp - 2) >> 3, hf = ((warp - 2) >> 2) & 1;   // row block; half of the keys (and of O)
+    const int x = warp >> 3, hf = (warp >> 2) & 1;   // row block; half of the keys (and of O)
     const int quarter = warp & 3, r = 32 * quarter + lane;   // TMEM lane == row of the block
     const uint32_t lane_off = uint32_t(32 * quarter) << 16;
     constexpr int kKeys = kTile / 2, kODims = D / 2;
     const float slog = p.scale_log2;                         // > 0, so max(s) * slog = max(s * slog)
     const uint32_t tS = tmem + 128 * x + lane_off + kKeys * hf;   // scores, and P over them
     const uint32_t tO = tmem + 256 + 128 * x + lane_off + kODims * hf;
-    uint8_t* out_stage = sOut + (warp - 2) * C::kOutBytes;
+    uint8_t* out_stage = sOut + warp * C::kOutBytes;
     // The two warps of a row quarter meet here, once per tile and once per item, also after a wait
     // gave up: then they only walk on to the item's end, so that neither is left waiting for the other.
     auto meet = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + 4 * x + quarter) : "memory"); };
@@ -470,10 +461,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t kt = 0, steps = 0, meets = 0;                   // tiles; this block's steps; meetings
     for (uint32_t i = 0; more && ok; ++i) {
       const Item it = this_item();
-      const int e = it.e0 + x, row = e / G * kTile + r;
+      const int e = it.e0 + x, row0 = e / G * kTile, row = row0 + r, shift = it.Lk - it.Lq;
       const int nx = x == 0 ? it.na : it.nb;
       float m = -INFINITY, l = 0.f;                          // m of the row, l of this thread's keys
       for (int t = 0; t < nx; ++t, ++meets) {
+        const int kb = (it.t0 + t) * kTile;
         // Waiting for PV(t - 1) on every tile keeps that barrier at most one phase ahead of this wait.
         ok = all(ok && mbar_wait(&bar_s_full[x], (steps + t) & 1u) &&
                  (t == 0 || mbar_wait(&bar_pv_done[x], (steps + t - 1) & 1u)));
@@ -482,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           continue;
         }
         tc_fence_after();
-        const int lim = min(row + it.Lk - it.Lq + 1, it.Lk) - (it.t0 + t) * kTile - kKeys * hf;   // keys 0 .. lim - 1 are attended
+        const int lim = min(row + shift + 1, it.Lk) - kb - kKeys * hf;   // keys 0 .. lim - 1 are attended
         float s[kKeys];
 #pragma unroll
         for (int cc = 0; cc < kKeys / 32; ++cc) tmem_ld32(tS + 32 * cc, *reinterpret_cast<float(*)[32]>(s + 32 * cc));
@@ -506,21 +498,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool grow = mt > m + kRescaleThreshold;        // also true for the first tile
         const float m_prev = m;
         if (grow) m = mt;
-        // The sequence's last tile may reach past its keys: zero those V rows, so that 0 * whatever
-        // the rows behind hold cannot turn into NaN (both blocks write the same zeros).
-        const int kb = (it.t0 + t) * kTile;
-        if (kb + kTile > it.Lk) {
-          const uint32_t st = (kt + t) % kStages;
-          ok = all(mbar_wait(&bar_v_full[st], ((kt + t) / kStages) & 1u));
-          if (!ok) continue;
-          if (kb + r >= it.Lk) {
-            const uint32_t vrow = smem_u32(sV + st * C::kTileBytes) + r * 128;
-#pragma unroll
-            for (int d = 0; d < D / 64; ++d)
-#pragma unroll
-              for (int cc = 0; cc < 4; ++cc) sts128(vrow + d * kHalfBytes + (4 * hf + cc) * 16, 0u, 0u, 0u, 0u);
-          }
-        }
         // P over S (keys 2e, 2e + 1 in column e).  A row without keys so far has m = -inf and every
         // s = -inf: m = 0 then gives P = 0.
         const float mu = m == -INFINITY ? 0.f : m;
@@ -555,7 +532,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (grow) l *= alpha;
         }
         tmem_wait_st();
-        if (kb + kTile > it.Lk) fence_proxy_async_smem();    // the zeroed V rows, to the tensor cores
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar_p_full[x]);
@@ -575,11 +551,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       l += xl[kTile * (hf ^ 1)];
       ok = ok && fine[x][meets & 1][hf ^ 1][quarter] != 0;   // both warps go on, or none
       ++meets;
-      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const float inv = 1.f / l;                             // l = 0: a row without keys; NaN stays
       if constexpr (kSplit) {                                // the rows are finished below
-        if (hf == 0) part_ml[x][r] = make_float2(nx > 0 ? m : -INFINITY, nx > 0 ? l : 0.f);
+        // m = -inf stands for no keys; a row whose scores are all NaN has some.
+        if (hf == 0) part_ml[x][r] = make_float2(m == -INFINITY && l != 0.f ? 0.f : m, l);
         break;
       }
+      const bool taken = *static_cast<volatile int*>(&masked_item[i & 3]) == int(i) + 1;
       uint32_t o[kODims / 2];
       if (nx > 0 && ok) {
 #pragma unroll
@@ -587,9 +565,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           float v[32];
           tmem_ld32(tO + 32 * cc, v);
           tmem_wait_ld();
+          if (taken) give_back(it, row, hf, 32 * cc, v);
 #pragma unroll
           for (int c = 0; c < 16; ++c)
-            o[16 * cc + c] = l > 0.f ? pack2<kBF16>(v[2 * c] * inv, v[2 * c + 1] * inv) : 0u;
+            o[16 * cc + c] = l == 0.f ? 0u : pack2<kBF16>(v[2 * c] * inv, v[2 * c + 1] * inv);
         }
         tc_fence_before();
         __syncwarp();
@@ -601,6 +580,204 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok) write_rows(it, e, hf, quarter, out_stage, o);
     }
     if (!ok && lane == 0) set_error(p.err, PKV_DEVERR_TIMEOUT);
+  } else {
+    if constexpr (!kSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if (warp == 16) {
+      // ---------------- TMA producer ----------------
+      const uint64_t pol_q = l2_policy_evict_first();
+      const uint64_t pol_kv = l2_policy_evict_last();          // re-read by the other heads and query tiles
+      bool ok = true, more = true;
+      uint32_t kt = 0, qi = 0;                                 // K/V tiles and items with keys so far
+      for (uint32_t i = 0; more && ok; ++i) {
+        // Ask for the item after this one.
+        ok = all(i < 2 || mbar_wait(&bar_read[i & 1], ((i >> 1) - 1) & 1u));
+        if (!kSplit && ok && lane == 0) {
+          mbar_arrive_expect_tx(&bar_next[i & 1], 16);
+          ask_for_cta(&response[i & 1], &bar_next[i & 1]);
+        }
+        const Item it = this_item();
+        if (ok && it.n > 0) {
+          ok = all(qi == 0 || mbar_wait(&bar_q_empty, (qi - 1) & 1u));
+          if (ok && lane == 0) {
+            mbar_arrive_expect_tx(&bar_q, 2 * C::kTileBytes);
+            for (int x = 0; x < 2; ++x) {
+              // A block past the sequence's end reads rows that nobody stores: its own first ones.
+              const int e = it.e0 + x, r0 = e / G * kTile < it.rows ? e / G * kTile : 0;
+              for (int d = 0; d < D / 64; ++d)
+                tma_load_3d(sQ + x * C::kTileBytes + d * kHalfBytes, &tmq, &bar_q, 64 * d, it.h * G + e % G, it.q0 + r0, pol_q);
+            }
+          }
+          ++qi;
+        }
+        for (int t = 0; ok && t < it.n; ++t, ++kt) {
+          const uint32_t st = kt % kStages, par = (kt / kStages - 1) & 1u;
+          ok = all(kt < uint32_t(kStages) || mbar_wait(&bar_k_empty[st], par));
+          if (ok && lane == 0) {
+            mbar_arrive_expect_tx(&bar_k_full[st], C::kTileBytes);
+            for (int d = 0; d < D / 64; ++d)
+              tma_load_3d(sK + st * C::kTileBytes + d * kHalfBytes, &tmk, &bar_k_full[st], 64 * d, it.h, it.k0 + (it.t0 + t) * kTile, pol_kv);
+          }
+          const bool v_ok = ok && all(kt < uint32_t(kStages) || mbar_wait(&bar_v_empty[st], par));
+          if (ok && !v_ok) (void)mbar_wait(&bar_k_full[st], (kt / kStages) & 1u);   // the K tile just started
+          ok = v_ok;
+          if (!ok) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&bar_v_full[st], C::kTileBytes);
+            for (int d = 0; d < D / 64; ++d)
+              tma_load_3d(sV + st * C::kTileBytes + d * kHalfBytes, &tmv, &bar_v_full[st], 64 * d, it.h, it.k0 + (it.t0 + t) * kTile, pol_kv);
+          }
+        }
+        // Also after a wait gave up: no answer may still be on its way when the CTA leaves.
+        bool came = true;
+        more = next_item(i, bx, by, bz, came);
+        ok = ok && came;
+      }
+      // Drain: the last loads of each stage have landed and the commits that release the stages and Q
+      // have arrived before the CTA may leave (each wait bounded).
+      if (!ok && lane == 0) set_error(p.err, PKV_DEVERR_TIMEOUT);
+      if (qi > 0) (void)mbar_wait(&bar_q, (qi - 1) & 1u);
+      if (ok && qi > 0) ok = mbar_wait(&bar_q_empty, (qi - 1) & 1u);
+      for (uint32_t u = kt < uint32_t(kStages) ? 0 : kt - kStages; u < kt; ++u) {
+        const uint32_t st = u % kStages, par = (u / kStages) & 1u;
+        (void)mbar_wait(&bar_k_full[st], par);
+        (void)mbar_wait(&bar_v_full[st], par);
+        if (ok) ok = mbar_wait(&bar_k_empty[st], par) && mbar_wait(&bar_v_empty[st], par);
+      }
+    } else if (warp == 17) {
+      // ---------------- MMA issuer (the whole warp; see mma_ss) ----------------
+      const uint32_t lead = elect_one();
+      const uint32_t idesc_s = umma_idesc_f16(kBF16, 128, 128, false, false);
+      const uint32_t idesc_o = umma_idesc_f16(kBF16, 128, D, false, true);
+      const uint64_t dQ = umma_sdesc_sw128(smem_u32(sQ), 16, 1024), dK = umma_sdesc_sw128(smem_u32(sK), 16, 1024);
+      const uint64_t dV = umma_sdesc_sw128(smem_u32(sV), kHalfBytes, 1024);
+      bool ok = true, more = true;
+      uint32_t kt = 0, qi = 0, s_of[2] = {0, 0}, o_of[2] = {0, 0};   // tiles; items with keys; steps and items of A, B
+      // S_x(t) = Q_x K_t^T into TMEM columns 128x .. 128x + 127.  A descriptor advances by bytes / 16.
+      auto issue_s = [&](int x, uint32_t tile) -> bool {
+        const uint32_t st = tile % kStages;
+        if (!all(mbar_wait(&bar_k_full[st], (tile / kStages) & 1u))) return false;
+        tc_fence_after();
+        const uint64_t a = dQ + uint32_t(x * C::kTileBytes / 16), b = dK + uint32_t(st * C::kTileBytes / 16);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_ss(lead, tmem + 128 * x, a + ((kk >> 2) * kHalfBytes + (kk & 3) * 32) / 16,
+                 b + ((kk >> 2) * kHalfBytes + (kk & 3) * 32) / 16, idesc_s, kk > 0);
+        commit(lead, &bar_s_full[x]);
+        return true;
+      };
+      // O_x += P_x(t) V_t; P_x of each half of the keys in the first 32 columns of that half's scores.
+      auto issue_pv = [&](int x, uint32_t tile, bool first) -> bool {
+        const uint32_t st = tile % kStages;
+        if (!all(mbar_wait(&bar_v_seen[st], (tile / kStages) & 1u))) return false;   // (long before P)
+        if (first && o_of[x] > 0 && !all(mbar_wait(&bar_o_free[x], (o_of[x] - 1) & 1u))) return false;
+        if (!all(mbar_wait(&bar_p_full[x], s_of[x] & 1u))) return false;
+        ++s_of[x];
+        tc_fence_after();
+        const uint64_t b = dV + uint32_t(st * C::kTileBytes / 16);
+#pragma unroll
+        for (int kk = 0; kk < kTile / 16; ++kk)
+          mma_ts(lead, tmem + 256 + 128 * x, tmem + 128 * x + (kk >> 2) * 64 + (kk & 3) * 8, b + kk * 2048 / 16, idesc_o,
+                 !first || kk > 0);
+        commit(lead, &bar_pv_done[x]);
+        return true;
+      };
+      for (uint32_t i = 0; more && ok; ++i) {
+        const Item it = this_item();
+        if (it.n > 0) {
+          ok = all(mbar_wait(&bar_q, qi & 1u));
+          ++qi;
+          // One block may walk fewer tiles than the other.  A stage is released once both have read it.
+          ok = ok && (it.na == 0 || issue_s(0, kt)) && (it.nb == 0 || issue_s(1, kt));
+          commit(lead, &bar_k_empty[kt % kStages]);
+          if (it.n == 1) commit(lead, &bar_q_empty);
+          for (int t = 0; ok && t < it.n; ++t, ++kt) {
+            if (t < it.na) ok = issue_pv(0, kt, t == 0);
+            if (ok && t + 1 < it.na) ok = issue_s(0, kt + 1);
+            if (ok && t < it.nb) ok = issue_pv(1, kt, t == 0);
+            commit(lead, &bar_v_empty[kt % kStages]);
+            if (ok && t + 1 < it.nb) ok = issue_s(1, kt + 1);
+            if (t + 1 < it.n) commit(lead, &bar_k_empty[(kt + 1) % kStages]);
+            if (t + 2 == it.n) commit(lead, &bar_q_empty);     // the item's last scores are on their way
+          }
+          o_of[0] += it.na > 0;
+          o_of[1] += it.nb > 0;
+        }
+        bool came = true;
+        more = next_item(i, bx, by, bz, came);
+        ok = ok && came;
+      }
+      if (!ok && lane == 0) set_error(p.err, PKV_DEVERR_TIMEOUT);
+    } else if (warp >= 18) {
+      // ---------------- V tiles, some of them seen in part ----------------
+      bool ok = true, more = true;
+      uint32_t kt = 0;
+      for (uint32_t i = 0; more && ok; ++i) {
+        if ((bx | by | bz | part) == 0 && warp == 18) {        // with the first item: the lengths, looked over once
+          bool wrong = lane == 0 && (p.cu_q[0] != 0 || p.cu_k[0] != 0);
+          for (int s = lane; s < p.num_seqs; s += 32) {
+            const Seq q(p, s);
+            wrong |= q.bad || q.Lq > p.max_q_len;
+          }
+          if (wrong) set_error(p.err, PKV_DEVERR_CHUNK);
+        }
+        const Item it = this_item();
+        for (int t = 0; ok && t < it.n; ++t, ++kt) {
+          // Every tile's phase in its turn: the stage's next load waits for this tile's products, and they
+          // for the arrival below.  A wait that skipped phases could take an earlier tile's for its own.
+          const uint32_t st = kt % kStages;
+          ok = all(mbar_wait(&bar_v_full[st], (kt / kStages) & 1u));
+          if (!ok) break;
+          if (it.t0 + t < it.masked) {
+            if (lane == 0) mbar_arrive(&bar_v_seen[st]);
+            continue;
+          }
+          const int kb = (it.t0 + t) * kTile;
+#pragma unroll
+          for (int rr = 0; rr < 2; ++rr) {
+            const int r = 64 * (warp - 18) + 32 * rr + lane;
+            const uint32_t vrow = smem_u32(sV + st * C::kTileBytes) + r * 128;
+            if (kb + r >= it.Lk) {
+#pragma unroll
+              for (int c = 0; c < D / 8; ++c) sts128(vrow + c / 8 * kHalfBytes + ((c ^ r) & 7) * 16, 0u, 0u, 0u, 0u);
+              continue;
+            }
+            uint32_t m[4] = {0, 0, 0, 0};                    // the largest magnitudes; NaN if any is
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) {                // (in an order without bank conflicts)
+              const uint4 v = lds128(vrow + c / 8 * kHalfBytes + ((c ^ r) & 7) * 16);
+              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+              for (int u = 0; u < 4; ++u) max_magnitudes<kBF16>(m[u], w[u]);
+            }
+            max_magnitudes<kBF16>(m[0], m[1]);
+            max_magnitudes<kBF16>(m[2], m[3]);
+            max_magnitudes<kBF16>(m[0], m[2]);
+            const float2 mm = unpack2<kBF16>(m[0]);
+            if (fabsf(mm.x) < INFINITY && fabsf(mm.y) < INFINITY) continue;
+            *static_cast<volatile int*>(&masked_item[i & 3]) = int(i) + 1;
+            for (int c = 0; c < D / 8; ++c) {
+              const uint32_t at = vrow + c / 8 * kHalfBytes + (c & 7) * 16;
+              const uint4 v = lds128(at);
+              uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                const float2 f = unpack2<kBF16>(w[u]);
+                if (!(fabsf(f.x) < INFINITY)) w[u] &= 0xffff0000u;
+                if (!(fabsf(f.y) < INFINITY)) w[u] &= 0x0000ffffu;
+              }
+              sts128(at, w[0], w[1], w[2], w[3]);
+            }
+          }
+          fence_proxy_async_smem();                            // the tile, to the tensor cores
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar_v_seen[st]);
+        }
+        bool came = true;
+        more = next_item(i, bx, by, bz, came);
+        ok = ok && came;
+      }
+      if (!ok && lane == 0) set_error(p.err, PKV_DEVERR_TIMEOUT);
+    }
   }
   tc_fence_before();
   if constexpr (!kSplit) {
@@ -621,13 +798,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     cluster_sync();                                          // every CTA's products are done: stages and Q are free
     tc_fence_after();
-    if (warp >= 2) {
-      const int x = (warp - 2) >> 3, hf = ((warp - 2) >> 2) & 1, quarter = warp & 3, r = 32 * quarter + lane;
+    if (warp < 16) {
+      const int x = warp >> 3, hf = (warp >> 2) & 1, quarter = warp & 3, r = 32 * quarter + lane;
       constexpr int kODims = D / 2;                          // elements of half a row
       static_assert(2 * kTile * 2 * kHalf <= 2 * kStages * C::kTileBytes, "all rows fit in the K/V stages");
       static_assert(kTile * 2 * kHalf <= 2 * C::kTileBytes, "a share of 128 rows, or two of 64, fit in the Q area");
       const int owner = (x * kTile + 32 * quarter) / share, rr = (x * kTile + r) % share;   // rr: row of the share
-      const bool any = (x == 0 ? it.na : it.nb) > 0;
+      const bool any = (x == 0 ? it.na : it.nb) > 0, taken = masked_item[0] != 0;
+      const int orow = (it.e0 + x) / G * kTile + r;
       const uint32_t tO = tmem + (uint32_t(32 * quarter) << 16) + 256 + 128 * x + kODims * hf;
       // Share s of this CTA's rows: [hf][row][kHalf], at 2 * share * kHalf * s in the stages.  What CTA
       // `from` sends to CTA `to` lands in its slot (from - to - 1) mod parts: slots 0 (and 1) in the Q area,
@@ -647,6 +825,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld32(tO + 32 * cc, v);
             tmem_wait_ld();
           }
+          if (taken) give_back(it, orow, hf, 32 * cc, v);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const uint32_t at = row + (((8 * cc + i) ^ (r & 7)) << 4);
@@ -686,7 +865,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           w[s] = ml[s].x == -INFINITY ? 0.f : fast_exp2(ml[s].x - mx);
           den += w[s] * ml[s].y;
         }
-        const float inv = den > 0.f ? 1.f / den : 0.f;
+        const float inv = den == 0.f ? 0.f : 1.f / den;      // (0: a row without keys; NaN stays)
         uint32_t o[kODims / 2];
 #pragma unroll
         for (int cc = 0; cc < kODims / 32; ++cc) {
@@ -695,8 +874,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld32(tO + 32 * cc, v);
             tmem_wait_ld();
           }
+          if (taken) give_back(it, orow, hf, 32 * cc, v);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = any && w[3] > 0.f ? v[i] * (w[3] * inv) : 0.f;
+          for (int i = 0; i < 32; ++i) v[i] = any && ml[3].x != -INFINITY ? v[i] * (w[3] * inv) : 0.f;
 #pragma unroll
           for (int s = 0; s < 3; ++s) {
             if (s + 1 >= parts || !got) break;
@@ -714,14 +894,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 16; ++i) o[16 * cc + i] = pack2<kBF16>(v[2 * i], v[2 * i + 1]);
         }
-        if (got) write_rows(it, it.e0 + x, hf, quarter, sOut + (warp - 2) * C::kOutBytes, o);
+        if (got) write_rows(it, it.e0 + x, hf, quarter, sOut + warp * C::kOutBytes, o);
       }
     }
     __syncwarp();
     cluster_sync();                                          // every copy out of this CTA has arrived
   }
   griddep_launch_dependents();
-  if (warp == 1) {
+  if (warp == 17) {
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
@@ -768,14 +948,24 @@ pkv_status launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMa
   using C = Cfg<D>;
   const unsigned groups = (unsigned((max_q_len - 1) / kTile + 1) * unsigned(prm.num_heads / prm.num_kv_heads) + 1) / 2;
   const int64_t items = int64_t(groups) * num_seqs * prm.num_kv_heads;
+  // Items that the sequences have at most, whatever their lengths.
+  const int64_t G = prm.num_heads / prm.num_kv_heads;
+  const int64_t most = ((int64_t(prm.total_q) / kTile + num_seqs + 1) * G / 2 + num_seqs) * prm.num_kv_heads;
   const int64_t mean_tiles = (int64_t(prm.total_k) / num_seqs + kTile - 1) / kTile;
   int parts = 1;
   while (parts < 4 && mean_tiles >= 4 * parts && items <= clusters_at_once<kBF16, D>(2 * parts)) parts *= 2;
+  // Numbering the items level by level starts the long ones first, but has an index for every sequence
+  // at every level of the longest one; past twice the items that there can be, or past what a grid
+  // holds, they are numbered sequence by sequence.
+  const bool compact = parts == 1 && (items > 2 * most || groups > 65535);
+  if (compact && most > 0x7fffffff) return PKV_ERR_UNSUPPORTED;
+  PromptParams params = prm;
+  params.compact = compact;
   auto kern = parts > 1 ? prompt_kernel<kBF16, D, true> : prompt_kernel<kBF16, D, false>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
     return PKV_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(prm.num_kv_heads) * parts, num_seqs, groups);
+  cfg.gridDim = compact ? dim3(unsigned(most)) : dim3(unsigned(prm.num_kv_heads) * parts, num_seqs, groups);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = stream;
@@ -788,7 +978,7 @@ pkv_status launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMa
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kern, tq, tk, tv, prm) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, kern, tq, tk, tv, params) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
 }  // namespace
@@ -806,10 +996,9 @@ extern "C" pkv_status pkv_prompt_attention(void* out, const void* q, const void*
   if (dtype != PKV_F16 && dtype != PKV_BF16) return PKV_ERR_INVALID_ARG;
   if (!(scale > 0.f)) return PKV_ERR_INVALID_ARG;            // the softmax takes max(s) * scale
   if (head_dim != 64 && head_dim != 128) return PKV_ERR_UNSUPPORTED;
-  if (num_seqs > 65535 || num_heads > 65535) return PKV_ERR_UNSUPPORTED;
-  // The row blocks of a sequence's kv head, two to a CTA, fill one grid dimension.
-  if ((int64_t((int64_t(max_q_len) + kTile - 1) / kTile) * (num_heads / num_kv_heads) + 1) / 2 > 65535)
-    return PKV_ERR_UNSUPPORTED;
+  if (num_seqs > kMaxSeqs || num_heads > 65535) return PKV_ERR_UNSUPPORTED;
+  // Row blocks of a sequence's kv head are numbered in 32 bits.
+  if ((int64_t(max_q_len) + kTile - 1) / kTile * (num_heads / num_kv_heads) >= (int64_t(1) << 31)) return PKV_ERR_UNSUPPORTED;
   if (num_seqs == 0 || total_q == 0 || max_q_len == 0) return PKV_OK;
   if (!out || !q || !cu_q_lens || !cu_k_lens || (total_k > 0 && (!k || !v))) return PKV_ERR_INVALID_ARG;
   auto bad_rows = [&](const void* t, int64_t stride, int heads) {
@@ -840,6 +1029,10 @@ extern "C" pkv_status pkv_prompt_attention(void* out, const void* q, const void*
   prm.cu_q = cu_q_lens;
   prm.cu_k = cu_k_lens;
   prm.out_stride = out_stride;
+  prm.v = static_cast<const uint8_t*>(v);
+  prm.v_stride = v_stride;
+  prm.num_seqs = num_seqs;
+  prm.compact = 0;
   prm.total_q = total_q;
   prm.total_k = total_k;
   prm.max_q_len = max_q_len;

@@ -149,6 +149,25 @@ def test_odd_head_scales(head_scale):
     assert np.array_equal(gc[0].transpose(1, 0, 2)[live], wc[live])
 
 
+@pytest.mark.parametrize("exponent", [-120, -99, -85, -80, -79, -60, 60, 99, 101])
+def test_elements_of_the_size_of_a_tiny_or_huge_head_scale(exponent):
+    """Elements down to subnormals: u = x / head scale is of ordinary size for the larger ones."""
+    import paged_kv_cache_160_gb300 as pkv
+    rng = np.random.default_rng(200 + exponent)
+    size = np.maximum(exponent + rng.integers(-16, 4, (64, 1, 16)), -133).astype(np.float64)
+    x = torch.from_numpy(rng.uniform(-2, 2, (64, 1, 16)) * 2.0 ** size).to(torch.bfloat16)
+    x[1] = 0.0
+    x[2, 0, 3:] = 0.0
+    scale = np.array([1.7 * 2.0 ** exponent], dtype=np.float32)
+    pool = torch.zeros(pkv.fp4_cache_shape(4, 1, 16, 16), dtype=torch.uint8, device="cuda")
+    dev = torch.from_numpy(scale).cuda()
+    pkv.pkv_kv_write(x.cuda(), x.cuda(), torch.arange(64, device="cuda"), pool, pool.clone(),
+                     pkv.cache_desc_fp4(pool, dev, dev))
+    codes, sc = fp4.unpack(pool.cpu().numpy())
+    want, want_sc = fp4.quantise(x.double().numpy(), scale)
+    assert (sc.reshape(64, 1, 1) == want_sc).all() and (codes.reshape(64, 1, 16) == want).all()
+
+
 def test_many_tokens_and_a_bad_slot():
     import paged_kv_cache_160_gb300 as pkv
     rng = np.random.default_rng(1)
@@ -331,6 +350,29 @@ def test_decode_large_batch_takes_the_four_warp_layout():
     """12 prefix bytes per sequence next to 12 warps' stages: past about 9,900 sequences four warps run."""
     rng = np.random.default_rng(4)
     _run_decode([int(n) for n in rng.integers(1, 20, 11000)], 1, 1, 128, "bf16", seed=5)
+
+
+@pytest.mark.parametrize("length", [40, 5000])
+@pytest.mark.parametrize("which", ["k", "v"])
+def test_a_nan_in_an_attended_row_reaches_its_head_only(which, length):
+    """One sequence inside a worker's range, one split over workers and merged."""
+    import paged_kv_cache_160_gb300 as pkv
+    lens, hq, hkv, dim = [length, 30], 4, 2, 128
+    rng, table, pools, _ = _decode_case(31, lens, hq, hkv, dim, 16, False)
+    codes, sc = pools[0 if which == "k" else 1]
+    j = length // 2
+    sc[table[0, j // 16], 1, j % 16, 3] = 0x7F                 # 16 elements of kv head 1
+    k, v = (torch.from_numpy(fp4.pack(*p)).cuda() for p in pools)
+    q = torch.from_numpy(rng.standard_normal((2, hq, dim))).to(torch.bfloat16).cuda()
+    out = torch.empty_like(q)
+    ws = torch.empty(pkv.pkv_decode_workspace_bytes(2, hq, hkv, dim, 16, length, 0), dtype=torch.uint8, device="cuda")
+    pkv.pkv_paged_decode(out, q, k, v, pkv.cache_desc_fp4(k), torch.from_numpy(table).cuda(),
+                         torch.tensor(lens, dtype=torch.int32, device="cuda"), length, 0.09, 0, ws)
+    assert pkv.pkv_get_device_error() == 0
+    nan = torch.isnan(out).cpu()
+    want = torch.zeros_like(nan)
+    want[0, 2:] = True if which == "k" else torch.arange(dim) // 16 == 3
+    assert torch.equal(nan, want)
 
 
 def test_decode_no_alloc_is_bit_identical():

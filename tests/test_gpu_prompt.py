@@ -108,6 +108,80 @@ def test_rows_without_keys_are_zero(dim):
     assert (out[:260] == 0).all() and (out[300:] == 0).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("dim,q_lens,k_lens,hq,hkv", [(128, [200, 90], [200, 90], 4, 2), (64, [130, 3], [330, 200], 3, 1),
+                                                      (128, [300], [333], 1, 1), (64, [40], [900], 2, 2),
+                                                      (128, [150], [1600], 3, 1)])
+def test_only_what_a_row_attends_reaches_it(dim, q_lens, k_lens, hq, hkv, dtype):
+    """Infinities and NaN in K and V rows: rows before them are as if they were not there, rows that attend
+    them are not finite where float64 says so."""
+    import paged_kv_cache_160_gb300 as pkv
+    dt = DT[dtype]
+    g = torch.Generator().manual_seed(dim + sum(q_lens))
+    q, k, v = (torch.randn((n, h, dim), generator=g).to(dt) for n, h in ((sum(q_lens), hq), (sum(k_lens), hkv), (sum(k_lens), hkv)))
+    # the second sequence's first key, a key in the middle of the first one's last tile, and its last key
+    bad = [(k_lens[0] - 1, 0, 5, float("nan")), (k_lens[0] - min(40, q_lens[0] - 1), hkv - 1, 7, float("inf")),
+           (k_lens[0] - min(30, q_lens[0] - 1), hkv - 1, dim - 1, -float("inf"))]
+    if len(k_lens) > 1:
+        bad.append((sum(k_lens) - 2, 0, 0, -float("inf")))
+    for j, h, d, x in bad:
+        v[j, h, d] = x
+    kbad = k_lens[0] - min(20, q_lens[0] - 1)
+    cu = [torch.tensor(np.cumsum([0] + n), dtype=torch.int32, device="cuda") for n in (q_lens, k_lens)]
+
+    def run(kk):
+        out = torch.empty((sum(q_lens), hq, dim), dtype=dt, device="cuda")
+        pkv.pkv_prompt_attention(out, q.cuda(), kk.cuda(), v.cuda(), *cu, max(q_lens), dim ** -0.5)
+        assert pkv.pkv_get_device_error() == 0
+        return out.double().cpu().numpy()
+
+    with np.errstate(all="ignore"):
+        ref, size = prompt.prompt_attention(*(t.double().numpy() for t in (q, k, v)), q_lens, k_lens, dim ** -0.5)
+        got = run(k)
+        fine = np.isfinite(ref)
+        assert (~fine).any() and np.array_equal(np.isnan(got), np.isnan(ref))
+        assert np.array_equal(got[~fine & ~np.isnan(ref)], ref[~fine & ~np.isnan(ref)])
+        u = torch.finfo(dt).eps / 2
+        assert (np.abs(got - ref)[fine] <= ((u + 2.0 ** -11) * size + u * np.abs(ref) + 2.0 ** -25)[fine]).all()
+        # a NaN key: rows from it on are NaN throughout (in the heads that see it), the others as before
+        k2 = k.clone()
+        k2[kbad, 0, 3] = float("nan")
+        again = run(k2)
+        first = kbad - (k_lens[0] - q_lens[0])                 # the first row that attends it
+        heads = np.arange(hq) // (hq // hkv) == 0
+        rows = np.arange(sum(q_lens))
+        hit = (rows >= max(first, 0)) & (rows < q_lens[0])
+        assert np.isnan(again[hit][:, heads]).all()
+        assert np.array_equal(again[~hit], got[~hit], equal_nan=True)
+        assert np.array_equal(again[:, ~heads], got[:, ~heads], equal_nan=True)
+
+
+@pytest.mark.parametrize("dim,hq,hkv", [(128, 3, 1), (64, 4, 2), (128, 1, 1)])
+def test_one_long_prompt_among_many_short_ones(dim, hq, hkv):
+    """Skewed lengths: the items are numbered sequence by sequence."""
+    rng = np.random.default_rng(dim + hq)
+    lens = [int(n) for n in rng.integers(0, 12, 90)]
+    lens[37] = 1500
+    _run(lens, lens, hq, hkv, dim, "bf16", seed=3)
+    lens[37], lens[89] = 5, 1030
+    _run(lens, [n + 3 for n in lens], hq, hkv, dim, "f16", seed=4)
+
+
+def test_a_grid_dimension_does_not_bound_the_length():
+    """max_q_len may be any bound, even one whose blocks no grid dimension holds."""
+    import paged_kv_cache_160_gb300 as pkv
+    g = torch.Generator().manual_seed(2)
+    q, k, v = (torch.randn((300, h, 64), generator=g).to(torch.bfloat16).cuda() for h in (4, 2, 2))
+    cu = torch.tensor([0, 100, 300], dtype=torch.int32, device="cuda")
+    outs = []
+    for bound in (200, 20_000_000):
+        out = torch.empty_like(q)
+        pkv.pkv_prompt_attention(out, q, k, v, cu, cu, bound, 0.1)
+        assert pkv.pkv_get_device_error() == 0
+        outs.append(out)
+    assert torch.equal(*outs)
+
+
 def test_no_keys_at_all():
     _run([5, 0], [0, 0], 4, 2, 128, "bf16")
 

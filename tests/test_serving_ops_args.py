@@ -100,7 +100,7 @@ def test_prompt_attention_checks():
                 dict(ck=None), dict(out=24), dict(q=24), dict(k=8), dict(v=8), dict(cq=18), dict(ck=18), dict(sq=511),
                 dict(sq=504), dict(so=500), dict(sk=248), dict(sv=255), dict(so=-512)):
         assert call(**bad) == INVALID, bad
-    for bad in (dict(dim=96, so=4096, sq=4096, sk=4096, sv=4096), dict(seqs=65536), dict(mq=128 * 65535 + 1),
+    for bad in (dict(dim=96, so=4096, sq=4096, sk=4096, sv=4096), dict(seqs=65536),
                 dict(hq=65536, hkv=1, so=1 << 24, sq=1 << 24), dict(sq=1 << 38)):
         assert call(**bad) == UNSUPPORTED, bad
 
