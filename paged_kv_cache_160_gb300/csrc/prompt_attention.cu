@@ -7,6 +7,12 @@
 // GB300 design: a CTA holds two row blocks of 128 query rows that read the same keys, so every K/V
 // tile feeds 256 rows.  S = Q K^T and O += P V run on tcgen05 with S, P and O in tensor memory; Q, K
 // and V arrive by TMA straight from the packed rows (any row stride).
+//
+// Bound: the tensor cores, and the exponentials beside them (a 128 x 128 tile is 16,384 of them, about as
+// many cycles of the special function units as of its two products).  Measured in a graph: 8192 tokens,
+// 32 heads over 8, D 128: 333 us, 1.65 PFLOP/s of causal pairs; 16 prompts of 64 to 2048 tokens, 28 heads
+// over 4: 218 us; 512 rows behind 3584 keys: 35 us.  The products alone, without a softmax, take 297 us of
+// the first.
 #include "pkv_device.cuh"
 #include "pkv_host.h"
 
@@ -128,7 +134,9 @@ __device__ __forceinline__ bool read_cta(const void* response, int& x, int& y, i
 //               only the other block's products cover (3200 cycles for both blocks, about 2400 of them
 //               products), so the softmax is spread over twice the threads: one thread per row took
 //               390 us for a prompt of 8192 tokens where two take 381.
-//   warp 16   : TMA producer of Q, K and V; asks for the next item
+//   warp 16   : TMA producer of Q, K and V; asks for the next item and hands it to the other warps through
+//               shared memory (16 packed prompts took 226 us when every warp read the lengths by itself, 218
+//               since, and small items gain most: 4 us each instead of 7)
 //   warp 17   : TMEM owner and MMA issuer, in the order S_A(0) S_B(0) | PV_A(t) S_A(t+1) PV_B(t) S_B(t+1) | ...
 //               so that one block's softmax overlaps the other's products
 //   warps 18-19: pass every V tile on to warp 17, having looked at those that some rows see only in part (from
@@ -153,7 +161,7 @@ struct Item {
   int t0;                 // first key tile
   int masked;             // key tiles from here on are seen only in part by some rows (tile index of the sequence)
   int na, nb, n;          // key tiles that A and B walk from there, and the larger
-  bool live;              // there is something to do
+  bool live;              // there are such rows
 };
 
 // A sequence: its rows, or none of them where the lengths are inconsistent.
@@ -229,6 +237,7 @@ __device__ __forceinline__ void add_non_finite(const PromptParams& p, int k0, in
 }
 
 constexpr int kMaxSeqs = 65535;
+constexpr int kItems = 4;                                    // items on their way from the producer to the other warps
 constexpr int kSeqChunk = 32;                                // sequences per entry of the compact numbering's table
 
 // The item of block index (x, y, z), for a whole warp.
@@ -296,8 +305,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   using C = Cfg<D>;
   constexpr int kStages = C::kStages;
   extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ __align__(16) uint4 response[2];                // ask_for_cta's answers, in turn
-  __shared__ __align__(8) uint64_t bar_next[2], bar_read[2]; // an answer has come / every warp has read it
+  __shared__ __align__(16) uint4 response;                   // ask_for_cta's answer
+  __shared__ __align__(8) uint64_t bar_answer;               // it has come
+  __shared__ __align__(16) int4 items[kItems][3];            // the items, by number mod kItems (see read_item)
+  __shared__ __align__(8) uint64_t bar_item[kItems], bar_item_read[kItems];   // one is there / the warps have read it
   // Q landed / no product reads it any more; K, V tiles likewise; S_x ready; P_x ready; PV_x done; O_x read.
   __shared__ __align__(8) uint64_t bar_q, bar_q_empty, bar_k_full[kStages], bar_k_empty[kStages], bar_v_full[kStages],
       bar_v_empty[kStages], bar_s_full[2], bar_p_full[2], bar_pv_done[2], bar_o_free[2],
@@ -305,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint32_t tmem_base_sh;
   __shared__ float exchange[2][2][2][kTile];                 // [block][step parity][key half][row]
   __shared__ int first_item[kSplit ? 1 : (kMaxSeqs + kSeqChunk - 1) / kSeqChunk + 1];
-  __shared__ int masked_item[4];                             // by item number mod 4: non-finite values were taken out (+ 1)
+  __shared__ int masked_item[2 * kItems];                    // by item number modulo that: non-finite values were taken out (+ 1)
   __shared__ __align__(16) float2 part_ml[2][kSplit ? kTile : 1];   // [block][row]: maximum and sum over this CTA's keys
   __shared__ __align__(16) float2 recv_ml[3][kSplit ? kTile : 1];   // [sender][row of this CTA's share]
   __shared__ __align__(8) uint64_t bar_recv;
@@ -327,10 +338,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&bar_q, 1);
     mbar_init(&bar_q_empty, 1);
     mbar_init(&bar_recv, 1);
-    for (int i = 0; i < 4; ++i) masked_item[i] = 0;
+    mbar_init(&bar_answer, 1);
+    for (int i = 0; i < 2 * kItems; ++i) masked_item[i] = 0;
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(&bar_item[i], 1);
+      mbar_init(&bar_item_read[i], kThreads / 32 - 1);       // every warp but the producer
+    }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bar_next[i], 1);
-      mbar_init(&bar_read[i], kThreads / 32);                // every warp, the asking one too
       mbar_init(&bar_s_full[i], 1);
       mbar_init(&bar_p_full[i], 8);                          // one arrival per softmax warp
       mbar_init(&bar_pv_done[i], 1);
@@ -358,17 +372,33 @@ __global__ void __launch_bounds__(kThreads, 1)
   griddep_wait();
   const int G = p.num_heads / p.num_kv_heads;
   auto all = [](bool v) -> bool { return __all_sync(0xffffffffu, v); };
-  // The next item's block index, for a whole warp: false when there is none, or (ok false) no answer.
-  auto next_item = [&](uint32_t i, int& bx, int& by, int& bz, bool& ok) -> bool {
-    if constexpr (kSplit) return false;
-    ok = all(ok && mbar_wait(&bar_next[i & 1], (i >> 1) & 1u));
-    if (!ok) return false;
-    const bool got = read_cta(&response[i & 1], bx, by, bz);
-    fence_proxy_async_smem();                                // the slot's next answer comes after this read
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&bar_read[i & 1]);
-    return got;
+  // Item number i, once its barrier's phase is complete; na = -1: there is none.
+  auto read_item = [&](uint32_t i) -> Item {
+    const int4 a = items[i % kItems][0], b = items[i % kItems][1], c = items[i % kItems][2];
+    Item it;
+    it.h = a.x;
+    it.q0 = a.y;
+    it.k0 = a.z;
+    it.Lq = a.w;
+    it.Lk = b.x;
+    it.rows = b.y;
+    it.e0 = b.z;
+    it.t0 = b.w;
+    it.masked = c.x;
+    it.na = c.y;
+    it.nb = c.z;
+    it.n = max(it.na, it.nb);
+    it.live = c.w != 0;
+    return it;
   };
+  // The same for a warp that works on it; the slot may be used again.
+  auto take_item = [&](uint32_t i) -> Item {
+    const Item it = read_item(i);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bar_item_read[i % kItems]);
+    return it;
+  };
+  auto wait_item = [&](uint32_t i) -> bool { return all(mbar_wait(&bar_item[i % kItems], i / kItems & 1u)); };
   // Writes a warp's 32 half rows of block e, one per lane as 16-bit pairs: kStageRows at a time through
   // the warp's own staging area (16-byte chunk c of row rr at c ^ rr against bank conflicts), so that the
   // warp writes whole runs.
@@ -443,6 +473,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     return it;
   };
 
+  // Item `it` as number i, by the producer (one lane).
+  auto put_item = [&](uint32_t i, const Item& it) {
+    items[i % kItems][0] = make_int4(it.h, it.q0, it.k0, it.Lq);
+    items[i % kItems][1] = make_int4(it.Lk, it.rows, it.e0, it.t0);
+    items[i % kItems][2] = make_int4(it.masked, it.na, it.nb, it.live);
+    mbar_arrive(&bar_item[i % kItems]);
+  };
+  if (warp == 16) {
+    const Item it = this_item();
+    if (lane == 0) put_item(0, it);
+  }
+  const bool first = (bx | by | bz | part) == 0;             // one CTA of the grid looks the lengths over
+  __syncthreads();
+
   if (warp < 16) {
     if constexpr (!kSplit) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");   // 512 * 104 + 128 * 64 = 640 * 96
     // ---------------- softmax: two threads per query row ----------------
@@ -457,10 +501,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The two warps of a row quarter meet here, once per tile and once per item, also after a wait
     // gave up: then they only walk on to the item's end, so that neither is left waiting for the other.
     auto meet = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + 4 * x + quarter) : "memory"); };
-    bool ok = true, more = true;
-    uint32_t kt = 0, steps = 0, meets = 0;                   // tiles; this block's steps; meetings
-    for (uint32_t i = 0; more && ok; ++i) {
-      const Item it = this_item();
+    bool ok = true;
+    uint32_t steps = 0, meets = 0;                           // this block's steps; meetings
+    for (uint32_t i = 0; ok; ++i) {
+      const Item it = take_item(i);
+      if (it.na < 0) break;
       const int e = it.e0 + x, row0 = e / G * kTile, row = row0 + r, shift = it.Lk - it.Lq;
       const int nx = x == 0 ? it.na : it.nb;
       float m = -INFINITY, l = 0.f;                          // m of the row, l of this thread's keys
@@ -539,11 +584,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         l += lo_f32(acc) + hi_f32(acc);
       }
       steps += nx;
-      kt += it.n;
       // ---------------- output ----------------
       ok = all(ok && (nx == 0 || mbar_wait(&bar_pv_done[x], (steps - 1) & 1u)));
       tc_fence_after();
-      more = next_item(i, bx, by, bz, ok);
+      if (!kSplit) ok = ok && wait_item(i + 1);              // here, so that both warps go on or none
       float* xl = &exchange[x][meets & 1][0][r];
       xl[kTile * hf] = l;
       if (lane == 0) fine[x][meets & 1][hf][quarter] = ok;
@@ -557,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (hf == 0) part_ml[x][r] = make_float2(m == -INFINITY && l != 0.f ? 0.f : m, l);
         break;
       }
-      const bool taken = *static_cast<volatile int*>(&masked_item[i & 3]) == int(i) + 1;
+      const bool taken = *static_cast<volatile int*>(&masked_item[i % (2 * kItems)]) == int(i) + 1;
       uint32_t o[kODims / 2];
       if (nx > 0 && ok) {
 #pragma unroll
@@ -586,16 +630,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------- TMA producer ----------------
       const uint64_t pol_q = l2_policy_evict_first();
       const uint64_t pol_kv = l2_policy_evict_last();          // re-read by the other heads and query tiles
-      bool ok = true, more = true;
-      uint32_t kt = 0, qi = 0;                                 // K/V tiles and items with keys so far
-      for (uint32_t i = 0; more && ok; ++i) {
-        // Ask for the item after this one.
-        ok = all(i < 2 || mbar_wait(&bar_read[i & 1], ((i >> 1) - 1) & 1u));
-        if (!kSplit && ok && lane == 0) {
-          mbar_arrive_expect_tx(&bar_next[i & 1], 16);
-          ask_for_cta(&response[i & 1], &bar_next[i & 1]);
+      bool ok = true;
+      uint32_t kt = 0, qi = 0, answers = 0;                    // K/V tiles; items with keys; answers so far
+      auto ask = [&]() {
+        fence_proxy_async_smem();                              // the answer comes after the last one was read
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&bar_answer, 16);
+          ask_for_cta(&response, &bar_answer);
         }
-        const Item it = this_item();
+      };
+      Item it = read_item(0);
+      for (uint32_t i = 0;; ++i) {
+        if (!kSplit) ask();                                    // for the item after this one
         if (ok && it.n > 0) {
           ok = all(qi == 0 || mbar_wait(&bar_q_empty, (qi - 1) & 1u));
           if (ok && lane == 0) {
@@ -628,9 +675,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         // Also after a wait gave up: no answer may still be on its way when the CTA leaves.
-        bool came = true;
-        more = next_item(i, bx, by, bz, came);
-        ok = ok && came;
+        if (kSplit) break;
+        // The next item, past those without rows.  Also after a wait gave up: no answer may still be on
+        // its way when the CTA leaves.
+        bool got = false;
+        while (true) {
+          const bool came = all(mbar_wait(&bar_answer, answers & 1u));
+          ++answers;
+          ok = ok && came;
+          if (!ok) break;
+          got = read_cta(&response, bx, by, bz);
+          if (!got) break;
+          it = this_item();
+          if (it.live) break;
+          ask();
+        }
+        ok = ok && (i + 1 < kItems || all(mbar_wait(&bar_item_read[(i + 1) % kItems], ((i + 1) / kItems - 1) & 1u)));
+        if (!ok) break;
+        if (!got) it.na = -1;
+        if (lane == 0) put_item(i + 1, it);
+        if (!got) break;
       }
       // Drain: the last loads of each stage have landed and the commits that release the stages and Q
       // have arrived before the CTA may leave (each wait bounded).
@@ -650,7 +714,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t idesc_o = umma_idesc_f16(kBF16, 128, D, false, true);
       const uint64_t dQ = umma_sdesc_sw128(smem_u32(sQ), 16, 1024), dK = umma_sdesc_sw128(smem_u32(sK), 16, 1024);
       const uint64_t dV = umma_sdesc_sw128(smem_u32(sV), kHalfBytes, 1024);
-      bool ok = true, more = true;
+      bool ok = true;
       uint32_t kt = 0, qi = 0, s_of[2] = {0, 0}, o_of[2] = {0, 0};   // tiles; items with keys; steps and items of A, B
       // S_x(t) = Q_x K_t^T into TMEM columns 128x .. 128x + 127.  A descriptor advances by bytes / 16.
       auto issue_s = [&](int x, uint32_t tile) -> bool {
@@ -681,8 +745,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         commit(lead, &bar_pv_done[x]);
         return true;
       };
-      for (uint32_t i = 0; more && ok; ++i) {
-        const Item it = this_item();
+      for (uint32_t i = 0; ok; ++i) {
+        const Item it = take_item(i);
+        if (it.na < 0) break;
         if (it.n > 0) {
           ok = all(mbar_wait(&bar_q, qi & 1u));
           ++qi;
@@ -702,25 +767,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           o_of[0] += it.na > 0;
           o_of[1] += it.nb > 0;
         }
-        bool came = true;
-        more = next_item(i, bx, by, bz, came);
-        ok = ok && came;
+        if (kSplit) break;
+        ok = ok && wait_item(i + 1);
       }
       if (!ok && lane == 0) set_error(p.err, PKV_DEVERR_TIMEOUT);
     } else if (warp >= 18) {
       // ---------------- V tiles, some of them seen in part ----------------
-      bool ok = true, more = true;
+      bool ok = true;
       uint32_t kt = 0;
-      for (uint32_t i = 0; more && ok; ++i) {
-        if ((bx | by | bz | part) == 0 && warp == 18) {        // with the first item: the lengths, looked over once
-          bool wrong = lane == 0 && (p.cu_q[0] != 0 || p.cu_k[0] != 0);
-          for (int s = lane; s < p.num_seqs; s += 32) {
-            const Seq q(p, s);
-            wrong |= q.bad || q.Lq > p.max_q_len;
-          }
-          if (wrong) set_error(p.err, PKV_DEVERR_CHUNK);
+      if (first && warp == 18) {                             // the lengths, looked over once
+        bool wrong = lane == 0 && (p.cu_q[0] != 0 || p.cu_k[0] != 0);
+        for (int s = lane; s < p.num_seqs; s += 32) {
+          const Seq q(p, s);
+          wrong |= q.bad || q.Lq > p.max_q_len;
         }
-        const Item it = this_item();
+        if (wrong) set_error(p.err, PKV_DEVERR_CHUNK);
+      }
+      for (uint32_t i = 0; ok; ++i) {
+        const Item it = take_item(i);
+        if (it.na < 0) break;
         for (int t = 0; ok && t < it.n; ++t, ++kt) {
           // Every tile's phase in its turn: the stage's next load waits for this tile's products, and they
           // for the arrival below.  A wait that skipped phases could take an earlier tile's for its own.
@@ -754,7 +819,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             max_magnitudes<kBF16>(m[0], m[2]);
             const float2 mm = unpack2<kBF16>(m[0]);
             if (fabsf(mm.x) < INFINITY && fabsf(mm.y) < INFINITY) continue;
-            *static_cast<volatile int*>(&masked_item[i & 3]) = int(i) + 1;
+            *static_cast<volatile int*>(&masked_item[i % (2 * kItems)]) = int(i) + 1;
             for (int c = 0; c < D / 8; ++c) {
               const uint32_t at = vrow + c / 8 * kHalfBytes + (c & 7) * 16;
               const uint4 v = lds128(at);
@@ -772,9 +837,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar_v_seen[st]);
         }
-        bool came = true;
-        more = next_item(i, bx, by, bz, came);
-        ok = ok && came;
+        if (kSplit) break;
+        ok = ok && wait_item(i + 1);
       }
       if (!ok && lane == 0) set_error(p.err, PKV_DEVERR_TIMEOUT);
     }
@@ -956,7 +1020,8 @@ pkv_status launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMa
   while (parts < 4 && mean_tiles >= 4 * parts && items <= clusters_at_once<kBF16, D>(2 * parts)) parts *= 2;
   // Numbering the items level by level starts the long ones first, but has an index for every sequence
   // at every level of the longest one; past twice the items that there can be, or past what a grid
-  // holds, they are numbered sequence by sequence.
+  // holds, they are numbered sequence by sequence.  One prompt of 8192 tokens among 255 of 32 (32 heads
+  // over 8): 2347 us level by level, 513 us by sequence; 16 prompts of 64 to 2048 tokens: 226 us and 240 us.
   const bool compact = parts == 1 && (items > 2 * most || groups > 65535);
   if (compact && most > 0x7fffffff) return PKV_ERR_UNSUPPORTED;
   PromptParams params = prm;
