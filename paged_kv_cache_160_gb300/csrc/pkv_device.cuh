@@ -286,6 +286,13 @@ __device__ __forceinline__ float2 unpack2(uint32_t w) {
   else return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 
+// In both halves of m: the value of larger magnitude of m and w, NaN if either is; its sign means nothing.
+template <bool kBF16>
+__device__ __forceinline__ void max_magnitudes(uint32_t& m, uint32_t w) {
+  if constexpr (kBF16) asm("max.NaN.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w));
+  else asm("max.NaN.xorsign.abs.f16x2 %0, %0, %1;" : "+r"(m) : "r"(w));
+}
+
 // -a / b for both halves, given y close to 1 / b: an estimate of the quotient corrected by its exact
 // residual, kSteps times.  With y = 1 / b correctly rounded the second step gives the correctly rounded
 // quotient (Markstein, "Computation of elementary functions on the IBM RISC System/6000 processor", 1990:
@@ -332,14 +339,10 @@ struct HeadScale {
 template <bool kBF16>
 __device__ __forceinline__ uint2 quant16_e2m1(const uint4 a, const uint4 b, const HeadScale& hs, uint32_t& scale_code) {
   const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-  uint32_t m = w[0] & 0x7fff7fffu;                           // max|x| of the low and the high halves, NaN if any is
+  uint32_t m = w[0];                                         // max|x| of the low and the high halves, NaN if any is
 #pragma unroll
-  for (int k = 1; k < 8; ++k) {
-    const uint32_t v = w[k] & 0x7fff7fffu;
-    if constexpr (kBF16) asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(v));
-    else asm("max.NaN.f16x2 %0, %0, %1;" : "+r"(m) : "r"(v));
-  }
-  const float2 mm = unpack2<kBF16>(m);
+  for (int k = 1; k < 8; ++k) max_magnitudes<kBF16>(m, w[k]);
+  const float2 mm = unpack2<kBF16>(m & 0x7fff7fffu);
   bool nan = mm.x != mm.x || mm.y != mm.y;
   float mx = fmaxf(mm.x, mm.y);
   uint64_t u[8];                                             // x, or -x / head scale
@@ -392,6 +395,47 @@ __device__ __forceinline__ uint2 quant16_e2m1(const uint4 a, const uint4 b, cons
   const float hi[8] = {q[8], q[9], q[10], q[11], q[12], q[13], q[14], q[15]};
   const uint32_t flip = hs.given ? 0u : 0x88888888u;         // the codes' sign bits
   return make_uint2(f32x8_to_e2m1x8(lo) ^ flip, f32x8_to_e2m1x8(hi) ^ flip);
+}
+
+// The ordinary case of it without branches, so that two of them overlap: false (and no result) where
+// some element is not finite or huge, or the head's scale is odd.
+template <bool kBF16, bool kScaled>
+__device__ __forceinline__ bool quant16_e2m1_ordinary(const uint4 a, const uint4 b, const HeadScale& hs, uint2& codes,
+                                                      uint32_t& scale_code) {
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  uint32_t m[2] = {w[0], w[1]};
+#pragma unroll
+  for (int k = 2; k < 8; ++k) max_magnitudes<kBF16>(m[k & 1], w[k]);
+  max_magnitudes<kBF16>(m[0], m[1]);
+  const float2 mm = unpack2<kBF16>(m[0] & 0x7fff7fffu);
+  bool ok = mm.x < 0x1p100f && mm.y < 0x1p100f;              // also no NaN
+  float mx = fmaxf(mm.x, mm.y);
+  if constexpr (kScaled) {
+    const float q = div_by(mx, fabsf(hs.scale), fabsf(hs.y));
+    ok = ok && hs.ordinary && q < 0x1p100f;
+    mx = mx < 0x1p-100f ? 0.f : q;
+  }
+  scale_code = f32x2_to_e4m3x2(fmaxf(div_by(mx, 6.f, 1.f / 6.f), 0x1p-9f), 0.f) & 0xFFu;
+  const float s = unpack2<false>(e4m3x2_to_f16x2(scale_code)).x;
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(s));
+  uint32_t c[2];
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    float q[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 f = unpack2<kBF16>(w[4 * half + k]);
+      uint64_t u = pack_f32x2(f.x, f.y);
+      if constexpr (kScaled) u = minus_div_f32x2<2>(u, pack_f32x2(hs.scale, hs.scale), pack_f32x2(-hs.y, -hs.y));
+      u = minus_div_f32x2<1>(u, pack_f32x2(s, s), pack_f32x2(-y, -y));
+      q[2 * k] = lo_f32(u);
+      q[2 * k + 1] = hi_f32(u);
+    }
+    c[half] = f32x8_to_e2m1x8(q) ^ (kScaled ? 0u : 0x88888888u);
+  }
+  codes = make_uint2(c[0], c[1]);
+  return ok;
 }
 
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {

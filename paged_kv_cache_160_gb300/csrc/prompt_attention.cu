@@ -209,13 +209,6 @@ __device__ __forceinline__ Item item_at(const PromptParams& p, int h, int s, int
   return it;
 }
 
-// In both halves of m: the value of larger magnitude of m and w, NaN if either is; its sign means nothing.
-template <bool kBF16>
-__device__ __forceinline__ void max_magnitudes(uint32_t& m, uint32_t w) {
-  if constexpr (kBF16) asm("max.NaN.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w));
-  else asm("max.NaN.xorsign.abs.f16x2 %0, %0, %1;" : "+r"(m) : "r"(w));
-}
-
 // Adds to v the non-finite values among V[j][d .. d + 31], d counting the elements of the packed row, of keys
 // j0 .. j1 - 1.
 template <bool kBF16>
