@@ -346,8 +346,8 @@ PKV_API pkv_status pkv_paged_prefill_chunk(void* out, const void* q, pkv_dtype q
  *   max_q_len      host upper bound of Lq (sizes the grid); a longer sequence sets PKV_DEVERR_CHUNK and
  *                  its rows past max_q_len stay unwritten
  * out must not overlap q, k or v.  Only what a row attends reaches it: infinities and NaN in other
- * rows' keys and values, and behind the sequences, do not.  cu_q_lens or cu_k_lens that are not ascending from 0 or pass the totals set
- * PKV_DEVERR_CHUNK and leave that sequence's rows unwritten.
+ * rows' keys and values, and behind the sequences, do not.  cu_q_lens or cu_k_lens that are not
+ * ascending from 0 or pass the totals set PKV_DEVERR_CHUNK and leave that sequence's rows unwritten.
  * Supported: head_dim 64 or 128, scale > 0, num_heads a multiple of num_kv_heads, num_seqs and
  * num_heads up to 65535.  P is rounded to dtype before its product with V, as the tensor cores take
  * it; sums and outputs are fp32 until the last rounding.  q, k and v must be device memory of the

@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) paged_decode_fp4_kernel(const 
       // The softmax takes max(s) * sl and -inf * sl, so sl has to be positive: its sign goes to the
       // queries, and 0 becomes the least normal number.
       const uint32_t flip = sl < 0.f ? 0x80008000u : 0u;
-      sl = fmaxf(fabsf(sl), 1.17549435e-38f);
+      sl = fabsf(sl) < 1.17549435e-38f ? 1.17549435e-38f : fabsf(sl);   // (NaN stays)
       const int64_t qrow = (int64_t(tl.s) * Hkv * G + int64_t(tl.h) * G + gq) * D + D / 4 * tq;
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {     // 8 elements: two k steps
