@@ -11,7 +11,7 @@
 // Bound: the tensor cores, and the exponentials beside them (a 128 x 128 tile is 16,384 of them, about as
 // many cycles of the special function units as of its two products).  Measured in a graph: 8192 tokens,
 // 32 heads over 8, D 128: 333 us, 1.65 PFLOP/s of causal pairs; 16 prompts of 64 to 2048 tokens, 28 heads
-// over 4: 218 us; 512 rows behind 3584 keys: 35 us.  The products alone, without a softmax, take 297 us of
+// over 4: 218 us; 512 rows behind 3584 keys: 33 us.  The products alone, without a softmax, take 297 us of
 // the first.
 #include "pkv_device.cuh"
 #include "pkv_host.h"
@@ -302,8 +302,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ __align__(8) uint64_t bar_answer;               // it has come
   __shared__ __align__(16) int4 items[kItems][3];            // the items, by number mod kItems (see read_item)
   __shared__ __align__(8) uint64_t bar_item[kItems], bar_item_read[kItems];   // one is there / the warps have read it
-  // Q landed / no product reads it any more; K, V tiles likewise; S_x ready; P_x ready; PV_x done; O_x read.
-  __shared__ __align__(8) uint64_t bar_q, bar_q_empty, bar_k_full[kStages], bar_k_empty[kStages], bar_v_full[kStages],
+  // Q_x landed / no product reads it any more; K, V tiles likewise; S_x ready; P_x ready; PV_x done; O_x read.
+  __shared__ __align__(8) uint64_t bar_q[2], bar_q_empty[2], bar_k_full[kStages], bar_k_empty[kStages], bar_v_full[kStages],
       bar_v_empty[kStages], bar_s_full[2], bar_p_full[2], bar_pv_done[2], bar_o_free[2],
       bar_v_seen[kStages];                                   // V landed and, from tile `masked` on, was looked at
   __shared__ uint32_t tmem_base_sh;
@@ -328,8 +328,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tensormap(&tmq);
     prefetch_tensormap(&tmk);
     prefetch_tensormap(&tmv);
-    mbar_init(&bar_q, 1);
-    mbar_init(&bar_q_empty, 1);
     mbar_init(&bar_recv, 1);
     mbar_init(&bar_answer, 1);
     for (int i = 0; i < 2 * kItems; ++i) masked_item[i] = 0;
@@ -338,6 +336,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bar_item_read[i], kThreads / 32 - 1);       // every warp but the producer
     }
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar_q[i], 1);
+      mbar_init(&bar_q_empty[i], 1);
       mbar_init(&bar_s_full[i], 1);
       mbar_init(&bar_p_full[i], 8);                          // one arrival per softmax warp
       mbar_init(&bar_pv_done[i], 1);
@@ -394,7 +394,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto wait_item = [&](uint32_t i) -> bool { return all(mbar_wait(&bar_item[i % kItems], i / kItems & 1u)); };
   // Writes a warp's 32 half rows of block e, one per lane as 16-bit pairs: kStageRows at a time through
   // the warp's own staging area (16-byte chunk c of row rr at c ^ rr against bank conflicts), so that the
-  // warp writes whole runs.
+  // warp writes whole runs.  (Straight from the registers a store touches 32 lines; 16 packed prompts took
+  // 227 us that way, 218 with this.)
   auto write_rows = [&](const Item& it, int e, int hf, int quarter, uint8_t* area, const uint32_t (&o)[D / 4]) {
     const int row0 = e / G * kTile + 32 * quarter;
     if (row0 >= it.rows) return;
@@ -490,7 +491,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float slog = p.scale_log2;                         // > 0, so max(s) * slog = max(s * slog)
     const uint32_t tS = tmem + 128 * x + lane_off + kKeys * hf;   // scores, and P over them
     const uint32_t tO = tmem + 256 + 128 * x + lane_off + kODims * hf;
-    uint8_t* out_stage = sOut + warp * C::kOutBytes;
     // The two warps of a row quarter meet here, once per tile and once per item, also after a wait
     // gave up: then they only walk on to the item's end, so that neither is left waiting for the other.
     auto meet = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + 4 * x + quarter) : "memory"); };
@@ -614,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < kODims / 2; ++c) o[c] = 0u;
       }
-      if (ok) write_rows(it, e, hf, quarter, out_stage, o);
+      if (ok) write_rows(it, e, hf, quarter, sOut + warp * C::kOutBytes, o);
     }
     if (!ok && lane == 0) set_error(p.err, PKV_DEVERR_TIMEOUT);
   } else {
@@ -624,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t pol_q = l2_policy_evict_first();
       const uint64_t pol_kv = l2_policy_evict_last();          // re-read by the other heads and query tiles
       bool ok = true;
-      uint32_t kt = 0, qi = 0, answers = 0;                    // K/V tiles; items with keys; answers so far
+      uint32_t kt = 0, q_of[2] = {0, 0}, answers = 0;          // K/V tiles; Q blocks A, B; answers so far
       auto ask = [&]() {
         fence_proxy_async_smem();                              // the answer comes after the last one was read
         __syncwarp();
@@ -636,19 +636,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       Item it = read_item(0);
       for (uint32_t i = 0;; ++i) {
         if (!kSplit) ask();                                    // for the item after this one
-        if (ok && it.n > 0) {
-          ok = all(qi == 0 || mbar_wait(&bar_q_empty, (qi - 1) & 1u));
-          if (ok && lane == 0) {
-            mbar_arrive_expect_tx(&bar_q, 2 * C::kTileBytes);
-            for (int x = 0; x < 2; ++x) {
-              // A block past the sequence's end reads rows that nobody stores: its own first ones.
-              const int e = it.e0 + x, r0 = e / G * kTile < it.rows ? e / G * kTile : 0;
-              for (int d = 0; d < D / 64; ++d)
-                tma_load_3d(sQ + x * C::kTileBytes + d * kHalfBytes, &tmq, &bar_q, 64 * d, it.h * G + e % G, it.q0 + r0, pol_q);
-            }
+        // The queries of block x, once the products with the last ones are done (never called without keys).
+        auto load_q = [&](int x) {
+          ok = ok && all(q_of[x] == 0 || mbar_wait(&bar_q_empty[x], (q_of[x] - 1) & 1u));
+          if (!ok) return;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&bar_q[x], C::kTileBytes);
+            const int e = it.e0 + x;
+            for (int d = 0; d < D / 64; ++d)
+              tma_load_3d(sQ + x * C::kTileBytes + d * kHalfBytes, &tmq, &bar_q[x], 64 * d, it.h * G + e % G, it.q0 + e / G * kTile, pol_q);
           }
-          ++qi;
-        }
+          ++q_of[x];
+        };
         for (int t = 0; ok && t < it.n; ++t, ++kt) {
           const uint32_t st = kt % kStages, par = (kt / kStages - 1) & 1u;
           ok = all(kt < uint32_t(kStages) || mbar_wait(&bar_k_empty[st], par));
@@ -657,15 +656,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int d = 0; d < D / 64; ++d)
               tma_load_3d(sK + st * C::kTileBytes + d * kHalfBytes, &tmk, &bar_k_full[st], 64 * d, it.h, it.k0 + (it.t0 + t) * kTile, pol_kv);
           }
+          const bool k_ok = ok;                                // a K tile is on its way
+          if (t == 0 && it.na > 0) load_q(0);
           const bool v_ok = ok && all(kt < uint32_t(kStages) || mbar_wait(&bar_v_empty[st], par));
-          if (ok && !v_ok) (void)mbar_wait(&bar_k_full[st], (kt / kStages) & 1u);   // the K tile just started
           ok = v_ok;
-          if (!ok) break;
+          if (!ok) {
+            if (k_ok) (void)mbar_wait(&bar_k_full[st], (kt / kStages) & 1u);
+            break;
+          }
           if (lane == 0) {
             mbar_arrive_expect_tx(&bar_v_full[st], C::kTileBytes);
             for (int d = 0; d < D / 64; ++d)
               tma_load_3d(sV + st * C::kTileBytes + d * kHalfBytes, &tmv, &bar_v_full[st], 64 * d, it.h, it.k0 + (it.t0 + t) * kTile, pol_kv);
           }
+          if (t == 0 && it.nb > 0) load_q(1);
         }
         // Also after a wait gave up: no answer may still be on its way when the CTA leaves.
         if (kSplit) break;
@@ -692,8 +696,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Drain: the last loads of each stage have landed and the commits that release the stages and Q
       // have arrived before the CTA may leave (each wait bounded).
       if (!ok && lane == 0) set_error(p.err, PKV_DEVERR_TIMEOUT);
-      if (qi > 0) (void)mbar_wait(&bar_q, (qi - 1) & 1u);
-      if (ok && qi > 0) ok = mbar_wait(&bar_q_empty, (qi - 1) & 1u);
+      for (int x = 0; x < 2; ++x) {
+        if (q_of[x] > 0) (void)mbar_wait(&bar_q[x], (q_of[x] - 1) & 1u);
+        if (ok && q_of[x] > 0) ok = mbar_wait(&bar_q_empty[x], (q_of[x] - 1) & 1u);
+      }
       for (uint32_t u = kt < uint32_t(kStages) ? 0 : kt - kStages; u < kt; ++u) {
         const uint32_t st = u % kStages, par = (u / kStages) & 1u;
         (void)mbar_wait(&bar_k_full[st], par);
@@ -708,9 +714,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t dQ = umma_sdesc_sw128(smem_u32(sQ), 16, 1024), dK = umma_sdesc_sw128(smem_u32(sK), 16, 1024);
       const uint64_t dV = umma_sdesc_sw128(smem_u32(sV), kHalfBytes, 1024);
       bool ok = true;
-      uint32_t kt = 0, qi = 0, s_of[2] = {0, 0}, o_of[2] = {0, 0};   // tiles; items with keys; steps and items of A, B
-      // S_x(t) = Q_x K_t^T into TMEM columns 128x .. 128x + 127.  A descriptor advances by bytes / 16.
-      auto issue_s = [&](int x, uint32_t tile) -> bool {
+      uint32_t kt = 0, s_of[2] = {0, 0}, q_of[2] = {0, 0}, o_of[2] = {0, 0};   // tiles; steps, Q blocks and outputs of A, B
+      // S_x(t) = Q_x K_t^T into TMEM columns 128x .. 128x + 127, t of the block's `count` tiles.  A descriptor
+      // advances by bytes / 16.
+      auto issue_s = [&](int x, uint32_t tile, int t, int count) -> bool {
+        if (t == 0 && !all(mbar_wait(&bar_q[x], q_of[x]++ & 1u))) return false;
         const uint32_t st = tile % kStages;
         if (!all(mbar_wait(&bar_k_full[st], (tile / kStages) & 1u))) return false;
         tc_fence_after();
@@ -720,6 +728,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_ss(lead, tmem + 128 * x, a + ((kk >> 2) * kHalfBytes + (kk & 3) * 32) / 16,
                  b + ((kk >> 2) * kHalfBytes + (kk & 3) * 32) / 16, idesc_s, kk > 0);
         commit(lead, &bar_s_full[x]);
+        if (t + 1 == count) commit(lead, &bar_q_empty[x]);
         return true;
       };
       // O_x += P_x(t) V_t; P_x of each half of the keys in the first 32 columns of that half's scores.
@@ -738,24 +747,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         commit(lead, &bar_pv_done[x]);
         return true;
       };
+      // One block may walk fewer tiles than the other.  A stage is released once both have read it.
       for (uint32_t i = 0; ok; ++i) {
         const Item it = take_item(i);
         if (it.na < 0) break;
         if (it.n > 0) {
-          ok = all(mbar_wait(&bar_q, qi & 1u));
-          ++qi;
-          // One block may walk fewer tiles than the other.  A stage is released once both have read it.
-          ok = ok && (it.na == 0 || issue_s(0, kt)) && (it.nb == 0 || issue_s(1, kt));
+          ok = (it.na == 0 || issue_s(0, kt, 0, it.na)) && (it.nb == 0 || issue_s(1, kt, 0, it.nb));
           commit(lead, &bar_k_empty[kt % kStages]);
-          if (it.n == 1) commit(lead, &bar_q_empty);
           for (int t = 0; ok && t < it.n; ++t, ++kt) {
             if (t < it.na) ok = issue_pv(0, kt, t == 0);
-            if (ok && t + 1 < it.na) ok = issue_s(0, kt + 1);
+            if (ok && t + 1 < it.na) ok = issue_s(0, kt + 1, t + 1, it.na);
             if (ok && t < it.nb) ok = issue_pv(1, kt, t == 0);
             commit(lead, &bar_v_empty[kt % kStages]);
-            if (ok && t + 1 < it.nb) ok = issue_s(1, kt + 1);
+            if (ok && t + 1 < it.nb) ok = issue_s(1, kt + 1, t + 1, it.nb);
             if (t + 1 < it.n) commit(lead, &bar_k_empty[(kt + 1) % kStages]);
-            if (t + 2 == it.n) commit(lead, &bar_q_empty);     // the item's last scores are on their way
           }
           o_of[0] += it.na > 0;
           o_of[1] += it.nb > 0;
@@ -997,8 +1002,8 @@ int clusters_at_once(int parts) {
 
 // One item walks its keys alone unless there are so few items that clusters of 2 or 4 CTAs for each still
 // run at once and every part has two key tiles or more (by the sequences' mean length).  A chunk of 512
-// rows after 3584 keys (56 items): 49.5 us alone, 35.8 us in clusters of 2; one row of 32 heads over 4096
-// keys (16 items): 48.1 us alone, 21.7 us in clusters of 4.
+// rows after 3584 keys (56 items): 49.5 us alone, 33.0 us in clusters of 2; one row of 32 heads over 4096
+// keys (16 items): 48.1 us alone, 19.4 us in clusters of 4.
 template <bool kBF16, int D>
 pkv_status launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PromptParams& prm,
                   int num_seqs, int max_q_len, cudaStream_t stream) {
