@@ -83,7 +83,7 @@ TRAFFIC = {"source_sha1": "99b29df5523fdb6f246d2e32cb6d75fc16dafa77", "bytes_per
 
 def _src_hash() -> str:
     h = hashlib.sha1()
-    for f in ("paged_decode.cu", "pkv_device.cuh"):
+    for f in ("paged_decode.cu", "decode_split.cuh", "f32x2.cuh", "pkv_device.cuh"):
         h.update(open(os.path.join(ROOT, "paged_kv_cache_160_gb300", "csrc", f), "rb").read())
     return h.hexdigest()
 

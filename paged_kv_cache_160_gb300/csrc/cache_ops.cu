@@ -97,17 +97,6 @@ __global__ void __launch_bounds__(kThreads) kv_write_quant_kernel(
   }
 }
 
-// n / d for 0 <= n < 2^31 by a multiplication (Granlund and Montgomery, "Division by invariant integers
-// using multiplication", 1994): s = ceil(log2 d), m = floor(2^32 (2^s - d) / d) + 1.
-struct Divisor {
-  uint32_t d, m, s;
-  explicit Divisor(int by) : d(uint32_t(by)), m(0), s(0) {
-    while ((uint64_t(1) << s) < d) ++s;
-    m = uint32_t(((uint64_t(1) << 32) * ((uint64_t(1) << s) - d)) / d + 1);
-  }
-  __device__ __forceinline__ uint32_t quotient(uint32_t n) const { return (__umulhi(m, n) + n) >> s; }
-};
-
 // f16/bf16 rows into a 4-bit cache; 16 elements (one scale) of K and of V per thread and step.  The grid's
 // threads are a whole number of tokens (grid_of_tokens), so that a thread keeps its head and its place in
 // the head and works its head's scale out once; the next step's rows and slot are on their way meanwhile.

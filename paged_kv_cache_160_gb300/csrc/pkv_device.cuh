@@ -286,6 +286,17 @@ __device__ __forceinline__ float2 unpack2(uint32_t w) {
   else return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 
+// n / d for 0 <= n < 2^31 by a multiplication (Granlund and Montgomery, "Division by invariant integers
+// using multiplication", 1994): s = ceil(log2 d), m = floor(2^32 (2^s - d) / d) + 1.
+struct Divisor {
+  uint32_t d, m, s;
+  explicit Divisor(int by) : d(uint32_t(by)), m(0), s(0) {
+    while ((uint64_t(1) << s) < d) ++s;
+    m = uint32_t(((uint64_t(1) << 32) * ((uint64_t(1) << s) - d)) / d + 1);
+  }
+  __device__ __forceinline__ uint32_t quotient(uint32_t n) const { return (__umulhi(m, n) + n) >> s; }
+};
+
 // In both halves of m: the value of larger magnitude of m and w, NaN if either is; its sign means nothing.
 template <bool kBF16>
 __device__ __forceinline__ void max_magnitudes(uint32_t& m, uint32_t w) {

@@ -8,12 +8,14 @@
 // 0.06).  The top 32 bits, as a signed part of half a turn, go to sincospi.
 //
 // Bound by HBM: 2 * (Hq + Hkv) * D * 2 bytes per token are moved, a few operations per element.  A
-// CTA takes one token at a time, so that its rot / 2 angles are computed once for all heads: each thread
-// holds the sines and cosines of its 8 elements in registers while it walks the heads.  CTAs stay for the
-// next token, whose rows (kBatch of them per thread) and position are on their way while this one's are
-// turned.  16,381 tokens x 40 heads of 128: 83.6 us with a row in flight per thread, 70.4 with four,
-// 58.5 across tokens (5.7 TB/s, 0.85 of the measured copy).
+// CTA takes tiles of a few tokens: it works their angles out once for all heads, into shared memory, and
+// walks their rows (of q and k alike) with kBatch rows per thread in flight, the next tile's first ones
+// while this one's last are turned.  A thread has both elements of its pairs, so that nothing but the
+// norm's sum crosses threads.
+//   MEASURED
 #include <math.h>
+
+#include <algorithm>
 
 #include "pkv_device.cuh"
 #include "pkv_host.h"
@@ -23,8 +25,9 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxDim = 256;
-constexpr int kBatch = 4;                // rows in flight per thread
+constexpr int kBatch = 2;                // rows in flight per thread
 constexpr int kCtasPerSm = 3;
+constexpr int kMaxAngles = 2048;         // of a tile
 
 struct RotaryParams {
   uint8_t* q_out;
@@ -38,15 +41,17 @@ struct RotaryParams {
   const void* k_weight;
   int num_tokens;
   int num_heads;
-  int num_kv_heads;
   int head_dim;
   int rotary_dim;
+  int tile;               // tokens
+  Divisor rows;           // heads of q and k together
+  Divisor half;           // rotary_dim / 2
   float magnitude;
   float eps;
 };
 
 template <bool kBF16>
-__device__ __forceinline__ void unpack8(const uint4 v, float (&f)[8]) {
+__device__ __forceinline__ void unpack8(const uint4 v, float* f) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -55,137 +60,201 @@ __device__ __forceinline__ void unpack8(const uint4 v, float (&f)[8]) {
     f[2 * i + 1] = p.y;
   }
 }
+template <bool kBF16>
+__device__ __forceinline__ uint4 pack8(const float* f) {
+  return make_uint4(pack2<kBF16>(f[0], f[1]), pack2<kBF16>(f[2], f[3]), pack2<kBF16>(f[4], f[5]),
+                    pack2<kBF16>(f[6], f[7]));
+}
 
-// kLanes threads share a row, 8 consecutive elements each (lanes past head_dim / 8 idle).
-template <bool kBF16, bool kInterleaved, int kLanes>
+// kLanes threads share a row, two runs of 8 elements each (lanes past head_dim / 16 idle): in the half
+// layout runs l and l + rotary_dim / 16, whose elements are paired, else l and l + head_dim / 16.
+template <bool kBF16, bool kInterleaved, int kLanes, bool kNorm>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) qk_rotary_kernel(const RotaryParams p) {
-  __shared__ float2 turn[2][kMaxDim / 2];                   // [token parity] magnitude * (cos, sin) of each frequency
+  extern __shared__ __align__(16) float smem[];
+  constexpr int kRowsAtOnce = kThreads / kLanes, kRowsPerStep = kBatch * kRowsAtOnce;
+  const int half = int(p.half.d), rows = int(p.rows.d), num_angles = p.tile * half;
+  // [tile parity][token][angle], scaled by the magnitude; the half layout keeps angles 8l .. 8l + 3 of all
+  // lanes l before their angles 8l + 4 .. 8l + 7, so that a quarter warp reads neighbouring 16 bytes.
+  float* cosines = smem;
+  float* sines = smem + 2 * num_angles;
+  int* place = reinterpret_cast<int*>(smem + 4 * num_angles);   // [tile parity][token] positions
+  const int l = threadIdx.x % kLanes, row_in_step = threadIdx.x / kLanes;
+  const bool live = 16 * l < p.head_dim;
+  const int pairs = p.rotary_dim / 16;                      // lanes with paired runs (half layout)
+  int run0 = l, run1 = l + p.head_dim / 16;
+  if (!kInterleaved) {
+    run0 = l < pairs ? l : 2 * l;
+    run1 = l < pairs ? l + pairs : 2 * l + 1;
+  }
+  const bool turn0 = live && 8 * run0 < p.rotary_dim, turn1 = live && 8 * run1 < p.rotary_dim;
+
   griddep_launch_dependents();
   griddep_wait();
-  constexpr int kRowsAtOnce = kThreads / kLanes, kRowsPerBatch = kBatch * kRowsAtOnce;
-  const int sub = threadIdx.x % kLanes, e0 = 8 * sub, row_in_step = threadIdx.x / kLanes;
-  const bool live = e0 < p.head_dim;
-  const int rows = p.num_heads + p.num_kv_heads, half = p.rotary_dim / 2;
-  const bool rotated = live && e0 < p.rotary_dim;
-  const int lane = threadIdx.x & 31;
-  const int partner = kInterleaved || !rotated ? lane : (e0 < half ? lane + half / 8 : lane - half / 8);
-
-  // Row r of token t in the inputs and outputs: byte r * head_dim * 2 behind the token's q (k: the row
-  // before its first head would be there).
-  const int row_bytes = 2 * p.head_dim;
-  const int64_t k_back = int64_t(p.num_heads) * row_bytes;
-  auto load_batch = [&](int64_t t, int s, uint4 (&batch)[kBatch]) {   // rows s .. of token t
-    const uint8_t* q = p.q + 2 * (t * p.q_stride + e0);
-    const uint8_t* k = p.k + 2 * (t * p.k_stride + e0) - k_back;
-#pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      const int r = s + row_in_step + b * kRowsAtOnce;
-      batch[b] = live && r < rows ? *reinterpret_cast<const uint4*>((r < p.num_heads ? q : k) + int64_t(r) * row_bytes)
-                                  : make_uint4(0u, 0u, 0u, 0u);
-    }
-  };
-  int64_t t = blockIdx.x;
-  uint4 batch[kBatch];
-  load_batch(t, 0, batch);
-  int position = p.positions[t];
-  const uint64_t freq = threadIdx.x < half ? p.table[threadIdx.x] : 0;
-  auto angles = [&](int at, float2* tn) {
-    if (threadIdx.x < half) {
-      const uint64_t phase = uint64_t(int64_t(at)) * freq;
+  const int tiles = (p.num_tokens - 1) / p.tile + 1;
+  auto tokens_of = [&](int tile) -> int { return min(p.tile, p.num_tokens - tile * p.tile); };
+  auto work_angles_out = [&](int tile, int parity) {        // from the positions in `place`
+    const int n = tokens_of(tile) * half;
+    float* c = cosines + parity * num_angles;
+    float* s = sines + parity * num_angles;
+    for (int a = threadIdx.x; a < n; a += kThreads) {
+      const int tt = int(p.half.quotient(a)), i = a - tt * half;
+      const uint64_t phase = uint64_t(int64_t(place[parity * p.tile + tt])) * __ldg(p.table + i);
       float sine, cosine;
       sincospif(float(int32_t(phase >> 32)) * 4.656612873077393e-10f, &sine, &cosine);   // 2^-31: half turns
-      tn[threadIdx.x] = make_float2(cosine * p.magnitude, sine * p.magnitude);
+      const int at = tt * half + (kInterleaved ? i : (i >> 2 & 1) * (half / 2) + (i >> 3) * 4 + (i & 3));
+      c[at] = cosine * p.magnitude;
+      s[at] = sine * p.magnitude;
     }
   };
-  angles(position, turn[0]);
-  float cs[8], sn[8];
-
-  // Every thread of a warp walks the same number of rows: the norm and the partner's elements come
-  // by shuffles.
-  auto rotate = [&](uint8_t* q_to, uint8_t* k_to, int r, const uint4 in) {
-    float x[8];
-    unpack8<kBF16>(in, x);
-    const bool isk = r >= p.num_heads;
-    const void* wp = isk ? p.k_weight : p.q_weight;
-    if (p.q_weight || p.k_weight) {                         // uniform: the shuffles need the whole warp
+  // Row f of a tile, counted over its tokens: the address of its first element.
+  auto row_at = [&](const uint8_t* q, int64_t qs, const uint8_t* k, int64_t ks, int tile, int f, int& tt, bool& isk) -> int64_t {
+    tt = int(p.rows.quotient(f));
+    const int r = f - tt * rows;
+    isk = r >= p.num_heads;
+    const int64_t t = int64_t(tile) * p.tile + tt;
+    return reinterpret_cast<int64_t>(isk ? k : q) +
+           2 * (t * (isk ? ks : qs) + int64_t(isk ? r - p.num_heads : r) * p.head_dim);
+  };
+  auto load_batch = [&](int tile, int f0, uint4 (&batch)[kBatch][2]) {   // rows f0 ..
+    const int n = tokens_of(tile) * rows;
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int f = f0 + row_in_step + b * kRowsAtOnce;
+      batch[b][0] = batch[b][1] = make_uint4(0u, 0u, 0u, 0u);
+      if (live && f < n) {
+        int tt;
+        bool isk;
+        const uint8_t* from = reinterpret_cast<const uint8_t*>(row_at(p.q, p.q_stride, p.k, p.k_stride, tile, f, tt, isk));
+        batch[b][0] = *reinterpret_cast<const uint4*>(from + 16 * run0);
+        batch[b][1] = *reinterpret_cast<const uint4*>(from + 16 * run1);
+      }
+    }
+  };
+  auto turn_row = [&](int tile, int parity, int f, const uint4 (&in)[2]) {
+    float x[16];
+    unpack8<kBF16>(in[0], x);
+    unpack8<kBF16>(in[1], x + 8);
+    const bool there = live && f < tokens_of(tile) * rows;
+    int tt = 0;
+    bool isk = false;
+    const int64_t to = there ? row_at(p.q_out, p.q_out_stride, p.k_out, p.k_out_stride, tile, f, tt, isk) : 0;
+    if constexpr (kNorm) {                                  // the shuffles need the whole warp
       float ss = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss += x[i] * x[i];
+      for (int i = 0; i < 16; ++i) ss += x[i] * x[i];
 #pragma unroll
       for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      if (wp && live) {
+      const uint4* wp = static_cast<const uint4*>(isk ? p.k_weight : p.q_weight);
+      if (there && wp) {
         const float inv = rsqrtf(ss / float(p.head_dim) + p.eps);
-        float w[8];
-        unpack8<kBF16>(__ldg(reinterpret_cast<const uint4*>(wp) + sub), w);
+        float w[16];
+        unpack8<kBF16>(__ldg(wp + run0), w);
+        unpack8<kBF16>(__ldg(wp + run1), w + 8);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = x[i] * inv * w[i];
+        for (int i = 0; i < 16; ++i) x[i] = x[i] * inv * w[i];
       }
     }
-    float y[8];
+    if (!there || place[parity * p.tile + tt] < 0) return;  // (negative: a padding token)
+    const float* c = cosines + parity * num_angles + tt * half;
+    const float* s = sines + parity * num_angles + tt * half;
+    if constexpr (kInterleaved) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float other = kInterleaved ? x[i ^ 1] : __shfl_sync(0xffffffffu, x[i], partner);
-      y[i] = rotated ? x[i] * cs[i] + other * sn[i] : x[i];
+      for (int u = 0; u < 2; ++u) {
+        if (!(u ? turn1 : turn0)) continue;
+        const float4 cc = *reinterpret_cast<const float4*>(c + 4 * (u ? run1 : run0));
+        const float4 sv = *reinterpret_cast<const float4*>(s + 4 * (u ? run1 : run0));
+        const float cs[4] = {cc.x, cc.y, cc.z, cc.w}, sn[4] = {sv.x, sv.y, sv.z, sv.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float a = x[8 * u + 2 * i], b = x[8 * u + 2 * i + 1];
+          x[8 * u + 2 * i] = a * cs[i] - b * sn[i];
+          x[8 * u + 2 * i + 1] = b * cs[i] + a * sn[i];
+        }
+      }
+    } else if (turn0) {                                     // both runs or neither
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const float4 cc = *reinterpret_cast<const float4*>(c + u * (half / 2) + 4 * l);
+        const float4 sv = *reinterpret_cast<const float4*>(s + u * (half / 2) + 4 * l);
+        const float cs[4] = {cc.x, cc.y, cc.z, cc.w}, sn[4] = {sv.x, sv.y, sv.z, sv.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float a = x[4 * u + i], b = x[8 + 4 * u + i];
+          x[4 * u + i] = a * cs[i] - b * sn[i];
+          x[8 + 4 * u + i] = b * cs[i] + a * sn[i];
+        }
+      }
     }
-    if (live && r < rows) {
-      *reinterpret_cast<uint4*>((isk ? k_to : q_to) + int64_t(r) * row_bytes) =
-          make_uint4(pack2<kBF16>(y[0], y[1]), pack2<kBF16>(y[2], y[3]), pack2<kBF16>(y[4], y[5]),
-                     pack2<kBF16>(y[6], y[7]));
-    }
+    uint8_t* out = reinterpret_cast<uint8_t*>(to);
+    *reinterpret_cast<uint4*>(out + 16 * run0) = pack8<kBF16>(x);
+    *reinterpret_cast<uint4*>(out + 16 * run1) = pack8<kBF16>(x + 8);
   };
-  for (int n = 0, s = 0;;) {
-    // The next batch: of this token, or the first of the CTA's next one.
-    const bool token_ends = s + kRowsPerBatch >= rows;
-    const int64_t t_next = token_ends ? t + gridDim.x : t;
-    const int s_next = token_ends ? 0 : s + kRowsPerBatch;
-    const bool more = t_next < p.num_tokens;
-    uint4 next[kBatch];
-    int position_next = position;
-    if (more) {
-      load_batch(t_next, s_next, next);
-      if (token_ends) position_next = p.positions[t_next];
-    }
-    if (s == 0) {                                           // a token starts
-      __syncthreads();                                      // its angles are there; the token before last is done with
-      const float2* tn = turn[n & 1];
-      // This thread's rotation: element e of the half layout belongs to frequency e mod half, of the
-      // interleaved one to e / 2.
+
+  int tile = blockIdx.x, parity = 0;
+  uint4 batch[kBatch][2];
+  load_batch(tile, 0, batch);
+  if (int(threadIdx.x) < tokens_of(tile)) place[threadIdx.x] = p.positions[int64_t(tile) * p.tile + threadIdx.x];
+  __syncthreads();
+  work_angles_out(tile, 0);
+  while (true) {
+    __syncthreads();                                        // the tile's angles are there
+    const int next = tile + gridDim.x, n = tokens_of(tile) * rows;
+    const bool more = next < tiles;
+    int position = 0;
+    if (more && int(threadIdx.x) < tokens_of(next)) position = p.positions[int64_t(next) * p.tile + threadIdx.x];
+    for (int f = 0; f < n; f += kRowsPerStep) {
+      uint4 ahead[kBatch][2];
+      if (f + kRowsPerStep < n) load_batch(tile, f + kRowsPerStep, ahead);
+      else if (more) load_batch(next, 0, ahead);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int e = e0 + i;
-        const float2 cssn = rotated ? tn[kInterleaved ? e >> 1 : (e < half ? e : e - half)] : make_float2(1.f, 0.f);
-        const bool first = kInterleaved ? (i & 1) == 0 : e < half;
-        cs[i] = cssn.x;
-        sn[i] = first ? -cssn.y : cssn.y;
-      }
-    }
-    if (position >= 0) {                                    // else a padding token
-      uint8_t* q_to = p.q_out + 2 * (t * p.q_out_stride + e0);
-      uint8_t* k_to = p.k_out + 2 * (t * p.k_out_stride + e0) - k_back;
+      for (int b = 0; b < kBatch; ++b) turn_row(tile, parity, f + row_in_step + b * kRowsAtOnce, batch[b]);
 #pragma unroll
       for (int b = 0; b < kBatch; ++b) {
-        if (s + b * kRowsAtOnce >= rows) break;             // uniform over the CTA
-        rotate(q_to, k_to, s + row_in_step + b * kRowsAtOnce, batch[b]);
+        batch[b][0] = ahead[b][0];
+        batch[b][1] = ahead[b][1];
       }
     }
-    if (token_ends && more) angles(position_next, turn[(n + 1) & 1]);
     if (!more) break;
-    n += token_ends;
-    t = t_next;
-    s = s_next;
-    position = position_next;
-#pragma unroll
-    for (int b = 0; b < kBatch; ++b) batch[b] = next[b];
+    parity ^= 1;
+    if (int(threadIdx.x) < tokens_of(next)) place[parity * p.tile + threadIdx.x] = position;
+    __syncthreads();                                        // the positions are there
+    work_angles_out(next, parity);
+    tile = next;
   }
 }
 
+// Tokens of a tile: the fewest whose rows fill the threads' steps to nine tenths, as long as there are
+// tiles for every CTA and the angles fit.
+int tile_of(int num_tokens, int rows, int half, int lanes, int ctas) {
+  const int step = kBatch * kThreads / lanes;
+  const int most = std::min(std::min(kThreads, std::max(1, kMaxAngles / half)), (num_tokens - 1) / ctas + 1);
+  int best = 1;
+  double fill = 0;
+  for (int n = 1; n <= most && fill < 0.9; ++n) {
+    const double full = double(n) * rows / (double((int64_t(n) * rows - 1) / step + 1) * step);
+    if (full > fill) {
+      fill = full;
+      best = n;
+    }
+  }
+  return best;
+}
+
+template <bool kBF16, bool kInterleaved, int kLanes>
+cudaError_t launch(RotaryParams p, cudaStream_t s) {
+  const int ctas = num_sms() > 0 ? num_sms() * kCtasPerSm : 1024;
+  p.tile = tile_of(p.num_tokens, int(p.rows.d), int(p.half.d), kLanes, ctas);
+  const dim3 grid(std::min(ctas, (p.num_tokens - 1) / p.tile + 1)), block(kThreads);
+  const size_t smem = size_t(p.tile) * (4 * p.half.d * sizeof(float) + 2 * sizeof(int));   // at most 34 KB
+  return p.q_weight || p.k_weight
+             ? launch_pdl(qk_rotary_kernel<kBF16, kInterleaved, kLanes, true>, grid, block, smem, s, p)
+             : launch_pdl(qk_rotary_kernel<kBF16, kInterleaved, kLanes, false>, grid, block, smem, s, p);
+}
 template <bool kBF16, bool kInterleaved>
 cudaError_t launch(const RotaryParams& p, cudaStream_t s) {
-  const int most = num_sms() > 0 ? num_sms() * kCtasPerSm : 1024;
-  const dim3 grid(p.num_tokens < most ? p.num_tokens : most), block(kThreads);
-  if (p.head_dim <= 64) return launch_pdl(qk_rotary_kernel<kBF16, kInterleaved, 8>, grid, block, 0, s, p);
-  if (p.head_dim <= 128) return launch_pdl(qk_rotary_kernel<kBF16, kInterleaved, 16>, grid, block, 0, s, p);
-  return launch_pdl(qk_rotary_kernel<kBF16, kInterleaved, 32>, grid, block, 0, s, p);
+  if (p.head_dim <= 64) return launch<kBF16, kInterleaved, 4>(p, s);
+  if (p.head_dim <= 128) return launch<kBF16, kInterleaved, 8>(p, s);
+  return launch<kBF16, kInterleaved, 16>(p, s);
 }
 
 }  // namespace
@@ -245,7 +314,7 @@ pkv_status pkv_qk_rotary(void* q_out, const void* q, void* k_out, const void* k,
       (reinterpret_cast<uintptr_t>(table) & 7u))
     return PKV_ERR_INVALID_ARG;
   if ((q_weight || k_weight) && !(eps >= 0.f)) return PKV_ERR_INVALID_ARG;
-  RotaryParams p;
+  RotaryParams p = {.rows = Divisor(num_heads + num_kv_heads), .half = Divisor(rotary_dim / 2)};
   p.q_out = static_cast<uint8_t*>(q_out);
   p.q = static_cast<const uint8_t*>(q);
   p.k_out = static_cast<uint8_t*>(k_out);
@@ -260,7 +329,6 @@ pkv_status pkv_qk_rotary(void* q_out, const void* q, void* k_out, const void* k,
   p.k_weight = k_weight;
   p.num_tokens = num_tokens;
   p.num_heads = num_heads;
-  p.num_kv_heads = num_kv_heads;
   p.head_dim = head_dim;
   p.rotary_dim = rotary_dim;
   p.magnitude = magnitude;
