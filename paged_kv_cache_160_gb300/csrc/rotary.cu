@@ -125,8 +125,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) qk_rotary_kernel(const R
         int tt;
         bool isk;
         const uint8_t* from = reinterpret_cast<const uint8_t*>(row_at(p.q, p.q_stride, p.k, p.k_stride, tile, f, tt, isk));
-        batch[b][0] = *reinterpret_cast<const uint4*>(from + 16 * run0);
-        batch[b][1] = *reinterpret_cast<const uint4*>(from + 16 * run1);
+        batch[b][0] = __ldcs(reinterpret_cast<const uint4*>(from + 16 * run0));
+        batch[b][1] = __ldcs(reinterpret_cast<const uint4*>(from + 16 * run1));
       }
     }
   };
@@ -139,9 +139,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) qk_rotary_kernel(const R
     bool isk = false;
     const int64_t to = there ? row_at(p.q_out, p.q_out_stride, p.k_out, p.k_out_stride, tile, f, tt, isk) : 0;
     if constexpr (kNorm) {                                  // the shuffles need the whole warp
-      float ss = 0.f;
+      uint64_t ss2 = 0;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) ss += x[i] * x[i];
+      for (int i = 0; i < 16; i += 2) {
+        const uint64_t v = pack_f32x2(x[i], x[i + 1]);
+        ss2 = fma_f32x2(v, v, ss2);
+      }
+      float ss = lo_f32(ss2) + hi_f32(ss2);
 #pragma unroll
       for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
       const uint4* wp = static_cast<const uint4*>(isk ? p.k_weight : p.q_weight);
@@ -151,7 +155,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) qk_rotary_kernel(const R
         unpack8<kBF16>(__ldg(wp + run0), w);
         unpack8<kBF16>(__ldg(wp + run1), w + 8);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = x[i] * inv * w[i];
+        for (int i = 0; i < 16; i += 2) {
+          const uint64_t v = mul_f32x2(mul_f32x2(pack_f32x2(x[i], x[i + 1]), pack_f32x2(inv, inv)), pack_f32x2(w[i], w[i + 1]));
+          x[i] = lo_f32(v);
+          x[i + 1] = hi_f32(v);
+        }
       }
     }
     if (!there || place[parity * p.tile + tt] < 0) return;  // (negative: a padding token)
