@@ -596,7 +596,7 @@ struct MergeParams {
   int max_len;            // the decode call's length clamp
   int part_blocks;        // the decode call's tiles per partition (0: balanced split)
   int num_workers;        // the decode call's worker warps
-  int nan_through;        // a NaN sum gives NaN, not zeros
+  int wide;               // the decode over 4 bits: its split (workers_wide), and a NaN sum gives NaN, not zeros
 };
 
 constexpr int kMergeWarps = 8;
@@ -606,14 +606,18 @@ constexpr int kMergeWarps = 8;
 // Lane k fetches piece k's (m, l) while every lane fetches its 16-byte chunk of up to
 // kChunk pieces' rows; the weights come from warp reductions over the lanes, so the
 // loads of a block of 32 pieces overlap and no exponential sits between a load and the sum.
-template <int QT, int D>
+// kShared: a CTA's warps share one (segment, query head), every kMergeWarps-th block of pieces each; for few
+// segments of many pieces.  Two sequences of at most 19,682 tokens, one kv head, over 4 bits: 52 us with a warp
+// for each head, 17 with a CTA.
+template <int QT, int D, bool kShared>
 __global__ void __launch_bounds__(kMergeWarps * 32, 2) split_kv_merge_kernel(const MergeParams p) {
   constexpr int kLanesPerHead = D / 4;       // 16-byte chunks of one head's row
   constexpr int kHP = 32 / kLanesPerHead;    // rows per load instruction of the warp
   constexpr int kChunk = 16;                 // loads in flight per lane
   const int lane = threadIdx.x & 31;
   const int G = p.group;
-  const int64_t item = int64_t(blockIdx.x) * kMergeWarps + (threadIdx.x >> 5);
+  const int warp = threadIdx.x >> 5;
+  const int64_t item = kShared ? int64_t(blockIdx.x) : int64_t(blockIdx.x) * kMergeWarps + warp;
   const bool active = item < int64_t(p.num_segments) * G;
   const int seg = active ? int(item / G) : 0, hh = active ? int(item % G) : 0;
 
@@ -643,7 +647,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 2) split_kv_merge_kernel(con
       mine += __shfl_xor_sync(0xffffffffu, mine, o);
     }
     const int64_t units = int64_t(Hkv) * tot;
-    const int64_t W = min(int64_t(p.num_workers), units);
+    const int64_t W = p.wide && !PB ? workers_wide(units, p.num_workers, p.num_segments) : min(int64_t(p.num_workers), units);
     if (mine > 0 && W > 0) {
       const int64_t u0 = int64_t(Hkv) * pre + int64_t(h) * mine, u1 = u0 + mine - 1;
       w0 = int(((u0 + 1) * W - 1) / units);
@@ -657,7 +661,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 2) split_kv_merge_kernel(con
   auto slot_of = [&](int k) -> int64_t { return k == 0 ? 2 * int64_t(w0) + z : 2 * int64_t(w0 + k); };
   const int rsub = lane / kLanesPerHead, dof = (lane % kLanesPerHead) * 4;
   float M = -INFINITY, den = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int kb = 0; kb < np; kb += 32) {
+  for (int kb = kShared ? 32 * warp : 0; kb < np; kb += kShared ? 32 * kMergeWarps : 32) {
     const int nb = min(32, np - kb);
     float mk = -INFINITY, lk = 0.f;
     if (lane < nb) {
@@ -710,8 +714,28 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 2) split_kv_merge_kernel(con
       for (int o = kLanesPerHead; o < 32; o <<= 1) acc[e] += __shfl_xor_sync(0xffffffffu, acc[e], o);
     }
   }
+  if constexpr (kShared) {                   // join the warps' sums
+    __shared__ float m_of[kMergeWarps], den_of[kMergeWarps], acc_of[kMergeWarps][D];
+    if (lane == 0) {
+      m_of[warp] = M;
+      den_of[warp] = den;
+    }
+    if (rsub == 0) *reinterpret_cast<float4*>(&acc_of[warp][dof]) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    __syncthreads();
+    if (warp > 0) return;
+    float Mz = -INFINITY;
+    for (int j = 0; j < kMergeWarps; ++j) Mz = fmaxf(Mz, m_of[j]);
+    if (Mz == -INFINITY) Mz = 0.f;
+    den = acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
+    for (int j = 0; j < kMergeWarps; ++j) {
+      const float wj = fast_exp2(m_of[j] - Mz);
+      den += wj * den_of[j];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[e] += wj * acc_of[j][dof + e];
+    }
+  }
   if (rsub == 0) {
-    const float inv = den > 0.f || (p.nan_through && den != den) ? 1.f / den : 0.f;
+    const float inv = den > 0.f || (p.wide && den != den) ? 1.f / den : 0.f;
     const int64_t obase = (int64_t(seg) * G + hh) * D + dof;   // out[s][h * G + hh][:]
 #pragma unroll
     for (int e = 0; e < 4; ++e) store_out<QT>(p.out, obase + e, acc[e] * inv);
@@ -739,7 +763,7 @@ Layout layout(int group, int head_dim, int64_t slots) {
 
 }  // namespace
 
-pkv_status launch_merge(const DecodeParams& prm, bool q_bf16, int head_dim, bool nan_through, cudaStream_t stream) {
+pkv_status launch_merge(const DecodeParams& prm, bool q_bf16, int head_dim, bool wide, cudaStream_t stream) {
   MergeParams mp;
   mp.out = prm.out;
   mp.ml = prm.ml;
@@ -752,11 +776,17 @@ pkv_status launch_merge(const DecodeParams& prm, bool q_bf16, int head_dim, bool
   mp.max_len = prm.max_len;
   mp.part_blocks = prm.part_blocks;
   mp.num_workers = prm.num_workers;
-  mp.nan_through = nan_through;
+  mp.wide = wide;
   const int64_t items = int64_t(mp.num_segments) * mp.group;
-  const int mgrid = int((items + kMergeWarps - 1) / kMergeWarps);
-  auto kern = q_bf16 ? (head_dim == 128 ? split_kv_merge_kernel<KV_BF16, 128> : split_kv_merge_kernel<KV_BF16, 64>)
-                     : (head_dim == 128 ? split_kv_merge_kernel<KV_F16, 128> : split_kv_merge_kernel<KV_F16, 64>);
+  // A segment has num_workers / num_segments pieces on average, and the longest several times as many.
+  const bool shared = wide && prm.num_workers > 8 * int64_t(mp.num_segments);
+  const int mgrid = shared ? int(items) : int((items + kMergeWarps - 1) / kMergeWarps);
+  auto pick = [&](auto is_shared) {
+    constexpr bool kShared = decltype(is_shared)::value;
+    return q_bf16 ? (head_dim == 128 ? split_kv_merge_kernel<KV_BF16, 128, kShared> : split_kv_merge_kernel<KV_BF16, 64, kShared>)
+                  : (head_dim == 128 ? split_kv_merge_kernel<KV_F16, 128, kShared> : split_kv_merge_kernel<KV_F16, 64, kShared>);
+  };
+  auto kern = shared ? pick(std::true_type{}) : pick(std::false_type{});
   return launch_pdl(kern, dim3(mgrid), dim3(kMergeWarps * 32), 0, stream, mp) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 

@@ -177,8 +177,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) paged_decode_fp4_kernel(const 
   const int T = Hkv * cum_nb[S];
   const int U = Hkv * cum_np[S];
   const int nunits = PB ? U : T;
-  const int W = min(p.num_workers, nunits);
-  const int w = blockIdx.x * kWarps + warp;
+  const int W = PB ? min(p.num_workers, nunits) : workers_wide(nunits, p.num_workers, S * Hkv);
+  const int w = warp * gridDim.x + blockIdx.x;   // a few workers get an SM each
   if (w >= W) {                              // no tiles for this warp
     griddep_wait();
     if (!p.defer_dependents) griddep_launch_dependents();
