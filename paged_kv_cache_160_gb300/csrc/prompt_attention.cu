@@ -399,25 +399,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto write_rows = [&](const Item& it, int e, int hf, int quarter, uint8_t* area, const uint32_t (&o)[D / 4]) {
     const int row0 = e / G * kTile + 32 * quarter;
     if (row0 >= it.rows) return;
-    constexpr int kChunks = D / 16, kRowBytes = D;           // of a half row
+    constexpr int kChunks = D / 16, kRowBytes = D, kRowsPerStore = 32 / kChunks;   // of half rows
+    static_assert(kRowsPerStore <= C::kStageRows && kChunks * 16 == kRowBytes, "whole stores of a staged part");
     const uint32_t stage = smem_u32(area);
-    uint8_t* dst = p.out + (int64_t(it.q0) * p.out_stride + int64_t(it.h * G + e % G) * D + D / 2 * hf) * 2;
+    const int rr = lane % C::kStageRows, rsub = lane / kChunks, chunk = lane % kChunks;
+    const uint32_t put = stage + rr * kRowBytes, turn = rr & (kChunks - 1);
+    const int64_t step = p.out_stride * (2 * kRowsPerStore);
+    uint8_t* dst = p.out + ((int64_t(it.q0) + row0 + rsub) * p.out_stride + int64_t(it.h * G + e % G) * D + D / 2 * hf) * 2 + 16 * chunk;
+    int left = it.rows - row0 - rsub;
 #pragma unroll
     for (int k = 0; k < 32 / C::kStageRows; ++k) {
       if (lane / C::kStageRows == k) {
-        const int rr = lane % C::kStageRows;
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c)
-          sts128(stage + rr * kRowBytes + ((c ^ (rr & (kChunks - 1))) << 4), o[4 * c], o[4 * c + 1], o[4 * c + 2],
-                 o[4 * c + 3]);
+        for (int c = 0; c < kChunks; ++c) sts128(put + ((c ^ turn) << 4), o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
       }
       __syncwarp();
 #pragma unroll
-      for (int c0 = 0; c0 < C::kStageRows * kChunks; c0 += 32) {
-        const int c = (c0 + lane) % kChunks, rr = (c0 + lane) / kChunks, orow = row0 + C::kStageRows * k + rr;
-        if (orow < it.rows)
-          reinterpret_cast<uint4*>(dst + orow * p.out_stride * 2)[c] =
-              lds128(stage + rr * kRowBytes + ((c ^ (rr & (kChunks - 1))) << 4));
+      for (int u = 0; u < C::kStageRows / kRowsPerStore; ++u) {
+        const int from = u * kRowsPerStore + rsub;
+        const uint4 v = lds128(stage + from * kRowBytes + ((chunk ^ (from & (kChunks - 1))) << 4));
+        if (left > 0) *reinterpret_cast<uint4*>(dst) = v;
+        dst += step;
+        left -= kRowsPerStore;
       }
       __syncwarp();
     }
@@ -588,7 +591,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       l += xl[kTile * (hf ^ 1)];
       ok = ok && fine[x][meets & 1][hf ^ 1][quarter] != 0;   // both warps go on, or none
       ++meets;
-      const float inv = 1.f / l;                             // l = 0: a row without keys; NaN stays
       if constexpr (kSplit) {                                // the rows are finished below
         // m = -inf stands for no keys; a row whose scores are all NaN has some.
         if (hf == 0) part_ml[x][r] = make_float2(m == -INFINITY && l != 0.f ? 0.f : m, l);
@@ -597,19 +599,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool taken = *static_cast<volatile int*>(&masked_item[i % (2 * kItems)]) == int(i) + 1;
       uint32_t o[kODims / 2];
       if (nx > 0 && ok) {
+        float v[kODims];
 #pragma unroll
-        for (int cc = 0; cc < kODims / 32; ++cc) {
-          float v[32];
-          tmem_ld32(tO + 32 * cc, v);
-          tmem_wait_ld();
-          if (taken) give_back(it, row, hf, 32 * cc, v);
-#pragma unroll
-          for (int c = 0; c < 16; ++c)
-            o[16 * cc + c] = l == 0.f ? 0u : pack2<kBF16>(v[2 * c] * inv, v[2 * c + 1] * inv);
-        }
+        for (int cc = 0; cc < kODims / 32; ++cc) tmem_ld32(tO + 32 * cc, *reinterpret_cast<float(*)[32]>(v + 32 * cc));
+        tmem_wait_ld();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar_o_free[x]);          // the next item may overwrite O
+        if (taken) {
+#pragma unroll
+          for (int cc = 0; cc < kODims / 32; ++cc) give_back(it, row, hf, 32 * cc, *reinterpret_cast<float(*)[32]>(v + 32 * cc));
+        }
+        const float inv = l == 0.f ? 0.f : 1.f / l;          // l = 0: a row without keys, whose O is 0; NaN stays
+        const uint64_t inv2 = pack_f32x2(inv, inv);
+#pragma unroll
+        for (int c = 0; c < kODims / 2; ++c) {
+          const uint64_t y = mul_f32x2(pack_f32x2(v[2 * c], v[2 * c + 1]), inv2);
+          o[c] = pack2<kBF16>(lo_f32(y), hi_f32(y));
+        }
       } else {
 #pragma unroll
         for (int c = 0; c < kODims / 2; ++c) o[c] = 0u;
