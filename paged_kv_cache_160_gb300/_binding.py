@@ -244,13 +244,17 @@ def pkv_kv_read(k_out: torch.Tensor, v_out: torch.Tensor, cu_lens: torch.Tensor,
                 k_cache: torch.Tensor, v_cache: torch.Tensor, desc: CacheDesc, stream=None) -> None:
     """The cached rows of each sequence, dequantised, in order: rows cu_lens[i] .. cu_lens[i+1]-1 of k_out
     and v_out ([total_tokens, num_kv_heads, head_dim]) become positions 0 .. of sequence i."""
-    assert cu_lens.dtype == torch.int32 and block_tables.dtype == torch.int32
-    assert k_out.dtype == v_out.dtype and k_out.shape == v_out.shape
-    assert tuple(k_out.shape[1:]) == (desc.num_kv_heads, desc.head_dim) and block_tables.shape[0] == cu_lens.numel() - 1
-    _check(lib.pkv_kv_read(_dev(k_out, "k_out"), _dev(v_out, "v_out"), pkv_dtype_of(k_out), k_out.shape[0],
-                           _dev(cu_lens, "cu_lens"), cu_lens.numel() - 1, _dev(block_tables, "block_tables"),
-                           block_tables.shape[1], _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"),
-                           ctypes.byref(desc), _stream(stream)), "pkv_kv_read")
+    assert cu_lens.dtype is torch.int32 and block_tables.dtype is torch.int32
+    shape, num_seqs = k_out.shape, cu_lens.numel() - 1
+    assert k_out.dtype is v_out.dtype and v_out.shape == shape
+    total, heads, dim = shape
+    assert heads == desc.num_kv_heads and dim == desc.head_dim
+    tables, max_blocks = block_tables.shape
+    assert tables == num_seqs
+    _check(lib.pkv_kv_read(_dev(k_out, "k_out"), _dev(v_out, "v_out"), pkv_dtype_of(k_out), total,
+                           _dev(cu_lens, "cu_lens"), num_seqs, _dev(block_tables, "block_tables"), max_blocks,
+                           _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"), ctypes.byref(desc), _stream(stream)),
+           "pkv_kv_read")
 
 
 def pkv_copy_blocks(k_cache: torch.Tensor, v_cache: torch.Tensor, desc: CacheDesc, block_pairs: torch.Tensor,
@@ -374,13 +378,14 @@ def pkv_paged_prefill_chunk(out: torch.Tensor, q: torch.Tensor, cu_q_lens: torch
                                        _stream(stream)), "pkv_paged_prefill_chunk")
 
 
-def _rows(t: torch.Tensor, name: str, dtype: torch.dtype, rows: int, heads: int, dim: int) -> Tuple[int, int]:
+def _rows(t: torch.Tensor, name: str, dtype: torch.dtype, shape: torch.Size) -> Tuple[int, int]:
     """(address, elements from row to row) of a CUDA tensor [rows, heads, dim] whose rows are dense."""
-    if t.dtype is not dtype or t.shape != (rows, heads, dim):
-        raise ValueError(f"{name}: expected {dtype} [{rows}, {heads}, {dim}], got {t.dtype} {list(t.shape)}")
+    if t.dtype is not dtype or t.shape != shape:
+        raise ValueError(f"{name}: expected {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (libpkv has no CPU path)")
     s0, s1, s2 = t.stride()
+    rows, heads, dim = shape
     if (s2 != 1 and dim > 1) or (s1 != dim and heads > 1):
         raise ValueError(f"{name}: the heads of a row must lie next to each other")
     return t.data_ptr(), (s0 if rows > 1 else max(heads * dim, 8))
@@ -393,11 +398,14 @@ def pkv_prompt_attention(out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v:
     sequence i are its last positions; a row without keys gives zeros."""
     assert cu_q_lens.dtype == torch.int32 and cu_k_lens.dtype == torch.int32
     assert cu_q_lens.numel() == cu_k_lens.numel()
-    dt, (tq, hq, dim), (tk, hkv, _) = q.dtype, q.shape, k.shape
-    pq, sq = _rows(q, "q", dt, tq, hq, dim)
-    po, so = _rows(out, "out", dt, tq, hq, dim)
-    pk, sk = _rows(k, "k", dt, tk, hkv, dim)
-    pv, sv = _rows(v, "v", dt, tk, hkv, dim)
+    dt, qs, ks = q.dtype, q.shape, k.shape
+    (tq, hq, dim), (tk, hkv, kdim) = qs, ks
+    if kdim != dim:
+        raise ValueError(f"k: expected heads of {dim}, got {list(ks)}")
+    pq, sq = _rows(q, "q", dt, qs)
+    po, so = _rows(out, "out", dt, qs)
+    pk, sk = _rows(k, "k", dt, ks)
+    pv, sv = _rows(v, "v", dt, ks)
     _check(lib.pkv_prompt_attention(po, pq, pk, pv, pkv_dtype_of(q), _dev(cu_q_lens, "cu_q_lens"),
                                     _dev(cu_k_lens, "cu_k_lens"), cu_q_lens.numel() - 1, tq, tk, max_q_len, hq, hkv, dim,
                                     so, sq, sk, sv, scale, _stream(stream)), "pkv_prompt_attention")
@@ -419,15 +427,18 @@ def pkv_qk_rotary(q_out: torch.Tensor, q: torch.Tensor, k_out: torch.Tensor, k: 
                   stream=None) -> None:
     """Per-head RMS norm (with weights) and rotation by position of q [tokens, num_heads, head_dim] and k
     [tokens, num_kv_heads, head_dim] (any row stride); q_out is q and k_out is k works in place."""
-    assert positions.dtype == torch.int32 and table.dtype == torch.int64
-    dt, (n, hq, dim), hkv = q.dtype, q.shape, k.shape[1]
+    assert positions.dtype is torch.int32 and table.dtype is torch.int64
+    dt, qs, ks = q.dtype, q.shape, k.shape
+    (n, hq, dim), (nk, hkv, kdim) = qs, ks
+    if nk != n or kdim != dim:
+        raise ValueError(f"k: expected [{n}, num_kv_heads, {dim}], got {list(ks)}")
     assert positions.numel() == n
-    for w in (q_weight, k_weight):
-        assert w is None or (w.dtype is dt and w.numel() == dim)
-    qi, qis = _rows(q, "q", dt, n, hq, dim)
-    qo, qos = _rows(q_out, "q_out", dt, n, hq, dim)
-    ki, kis = _rows(k, "k", dt, n, hkv, dim)
-    ko, kos = _rows(k_out, "k_out", dt, n, hkv, dim)
+    assert q_weight is None or (q_weight.dtype is dt and q_weight.numel() == dim)
+    assert k_weight is None or (k_weight.dtype is dt and k_weight.numel() == dim)
+    qi, qis = _rows(q, "q", dt, qs)
+    ki, kis = _rows(k, "k", dt, ks)
+    qo, qos = (qi, qis) if q_out is q else _rows(q_out, "q_out", dt, qs)
+    ko, kos = (ki, kis) if k_out is k else _rows(k_out, "k_out", dt, ks)
     _check(lib.pkv_qk_rotary(qo, qi, ko, ki, pkv_dtype_of(q), n, hq, hkv, dim, qos, qis, kos, kis,
                              _dev(positions, "positions"), _dev(table, "table"), 2 * table.numel(),
                              ROPE_LAYOUT[layout], magnitude, _dev(q_weight, "q_weight"), _dev(k_weight, "k_weight"), eps,
