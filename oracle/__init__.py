@@ -17,6 +17,11 @@ What it computes, and where the method is stated:
                          arithmetic equals dense attention).
 * ``cache_ops``        — KV write into slots and copy-on-write block copies
                          (Lecture 33 §2.4; "PagedAttention ... virtual memory" §3.3).
+* ``fp4``              — the 4-bit cache: quantising to e2m1 codes with an e4m3 scale per 16
+                         elements, their values, and the tile layout (from the formats' definitions).
+* ``rotary``           — frequencies of rotary positions with their scalings, per-head RMS norm and
+                         rotation, with float64 sines.
+* ``prompt``           — causal attention of packed prompts over plain rows, dense in float64.
 * ``block_manager``    — free-block FIFO, ref_cnt, append/fork/CoW/free
                          ("PagedAttention ... virtual memory" §3.2–§3.3, Lecture 33 §2.4).
 * ``workload``         — the oracle's side of one synthetic step: planning on the model
