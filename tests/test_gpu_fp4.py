@@ -215,6 +215,11 @@ def test_read_back(lens, dim, heads, block, scaled, out):
         _close(o[:total], ref, u * np.abs(ref) * (1 + 2.0 ** -12) + 2.0 ** -25)
 
 
+@pytest.mark.parametrize("lens,heads,dim", [([9001, 3], 4, 128), ([20001], 2, 128), ([3000, 0, 801], 16, 64)])
+def test_read_back_of_many_rows(lens, heads, dim):
+    test_read_back(lens, dim, heads, 16, True, "bf16")
+
+
 def test_read_back_of_16_bit_and_e4m3_caches():
     import paged_kv_cache_160_gb300 as pkv
     rng = np.random.default_rng(8)
@@ -344,6 +349,13 @@ def test_decode_lengths(lens):
 @pytest.mark.parametrize("scale", [0.0, -0.1])
 def test_decode_with_a_zero_or_negative_scale(scale):
     _run_decode(RAGGED, 8, 2, 128, "bf16", seed=8, scale=scale)
+
+
+@pytest.mark.parametrize("lens,hq,hkv,dim", [([20000], 8, 1, 64), ([9001, 17], 4, 2, 128), ([0, 30001, 5], 3, 1, 128),
+                                            ([4099] * 9, 6, 3, 64)])
+def test_decode_of_few_long_sequences(lens, hq, hkv, dim):
+    """Fewer workers than warps, and merges that a CTA's warps share."""
+    _run_decode(lens, hq, hkv, dim, "bf16", seed=len(lens) + dim)
 
 
 def test_decode_large_batch_takes_the_four_warp_layout():

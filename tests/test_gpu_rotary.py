@@ -94,6 +94,17 @@ def test_head_counts(hq, hkv):
 
 
 @pytest.mark.parametrize("norm", [True, False])
+@pytest.mark.parametrize("tokens,hq,hkv,dim,rot,layout", [
+    (2500, 1, 1, 64, 64, "half"), (2501, 2, 1, 128, 32, "interleaved"), (3001, 5, 1, 256, 256, "half"),
+    (1400, 40, 8, 96, 80, "half"), (1399, 33, 8, 80, 80, "interleaved"), (457, 3, 1, 128, 128, "half")])
+def test_tiles_of_several_tokens(tokens, hq, hkv, dim, rot, layout, norm):
+    """More tokens than CTAs, few heads and many, padding tokens among them."""
+    g = np.random.default_rng(tokens + dim)
+    positions = np.where(g.random(tokens) < 0.1, -1, g.integers(0, 1 << 18, tokens)).tolist()
+    _run(tokens, hq, hkv, dim, rot, layout, "none", torch.bfloat16, norm, positions, in_place=norm, seed=3)
+
+
+@pytest.mark.parametrize("norm", [True, False])
 @pytest.mark.parametrize("layout", ["half", "interleaved"])
 def test_in_place_and_padding_tokens(layout, norm):
     _run(6, 5, 3, 96, 64, layout, "none", torch.float16, norm, [4, -1, 0, 300, -7, 12], in_place=True)
