@@ -4,15 +4,18 @@
 // pass over the keys in tiles of 128 with the running maximum m and sum l of the softmax (in units
 // of log2): P = 2^(s c - m), O = O 2^(m_old - m) + P V, out = O / l.
 //
-// GB300 design: a CTA holds two row blocks of 128 query rows that read the same keys, so every K/V
-// tile feeds 256 rows.  S = Q K^T and O += P V run on tcgen05 with S, P and O in tensor memory; Q, K
+// GB300 design: a CTA holds two row blocks of 128 rows that read the same keys, so every K/V tile feeds 256
+// rows: query rows of one head, or of all query heads of a kv head (Blocks).  S = Q K^T and O += P V run on tcgen05 with S, P and O in tensor memory; Q, K
 // and V arrive by TMA straight from the packed rows (any row stride).
 //
 // Bound: the tensor cores, and the exponentials beside them (a 128 x 128 tile is 16,384 of them, about as
 // many cycles of the special function units as of its two products).  Measured in a graph: 8192 tokens,
-// 32 heads over 8, D 128: 333 us, 1.65 PFLOP/s of causal pairs; 16 prompts of 64 to 2048 tokens, 28 heads
-// over 4: 218 us; 512 rows behind 3584 keys: 33 us.  The products alone, without a softmax, take 297 us of
+// 32 heads over 8, D 128: 322 us, 1.71 PFLOP/s of causal pairs; 16 prompts of 64 to 2048 tokens, 28 heads
+// over 4: 208 us; 512 rows behind 3584 keys: 33 us.  The products alone, without a softmax, take 297 us of
 // the first.
+#include <algorithm>
+#include <type_traits>
+
 #include "pkv_device.cuh"
 #include "pkv_host.h"
 
@@ -41,6 +44,7 @@ struct PromptParams {
   int num_kv_heads;
   float scale_log2;
   unsigned* err;
+  Divisor group;          // query heads per kv head
 };
 
 __device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t (&r)[16]) {
@@ -164,6 +168,15 @@ struct Item {
   bool live;              // there are such rows
 };
 
+// What a row block holds: 128 rows of one query head; or, packed, `rows` rows of all G query heads of a kv head,
+// block row i being row i / G of head i mod G.  Blocks are numbered query tile by query tile, its heads inside.
+struct Blocks {
+  int rows;               // query rows of a block
+  int per_tile;           // blocks of the same rows
+  __host__ __device__ Blocks(bool packed, int G) : rows(packed ? kTile / G : kTile), per_tile(packed ? 1 : G) {}
+  __device__ __forceinline__ int first_row(int e) const { return e / per_tile * rows; }
+};
+
 // A sequence: its rows, or none of them where the lengths are inconsistent.
 struct Seq {
   int q0, k0, Lq, Lk, rows;
@@ -177,14 +190,12 @@ struct Seq {
     rows = bad ? 0 : min(Lq, p.max_q_len);
   }
   // Items of one of its kv heads: two row blocks each.
-  __device__ __forceinline__ int items(int G) const { return ((rows + kTile - 1) / kTile * G + 1) / 2; }
+  __device__ __forceinline__ int items(const Blocks& b) const { return ((rows + b.rows - 1) / b.rows * b.per_tile + 1) / 2; }
 };
 
-// The item of a sequence's kv head h with row blocks 2 * level and 2 * level + 1.  The blocks of a
-// (sequence, kv head) are numbered query tile by query tile, its query heads inside a tile.
-__device__ __forceinline__ Item item_at(const PromptParams& p, int h, int s, int level) {
+// The item of a sequence's kv head h with row blocks 2 * level and 2 * level + 1.
+__device__ __forceinline__ Item item_at(const PromptParams& p, const Blocks& blocks, int h, int s, int level) {
   const Seq q(p, s);
-  const int G = p.num_heads / p.num_kv_heads;
   Item it;
   it.h = h;
   it.q0 = q.q0;
@@ -193,19 +204,19 @@ __device__ __forceinline__ Item item_at(const PromptParams& p, int h, int s, int
   it.Lk = q.Lk;
   it.rows = q.rows;
   it.e0 = 2 * level;
-  it.live = unsigned(level) < unsigned(q.items(G));
+  it.live = unsigned(level) < unsigned(q.items(blocks));
   // Key tiles that the rows of block e attend (0: none, or no such rows).
   auto tiles_of = [&](int e) -> int {
-    const int r0 = e / G * kTile;
+    const int r0 = blocks.first_row(e);
     if (r0 >= it.rows) return 0;
-    const int keys = min(it.Lq, r0 + kTile) + it.Lk - it.Lq;
+    const int keys = min(it.Lq, r0 + blocks.rows) + it.Lk - it.Lq;
     return keys > 0 ? (keys + kTile - 1) / kTile : 0;
   };
   it.na = it.live ? tiles_of(it.e0) : 0;
   it.nb = it.live ? tiles_of(it.e0 + 1) : 0;
   it.n = max(it.na, it.nb);
   it.t0 = 0;
-  it.masked = max(0, it.e0 / G * kTile + it.Lk - it.Lq + 1) / kTile;   // the earlier block's first row decides
+  it.masked = max(0, blocks.first_row(it.e0) + it.Lk - it.Lq + 1) / kTile;   // the earlier block's first row decides
   return it;
 }
 
@@ -239,16 +250,17 @@ constexpr int kSeqChunk = 32;                                // sequences per en
 // keys come first.  Shorter sequences' indexes have nothing to do.
 //   Sequence by sequence (compact 1), where those would be too many: x counts kv heads, then a sequence's
 // levels down, then sequences; `first` holds the number of every kSeqChunk-th sequence's first item.
-__device__ __forceinline__ Item item_of(const PromptParams& p, int x, int y, int z, int nz, const int* first, int lane) {
-  if (!p.compact) return item_at(p, x, y, nz - 1 - z);
-  const int h = x % p.num_kv_heads, j = x / p.num_kv_heads, G = p.num_heads / p.num_kv_heads;
+__device__ __forceinline__ Item item_of(const PromptParams& p, const Blocks& blocks, int x, int y, int z, int nz,
+                                        const int* first, int lane) {
+  if (!p.compact) return item_at(p, blocks, x, y, nz - 1 - z);
+  const int h = x % p.num_kv_heads, j = x / p.num_kv_heads;
   int lo = 0, hi = (p.num_seqs + kSeqChunk - 1) / kSeqChunk; // the chunk of item j: first[lo] <= j < first[hi]
   if (j >= first[hi]) return Item{};
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (first[mid] <= j) lo = mid; else hi = mid;
   }
-  const int s = lo * kSeqChunk + lane, mine = s < p.num_seqs ? Seq(p, s).items(G) : 0;
+  const int s = lo * kSeqChunk + lane, mine = s < p.num_seqs ? Seq(p, s).items(blocks) : 0;
   int sum = mine;                                            // inclusive scan over the chunk
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -260,7 +272,7 @@ __device__ __forceinline__ Item item_of(const PromptParams& p, int x, int y, int
   if (past == 0) return Item{};                              // (lengths that contradict one another)
   const int l = __ffs(past) - 1;
   const int before = __shfl_sync(0xffffffffu, sum - mine, l), count = __shfl_sync(0xffffffffu, mine, l);
-  return item_at(p, h, lo * kSeqChunk + l, count - 1 - (rest - before));
+  return item_at(p, blocks, h, lo * kSeqChunk + l, count - 1 - (rest - before));
 }
 
 // Part `part` of `parts` of an item's key tiles.
@@ -291,7 +303,7 @@ __device__ __forceinline__ void copy_to_cta(uint32_t dst, uint32_t src, uint32_t
 // blocks, or 64 rows of one.  The others send it those rows, unnormalised, with their maxima and sums, by
 // bulk copies from their idle K/V stages to its idle Q area (and the place of its own rows).  Reading
 // them from the other CTA's shared memory with loads took 14 us instead.
-template <bool kBF16, int D, bool kSplit>
+template <bool kBF16, int D, bool kSplit, bool kPacked>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                   const __grid_constant__ CUtensorMap tmv, const PromptParams p) {
@@ -363,7 +375,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // Only the set-up above may run before the previous kernel on the stream has finished.
   griddep_wait();
-  const int G = p.num_heads / p.num_kv_heads;
+  const int G = int(p.group.d);
+  const Blocks blocks(kPacked, G);
   auto all = [](bool v) -> bool { return __all_sync(0xffffffffu, v); };
   // Item number i, once its barrier's phase is complete; na = -1: there is none.
   auto read_item = [&](uint32_t i) -> Item {
@@ -392,21 +405,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     return it;
   };
   auto wait_item = [&](uint32_t i) -> bool { return all(mbar_wait(&bar_item[i % kItems], i / kItems & 1u)); };
+  // Block e's rows that exist, and the query row of block row r.
+  auto rows_of = [&](const Item& it, int e) -> int {
+    const int rows = it.rows - blocks.first_row(e);
+    return kPacked ? min(rows, blocks.rows) * G : min(rows, kTile);
+  };
+  auto query_row = [&](int e, int r) -> int { return blocks.first_row(e) + (kPacked ? int(p.group.quotient(r)) : r); };
   // Writes a warp's 32 half rows of block e, one per lane as 16-bit pairs: kStageRows at a time through
   // the warp's own staging area (16-byte chunk c of row rr at c ^ rr against bank conflicts), so that the
   // warp writes whole runs.  (Straight from the registers a store touches 32 lines; 16 packed prompts took
   // 227 us that way, 218 with this.)
   auto write_rows = [&](const Item& it, int e, int hf, int quarter, uint8_t* area, const uint32_t (&o)[D / 4]) {
-    const int row0 = e / G * kTile + 32 * quarter;
-    if (row0 >= it.rows) return;
+    int left = rows_of(it, e) - 32 * quarter;                // of the block's rows, from the warp's first on
+    if (left <= 0) return;
     constexpr int kChunks = D / 16, kRowBytes = D, kRowsPerStore = 32 / kChunks;   // of half rows
     static_assert(kRowsPerStore <= C::kStageRows && kChunks * 16 == kRowBytes, "whole stores of a staged part");
     const uint32_t stage = smem_u32(area);
     const int rr = lane % C::kStageRows, rsub = lane / kChunks, chunk = lane % kChunks;
     const uint32_t put = stage + rr * kRowBytes, turn = rr & (kChunks - 1);
     const int64_t step = p.out_stride * (2 * kRowsPerStore);
-    uint8_t* dst = p.out + ((int64_t(it.q0) + row0 + rsub) * p.out_stride + int64_t(it.h * G + e % G) * D + D / 2 * hf) * 2 + 16 * chunk;
-    int left = it.rows - row0 - rsub;
+    uint8_t* dst = p.out + ((int64_t(it.q0) + blocks.first_row(e)) * p.out_stride + int64_t(it.h * G) * D + D / 2 * hf) * 2 + 16 * chunk;
+    if (!kPacked) dst += ((32 * quarter + rsub) * p.out_stride + int64_t(e % G) * D) * 2;
+    left -= rsub;
 #pragma unroll
     for (int k = 0; k < 32 / C::kStageRows; ++k) {
       if (lane / C::kStageRows == k) {
@@ -418,8 +438,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int u = 0; u < C::kStageRows / kRowsPerStore; ++u) {
         const int from = u * kRowsPerStore + rsub;
         const uint4 v = lds128(stage + from * kRowBytes + ((chunk ^ (from & (kChunks - 1))) << 4));
-        if (left > 0) *reinterpret_cast<uint4*>(dst) = v;
-        dst += step;
+        if constexpr (kPacked) {
+          const int i = 32 * quarter + k * C::kStageRows + from, row = int(p.group.quotient(i));
+          if (left > 0) *reinterpret_cast<uint4*>(dst + (row * p.out_stride + int64_t(i - row * G) * D) * 2) = v;
+        } else {
+          if (left > 0) *reinterpret_cast<uint4*>(dst) = v;
+          dst += step;
+        }
         left -= kRowsPerStore;
       }
       __syncwarp();
@@ -443,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int chunks = (p.num_seqs + kSeqChunk - 1) / kSeqChunk;
       for (int c = threadIdx.x; c < chunks; c += kThreads) {
         int sum = 0;
-        for (int s = c * kSeqChunk; s < min(p.num_seqs, (c + 1) * kSeqChunk); ++s) sum += Seq(p, s).items(G);
+        for (int s = c * kSeqChunk; s < min(p.num_seqs, (c + 1) * kSeqChunk); ++s) sum += Seq(p, s).items(blocks);
         first_item[c + 1] = sum;
       }
       __syncthreads();
@@ -465,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   auto this_item = [&]() -> Item {
-    Item it = item_of(p, bx, by, bz, gridDim.z, first_item, lane);
+    Item it = item_of(p, blocks, bx, by, bz, gridDim.z, first_item, lane);
     if constexpr (kSplit) take_part(it, part, parts);
     return it;
   };
@@ -502,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (uint32_t i = 0; ok; ++i) {
       const Item it = take_item(i);
       if (it.na < 0) break;
-      const int e = it.e0 + x, row0 = e / G * kTile, row = row0 + r, shift = it.Lk - it.Lq;
+      const int e = it.e0 + x, row = query_row(e, r), shift = it.Lk - it.Lq;
       const int nx = x == 0 ? it.na : it.nb;
       float m = -INFINITY, l = 0.f;                          // m of the row, l of this thread's keys
       for (int t = 0; t < nx; ++t, ++meets) {
@@ -648,10 +673,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = ok && all(q_of[x] == 0 || mbar_wait(&bar_q_empty[x], (q_of[x] - 1) & 1u));
           if (!ok) return;
           if (lane == 0) {
-            mbar_arrive_expect_tx(&bar_q[x], C::kTileBytes);
+            mbar_arrive_expect_tx(&bar_q[x], kPacked ? blocks.rows * G * D * 2 : C::kTileBytes);
             const int e = it.e0 + x;
             for (int d = 0; d < D / 64; ++d)
-              tma_load_3d(sQ + x * C::kTileBytes + d * kHalfBytes, &tmq, &bar_q[x], 64 * d, it.h * G + e % G, it.q0 + e / G * kTile, pol_q);
+              tma_load_3d(sQ + x * C::kTileBytes + d * kHalfBytes, &tmq, &bar_q[x], 64 * d, it.h * G + (kPacked ? 0 : e % G), it.q0 + blocks.first_row(e), pol_q);
           }
           ++q_of[x];
         };
@@ -859,8 +884,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kHalf = 2 * D;
     const int share = 2 * kTile / parts;                     // 128 or 64 rows
     auto rows_in = [&](int owner) -> int {                   // rows of a share that exist
-      const int e = it.e0 + owner * share / kTile, first = e / G * kTile + owner * share % kTile;
-      return min(share, max(0, it.rows - first));
+      return min(share, max(0, rows_of(it, it.e0 + owner * share / kTile) - owner * share % kTile));
     };
     if (threadIdx.x == 0)
       mbar_arrive_expect_tx(&bar_recv, (parts - 1) * (rows_in(part) * 2 * kHalf + share * int(sizeof(float2))));
@@ -874,7 +898,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       static_assert(kTile * 2 * kHalf <= 2 * C::kTileBytes, "a share of 128 rows, or two of 64, fit in the Q area");
       const int owner = (x * kTile + 32 * quarter) / share, rr = (x * kTile + r) % share;   // rr: row of the share
       const bool any = (x == 0 ? it.na : it.nb) > 0, taken = masked_item[0] != 0;
-      const int orow = (it.e0 + x) / G * kTile + r;
+      const int orow = query_row(it.e0 + x, r);
       const uint32_t tO = tmem + (uint32_t(32 * quarter) << 16) + 256 + 128 * x + kODims * hf;
       // Share s of this CTA's rows: [hf][row][kHalf], at 2 * share * kHalf * s in the stages.  What CTA
       // `from` sends to CTA `to` lands in its slot (from - to - 1) mod parts: slots 0 (and 1) in the Q area,
@@ -978,14 +1002,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Clusters of `parts` CTAs of the split kernel that the current device holds at once (0 on failure).
-template <bool kBF16, int D>
+template <bool kBF16, int D, bool kPacked>
 int clusters_at_once(int parts) {
   static thread_local int cached_dev = -1;
   static thread_local int cached[2];                         // parts 2 and 4
   const int dev = current_device();
   if (dev < 0) return 0;
   if (dev != cached_dev) {                                   // looked up once per device and thread
-    auto kern = prompt_kernel<kBF16, D, true>;
+    auto kern = prompt_kernel<kBF16, D, true, kPacked>;
     for (int i = 0; i < 2; ++i) {
       cudaLaunchConfig_t cfg = {};
       cfg.gridDim = dim3(2 << i);
@@ -1010,32 +1034,32 @@ int clusters_at_once(int parts) {
 // One item walks its keys alone unless there are so few items that clusters of 2 or 4 CTAs for each still
 // run at once and every part has two key tiles or more (by the sequences' mean length).  A chunk of 512
 // rows after 3584 keys (56 items): 49.5 us alone, 33.0 us in clusters of 2; one row of 32 heads over 4096
-// keys (16 items): 48.1 us alone, 19.4 us in clusters of 4.
-template <bool kBF16, int D>
+// keys (16 items, a head per block): 48.1 us alone, 19.4 us in clusters of 4 (17.3 with all heads in a block).
+template <bool kBF16, int D, bool kPacked>
 pkv_status launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PromptParams& prm,
                   int num_seqs, int max_q_len, cudaStream_t stream) {
   using C = Cfg<D>;
-  const unsigned groups = (unsigned((max_q_len - 1) / kTile + 1) * unsigned(prm.num_heads / prm.num_kv_heads) + 1) / 2;
-  const int64_t items = int64_t(groups) * num_seqs * prm.num_kv_heads;
+  const Blocks blocks(kPacked, prm.num_heads / prm.num_kv_heads);
+  const int64_t groups = ((int64_t(max_q_len) - 1) / blocks.rows * blocks.per_tile + blocks.per_tile + 1) / 2;
+  const int64_t items = groups * num_seqs * prm.num_kv_heads;
   // Items that the sequences have at most, whatever their lengths.
-  const int64_t G = prm.num_heads / prm.num_kv_heads;
-  const int64_t most = ((int64_t(prm.total_q) / kTile + num_seqs + 1) * G / 2 + num_seqs) * prm.num_kv_heads;
+  const int64_t most = ((int64_t(prm.total_q) / blocks.rows + num_seqs + 1) * blocks.per_tile / 2 + num_seqs) * prm.num_kv_heads;
   const int64_t mean_tiles = (int64_t(prm.total_k) / num_seqs + kTile - 1) / kTile;
   int parts = 1;
-  while (parts < 4 && mean_tiles >= 4 * parts && items <= clusters_at_once<kBF16, D>(2 * parts)) parts *= 2;
+  while (parts < 4 && mean_tiles >= 4 * parts && items <= clusters_at_once<kBF16, D, kPacked>(2 * parts)) parts *= 2;
   // Numbering the items level by level starts the long ones first, but has an index for every sequence
   // at every level of the longest one; past twice the items that there can be, or past what a grid
   // holds, they are numbered sequence by sequence.  One prompt of 8192 tokens among 255 of 32 (32 heads
-  // over 8): 2347 us level by level, 513 us by sequence; 16 prompts of 64 to 2048 tokens: 226 us and 240 us.
+  // over 8, a head per block): 2347 us level by level, 513 us by sequence; 16 prompts of 64 to 2048 tokens: 226 us and 240 us.
   const bool compact = parts == 1 && (items > 2 * most || groups > 65535);
   if (compact && most > 0x7fffffff) return PKV_ERR_UNSUPPORTED;
   PromptParams params = prm;
   params.compact = compact;
-  auto kern = parts > 1 ? prompt_kernel<kBF16, D, true> : prompt_kernel<kBF16, D, false>;
+  auto kern = parts > 1 ? prompt_kernel<kBF16, D, true, kPacked> : prompt_kernel<kBF16, D, false, kPacked>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
     return PKV_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = compact ? dim3(unsigned(most)) : dim3(unsigned(prm.num_kv_heads) * parts, num_seqs, groups);
+  cfg.gridDim = compact ? dim3(unsigned(most)) : dim3(unsigned(prm.num_kv_heads) * parts, num_seqs, unsigned(groups));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = stream;
@@ -1084,17 +1108,27 @@ extern "C" pkv_status pkv_prompt_attention(void* out, const void* q, const void*
     return PKV_ERR_INVALID_ARG;
   unsigned* err = error_word_ptr();
   if (!err) return PKV_ERR_CUDA;
-  // Rows as (dims, heads, rows): a box is 64 dims of one head of 128 rows.
-  auto encode = [&](CUtensorMap* m, const void* base, int heads, int rows, int64_t stride) {
+  // The heads of a kv head share a block unless that takes more than a sixteenth more blocks at the mean
+  // length (groups that fill 128 rows badly).  Short sequences then need a fraction of the blocks, and the
+  // causal border cuts off more of a block of fewer query rows.  32 sequences of 8 rows over 2048 keys, 28
+  // heads over 4: 27.6 us, 99.1 with a head per block; 16 prompts of 64 to 2048 tokens: 208 us and 215; one
+  // of 8192, 32 heads over 8: 322 us and 330.
+  const int G = num_heads / num_kv_heads, mean = (total_q - 1) / num_seqs + 1;
+  const Blocks together(true, std::min(G, kTile)), apart(false, G);
+  const bool packed = G > 1 && G <= kTile &&
+                      16 * int64_t((mean - 1) / together.rows + 1) <= 17 * int64_t((mean - 1) / kTile + 1) * G;
+  // Rows as (dims, heads, rows): a box is 64 dims of a block's rows.
+  auto encode = [&](CUtensorMap* m, const void* base, int heads, int rows, int64_t stride, const Blocks& box) {
     return encode_tmap_3d(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, base, uint64_t(head_dim), uint64_t(heads), uint64_t(rows),
-                          uint64_t(head_dim) * 2, uint64_t(stride) * 2, 64, 1, kTile,
+                          uint64_t(head_dim) * 2, uint64_t(stride) * 2, 64, box.rows == kTile ? 1 : G, box.rows,
                           CU_TENSOR_MAP_SWIZZLE_128B);
   };
   CUtensorMap tq, tk = {}, tv = {};
-  if (!encode(&tq, q, num_heads, total_q, q_stride)) return PKV_ERR_CUDA;
-  if (total_k > 0 && (!encode(&tk, k, num_kv_heads, total_k, k_stride) || !encode(&tv, v, num_kv_heads, total_k, v_stride)))
+  if (!encode(&tq, q, num_heads, total_q, q_stride, packed ? together : apart)) return PKV_ERR_CUDA;
+  if (total_k > 0 && (!encode(&tk, k, num_kv_heads, total_k, k_stride, apart) ||
+                      !encode(&tv, v, num_kv_heads, total_k, v_stride, apart)))
     return PKV_ERR_CUDA;
-  PromptParams prm;
+  PromptParams prm = {.group = Divisor(G)};
   prm.out = static_cast<uint8_t*>(out);
   prm.cu_q = cu_q_lens;
   prm.cu_k = cu_k_lens;
@@ -1111,9 +1145,13 @@ extern "C" pkv_status pkv_prompt_attention(void* out, const void* q, const void*
   prm.scale_log2 = scale * 1.4426950408889634f;
   prm.err = err;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (dtype == PKV_BF16)
-    return head_dim == 128 ? launch<true, 128>(tq, tk, tv, prm, num_seqs, max_q_len, s)
-                           : launch<true, 64>(tq, tk, tv, prm, num_seqs, max_q_len, s);
-  return head_dim == 128 ? launch<false, 128>(tq, tk, tv, prm, num_seqs, max_q_len, s)
-                         : launch<false, 64>(tq, tk, tv, prm, num_seqs, max_q_len, s);
+  auto run = [&](auto is_packed) -> pkv_status {
+    constexpr bool kPacked = decltype(is_packed)::value;
+    if (dtype == PKV_BF16)
+      return head_dim == 128 ? launch<true, 128, kPacked>(tq, tk, tv, prm, num_seqs, max_q_len, s)
+                             : launch<true, 64, kPacked>(tq, tk, tv, prm, num_seqs, max_q_len, s);
+    return head_dim == 128 ? launch<false, 128, kPacked>(tq, tk, tv, prm, num_seqs, max_q_len, s)
+                           : launch<false, 64, kPacked>(tq, tk, tv, prm, num_seqs, max_q_len, s);
+  };
+  return packed ? run(std::true_type{}) : run(std::false_type{});
 }

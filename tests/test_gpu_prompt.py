@@ -276,3 +276,17 @@ def test_captured_and_replayed():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, eager)
+
+
+@pytest.mark.parametrize("hq,hkv,dim", [(4, 1, 128), (7, 1, 128), (6, 2, 64), (28, 4, 128), (5, 1, 64), (40, 2, 128), (128, 1, 64),
+                                        (131, 1, 128)])
+@pytest.mark.parametrize("q_lens,k_lens", [([1, 2, 17, 18, 19, 0, 25], [40, 2, 17, 300, 129, 5, 20]), ([8] * 6, [700] * 6),
+                                           ([1], [2049]), ([33, 70, 64], [33, 70, 200])])
+def test_short_sequences_share_blocks_between_heads(q_lens, k_lens, hq, hkv, dim):
+    """Few rows per sequence: a block holds them for all query heads of a kv head, whatever their number."""
+    _run(q_lens, k_lens, hq, hkv, dim, "bf16", seed=hq + len(q_lens))
+
+
+def test_blocks_shared_between_heads_in_rows_of_a_packed_projection():
+    lens = [20, 1, 33, 7]
+    _run(lens, lens, 14, 2, 128, "f16", packed=True, pad=3)
