@@ -111,3 +111,76 @@ def test_prompt_chunk_and_decode_steps(dim, hq, hkv, block, dtype):
         # scores of normed rows: scale * sum |q k| < 32, as for the decode's own tests
         _close(out, ref, 2.0 ** -10 * size + u * np.abs(ref) + 2.0 ** -25)
     assert pkv.pkv_get_device_error() == 0
+
+
+def test_blocks_past_4_gib_of_a_pool():
+    """Written, read back and decoded at the end of a pool of more than 2^32 bytes, as in a small pool."""
+    import paged_kv_cache_160_gb300 as pkv
+    heads, dim, lens = 8, 128, [40, 100]
+    g = torch.Generator().manual_seed(7)
+    rows = [torch.randn((sum(lens), heads, dim), generator=g).to(torch.bfloat16).cuda() for _ in range(2)]
+    q = torch.randn((2, 4 * heads, dim), generator=g).to(torch.bfloat16).cuda()
+    need = [-(-n // 16) for n in lens]
+    cu = torch.tensor([0, *np.cumsum(lens)], dtype=torch.int32, device="cuda")
+    results = []
+    for nb in (sum(need), 480_000):
+        pools = [torch.zeros(pkv.fp4_cache_shape(nb, heads, 16, dim), dtype=torch.uint8, device="cuda") for _ in range(2)]
+        assert nb < 1000 or pools[0].numel() > 2 ** 32
+        ids = list(range(nb - sum(need), nb))
+        table = np.full((2, max(need)), -1, dtype=np.int32)
+        for i, n in enumerate(need):
+            table[i, :n] = [ids.pop() for _ in range(n)]
+        slots = np.concatenate([table[i, np.arange(n) // 16].astype(np.int64) * 16 + np.arange(n) % 16
+                                for i, n in enumerate(lens)])
+        desc, tables = pkv.cache_desc_fp4(pools[0]), torch.from_numpy(table).cuda()
+        pkv.pkv_kv_write(*rows, torch.from_numpy(slots).cuda(), *pools, desc)
+        back = [torch.zeros_like(rows[0]) for _ in range(2)]
+        pkv.pkv_kv_read(*back, cu, tables, *pools, desc)
+        out = torch.zeros_like(q)
+        ws = torch.empty(pkv.pkv_decode_workspace_bytes(2, 4 * heads, heads, dim, 16, max(lens), 0), dtype=torch.uint8,
+                         device="cuda")
+        pkv.pkv_paged_decode(out, q, *pools, desc, tables, torch.tensor(lens, dtype=torch.int32, device="cuda"), max(lens),
+                             0.09, 0, ws)
+        assert pkv.pkv_get_device_error() == 0
+        results.append([*back, out])
+        del pools
+    assert results[0][0].abs().sum() > 0 and results[0][2].abs().sum() > 0
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
+
+
+def test_two_streams_at_once():
+    """The same calls on two streams, with their own tensors, give what they give one after the other."""
+    import paged_kv_cache_160_gb300 as pkv
+    table = pkv.pkv_rope_table(128).cuda()
+
+    def inputs(seed, lens):
+        g = torch.Generator().manual_seed(seed)
+        qkv = torch.randn((sum(lens), 12, 128), generator=g).to(torch.bfloat16).cuda()
+        cu = torch.tensor([0, *np.cumsum(lens)], dtype=torch.int32, device="cuda")
+        pos = torch.cat([torch.arange(n) for n in lens]).to(torch.int32).cuda()
+        return qkv, cu, pos, max(lens)
+
+    def step(x):
+        qkv, cu, pos, longest = x
+        q, k, v = (t.clone() for t in qkv.split([8, 2, 2], 1))
+        pkv.pkv_qk_rotary(q, q, k, k, pos, table)
+        out = torch.zeros_like(q)
+        pkv.pkv_prompt_attention(out, q, k, v, cu, cu, longest, 0.09)
+        return q, k, out
+
+    # many items on one stream, few with split keys on the other
+    sides = [inputs(1, [700, 30, 1, 513]), inputs(2, [1100])]
+    alone = [step(x) for x in sides]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sides]
+    together = [[], []]
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                together[i].append(step(sides[i]))
+    torch.cuda.synchronize()
+    assert pkv.pkv_get_device_error() == 0
+    for want, runs in zip(alone, together):
+        for got in runs:
+            assert all(torch.equal(a, b) for a, b in zip(want, got))
