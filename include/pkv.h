@@ -210,7 +210,8 @@ PKV_API size_t pkv_decode_workspace_bytes(int num_seqs, int num_heads, int num_k
  * them in place over the host link, so a serving loop needs no separate copies.  The caches
  * and the workspace must be device memory.
  * Supported: kv f16/bf16 with the same q dtype, or e4m3 (head_dim 128) or 4-bit kv with f16/bf16 q
- * (both compute in fp16, so |q| must stay below 65504); head_dim 64/128; block_size 16 or 32;
+ * (e4m3: q is taken as fp16, so bf16 |q| must stay below 65504 and loses bits below 2^-14; 4-bit: bf16
+ * q of any size, each row times a power of two of its own); head_dim 64/128; block_size 16 or 32;
  * num_heads / num_kv_heads in 1..8; num_kv_heads * num_seqs * ceil(L_max / 16) < 2^31, where
  * L_max = min(max_context_len, max_blocks_per_seq * block_size) (else PKV_ERR_UNSUPPORTED).
  * Launch order: the decode kernel is launched as a programmatic dependent of the previous

@@ -495,3 +495,52 @@ def test_write_read_decode_captured_and_replayed():
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip((out, ko, vo), eager))
     assert pkv.pkv_get_device_error() == 0
+
+
+@pytest.mark.parametrize("dim,dtype,exponent", [(128, "bf16", -20), (64, "bf16", -20), (128, "f16", -20), (128, "bf16", -118),
+                                                (64, "bf16", 20), (128, "bf16", 100)])
+def test_decode_of_queries_far_below_and_above_one(dim, dtype, exponent):
+    """Queries of size 2^exponent under head scales of the inverse size: scores of ordinary size.  Half of the query
+    heads are another 2^-9 smaller."""
+    import paged_kv_cache_160_gb300 as pkv
+    lens, hq, hkv = RAGGED + [3000], 8, 2
+    rng, table, pools, scales = _decode_case(200 + exponent, lens, hq, hkv, dim, 16, True)
+    scales[0] = scales[0] * np.float32(2.0) ** -exponent
+    dev = [torch.from_numpy(fp4.pack(*p)).cuda() for p in pools]
+    desc = pkv.cache_desc_fp4(dev[0], *(torch.from_numpy(s).cuda() for s in scales))
+    q = rng.standard_normal((len(lens), hq, dim)) * 2.0 ** exponent
+    q[:, 1::2] *= 2.0 ** -9 if dtype == "bf16" else 1.0
+    q = torch.from_numpy(q).to(DT[dtype])
+    out = torch.empty(q.shape, dtype=DT[dtype], device="cuda")
+    ws = torch.empty(pkv.pkv_decode_workspace_bytes(len(lens), hq, hkv, dim, 16, 3000, 0), dtype=torch.uint8, device="cuda")
+    pkv.pkv_paged_decode(out, q.cuda(), *dev, desc, torch.from_numpy(table).cuda(),
+                         torch.tensor(lens, dtype=torch.int32, device="cuda"), 3000, dim ** -0.5, 0, ws)
+    assert pkv.pkv_get_device_error() == 0
+    k, v = (np.concatenate([_rows(*p, table[i], n, 16, s) for i, n in enumerate(lens)]) for p, s in zip(pools, scales))
+    ref, size = prompt.prompt_attention(q.double().numpy(), k, v, [1] * len(lens), lens, dim ** -0.5)
+    _close(out, ref, _bound(ref, size, DT[dtype]))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_a_query_that_is_not_finite_reaches_its_own_head_only(dtype):
+    import paged_kv_cache_160_gb300 as pkv
+    lens, hq, hkv, dim = [70, 2000, 33], 8, 2, 128
+    rng, table, pools, _ = _decode_case(33, lens, hq, hkv, dim, 16, False)
+    k, v = (torch.from_numpy(fp4.pack(*p)).cuda() for p in pools)
+    q = torch.from_numpy(rng.standard_normal((3, hq, dim))).to(DT[dtype])
+    q[2, 5] = 0.0                                              # a row of zeros: the mean of its values
+    broken = q.clone()
+    broken[0, 1, 5], broken[1, 6, 100] = float("inf"), float("nan")
+    ws = torch.empty(pkv.pkv_decode_workspace_bytes(3, hq, hkv, dim, 16, 2000, 0), dtype=torch.uint8, device="cuda")
+    outs = []
+    for x in (q, broken):
+        out = torch.empty(q.shape, dtype=DT[dtype], device="cuda")
+        pkv.pkv_paged_decode(out, x.cuda(), k, v, pkv.cache_desc_fp4(k), torch.from_numpy(table).cuda(),
+                             torch.tensor(lens, dtype=torch.int32, device="cuda"), 2000, dim ** -0.5, 0, ws)
+        outs.append(out.cpu())
+    assert pkv.pkv_get_device_error() == 0
+    hit = torch.zeros((3, hq), dtype=torch.bool)
+    hit[0, 1] = hit[1, 6] = True
+    assert torch.isnan(outs[1][hit]).all() and torch.equal(outs[1][~hit], outs[0][~hit])
+    rows = _rows(*pools[1], table[2], 33, 16, None)[:, 1]
+    _close(outs[0][2, 5], rows.mean(0), _bound(rows.mean(0), np.abs(rows).mean(0), DT[dtype]))
