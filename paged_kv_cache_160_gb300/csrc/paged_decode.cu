@@ -596,7 +596,6 @@ struct MergeParams {
   int max_len;            // the decode call's length clamp
   int part_blocks;        // the decode call's tiles per partition (0: balanced split)
   int num_workers;        // the decode call's worker warps
-  int wide;               // the decode over 4 bits: its split (workers_wide), and a NaN sum gives NaN, not zeros
 };
 
 constexpr int kMergeWarps = 8;
@@ -606,10 +605,11 @@ constexpr int kMergeWarps = 8;
 // Lane k fetches piece k's (m, l) while every lane fetches its 16-byte chunk of up to
 // kChunk pieces' rows; the weights come from warp reductions over the lanes, so the
 // loads of a block of 32 pieces overlap and no exponential sits between a load and the sum.
+// kWide: the decode over 4 bits, whose split is workers_wide's and whose NaN sums give NaN, not zeros.
 // kShared: a CTA's warps share one (segment, query head), every kMergeWarps-th block of pieces each; for few
 // segments of many pieces.  Two sequences of at most 19,682 tokens, one kv head, over 4 bits: 52 us with a warp
 // for each head, 17 with a CTA.
-template <int QT, int D, bool kShared>
+template <int QT, int D, bool kWide, bool kShared>
 __global__ void __launch_bounds__(kMergeWarps * 32, 2) split_kv_merge_kernel(const MergeParams p) {
   constexpr int kLanesPerHead = D / 4;       // 16-byte chunks of one head's row
   constexpr int kHP = 32 / kLanesPerHead;    // rows per load instruction of the warp
@@ -647,7 +647,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 2) split_kv_merge_kernel(con
       mine += __shfl_xor_sync(0xffffffffu, mine, o);
     }
     const int64_t units = int64_t(Hkv) * tot;
-    const int64_t W = p.wide && !PB ? workers_wide(units, p.num_workers, p.num_segments) : min(int64_t(p.num_workers), units);
+    int64_t W = min(int64_t(p.num_workers), units);
+    if (kWide && !PB) W = workers_wide(units, p.num_workers, p.num_segments);
     if (mine > 0 && W > 0) {
       const int64_t u0 = int64_t(Hkv) * pre + int64_t(h) * mine, u1 = u0 + mine - 1;
       w0 = int(((u0 + 1) * W - 1) / units);
@@ -735,7 +736,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 2) split_kv_merge_kernel(con
     }
   }
   if (rsub == 0) {
-    const float inv = den > 0.f || (p.wide && den != den) ? 1.f / den : 0.f;
+    const float inv = den > 0.f || (kWide && den != den) ? 1.f / den : 0.f;
     const int64_t obase = (int64_t(seg) * G + hh) * D + dof;   // out[s][h * G + hh][:]
 #pragma unroll
     for (int e = 0; e < 4; ++e) store_out<QT>(p.out, obase + e, acc[e] * inv);
@@ -776,17 +777,20 @@ pkv_status launch_merge(const DecodeParams& prm, bool q_bf16, int head_dim, bool
   mp.max_len = prm.max_len;
   mp.part_blocks = prm.part_blocks;
   mp.num_workers = prm.num_workers;
-  mp.wide = wide;
   const int64_t items = int64_t(mp.num_segments) * mp.group;
   // A segment has num_workers / num_segments pieces on average, and the longest several times as many.
   const bool shared = wide && prm.num_workers > 8 * int64_t(mp.num_segments);
   const int mgrid = shared ? int(items) : int((items + kMergeWarps - 1) / kMergeWarps);
-  auto pick = [&](auto is_shared) {
-    constexpr bool kShared = decltype(is_shared)::value;
-    return q_bf16 ? (head_dim == 128 ? split_kv_merge_kernel<KV_BF16, 128, kShared> : split_kv_merge_kernel<KV_BF16, 64, kShared>)
-                  : (head_dim == 128 ? split_kv_merge_kernel<KV_F16, 128, kShared> : split_kv_merge_kernel<KV_F16, 64, kShared>);
+  auto pick = [&](auto is_wide, auto is_shared) {
+    constexpr bool kWide = decltype(is_wide)::value, kShared = decltype(is_shared)::value;
+    return q_bf16 ? (head_dim == 128 ? split_kv_merge_kernel<KV_BF16, 128, kWide, kShared>
+                                     : split_kv_merge_kernel<KV_BF16, 64, kWide, kShared>)
+                  : (head_dim == 128 ? split_kv_merge_kernel<KV_F16, 128, kWide, kShared>
+                                     : split_kv_merge_kernel<KV_F16, 64, kWide, kShared>);
   };
-  auto kern = shared ? pick(std::true_type{}) : pick(std::false_type{});
+  using No = std::false_type;
+  using Yes = std::true_type;
+  auto kern = shared ? pick(Yes{}, Yes{}) : wide ? pick(Yes{}, No{}) : pick(No{}, No{});
   return launch_pdl(kern, dim3(mgrid), dim3(kMergeWarps * 32), 0, stream, mp) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
