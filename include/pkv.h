@@ -213,7 +213,9 @@ PKV_API size_t pkv_decode_workspace_bytes(int num_seqs, int num_heads, int num_k
  * (e4m3: q is taken as fp16, so bf16 |q| must stay below 65504 and loses bits below 2^-14; 4-bit: bf16
  * q of any size, each row times a power of two of its own); head_dim 64/128; block_size 16 or 32;
  * num_heads / num_kv_heads in 1..8; num_kv_heads * num_seqs * ceil(L_max / 16) < 2^31, where
- * L_max = min(max_context_len, max_blocks_per_seq * block_size) (else PKV_ERR_UNSUPPORTED).
+ * L_max = min(max_context_len, max_blocks_per_seq * block_size); up to about 13,000 sequences, whose
+ * prefix sums share an SM's shared memory with the tiles (4-bit kv 13,180, 16-bit kv of head_dim 128
+ * 13,700, else 16,400) (else PKV_ERR_UNSUPPORTED).
  * Launch order: the decode kernel is launched as a programmatic dependent of the previous
  * kernel on `stream`.  If that kernel allows early dependent launch (pkv_kv_write does), the
  * decode kernel may already read context_lens and block_tables while it still runs; q, the

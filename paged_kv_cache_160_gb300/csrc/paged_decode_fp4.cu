@@ -643,8 +643,8 @@ pkv_status launch_cfg(DecodeParams prm, int grid, cudaStream_t stream) {
   return launch_merge(prm, kQBF16, D, true, stream);
 }
 
-// 12 worker warps when the per-sequence prefix arrays fit next to their stages (up to about 900
-// sequences at head_dim 128), else 8 (about 6,500) or 4.
+// 12 worker warps when the per-sequence prefix arrays (12 bytes each) fit next to their stages (18 KB per
+// warp): up to about 900 sequences; else 8 (about 7,040) or 4 (about 13,180; more are refused).
 template <bool kQBF16, int D>
 pkv_status launch(const DecodeParams& prm, int grid, cudaStream_t stream) {
   static thread_local int cached_dev = -1;

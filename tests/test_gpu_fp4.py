@@ -544,3 +544,53 @@ def test_a_query_that_is_not_finite_reaches_its_own_head_only(dtype):
     assert torch.isnan(outs[1][hit]).all() and torch.equal(outs[1][~hit], outs[0][~hit])
     rows = _rows(*pools[1], table[2], 33, 16, None)[:, 1]
     _close(outs[0][2, 5], rows.mean(0), _bound(rows.mean(0), np.abs(rows).mean(0), DT[dtype]))
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("seqs", [1000, 5000, 8000])
+def test_decode_and_append_of_large_batches(seqs, dim):
+    """12 prefix bytes per sequence beside the warps' stages: 12 warps run up to about 900 sequences, 8 up to about
+    7,040, then 4."""
+    import paged_kv_cache_160_gb300 as pkv
+    rng = np.random.default_rng(seqs + dim)
+    lens, hq, hkv = [int(n) for n in rng.integers(0, 40, seqs)], 3, 1
+    lens[seqs // 2] = 700
+    _run_decode(lens, hq, hkv, dim, "bf16", seed=seqs)
+    _, table, pools, _ = _decode_case(seqs + 1, lens, hq, hkv, dim, 16, False)
+    host = [torch.from_numpy(fp4.pack(*p)) for p in pools]
+    q, kn, vn = (torch.from_numpy(rng.standard_normal((seqs, h, dim))).to(torch.bfloat16).cuda() for h in (hq, hkv, hkv))
+    slots = torch.tensor([int(table[i, (n - 1) // 16]) * 16 + (n - 1) % 16 if n else -1 for i, n in enumerate(lens)],
+                         device="cuda")
+    tail = (torch.from_numpy(table).cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"), 700, dim ** -0.5, 0,
+            torch.empty(pkv.pkv_decode_workspace_bytes(seqs, hq, hkv, dim, 16, 700, 0), dtype=torch.uint8, device="cuda"))
+    got = []
+    for fused in (False, True):
+        k, v = host[0].cuda(), host[1].cuda()
+        out = torch.empty_like(q)
+        if fused:
+            pkv.pkv_paged_decode_append(out, q, kn, vn, k, v, pkv.cache_desc_fp4(k), *tail)
+        else:
+            pkv.pkv_kv_write(kn, vn, slots, k, v, pkv.cache_desc_fp4(k))
+            pkv.pkv_paged_decode(out, q, k, v, pkv.cache_desc_fp4(k), *tail)
+        assert pkv.pkv_get_device_error() == 0
+        got.append((out, k, v))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+
+
+def test_batches_past_the_limit_are_refused():
+    import paged_kv_cache_160_gb300 as pkv
+    for seqs, dim in ((13100, 64), (13100, 128), (13300, 64), (13300, 128)):
+        k = torch.zeros(pkv.fp4_cache_shape(1, 1, 16, dim), dtype=torch.uint8, device="cuda")
+        q = torch.ones((seqs, 1, dim), dtype=torch.bfloat16, device="cuda")
+        out = torch.full_like(q, 7.0)
+        ws = torch.empty(pkv.pkv_decode_workspace_bytes(seqs, 1, 1, dim, 16, 16, 0), dtype=torch.uint8, device="cuda")
+        args = (out, q, k, k, pkv.cache_desc_fp4(k), torch.zeros((seqs, 1), dtype=torch.int32, device="cuda"),
+                torch.full((seqs,), 3, dtype=torch.int32, device="cuda"), 16, 0.1, 0, ws)
+        if seqs < 13150:
+            pkv.pkv_paged_decode(*args)
+            assert pkv.pkv_get_device_error() == 0 and (out == 0).all()
+        else:
+            with pytest.raises(pkv.PkvError):
+                pkv.pkv_paged_decode(*args)
+            assert (out == 7.0).all()
