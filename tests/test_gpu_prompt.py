@@ -290,3 +290,67 @@ def test_short_sequences_share_blocks_between_heads(q_lens, k_lens, hq, hkv, dim
 def test_blocks_shared_between_heads_in_rows_of_a_packed_projection():
     lens = [20, 1, 33, 7]
     _run(lens, lens, 14, 2, 128, "f16", packed=True, pad=3)
+
+
+@pytest.mark.parametrize("dim,hq,hkv,longest", [(128, 4, 4, 0), (64, 4, 4, 1500), (128, 6, 3, 1500), (64, 6, 3, 0)])
+def test_many_items_for_each_resident_cta(dim, hq, hkv, longest):
+    """About 1,700 items, at least ten for each CTA that the GPU holds, numbered level by level and (with one long
+    sequence among the short ones) sequence by sequence; infinities and NaN in V rows of scattered sequences."""
+    import paged_kv_cache_160_gb300 as pkv
+    rng = np.random.default_rng(dim + hq)
+    n = 1700 // hkv
+    q_lens = [int(x) for x in rng.integers(0, 50, n)]
+    if longest:
+        q_lens[n // 3] = longest
+    k_lens = [x + int(rng.integers(0, 40)) for x in q_lens]
+    tq, tk, starts = sum(q_lens), sum(k_lens), np.cumsum([0] + k_lens)
+    g = torch.Generator().manual_seed(dim)
+    q, k, v = (torch.randn((rows, h, dim), generator=g).to(torch.bfloat16) for rows, h in ((tq, hq), (tk, hkv), (tk, hkv)))
+    for i in rng.permutation(n)[:60]:
+        if k_lens[i]:
+            j = starts[i] + int(rng.integers(0, k_lens[i]))
+            v[j, int(rng.integers(0, hkv)), int(rng.integers(0, dim))] = rng.choice([float("nan"), float("inf"), -float("inf")])
+    cu = [torch.tensor(np.cumsum([0] + x), dtype=torch.int32, device="cuda") for x in (q_lens, k_lens)]
+    out = torch.full((tq, hq, dim), 5.0, dtype=torch.bfloat16, device="cuda")
+    pkv.pkv_prompt_attention(out, q.cuda(), k.cuda(), v.cuda(), *cu, max(q_lens), dim ** -0.5)
+    assert pkv.pkv_get_device_error() == 0
+    got = out.double().cpu().numpy()
+    with np.errstate(all="ignore"):
+        ref, size = prompt.prompt_attention(*(t.double().numpy() for t in (q, k, v)), q_lens, k_lens, dim ** -0.5)
+        fine = np.isfinite(ref)
+        assert np.isnan(ref).any() and np.isinf(ref).any() and np.array_equal(np.isnan(got), np.isnan(ref))
+        assert np.array_equal(got[np.isinf(ref)], ref[np.isinf(ref)])
+        u = torch.finfo(torch.bfloat16).eps / 2
+        err, bound = np.abs(got - ref)[fine], ((u + 2.0 ** -11) * size + u * np.abs(ref) + 2.0 ** -25)[fine]
+    assert (err <= bound).all(), float((err / bound).max())
+
+
+@pytest.mark.parametrize("dim,hq,hkv", [(128, 2, 2), (64, 8, 2)])
+def test_many_long_items_for_each_resident_cta(dim, hq, hkv):
+    """The same with several key tiles per item, so that stages and barriers wrap at every phase: one sequence's rows
+    are those of the sequence alone."""
+    import paged_kv_cache_160_gb300 as pkv
+    rng = np.random.default_rng(hq)
+    lens = [int(x) for x in rng.integers(1, 700, 900)]
+    q, k, v = (torch.randn((sum(lens), h, dim), generator=torch.Generator().manual_seed(h + i)).to(torch.bfloat16).cuda()
+               for i, h in enumerate((hq, hkv, hkv)))
+    starts = np.cumsum([0] + lens)
+
+    def run(a, b):
+        n, s, e = lens[a:b], starts[a], starts[b]
+        cu = torch.tensor(np.cumsum([0] + n), dtype=torch.int32, device="cuda")
+        out = torch.empty_like(q[s:e])
+        pkv.pkv_prompt_attention(out, q[s:e], k[s:e], v[s:e], cu, cu, max(n), dim ** -0.5)
+        return out
+
+    whole = run(0, 900)
+    assert torch.equal(whole, run(0, 900))
+    for a in (0, 150, 300, 450, 600, 750):                     # fewer items each, in other CTAs
+        assert torch.equal(whole[starts[a]:starts[a + 150]], run(a, a + 150))
+    assert pkv.pkv_get_device_error() == 0
+    for i in (3, 444, 899):
+        s, e = starts[i], starts[i + 1]
+        ref, size = prompt.prompt_attention(*(t[s:e].double().cpu().numpy() for t in (q, k, v)), [e - s], [e - s], dim ** -0.5)
+        u = torch.finfo(torch.bfloat16).eps / 2
+        err = np.abs(whole[s:e].double().cpu().numpy() - ref)
+        assert (err <= (u + 2.0 ** -11) * size + u * np.abs(ref) + 2.0 ** -25).all()
