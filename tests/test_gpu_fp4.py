@@ -594,3 +594,24 @@ def test_batches_past_the_limit_are_refused():
             with pytest.raises(pkv.PkvError):
                 pkv.pkv_paged_decode(*args)
             assert (out == 7.0).all()
+
+
+def test_append_from_pinned_host_memory():
+    import paged_kv_cache_160_gb300 as pkv
+    lens, hq, hkv, dim = [1, 16, 0, 500, 3000], 8, 2, 128
+    rng, table, pools, scales = _decode_case(46, lens, hq, hkv, dim, 16, True)
+    host = [torch.from_numpy(fp4.pack(*p)) for p in pools]
+    x = [torch.from_numpy(rng.standard_normal((len(lens), h, dim))).to(torch.bfloat16) for h in (hq, hkv, hkv)]
+    x += [torch.from_numpy(table), torch.tensor(lens, dtype=torch.int32)]
+    ws = torch.empty(pkv.pkv_decode_workspace_bytes(len(lens), hq, hkv, dim, 16, 3000, 0), dtype=torch.uint8, device="cuda")
+    got = []
+    for put in (torch.Tensor.cuda, torch.Tensor.pin_memory):
+        k, v = host[0].cuda(), host[1].cuda()
+        desc = pkv.cache_desc_fp4(k, *(torch.from_numpy(s).cuda() for s in scales))
+        q, kn, vn, tab, ln = (put(t) for t in x)
+        out = put(torch.zeros(x[0].shape, dtype=torch.bfloat16))
+        pkv.pkv_paged_decode_append(out, q, kn, vn, k, v, desc, tab, ln, 3000, dim ** -0.5, 0, ws)
+        assert pkv.pkv_get_device_error() == 0                 # (waits)
+        got.append((out.cpu(), k, v))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
