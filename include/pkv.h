@@ -312,7 +312,8 @@ PKV_API int pkv_get_decode_sm_budget(void);
  *   q_start_pos   (device) int32 [num_chunks]
  *   block_tables  (device) int32 [num_chunks][max_blocks_per_seq]
  *   max_q_len     host upper bound of the chunks' lengths (sizes the grid); a longer chunk
- *                 sets PKV_DEVERR_CHUNK and its rows past max_q_len stay unwritten
+ *                 sets PKV_DEVERR_CHUNK and its rows past max_q_len stay unwritten.  0 says that
+ *                 every chunk is empty: nothing is enqueued, and the lengths are not looked at
  * Supported: f16/bf16 cache with the same q dtype, head_dim 128, block_size 16 or 32,
  * num_heads a multiple of num_kv_heads (any group size).  Tensor cores (tcgen05, TMEM
  * accumulators), K/V tiles fetched by TMA straight from the physical blocks; with two or
@@ -347,7 +348,8 @@ PKV_API pkv_status pkv_paged_prefill_chunk(void* out, const void* q, pkv_dtype q
  *   cu_q_lens, cu_k_lens (device) int32 [num_seqs + 1], from 0, ascending, the last at most total_q
  *                  (total_k); output rows from cu_q_lens[num_seqs] on are left as they were
  *   max_q_len      host upper bound of Lq (sizes the grid); a longer sequence sets PKV_DEVERR_CHUNK and
- *                  its rows past max_q_len stay unwritten
+ *                  its rows past max_q_len stay unwritten.  0 says that every sequence is empty: the call
+ *                  returns PKV_OK at once, enqueues nothing, and the lengths are not looked at
  * out must not overlap q, k or v.  Only what a row attends reaches it: infinities and NaN in other
  * rows' keys and values, and behind the sequences, do not.  cu_q_lens or cu_k_lens that are not
  * ascending from 0 or pass the totals set PKV_DEVERR_CHUNK and leave that sequence's rows unwritten.
