@@ -131,7 +131,9 @@ PKV_API pkv_status pkv_kv_write(const void* k_new, const void* v_new, pkv_dtype 
  *                  total_tokens
  *   block_tables   (device) int32 [num_seqs][max_blocks_per_seq]
  * Output row cu_lens[i] + j becomes position j of sequence i, for K and for V:
- *   out[cu_lens[i] + j][h][:] = cache[T_i[j / B]][h][j % B][:]  (its value, rounded once to out_dtype)
+ *   out[cu_lens[i] + j][h][:] = cache[T_i[j / B]][h][j % B][:]
+ * 16-bit rows are copied.  Otherwise the code (4-bit: code * scale, exact) times k_scale / v_scale of the
+ * head is rounded to fp32 and then to out_dtype.
  * Rows from cu_lens[num_seqs] on are left as they were.  A block id outside the pool leaves its rows
  * as they were and is flagged PKV_DEVERR_BLOCK_ID; so are rows of a sequence longer than its table
  * and, as far as the inconsistency reaches, rows under cu_lens that are not ascending from 0 or pass
@@ -195,7 +197,8 @@ PKV_API size_t pkv_decode_workspace_bytes(int num_seqs, int num_heads, int num_k
  * or only at multiples of partition_size tokens.  A worker runs an online softmax over
  * its range (consecutive partitions merge in registers); pieces of one sequence held by
  * different workers are merged by log-sum-exp in a second kernel on the same stream,
- * launched as a programmatic dependent of the first.  fp32 accumulation.
+ * launched as a programmatic dependent of the first.  fp32 accumulation; the softmax's exponentials
+ * are rounded to the type of their products with V (the cache's; fp16 over e4m3 and 4 bits).
  *   out            (device) [num_seqs][num_heads][head_dim] of q_dtype
  *   q              (device) [num_seqs][num_heads][head_dim] of q_dtype (f16 or bf16)
  *   block_tables   (device) int32 [num_seqs][max_blocks_per_seq]
@@ -217,8 +220,8 @@ PKV_API size_t pkv_decode_workspace_bytes(int num_seqs, int num_heads, int num_k
  * prefix sums share an SM's shared memory with the tiles (4-bit kv 13,180, 16-bit kv of head_dim 128
  * 13,700, else 16,400) (else PKV_ERR_UNSUPPORTED).
  * Launch order: the decode kernel is launched as a programmatic dependent of the previous
- * kernel on `stream`.  If that kernel allows early dependent launch (pkv_kv_write does), the
- * decode kernel may already read context_lens and block_tables while it still runs; q, the
+ * kernel on `stream`.  If that kernel allows early dependent launch (pkv_kv_write, pkv_kv_read
+ * and pkv_qk_rotary do), the decode kernel may already read context_lens and block_tables while it still runs; q, the
  * caches, out and the workspace are touched only after it has completed.  So the kernel
  * right before a decode call must not write context_lens or block_tables unless it leaves
  * dependent launch at its default (wait for completion).
@@ -235,8 +238,9 @@ PKV_API pkv_status pkv_paged_decode(void* out, const void* q, pkv_dtype q_dtype,
  * pkv_paged_decode (PagedAttention §3.3: each new token fills its sequence's last block).
  * For every sequence i with L = context_lens[i] >= 1, the new rows k_new[i] and v_new[i] are
  * stored at position L - 1, i.e. slot block_tables[i][(L - 1) / B] * B + (L - 1) % B, quantised
- * for an e4m3 or 4-bit cache exactly as pkv_kv_write does, and the decode then attends positions 0 .. L - 1, the new one included.  Caches and out are bit-identical to
- * pkv_kv_write (with those slots) followed by pkv_paged_decode.
+ * for an e4m3 or 4-bit cache exactly as pkv_kv_write does, and the decode then attends positions
+ * 0 .. L - 1, the new one included.  Caches and out are bit-identical to pkv_kv_write (with those
+ * slots) followed by pkv_paged_decode.
  *   k_new, v_new  (device, or pinned host memory as for q) [num_seqs][num_kv_heads][head_dim]
  *                 of q_dtype, 16-byte aligned
  *   k_cache, v_cache  (device) written at those positions only

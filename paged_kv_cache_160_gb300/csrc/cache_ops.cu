@@ -387,8 +387,6 @@ __global__ void __launch_bounds__(kThreads) swap_blocks_kernel(uint4* __restrict
   for (; i < chunks; i += blockDim.x) dp[i] = sp[i];
 }
 
-// One 16-byte chunk per thread: these kernels are latency-bound at serving sizes, so every
-// thread should issue its loads once rather than loop.
 // CTAs for tokens of `per_token` threads' work, whose threads are a whole number of tokens: about `resident`
 // of them, fewer where there is less to do.
 unsigned grid_of_tokens(int num_tokens, int64_t per_token, int64_t resident) {
@@ -397,6 +395,8 @@ unsigned grid_of_tokens(int num_tokens, int64_t per_token, int64_t resident) {
   return unsigned(std::min((needed - 1) / unit + 1, std::max<int64_t>(1, resident / unit)) * unit);
 }
 
+// One 16-byte chunk per thread: these kernels are latency-bound at serving sizes, so every
+// thread should issue its loads once rather than loop.
 int grid_for(int64_t work) {
   const int64_t per = kThreads;
   int64_t g = (work + per - 1) / per;

@@ -5,7 +5,8 @@
 // merged by log-sum-exp), with K and V as code * scale of 16 elements * scale of the head.  code *
 // scale is exact in fp16 (a 2-bit times a 4-bit significand, 2^-10 .. 2688), so the tensor cores
 // multiply the stored values themselves; the head's k_scale goes into the softmax scale, its v_scale
-// into the output.
+// into the output.  P is rounded to fp16 for its product with V (2^-11 of each weight); the sum of the
+// weights takes them unrounded.
 //
 // What bounds it: a 16-token tile of K and V is 18 * head_dim bytes, about 100 SM cycles at the
 // measured copy bandwidth, while turning its 32 * head_dim codes into fp16 fragments takes

@@ -5,8 +5,10 @@
 // of log2): P = 2^(s c - m), O = O 2^(m_old - m) + P V, out = O / l.
 //
 // GB300 design: a CTA holds two row blocks of 128 rows that read the same keys, so every K/V tile feeds 256
-// rows: query rows of one head, or of all query heads of a kv head (Blocks).  S = Q K^T and O += P V run on tcgen05 with S, P and O in tensor memory; Q, K
-// and V arrive by TMA straight from the packed rows (any row stride).
+// rows: query rows of one head, or of all query heads of a kv head (Blocks).  S = Q K^T and O += P V run on
+// tcgen05 with S, P and O in tensor memory; Q, K and V arrive by TMA straight from the packed rows (any row
+// stride).  P is rounded to the type of V, as both operands of a product share a type (2^-8 of each weight in
+// bf16, 2^-11 in f16); l sums the unrounded fp32 values.
 //
 // Bound: the tensor cores, and the exponentials beside them (a 128 x 128 tile is 16,384 of them, about as
 // many cycles of the special function units as of its two products).  Measured in a graph: 8192 tokens,
@@ -321,7 +323,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint32_t tmem_base_sh;
   __shared__ float exchange[2][2][2][kTile];                 // [block][step parity][key half][row]
   __shared__ int first_item[kSplit ? 1 : (kMaxSeqs + kSeqChunk - 1) / kSeqChunk + 1];
-  __shared__ int masked_item[2 * kItems];                    // by item number modulo that: non-finite values were taken out (+ 1)
+  __shared__ int masked_item[2 * kItems];                    // by item number modulo that: the last such item that
+                                                             // non-finite values were taken out for, + 1
   __shared__ __align__(16) float2 part_ml[2][kSplit ? kTile : 1];   // [block][row]: maximum and sum over this CTA's keys
   __shared__ __align__(16) float2 recv_ml[3][kSplit ? kTile : 1];   // [sender][row of this CTA's share]
   __shared__ __align__(8) uint64_t bar_recv;
@@ -424,7 +427,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int rr = lane % C::kStageRows, rsub = lane / kChunks, chunk = lane % kChunks;
     const uint32_t put = stage + rr * kRowBytes, turn = rr & (kChunks - 1);
     const int64_t step = p.out_stride * (2 * kRowsPerStore);
-    uint8_t* dst = p.out + ((int64_t(it.q0) + blocks.first_row(e)) * p.out_stride + int64_t(it.h * G) * D + D / 2 * hf) * 2 + 16 * chunk;
+    uint8_t* dst = p.out + 16 * chunk +
+                   ((int64_t(it.q0) + blocks.first_row(e)) * p.out_stride + int64_t(it.h * G) * D + D / 2 * hf) * 2;
     if (!kPacked) dst += ((32 * quarter + rsub) * p.out_stride + int64_t(e % G) * D) * 2;
     left -= rsub;
 #pragma unroll
@@ -633,7 +637,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&bar_o_free[x]);          // the next item may overwrite O
         if (taken) {
 #pragma unroll
-          for (int cc = 0; cc < kODims / 32; ++cc) give_back(it, row, hf, 32 * cc, *reinterpret_cast<float(*)[32]>(v + 32 * cc));
+          for (int cc = 0; cc < kODims / 32; ++cc)
+            give_back(it, row, hf, 32 * cc, *reinterpret_cast<float(*)[32]>(v + 32 * cc));
         }
         const float inv = l == 0.f ? 0.f : 1.f / l;          // l = 0: a row without keys, whose O is 0; NaN stays
         const uint64_t inv2 = pack_f32x2(inv, inv);
@@ -676,7 +681,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive_expect_tx(&bar_q[x], kPacked ? blocks.rows * G * D * 2 : C::kTileBytes);
             const int e = it.e0 + x;
             for (int d = 0; d < D / 64; ++d)
-              tma_load_3d(sQ + x * C::kTileBytes + d * kHalfBytes, &tmq, &bar_q[x], 64 * d, it.h * G + (kPacked ? 0 : e % G), it.q0 + blocks.first_row(e), pol_q);
+              tma_load_3d(sQ + x * C::kTileBytes + d * kHalfBytes, &tmq, &bar_q[x], 64 * d,
+                          it.h * G + (kPacked ? 0 : e % G), it.q0 + blocks.first_row(e), pol_q);
           }
           ++q_of[x];
         };
@@ -686,7 +692,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (ok && lane == 0) {
             mbar_arrive_expect_tx(&bar_k_full[st], C::kTileBytes);
             for (int d = 0; d < D / 64; ++d)
-              tma_load_3d(sK + st * C::kTileBytes + d * kHalfBytes, &tmk, &bar_k_full[st], 64 * d, it.h, it.k0 + (it.t0 + t) * kTile, pol_kv);
+              tma_load_3d(sK + st * C::kTileBytes + d * kHalfBytes, &tmk, &bar_k_full[st], 64 * d, it.h,
+                          it.k0 + (it.t0 + t) * kTile, pol_kv);
           }
           const bool k_ok = ok;                                // a K tile is on its way
           if (t == 0 && it.na > 0) load_q(0);
@@ -699,11 +706,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) {
             mbar_arrive_expect_tx(&bar_v_full[st], C::kTileBytes);
             for (int d = 0; d < D / 64; ++d)
-              tma_load_3d(sV + st * C::kTileBytes + d * kHalfBytes, &tmv, &bar_v_full[st], 64 * d, it.h, it.k0 + (it.t0 + t) * kTile, pol_kv);
+              tma_load_3d(sV + st * C::kTileBytes + d * kHalfBytes, &tmv, &bar_v_full[st], 64 * d, it.h,
+                          it.k0 + (it.t0 + t) * kTile, pol_kv);
           }
           if (t == 0 && it.nb > 0) load_q(1);
         }
-        // Also after a wait gave up: no answer may still be on its way when the CTA leaves.
         if (kSplit) break;
         // The next item, past those without rows.  Also after a wait gave up: no answer may still be on
         // its way when the CTA leaves.
@@ -1033,8 +1040,8 @@ int clusters_at_once(int parts) {
 
 // One item walks its keys alone unless there are so few items that clusters of 2 or 4 CTAs for each still
 // run at once and every part has two key tiles or more (by the sequences' mean length).  A chunk of 512
-// rows after 3584 keys (56 items): 49.5 us alone, 33.0 us in clusters of 2; one row of 32 heads over 4096
-// keys (16 items, a head per block): 48.1 us alone, 19.4 us in clusters of 4 (17.3 with all heads in a block).
+// rows after 3584 keys (60 items of 28 heads over 4): 48.4 us alone, 33.4 us in clusters of 2; one row of 32
+// heads over 8 and 4096 keys (8 items): 44.0 us alone, 17.8 us in clusters of 4.
 template <bool kBF16, int D, bool kPacked>
 pkv_status launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PromptParams& prm,
                   int num_seqs, int max_q_len, cudaStream_t stream) {
@@ -1043,14 +1050,16 @@ pkv_status launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMa
   const int64_t groups = ((int64_t(max_q_len) - 1) / blocks.rows * blocks.per_tile + blocks.per_tile + 1) / 2;
   const int64_t items = groups * num_seqs * prm.num_kv_heads;
   // Items that the sequences have at most, whatever their lengths.
-  const int64_t most = ((int64_t(prm.total_q) / blocks.rows + num_seqs + 1) * blocks.per_tile / 2 + num_seqs) * prm.num_kv_heads;
+  const int64_t most =
+      ((int64_t(prm.total_q) / blocks.rows + num_seqs + 1) * blocks.per_tile / 2 + num_seqs) * prm.num_kv_heads;
   const int64_t mean_tiles = (int64_t(prm.total_k) / num_seqs + kTile - 1) / kTile;
   int parts = 1;
   while (parts < 4 && mean_tiles >= 4 * parts && items <= clusters_at_once<kBF16, D, kPacked>(2 * parts)) parts *= 2;
   // Numbering the items level by level starts the long ones first, but has an index for every sequence
   // at every level of the longest one; past twice the items that there can be, or past what a grid
   // holds, they are numbered sequence by sequence.  One prompt of 8192 tokens among 255 of 32 (32 heads
-  // over 8, a head per block): 2347 us level by level, 513 us by sequence; 16 prompts of 64 to 2048 tokens: 226 us and 240 us.
+  // over 8): 1098 us level by level, 368 us by sequence; 16 prompts of 64 to 2048 tokens (13,165 in
+  // all, 28 heads over 4): 110 us and 115 us.
   const bool compact = parts == 1 && (items > 2 * most || groups > 65535);
   if (compact && most > 0x7fffffff) return PKV_ERR_UNSUPPORTED;
   PromptParams params = prm;
