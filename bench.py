@@ -78,7 +78,7 @@ FALLBACK_BF16_TFLOPS = 1900.0
 # capture; ncu flushes the caches before each kernel, so the merge's reads of the
 # partials count as DRAM reads), valid only for the kernel source with this hash; when the
 # source changes, traffic is reported as null until re-measured.
-TRAFFIC = {"source_sha1": "d63ad2fd4c13114248bc8a47aab535d9c1e45498", "bytes_per_launch": 161544192}
+TRAFFIC = {"source_sha1": "35e6d8965aba30b574b8b43073409bb5999cf14d", "bytes_per_launch": 161117440}
 
 
 def _src_hash() -> str:
