@@ -184,3 +184,45 @@ def test_two_streams_at_once():
     for want, runs in zip(alone, together):
         for got in runs:
             assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("longest", [0, 3000])
+def test_rows_past_4_gib(longest):
+    """Rotation and attention of 65,535 sequences, the most that a call takes, in more than 2^32 bytes of rows: parts
+    of them are as alone."""
+    import paged_kv_cache_160_gb300 as pkv
+    hq, hkv, dim = 14, 2, 128
+    rng = np.random.default_rng(12)
+    lens = rng.integers(0, 40, 65535)
+    if longest:
+        lens[50_000] = longest
+    start = np.concatenate([[0], np.cumsum(lens)])
+    total = int(start[-1])
+    g = torch.Generator(device="cuda").manual_seed(3)
+    qkv = torch.randn((total, hq + 2 * hkv, dim), generator=g, device="cuda", dtype=torch.bfloat16)
+    assert qkv.numel() * 2 > 2 ** 32
+    pos = torch.from_numpy(np.arange(total) - np.repeat(start[:-1], lens)).to(torch.int32).cuda()
+    table = pkv.pkv_rope_table(dim).cuda()
+    parts = [(0, 40), (49_990, 50_010), (65_500, 65_535)]
+    before = [qkv[start[a]:start[b]].clone() for a, b in parts]
+
+    def step(x, p, n):
+        q, k, v = x.split([hq, hkv, hkv], 1)
+        pkv.pkv_qk_rotary(q, q, k, k, p, table)
+        out = torch.zeros((len(x), hq, dim), dtype=x.dtype, device="cuda")
+        cu = torch.from_numpy(np.concatenate([[0], np.cumsum(n)])).to(torch.int32).cuda()
+        pkv.pkv_prompt_attention(out, q, k, v, cu, cu, int(max(n)), dim ** -0.5)
+        return out
+
+    whole = step(qkv, pos, lens)
+    assert pkv.pkv_get_device_error() == 0
+    for (a, b), x in zip(parts, before):
+        s, e = start[a], start[b]
+        out = step(x, pos[s:e].clone(), lens[a:b])
+        assert pkv.pkv_get_device_error() == 0
+        assert torch.equal(x, qkv[s:e])
+        # Few items may share their keys between CTAs, with sums in another order: each side is within
+        # (2^-8 + 2^-11) sum_j p_j |v_j| + 2^-8 |out| of the exact row (tests/test_gpu_prompt.py), and sum_j p_j |v_j| <= max |v|.
+        err = (out.double() - whole[s:e].double()).abs()
+        most = x[:, hq + hkv:].double().abs().max()
+        assert (err <= 2 * ((2.0 ** -8 + 2.0 ** -11) * most + 2.0 ** -8 * out.double().abs())).all() and (out != 0).any()
