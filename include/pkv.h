@@ -368,6 +368,111 @@ PKV_API pkv_status pkv_prompt_attention(void* out, const void* q, const void* k,
                                         int head_dim, int64_t out_stride, int64_t q_stride, int64_t k_stride,
                                         int64_t v_stride, float scale, pkv_stream_t stream);
 
+/*
+ * Workspace bytes pkv_paged_chunk_attention needs on the current device.  It depends on the SM count and the
+ * shapes given, not on the lengths.  The workspace needs no initialisation; calls that share one must not overlap.
+ */
+PKV_API size_t pkv_chunk_workspace_bytes(int total_q, int num_heads, int num_kv_heads, int head_dim);
+
+/*
+ * paged_chunk_attention: causal attention of each sequence's new rows over its paged cache, of any type:
+ * drafted tokens to verify, a prompt's next chunk, or one token.  The keys are split over the GPU, so that few
+ * rows over long histories use all of it.  Chunk c holds query rows cu_q_lens[c] .. cu_q_lens[c+1]-1; row r of the
+ * chunk is at position p = q_start_pos[c] + r and attends keys 0 .. p, whose K/V must be in the cache
+ * (pkv_kv_write first).  With g = h / (num_heads / num_kv_heads):
+ *   s_j = scale * q[r][h] . K[j][g],   out[r][h] = sum_j softmax(s)_j V[j][g],   lse[r][h] = log sum_j exp(s_j)
+ *   out, q         (device) [total_q][num_heads][head_dim] of q_dtype (f16 or bf16; for a 16-bit cache its type)
+ *   lse            (device) fp32 [total_q][num_heads], or NULL
+ *   cu_q_lens      (device) int32 [num_chunks + 1], from 0, ascending, the last at most total_q; output rows from
+ *                  cu_q_lens[num_chunks] on are left as they were
+ *   q_start_pos    (device) int32 [num_chunks]
+ *   block_tables   (device) int32 [num_chunks][max_blocks_per_seq]
+ *   workspace      (device) >= pkv_chunk_workspace_bytes(...) bytes
+ * out must not overlap q.  Only what a row attends reaches it: infinities and NaN in other keys and values, in
+ * stale rows of a block, and behind the chunks, do not.  A chunk whose lengths are inconsistent (cu_q_lens not
+ * ascending from 0 or past total_q, q_start_pos < 0, or positions past its table) sets PKV_DEVERR_CHUNK and its
+ * rows stay unwritten.  A block id outside the pool sets PKV_DEVERR_BLOCK_ID; its keys and values count as zeros.
+ * Supported: f16, bf16, e4m3 and 4-bit caches, head_dim 64 or 128, block_size 16 or 32, any number of query heads
+ * per kv head, scale > 0 and finite, num_chunks up to 65535, total_q * num_heads and max_blocks_per_seq * block_size
+ * below 2^31, and (total_q * (num_heads / num_kv_heads) / 256 + num_chunks) * (max_blocks_per_seq * block_size / 64 + 2)
+ * below 2^31.  Sums, maxima and outputs are fp32 until the last rounding; the softmax's exponentials are rounded to
+ * the type of their product with V (q_dtype; fp16 over e4m3 and 4 bits).  Over e4m3 and 4 bits, bf16 q is taken as
+ * fp16 after a power of two for each row (bits below 2^-25 of the row's largest are lost).  All of it
+ * must be memory of the current GPU.  Launch order as pkv_kv_write (waits before touching memory).
+ */
+PKV_API pkv_status pkv_paged_chunk_attention(void* out, float* lse, const void* q, pkv_dtype q_dtype,
+                                             const int32_t* cu_q_lens, const int32_t* q_start_pos, int num_chunks,
+                                             int total_q, int num_heads, const void* k_cache, const void* v_cache,
+                                             const pkv_cache_desc* cache, const int32_t* block_tables,
+                                             int max_blocks_per_seq, float scale, void* workspace,
+                                             size_t workspace_bytes, pkv_stream_t stream);
+
+/*
+ * Eviction by attention weight: a sequence's cache is cut to the tokens that its queries look at.
+ * pkv_attention_weights adds up the attention that each cached token gets, pkv_evict_select picks the tokens each
+ * kv head keeps, pkv_bm_evict gives the sequence its new table, and pkv_evict_compact moves the kept rows to
+ * its front.  Every head keeps the same number of tokens, not the same tokens.  Keys keep the positions that they
+ * were rotated by; later tokens go on with their own.
+ *
+ * Weights are fp32 [num_rows][num_kv_heads][max_len]; sequence i has row rows[i] (row i if rows is NULL).  A
+ * negative row says that the sequence has none (nothing is read or written for it); one from num_rows on sets
+ * PKV_DEVERR_SLOT and counts as none.  Rows that repeat within one call: one of the writers wins.
+ *
+ * attention_weights: for the rows of chunk c (as in pkv_paged_chunk_attention) and key j < q_start_pos[c] + Lq
+ *   w[j] = sum over rows r with q_start_pos[c] + r >= j and over the query heads h of the kv head of
+ *          exp(scale * q[r][h] . K[j] - lse[r][h])
+ *   out[row][kv head][j] = decay * weights[row][kv head][j] + w[j]   for j < q_start_pos[c] and weights given
+ *                        = w[j]                                      otherwise (the chunk's own tokens are new)
+ * Positions from q_start_pos[c] + Lq on, and the rows of chunks without query rows, are left as they were.
+ *   out            (device) the weights' layout; may be `weights` itself, other overlaps not
+ *   weights        (device) or NULL: none so far
+ *   q, cu_q_lens, q_start_pos, block_tables, k_cache   as for pkv_paged_chunk_attention
+ *   lse            (device) fp32 [total_q][num_heads], from pkv_paged_chunk_attention over the same keys
+ *   decay          finite, >= 0
+ * Errors as for pkv_paged_chunk_attention; a chunk longer than max_len sets PKV_DEVERR_CONTEXT_LEN and is left
+ * out.  fp32 sums in an order that does not change from run to run.  Supported as there, scale included.
+ */
+PKV_API pkv_status pkv_attention_weights(float* out, const float* weights, float decay, int num_rows, int max_len,
+                                         const int32_t* rows, const void* q, pkv_dtype q_dtype, const float* lse,
+                                         const int32_t* cu_q_lens, const int32_t* q_start_pos, int num_chunks,
+                                         int total_q, int num_heads, const void* k_cache, const pkv_cache_desc* cache,
+                                         const int32_t* block_tables, int max_blocks_per_seq, float scale,
+                                         pkv_stream_t stream);
+
+/*
+ * evict_select: kept[i][h][0 .. n-1] = the positions that kv head h of sequence i keeps, ascending; the rest of
+ * its max_keep entries become -1.  With L = context_lens[i], n = min(keep_lens[i], L):
+ *   the newest min(recent, n) positions, then the first min(first, what is left of n), then those of the largest
+ *   weights; of equal weights (-0 equals 0; NaN is less than all) the lower position.
+ *   kept           (device) int32 [num_seqs][num_kv_heads][max_keep]
+ *   context_lens, keep_lens (device) int32 [num_seqs]; a context_len outside 0 .. max_len or a keep_len outside
+ *                  0 .. max_keep sets PKV_DEVERR_CONTEXT_LEN and gives -1 throughout, as does a sequence without a row
+ */
+PKV_API pkv_status pkv_evict_select(int32_t* kept, int max_keep, const float* weights, int num_rows, int max_len,
+                                    const int32_t* rows, const int32_t* context_lens, const int32_t* keep_lens,
+                                    int num_seqs, int num_kv_heads, int first, int recent, pkv_stream_t stream);
+
+/*
+ * evict_compact: for every sequence i, kv head h and j < keep_lens[i] with p = kept[i][h][j] >= 0, position j of
+ * dst_tables[i] gets K, V and weight of position p of src_tables[i], in the cache's own type:
+ *   cache[dst_tables[i][j / B]][h][j % B] = cache[src_tables[i][p / B]][h][p % B]
+ *   weights[dst_rows[i]][h][j] = weights[rows[i]][h][p]
+ * as if all were read before any is written.  dst_tables may be src_tables (in place); in general dst_tables[i][b]
+ * is src_tables[i][b] or a block that no table of the call reads, as pkv_bm_evict gives them, and no two sequences write the same block.
+ * kept has to ascend (pkv_evict_select): an entry that does not, or is past its table, sets PKV_DEVERR_CHUNK and is
+ * left out.  keep_lens outside 0 .. max_keep set PKV_DEVERR_CONTEXT_LEN and leave the sequence alone, positions
+ * past max_len the weight; block ids outside the pool set PKV_DEVERR_BLOCK_ID and leave the row out.
+ *   src_tables     (device) int32 [num_seqs][src_max_blocks]; dst_tables [num_seqs][dst_max_blocks]
+ *   weights        (device) or NULL: only K and V move
+ *   dst_rows       (device) or NULL: rows.  Distinct rows; dst_rows[i] is rows[i] or a row that the call does not read
+ * Any cache type, head_dim a multiple of 16.  Launch order as pkv_kv_write, for all four calls.
+ */
+PKV_API pkv_status pkv_evict_compact(void* k_cache, void* v_cache, const pkv_cache_desc* cache, const int32_t* kept,
+                                     int max_keep, const int32_t* keep_lens, const int32_t* src_tables,
+                                     int src_max_blocks, const int32_t* dst_tables, int dst_max_blocks, float* weights,
+                                     int num_rows, int max_len, const int32_t* rows, const int32_t* dst_rows,
+                                     int num_seqs, pkv_stream_t stream);
+
 /* Rotary positions.  Pair i of a head (0 <= i < rotary_dim / 2) turns by position * f_i. */
 typedef enum {
   PKV_ROPE_HALF = 0,         /* pair i is elements i and i + rotary_dim / 2 */
@@ -497,6 +602,18 @@ PKV_API pkv_status pkv_bm_fork(pkv_block_manager* bm, int64_t parent, int64_t ch
 /* Drop the sequence: each block's ref_cnt falls by one; blocks reaching 0 go to the
  * tail of the free queue, in table order. */
 PKV_API pkv_status pkv_bm_free(pkv_block_manager* bm, int64_t seq);
+
+/* Eviction: sequence seqs[i] goes down to its first new_lens[i] positions, which pkv_evict_compact fills with the
+ * tokens that it keeps.  src_tables and src_lens are what it had, dst_tables what it has now: the same blocks, but
+ * a new one in the place of each that another holder shares, whose contents stay.  Blocks past the new length are
+ * released, in table order, after every new block was popped; a block that is written loses its prefix-cache hash.
+ * A sequence whose length does not change keeps its table.  Launch the compaction before anything that uses the
+ * released blocks.
+ *   src_tables int32 [n][src_max_blocks], dst_tables int32 [n][dst_max_blocks], padded with -1; src_lens int32 [n]
+ * PKV_ERR_NO_BLOCKS, changing nothing, if the shared blocks outnumber the free ones. */
+PKV_API pkv_status pkv_bm_evict(pkv_block_manager* bm, const int64_t* seqs, int n, const int32_t* new_lens,
+                                int src_max_blocks, int32_t* src_tables, int32_t* src_lens, int dst_max_blocks,
+                                int32_t* dst_tables);
 
 /* tables int32 [n][max_blocks] (padded with -1), lens int32 [n]. */
 PKV_API pkv_status pkv_bm_export(const pkv_block_manager* bm, const int64_t* seqs, int n, int max_blocks,

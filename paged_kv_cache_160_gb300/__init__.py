@@ -14,12 +14,17 @@ from ._binding import (  # noqa: F401
     cache_desc_fp4,
     fp4_cache_shape,
     lib,
+    pkv_attention_weights,
     pkv_check_bounded_wait,
+    pkv_chunk_workspace_bytes,
     pkv_copy_blocks,
     pkv_decode_workspace_bytes,
+    pkv_evict_compact,
+    pkv_evict_select,
     pkv_get_device_error,
     pkv_kv_read,
     pkv_kv_write,
+    pkv_paged_chunk_attention,
     pkv_paged_decode,
     pkv_paged_decode_append,
     pkv_paged_decode_noalloc,

@@ -91,6 +91,23 @@ def _load() -> ctypes.CDLL:
     lib.pkv_prompt_attention.argtypes = [c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_void_p, c_void_p, c_int,
                                          c_int, c_int, c_int, c_int, c_int, c_int, c_int64, c_int64, c_int64,
                                          c_int64, c_float, c_void_p]
+    lib.pkv_chunk_workspace_bytes.restype = c_size_t
+    lib.pkv_chunk_workspace_bytes.argtypes = [c_int] * 4
+    lib.pkv_paged_chunk_attention.restype = S
+    lib.pkv_paged_chunk_attention.argtypes = [c_void_p, c_void_p, c_void_p, c_int, c_void_p, c_void_p, c_int, c_int,
+                                              c_int, c_void_p, c_void_p, POINTER(CacheDesc), c_void_p, c_int, c_float,
+                                              c_void_p, c_size_t, c_void_p]
+    lib.pkv_attention_weights.restype = S
+    lib.pkv_attention_weights.argtypes = [c_void_p, c_void_p, c_float, c_int, c_int, c_void_p, c_void_p, c_int,
+                                          c_void_p, c_void_p, c_void_p, c_int, c_int, c_int, c_void_p,
+                                          POINTER(CacheDesc), c_void_p, c_int, c_float, c_void_p]
+    lib.pkv_evict_select.restype = S
+    lib.pkv_evict_select.argtypes = [c_void_p, c_int, c_void_p, c_int, c_int, c_void_p, c_void_p, c_void_p, c_int,
+                                     c_int, c_int, c_int, c_void_p]
+    lib.pkv_evict_compact.restype = S
+    lib.pkv_evict_compact.argtypes = [c_void_p, c_void_p, POINTER(CacheDesc), c_void_p, c_int, c_void_p, c_void_p,
+                                      c_int, c_void_p, c_int, c_void_p, c_int, c_int, c_void_p, c_void_p, c_int,
+                                      c_void_p]
     lib.pkv_rope_table.restype = S
     lib.pkv_rope_table.argtypes = [c_void_p, c_int, c_double, c_int, c_double, c_double, c_double, c_double]
     lib.pkv_qk_rotary.restype = S
@@ -120,6 +137,9 @@ def _load() -> ctypes.CDLL:
     lib.pkv_bm_fork.argtypes = [BM, c_int64, c_int64]
     lib.pkv_bm_free.restype = S
     lib.pkv_bm_free.argtypes = [BM, c_int64]
+    lib.pkv_bm_evict.restype = S
+    lib.pkv_bm_evict.argtypes = [BM, POINTER(c_int64), c_int, POINTER(c_int32), c_int, POINTER(c_int32),
+                                 POINTER(c_int32), c_int, POINTER(c_int32)]
     lib.pkv_bm_export.restype = S
     lib.pkv_bm_export.argtypes = [BM, POINTER(c_int64), c_int, c_int, POINTER(c_int32), POINTER(c_int32)]
     lib.pkv_bm_allocate_cached.restype = S
@@ -411,6 +431,114 @@ def pkv_prompt_attention(out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v:
                                     so, sq, sk, sv, scale, _stream(stream)), "pkv_prompt_attention")
 
 
+def pkv_chunk_workspace_bytes(total_q: int, num_heads: int, num_kv_heads: int, head_dim: int) -> int:
+    return int(lib.pkv_chunk_workspace_bytes(total_q, num_heads, num_kv_heads, head_dim))
+
+
+def _chunks(q: torch.Tensor, cu_q_lens: torch.Tensor, q_start_pos: torch.Tensor, desc: CacheDesc,
+            block_tables: torch.Tensor, lse: Optional[torch.Tensor]):
+    """(total_q, num_heads, number of chunks) of the rows of chunks, checked."""
+    assert cu_q_lens.dtype is torch.int32 and q_start_pos.dtype is torch.int32 and block_tables.dtype is torch.int32
+    total, heads, dim = q.shape
+    n = q_start_pos.numel()
+    if cu_q_lens.numel() != n + 1 or block_tables.shape[0] != n:
+        raise ValueError("cu_q_lens, q_start_pos and block_tables are of different numbers of chunks")
+    if dim != desc.head_dim:
+        raise ValueError(f"q: expected heads of {desc.head_dim}, got {list(q.shape)}")
+    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (total, heads)):
+        raise ValueError(f"lse: expected float32 {[total, heads]}, got {lse.dtype} {list(lse.shape)}")
+    return total, heads, n
+
+
+def pkv_paged_chunk_attention(out: torch.Tensor, q: torch.Tensor, cu_q_lens: torch.Tensor, q_start_pos: torch.Tensor,
+                              k_cache: torch.Tensor, v_cache: torch.Tensor, desc: CacheDesc,
+                              block_tables: torch.Tensor, scale: float, workspace: torch.Tensor,
+                              lse: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Causal attention of each sequence's new rows (q and out [total_q, num_heads, head_dim]) over its paged cache of
+    any type; lse (float32 [total_q, num_heads]) gets each row's log of the sum of exponentials."""
+    total, heads, n = _chunks(q, cu_q_lens, q_start_pos, desc, block_tables, lse)
+    if out.dtype is not q.dtype or out.shape != q.shape:
+        raise ValueError(f"out: expected {q.dtype} {list(q.shape)}, got {out.dtype} {list(out.shape)}")
+    _check(lib.pkv_paged_chunk_attention(_dev(out, "out"), _dev(lse, "lse"), _dev(q, "q"), pkv_dtype_of(q),
+                                         _dev(cu_q_lens, "cu_q_lens"), _dev(q_start_pos, "q_start_pos"), n, total, heads,
+                                         _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"), ctypes.byref(desc),
+                                         _dev(block_tables, "block_tables"), block_tables.shape[1], scale,
+                                         _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(),
+                                         _stream(stream)), "pkv_paged_chunk_attention")
+
+
+def _weight_rows(weights: torch.Tensor, name: str, kv_heads: int) -> Tuple[int, int]:
+    """(rows, length) of float32 [rows, num_kv_heads, length]."""
+    if weights.dtype is not torch.float32 or weights.dim() != 3 or weights.shape[1] != kv_heads:
+        raise ValueError(f"{name}: expected float32 [rows, {kv_heads}, length], got {weights.dtype} {list(weights.shape)}")
+    return weights.shape[0], weights.shape[2]
+
+
+def _per_seq(t: Optional[torch.Tensor], name: str, n: int) -> int:
+    if t is not None and (t.dtype is not torch.int32 or t.numel() != n):
+        raise ValueError(f"{name}: expected int32 [{n}], got {t.dtype} {list(t.shape)}")
+    return _dev(t, name)
+
+
+def pkv_attention_weights(out: torch.Tensor, weights: Optional[torch.Tensor], decay: float, q: torch.Tensor,
+                          lse: torch.Tensor, cu_q_lens: torch.Tensor, q_start_pos: torch.Tensor, k_cache: torch.Tensor,
+                          desc: CacheDesc, block_tables: torch.Tensor, scale: float,
+                          rows: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Adds the attention that each cached token gets from the chunks' rows to decay * weights (float32 [rows,
+    num_kv_heads, max_len]; None: nothing so far); out may be weights.  Chunk i has row rows[i], or i."""
+    total, heads, n = _chunks(q, cu_q_lens, q_start_pos, desc, block_tables, lse)
+    num_rows, max_len = _weight_rows(out, "out", desc.num_kv_heads)
+    if weights is not None and (weights.dtype is not torch.float32 or weights.shape != out.shape):
+        raise ValueError(f"weights: expected float32 {list(out.shape)}, got {weights.dtype} {list(weights.shape)}")
+    if rows is None and num_rows < n:
+        raise ValueError(f"out: {num_rows} rows for {n} chunks")
+    _check(lib.pkv_attention_weights(_dev(out, "out"), _dev(weights, "weights"), decay, num_rows, max_len,
+                                     _per_seq(rows, "rows", n), _dev(q, "q"), pkv_dtype_of(q), _dev(lse, "lse"),
+                                     _dev(cu_q_lens, "cu_q_lens"), _dev(q_start_pos, "q_start_pos"), n, total, heads,
+                                     _dev(k_cache, "k_cache"), ctypes.byref(desc), _dev(block_tables, "block_tables"),
+                                     block_tables.shape[1], scale, _stream(stream)), "pkv_attention_weights")
+
+
+def pkv_evict_select(kept: torch.Tensor, weights: torch.Tensor, context_lens: torch.Tensor, keep_lens: torch.Tensor,
+                     first: int = 0, recent: int = 0, rows: Optional[torch.Tensor] = None, stream=None) -> None:
+    """kept (int32 [num_seqs, num_kv_heads, max_keep]) gets the positions that each kv head keeps, ascending, then -1:
+    the newest `recent`, the `first` ones, and those of the largest weights."""
+    n = context_lens.numel()
+    if kept.dtype is not torch.int32 or kept.dim() != 3 or kept.shape[0] != n:
+        raise ValueError(f"kept: expected int32 [{n}, num_kv_heads, max_keep], got {kept.dtype} {list(kept.shape)}")
+    num_rows, max_len = _weight_rows(weights, "weights", kept.shape[1])
+    if rows is None and num_rows < n:
+        raise ValueError(f"weights: {num_rows} rows for {n} sequences")
+    _check(lib.pkv_evict_select(_dev(kept, "kept"), kept.shape[2], _dev(weights, "weights"), num_rows, max_len,
+                                _per_seq(rows, "rows", n), _per_seq(context_lens, "context_lens", n),
+                                _per_seq(keep_lens, "keep_lens", n), n, kept.shape[1], first, recent, _stream(stream)),
+           "pkv_evict_select")
+
+
+def pkv_evict_compact(k_cache: torch.Tensor, v_cache: torch.Tensor, desc: CacheDesc, kept: torch.Tensor,
+                      keep_lens: torch.Tensor, src_tables: torch.Tensor, dst_tables: Optional[torch.Tensor] = None,
+                      weights: Optional[torch.Tensor] = None, rows: Optional[torch.Tensor] = None,
+                      dst_rows: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Moves the kept rows of each (sequence, kv head), and their weights, to the front of dst_tables (None: in
+    place).  A destination block is the source's at the same place or one that the call does not read."""
+    n = src_tables.shape[0]
+    dst_tables = src_tables if dst_tables is None else dst_tables
+    assert src_tables.dtype is torch.int32 and dst_tables.dtype is torch.int32 and dst_tables.shape[0] == n
+    if kept.dtype is not torch.int32 or kept.dim() != 3 or kept.shape[:2] != (n, desc.num_kv_heads):
+        raise ValueError(f"kept: expected int32 [{n}, {desc.num_kv_heads}, max_keep], got {kept.dtype} {list(kept.shape)}")
+    num_rows = max_len = 0
+    if weights is not None:
+        num_rows, max_len = _weight_rows(weights, "weights", desc.num_kv_heads)
+        if rows is None and num_rows < n:
+            raise ValueError(f"weights: {num_rows} rows for {n} sequences")
+    _check(lib.pkv_evict_compact(_dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"), ctypes.byref(desc),
+                                 _dev(kept, "kept"), kept.shape[2], _per_seq(keep_lens, "keep_lens", n),
+                                 _dev(src_tables, "src_tables"), src_tables.shape[1], _dev(dst_tables, "dst_tables"),
+                                 dst_tables.shape[1], _dev(weights, "weights"), num_rows, max_len,
+                                 _per_seq(rows, "rows", n), _per_seq(dst_rows, "dst_rows", n), n, _stream(stream)),
+           "pkv_evict_compact")
+
+
 def pkv_rope_table(rotary_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
                    original_context: float = 0.0, alpha: float = 1.0, beta: float = 32.0) -> torch.Tensor:
     """Frequencies for pkv_qk_rotary (int64 [rotary_dim / 2] on the host; move it to the device once).
@@ -554,6 +682,19 @@ class BlockManager:
 
     def is_swapped(self, seq: int) -> int:
         return lib.pkv_bm_is_swapped(self._h, seq)
+
+    def evict(self, seqs: Sequence[int], new_lens: Sequence[int], src_max_blocks: int, dst_max_blocks: int):
+        """Cut the sequences to new_lens; (tables before, lens before, tables after), padded with -1."""
+        n = len(seqs)
+        if len(new_lens) != n:
+            raise ValueError(f"{len(new_lens)} lengths for {n} sequences")
+        s = (c_int64 * max(1, n))(*seqs)
+        src, dst = (c_int32 * max(1, n * src_max_blocks))(), (c_int32 * max(1, n * dst_max_blocks))()
+        lens = (c_int32 * max(1, n))()
+        _check(lib.pkv_bm_evict(self._h, s, n, _i32(new_lens), src_max_blocks, src, lens, dst_max_blocks, dst),
+               "pkv_bm_evict")
+        rows = lambda t, w: [list(t[i * w:(i + 1) * w]) for i in range(n)]  # noqa: E731
+        return rows(src, src_max_blocks), list(lens[:n]), rows(dst, dst_max_blocks)
 
     def export(self, seqs: Sequence[int], max_blocks: int):
         n = len(seqs)

@@ -71,12 +71,15 @@ struct pkv_block_manager {
     int32_t b = head;
     unlink(b);
     ref[b] = 1;
-    if (has_hash[b]) {    // the block gets new contents: its cached prefix is gone
-      auto it = hash_to_block.find(bhash[b]);
-      if (it != hash_to_block.end() && it->second == b) hash_to_block.erase(it);
-      has_hash[b] = 0;
-    }
+    drop_hash(b);
     return b;
+  }
+  // The block gets new contents: its cached prefix is gone.
+  void drop_hash(int32_t b) {
+    if (!has_hash[b]) return;
+    auto it = hash_to_block.find(bhash[b]);
+    if (it != hash_to_block.end() && it->second == b) hash_to_block.erase(it);
+    has_hash[b] = 0;
   }
   // Prefix-cache hit: one more holder; a block nobody held leaves the free queue.
   void touch(int32_t b) {
@@ -268,6 +271,56 @@ pkv_status pkv_bm_free(pkv_block_manager* bm, int64_t seq) {
     for (int32_t b : it->second.blocks) bm->release(b);
   }
   bm->seqs.erase(it);
+  return PKV_OK;
+}
+
+pkv_status pkv_bm_evict(pkv_block_manager* bm, const int64_t* seqs, int n, const int32_t* new_lens, int src_max_blocks,
+                        int32_t* src_tables, int32_t* src_lens, int dst_max_blocks, int32_t* dst_tables) {
+  if (!bm || n < 0 || src_max_blocks < 0 || dst_max_blocks < 0) return PKV_ERR_INVALID_ARG;
+  if (n > 0 && (!seqs || !new_lens || !src_tables || !src_lens || !dst_tables)) return PKV_ERR_INVALID_ARG;
+  std::unordered_set<int64_t> seen;
+  std::vector<Seq*> batch(n);
+  // A block that others hold too, when the call begins, is read but not written: the sequence gets one of its own.
+  std::vector<std::vector<uint8_t>> fresh(n);
+  int64_t need = 0;
+  for (int i = 0; i < n; ++i) {
+    Seq* s = batch[i] = bm->resident(seqs[i]);
+    if (!s || !seen.insert(seqs[i]).second || new_lens[i] < 0 || new_lens[i] > s->n_tokens || s->n_tokens > INT32_MAX ||
+        int64_t(s->blocks.size()) > src_max_blocks || bm->blocks_for(new_lens[i]) > dst_max_blocks)
+      return PKV_ERR_INVALID_ARG;
+    if (new_lens[i] == s->n_tokens) continue;
+    fresh[i].assign(bm->blocks_for(new_lens[i]), 0);
+    for (size_t k = 0; k < fresh[i].size(); ++k) need += fresh[i][k] = bm->ref[s->blocks[k]] > 1;
+  }
+  if (need > bm->num_free) return PKV_ERR_NO_BLOCKS;
+  for (int i = 0; i < n; ++i) {
+    const Seq& s = *batch[i];
+    int32_t* row = src_tables + int64_t(i) * src_max_blocks;
+    for (size_t k = 0; k < size_t(src_max_blocks); ++k) row[k] = k < s.blocks.size() ? s.blocks[k] : -1;
+    src_lens[i] = int32_t(s.n_tokens);
+  }
+  // Every pop before the first release: no block that the call still reads becomes one that it writes.
+  std::vector<int32_t> released;
+  for (int i = 0; i < n; ++i) {
+    Seq& s = *batch[i];
+    if (new_lens[i] != s.n_tokens) {
+      const size_t kept = fresh[i].size();
+      for (size_t k = 0; k < kept; ++k) {
+        if (fresh[i][k]) {
+          released.push_back(s.blocks[k]);
+          s.blocks[k] = bm->pop_head();
+        } else {
+          bm->drop_hash(s.blocks[k]);
+        }
+      }
+      released.insert(released.end(), s.blocks.begin() + kept, s.blocks.end());
+      s.blocks.resize(kept);
+      s.n_tokens = new_lens[i];
+    }
+    int32_t* row = dst_tables + int64_t(i) * dst_max_blocks;
+    for (size_t k = 0; k < size_t(dst_max_blocks); ++k) row[k] = k < s.blocks.size() ? s.blocks[k] : -1;
+  }
+  for (int32_t b : released) bm->release(b);
   return PKV_OK;
 }
 
