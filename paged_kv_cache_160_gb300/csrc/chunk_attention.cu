@@ -140,11 +140,10 @@ __device__ __noinline__ void give_back(const ChunkParams& p, pkv_dtype kv, int s
 }
 
 // ---------------------------------------------------------------------------------------
-//   warps 0-3  : softmax of chain A, warps 4-7: of chain B; a thread per row
+//   warps 0-3  : softmax of chain A, warps 4-7: of chain B; a thread per row.  Also the queries of items of two blocks
 //   warps 8-11 : K tiles; warps 12-15: V tiles (16-bit caches: warp 8 asks for K and warp 9 for V by TMA; warps 12-15 look
 //                at V tiles that some rows see only in part: 0 * V must not turn the rows' other keys into NaN.  Values that are
-//                not finite become zeros there, and the rows that do see them get them back at the end).  Items of two blocks:
-//                also their queries
+//                not finite become zeros there, and the rows that do see them get them back at the end).
 //   warp 16    : cuts this CTA's range of the work into items and hands them to the other warps
 //   warp 17    : TMEM owner and MMA issuer, in the order S(0) S(1) | PV(n) S(n + 2) ..., step n in chain n mod 2
 //   warps 18-19: queries of items of one block, in the two query areas by turns, ahead of the products
@@ -276,18 +275,117 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tS = tmem + 128 * x + lane_off, tO = tmem + 256 + lane_off;
     uint32_t steps = 0, turn = 0, merges = 0;                // this chain's steps; items of one block
     Pair uses;                                               // of the query areas
-    for (uint32_t i = 0;; ++i) {
-      ok = ok && wait_item(i);
+    // The item before this one is written after this one's queries (of two blocks) are under way.
+    Item it = {};
+    bool two = false, busy = false;
+    int rows = 0, f = 0, qrow = 0, keys = 0, nx = 0;
+    float m = 0.f, l = 0.f;
+    for (uint32_t n = 0;; ++n) {
+      ok = ok && wait_item(n);
       if (!ok) break;
-      const Item it = read_item(i);
-      done_reading(i);
-      if (it.rows == 0) break;
-      const bool two = it.two();
-      const int tiles = it.t1 - it.t0, nx = two ? tiles : (tiles + 1 - x) / 2;
-      const int rows = two ? (x == 0 ? kTile : it.rows - kTile) : it.rows;   // of this chain's block
-      const bool busy = 32 * quarter < rows;                 // some row of this warp exists
-      const int f = it.f0 + (two ? kTile * x : 0) + min(r, rows - 1);
-      const int qrow = int(p.group.quotient(f)), keys = it.start + qrow + 1;
+      const Item next = read_item(n);
+      done_reading(n);
+      if (next.two()) {
+        ok = all(uses[x] == 0 || mbar_wait(&bar_q_empty[x], (uses[x] - 1) & 1u));
+        if (!ok) break;
+        load_queries<kBF16, !kWide, D, 128>(smem_u32(sQ) + x * C::kTileBytes, factor[x][uses[x] & 1u], p.q, next.q0, p.num_heads,
+                                            next.h, p.group, next.f0 + kTile * x, x == 0 ? kTile : next.rows - kTile, p.scale_log2,
+                                            !kWide && p.k_scale ? __ldg(p.k_scale + next.h) : 1.f, int(threadIdx.x & 127));
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar_q[x]);
+      }
+      if (n > 0) {
+        // ---------------- output of item n - 1 ----------------
+        const uint32_t i = n - 1;
+        ok = ok && (nx == 0 || all(mbar_wait(&bar_pv_done[x], (steps - 1) & 1u)));
+        if (!ok) break;
+        // m = -inf stands for no keys; a row whose scores are all NaN has some.
+        if (m == -INFINITY && l != 0.f) m = 0.f;
+        float2 ml0 = make_float2(m, l), ml1 = make_float2(-INFINITY, 0.f);     // of the chains that hold this row
+        if (!two) {
+          const int par = merges & 1u;
+          tc_fence_after();
+          tc_fence_before();
+          chain_ml[par][x][r] = make_float2(m, l);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar_ml);
+          ok = all(mbar_wait(&bar_ml, par));
+          if (!ok) break;
+          ++merges;
+          ml0 = chain_ml[par][0][r];
+          ml1 = chain_ml[par][1][r];
+        }
+        tc_fence_after();
+        const float top = fmaxf(ml0.x, ml1.x);
+        const bool have0 = ml0.x != -INFINITY, have1 = ml1.x != -INFINITY;
+        float w0 = have0 ? fast_exp2(ml0.x - top) : 0.f, w1 = have1 ? fast_exp2(ml1.x - top) : 0.f;
+        const float sum = w0 * ml0.y + w1 * ml1.y;
+        const bool taken = *static_cast<volatile int*>(&masked_item[i % (2 * kItems)]) == int(i) + 1;
+        const int64_t unit = (int64_t(it.q0) + qrow) * p.num_heads + int64_t(it.h) * G + (f - qrow * G);   // row of out
+        const float vs = !kWide && p.v_scale ? __ldg(p.v_scale + it.h) : 1.f;
+        const float scale = it.slot >= 0 ? 1.f : sum == 0.f ? 0.f : vs / sum;
+        w0 *= scale;
+        w1 *= scale;
+        float* part_o = nullptr;
+        if (it.slot >= 0) {
+          uint8_t* body = p.parts + size_t(gridDim.x) * 2 * sizeof(Part) + size_t(it.slot) * part_bytes(p.part_rows, D);
+          const int pr = (two ? kTile * x : 0) + r;
+          part_o = reinterpret_cast<float*>(body + part_head(p.part_rows)) + size_t(pr) * D;
+          if (r < rows && (two || x == 0)) reinterpret_cast<float2*>(body)[pr] = make_float2(top, sum);
+        } else if (p.lse && r < rows && (two || x == 0)) {
+          p.lse[unit] = (top + log2f(sum)) * 0.6931471805599453f;
+        }
+        // Items of one block: each chain writes half of the elements, from both chains' O.
+        const int c0 = two ? 0 : x * (D / 64), c1 = two ? D / 32 : c0 + D / 64;
+        if (busy) {
+          for (int cc = c0; cc < c1; ++cc) {
+            float v[32];
+            if (two) {
+              tmem_ld32(tO + 128 * x + 32 * cc, v);
+              tmem_wait_ld();
+  #pragma unroll
+              for (int c = 0; c < 32; ++c) v[c] = have0 ? v[c] * w0 : 0.f;
+            } else {
+              float b[32];
+              tmem_ld32(tO + 32 * cc, v);
+              tmem_ld32(tO + 128 + 32 * cc, b);
+              tmem_wait_ld();
+  #pragma unroll
+              for (int c = 0; c < 32; ++c) v[c] = (have0 ? v[c] * w0 : 0.f) + (have1 ? b[c] * w1 : 0.f);
+            }
+            if (r < rows) {
+              if (it.slot >= 0) {
+  #pragma unroll
+                for (int c = 0; c < 8; ++c)
+                  reinterpret_cast<float4*>(part_o)[8 * cc + c] = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+              } else {
+                uint4* dst = reinterpret_cast<uint4*>(p.out + unit * (2 * D) + 64 * cc);
+  #pragma unroll
+                for (int c = 0; c < 4; ++c)
+                  dst[c] = make_uint4(pack2<kBF16>(v[8 * c], v[8 * c + 1]), pack2<kBF16>(v[8 * c + 2], v[8 * c + 3]),
+                                      pack2<kBF16>(v[8 * c + 4], v[8 * c + 5]), pack2<kBF16>(v[8 * c + 6], v[8 * c + 7]));
+              }
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar_o_free);
+        if (taken && r < rows)
+          give_back<kBF16, D>(p, pkv_dtype(KV), it.seq, it.h, max(it.masked, it.t0) * kTile, min(keys, it.t1 * kTile), 32 * c0, 32 * c1,
+                              it.slot < 0 ? vs : 1.f, p.out + unit * (2 * D), part_o);
+      }
+      if (next.rows == 0) break;
+      it = next;
+      two = it.two();
+      const int tiles = it.t1 - it.t0;
+      nx = two ? tiles : (tiles + 1 - x) / 2;
+      rows = two ? (x == 0 ? kTile : it.rows - kTile) : it.rows;             // of this chain's block
+      busy = 32 * quarter < rows;                            // some row of this warp exists
+      f = it.f0 + (two ? kTile * x : 0) + min(r, rows - 1);
+      qrow = int(p.group.quotient(f));
+      keys = it.start + qrow + 1;
       const int area = two ? x : int(turn & 1u);
       const float* fac = &factor[area][uses[area] & 1u][min(r, rows - 1)];
       if (two) {
@@ -297,7 +395,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         uses.up(area);
         ++turn;
       }
-      float m = -INFINITY, l = 0.f, slog = 0.f;
+      m = -INFINITY;
+      l = 0.f;
+      float slog = 0.f;
       for (int k = 0; k < nx && ok; ++k) {
         const int tile = it.t0 + (two ? k : 2 * k + x);
         // Waiting for the last PV on every step keeps that barrier at most one phase ahead of this wait.
@@ -378,111 +478,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&bar_p_full[x]);
       }
       steps += nx;
-      ok = ok && (nx == 0 || all(mbar_wait(&bar_pv_done[x], (steps - 1) & 1u)));
-      if (!ok) break;
-      // ---------------- output ----------------
-      // m = -inf stands for no keys; a row whose scores are all NaN has some.
-      if (m == -INFINITY && l != 0.f) m = 0.f;
-      float2 ml0 = make_float2(m, l), ml1 = make_float2(-INFINITY, 0.f);     // of the chains that hold this row
-      if (!two) {
-        const int par = merges & 1u;
-        tc_fence_after();
-        tc_fence_before();
-        chain_ml[par][x][r] = make_float2(m, l);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar_ml);
-        ok = all(mbar_wait(&bar_ml, par));
-        if (!ok) break;
-        ++merges;
-        ml0 = chain_ml[par][0][r];
-        ml1 = chain_ml[par][1][r];
-      }
-      tc_fence_after();
-      const float top = fmaxf(ml0.x, ml1.x);
-      const bool have0 = ml0.x != -INFINITY, have1 = ml1.x != -INFINITY;
-      float w0 = have0 ? fast_exp2(ml0.x - top) : 0.f, w1 = have1 ? fast_exp2(ml1.x - top) : 0.f;
-      const float sum = w0 * ml0.y + w1 * ml1.y;
-      const bool taken = *static_cast<volatile int*>(&masked_item[i % (2 * kItems)]) == int(i) + 1;
-      const int64_t unit = (int64_t(it.q0) + qrow) * p.num_heads + int64_t(it.h) * G + (f - qrow * G);   // row of out
-      const float vs = !kWide && p.v_scale ? __ldg(p.v_scale + it.h) : 1.f;
-      const float scale = it.slot >= 0 ? 1.f : sum == 0.f ? 0.f : vs / sum;
-      w0 *= scale;
-      w1 *= scale;
-      float* part_o = nullptr;
-      if (it.slot >= 0) {
-        uint8_t* body = p.parts + size_t(gridDim.x) * 2 * sizeof(Part) + size_t(it.slot) * part_bytes(p.part_rows, D);
-        const int pr = (two ? kTile * x : 0) + r;
-        part_o = reinterpret_cast<float*>(body + part_head(p.part_rows)) + size_t(pr) * D;
-        if (r < rows && (two || x == 0)) reinterpret_cast<float2*>(body)[pr] = make_float2(top, sum);
-      } else if (p.lse && r < rows && (two || x == 0)) {
-        p.lse[unit] = (top + log2f(sum)) * 0.6931471805599453f;
-      }
-      // Items of one block: each chain writes half of the elements, from both chains' O.
-      const int c0 = two ? 0 : x * (D / 64), c1 = two ? D / 32 : c0 + D / 64;
-      if (busy) {
-        for (int cc = c0; cc < c1; ++cc) {
-          float v[32];
-          if (two) {
-            tmem_ld32(tO + 128 * x + 32 * cc, v);
-            tmem_wait_ld();
-#pragma unroll
-            for (int c = 0; c < 32; ++c) v[c] = have0 ? v[c] * w0 : 0.f;
-          } else {
-            float b[32];
-            tmem_ld32(tO + 32 * cc, v);
-            tmem_ld32(tO + 128 + 32 * cc, b);
-            tmem_wait_ld();
-#pragma unroll
-            for (int c = 0; c < 32; ++c) v[c] = (have0 ? v[c] * w0 : 0.f) + (have1 ? b[c] * w1 : 0.f);
-          }
-          if (r < rows) {
-            if (it.slot >= 0) {
-#pragma unroll
-              for (int c = 0; c < 8; ++c)
-                reinterpret_cast<float4*>(part_o)[8 * cc + c] = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
-            } else {
-              uint4* dst = reinterpret_cast<uint4*>(p.out + unit * (2 * D) + 64 * cc);
-#pragma unroll
-              for (int c = 0; c < 4; ++c)
-                dst[c] = make_uint4(pack2<kBF16>(v[8 * c], v[8 * c + 1]), pack2<kBF16>(v[8 * c + 2], v[8 * c + 3]),
-                                    pack2<kBF16>(v[8 * c + 4], v[8 * c + 5]), pack2<kBF16>(v[8 * c + 6], v[8 * c + 7]));
-            }
-          }
-        }
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar_o_free);
-      if (taken && r < rows)
-        give_back<kBF16, D>(p, pkv_dtype(KV), it.seq, it.h, max(it.masked, it.t0) * kTile, min(keys, it.t1 * kTile), 32 * c0, 32 * c1,
-                            it.slot < 0 ? vs : 1.f, p.out + unit * (2 * D), part_o);
     }
   } else if (warp < 16) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
     // ---------------- K and V tiles ----------------
     const bool is_v = warp >= 12;
     const int w = warp & 3, tid = threadIdx.x & 127;
-    uint32_t kt = 0, turn = 0;                               // tiles; items of one block
-    Pair uses;                                               // of the query areas
-    // The queries of this warpgroup's block of an item of two.
-    auto item_begins = [&](const Item& it) {
-      const int x = is_v ? 1 : 0;
-      if (it.two()) {
-        ok = ok && all(uses[x] == 0 || mbar_wait(&bar_q_empty[x], (uses[x] - 1) & 1u));
-        if (ok) {
-          load_queries<kBF16, !kWide, D, 128>(smem_u32(sQ) + x * C::kTileBytes, factor[x][uses[x] & 1u], p.q, it.q0, p.num_heads, it.h, p.group,
-                                              it.f0 + kTile * x, x == 0 ? kTile : it.rows - kTile, p.scale_log2,
-                                              !kWide && p.k_scale ? __ldg(p.k_scale + it.h) : 1.f, tid);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bar_q[x]);
-        }
-        uses.up(0);
-        uses.up(1);
-      } else {
-        uses.up(turn++ & 1u);
-      }
-    };
+    uint32_t kt = 0;
     if constexpr (kWide) {
       const uint64_t pol = l2_policy_evict_last();
       TableWindow win;
@@ -493,7 +495,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         done_reading(i);
         if (it.rows == 0) break;
         win.open(p.pc.tables + int64_t(it.seq) * p.pc.max_blocks, min(p.pc.max_blocks, ((it.end - 1) >> p.pc.block_shift) + 1));
-        item_begins(it);
         for (int t = it.t0; t < it.t1 && ok; ++t, ++kt) {
           const uint32_t st = kt % kStages, n = kt / kStages;
           if (!is_v) {
@@ -547,7 +548,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 going = false;
               } else {
                 t = it.t0;
-                item_begins(it);
               }
             }
             const uint32_t st = kt % kStages, round = kt / kStages;
@@ -555,11 +555,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             going = going && ok;
             if (going) {
               const uint32_t base = smem_u32(is_v ? sV : sK) + st * C::kTileBytes;
+              ahead[u].store(base, w, lane);
               if (is_v && t >= it.masked) {
-                if (ahead[u].template store<true>(base, w, lane))
+                __syncwarp();                                // a row's lanes are of one warp
+                if (make_row_finite<false, D>(base, StoredTile<KV, D>::row_of_lane(w, lane)))
                   *static_cast<volatile int*>(&masked_item[i % (2 * kItems)]) = int(i) + 1;
-              } else {
-                ahead[u].template store<false>(base, w, lane);
               }
               fence_proxy_async_smem();
               __syncwarp();

@@ -111,10 +111,13 @@ struct StoredTile {
     }
   }
 
-  // As fp16 to the operand at `base`.  kFinite: infinities and NaN become zeros; returns whether there were any.
-  template <bool kFinite>
-  __device__ __forceinline__ bool store(uint32_t base, int warp, int lane) const {
-    bool odd = false;
+  // A row for each lane, of the 32 that its warp stores.
+  static __device__ __forceinline__ int row_of_lane(int warp, int lane) {
+    return lane / (kPassRows / 4) * kPassRows + warp * (kPassRows / 4) + lane % (kPassRows / 4);
+  }
+
+  // As fp16 to the operand at `base`.
+  __device__ __forceinline__ void store(uint32_t base, int warp, int lane) const {
     const int s = sub(lane);
 #pragma unroll
     for (int p = 0; p < kPasses; ++p) {
@@ -135,17 +138,9 @@ struct StoredTile {
           o[2] = e4m3x2_to_f16x2(w[2 * c + 1]);
           o[3] = e4m3x2_to_f16x2(w[2 * c + 1] >> 16);
         }
-        if constexpr (kFinite) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if ((o[k] & 0x7C00u) == 0x7C00u) o[k] &= 0xFFFF0000u, odd = true;
-            if ((o[k] & 0x7C000000u) == 0x7C000000u) o[k] &= 0x0000FFFFu, odd = true;
-          }
-        }
         sts128(operand_at(base, r, kChunks * s + c), o[0], o[1], o[2], o[3]);
       }
     }
-    return odd;
   }
 };
 
@@ -174,7 +169,7 @@ __device__ __forceinline__ void load_tile_16bit(uint8_t* dst, const CUtensorMap*
 template <bool kBF16, int D>
 __device__ __forceinline__ bool make_row_finite(uint32_t base, int r) {
   uint32_t m = 0;                                            // the largest magnitudes; NaN if any is
-#pragma unroll
+#pragma unroll 4
   for (int c = 0; c < D / 8; ++c) {
     const uint4 v = lds128(operand_at(base, r, c));
     max_magnitudes<kBF16>(m, v.x);
