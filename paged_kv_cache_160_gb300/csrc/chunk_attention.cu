@@ -10,8 +10,8 @@
 // the same keys, or, for an item of one block, of every other key tile (merged within the CTA).  The list of (item, key tile)
 // is cut into one equal range per SM, whatever the chunks' lengths: few rows over long histories use every SM, and no SM
 // works on for long after the others.  Items that several SMs work on are merged by a second kernel.
-//   Quantised rows are read from their blocks into registers two tiles ahead, turned into fp16 (exact) and stored as
-// operands by 8 warps beside the softmax; 16-bit rows come by TMA.
+//   Quantised rows are read from their blocks into registers, turned into fp16 (exact) and stored as operands by 16 warps
+// beside the softmax; 16-bit rows come by TMA.
 #include <algorithm>
 
 #include "paged_tiles.cuh"
@@ -20,14 +20,14 @@
 namespace pkv {
 namespace {
 
-constexpr int kThreads = 640;
+constexpr int kThreads = 896;
 constexpr uint32_t kTmemCols = 512;           // S_A | S_B | O_A | O_B, 128 columns each
 constexpr float kRescaleThreshold = 8.f;      // log2 units
 constexpr int kItems = 8;                     // items on their way from the scheduler to the other warps
 constexpr int kItemRows = 2 * kTile;
 constexpr int kMaxChunks = 65535;
 constexpr int kSeqChunk = 32;                 // chunks per entry of the table of work
-constexpr int kReaders = 8 + 8 + 1 + 2;       // warps that read the items: softmax, loaders, MMA, queries
+constexpr int kReaders = 8 + 16 + 1 + 2;      // warps that read the items: softmax, loaders, MMA, queries
 constexpr int kMergeThreads = 256;
 
 struct ChunkParams {
@@ -141,12 +141,13 @@ __device__ __noinline__ void give_back(const ChunkParams& p, pkv_dtype kv, int s
 
 // ---------------------------------------------------------------------------------------
 //   warps 0-3  : softmax of chain A, warps 4-7: of chain B; a thread per row.  Also the queries of items of two blocks
-//   warps 8-11 : K tiles; warps 12-15: V tiles (16-bit caches: warp 8 asks for K and warp 9 for V by TMA; warps 12-15 look
-//                at V tiles that some rows see only in part: 0 * V must not turn the rows' other keys into NaN.  Values that are
-//                not finite become zeros there, and the rows that do see them get them back at the end).
-//   warp 16    : cuts this CTA's range of the work into items and hands them to the other warps
-//   warp 17    : TMEM owner and MMA issuer, in the order S(0) S(1) | PV(n) S(n + 2) ..., step n in chain n mod 2
-//   warps 18-19: queries of items of one block, in the two query areas by turns, ahead of the products
+//   warps 8-23 : the quantised tiles, four warps each for K and V tiles of even and odd number.  (16-bit caches: warp 8 asks
+//                for K and warp 9 for V by TMA.)  V tiles that some rows see only in part are looked at: 0 * V must not turn the
+//                rows' other keys into NaN.  Values that are not finite become zeros there, and the rows that do see them get
+//                them back at the end
+//   warp 24    : cuts this CTA's range of the work into items and hands them to the other warps
+//   warp 25    : TMEM owner and MMA issuer, in the order S(0) S(1) | PV(n) S(n + 2) ..., step n in chain n mod 2
+//   warps 26-27: queries of items of one block, in the two query areas by turns, ahead of the products
 // Every barrier's phases are counted over all items by each of its users.
 // ---------------------------------------------------------------------------------------
 template <int KV, bool kBF16, int D>
@@ -207,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&bar_drain, 1);
     fence_mbar_init();
   }
-  if (warp == 17) {
+  if (warp == 25) {
     tmem_alloc(&tmem_base_sh, kTmemCols);
     tmem_relinquish();
   }
@@ -268,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   bool ok = true;
 
   if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");    // 256 * 104 + 256 * 104 + 128 * 64 = 640 * 96
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");     // 256 * 96 + 512 * 64 + 128 * 56 = 896 * 72
     // ---------------- softmax and output: a thread per row ----------------
     const int x = warp >> 2, quarter = warp & 3, r = 32 * quarter + lane;    // TMEM lane == row of the block
     const uint32_t lane_off = uint32_t(32 * quarter) << 16;
@@ -407,17 +408,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (busy) {
           if (k == 0) slog = *fac;
           const int lim = keys - tile * kTile;               // keys 0 .. lim - 1 are attended
-          const bool cut = __any_sync(0xffffffffu, lim < kTile);
-          float mt = -INFINITY;
+          if (__any_sync(0xffffffffu, lim < kTile)) {        // the others' scores: -inf
+#pragma unroll 1
+            for (int cc = 0; cc < 4; ++cc) {
+              float s[32];
+              tmem_ld32(tS + 32 * cc, s);
+              tmem_wait_ld();
 #pragma unroll
+              for (int c = 0; c < 32; ++c) s[c] = 32 * cc + c < lim ? s[c] : -INFINITY;
+              tmem_st32(tS + 32 * cc, s);
+            }
+            tmem_wait_st();
+          }
+          float mt = -INFINITY;
+#pragma unroll 1
           for (int cc = 0; cc < 4; ++cc) {
             float s[32];
             tmem_ld32(tS + 32 * cc, s);
             tmem_wait_ld();
-            if (cut) {
-#pragma unroll
-              for (int c = 0; c < 32; ++c) s[c] = 32 * cc + c < lim ? s[c] : -INFINITY;
-            }
             float c4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
             for (int c = 4; c < 32; c += 8) {
@@ -427,8 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             mt = fmaxf(mt, fmaxf(fmaxf(c4[0], c4[1]), fmaxf(c4[2], c4[3])));
           }
-          // (slog >= 0.  A row without keys so far: 0 * -inf would be NaN.)
-          mt = mt == -INFINITY ? mt : mt * slog;
+          mt *= slog;                                        // (slog > 0)
           const bool grow = mt > m + kRescaleThreshold;      // also true for the first keys
           const float m_prev = m;
           if (grow) m = mt;
@@ -437,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float mu = m == -INFINITY ? 0.f : m;
           const uint64_t sl2 = pack_f32x2(slog, slog), nm2 = pack_f32x2(-mu, -mu);
           uint64_t acc0 = pack_f32x2(0.f, 0.f), acc1 = acc0;
-#pragma unroll
+#pragma unroll 1
           for (int cc = 0; cc < 4; ++cc) {
             float s[32];
             tmem_ld32(tS + 32 * cc, s);
@@ -445,9 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t w[16];
 #pragma unroll
             for (int c = 0; c < 16; ++c) {
-              uint64_t x2 = fma_f32x2(pack_f32x2(s[2 * c], s[2 * c + 1]), sl2, nm2);
-              if (cut)
-                x2 = pack_f32x2(32 * cc + 2 * c < lim ? lo_f32(x2) : -INFINITY, 32 * cc + 2 * c + 1 < lim ? hi_f32(x2) : -INFINITY);
+              const uint64_t x2 = fma_f32x2(pack_f32x2(s[2 * c], s[2 * c + 1]), sl2, nm2);
               const float pa = fast_exp2(lo_f32(x2)), pb = fast_exp2(hi_f32(x2));
               const uint64_t p2 = pack_f32x2(pa, pb);
               if (c & 1) acc1 = add_f32x2(acc1, p2);
@@ -458,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (__any_sync(0xffffffffu, grow && k >= 1)) {     // rescale this row of O
             const float alpha = (grow && m_prev != -INFINITY) ? fast_exp2(m_prev - m) : 1.f;
-#pragma unroll
+#pragma unroll 1
             for (int cc = 0; cc < D / 32; ++cc) {
               float v[32];
               tmem_ld32(tO + 128 * x + 32 * cc, v);
@@ -479,14 +484,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       steps += nx;
     }
-  } else if (warp < 16) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+  } else if (warp < 24) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     // ---------------- K and V tiles ----------------
-    const bool is_v = warp >= 12;
-    const int w = warp & 3, tid = threadIdx.x & 127;
-    uint32_t kt = 0;
+    const bool is_v = (warp >> 2 & 1) != 0;
+    const int w = warp & 3, par = warp >= 16;                // quantised: tiles of one parity
     if constexpr (kWide) {
       const uint64_t pol = l2_policy_evict_last();
+      const int tid = threadIdx.x & 127;
+      uint32_t kt = 0;                                       // tiles
       TableWindow win;
       for (uint32_t i = 0; ok; ++i) {
         ok = wait_item(i);
@@ -498,12 +504,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int t = it.t0; t < it.t1 && ok; ++t, ++kt) {
           const uint32_t st = kt % kStages, n = kt / kStages;
           if (!is_v) {
-            if (w > 1) continue;
+            if (w > 1 || par) continue;
             ok = all(n == 0 || mbar_wait(w == 0 ? &bar_k_empty[st] : &bar_v_empty[st], (n - 1) & 1u));
             if (!ok) break;
             load_tile_16bit<D>((w == 0 ? sK : sV) + st * C::kTileBytes, w == 0 ? &tmk : &tmv,
                                w == 0 ? &bar_k_full[st] : &bar_v_full[st], p.pc, win, it.h, t, it.end, lane, pol);
-          } else {
+          } else if (!par) {
             ok = all(mbar_wait(&bar_v_full[st], n & 1u));
             if (!ok) break;
             if (t >= it.masked) {
@@ -521,75 +527,70 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (!is_v && w <= 1) {                                 // no copy may be on its way when the CTA leaves
+      if (!is_v && w <= 1 && !par) {                                 // no copy may be on its way when the CTA leaves
         for (uint32_t u = kt < uint32_t(kStages) ? 0 : kt - kStages; u < kt; ++u)
           (void)mbar_wait(w == 0 ? &bar_k_full[u % kStages] : &bar_v_full[u % kStages], (u / kStages) & 1u);
       }
     } else {
-      // One or two tiles (32 or 40 registers) are on their way in registers (la: the one to load next, it: the one to store next, maybe of an
-      // earlier item).
-      constexpr int kSets = StoredTile<KV, D>::kPasses == 8 ? 1 : 2;
-      StoredTile<KV, D> ahead[kSets];
+      // A tile is on its way in registers while the one before it is turned (la: the item of the tile to load, it: of the
+      // tile to store).  Loops that stay small: with two tiles' registers and code in each of 8 warps, instructions were
+      // fetched more slowly than they ran (8 sequences of 32K to 128K tokens: 391 us).
+      StoredTile<KV, D> ahead;
       TableWindow win;
       const uint8_t* cache = is_v ? p.v_cache : p.k_cache;
-      uint32_t li = 0, i = 0;
+      uint32_t li = 0, i = 0, kt = par;
       Item la = {}, it = {};
-      int lt = 0, t = 0;                                     // their next tiles
-      bool more = true, going = true;
-      for (uint32_t n = 0; going; ++n) {
-#pragma unroll
-        for (int u = 0; u < kSets; ++u) {
-          if (n > 0 && going) {                              // store
-            if (t >= it.t1) {
-              if (it.rows > 0) done_reading(i++);
-              ok = ok && wait_item(i);
-              if (ok) it = read_item(i);
-              if (!ok || it.rows == 0) {
-                going = false;
-              } else {
-                t = it.t0;
-              }
-            }
-            const uint32_t st = kt % kStages, round = kt / kStages;
-            ok = ok && (!going || all(round == 0 || mbar_wait(is_v ? &bar_v_empty[st] : &bar_k_empty[st], (round - 1) & 1u)));
-            going = going && ok;
-            if (going) {
-              const uint32_t base = smem_u32(is_v ? sV : sK) + st * C::kTileBytes;
-              ahead[u].store(base, w, lane);
-              if (is_v && t >= it.masked) {
-                __syncwarp();                                // a row's lanes are of one warp
-                if (make_row_finite<false, D>(base, StoredTile<KV, D>::row_of_lane(w, lane)))
-                  *static_cast<volatile int*>(&masked_item[i % (2 * kItems)]) = int(i) + 1;
-              }
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(is_v ? &bar_v_seen[st] : &bar_k_full[st]);
-              ++kt;
-              ++t;
-            }
+      int lt = par, t = par;                                 // their next tiles
+      bool more = true;
+      while (true) {
+        if (kt >= 2) {                                       // store tile kt - 2
+          while (t >= it.t1) {                               // (first: 0 >= 0)
+            const int over = t - it.t1;
+            if (it.rows > 0) done_reading(i++);
+            ok = ok && wait_item(i);
+            if (!ok) break;
+            it = read_item(i);
+            if (it.rows == 0) break;
+            t = it.t0 + over;
           }
-          if (more && going) {                               // load
-            if (lt >= la.t1) {
-              if (la.rows > 0) ++li;
-              ok = ok && wait_item(li);
-              if (ok) la = read_item(li);
-              more = ok && la.rows > 0;
-              if (more) {
-                lt = la.t0;
-                win.open(p.pc.tables + int64_t(la.seq) * p.pc.max_blocks,
-                         min(p.pc.max_blocks, ((la.end - 1) >> p.pc.block_shift) + 1));
-              }
-            }
-            if (more) ahead[u].load(cache, p.pc, win, la.h, lt++, la.end, w, lane);
+          if (!ok || it.rows == 0) break;
+          const uint32_t n = kt - 2, st = n % kStages, round = n / kStages;
+          ok = all(round == 0 || mbar_wait(is_v ? &bar_v_empty[st] : &bar_k_empty[st], (round - 1) & 1u));
+          if (!ok) break;
+          const uint32_t base = smem_u32(is_v ? sV : sK) + st * C::kTileBytes;
+          ahead.store(base, w, lane);
+          if (is_v && t >= it.masked) {
+            __syncwarp();                                    // a row's lanes are of one warp
+            if (make_row_finite<false, D>(base, StoredTile<KV, D>::row_of_lane(w, lane)))
+              *static_cast<volatile int*>(&masked_item[i % (2 * kItems)]) = int(i) + 1;
           }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(is_v ? &bar_v_seen[st] : &bar_k_full[st]);
+          t += 2;
         }
+        while (more && lt >= la.t1) {
+          const int over = lt - la.t1;
+          if (la.rows > 0) ++li;
+          ok = wait_item(li);
+          if (!ok) break;
+          la = read_item(li);
+          more = la.rows > 0;
+          if (!more) break;
+          lt = la.t0 + over;
+          win.open(p.pc.tables + int64_t(la.seq) * p.pc.max_blocks, min(p.pc.max_blocks, ((la.end - 1) >> p.pc.block_shift) + 1));
+        }
+        if (!ok) break;
+        if (more) ahead.load(cache, p.pc, win, la.h, lt, la.end, w, lane);
+        lt += 2;
+        kt += 2;
       }
       if (ok && it.rows == 0) done_reading(i);
     }
     if (!ok && lane == 0) set_error(p.pc.err, PKV_DEVERR_TIMEOUT);
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-  if (warp == 16) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+  if (warp == 24) {
     // ---------------- this CTA's range of the work, item by item ----------------
     const int64_t total = int64_t(hkv) * first_unit[tables];
     const int64_t lo = total * blockIdx.x / gridDim.x, hi = total * (blockIdx.x + 1) / gridDim.x;
@@ -672,7 +673,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane < 2) reinterpret_cast<Part*>(p.parts)[2 * blockIdx.x + lane] = lane ? parts[1] : parts[0];
     put(Item{});
     if (!ok && lane == 0) set_error(p.pc.err, PKV_DEVERR_TIMEOUT);
-  } else if (warp == 17) {
+  } else if (warp == 25) {
     // ---------------- MMA issuer (the whole warp; see mma_ss) ----------------
     const uint32_t lead = elect_one();
     constexpr uint32_t idesc_s = umma_idesc_f16(kMmaBF16, 128, 128, false, false);
@@ -741,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     (void)mbar_wait(&bar_drain, 0);
   } else {
     // ---------------- queries of items of one block ----------------
-    const int tid = threadIdx.x - 18 * 32;
+    const int tid = threadIdx.x - 26 * 32;
     uint32_t turn = 0;
     Pair uses;
     for (uint32_t i = 0;; ++i) {
@@ -774,7 +775,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 17) {
+  if (warp == 25) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }

@@ -27,11 +27,22 @@ __device__ __forceinline__ uint32_t operand_at(uint32_t base, int row, int c8) {
   return base + (c8 >> 3) * kHalfBytes + swz128(row, c8 & 7);
 }
 
-__device__ __forceinline__ uint4 ld_stream(const void* p) {
+// 16 bytes, or zeros where `on` is not set; no branch.
+__device__ __forceinline__ uint4 ld_stream(const void* p, bool on) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "mov.u32 %0, 0;\n\tmov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\tmov.u32 %3, 0;\n\t"
+      "@p ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}\n"
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+      : "l"(p), "r"(int(on)));
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_16(const void* p, bool on) {
+  uint16_t v;
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\tmov.u16 %0, 0;\n\t@p ld.global.nc.u16 %0, [%1];\n\t}\n"
+               : "=&h"(v)
+               : "l"(p), "r"(int(on)));
   return v;
 }
 
@@ -88,27 +99,27 @@ struct StoredTile {
                                        int end, int warp, int lane) {
     const int per_window = pc.block_shift + 5 - 7;           // log2 of the tiles in a window
     win.move(tile >> per_window, lane);
-    const int s = sub(lane);
+    const int s = sub(lane), j0 = tile * kTile + row(warp, lane, 0);
+    int blk[kPasses];
+    bool missing = false;
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p) blk[p] = win.entry((j0 + p * kPassRows) >> pc.block_shift);
 #pragma unroll
     for (int p = 0; p < kPasses; ++p) {
-      const int j = tile * kTile + row(warp, lane, p);
-      const int blk = win.entry(j >> pc.block_shift);
-      const bool there = unsigned(blk) < unsigned(pc.num_blocks);
-      if (j < end && !there) set_error(pc.err, PKV_DEVERR_BLOCK_ID);
-      code[p] = make_uint4(0, 0, 0, 0);
-      if constexpr (kFp4) scale[p] = 0;
-      if (j < end && there) {
-        const int64_t at = (int64_t(blk) * pc.num_kv_heads + h) * pc.block_size + (j & (pc.block_size - 1));
-        if constexpr (kFp4) {
-          const uint8_t* t = cache + (at >> 4) * (9 * D);
-          const int rr = int(at & 15);
-          code[p] = ld_stream(t + rr * (D / 2) + 16 * s);
-          scale[p] = __ldg(reinterpret_cast<const uint16_t*>(t + 8 * D + rr * (D / 16) + 2 * s));
-        } else {
-          code[p] = ld_stream(cache + at * D + 16 * s);
-        }
+      const int j = j0 + p * kPassRows;
+      const bool there = unsigned(blk[p]) < unsigned(pc.num_blocks), on = j < end && there;
+      missing |= j < end && !there;
+      const int64_t at = (int64_t(blk[p]) * pc.num_kv_heads + h) * pc.block_size + (j & (pc.block_size - 1));
+      if constexpr (kFp4) {
+        const uint8_t* t = cache + (at >> 4) * (9 * D);
+        const int rr = int(at & 15);
+        code[p] = ld_stream(t + rr * (D / 2) + 16 * s, on);
+        scale[p] = ld_16(t + 8 * D + rr * (D / 16) + 2 * s, on);
+      } else {
+        code[p] = ld_stream(cache + at * D + 16 * s, on);
       }
     }
+    if (missing) set_error(pc.err, PKV_DEVERR_BLOCK_ID);
   }
 
   // A row for each lane, of the 32 that its warp stores.
@@ -218,7 +229,7 @@ __device__ __forceinline__ void load_queries(uint32_t base, float* factor, const
         const int f = f0 + r, row = int(group.quotient(f));
         const uint8_t* src = q + ((q0 + row) * num_heads + int64_t(h) * G + (f - row * G)) * (2 * D);
 #pragma unroll
-        for (int c = 0; c < kVec; ++c) v[u][c] = ld_stream(src + 16 * (sub + 8 * c));
+        for (int c = 0; c < kVec; ++c) v[u][c] = ld_stream(src + 16 * (sub + 8 * c), true);
       }
     }
 #pragma unroll
@@ -244,8 +255,10 @@ __device__ __forceinline__ void load_queries(uint32_t base, float* factor, const
         mul = __uint_as_float(uint32_t(127 + shift) << 23);  // shift is -113 .. 126
       }
       if (r < n) {
-        if (sub == 0)
-          factor[r] = kToF16 ? float(double(scale_log2) * fabs(double(head_scale)) * exp2_int(-shift)) : scale_log2;
+        if (sub == 0) {
+          const float c = kToF16 ? float(double(scale_log2) * fabs(double(head_scale)) * exp2_int(-shift)) : scale_log2;
+          factor[r] = c < 1e-35f ? 1e-35f : c;               // not 0 (a head's scale may be): it multiplies -inf; NaN stays
+        }
 #pragma unroll
         for (int c = 0; c < kVec; ++c) {
           uint32_t w[4] = {v[u][c].x, v[u][c].y, v[u][c].z, v[u][c].w};
