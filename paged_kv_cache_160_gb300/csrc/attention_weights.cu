@@ -3,11 +3,29 @@
 //
 // Mathematics: with the rows' log-sum-exp known, p = exp(scale q . k - lse) needs no other key: a key's sum is
 // its own, and nothing is exchanged between keys.
-#include "cache_row.cuh"
-#include "pkv_host.h"
+//
+// GB300 design: S^T = K Q^T on tcgen05, 128 keys by up to 128 flat query rows (row f is head f mod G of query row f / G), so that
+// a tensor memory lane is a key and its thread adds up a row of exponentials without a word to other threads.  Up to four
+// key tiles stay in shared memory while the blocks of query rows pass by, each tile's scores in 128 columns of their own: while one
+// tile's products run, the exponentials of the others are taken.  One or two blocks of rows stay too, and the key tiles pass
+// by.  The list of (chunk, kv head, key tile) is cut over the SMs by the number of blocks that see each tile: no tile's sum is
+// split, so no order of sums depends on the run.
+#include <algorithm>
+
+#include "paged_tiles.cuh"
+#include "umma_issue.cuh"
 
 namespace pkv {
 namespace {
+
+constexpr int kThreads = 896;
+constexpr uint32_t kTmemCols = 512;           // four slots of 128 columns
+constexpr int kSlots = 4;
+constexpr int kItems = 8;                     // items on their way from the scheduler to the other warps
+constexpr int kMaxChunks = 65535;
+constexpr int kSeqChunk = 32;                 // chunks per entry of the table of work
+constexpr int kReaders = 16 + 8 + 1 + 1;      // warps that read the items: exponentials, loaders, MMA, key tiles by TMA
+constexpr int kTileCost = 2;                  // of a key tile beside its blocks: loading it takes about as long as two blocks' products
 
 struct WeightsParams {
   float* out;
@@ -18,64 +36,514 @@ struct WeightsParams {
   const float* lse;
   const int32_t* cu_q;
   const int32_t* start;
-  const int32_t* tables;
   const uint8_t* k_cache;
   const float* k_scale;
-  int num_rows, max_len, num_chunks, total_q, num_heads, num_kv_heads, max_blocks, num_blocks, block_size;
-  pkv_dtype kv;
-  float scale;
-  unsigned* err;
+  int num_rows, max_len, num_chunks, total_q, num_heads;
+  float scale_log2;
+  Divisor group;          // query heads per kv head
+  PagedCache pc;
 };
 
-// A warp per (chunk, kv head, key).
-template <bool kBF16, int D>
-__global__ void __launch_bounds__(256) weights_kernel(const WeightsParams p) {
+// Key tiles of a (chunk, kv head) that this CTA works on.
+struct Item {
+  int seq, h, q0, start;  // chunk, kv head, first query row, its position
+  int F, k0, k1, row;     // flat rows (0: no more items), key tiles, row of the weights
+  __device__ __forceinline__ int blocks() const { return (F + kTile - 1) / kTile; }
+};
+
+// A chunk: its rows, or none where there is nothing to do.
+struct Chunk {
+  int q0, len, start, row;
+  unsigned error;
+  __device__ __forceinline__ Chunk(const WeightsParams& p, int s) {
+    q0 = p.cu_q[s];
+    start = p.start[s];
+    row = p.rows ? p.rows[s] : s;
+    const int64_t n = int64_t(p.cu_q[s + 1]) - q0;
+    error = 0;
+    if (q0 < 0 || n < 0 || q0 + n > p.total_q || start < 0 ||
+        (n > 0 && start + n > (int64_t(p.pc.max_blocks) << p.pc.block_shift)))
+      error = PKV_DEVERR_CHUNK;
+    else if (n > 0 && row >= p.num_rows)
+      error = PKV_DEVERR_SLOT;
+    else if (n > 0 && row >= 0 && start + n > p.max_len)
+      error = PKV_DEVERR_CONTEXT_LEN;
+    len = error || row < 0 ? 0 : int(n);
+  }
+  __device__ __forceinline__ int tiles() const { return len == 0 ? 0 : (start + len + kTile - 1) / kTile; }
+};
+
+// The first block of 128 flat rows that sees key tile t.
+__device__ __forceinline__ int first_block(int start, int G, int t) {
+  const int64_t f = (int64_t(t) * kTile - start) * G;
+  return f > 0 ? int(f / kTile) : 0;
+}
+
+// Key tiles that every block sees; the others come after them.
+__device__ __forceinline__ int old_tiles(const Chunk& c) { return min(c.tiles(), c.start / kTile + 1); }
+
+// Work of a chunk's kv head.
+__device__ __forceinline__ int units_of(const Chunk& c, int G) {
+  if (c.len == 0) return 0;
+  const int blocks = (c.len * G + kTile - 1) / kTile, n = old_tiles(c);
+  int units = n * (blocks + kTileCost);
+  for (int t = n; t < c.tiles(); ++t) units += blocks - first_block(c.start, G, t) + kTileCost;
+  return units;
+}
+
+// The first key tile at or behind `at` units into a chunk's kv head.
+__device__ __forceinline__ int tile_at(const Chunk& c, int G, int64_t at) {
+  if (at <= 0) return 0;
+  const int blocks = (c.len * G + kTile - 1) / kTile, n = old_tiles(c), per = blocks + kTileCost;
+  if (at <= int64_t(n) * per) return int((at + per - 1) / per);
+  at -= int64_t(n) * per;
+  int t = n;
+  for (; t < c.tiles() && at > 0; ++t) at -= blocks - first_block(c.start, G, t) + kTileCost;
+  return t;
+}
+
+template <int D>
+struct Cfg {
+  static constexpr int kTileBytes = D / 64 * kHalfBytes;
+  static constexpr int kSmem = (kSlots + 2) * kTileBytes;    // key tiles, blocks of queries
+};
+
+// ---------------------------------------------------------------------------------------
+//   warps 0-15 : exponentials and sums, four warps for each slot of scores; a thread per key
+//   warps 16-23: the quantised key tiles and the blocks of queries, four warps each for those of even and odd number
+//   warp 24    : cuts this CTA's range of the work into items and hands them to the other warps
+//   warp 25    : TMEM owner and MMA issuer
+//   warp 26    : key tiles of 16-bit caches by TMA
+// An item's key tiles are taken in groups of four (the last may be smaller).  A group's steps are its blocks of queries, and
+// within a block its tiles; tile x of a group has slot x.  A group of one or two tiles has two or four slots for each tile,
+// taken by turns from block to block, and their sums are added at the end.
+// One or two blocks stay for all groups; more pass by once for every group.
+// ---------------------------------------------------------------------------------------
+template <int KV, bool kBF16, int D>
+__global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_constant__ CUtensorMap tmk, const WeightsParams p) {
+  using C = Cfg<D>;
+  constexpr bool kWide = KV == PKV_F16 || KV == PKV_BF16;    // 16-bit caches
+  constexpr bool kMmaBF16 = KV == PKV_BF16;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ __align__(16) int4 items[kItems][2];
+  __shared__ __align__(8) uint64_t bar_item[kItems], bar_item_read[kItems];
+  // Query block there / not read any more; key tiles likewise; scores there / read; sums of a group there.
+  __shared__ __align__(8) uint64_t bar_q[2], bar_q_empty[2], bar_k[kSlots], bar_k_empty[kSlots], bar_s[kSlots], bar_s_free[kSlots],
+      bar_sum, bar_drain;
+  __shared__ uint32_t tmem_base_sh;
+  // [block number mod 8]: (factor, factor, -lse, -lse) of row pairs.  Block u + 8 is loaded once the products of u + 6 are done, and
+  // those of u + 4 at the latest waited for the sums of u.
+  __shared__ __align__(16) float row_terms[8][2 * kTile];
+  __shared__ float sums[2][kSlots][kTile];
+  __shared__ int first_unit[(kMaxChunks + kSeqChunk - 1) / kSeqChunk + 1];
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // uniform in the warp
+
+  uint8_t* sK = smem;                                        // [slot][64-dim half][128 rows]
+  uint8_t* sQ = smem + kSlots * C::kTileBytes;               // [block mod 2][64-dim half][128 rows]
+  if (smem_u32(smem) & 1023u) {                              // the 128-byte swizzle needs 1 KB alignment
+    if (threadIdx.x == 0) set_error(p.pc.err, PKV_DEVERR_CHUNK);
+    return;
+  }
+  if (threadIdx.x == 0) {
+    if constexpr (kWide) prefetch_tensormap(&tmk);
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(&bar_item[i], 1);
+      mbar_init(&bar_item_read[i], kReaders);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar_q[i], 4);
+      mbar_init(&bar_q_empty[i], 1);
+    }
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(&bar_k[i], kWide ? 1 : 4);
+      mbar_init(&bar_k_empty[i], 1);
+      mbar_init(&bar_s[i], 1);
+      mbar_init(&bar_s_free[i], 4);
+    }
+    mbar_init(&bar_sum, 16);
+    mbar_init(&bar_drain, 1);
+    fence_mbar_init();
+  }
+  if (warp == 25) {
+    tmem_alloc(&tmem_base_sh, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base_sh;
   griddep_launch_dependents();
+  // Only the set-up above may run before the previous kernel on the stream has finished.
   griddep_wait();
-  const int lane = threadIdx.x & 31, g = blockIdx.y, G = p.num_heads / p.num_kv_heads;
-  for (int i = blockIdx.z; i < p.num_chunks; i += gridDim.z) {
-    const int64_t q0 = p.cu_q[i], n = p.cu_q[i + 1] - q0, start = p.start[i];
-    const bool one = threadIdx.x == 0 && blockIdx.x == 0 && g == 0;
-    if (one && i == 0 && p.cu_q[0] != 0) set_error(p.err, PKV_DEVERR_CHUNK);
-    if (q0 < 0 || n < 0 || q0 + n > p.total_q || start < 0 || (n > 0 && start + n > int64_t(p.max_blocks) * p.block_size)) {
-      if (one) set_error(p.err, PKV_DEVERR_CHUNK);
-      continue;
+
+  const int G = int(p.group.d), hkv = p.pc.num_kv_heads;
+  auto all = [](bool v) -> bool { return __all_sync(0xffffffffu, v); };
+
+  // The units of each kSeqChunk chunks, then their running sums.
+  const int tables = (p.num_chunks + kSeqChunk - 1) / kSeqChunk;
+  unsigned error = blockIdx.x == 0 && threadIdx.x == 0 && p.cu_q[0] != 0 ? PKV_DEVERR_CHUNK : 0;
+  for (int c = warp; c < tables; c += kThreads / 32) {
+    const int s = c * kSeqChunk + lane;
+    int units = 0;
+    if (s < p.num_chunks) {
+      const Chunk ch(p, s);
+      units = units_of(ch, G);
+      if (blockIdx.x == 0) error |= ch.error;
     }
-    const int row = p.rows ? p.rows[i] : i;
-    if (n == 0 || row < 0) continue;
-    if (row >= p.num_rows || start + n > p.max_len) {
-      if (one) set_error(p.err, row >= p.num_rows ? PKV_DEVERR_SLOT : PKV_DEVERR_CONTEXT_LEN);
-      continue;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) units += __shfl_xor_sync(0xffffffffu, units, o);
+    if (lane == 0) first_unit[c + 1] = units;
+  }
+  if (error) set_error(p.pc.err, error);
+  __syncthreads();
+  if (warp == 0) {
+    int total = 0;
+    for (int c0 = 0; c0 < tables; c0 += 32) {
+      int v = c0 + lane < tables ? first_unit[c0 + lane + 1] : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int w = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += w;
+      }
+      if (c0 + lane < tables) first_unit[c0 + lane + 1] = total + v;
+      total += __shfl_sync(0xffffffffu, v, 31);
     }
-    constexpr int kPairs = D / 64;
-    const float ks = (p.k_scale ? p.k_scale[g] : 1.f) * p.scale;
-    for (int64_t j = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5); j < start + n; j += int64_t(gridDim.x) * 8) {
-      const int blk = p.tables[int64_t(i) * p.max_blocks + j / p.block_size];
-      const bool there = blk >= 0 && blk < p.num_blocks;
-      if (!there && lane == 0) set_error(p.err, PKV_DEVERR_BLOCK_ID);
-      const int64_t at = (int64_t(blk) * p.num_kv_heads + g) * p.block_size + j % p.block_size;
-      float2 k[kPairs];
-      for (int c = 0; c < kPairs; ++c)
-        k[c] = there ? cache_pair(p.k_cache, p.kv, D, at, 32 * c + lane) : make_float2(0.f, 0.f);
-      float sum = 0.f;
-      for (int64_t r = j > start ? j - start : 0; r < n; ++r) {
-        for (int h = g * G; h < (g + 1) * G; ++h) {
-          const int64_t unit = (q0 + r) * p.num_heads + h;
-          float s = 0.f;
-          for (int c = 0; c < kPairs; ++c) {
-            const float2 q = unpack2<kBF16>(reinterpret_cast<const uint32_t*>(p.q)[unit * (D / 2) + 32 * c + lane]);
-            s += q.x * k[c].x + q.y * k[c].y;
+    if (lane == 0) first_unit[0] = 0;
+  }
+  __syncthreads();
+
+  auto wait_item = [&](uint32_t i) -> bool { return all(mbar_wait(&bar_item[i % kItems], i / kItems & 1u)); };
+  auto read_item = [&](uint32_t i) -> Item {
+    const int4 a = items[i % kItems][0], b = items[i % kItems][1];
+    return Item{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  };
+  auto done_reading = [&](uint32_t i) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bar_item_read[i % kItems]);
+  };
+  // Calls group(t, nt, b0) for the groups of nt key tiles from t on, which the blocks from b0 on see.
+  auto each_group = [&](const Item& it, auto group) -> bool {
+    for (int t = it.k0; t < it.k1; t += kSlots) {
+      // Blocks that stay are taken from the first on, so that all groups agree on them.
+      const int b0 = it.blocks() <= 2 ? 0 : first_block(it.start, G, t);
+      if (!group(t, min(kSlots, it.k1 - t), b0)) return false;
+    }
+    return true;
+  };
+  bool ok = true;
+
+  if (warp < 16) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");     // 512 * 64 + 256 * 96 + 128 * 56 = 896 * 72
+    // ---------------- exponentials and sums ----------------
+    const int x = warp >> 2, r = threadIdx.x & 127;          // slot; key of the tile
+    const uint32_t tS = tmem + 128 * x + (uint32_t(32 * (warp & 3)) << 16);
+    uint32_t steps = 0, merges = 0, qc = 0;                  // of this slot; smaller groups; blocks so far
+    for (uint32_t i = 0;; ++i) {
+      ok = ok && wait_item(i);
+      if (!ok) break;
+      const Item it = read_item(i);
+      done_reading(i);
+      if (it.F == 0) break;
+      const int NB = it.blocks();
+      const bool stay = NB <= 2;
+      ok = each_group(it, [&](int t, int nt, int b0) -> bool {
+        const int turns = nt == 1 ? 4 : nt == 2 ? 2 : 1;     // slots of a tile
+        const int mine = x < nt * turns ? x % nt : -1, turn = x / nt;        // tile of the group; which of its slots
+        const int key = (t + max(mine, 0)) * kTile + r;
+        float sum = 0.f, lost = 0.f;                         // compensated
+        for (int b = b0 + turn; mine >= 0 && b < NB; b += turns, ++steps) {
+          const uint32_t use = qc + (b - (stay ? 0 : b0));   // number of the block among all that were loaded
+          if (!all(mbar_wait(&bar_s[x], steps & 1u))) return false;
+          tc_fence_after();
+          const int n = min(kTile, it.F - b * kTile);
+          const int64_t before = (int64_t(key) - it.start) * G - int64_t(b) * kTile;   // rows of the block that do not see the key
+          const int lo = int(max(int64_t(0), min(before, int64_t(kTile))));
+          const bool whole = all(lo == 0 && n == kTile);
+          const float* terms = row_terms[use & 7u];
+          uint64_t acc0 = pack_f32x2(0.f, 0.f), acc1 = acc0;
+          const int chunks = (n + 31) / 32;
+#pragma unroll 1
+          for (int cc = 0; cc < chunks; ++cc) {
+            float s[32];
+            tmem_ld32(tS + 32 * cc, s);
+            tmem_wait_ld();
+            if (whole) {
+#pragma unroll
+              for (int c = 0; c < 16; ++c) {
+                const float4 f = reinterpret_cast<const float4*>(terms)[16 * cc + c];
+                const uint64_t e = fma_f32x2(pack_f32x2(s[2 * c], s[2 * c + 1]), pack_f32x2(f.x, f.y), pack_f32x2(f.z, f.w));
+                const uint64_t pe = pack_f32x2(fast_exp2(lo_f32(e)), fast_exp2(hi_f32(e)));
+                if (c & 1) acc1 = add_f32x2(acc1, pe);
+                else acc0 = add_f32x2(acc0, pe);
+              }
+            } else {
+#pragma unroll
+              for (int c = 0; c < 16; ++c) {
+                const float4 f = reinterpret_cast<const float4*>(terms)[16 * cc + c];
+                const int c0 = 32 * cc + 2 * c;
+                const float e0 = c0 >= lo && c0 < n ? fmaf(s[2 * c], f.x, f.z) : -INFINITY;
+                const float e1 = c0 + 1 >= lo && c0 + 1 < n ? fmaf(s[2 * c + 1], f.y, f.w) : -INFINITY;
+                const uint64_t pe = pack_f32x2(fast_exp2(e0), fast_exp2(e1));
+                if (c & 1) acc1 = add_f32x2(acc1, pe);
+                else acc0 = add_f32x2(acc0, pe);
+              }
+            }
           }
-          for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-          sum += expf(s * ks - p.lse[unit]);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar_s_free[x]);        // the next products may overwrite the scores
+          const uint64_t acc = add_f32x2(acc0, acc1);
+          const float y = lo_f32(acc) + hi_f32(acc) - lost, z = sum + y;
+          lost = (z - sum) - y;
+          if (!(fabsf(lost) < INFINITY)) lost = 0.f;
+          sum = z;
+        }
+        if (nt < kSlots) {                                   // (of three tiles: no sums to add, but no slot is left behind)
+          const int par = merges & 1u;
+          sums[par][x][r] = sum - lost;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar_sum);
+          if (!all(mbar_wait(&bar_sum, par))) return false;
+          ++merges;
+          if (turn == 0 && turns > 1) {
+            sum = 0.f;
+            lost = 0.f;
+            for (int u = 0; u < turns; ++u) sum += sums[par][u * nt + mine][r];
+          }
+        }
+        if (mine >= 0 && turn == 0 && key < it.start + int(p.group.quotient(it.F))) {
+          const int64_t at = (int64_t(it.row) * hkv + it.h) * p.max_len + key;
+          sum -= lost;
+          p.out[at] = p.in && key < it.start ? fmaf(p.decay, p.in[at], sum) : sum;
+        }
+        if (!stay) qc += NB - b0;
+        return true;
+      });
+      if (stay) qc += NB;
+    }
+    if (!ok && lane == 0) set_error(p.pc.err, PKV_DEVERR_TIMEOUT);
+  } else if (warp < 24) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
+    // ---------------- key tiles and queries ----------------
+    const int par = (warp >> 2) & 1, w = warp & 3, tid = threadIdx.x & 127;
+    uint32_t kc = 0, qc = 0, li = 0;                         // key tiles, blocks of queries, item of the tile to load
+    StoredTile<kWide ? int(PKV_FP8_E4M3) : KV, D> ahead;     // (16-bit caches: not used)
+    TableWindow win;
+    Item la = {};
+    int lt = par;                                            // the next tile to load, of item `la`
+    bool more = !kWide;
+    auto load_ahead = [&]() -> bool {
+      while (more && lt >= la.k1) {
+        const int over = lt - la.k1;
+        if (la.F > 0) ++li;
+        if (!wait_item(li)) return false;
+        la = read_item(li);
+        more = la.F > 0;
+        if (!more) break;
+        lt = la.k0 + over;
+        const int end = la.start + int(p.group.quotient(la.F));
+        win.open(p.pc.tables + int64_t(la.seq) * p.pc.max_blocks, min(p.pc.max_blocks, ((end - 1) >> p.pc.block_shift) + 1));
+      }
+      if (more) ahead.load(p.k_cache, p.pc, win, la.h, lt, la.start + int(p.group.quotient(la.F)), w, lane);
+      lt += 2;
+      return true;
+    };
+    ok = load_ahead();
+    for (uint32_t i = 0; ok; ++i) {
+      ok = wait_item(i);
+      if (!ok) break;
+      const Item it = read_item(i);
+      if (it.F == 0) {
+        done_reading(i);
+        break;
+      }
+      const int NB = it.blocks();
+      const bool stay = NB <= 2;
+      ok = each_group(it, [&](int t, int nt, int b0) -> bool {
+        for (int u = 0; u < nt; ++u, ++kc) {
+          if (kWide || (kc & 1u) != uint32_t(par)) continue;
+          const uint32_t st = kc % kSlots, round = kc / kSlots;
+          if (!all(round == 0 || mbar_wait(&bar_k_empty[st], (round - 1) & 1u))) return false;
+          ahead.store(smem_u32(sK) + st * C::kTileBytes, w, lane);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar_k[st]);
+          if (!load_ahead()) return false;
+        }
+        if (stay && t != it.k0) return true;                 // its blocks are there
+        for (int b = b0; b < NB; ++b, ++qc) {
+          if ((qc & 1u) != uint32_t(par)) continue;
+          const uint32_t use = qc >> 1;
+          if (!all(use == 0 || mbar_wait(&bar_q_empty[par], (use - 1) & 1u))) return false;
+          float* terms = row_terms[qc & 7u];
+          load_queries<kBF16, !kWide, D, 128>(smem_u32(sQ) + par * C::kTileBytes, p.q, it.q0, p.num_heads, it.h, p.group, b * kTile,
+                                              min(kTile, it.F - b * kTile), p.scale_log2,
+                                              !kWide && p.k_scale ? __ldg(p.k_scale + it.h) : 1.f, tid,
+                                              [&](int row, float c, int64_t n) {
+                                                terms[(row >> 1) * 4 + (row & 1)] = c;
+                                                terms[(row >> 1) * 4 + 2 + (row & 1)] = __ldg(p.lse + n) * -1.4426950408889634f;
+                                              });
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar_q[par]);
+        }
+        return true;
+      });
+      done_reading(i);
+    }
+    if (!ok && lane == 0) set_error(p.pc.err, PKV_DEVERR_TIMEOUT);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == 24) {
+      // ---------------- this CTA's range of the work, item by item ----------------
+      const int64_t total = int64_t(hkv) * first_unit[tables];
+      const int64_t lo = total * blockIdx.x / gridDim.x, hi = total * (blockIdx.x + 1) / gridDim.x;
+      uint32_t i = 0;
+      auto put = [&](const Item& it) {
+        ok = ok && (i < uint32_t(kItems) || all(mbar_wait(&bar_item_read[i % kItems], (i / kItems - 1) & 1u)));
+        if (!ok) return;
+        if (lane == 0) {
+          items[i % kItems][0] = make_int4(it.seq, it.h, it.q0, it.start);
+          items[i % kItems][1] = make_int4(it.F, it.k0, it.k1, it.row);
+          mbar_arrive(&bar_item[i % kItems]);
+        }
+        __syncwarp();
+        ++i;
+      };
+      if (lo < hi) {
+        int a = 0, b = tables;                               // hkv first_unit[a] <= lo < hkv first_unit[a + 1]
+        while (b - a > 1) {
+          const int mid = (a + b) >> 1;
+          if (int64_t(hkv) * first_unit[mid] <= lo) a = mid; else b = mid;
+        }
+        const int s0 = a * kSeqChunk + lane;
+        int mine = s0 < p.num_chunks ? units_of(Chunk(p, s0), G) : 0, sum = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, sum, o);
+          if (lane >= o) sum += v;
+        }
+        const int64_t in_table = lo - int64_t(hkv) * first_unit[a];
+        const unsigned past = __ballot_sync(0xffffffffu, int64_t(hkv) * sum > in_table);
+        const int l = past ? __ffs(past) - 1 : 31;
+        const int64_t before = int64_t(hkv) * __shfl_sync(0xffffffffu, sum - mine, l);
+        int units = __shfl_sync(0xffffffffu, mine, l);
+        int seq = a * kSeqChunk + l;
+        int h = int((in_table - before) / max(1, units));
+        int64_t pos = lo - (in_table - before) % max(1, units);              // of the (chunk, kv head)'s first unit
+        Chunk ch(p, min(seq, p.num_chunks - 1));
+        while (past && pos < hi && ok) {
+          if (h >= hkv || units == 0) {                      // the next chunk
+            h = 0;
+            if (++seq >= p.num_chunks) break;
+            ch = Chunk(p, seq);
+            units = units_of(ch, G);
+            continue;
+          }
+          Item it;
+          it.seq = seq;
+          it.h = h;
+          it.q0 = ch.q0;
+          it.start = ch.start;
+          it.F = ch.len * G;
+          it.k0 = tile_at(ch, G, lo - pos);
+          it.k1 = hi < pos + units ? tile_at(ch, G, hi - pos) : ch.tiles();
+          it.row = ch.row;
+          if (it.k1 > it.k0) put(it);
+          pos += units;
+          ++h;
         }
       }
-      if (lane == 0) {
-        const int64_t w = (int64_t(row) * p.num_kv_heads + g) * p.max_len + j;
-        p.out[w] = p.in && j < start ? p.decay * p.in[w] + sum : sum;
+      put(Item{});
+    } else if (warp == 25) {
+      // ---------------- MMA issuer (the whole warp; see mma_ss) ----------------
+      const uint32_t lead = elect_one();
+      const uint64_t dK = umma_sdesc_sw128(smem_u32(sK), 16, 1024), dQ = umma_sdesc_sw128(smem_u32(sQ), 16, 1024);
+      uint32_t kc = 0, qc = 0, used = 0, parity = 0;         // key tiles; blocks; by slot: its scores were written, how often mod 2
+      for (uint32_t i = 0;; ++i) {
+        ok = ok && wait_item(i);
+        if (!ok) break;
+        const Item it = read_item(i);
+        done_reading(i);
+        if (it.F == 0) break;
+        const int NB = it.blocks();
+        const bool stay = NB <= 2;
+        ok = each_group(it, [&](int t, int nt, int b0) -> bool {
+          const int turns = nt == 1 ? 4 : nt == 2 ? 2 : 1;
+          for (int b = b0; b < NB; ++b) {
+            const uint32_t use = qc + (b - (stay ? 0 : b0)), st = use & 1u;
+            if (!all(mbar_wait(&bar_q[st], use >> 1 & 1u))) return false;
+            const uint32_t idesc = umma_idesc_f16(kMmaBF16, 128, (min(kTile, it.F - b * kTile) + 15) & ~15, false, false);
+            for (int u = 0; u < nt; ++u) {
+              const uint32_t ks = (kc + u) % kSlots, slot = uint32_t((b - b0) % turns * nt + u);
+              if (!all(mbar_wait(&bar_k[ks], (kc + u) / kSlots & 1u))) return false;
+              if ((used >> slot & 1u) && !all(mbar_wait(&bar_s_free[slot], (parity >> slot & 1u) ^ 1u))) return false;
+              used |= 1u << slot;
+              parity ^= 1u << slot;
+              tc_fence_after();
+              const uint64_t da = dK + uint32_t(ks * C::kTileBytes / 16), db = dQ + uint32_t(st * C::kTileBytes / 16);
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk)
+                mma_ss(lead, tmem + 128 * slot, da + ((kk >> 2) * kHalfBytes + (kk & 3) * 32) / 16,
+                       db + ((kk >> 2) * kHalfBytes + (kk & 3) * 32) / 16, idesc, kk > 0);
+              commit(lead, &bar_s[slot]);
+              if (b == NB - 1) commit(lead, &bar_k_empty[ks]);
+            }
+            if (!stay || t + nt >= it.k1) commit(lead, &bar_q_empty[st]);
+          }
+          kc += nt;
+          if (!stay) qc += NB - b0;
+          return true;
+        });
+        if (!ok) break;
+        if (stay) qc += NB;
+      }
+      commit(lead, &bar_drain);                              // no product may be under way when the CTA leaves
+      (void)mbar_wait(&bar_drain, 0);
+    } else if (warp == 26) {
+      // ---------------- key tiles of 16-bit caches ----------------
+      const uint64_t pol = l2_policy_evict_first();
+      uint32_t kc = 0;
+      TableWindow win;
+      for (uint32_t i = 0; ok; ++i) {
+        ok = wait_item(i);
+        if (!ok) break;
+        const Item it = read_item(i);
+        done_reading(i);
+        if (it.F == 0) break;
+        if constexpr (kWide) {
+          const int end = it.start + int(p.group.quotient(it.F));
+          win.open(p.pc.tables + int64_t(it.seq) * p.pc.max_blocks, min(p.pc.max_blocks, ((end - 1) >> p.pc.block_shift) + 1));
+          for (int t = it.k0; t < it.k1 && ok; ++t) {
+            const uint32_t st = kc % kSlots, round = kc / kSlots;
+            ok = all(round == 0 || mbar_wait(&bar_k_empty[st], (round - 1) & 1u));
+            if (!ok) break;
+            load_tile_16bit<D>(sK + st * C::kTileBytes, &tmk, &bar_k[st], p.pc, win, it.h, t, end, lane, pol);
+            ++kc;
+          }
+        }
+      }
+      // No copy may be on its way when the CTA leaves.
+      if constexpr (kWide) {
+        for (uint32_t u = kc < uint32_t(kSlots) ? 0 : kc - kSlots; u < kc; ++u) (void)mbar_wait(&bar_k[u % kSlots], (u / kSlots) & 1u);
       }
     }
+    if (!ok && lane == 0) set_error(p.pc.err, PKV_DEVERR_TIMEOUT);
   }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 25) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <int KV, bool kBF16, int D>
+pkv_status launch(const CUtensorMap& tk, const WeightsParams& prm, cudaStream_t stream) {
+  constexpr int smem = Cfg<D>::kSmem;
+  auto kern = weights_kernel<KV, kBF16, D>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return PKV_ERR_CUDA;
+  return launch_pdl(kern, dim3(num_sms()), dim3(kThreads), smem, stream, tk, prm) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
 }  // namespace
@@ -110,7 +578,7 @@ extern "C" pkv_status pkv_attention_weights(float* out, const float* weights, fl
     return PKV_ERR_INVALID_ARG;
   unsigned* err = error_word_ptr();
   if (!err) return PKV_ERR_CUDA;
-  WeightsParams prm;
+  WeightsParams prm = {.group = Divisor(num_heads / cache->num_kv_heads)};
   prm.out = out;
   prm.in = weights;
   prm.decay = decay;
@@ -119,7 +587,6 @@ extern "C" pkv_status pkv_attention_weights(float* out, const float* weights, fl
   prm.lse = lse;
   prm.cu_q = cu_q_lens;
   prm.start = q_start_pos;
-  prm.tables = block_tables;
   prm.k_cache = static_cast<const uint8_t*>(k_cache);
   prm.k_scale = cache->k_scale;
   prm.num_rows = num_rows;
@@ -127,17 +594,32 @@ extern "C" pkv_status pkv_attention_weights(float* out, const float* weights, fl
   prm.num_chunks = num_chunks;
   prm.total_q = total_q;
   prm.num_heads = num_heads;
-  prm.num_kv_heads = cache->num_kv_heads;
-  prm.max_blocks = max_blocks_per_seq;
-  prm.num_blocks = cache->num_blocks;
-  prm.block_size = cache->block_size;
-  prm.kv = cache->kv_dtype;
-  prm.scale = scale;
-  prm.err = err;
-  auto kern = q_dtype == PKV_BF16 ? (cache->head_dim == 128 ? weights_kernel<true, 128> : weights_kernel<true, 64>)
-                                  : (cache->head_dim == 128 ? weights_kernel<false, 128> : weights_kernel<false, 64>);
-  const dim3 grid(unsigned(max_len < 8 * 1024 ? (max_len + 7) / 8 : 1024), unsigned(cache->num_kv_heads),
-                  unsigned(num_chunks < 65535 ? num_chunks : 65535));
-  return launch_pdl(kern, grid, dim3(256), 0, reinterpret_cast<cudaStream_t>(stream), prm) == cudaSuccess ? PKV_OK
-                                                                                                         : PKV_ERR_CUDA;
+  prm.scale_log2 = scale * 1.4426950408889634f;
+  prm.pc.tables = block_tables;
+  prm.pc.max_blocks = max_blocks_per_seq;
+  prm.pc.num_blocks = cache->num_blocks;
+  prm.pc.num_kv_heads = cache->num_kv_heads;
+  prm.pc.block_size = cache->block_size;
+  prm.pc.block_shift = cache->block_size == 16 ? 4 : 5;
+  prm.pc.err = err;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  CUtensorMap tk = {};
+  if (cache->kv_dtype == PKV_F16 || cache->kv_dtype == PKV_BF16) {           // boxes of 64 elements by 16 of the pool's rows
+    const int64_t pool_rows = int64_t(cache->num_blocks) * cache->num_kv_heads * cache->block_size;
+    if (pool_rows >= (int64_t(1) << 31) - 1) return PKV_ERR_UNSUPPORTED;
+    if (!encode_tmap_2d(&tk, CU_TENSOR_MAP_DATA_TYPE_UINT16, k_cache, uint64_t(cache->head_dim), uint64_t(pool_rows),
+                        uint64_t(cache->head_dim) * 2, 64, 16, CU_TENSOR_MAP_SWIZZLE_128B))
+      return PKV_ERR_CUDA;
+  }
+  const bool d128 = cache->head_dim == 128, bf = q_dtype == PKV_BF16;
+  switch (cache->kv_dtype) {
+    case PKV_F16: return d128 ? launch<PKV_F16, false, 128>(tk, prm, s) : launch<PKV_F16, false, 64>(tk, prm, s);
+    case PKV_BF16: return d128 ? launch<PKV_BF16, true, 128>(tk, prm, s) : launch<PKV_BF16, true, 64>(tk, prm, s);
+    case PKV_FP8_E4M3:
+      return bf ? (d128 ? launch<PKV_FP8_E4M3, true, 128>(tk, prm, s) : launch<PKV_FP8_E4M3, true, 64>(tk, prm, s))
+                : (d128 ? launch<PKV_FP8_E4M3, false, 128>(tk, prm, s) : launch<PKV_FP8_E4M3, false, 64>(tk, prm, s));
+    default:
+      return bf ? (d128 ? launch<PKV_FP4_E2M1, true, 128>(tk, prm, s) : launch<PKV_FP4_E2M1, true, 64>(tk, prm, s))
+                : (d128 ? launch<PKV_FP4_E2M1, false, 128>(tk, prm, s) : launch<PKV_FP4_E2M1, false, 64>(tk, prm, s));
+  }
 }

@@ -210,11 +210,12 @@ __device__ __forceinline__ double exp2_int(int e) { return __hiloint2double((102
 
 // Flat rows f0 .. f0 + n - 1 (n <= 128) of a chunk whose first row is q0 and of kv head h, flat row f being row f / G
 // of head h G + f mod G, as an operand at `base`, by kThreadsOf threads, 8 for a row.  Quantised caches (kToF16): as fp16, times the
-// sign of the kv head's scale, and for bf16 times a power of two; factor[r] takes the factor from products to
-// scores in units of log2 (scale_log2 * head_scale, for 16-bit caches scale_log2).
-template <bool kBF16, bool kToF16, int D, int kThreadsOf>
-__device__ __forceinline__ void load_queries(uint32_t base, float* factor, const uint8_t* q, int64_t q0, int num_heads, int h,
-                                             const Divisor& group, int f0, int n, float scale_log2, float head_scale, int tid) {
+// sign of the kv head's scale, and for bf16 times a power of two.  put(r, c, i) gets, once for row r, the factor c from
+// products to scores in units of log2 (scale_log2 * head_scale and that power; for 16-bit caches scale_log2) and the row's
+// number i among [total_q][num_heads].
+template <bool kBF16, bool kToF16, int D, int kThreadsOf, typename Put>
+__device__ __forceinline__ void load_queries(uint32_t base, const uint8_t* q, int64_t q0, int num_heads, int h,
+                                             const Divisor& group, int f0, int n, float scale_log2, float head_scale, int tid, Put put) {
   constexpr int kRows = kThreadsOf / 8, kVec = D / 64, kAhead = kThreadsOf == 128 ? 2 : 4;            // rows of a pass; 16-byte vectors per lane and row
   const int G = int(group.d), sub = tid & 7, r0 = tid >> 3;
   const uint32_t flip = kToF16 && head_scale < 0.f ? 0x80008000u : 0u;
@@ -257,7 +258,8 @@ __device__ __forceinline__ void load_queries(uint32_t base, float* factor, const
       if (r < n) {
         if (sub == 0) {
           const float c = kToF16 ? float(double(scale_log2) * fabs(double(head_scale)) * exp2_int(-shift)) : scale_log2;
-          factor[r] = c < 1e-35f ? 1e-35f : c;               // not 0 (a head's scale may be): it multiplies -inf; NaN stays
+          const int f = f0 + r, row = int(group.quotient(f));
+          put(r, c < 1e-35f ? 1e-35f : c, (q0 + row) * num_heads + int64_t(h) * G + (f - row * G));   // (0 * -inf would be NaN)
         }
 #pragma unroll
         for (int c = 0; c < kVec; ++c) {
