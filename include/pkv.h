@@ -465,7 +465,7 @@ PKV_API pkv_status pkv_evict_select(int32_t* kept, int max_keep, const float* we
  *   src_tables     (device) int32 [num_seqs][src_max_blocks]; dst_tables [num_seqs][dst_max_blocks]
  *   weights        (device) or NULL: only K and V move
  *   dst_rows       (device) or NULL: rows.  Distinct rows; dst_rows[i] is rows[i] or a row that the call does not read
- * Any cache type, head_dim a multiple of 16.  Launch order as pkv_kv_write, for all four calls.
+ * Any cache type, head_dim a multiple of 16 up to 256.  Launch order as pkv_kv_write, for all four calls.
  */
 PKV_API pkv_status pkv_evict_compact(void* k_cache, void* v_cache, const pkv_cache_desc* cache, const int32_t* kept,
                                      int max_keep, const int32_t* keep_lens, const int32_t* src_tables,

@@ -1,5 +1,7 @@
 // evict_select and evict_compact: which tokens of a sequence each kv head keeps, and their move to the front of
 // the sequence's blocks.
+#include <algorithm>
+
 #include "pkv_device.cuh"
 #include "pkv_host.h"
 
@@ -9,7 +11,11 @@ namespace {
 // ---------------------------------------------------------------------------------------
 // select
 // ---------------------------------------------------------------------------------------
-constexpr int kSelThreads = 1024;
+constexpr int kSelThreads = 512;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kMaxCluster = 8;
+constexpr int kDigits = 3;                    // of 11, 11 and 10 bits, from the top
+constexpr int kBins = 2048;
 
 struct SelectParams {
   int32_t* kept;
@@ -17,7 +23,7 @@ struct SelectParams {
   const int32_t* rows;
   const int32_t* lens;
   const int32_t* keep;
-  int max_keep, num_rows, max_len, num_seqs, num_kv_heads, first, recent;
+  int max_keep, num_rows, max_len, num_kv_heads, first, recent;
   unsigned* err;
 };
 
@@ -28,93 +34,176 @@ __device__ __forceinline__ uint32_t rank_of(float w) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// Exclusive sum over the CTA's threads; total in `total`.  Two barriers.
-__device__ __forceinline__ uint32_t scan_cta(uint32_t v, uint32_t* sums, uint32_t& total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint32_t x = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  if (lane == 31) sums[warp] = x;
-  __syncthreads();
-  uint32_t s = sums[lane], t = s;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t y = __shfl_up_sync(0xffffffffu, t, o);
-    if (lane >= o) t += y;
-  }
-  total = __shfl_sync(0xffffffffu, t, 31);
-  const uint32_t before = __shfl_sync(0xffffffffu, t - s, warp);
-  __syncthreads();
-  return before + x - v;
+// The 32-bit word at the place of `p` (shared memory) in the CTA of the given rank of the cluster.
+__device__ __forceinline__ uint32_t peer_word(const void* p, uint32_t rank) {
+  uint32_t a, v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
 }
 
-// A CTA per (sequence, kv head): the rank of the last one kept is found 8 bits at a time, then one ordered pass
-// writes the positions.
-__global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams p) {
-  __shared__ uint32_t hist[256], sums[32], found[2];
+// A cluster of 1 to 8 CTAs per (sequence, kv head).  Every warp has a run of consecutive positions, so that counts
+// and ballots alone give the order of the output.
+//   The rank of the last one kept is found a digit at a time: each CTA counts its own positions' digits, and all add
+// up the cluster's counts.  (11 bits: the first digit holds the exponent and two bits of the mantissa, which spreads
+// weights of similar size over several counters.)
+//   K > 0: a thread's K ranks stay in registers, one pass over the weights; 0: longer rows, read again for each digit.
+// Bound: launch, and three rounds of counting, a barrier and a scan.
+template <int K>
+__global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectParams p, int ctas) {
+  __shared__ uint32_t hist[kDigits][kBins];
+  __shared__ uint32_t warp_sum[kSelWarps], found[2];
+  __shared__ uint32_t warp_above[kSelWarps], warp_equal[kSelWarps], cta_above, cta_equal;
   griddep_launch_dependents();
   griddep_wait();
-  const int i = blockIdx.x / p.num_kv_heads, h = blockIdx.x % p.num_kv_heads, tid = threadIdx.x;
-  int32_t* kept = p.kept + int64_t(blockIdx.x) * p.max_keep;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int job = blockIdx.x / ctas, rank = blockIdx.x % ctas;
+  const int i = job / p.num_kv_heads, h = job % p.num_kv_heads;
+  int32_t* kept = p.kept + int64_t(job) * p.max_keep;
   const int L = p.lens[i], want = p.keep[i], row = p.rows ? p.rows[i] : i;
+  const int all_tid = rank * kSelThreads + tid, all_threads = ctas * kSelThreads;
   int n = 0;
   if (L < 0 || L > p.max_len || want < 0 || want > p.max_keep) {
-    if (tid == 0) set_error(p.err, PKV_DEVERR_CONTEXT_LEN);
+    if (all_tid == 0) set_error(p.err, PKV_DEVERR_CONTEXT_LEN);
   } else if (row >= p.num_rows) {
-    if (tid == 0) set_error(p.err, PKV_DEVERR_SLOT);
+    if (all_tid == 0) set_error(p.err, PKV_DEVERR_SLOT);
   } else if (row >= 0) {
     n = min(L, want);
   }
-  for (int j = n + tid; j < p.max_keep; j += kSelThreads) kept[j] = -1;
-  if (n == 0) return;
   const int r = min(p.recent, n), f = min(p.first, n - r), rest = n - r - f;
-  for (int j = tid; j < f; j += kSelThreads) kept[j] = j;
-  for (int j = tid; j < r; j += kSelThreads) kept[n - r + j] = L - r + j;
-  if (rest == 0) return;
-  const float* w = p.weights + (int64_t(row) * p.num_kv_heads + h) * p.max_len;
+  for (int j = n + all_tid; j < p.max_keep; j += all_threads) kept[j] = -1;
+  for (int j = all_tid; j < f; j += all_threads) kept[j] = j;
+  for (int j = all_tid; j < r; j += all_threads) kept[n - r + j] = L - r + j;
+  if (rest == 0) return;                                     // (the same for the whole cluster)
   const int lo = f, hi = L - r;
-  uint32_t prefix = 0, need = rest;                          // the threshold's leading bits; how many from there on
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    if (tid < 256) hist[tid] = 0;
-    __syncthreads();
-    for (int j = lo + tid; j < hi; j += kSelThreads) {
-      const uint32_t k = rank_of(w[j]);
-      if (shift == 24 || k >> (shift + 8) == prefix) atomicAdd(&hist[(k >> shift) & 255], 1u);
+  if (rest == hi - lo) {
+    for (int j = all_tid; j < rest; j += all_threads) kept[f + j] = lo + j;
+    return;
+  }
+  const float* w = p.weights + (int64_t(row) * p.num_kv_heads + h) * p.max_len;
+  // This warp's positions: run of them from `from` on, lane + 32 k.
+  const int run = ((hi - lo + ctas * kSelWarps - 1) / (ctas * kSelWarps) + 31) & ~31;
+  const int64_t from64 = lo + int64_t(rank * kSelWarps + warp) * run;
+  const int from = int(min(from64, int64_t(hi))), to = int(min(from64 + run, int64_t(hi)));
+  uint32_t mine[K > 0 ? K : 1];
+  if constexpr (K > 0) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int j = from + 32 * k + lane;
+      mine[k] = j < to ? rank_of(__ldg(w + j)) : 0u;
     }
+  }
+  // Calls body(rank, there) for this thread's positions in ascending order; whole warps.
+  auto each = [&](auto body) {
+    if constexpr (K > 0) {
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        if (from + 32 * k < to) body(mine[k], from + 32 * k + lane < to, from + 32 * k + lane);
+    } else {
+      for (int j = from; j < to; j += 32) body(j + lane < to ? rank_of(__ldg(w + j + lane)) : 0u, j + lane < to, j + lane);
+    }
+  };
+  for (int b = tid; b < kDigits * kBins; b += kSelThreads) (&hist[0][0])[b] = 0;
+  __syncthreads();
+  uint32_t prefix = 0, need = rest;                          // the threshold's leading bits; how many from there on
+#pragma unroll 1
+  for (int d = 0; d < kDigits; ++d) {
+    const int shift = d == 0 ? 21 : d == 1 ? 10 : 0, bits = d == 2 ? 10 : 11, bins = 1 << bits;
+    each([&](uint32_t k, bool there, int) {
+      if (there && (d == 0 || k >> (shift + bits) == prefix)) atomicAdd(&hist[d][(k >> shift) & (bins - 1)], 1u);
+    });
+    if (ctas > 1) cluster_sync(); else __syncthreads();
+    // Four bins a thread, from the top down: bins - 1 - 4 tid ...
+    uint32_t c[4] = {0, 0, 0, 0}, sum = 0;
+    if (4 * tid < bins) {
+      for (int q = 0; q < ctas; ++q) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const uint32_t* at = &hist[d][bins - 1 - 4 * tid - u];
+          c[u] += ctas > 1 ? peer_word(at, q) : *at;
+        }
+      }
+      sum = c[0] + c[1] + c[2] + c[3];
+    }
+    uint32_t before = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t v = __shfl_up_sync(0xffffffffu, before, o);
+      if (lane >= o) before += v;
+    }
+    if (lane == 31) warp_sum[warp] = before;
+    before -= sum;
     __syncthreads();
-    uint32_t total;                                          // bins from the top down
-    const uint32_t c = tid < 256 ? hist[255 - tid] : 0, before = scan_cta(c, sums, total);
-    if (tid < 256 && before < need && need <= before + c) {
-      found[0] = prefix << 8 | (255 - tid);
-      found[1] = need - before;
+    for (int q = 0; q < warp; ++q) before += warp_sum[q];
+    if (before < need && need <= before + sum) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (before < need && need <= before + c[u]) {
+          found[0] = prefix << bits | uint32_t(bins - 1 - 4 * tid - u);
+          found[1] = need - before;
+        }
+        before += c[u];
+      }
     }
     __syncthreads();
     prefix = found[0];
     need = found[1];
     __syncthreads();
   }
-  // prefix: the least rank kept; `need` of its holders, the lowest positions.
-  uint32_t above = 0, equal = 0;                             // among the positions walked
-  for (int j0 = lo; j0 < hi; j0 += kSelThreads) {
-    const int j = j0 + tid;
-    const uint32_t k = j < hi ? rank_of(w[j]) : 0;
-    const bool a = j < hi && k > prefix, e = j < hi && k == prefix;
-    uint32_t total;
-    const uint32_t before = scan_cta(uint32_t(a) | uint32_t(e) << 16, sums, total);
-    const uint32_t na = above + (before & 0xffffu), ne = equal + (before >> 16);
-    if (a || (e && ne < need)) kept[f + na + min(ne, need)] = j;
-    above += total & 0xffffu;
-    equal += total >> 16;
+  // prefix: the least rank kept; `need` of its holders, those of the lowest positions.
+  uint32_t above = 0, equal = 0;                             // before this warp
+  {
+    uint32_t a = 0, e = 0;
+    each([&](uint32_t k, bool there, int) {
+      a += there && k > prefix;
+      e += there && k == prefix;
+    });
+    a = __reduce_add_sync(0xffffffffu, a);
+    e = __reduce_add_sync(0xffffffffu, e);
+    if (lane == 0) {
+      warp_above[warp] = a;
+      warp_equal[warp] = e;
+    }
+    __syncthreads();
+    uint32_t ta = 0, te = 0;
+    for (int q = 0; q < kSelWarps; ++q) {
+      if (q == warp) {
+        above = ta;
+        equal = te;
+      }
+      ta += warp_above[q];
+      te += warp_equal[q];
+    }
+    if (ctas > 1) {
+      if (tid == 0) {
+        cta_above = ta;
+        cta_equal = te;
+      }
+      cluster_sync();
+      for (int q = 0; q < rank; ++q) {
+        above += peer_word(&cta_above, q);
+        equal += peer_word(&cta_equal, q);
+      }
+    }
   }
+  const unsigned below = (1u << lane) - 1;
+  each([&](uint32_t k, bool there, int j) {
+    const unsigned ma = __ballot_sync(0xffffffffu, there && k > prefix), me = __ballot_sync(0xffffffffu, there && k == prefix);
+    const uint32_t na = above + __popc(ma & below), ne = equal + __popc(me & below);
+    if (there && (k > prefix || (k == prefix && ne < need))) kept[f + na + min(ne, need)] = j;
+    above += __popc(ma);
+    equal += __popc(me);
+  });
+  if (ctas > 1) cluster_sync();                              // the others have read this CTA's counts
 }
 
 // ---------------------------------------------------------------------------------------
 // compact
 // ---------------------------------------------------------------------------------------
 constexpr int kMoveThreads = 256;
+constexpr int kMoveAhead = 8;                 // pieces of a row that a thread has in flight
+constexpr int kMoveRows = 512;                // rows of a round at most
+constexpr int kMoveCtas = 4;                  // resident per SM
 
 struct CompactParams {
   uint8_t* cache[2];
@@ -125,76 +214,181 @@ struct CompactParams {
   float* weights;
   const int32_t* rows;
   const int32_t* dst_rows;
-  int max_keep, src_blocks, dst_blocks, num_rows, max_len, num_kv_heads, num_blocks, block_size, head_dim, kv;
+  int max_keep, src_blocks, dst_blocks, num_rows, max_len, num_kv_heads, num_blocks, block_size, head_dim;
+  int round_rows;         // rows that a CTA moves between two barriers
+  Divisor pieces;         // of a row: 16 bytes each (8 where kUnit8), and in a 4-bit cache one more for its scales
   unsigned* err;
 };
 
-// A CTA per (sequence, kv head) and K, V or the weights: a thread per kept row, as many rows at a time as threads.
-// Rows only move forward to lower positions, so a step's reads are all that its writes have to wait for.
-__global__ void __launch_bounds__(kMoveThreads) compact_kernel(const CompactParams p) {
+// A cluster of CTAs per (sequence, kv head) and K, V or the weights (blockIdx.y).
+//   In place: kept positions ascend, so a row only ever moves to a lower position, and what a row at position d
+// overwrites is needed by rows up to d alone.  A round reads the sources of consecutive destinations, all CTAs of the
+// cluster meet, and then it writes; rounds ascend.  The next round's reads lie behind everything that this one writes.
+// Bound: HBM, by reads and writes in flight: rows are `pieces` of 16 bytes, eight of them in flight per thread, and the next
+// round's moves are looked up beside them.
+template <bool kFp4, bool kUnit8>
+__global__ void __launch_bounds__(kMoveThreads, kMoveCtas) compact_kernel(const CompactParams p, int ctas) {
+  __shared__ int64_t src_at[2][kMoveRows], dst_at[2][kMoveRows];             // rows of the pool; -1: no move
   griddep_launch_dependents();
   griddep_wait();
-  const int i = blockIdx.x / p.num_kv_heads, h = blockIdx.x % p.num_kv_heads, which = blockIdx.y;
-  const int32_t* kept = p.kept + int64_t(blockIdx.x) * p.max_keep;
-  int n = p.keep[i];
-  if (n < 0 || n > p.max_keep) {
-    if (threadIdx.x == 0) set_error(p.err, PKV_DEVERR_CONTEXT_LEN);
+  const int tid = threadIdx.x, job = blockIdx.x / ctas, rank = blockIdx.x % ctas, which = blockIdx.y;
+  const int i = job / p.num_kv_heads, h = job % p.num_kv_heads;
+  const int32_t* kept = p.kept + int64_t(job) * p.max_keep;
+  const int n = p.keep[i];
+  if (n < 0 || n > p.max_keep) {                             // (the same for the whole cluster)
+    if (tid == 0) set_error(p.err, PKV_DEVERR_CONTEXT_LEN);
     return;
   }
-  const int D = p.head_dim;
-  for (int j0 = 0; j0 < n; j0 += kMoveThreads) {
-    const int j = j0 + threadIdx.x, q = j < n ? kept[j] : -1;
-    bool ok = q >= 0;
-    if (ok && (q < j || (j > 0 && kept[j - 1] >= q))) {
+  auto meet = [&]() {
+    if (ctas > 1) cluster_sync(); else __syncthreads();
+  };
+  // Entry j of the list, or -1 where there is none or it does not ascend.
+  auto entry = [&](int j) -> int {
+    if (j >= n) return -1;
+    const int q = __ldg(kept + j);
+    if (q < 0) return -1;
+    if (q < j || (j > 0 && __ldg(kept + j - 1) >= q)) {
       set_error(p.err, PKV_DEVERR_CHUNK);
-      ok = false;
+      return -1;
     }
-    if (which == 2) {
-      const int from = p.rows ? p.rows[i] : i, to = p.dst_rows ? p.dst_rows[i] : from;
-      ok = ok && from >= 0 && to >= 0;
-      if (ok && (from >= p.num_rows || to >= p.num_rows || q >= p.max_len)) {
-        set_error(p.err, q >= p.max_len ? PKV_DEVERR_CONTEXT_LEN : PKV_DEVERR_SLOT);
-        ok = false;
+    return q;
+  };
+  if (which == 2) {
+    const int from = p.rows ? p.rows[i] : i, to = p.dst_rows ? p.dst_rows[i] : from;
+    if (from < 0 || to < 0) return;
+    if (from >= p.num_rows || to >= p.num_rows) {
+      if (tid == 0) set_error(p.err, PKV_DEVERR_SLOT);
+      return;
+    }
+    const float* src = p.weights + (int64_t(from) * p.num_kv_heads + h) * p.max_len;
+    float* dst = p.weights + (int64_t(to) * p.num_kv_heads + h) * p.max_len;
+    constexpr int kStep = kMoveThreads * kMoveAhead;
+    for (int j0 = rank * kStep; j0 - rank * kStep < n; j0 += ctas * kStep) {
+      float v[kMoveAhead];
+      bool on[kMoveAhead];
+#pragma unroll
+      for (int u = 0; u < kMoveAhead; ++u) {
+        const int q = entry(j0 + u * kMoveThreads + tid);
+        on[u] = q >= 0 && q < p.max_len;
+        if (q >= p.max_len) set_error(p.err, PKV_DEVERR_CONTEXT_LEN);
+        if (on[u]) v[u] = src[q];
       }
-      const float v = ok ? p.weights[(int64_t(from) * p.num_kv_heads + h) * p.max_len + q] : 0.f;
-      __syncthreads();
-      if (ok) p.weights[(int64_t(to) * p.num_kv_heads + h) * p.max_len + j] = v;
-      continue;
+      meet();
+#pragma unroll
+      for (int u = 0; u < kMoveAhead; ++u)
+        if (on[u]) dst[j0 + u * kMoveThreads + tid] = v[u];
     }
-    int64_t src = 0, dst = 0;
-    if (ok && (q / p.block_size >= p.src_blocks || j / p.block_size >= p.dst_blocks)) {
-      set_error(p.err, PKV_DEVERR_CHUNK);
-      ok = false;
-    }
-    if (ok) {
-      const int sb = p.src_tables[int64_t(i) * p.src_blocks + q / p.block_size];
-      const int db = p.dst_tables[int64_t(i) * p.dst_blocks + j / p.block_size];
-      if (sb < 0 || sb >= p.num_blocks || db < 0 || db >= p.num_blocks) {
-        set_error(p.err, PKV_DEVERR_BLOCK_ID);
-        ok = false;
-      }
-      src = (int64_t(sb) * p.num_kv_heads + h) * p.block_size + q % p.block_size;
-      dst = (int64_t(db) * p.num_kv_heads + h) * p.block_size + j % p.block_size;
-    }
-    uint8_t* cache = p.cache[which];
-    const bool fp4 = p.kv == PKV_FP4_E2M1;
-    const int bytes = fp4 ? D / 2 : p.kv == PKV_FP8_E4M3 ? D : 2 * D;
-    auto code_of = [&](int64_t row) { return fp4 ? (row >> 4) * 9 * D + (row & 15) * (D / 2) : row * bytes; };
-    auto scale_of = [&](int64_t row) { return (row >> 4) * 9 * D + 8 * D + (row & 15) * (D / 16); };
-    for (int b = 0; b < bytes; b += 64) {                    // 64 bytes of the row at a time, the whole CTA's rows
-      uint2 v[8];
-      for (int c = 0; c < 8 && ok; ++c)
-        if (b + 8 * c < bytes) v[c] = *reinterpret_cast<const uint2*>(cache + code_of(src) + b + 8 * c);
-      __syncthreads();
-      for (int c = 0; c < 8 && ok; ++c)
-        if (b + 8 * c < bytes) *reinterpret_cast<uint2*>(cache + code_of(dst) + b + 8 * c) = v[c];
-    }
-    for (int c = 0; fp4 && c < D / 16; ++c) {
-      const uint8_t v = ok ? cache[scale_of(src) + c] : 0;
-      __syncthreads();
-      if (ok) cache[scale_of(dst) + c] = v;
-    }
+    return;
   }
+  const int D = p.head_dim, R = p.round_rows;
+  const int row_bytes = kFp4 ? D / 2 : int(p.pieces.d) * 16; // of codes
+  auto place = [&](int64_t row) -> int64_t { return kFp4 ? (row >> 4) * 9 * D + (row & 15) * (D / 2) : row * row_bytes; };
+  // The moves of the rows from j0 on.
+  auto look_up = [&](int j0, int buf) {
+    for (int t = tid; t < R; t += kMoveThreads) {
+      const int j = j0 + t, q = entry(j);
+      int64_t s = -1, d = -1;
+      if (q >= 0) {
+        if (q / p.block_size >= p.src_blocks || j / p.block_size >= p.dst_blocks) {
+          set_error(p.err, PKV_DEVERR_CHUNK);
+        } else {
+          const int sb = __ldg(p.src_tables + int64_t(i) * p.src_blocks + q / p.block_size);
+          const int db = __ldg(p.dst_tables + int64_t(i) * p.dst_blocks + j / p.block_size);
+          if (unsigned(sb) >= unsigned(p.num_blocks) || unsigned(db) >= unsigned(p.num_blocks)) {
+            set_error(p.err, PKV_DEVERR_BLOCK_ID);
+          } else {
+            s = (int64_t(sb) * p.num_kv_heads + h) * p.block_size + q % p.block_size;
+            d = (int64_t(db) * p.num_kv_heads + h) * p.block_size + j % p.block_size;
+            if (s == d) s = -1;                              // it stays
+          }
+        }
+      }
+      src_at[buf][t] = s;
+      dst_at[buf][t] = d;
+    }
+  };
+  auto scales = [&](int64_t row) -> int64_t { return (row >> 4) * 9 * D + 8 * D + (row & 15) * (D / 16); };
+  uint8_t* cache = p.cache[which];
+  const int pieces = int(p.pieces.d), work = R * pieces;
+  look_up(rank * R, 0);
+  __syncthreads();
+  int buf = 0;
+  for (int j0 = rank * R; j0 - rank * R < n; j0 += ctas * R, buf ^= 1) {
+    uint4 v[kMoveAhead];
+#pragma unroll
+    for (int u = 0; u < kMoveAhead; ++u) {
+      const int k = u * kMoveThreads + tid;
+      if (k >= work) continue;
+      const int t = int(p.pieces.quotient(k)), c = k - t * pieces;
+      const int64_t s = src_at[buf][t];
+      if (s < 0) continue;
+      if (kFp4 && c == pieces - 1) {
+        const uint8_t* sc = cache + scales(s);
+        if (D == 128) {
+          const uint2 x = *reinterpret_cast<const uint2*>(sc);
+          v[u].x = x.x;
+          v[u].y = x.y;
+        } else if (D == 64) {
+          v[u].x = *reinterpret_cast<const uint32_t*>(sc);
+        } else {
+          uint32_t x[4] = {0, 0, 0, 0};
+          for (int b = 0; b < D / 16; ++b) x[b >> 2 & 3] |= uint32_t(sc[b]) << (8 * (b & 3));
+          v[u] = make_uint4(x[0], x[1], x[2], x[3]);
+        }
+      } else if constexpr (kUnit8) {
+        const uint2 x = *reinterpret_cast<const uint2*>(cache + place(s) + 8 * c);
+        v[u].x = x.x;
+        v[u].y = x.y;
+      } else {
+        v[u] = *reinterpret_cast<const uint4*>(cache + place(s) + 16 * c);
+      }
+    }
+    if (j0 + ctas * R < n + rank * R) look_up(j0 + ctas * R, buf ^ 1);
+    meet();
+#pragma unroll
+    for (int u = 0; u < kMoveAhead; ++u) {
+      const int k = u * kMoveThreads + tid;
+      if (k >= work) continue;
+      const int t = int(p.pieces.quotient(k)), c = k - t * pieces;
+      if (src_at[buf][t] < 0) continue;
+      const int64_t d = dst_at[buf][t];
+      if (kFp4 && c == pieces - 1) {
+        uint8_t* sc = cache + scales(d);
+        if (D == 128) {
+          *reinterpret_cast<uint2*>(sc) = make_uint2(v[u].x, v[u].y);
+        } else if (D == 64) {
+          *reinterpret_cast<uint32_t*>(sc) = v[u].x;
+        } else {
+          const uint32_t x[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+          for (int b = 0; b < D / 16; ++b) sc[b] = uint8_t(x[b >> 2 & 3] >> (8 * (b & 3)));
+        }
+      } else if constexpr (kUnit8) {
+        *reinterpret_cast<uint2*>(cache + place(d) + 8 * c) = make_uint2(v[u].x, v[u].y);
+      } else {
+        *reinterpret_cast<uint4*>(cache + place(d) + 16 * c) = v[u];
+      }
+    }
+    __syncthreads();                                         // this round's addresses may be overwritten
+  }
+}
+
+// Launches `kern` with clusters of `ctas` along x, as a programmatic dependent.
+template <typename... Params, typename... Args>
+cudaError_t launch_clusters(void (*kern)(Params...), dim3 grid, int threads, int ctas, cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = unsigned(ctas);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 }  // namespace
@@ -214,13 +408,21 @@ pkv_status pkv_evict_select(int32_t* kept, int max_keep, const float* weights, i
                         static_cast<const void*>(rows), static_cast<const void*>(context_lens),
                         static_cast<const void*>(keep_lens)})
     if (reinterpret_cast<uintptr_t>(p) & 3u) return PKV_ERR_INVALID_ARG;
-  if (int64_t(num_seqs) * num_kv_heads >= (int64_t(1) << 31)) return PKV_ERR_UNSUPPORTED;
+  if (int64_t(num_seqs) * num_kv_heads >= (int64_t(1) << 31) / kMaxCluster) return PKV_ERR_UNSUPPORTED;
   unsigned* err = error_word_ptr();
   if (!err) return PKV_ERR_CUDA;
-  SelectParams prm = {kept,    weights, rows,     context_lens, keep_lens, max_keep, num_rows,
-                      max_len, num_seqs, num_kv_heads, first,     recent,   err};
-  return launch_pdl(select_kernel, dim3(unsigned(num_seqs * num_kv_heads)), dim3(kSelThreads), 0,
-                    reinterpret_cast<cudaStream_t>(stream), prm) == cudaSuccess
+  SelectParams prm = {kept, weights, rows, context_lens, keep_lens, max_keep, num_rows, max_len, num_kv_heads, first, recent, err};
+  // Few positions per thread while one CTA will do, then more CTAs, then more positions, then they are read again.
+  int per = 4, ctas = 1;
+  auto room = [&]() { return int64_t(kSelThreads) * per * ctas; };
+  while (room() < max_len && per < 8) per *= 2;
+  while (room() < max_len && ctas < kMaxCluster) ctas *= 2;
+  while (room() < max_len && per < 32) per *= 2;
+  auto kern = room() < max_len ? select_kernel<0> : per == 4 ? select_kernel<4> : per == 8 ? select_kernel<8>
+              : per == 16 ? select_kernel<16> : select_kernel<32>;
+  const int64_t jobs = int64_t(num_seqs) * num_kv_heads;
+  return launch_clusters(kern, dim3(unsigned(jobs * ctas)), kSelThreads, ctas, reinterpret_cast<cudaStream_t>(stream), prm, ctas) ==
+                 cudaSuccess
              ? PKV_OK
              : PKV_ERR_CUDA;
 }
@@ -234,7 +436,7 @@ pkv_status pkv_evict_compact(void* k_cache, void* v_cache, const pkv_cache_desc*
   if (st != PKV_OK) return st;
   if (max_keep < 0 || src_max_blocks < 0 || dst_max_blocks < 0 || num_rows < 0 || max_len < 0 || num_seqs < 0)
     return PKV_ERR_INVALID_ARG;
-  if (cache->head_dim % 16) return PKV_ERR_UNSUPPORTED;
+  if (cache->head_dim % 16 || cache->head_dim > 256) return PKV_ERR_UNSUPPORTED;
   if (num_seqs == 0 || max_keep == 0) return PKV_OK;
   if (!k_cache || !v_cache || !kept || !keep_lens || !src_tables || !dst_tables || src_max_blocks == 0 ||
       dst_max_blocks == 0 || (weights && (num_rows == 0 || max_len == 0)))
@@ -245,15 +447,42 @@ pkv_status pkv_evict_compact(void* k_cache, void* v_cache, const pkv_cache_desc*
                         static_cast<const void*>(keep_lens), static_cast<const void*>(src_tables),
                         static_cast<const void*>(dst_tables)})
     if (reinterpret_cast<uintptr_t>(p) & 3u) return PKV_ERR_INVALID_ARG;
-  if (int64_t(num_seqs) * cache->num_kv_heads >= (int64_t(1) << 31)) return PKV_ERR_UNSUPPORTED;
+  if (int64_t(num_seqs) * cache->num_kv_heads >= (int64_t(1) << 31) / kMaxCluster) return PKV_ERR_UNSUPPORTED;
   unsigned* err = error_word_ptr();
   if (!err) return PKV_ERR_CUDA;
-  CompactParams prm = {{static_cast<uint8_t*>(k_cache), static_cast<uint8_t*>(v_cache)},
-                       kept, keep_lens, src_tables, dst_tables, weights, rows, dst_rows, max_keep, src_max_blocks,
-                       dst_max_blocks, num_rows, max_len, cache->num_kv_heads, cache->num_blocks, cache->block_size,
-                       cache->head_dim, cache->kv_dtype, err};
-  return launch_pdl(compact_kernel, dim3(unsigned(num_seqs * cache->num_kv_heads), weights ? 3 : 2), dim3(kMoveThreads),
-                    0, reinterpret_cast<cudaStream_t>(stream), prm) == cudaSuccess
+  const bool fp4 = cache->kv_dtype == PKV_FP4_E2M1;
+  const int D = cache->head_dim, row_bytes = fp4 ? D / 2 : D * dtype_bytes(cache->kv_dtype);
+  const bool unit8 = row_bytes % 16 != 0;                    // (4-bit rows of some head sizes)
+  const int pieces = row_bytes / (unit8 ? 8 : 16) + (fp4 ? 1 : 0);
+  CompactParams prm = {.pieces = Divisor(pieces)};
+  prm.cache[0] = static_cast<uint8_t*>(k_cache);
+  prm.cache[1] = static_cast<uint8_t*>(v_cache);
+  prm.kept = kept;
+  prm.keep = keep_lens;
+  prm.src_tables = src_tables;
+  prm.dst_tables = dst_tables;
+  prm.weights = weights;
+  prm.rows = rows;
+  prm.dst_rows = dst_rows;
+  prm.max_keep = max_keep;
+  prm.src_blocks = src_max_blocks;
+  prm.dst_blocks = dst_max_blocks;
+  prm.num_rows = num_rows;
+  prm.max_len = max_len;
+  prm.num_kv_heads = cache->num_kv_heads;
+  prm.num_blocks = cache->num_blocks;
+  prm.block_size = cache->block_size;
+  prm.head_dim = D;
+  prm.round_rows = std::min(kMoveRows, kMoveThreads * kMoveAhead / pieces);
+  prm.err = err;
+  // More CTAs for a list while the lists alone do not fill the SMs and each CTA still has rows to move.
+  const int64_t jobs = int64_t(num_seqs) * cache->num_kv_heads;
+  int ctas = 1;
+  while (ctas < kMaxCluster && 2 * jobs * ctas < int64_t(kMoveCtas) * std::max(1, num_sms()) && max_keep > ctas * prm.round_rows)
+    ctas *= 2;
+  auto kern = fp4 ? (unit8 ? compact_kernel<true, true> : compact_kernel<true, false>) : compact_kernel<false, false>;
+  return launch_clusters(kern, dim3(unsigned(jobs * ctas), weights ? 3 : 2), kMoveThreads, ctas,
+                         reinterpret_cast<cudaStream_t>(stream), prm, ctas) == cudaSuccess
              ? PKV_OK
              : PKV_ERR_CUDA;
 }

@@ -90,7 +90,7 @@ def test_refusals_of_select_and_compact():
                 dict(src=0), dict(src=3), dict(dst=0), dict(dst=2), dict(sb=0), dict(db=0), dict(sb=-1), dict(db=-1),
                 dict(w=2), dict(num_rows=0), dict(max_len=0), dict(rows=1), dict(dst_rows=1), dict(n=-1), dict(max_keep=-1)):
         assert move(**bad) == INVALID, bad
-    assert move(desc=_desc(kv=1, dim=40)) == UNSUPPORTED
+    assert move(desc=_desc(kv=1, dim=40)) == UNSUPPORTED and move(desc=_desc(dim=272)) == UNSUPPORTED
     assert move(desc=_desc(block=8)) == UNSUPPORTED
     assert move(n=1 << 30) == UNSUPPORTED
     assert move(n=0) == OK and move(max_keep=0) == OK and move(w=0, num_rows=0, max_len=0, n=0) == OK
