@@ -34,11 +34,23 @@ __device__ __forceinline__ uint32_t rank_of(float w) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// The 32-bit word at the place of `p` (shared memory) in the CTA of the given rank of the cluster.
-__device__ __forceinline__ uint32_t peer_word(const void* p, uint32_t rank) {
-  uint32_t a, v;
+// What lies at the place of `p` (shared memory) in the CTA of the given rank of the cluster.
+__device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t rank) {
+  uint32_t a;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return a;
+}
+__device__ __forceinline__ uint32_t peer_word(const void* p, uint32_t rank) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(peer_addr(p, rank)) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint4 peer_words(const void* p, uint32_t rank) {
+  uint4 v;
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(peer_addr(p, rank))
+               : "memory");
   return v;
 }
 
@@ -47,11 +59,13 @@ __device__ __forceinline__ uint32_t peer_word(const void* p, uint32_t rank) {
 //   The rank of the last one kept is found a digit at a time: each CTA counts its own positions' digits, and all add
 // up the cluster's counts.  (11 bits: the first digit holds the exponent and two bits of the mantissa, which spreads
 // weights of similar size over several counters.)
-//   K > 0: a thread's K ranks stay in registers, one pass over the weights; 0: longer rows, read again for each digit.
+//   kStored: the ranks stay in shared memory, one pass over the weights; else (longer rows) the weights are read again for
+// each digit.
 // Bound: launch, and three rounds of counting, a barrier and a scan.
-template <int K>
+template <bool kStored>
 __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectParams p, int ctas) {
-  __shared__ uint32_t hist[kDigits][kBins];
+  extern __shared__ uint32_t ranks[];                        // [warp][run]
+  __shared__ __align__(16) uint32_t hist[kDigits][kBins];
   __shared__ uint32_t warp_sum[kSelWarps], found[2];
   __shared__ uint32_t warp_above[kSelWarps], warp_equal[kSelWarps], cta_above, cta_equal;
   griddep_launch_dependents();
@@ -85,23 +99,16 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectPara
   const int run = ((hi - lo + ctas * kSelWarps - 1) / (ctas * kSelWarps) + 31) & ~31;
   const int64_t from64 = lo + int64_t(rank * kSelWarps + warp) * run;
   const int from = int(min(from64, int64_t(hi))), to = int(min(from64 + run, int64_t(hi)));
-  uint32_t mine[K > 0 ? K : 1];
-  if constexpr (K > 0) {
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int j = from + 32 * k + lane;
-      mine[k] = j < to ? rank_of(__ldg(w + j)) : 0u;
-    }
+  uint32_t* mine = ranks + warp * run;
+  if constexpr (kStored) {
+#pragma unroll 8
+    for (int j = from + lane; j < to; j += 32) mine[j - from] = rank_of(__ldg(w + j));
   }
-  // Calls body(rank, there) for this thread's positions in ascending order; whole warps.
+  // Calls body(rank, there, position) for this thread's positions in ascending order; whole warps.
   auto each = [&](auto body) {
-    if constexpr (K > 0) {
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-        if (from + 32 * k < to) body(mine[k], from + 32 * k + lane < to, from + 32 * k + lane);
-    } else {
-      for (int j = from; j < to; j += 32) body(j + lane < to ? rank_of(__ldg(w + j + lane)) : 0u, j + lane < to, j + lane);
-    }
+#pragma unroll 4
+    for (int j = from + lane; j < to + lane; j += 32)
+      body(j >= to ? 0u : kStored ? mine[j - from] : rank_of(__ldg(w + j)), j < to, j);
   };
   for (int b = tid; b < kDigits * kBins; b += kSelThreads) (&hist[0][0])[b] = 0;
   __syncthreads();
@@ -116,12 +123,17 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectPara
     // Four bins a thread, from the top down: bins - 1 - 4 tid ...
     uint32_t c[4] = {0, 0, 0, 0}, sum = 0;
     if (4 * tid < bins) {
-      for (int q = 0; q < ctas; ++q) {
+      const uint32_t* at = &hist[d][bins - 4 - 4 * tid];
+      uint4 v[kMaxCluster];                                  // (a load from another CTA takes a microsecond: all at once)
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const uint32_t* at = &hist[d][bins - 1 - 4 * tid - u];
-          c[u] += ctas > 1 ? peer_word(at, q) : *at;
-        }
+      for (int q = 0; q < kMaxCluster; ++q)
+        v[q] = q >= ctas ? make_uint4(0, 0, 0, 0) : ctas > 1 ? peer_words(at, q) : *reinterpret_cast<const uint4*>(at);
+#pragma unroll
+      for (int q = 0; q < kMaxCluster; ++q) {
+        c[0] += v[q].w;
+        c[1] += v[q].z;
+        c[2] += v[q].y;
+        c[3] += v[q].x;
       }
       sum = c[0] + c[1] + c[2] + c[3];
     }
@@ -374,10 +386,11 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveCtas) compact_kernel(const 
 
 // Launches `kern` with clusters of `ctas` along x, as a programmatic dependent.
 template <typename... Params, typename... Args>
-cudaError_t launch_clusters(void (*kern)(Params...), dim3 grid, int threads, int ctas, cudaStream_t stream, Args... args) {
+cudaError_t launch_clusters(void (*kern)(Params...), dim3 grid, int threads, int ctas, int smem, cudaStream_t stream, Args... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -412,16 +425,18 @@ pkv_status pkv_evict_select(int32_t* kept, int max_keep, const float* weights, i
   unsigned* err = error_word_ptr();
   if (!err) return PKV_ERR_CUDA;
   SelectParams prm = {kept, weights, rows, context_lens, keep_lens, max_keep, num_rows, max_len, num_kv_heads, first, recent, err};
-  // Few positions per thread while one CTA will do, then more CTAs, then more positions, then they are read again.
-  int per = 4, ctas = 1;
-  auto room = [&]() { return int64_t(kSelThreads) * per * ctas; };
-  while (room() < max_len && per < 8) per *= 2;
-  while (room() < max_len && ctas < kMaxCluster) ctas *= 2;
-  while (room() < max_len && per < 32) per *= 2;
-  auto kern = room() < max_len ? select_kernel<0> : per == 4 ? select_kernel<4> : per == 8 ? select_kernel<8>
-              : per == 16 ? select_kernel<16> : select_kernel<32>;
+  // One CTA for up to 4096 positions, then up to eight, then more positions for each as far as two CTAs of an SM have
+  // shared memory for their ranks.
+  constexpr int kFew = 4096, kMost = 16384;
+  int ctas = 1;
+  while (ctas < kMaxCluster && int64_t(kFew) * ctas < max_len) ctas *= 2;
+  const int64_t per_warp = (((int64_t(max_len) + ctas * kSelWarps - 1) / (ctas * kSelWarps)) + 31) / 32 * 32;
+  const bool stored = per_warp * kSelWarps <= kMost;
+  const int smem = stored ? int(per_warp) * kSelWarps * 4 : 0;
+  auto kern = stored ? select_kernel<true> : select_kernel<false>;
+  if (stored && cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost * 4) != cudaSuccess) return PKV_ERR_CUDA;
   const int64_t jobs = int64_t(num_seqs) * num_kv_heads;
-  return launch_clusters(kern, dim3(unsigned(jobs * ctas)), kSelThreads, ctas, reinterpret_cast<cudaStream_t>(stream), prm, ctas) ==
+  return launch_clusters(kern, dim3(unsigned(jobs * ctas)), kSelThreads, ctas, smem, reinterpret_cast<cudaStream_t>(stream), prm, ctas) ==
                  cudaSuccess
              ? PKV_OK
              : PKV_ERR_CUDA;
@@ -481,7 +496,7 @@ pkv_status pkv_evict_compact(void* k_cache, void* v_cache, const pkv_cache_desc*
   while (ctas < kMaxCluster && 2 * jobs * ctas < int64_t(kMoveCtas) * std::max(1, num_sms()) && max_keep > ctas * prm.round_rows)
     ctas *= 2;
   auto kern = fp4 ? (unit8 ? compact_kernel<true, true> : compact_kernel<true, false>) : compact_kernel<false, false>;
-  return launch_clusters(kern, dim3(unsigned(jobs * ctas), weights ? 3 : 2), kMoveThreads, ctas,
+  return launch_clusters(kern, dim3(unsigned(jobs * ctas), weights ? 3 : 2), kMoveThreads, ctas, 0,
                          reinterpret_cast<cudaStream_t>(stream), prm, ctas) == cudaSuccess
              ? PKV_OK
              : PKV_ERR_CUDA;
