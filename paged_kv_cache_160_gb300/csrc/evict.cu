@@ -45,19 +45,16 @@ __device__ __forceinline__ uint32_t peer_word(const void* p, uint32_t rank) {
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(peer_addr(p, rank)) : "memory");
   return v;
 }
-__device__ __forceinline__ uint4 peer_words(const void* p, uint32_t rank) {
-  uint4 v;
-  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(peer_addr(p, rank))
-               : "memory");
-  return v;
+__device__ __forceinline__ void add_to_peer(const void* p, uint32_t rank, uint32_t v) {
+  asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(peer_addr(p, rank)), "r"(v) : "memory");
 }
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 // A cluster of 1 to 8 CTAs per (sequence, kv head).  Every warp has a run of consecutive positions, so that counts
 // and ballots alone give the order of the output.
-//   The rank of the last one kept is found a digit at a time: each CTA counts its own positions' digits, and all add
-// up the cluster's counts.  (11 bits: the first digit holds the exponent and two bits of the mantissa, which spreads
+//   The rank of the last one kept is found a digit at a time: each CTA counts its own positions' digits and adds the counts
+// that are not zero to every CTA's totals.  (Reading all counts of all CTAs took 4 to 8 thousand cycles a digit.  11 bits: the first digit holds the exponent and two bits of the mantissa, which spreads
 // weights of similar size over several counters.)
 //   kStored: the ranks stay in shared memory, one pass over the weights; else (longer rows) the weights are read again for
 // each digit.
@@ -65,7 +62,7 @@ __device__ __forceinline__ uint4 peer_words(const void* p, uint32_t rank) {
 template <bool kStored>
 __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectParams p, int ctas) {
   extern __shared__ uint32_t ranks[];                        // [warp][run]
-  __shared__ __align__(16) uint32_t hist[kDigits][kBins];
+  __shared__ __align__(16) uint32_t hist[kBins], totals[kDigits][kBins];       // of this CTA (0 between digits); of the cluster
   __shared__ uint32_t warp_sum[kSelWarps], found[2];
   __shared__ uint32_t warp_above[kSelWarps], warp_equal[kSelWarps], cta_above, cta_equal;
   griddep_launch_dependents();
@@ -99,6 +96,9 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectPara
   const int run = ((hi - lo + ctas * kSelWarps - 1) / (ctas * kSelWarps) + 31) & ~31;
   const int64_t from64 = lo + int64_t(rank * kSelWarps + warp) * run;
   const int from = int(min(from64, int64_t(hi))), to = int(min(from64 + run, int64_t(hi)));
+  for (int b = tid; b < kDigits * kBins; b += kSelThreads) (&totals[0][0])[b] = 0;
+  for (int b = tid; b < kBins; b += kSelThreads) hist[b] = 0;
+  if (ctas > 1) cluster_arrive();
   uint32_t* mine = ranks + warp * run;
   if constexpr (kStored) {
 #pragma unroll 8
@@ -110,31 +110,35 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectPara
     for (int j = from + lane; j < to + lane; j += 32)
       body(j >= to ? 0u : kStored ? mine[j - from] : rank_of(__ldg(w + j)), j < to, j);
   };
-  for (int b = tid; b < kDigits * kBins; b += kSelThreads) (&hist[0][0])[b] = 0;
   __syncthreads();
   uint32_t prefix = 0, need = rest;                          // the threshold's leading bits; how many from there on
 #pragma unroll 1
   for (int d = 0; d < kDigits; ++d) {
     const int shift = d == 0 ? 21 : d == 1 ? 10 : 0, bits = d == 2 ? 10 : 11, bins = 1 << bits;
     each([&](uint32_t k, bool there, int) {
-      if (there && (d == 0 || k >> (shift + bits) == prefix)) atomicAdd(&hist[d][(k >> shift) & (bins - 1)], 1u);
+      if (there && (d == 0 || k >> (shift + bits) == prefix)) atomicAdd(&hist[(k >> shift) & (bins - 1)], 1u);
     });
-    if (ctas > 1) cluster_sync(); else __syncthreads();
+    __syncthreads();
+    if (ctas > 1) {
+      if (d == 0) cluster_wait();                            // everyone's totals are zero
+      for (int b = tid; b < bins; b += kSelThreads) {
+        const uint32_t v = hist[b];
+        if (v == 0) continue;
+        hist[b] = 0;
+        for (int q = 0; q < ctas; ++q) add_to_peer(&totals[d][b], q, v);
+      }
+      cluster_sync();
+    }
     // Four bins a thread, from the top down: bins - 1 - 4 tid ...
     uint32_t c[4] = {0, 0, 0, 0}, sum = 0;
     if (4 * tid < bins) {
-      const uint32_t* at = &hist[d][bins - 4 - 4 * tid];
-      uint4 v[kMaxCluster];                                  // (a load from another CTA takes a microsecond: all at once)
-#pragma unroll
-      for (int q = 0; q < kMaxCluster; ++q)
-        v[q] = q >= ctas ? make_uint4(0, 0, 0, 0) : ctas > 1 ? peer_words(at, q) : *reinterpret_cast<const uint4*>(at);
-#pragma unroll
-      for (int q = 0; q < kMaxCluster; ++q) {
-        c[0] += v[q].w;
-        c[1] += v[q].z;
-        c[2] += v[q].y;
-        c[3] += v[q].x;
-      }
+      uint32_t* at = &(ctas > 1 ? totals[d] : hist)[bins - 4 - 4 * tid];
+      const uint4 v = *reinterpret_cast<const uint4*>(at);
+      if (ctas == 1) *reinterpret_cast<uint4*>(at) = make_uint4(0, 0, 0, 0);
+      c[0] = v.w;
+      c[1] = v.z;
+      c[2] = v.y;
+      c[3] = v.x;
       sum = c[0] + c[1] + c[2] + c[3];
     }
     uint32_t before = sum;
@@ -192,10 +196,9 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectPara
         cta_equal = te;
       }
       cluster_sync();
-      for (int q = 0; q < rank; ++q) {
-        above += peer_word(&cta_above, q);
-        equal += peer_word(&cta_equal, q);
-      }
+      const bool before = lane < rank;                       // a lane for each of the CTAs before this one
+      above += __reduce_add_sync(0xffffffffu, before ? peer_word(&cta_above, lane) : 0u);
+      equal += __reduce_add_sync(0xffffffffu, before ? peer_word(&cta_equal, lane) : 0u);
     }
   }
   const unsigned below = (1u << lane) - 1;
