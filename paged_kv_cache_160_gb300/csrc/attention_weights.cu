@@ -377,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
           if (!all(use == 0 || mbar_wait(&bar_q_empty[par], (use - 1) & 1u))) return false;
           float* terms = row_terms[qc & 7u];
           load_queries<kBF16, !kWide, D, 128>(smem_u32(sQ) + par * C::kTileBytes, p.q, it.q0, p.num_heads, it.h, p.group, b * kTile,
-                                              min(kTile, it.F - b * kTile), p.scale_log2,
+                                              min(kTile, it.F - b * kTile), 1, p.scale_log2,
                                               !kWide && p.k_scale ? __ldg(p.k_scale + it.h) : 1.f, tid,
                                               [&](int row, float c, int64_t n) {
                                                 terms[(row >> 1) * 4 + (row & 1)] = c;

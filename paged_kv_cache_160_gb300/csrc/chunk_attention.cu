@@ -25,6 +25,7 @@ constexpr uint32_t kTmemCols = 512;           // S_A | S_B | O_A | O_B, 128 colu
 constexpr float kRescaleThreshold = 8.f;      // log2 units
 constexpr int kItems = 8;                     // items on their way from the scheduler to the other warps
 constexpr int kItemRows = 2 * kTile;
+constexpr int kFewRows = 32;                  // items of so few rows share each row's keys among four warps
 constexpr int kMaxChunks = 65535;
 constexpr int kSeqChunk = 32;                 // chunks per entry of the table of work
 constexpr int kReaders = 8 + 16 + 1 + 2;      // warps that read the items: softmax, loaders, MMA, queries
@@ -67,7 +68,9 @@ template <int KV, int D>
 struct Cfg {
   static constexpr int kTileBytes = D / 64 * kHalfBytes;     // 128 rows of Q, K or V
   static constexpr int kStages = D == 128 ? 2 : 4;           // K and V tiles in shared memory
-  static constexpr int kSmem = (2 + 2 * kStages) * kTileBytes;
+  static constexpr int kWeightHalf = kFewRows * 128;         // softmax weights of few rows by 64 keys
+  static constexpr int kWeights = 2 * kWeightHalf;           // of a chain
+  static constexpr int kSmem = 2 * kWeights + (2 + 2 * kStages) * kTileBytes;
 };
 
 // An item's part that this CTA works on.
@@ -79,6 +82,7 @@ struct Item {
   int masked;             // key tiles from here on are seen only in part by some rows
   int slot;               // -1: all of the item's keys; else the part to leave it in
   __device__ __forceinline__ bool two() const { return rows > kTile; }
+  __device__ __forceinline__ bool few() const { return rows <= kFewRows; }
   __device__ __forceinline__ int steps() const { return two() ? 2 * (t1 - t0) : t1 - t0; }
 };
 
@@ -163,17 +167,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Q area filled / no product reads it any more; K, V tiles likewise (V: looked at); S_x ready; P_x ready; PV_x done;
   // O read; both chains' maxima and sums there.
   __shared__ __align__(8) uint64_t bar_q[2], bar_q_empty[2], bar_k_full[kStages], bar_k_empty[kStages], bar_v_full[kStages],
-      bar_v_seen[kStages], bar_v_empty[kStages], bar_s_full[2], bar_p_full[2], bar_pv_done[2], bar_o_free, bar_ml, bar_drain;
+      bar_v_seen[kStages], bar_v_empty[kStages], bar_s_full[2], bar_p_full[2], bar_pv_done[2], bar_o_free, bar_ml, bar_peak[2], bar_drain;
   __shared__ uint32_t tmem_base_sh;
   __shared__ float factor[2][2][kTile];                      // [query area][use mod 2][row]: products to scores in log2 units
   __shared__ __align__(8) float2 chain_ml[2][2][kTile];      // [item parity][chain][row]
+  __shared__ float peak[2][2][4][kFewRows];                  // [chain][step mod 2][quarter of the keys][row]: largest scores
   __shared__ int masked_item[2 * kItems];                    // by item number modulo that: the last such item that non-finite
                                                              // values were taken out for, + 1
   __shared__ int first_unit[(kMaxChunks + kSeqChunk - 1) / kSeqChunk + 1];
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // uniform in the warp
 
-  uint8_t* sQ = smem;                                        // [area][64-dim half][128 rows]
-  uint8_t* sK = smem + 2 * C::kTileBytes;                    // [stage][64-dim half][128 rows]
+  // Weights of few rows come first: as an operand of 128 rows they reach into the queries, whose rows count for nothing.
+  uint8_t* sP = smem;                                        // [chain][64-key half][32 rows]
+  uint8_t* sQ = smem + 2 * C::kWeights;                      // [area][64-dim half][128 rows]
+  uint8_t* sK = sQ + 2 * C::kTileBytes;                      // [stage][64-dim half][128 rows]
   uint8_t* sV = sK + kStages * C::kTileBytes;
   if (smem_u32(smem) & 1023u) {                              // the 128-byte swizzle needs 1 KB alignment
     if (threadIdx.x == 0) set_error(p.pc.err, PKV_DEVERR_CHUNK);
@@ -195,6 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bar_s_full[i], 1);
       mbar_init(&bar_p_full[i], 4);                          // one arrival per softmax warp
       mbar_init(&bar_pv_done[i], 1);
+      mbar_init(&bar_peak[i], 4);
     }
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&bar_k_full[i], kWide ? 1 : 4);
@@ -274,11 +282,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int x = warp >> 2, quarter = warp & 3, r = 32 * quarter + lane;    // TMEM lane == row of the block
     const uint32_t lane_off = uint32_t(32 * quarter) << 16;
     const uint32_t tS = tmem + 128 * x + lane_off, tO = tmem + 256 + lane_off;
-    uint32_t steps = 0, turn = 0, merges = 0;                // this chain's steps; items of one block
+    uint32_t steps = 0, turn = 0, merges = 0, peaks = 0;     // this chain's steps; items of one block; steps of few rows
     Pair uses;                                               // of the query areas
     // The item before this one is written after this one's queries (of two blocks) are under way.
     Item it = {};
-    bool two = false, busy = false;
+    bool two = false, few = false, busy = false;
     int rows = 0, f = 0, qrow = 0, keys = 0, nx = 0;
     float m = 0.f, l = 0.f;
     for (uint32_t n = 0;; ++n) {
@@ -291,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         float* fac = factor[x][uses[x] & 1u];
         load_queries<kBF16, !kWide, D, 128>(smem_u32(sQ) + x * C::kTileBytes, p.q, next.q0, p.num_heads, next.h, p.group,
-                                            next.f0 + kTile * x, x == 0 ? kTile : next.rows - kTile, p.scale_log2,
+                                            next.f0 + kTile * x, x == 0 ? kTile : next.rows - kTile, 1, p.scale_log2,
                                             !kWide && p.k_scale ? __ldg(p.k_scale + next.h) : 1.f, int(threadIdx.x & 127),
                                             [&](int row, float c, int64_t) { fac[row] = c; });
         fence_proxy_async_smem();
@@ -318,6 +326,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++merges;
           ml0 = chain_ml[par][0][r];
           ml1 = chain_ml[par][1][r];
+          if (few && quarter == 0) {                         // the sums of the other quarters' keys
+            for (int c = 1; c < 4; ++c) {
+              ml0.y += chain_ml[par][0][32 * c + lane].y;
+              ml1.y += chain_ml[par][1][32 * c + lane].y;
+            }
+            if (ml0.x == -INFINITY && ml0.y != 0.f) ml0.x = 0.f;
+            if (ml1.x == -INFINITY && ml1.y != 0.f) ml1.x = 0.f;
+          }
         }
         tc_fence_after();
         const float top = fmaxf(ml0.x, ml1.x);
@@ -385,12 +401,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int tiles = it.t1 - it.t0;
       nx = two ? tiles : (tiles + 1 - x) / 2;
       rows = two ? (x == 0 ? kTile : it.rows - kTile) : it.rows;             // of this chain's block
-      busy = 32 * quarter < rows;                            // some row of this warp exists
-      f = it.f0 + (two ? kTile * x : 0) + min(r, rows - 1);
+      few = it.few();
+      busy = 32 * quarter < rows;                            // some row of this warp exists (of O: few rows are warp 0's)
+      const int rr = min(few ? lane : r, rows - 1);
+      f = it.f0 + (two ? kTile * x : 0) + rr;
       qrow = int(p.group.quotient(f));
       keys = it.start + qrow + 1;
       const int area = two ? x : int(turn & 1u);
-      const float* fac = &factor[area][uses[area] & 1u][min(r, rows - 1)];
+      const float* fac = &factor[area][uses[area] & 1u][rr];
       if (two) {
         uses.up(0);
         uses.up(1);
@@ -407,9 +425,74 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = all(mbar_wait(&bar_s_full[x], (steps + k) & 1u) && (k == 0 || mbar_wait(&bar_pv_done[x], (steps + k - 1) & 1u)));
         if (!ok) break;
         tc_fence_after();
-        if (busy) {
-          if (k == 0) slog = *fac;
-          const int lim = keys - tile * kTile;               // keys 0 .. lim - 1 are attended
+        if (k == 0) slog = *fac;
+        const int lim = keys - tile * kTile;                 // keys 0 .. lim - 1 are attended
+        if (few) {
+          // Every quarter of the lanes has a copy of the rows' scores; its warp takes a quarter of the keys.  One warp for
+          // all of a row's keys took 2400 cycles a tile, on one of the SM's four schedulers.
+          float s[32];
+          tmem_ld32(tS + 32 * quarter, s);
+          tmem_wait_ld();
+          if (__any_sync(0xffffffffu, lim < 32 * (quarter + 1))) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) s[c] = 32 * quarter + c < lim ? s[c] : -INFINITY;
+          }
+          float c4[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+          for (int c = 4; c < 32; c += 8) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              if (c + 2 * u + 1 < 32) c4[u] = fmax3(c4[u], s[c + 2 * u], s[c + 2 * u + 1]);
+          }
+          float(*pk)[kFewRows] = peak[x][peaks & 1u];
+          pk[quarter][lane] = fmaxf(fmaxf(c4[0], c4[1]), fmaxf(c4[2], c4[3]));
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar_peak[x]);
+          ok = all(mbar_wait(&bar_peak[x], peaks & 1u));
+          if (!ok) break;
+          ++peaks;
+          const float mt = fmaxf(fmaxf(pk[0][lane], pk[1][lane]), fmaxf(pk[2][lane], pk[3][lane])) * slog;
+          const bool grow = mt > m + kRescaleThreshold;      // (the same in all four warps)
+          const float m_prev = m;
+          if (grow) m = mt;
+          const float mu = m == -INFINITY ? 0.f : m;
+          const uint64_t sl2 = pack_f32x2(slog, slog), nm2 = pack_f32x2(-mu, -mu);
+          uint64_t acc0 = pack_f32x2(0.f, 0.f), acc1 = acc0;
+          const uint32_t row = smem_u32(sP) + x * C::kWeights + (quarter >> 1) * C::kWeightHalf;
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {                      // 8 keys: 16 bytes
+            uint32_t w[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const uint64_t x2 = fma_f32x2(pack_f32x2(s[8 * g + 2 * c], s[8 * g + 2 * c + 1]), sl2, nm2);
+              const float pa = fast_exp2(lo_f32(x2)), pb = fast_exp2(hi_f32(x2));
+              const uint64_t p2 = pack_f32x2(pa, pb);
+              if (c & 1) acc1 = add_f32x2(acc1, p2);
+              else acc0 = add_f32x2(acc0, p2);
+              w[c] = pack2<kMmaBF16>(pa, pb);
+            }
+            sts128(row + swz128(lane, 4 * (quarter & 1) + g), w[0], w[1], w[2], w[3]);
+          }
+          if (__any_sync(0xffffffffu, grow && k >= 1)) {
+            const float alpha = (grow && m_prev != -INFINITY) ? fast_exp2(m_prev - m) : 1.f;
+            if (quarter == 0) {                              // the rows of O
+#pragma unroll 1
+              for (int cc = 0; cc < D / 32; ++cc) {
+                float v[32];
+                tmem_ld32(tO + 128 * x + 32 * cc, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int c = 0; c < 32; ++c) v[c] *= alpha;
+                tmem_st32(tO + 128 * x + 32 * cc, v);
+              }
+              tmem_wait_st();
+            }
+            if (grow) l *= alpha;
+          }
+          const uint64_t acc = add_f32x2(acc0, acc1);
+          l += lo_f32(acc) + hi_f32(acc);
+          fence_proxy_async_smem();                          // the weights, to the tensor cores
+        } else if (busy) {
           if (__any_sync(0xffffffffu, lim < kTile)) {        // the others' scores: -inf
 #pragma unroll 1
             for (int cc = 0; cc < 4; ++cc) {
@@ -681,7 +764,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t idesc_s = umma_idesc_f16(kMmaBF16, 128, 128, false, false);
     constexpr uint32_t idesc_o = umma_idesc_f16(kMmaBF16, 128, D, false, true);
     const uint64_t dQ = umma_sdesc_sw128(smem_u32(sQ), 16, 1024), dK = umma_sdesc_sw128(smem_u32(sK), 16, 1024);
-    const uint64_t dV = umma_sdesc_sw128(smem_u32(sV), kHalfBytes, 1024);
+    const uint64_t dV = umma_sdesc_sw128(smem_u32(sV), kHalfBytes, 1024), dP = umma_sdesc_sw128(smem_u32(sP), 16, 1024);
     uint32_t kt = 0, turn = 0, done = 0;                     // tiles; items of one block; items
     Pair uses, p_of;                                         // of the query areas; steps of A and B
     for (;; ++done) {
@@ -690,7 +773,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Item it = read_item(done);
       done_reading(done);
       if (it.rows == 0) break;
-      const bool two = it.two();
+      const bool two = it.two(), few = it.few();
       const int N = it.steps();
       const int area = int(turn & 1u);                       // of an item of one block
       // S_x(n) = Q K^T into TMEM columns 128x .. 128x + 127.  A descriptor advances by bytes / 16.
@@ -710,7 +793,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (two ? n + 2 >= N : n + 1 == N) commit(lead, &bar_q_empty[a]);
         return true;
       };
-      // O_x += P_x V, P_x in the first 64 columns of the scores.
+      // O_x += P_x V, P_x in the first 64 columns of the scores, or of few rows in shared memory.
       auto issue_pv = [&](int n) -> bool {
         const int x = n & 1;
         const uint32_t tile = kt + (two ? n >> 1 : n), st = tile % kStages;
@@ -720,9 +803,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         p_of.up(x);
         tc_fence_after();
         const uint64_t b = dV + uint32_t(st * C::kTileBytes / 16);
+        if (few) {
+          const uint64_t a = dP + uint32_t(x * C::kWeights / 16);
 #pragma unroll
-        for (int kk = 0; kk < kTile / 16; ++kk)
-          mma_ts(lead, tmem + 256 + 128 * x, tmem + 128 * x + kk * 8, b + kk * 2048 / 16, idesc_o, n >= 2 || kk > 0);
+          for (int kk = 0; kk < kTile / 16; ++kk)
+            mma_ss(lead, tmem + 256 + 128 * x, a + ((kk >> 2) * C::kWeightHalf + (kk & 3) * 32) / 16, b + kk * 2048 / 16, idesc_o,
+                   n >= 2 || kk > 0);
+        } else {
+#pragma unroll
+          for (int kk = 0; kk < kTile / 16; ++kk)
+            mma_ts(lead, tmem + 256 + 128 * x, tmem + 128 * x + kk * 8, b + kk * 2048 / 16, idesc_o, n >= 2 || kk > 0);
+        }
         commit(lead, &bar_pv_done[x]);
         if (!two || x == 1) commit(lead, &bar_v_empty[st]);
         return true;
@@ -764,7 +855,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float* fac = factor[a][uses[a] & 1u];
       uses.up(a);
       load_queries<kBF16, !kWide, D, 64>(smem_u32(sQ) + a * C::kTileBytes, p.q, it.q0, p.num_heads, it.h, p.group, it.f0, it.rows,
-                                         p.scale_log2, !kWide && p.k_scale ? __ldg(p.k_scale + it.h) : 1.f, tid,
+                                         it.few() ? kTile / kFewRows : 1, p.scale_log2, !kWide && p.k_scale ? __ldg(p.k_scale + it.h) : 1.f, tid,
                                          [&](int row, float c, int64_t) { fac[row] = c; });
       fence_proxy_async_smem();
       __syncwarp();
@@ -784,48 +875,73 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Merges the parts of items that several CTAs worked on: a CTA per part that begins an item and 32 of its rows, a warp
-// per row.  The other parts are the first ones of the CTAs after it.
+// Merges the parts of items that several CTAs worked on.  A CTA begins at most one such item, as its last; the other parts
+// are the first ones of the CTAs after it.  blockIdx.x: the CTA that began it; kMergeRows rows each, a warp per row.
+constexpr int kMergeRows = 16;
 template <bool kBF16, int D>
 __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const ChunkParams p, int ctas, bool scaled) {
+  __shared__ int slots[2 * 1024];
+  __shared__ int count;
   griddep_launch_dependents();
   griddep_wait();
   const Part* headers = reinterpret_cast<const Part*>(p.parts);
-  const Part me = headers[blockIdx.x];
-  if (me.rows == 0 || me.t0 != 0) return;
+  const Part a = headers[2 * blockIdx.x], b = headers[2 * blockIdx.x + 1];
+  const bool second = b.rows != 0;                           // (an unfinished item behind another is the last)
+  const Part me = second ? b : a;
+  const int row0 = blockIdx.y * kMergeRows;
+  if (me.rows == 0 || me.t0 != 0 || row0 >= me.rows) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = int(p.group.d);
+  if (warp == 0) {                                           // the parts, in the order of their keys
+    if (lane == 0) slots[0] = 2 * blockIdx.x + second;
+    int n = 1;
+    bool more = me.t1 < me.tiles;
+    for (int w0 = blockIdx.x + 1; more && w0 < ctas; w0 += 32) {
+      Part part = {};
+      if (w0 + lane < ctas) part = headers[2 * (w0 + lane)];
+      const bool same = part.rows != 0 && part.t0 != 0 && part.seq == me.seq && part.h == me.h && part.f0 == me.f0;
+      const unsigned m = __ballot_sync(0xffffffffu, same);
+      if (same) slots[n + __popc(m & ((1u << lane) - 1))] = 2 * (w0 + lane);
+      n += __popc(m);
+      more = !__any_sync(0xffffffffu, same && part.t1 >= part.tiles);
+    }
+    if (lane == 0) count = n;
+  }
+  __syncthreads();
+  const int n = count;
   const uint8_t* bodies = p.parts + size_t(ctas) * 2 * sizeof(Part);
   const size_t stride = part_bytes(p.part_rows, D);
-  const int lane = threadIdx.x & 31, G = int(p.group.d);
-  constexpr int kVec = D / 64;                               // float2 of a lane
+  constexpr int kVec = D / 64, kAhead = 4;                   // float2 of a lane; parts in flight
   const float vs = scaled && p.v_scale ? p.v_scale[me.h] : 1.f;
-  for (int r = blockIdx.y * 32 + (threadIdx.x >> 5); r < min(me.rows, int(blockIdx.y) * 32 + 32); r += kMergeThreads / 32) {
-    float m = -INFINITY, l = 0.f;
+  for (int r = row0 + warp; r < min(me.rows, row0 + kMergeRows); r += kMergeThreads / 32) {
+    float m = -INFINITY;
+    for (int k = lane; k < n; k += 32) m = fmaxf(m, reinterpret_cast<const float2*>(bodies + slots[k] * stride)[r].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float l = 0.f;
     float2 o[kVec];
 #pragma unroll
     for (int c = 0; c < kVec; ++c) o[c] = make_float2(0.f, 0.f);
-    int slot = blockIdx.x, t = 0;
-    while (true) {
-      const Part part = headers[slot];
-      if (part.rows != 0 && part.t0 == t && part.seq == me.seq && part.h == me.h && part.f0 == me.f0) {
-        const uint8_t* body = bodies + slot * stride;
-        const float2 ml = reinterpret_cast<const float2*>(body)[r];
-        if (ml.x != -INFINITY) {
-          const float2* src = reinterpret_cast<const float2*>(body + part_head(p.part_rows)) + size_t(r) * (D / 2) + lane;
-          const float top = fmaxf(m, ml.x), a = m == -INFINITY ? 0.f : fast_exp2(m - top), b = fast_exp2(ml.x - top);
-          l = l * a + ml.y * b;
+    for (int k0 = 0; k0 < n; k0 += kAhead) {
+      float2 ml[kAhead], v[kAhead][kVec];
 #pragma unroll
-          for (int c = 0; c < kVec; ++c) {
-            const float2 v = src[32 * c];
-            o[c].x = o[c].x * a + v.x * b;
-            o[c].y = o[c].y * a + v.y * b;
-          }
-          m = top;
-        }
-        t = part.t1;
-        if (t >= part.tiles) break;
+      for (int u = 0; u < kAhead; ++u) {
+        const uint8_t* body = bodies + slots[min(k0 + u, n - 1)] * stride;
+        ml[u] = reinterpret_cast<const float2*>(body)[r];
+        const float2* src = reinterpret_cast<const float2*>(body + part_head(p.part_rows)) + size_t(r) * (D / 2) + lane;
+#pragma unroll
+        for (int c = 0; c < kVec; ++c) v[u][c] = src[32 * c];
       }
-      slot = (slot | 1) + 1;                                 // the next CTA's first part
-      if (slot >= 2 * ctas) break;
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        if (k0 + u >= n || ml[u].x == -INFINITY) continue;   // (a part without keys for the row: its O is 0 or was never written)
+        const float w = fast_exp2(ml[u].x - m);
+        l += ml[u].y * w;
+#pragma unroll
+        for (int c = 0; c < kVec; ++c) {
+          o[c].x += v[u][c].x * w;
+          o[c].y += v[u][c].y * w;
+        }
+      }
     }
     const int f = me.f0 + r, row = int(p.group.quotient(f));
     const int64_t unit = (int64_t(me.q0) + row) * p.num_heads + int64_t(me.h) * G + (f - row * G);
@@ -847,8 +963,9 @@ pkv_status launch(const CUtensorMap& tk, const CUtensorMap& tv, const ChunkParam
   auto kern = chunk_kernel<KV, kBF16, D>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return PKV_ERR_CUDA;
   const int ctas = num_sms();
+  if (ctas < 1 || ctas > 1024) return PKV_ERR_UNSUPPORTED;   // (the merge's list)
   if (launch_pdl(kern, dim3(ctas), dim3(kThreads), smem, stream, tk, tv, prm) != cudaSuccess) return PKV_ERR_CUDA;
-  return launch_pdl(chunk_merge_kernel<kBF16, D>, dim3(2 * ctas, (prm.part_rows + 31) / 32), dim3(kMergeThreads), 0, stream, prm,
+  return launch_pdl(chunk_merge_kernel<kBF16, D>, dim3(ctas, (prm.part_rows + kMergeRows - 1) / kMergeRows), dim3(kMergeThreads), 0, stream, prm,
                     ctas, KV != PKV_F16 && KV != PKV_BF16) == cudaSuccess
              ? PKV_OK
              : PKV_ERR_CUDA;

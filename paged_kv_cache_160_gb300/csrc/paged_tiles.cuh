@@ -212,10 +212,11 @@ __device__ __forceinline__ double exp2_int(int e) { return __hiloint2double((102
 // of head h G + f mod G, as an operand at `base`, by kThreadsOf threads, 8 for a row.  Quantised caches (kToF16): as fp16, times the
 // sign of the kv head's scale, and for bf16 times a power of two.  put(r, c, i) gets, once for row r, the factor c from
 // products to scores in units of log2 (scale_log2 * head_scale and that power; for 16-bit caches scale_log2) and the row's
-// number i among [total_q][num_heads].
+// number i among [total_q][num_heads].  With copies > 1 (n <= 32) the rows also go to rows 32, 64 .. on.
 template <bool kBF16, bool kToF16, int D, int kThreadsOf, typename Put>
 __device__ __forceinline__ void load_queries(uint32_t base, const uint8_t* q, int64_t q0, int num_heads, int h,
-                                             const Divisor& group, int f0, int n, float scale_log2, float head_scale, int tid, Put put) {
+                                             const Divisor& group, int f0, int n, int copies, float scale_log2, float head_scale, int tid,
+                                             Put put) {
   constexpr int kRows = kThreadsOf / 8, kVec = D / 64, kAhead = kThreadsOf == 128 ? 2 : 4;            // rows of a pass; 16-byte vectors per lane and row
   const int G = int(group.d), sub = tid & 7, r0 = tid >> 3;
   const uint32_t flip = kToF16 && head_scale < 0.f ? 0x80008000u : 0u;
@@ -274,7 +275,7 @@ __device__ __forceinline__ void load_queries(uint32_t base, const uint8_t* q, in
               w[k] ^= flip;
             }
           }
-          sts128(operand_at(base, r, sub + 8 * c), w[0], w[1], w[2], w[3]);
+          for (int k = 0; k < copies; ++k) sts128(operand_at(base, r + 32 * k, sub + 8 * c), w[0], w[1], w[2], w[3]);
         }
       }
     }
