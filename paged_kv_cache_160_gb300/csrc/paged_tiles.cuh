@@ -210,18 +210,20 @@ __device__ __forceinline__ double exp2_int(int e) { return __hiloint2double((102
 
 // Flat rows f0 .. f0 + n - 1 (n <= 128) of a chunk whose first row is q0 and of kv head h, flat row f being row f / G
 // of head h G + f mod G, as an operand at `base`, by kThreadsOf threads, 8 for a row.  Quantised caches (kToF16): as fp16, times the
-// sign of the kv head's scale, and for bf16 times a power of two.  put(r, c, i) gets, once for row r, the factor c from
-// products to scores in units of log2 (scale_log2 * head_scale and that power; for 16-bit caches scale_log2) and the row's
-// number i among [total_q][num_heads].  With copies > 1 (n <= 32) the rows also go to rows 32, 64 .. on.
-template <bool kBF16, bool kToF16, int D, int kThreadsOf, typename Put>
+// sign of the kv head's scale, and for bf16 times a power of two.  put(r, c, e) gets, once for row r, the factor c from
+// products to scores in units of log2 (scale_log2 * head_scale and that power; for 16-bit caches scale_log2) and e = extra(i),
+// i being the row's number among [total_q][num_heads]; it is asked for together with the rows.  kAhead rows of a thread are
+// on their way at a time.  With copies > 1 (n <= 32) the rows also go to rows 32, 64 .. on.
+template <bool kBF16, bool kToF16, int D, int kThreadsOf, int kAhead, typename Extra, typename Put>
 __device__ __forceinline__ void load_queries(uint32_t base, const uint8_t* q, int64_t q0, int num_heads, int h,
                                              const Divisor& group, int f0, int n, int copies, float scale_log2, float head_scale, int tid,
-                                             Put put) {
-  constexpr int kRows = kThreadsOf / 8, kVec = D / 64, kAhead = kThreadsOf == 128 ? 2 : 4;            // rows of a pass; 16-byte vectors per lane and row
+                                             Extra extra, Put put) {
+  constexpr int kRows = kThreadsOf / 8, kVec = D / 64;            // rows of a pass; 16-byte vectors per lane and row
   const int G = int(group.d), sub = tid & 7, r0 = tid >> 3;
   const uint32_t flip = kToF16 && head_scale < 0.f ? 0x80008000u : 0u;
   for (int b = r0; b < n + r0; b += kRows * kAhead) {        // (the same trip count for every thread)
     uint4 v[kAhead][kVec];
+    float ex[kAhead];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       const int r = b + u * kRows;
@@ -229,7 +231,9 @@ __device__ __forceinline__ void load_queries(uint32_t base, const uint8_t* q, in
       for (int c = 0; c < kVec; ++c) v[u][c] = make_uint4(0, 0, 0, 0);
       if (r < n) {
         const int f = f0 + r, row = int(group.quotient(f));
-        const uint8_t* src = q + ((q0 + row) * num_heads + int64_t(h) * G + (f - row * G)) * (2 * D);
+        const int64_t i = (q0 + row) * num_heads + int64_t(h) * G + (f - row * G);
+        const uint8_t* src = q + i * (2 * D);
+        ex[u] = extra(i);
 #pragma unroll
         for (int c = 0; c < kVec; ++c) v[u][c] = ld_stream(src + 16 * (sub + 8 * c), true);
       }
@@ -259,8 +263,7 @@ __device__ __forceinline__ void load_queries(uint32_t base, const uint8_t* q, in
       if (r < n) {
         if (sub == 0) {
           const float c = kToF16 ? float(double(scale_log2) * fabs(double(head_scale)) * exp2_int(-shift)) : scale_log2;
-          const int f = f0 + r, row = int(group.quotient(f));
-          put(r, c < 1e-35f ? 1e-35f : c, (q0 + row) * num_heads + int64_t(h) * G + (f - row * G));   // (0 * -inf would be NaN)
+          put(r, c < 1e-35f ? 1e-35f : c, ex[u]);            // (0 * -inf would be NaN)
         }
 #pragma unroll
         for (int c = 0; c < kVec; ++c) {
