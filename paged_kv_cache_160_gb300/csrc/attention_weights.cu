@@ -374,16 +374,17 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
         for (int b = b0; b < NB; ++b, ++qc) {
           if ((qc & 1u) != uint32_t(par)) continue;
           const uint32_t use = qc >> 1;
-          if (!all(use == 0 || mbar_wait(&bar_q_empty[par], (use - 1) & 1u))) return false;
           float* terms = row_terms[qc & 7u];
-          load_queries<kBF16, !kWide, D, 128, kWide ? 8 : 4>(smem_u32(sQ) + par * C::kTileBytes, p.q, it.q0, p.num_heads, it.h, p.group, b * kTile,
+          const bool loaded = load_queries<kBF16, !kWide, D, 128, kWide ? 8 : 4>(smem_u32(sQ) + par * C::kTileBytes, p.q, it.q0, p.num_heads, it.h, p.group, b * kTile,
                                               min(kTile, it.F - b * kTile), 1, p.scale_log2,
                                               !kWide && p.k_scale ? __ldg(p.k_scale + it.h) : 1.f, tid,
+                                              [&] { return all(use == 0 || mbar_wait(&bar_q_empty[par], (use - 1) & 1u)); },
                                               [&](int64_t n) { return __ldg(p.lse + n) * -1.4426950408889634f; },
                                               [&](int row, float c, float e) {
                                                 terms[(row >> 1) * 4 + (row & 1)] = c;
                                                 terms[(row >> 1) * 4 + 2 + (row & 1)] = e;
                                               });
+          if (!loaded) return false;
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar_q[par]);

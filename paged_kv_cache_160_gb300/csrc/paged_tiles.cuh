@@ -213,11 +213,12 @@ __device__ __forceinline__ double exp2_int(int e) { return __hiloint2double((102
 // sign of the kv head's scale, and for bf16 times a power of two.  put(r, c, e) gets, once for row r, the factor c from
 // products to scores in units of log2 (scale_log2 * head_scale and that power; for 16-bit caches scale_log2) and e = extra(i),
 // i being the row's number among [total_q][num_heads]; it is asked for together with the rows.  kAhead rows of a thread are
-// on their way at a time.  With copies > 1 (n <= 32) the rows also go to rows 32, 64 .. on.
-template <bool kBF16, bool kToF16, int D, int kThreadsOf, int kAhead, typename Extra, typename Put>
-__device__ __forceinline__ void load_queries(uint32_t base, const uint8_t* q, int64_t q0, int num_heads, int h,
+// on their way at a time, and ready() is called when the first of them are: it waits until the operand's place is free, and where
+// it returns false nothing is written.  With copies > 1 (n <= 32) the rows also go to rows 32, 64 .. on.
+template <bool kBF16, bool kToF16, int D, int kThreadsOf, int kAhead, typename Ready, typename Extra, typename Put>
+__device__ __forceinline__ bool load_queries(uint32_t base, const uint8_t* q, int64_t q0, int num_heads, int h,
                                              const Divisor& group, int f0, int n, int copies, float scale_log2, float head_scale, int tid,
-                                             Extra extra, Put put) {
+                                             Ready ready, Extra extra, Put put) {
   constexpr int kRows = kThreadsOf / 8, kVec = D / 64;            // rows of a pass; 16-byte vectors per lane and row
   const int G = int(group.d), sub = tid & 7, r0 = tid >> 3;
   const uint32_t flip = kToF16 && head_scale < 0.f ? 0x80008000u : 0u;
@@ -238,6 +239,7 @@ __device__ __forceinline__ void load_queries(uint32_t base, const uint8_t* q, in
         for (int c = 0; c < kVec; ++c) v[u][c] = ld_stream(src + 16 * (sub + 8 * c), true);
       }
     }
+    if (b == r0 && !ready()) return false;
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       const int r = b + u * kRows;
@@ -283,6 +285,7 @@ __device__ __forceinline__ void load_queries(uint32_t base, const uint8_t* q, in
       }
     }
   }
+  return true;
 }
 
 }  // namespace pkv
