@@ -394,7 +394,7 @@ PKV_API size_t pkv_chunk_workspace_bytes(int total_q, int num_heads, int num_kv_
  * rows stay unwritten.  A block id outside the pool sets PKV_DEVERR_BLOCK_ID; its keys and values count as zeros.
  * Supported: f16, bf16, e4m3 and 4-bit caches, head_dim 64 or 128, block_size 16 or 32, any number of query heads
  * per kv head, scale > 0 and finite, num_chunks up to 65535, total_q * num_heads and max_blocks_per_seq * block_size
- * below 2^31, and (total_q * (num_heads / num_kv_heads) / 256 + 2 num_chunks) * (max_blocks_per_seq * block_size / 64 + 2)
+ * below 2^31, and (total_q * (num_heads / num_kv_heads) / 64 + 3 num_chunks) * (max_blocks_per_seq * block_size / 128 + 2)
  * below 2^31.  Sums, maxima and outputs are fp32 until the last rounding; the softmax's exponentials are rounded to
  * the type of their product with V (q_dtype; fp16 over e4m3 and 4 bits).  Over e4m3 and 4 bits, bf16 q is taken as
  * fp16 after a power of two for each row (bits below 2^-25 of the row's largest are lost).  All of it

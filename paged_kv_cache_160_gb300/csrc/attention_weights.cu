@@ -8,7 +8,8 @@
 // a tensor memory lane is a key and its thread adds up a row of exponentials without a word to other threads.  Up to four
 // key tiles stay in shared memory while the blocks of query rows pass by, each tile's scores in 128 columns of their own: while one
 // tile's products run, the exponentials of the others are taken.  One or two blocks of rows stay too, and the key tiles pass
-// by.  The list of (chunk, kv head, key tile) is cut over the SMs by the number of blocks that see each tile: no tile's sum is
+// by.  Queries that need no change come by TMA, whole query rows a block; over e4m3 and 4 bits bf16 queries are turned into fp16
+// by the warps that turn the keys.  The list of (chunk, kv head, key tile) is cut over the SMs by the number of blocks that see each tile: no tile's sum is
 // split, so no order of sums depends on the run.
 #include <algorithm>
 
@@ -41,6 +42,8 @@ struct WeightsParams {
   int num_rows, max_len, num_chunks, total_q, num_heads;
   float scale_log2;
   Divisor group;          // query heads per kv head
+  Divisor block;          // flat rows of a block: 128, or as many whole query rows as that holds (queries by TMA)
+  bool tma;               // queries by TMA
   PagedCache pc;
 };
 
@@ -48,7 +51,6 @@ struct WeightsParams {
 struct Item {
   int seq, h, q0, start;  // chunk, kv head, first query row, its position
   int F, k0, k1, row;     // flat rows (0: no more items), key tiles, row of the weights
-  __device__ __forceinline__ int blocks() const { return (F + kTile - 1) / kTile; }
 };
 
 // A chunk: its rows, or none where there is nothing to do.
@@ -73,32 +75,33 @@ struct Chunk {
   __device__ __forceinline__ int tiles() const { return len == 0 ? 0 : (start + len + kTile - 1) / kTile; }
 };
 
-// The first block of 128 flat rows that sees key tile t.
-__device__ __forceinline__ int first_block(int start, int G, int t) {
-  const int64_t f = (int64_t(t) * kTile - start) * G;
-  return f > 0 ? int(f / kTile) : 0;
+// Blocks of F flat rows, and the first that sees key tile t (which some row does).
+__device__ __forceinline__ int blocks_of(const WeightsParams& p, int F) { return int(p.block.quotient(F + int(p.block.d) - 1)); }
+__device__ __forceinline__ int first_block(const WeightsParams& p, int start, int t) {
+  const int rows = t * kTile - start;
+  return rows > 0 ? int(p.block.quotient(rows * int(p.group.d))) : 0;
 }
 
 // Key tiles that every block sees; the others come after them.
 __device__ __forceinline__ int old_tiles(const Chunk& c) { return min(c.tiles(), c.start / kTile + 1); }
 
 // Work of a chunk's kv head.
-__device__ __forceinline__ int units_of(const Chunk& c, int G) {
+__device__ __forceinline__ int units_of(const WeightsParams& p, const Chunk& c) {
   if (c.len == 0) return 0;
-  const int blocks = (c.len * G + kTile - 1) / kTile, n = old_tiles(c);
+  const int blocks = blocks_of(p, c.len * int(p.group.d)), n = old_tiles(c);
   int units = n * (blocks + kTileCost);
-  for (int t = n; t < c.tiles(); ++t) units += blocks - first_block(c.start, G, t) + kTileCost;
+  for (int t = n; t < c.tiles(); ++t) units += blocks - first_block(p, c.start, t) + kTileCost;
   return units;
 }
 
 // The first key tile at or behind `at` units into a chunk's kv head.
-__device__ __forceinline__ int tile_at(const Chunk& c, int G, int64_t at) {
+__device__ __forceinline__ int tile_at(const WeightsParams& p, const Chunk& c, int64_t at) {
   if (at <= 0) return 0;
-  const int blocks = (c.len * G + kTile - 1) / kTile, n = old_tiles(c), per = blocks + kTileCost;
+  const int blocks = blocks_of(p, c.len * int(p.group.d)), n = old_tiles(c), per = blocks + kTileCost;
   if (at <= int64_t(n) * per) return int((at + per - 1) / per);
   at -= int64_t(n) * per;
   int t = n;
-  for (; t < c.tiles() && at > 0; ++t) at -= blocks - first_block(c.start, G, t) + kTileCost;
+  for (; t < c.tiles() && at > 0; ++t) at -= blocks - first_block(p, c.start, t) + kTileCost;
   return t;
 }
 
@@ -120,7 +123,8 @@ struct Cfg {
 // One or two blocks stay for all groups; more pass by once for every group.
 // ---------------------------------------------------------------------------------------
 template <int KV, bool kBF16, int D>
-__global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_constant__ CUtensorMap tmk, const WeightsParams p) {
+__global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_constant__ CUtensorMap tmk,
+                                                              const __grid_constant__ CUtensorMap tmq, const WeightsParams p) {
   using C = Cfg<D>;
   constexpr bool kWide = KV == PKV_F16 || KV == PKV_BF16;    // 16-bit caches
   constexpr bool kMmaBF16 = KV == PKV_BF16;
@@ -146,6 +150,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
   }
   if (threadIdx.x == 0) {
     if constexpr (kWide) prefetch_tensormap(&tmk);
+    if (p.tma) prefetch_tensormap(&tmq);
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&bar_item[i], 1);
       mbar_init(&bar_item_read[i], kReaders);
@@ -187,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
     int units = 0;
     if (s < p.num_chunks) {
       const Chunk ch(p, s);
-      units = units_of(ch, G);
+      units = units_of(p, ch);
       if (blockIdx.x == 0) error |= ch.error;
     }
 #pragma unroll
@@ -225,11 +230,12 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
   auto each_group = [&](const Item& it, auto group) -> bool {
     for (int t = it.k0; t < it.k1; t += kSlots) {
       // Blocks that stay are taken from the first on, so that all groups agree on them.
-      const int b0 = it.blocks() <= 2 ? 0 : first_block(it.start, G, t);
+      const int b0 = blocks_of(p, it.F) <= 2 ? 0 : first_block(p, it.start, t);
       if (!group(t, min(kSlots, it.k1 - t), b0)) return false;
     }
     return true;
   };
+  const int BR = int(p.block.d);
   bool ok = true;
 
   if (warp < 16) {
@@ -244,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
       const Item it = read_item(i);
       done_reading(i);
       if (it.F == 0) break;
-      const int NB = it.blocks();
+      const int NB = blocks_of(p, it.F);
       const bool stay = NB <= 2;
       ok = each_group(it, [&](int t, int nt, int b0) -> bool {
         const int turns = nt == 1 ? 4 : nt == 2 ? 2 : 1;     // slots of a tile
@@ -255,23 +261,22 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
           const uint32_t use = qc + (b - (stay ? 0 : b0));   // number of the block among all that were loaded
           if (!all(mbar_wait(&bar_s[x], steps & 1u))) return false;
           tc_fence_after();
-          const int n = min(kTile, it.F - b * kTile);
-          const int64_t before = (int64_t(key) - it.start) * G - int64_t(b) * kTile;   // rows of the block that do not see the key
+          const int n = min(BR, it.F - b * BR);
+          const int64_t before = (int64_t(key) - it.start) * G - int64_t(b) * BR;   // rows of the block that do not see the key
           const int lo = int(max(int64_t(0), min(before, int64_t(kTile))));
-          const bool whole = all(lo == 0 && n == kTile);
+          const bool whole = all(lo == 0 && n % 32 == 0);
           const float* terms = row_terms[use & 7u];
           uint64_t acc0 = pack_f32x2(0.f, 0.f), acc1 = acc0;
           const int chunks = (n + 31) / 32;
 #pragma unroll 1
           for (int cc = 0; cc < chunks; ++cc) {
-            float s[32];
-            tmem_ld32(tS + 32 * cc, s);
-            tmem_wait_ld();
+            uint64_t s[16];
+            tmem_ld_pairs(tS + 32 * cc, s);
             if (whole) {
 #pragma unroll
               for (int c = 0; c < 16; ++c) {
                 const float4 f = reinterpret_cast<const float4*>(terms)[16 * cc + c];
-                const uint64_t e = fma_f32x2(pack_f32x2(s[2 * c], s[2 * c + 1]), pack_f32x2(f.x, f.y), pack_f32x2(f.z, f.w));
+                const uint64_t e = fma_f32x2(s[c], pack_f32x2(f.x, f.y), pack_f32x2(f.z, f.w));
                 const uint64_t pe = pack_f32x2(fast_exp2(lo_f32(e)), fast_exp2(hi_f32(e)));
                 if (c & 1) acc1 = add_f32x2(acc1, pe);
                 else acc0 = add_f32x2(acc0, pe);
@@ -281,8 +286,8 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
               for (int c = 0; c < 16; ++c) {
                 const float4 f = reinterpret_cast<const float4*>(terms)[16 * cc + c];
                 const int c0 = 32 * cc + 2 * c;
-                const float e0 = c0 >= lo && c0 < n ? fmaf(s[2 * c], f.x, f.z) : -INFINITY;
-                const float e1 = c0 + 1 >= lo && c0 + 1 < n ? fmaf(s[2 * c + 1], f.y, f.w) : -INFINITY;
+                const float e0 = c0 >= lo && c0 < n ? fmaf(lo_f32(s[c]), f.x, f.z) : -INFINITY;
+                const float e1 = c0 + 1 >= lo && c0 + 1 < n ? fmaf(hi_f32(s[c]), f.y, f.w) : -INFINITY;
                 const uint64_t pe = pack_f32x2(fast_exp2(e0), fast_exp2(e1));
                 if (c & 1) acc1 = add_f32x2(acc1, pe);
                 else acc0 = add_f32x2(acc0, pe);
@@ -357,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
         done_reading(i);
         break;
       }
-      const int NB = it.blocks();
+      const int NB = blocks_of(p, it.F);
       const bool stay = NB <= 2;
       ok = each_group(it, [&](int t, int nt, int b0) -> bool {
         for (int u = 0; u < nt; ++u, ++kc) {
@@ -375,11 +380,31 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
           if ((qc & 1u) != uint32_t(par)) continue;
           const uint32_t use = qc >> 1;
           float* terms = row_terms[qc & 7u];
-          const bool loaded = load_queries<kBF16, !kWide, D, 128, kWide ? 8 : 4>(smem_u32(sQ) + par * C::kTileBytes, p.q, it.q0, p.num_heads, it.h, p.group, b * kTile,
-                                              min(kTile, it.F - b * kTile), 1, p.scale_log2,
-                                              !kWide && p.k_scale ? __ldg(p.k_scale + it.h) : 1.f, tid,
+          const int n = min(BR, it.F - b * BR);
+          const float head_scale = !kWide && p.k_scale ? __ldg(p.k_scale + it.h) : 1.f;
+          if (p.tma) {                                       // (a thread per row for its terms)
+            const int f = b * BR + tid, row = int(p.group.quotient(f));
+            float e = 0.f;
+            if (tid < n) e = __ldg(p.lse + (it.q0 + row) * p.num_heads + it.h * G + (f - row * G)) * -1.4426950408889634f;
+            if (!all(use == 0 || mbar_wait(&bar_q_empty[par], (use - 1) & 1u))) return false;
+            if (tid == 0) {
+              mbar_arrive_expect_tx(&bar_q[par], BR * D * 2);
+              for (int d = 0; d < D / 64; ++d)
+                tma_load_3d(sQ + par * C::kTileBytes + d * kHalfBytes, &tmq, &bar_q[par], 64 * d, it.h * G,
+                            it.q0 + int(p.group.quotient(b * BR)), l2_policy_evict_last());
+            }
+            if (tid < n) {
+              terms[(tid >> 1) * 4 + (tid & 1)] = p.scale_log2 * head_scale;
+              terms[(tid >> 1) * 4 + 2 + (tid & 1)] = e;
+            }
+            __syncwarp();
+            if (lane == 0 && w > 0) mbar_arrive(&bar_q[par]);
+            continue;
+          }
+          const bool loaded = load_queries<kBF16, !kWide, D, 128, 4>(smem_u32(sQ) + par * C::kTileBytes, p.q, it.q0, p.num_heads, it.h, p.group, b * BR, n, 1,
+                                              p.scale_log2, head_scale, tid,
                                               [&] { return all(use == 0 || mbar_wait(&bar_q_empty[par], (use - 1) & 1u)); },
-                                              [&](int64_t n) { return __ldg(p.lse + n) * -1.4426950408889634f; },
+                                              [&](int i) { return __ldg(p.lse + i) * -1.4426950408889634f; },
                                               [&](int row, float c, float e) {
                                                 terms[(row >> 1) * 4 + (row & 1)] = c;
                                                 terms[(row >> 1) * 4 + 2 + (row & 1)] = e;
@@ -419,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
           if (int64_t(hkv) * first_unit[mid] <= lo) a = mid; else b = mid;
         }
         const int s0 = a * kSeqChunk + lane;
-        int mine = s0 < p.num_chunks ? units_of(Chunk(p, s0), G) : 0, sum = mine;
+        int mine = s0 < p.num_chunks ? units_of(p, Chunk(p, s0)) : 0, sum = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
           const int v = __shfl_up_sync(0xffffffffu, sum, o);
@@ -439,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
             h = 0;
             if (++seq >= p.num_chunks) break;
             ch = Chunk(p, seq);
-            units = units_of(ch, G);
+            units = units_of(p, ch);
             continue;
           }
           Item it;
@@ -448,8 +473,8 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
           it.q0 = ch.q0;
           it.start = ch.start;
           it.F = ch.len * G;
-          it.k0 = tile_at(ch, G, lo - pos);
-          it.k1 = hi < pos + units ? tile_at(ch, G, hi - pos) : ch.tiles();
+          it.k0 = tile_at(p, ch, lo - pos);
+          it.k1 = hi < pos + units ? tile_at(p, ch, hi - pos) : ch.tiles();
           it.row = ch.row;
           if (it.k1 > it.k0) put(it);
           pos += units;
@@ -468,14 +493,14 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
         const Item it = read_item(i);
         done_reading(i);
         if (it.F == 0) break;
-        const int NB = it.blocks();
+        const int NB = blocks_of(p, it.F);
         const bool stay = NB <= 2;
         ok = each_group(it, [&](int t, int nt, int b0) -> bool {
           const int turns = nt == 1 ? 4 : nt == 2 ? 2 : 1;
           for (int b = b0; b < NB; ++b) {
             const uint32_t use = qc + (b - (stay ? 0 : b0)), st = use & 1u;
             if (!all(mbar_wait(&bar_q[st], use >> 1 & 1u))) return false;
-            const uint32_t idesc = umma_idesc_f16(kMmaBF16, 128, (min(kTile, it.F - b * kTile) + 15) & ~15, false, false);
+            const uint32_t idesc = umma_idesc_f16(kMmaBF16, 128, (min(BR, it.F - b * BR) + 15) & ~15, false, false);
             for (int u = 0; u < nt; ++u) {
               const uint32_t ks = (kc + u) % kSlots, slot = uint32_t((b - b0) % turns * nt + u);
               if (!all(mbar_wait(&bar_k[ks], (kc + u) / kSlots & 1u))) return false;
@@ -541,11 +566,11 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
 }
 
 template <int KV, bool kBF16, int D>
-pkv_status launch(const CUtensorMap& tk, const WeightsParams& prm, cudaStream_t stream) {
+pkv_status launch(const CUtensorMap& tk, const CUtensorMap& tq, const WeightsParams& prm, cudaStream_t stream) {
   constexpr int smem = Cfg<D>::kSmem;
   auto kern = weights_kernel<KV, kBF16, D>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return PKV_ERR_CUDA;
-  return launch_pdl(kern, dim3(num_sms()), dim3(kThreads), smem, stream, tk, prm) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+  return launch_pdl(kern, dim3(num_sms()), dim3(kThreads), smem, stream, tk, tq, prm) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
 }  // namespace
@@ -580,7 +605,13 @@ extern "C" pkv_status pkv_attention_weights(float* out, const float* weights, fl
     return PKV_ERR_INVALID_ARG;
   unsigned* err = error_word_ptr();
   if (!err) return PKV_ERR_CUDA;
-  WeightsParams prm = {.group = Divisor(num_heads / cache->num_kv_heads)};
+  const bool wide = cache->kv_dtype == PKV_F16 || cache->kv_dtype == PKV_BF16;
+  const int G = num_heads / cache->num_kv_heads;
+  // bf16 queries over e4m3 and 4 bits are changed on the way; of more than 128 heads a kv head, no block holds a query row.
+  const bool tma = (wide || q_dtype == PKV_F16) && G <= kTile;
+  const int whole = tma ? kTile / G : 1;                     // query rows of a block
+  WeightsParams prm = {.group = Divisor(G), .block = Divisor(tma ? whole * G : kTile)};
+  prm.tma = tma;
   prm.out = out;
   prm.in = weights;
   prm.decay = decay;
@@ -605,8 +636,12 @@ extern "C" pkv_status pkv_attention_weights(float* out, const float* weights, fl
   prm.pc.block_shift = cache->block_size == 16 ? 4 : 5;
   prm.pc.err = err;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  CUtensorMap tk = {};
-  if (cache->kv_dtype == PKV_F16 || cache->kv_dtype == PKV_BF16) {           // boxes of 64 elements by 16 of the pool's rows
+  CUtensorMap tk = {}, tq = {};
+  if (tma && !encode_tmap_3d(&tq, CU_TENSOR_MAP_DATA_TYPE_UINT16, q, uint64_t(cache->head_dim), uint64_t(num_heads),
+                             uint64_t(total_q), uint64_t(cache->head_dim) * 2, uint64_t(num_heads) * cache->head_dim * 2, 64, G,
+                             whole, CU_TENSOR_MAP_SWIZZLE_128B))
+    return PKV_ERR_CUDA;
+  if (wide) {                                                // boxes of 64 elements by 16 of the pool's rows
     const int64_t pool_rows = int64_t(cache->num_blocks) * cache->num_kv_heads * cache->block_size;
     if (pool_rows >= (int64_t(1) << 31) - 1) return PKV_ERR_UNSUPPORTED;
     if (!encode_tmap_2d(&tk, CU_TENSOR_MAP_DATA_TYPE_UINT16, k_cache, uint64_t(cache->head_dim), uint64_t(pool_rows),
@@ -615,13 +650,13 @@ extern "C" pkv_status pkv_attention_weights(float* out, const float* weights, fl
   }
   const bool d128 = cache->head_dim == 128, bf = q_dtype == PKV_BF16;
   switch (cache->kv_dtype) {
-    case PKV_F16: return d128 ? launch<PKV_F16, false, 128>(tk, prm, s) : launch<PKV_F16, false, 64>(tk, prm, s);
-    case PKV_BF16: return d128 ? launch<PKV_BF16, true, 128>(tk, prm, s) : launch<PKV_BF16, true, 64>(tk, prm, s);
+    case PKV_F16: return d128 ? launch<PKV_F16, false, 128>(tk, tq, prm, s) : launch<PKV_F16, false, 64>(tk, tq, prm, s);
+    case PKV_BF16: return d128 ? launch<PKV_BF16, true, 128>(tk, tq, prm, s) : launch<PKV_BF16, true, 64>(tk, tq, prm, s);
     case PKV_FP8_E4M3:
-      return bf ? (d128 ? launch<PKV_FP8_E4M3, true, 128>(tk, prm, s) : launch<PKV_FP8_E4M3, true, 64>(tk, prm, s))
-                : (d128 ? launch<PKV_FP8_E4M3, false, 128>(tk, prm, s) : launch<PKV_FP8_E4M3, false, 64>(tk, prm, s));
+      return bf ? (d128 ? launch<PKV_FP8_E4M3, true, 128>(tk, tq, prm, s) : launch<PKV_FP8_E4M3, true, 64>(tk, tq, prm, s))
+                : (d128 ? launch<PKV_FP8_E4M3, false, 128>(tk, tq, prm, s) : launch<PKV_FP8_E4M3, false, 64>(tk, tq, prm, s));
     default:
-      return bf ? (d128 ? launch<PKV_FP4_E2M1, true, 128>(tk, prm, s) : launch<PKV_FP4_E2M1, true, 64>(tk, prm, s))
-                : (d128 ? launch<PKV_FP4_E2M1, false, 128>(tk, prm, s) : launch<PKV_FP4_E2M1, false, 64>(tk, prm, s));
+      return bf ? (d128 ? launch<PKV_FP4_E2M1, true, 128>(tk, tq, prm, s) : launch<PKV_FP4_E2M1, true, 64>(tk, tq, prm, s))
+                : (d128 ? launch<PKV_FP4_E2M1, false, 128>(tk, tq, prm, s) : launch<PKV_FP4_E2M1, false, 64>(tk, tq, prm, s));
   }
 }

@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                             next.f0 + kTile * x, x == 0 ? kTile : next.rows - kTile, 1, p.scale_log2,
                                             !kWide && p.k_scale ? __ldg(p.k_scale + next.h) : 1.f, int(threadIdx.x & 127),
                                             [&] { return all(uses[x] == 0 || mbar_wait(&bar_q_empty[x], (uses[x] - 1) & 1u)); },
-                                            [](int64_t) { return 0.f; }, [&](int row, float c, float) { fac[row] = c; });
+                                            [](int) { return 0.f; }, [&](int row, float c, float) { fac[row] = c; });
         if (!ok) break;
         fence_proxy_async_smem();
         __syncwarp();
@@ -854,7 +854,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = load_queries<kBF16, !kWide, D, 64, 4>(smem_u32(sQ) + a * C::kTileBytes, p.q, it.q0, p.num_heads, it.h, p.group, it.f0, it.rows,
                                          it.few() ? kTile / kFewRows : 1, p.scale_log2, !kWide && p.k_scale ? __ldg(p.k_scale + it.h) : 1.f, tid,
                                          [&] { return all(uses[a] == 0 || mbar_wait(&bar_q_empty[a], (uses[a] - 1) & 1u)); },
-                                         [](int64_t) { return 0.f; }, [&](int row, float c, float) { fac[row] = c; });
+                                         [](int) { return 0.f; }, [&](int row, float c, float) { fac[row] = c; });
       if (!ok) break;
       uses.up(a);
       fence_proxy_async_smem();

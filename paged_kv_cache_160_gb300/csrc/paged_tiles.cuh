@@ -221,6 +221,7 @@ __device__ __forceinline__ bool load_queries(uint32_t base, const uint8_t* q, in
                                              Ready ready, Extra extra, Put put) {
   constexpr int kRows = kThreadsOf / 8, kVec = D / 64;            // rows of a pass; 16-byte vectors per lane and row
   const int G = int(group.d), sub = tid & 7, r0 = tid >> 3;
+  const int first = int(q0 * num_heads) + h * G;
   const uint32_t flip = kToF16 && head_scale < 0.f ? 0x80008000u : 0u;
   for (int b = r0; b < n + r0; b += kRows * kAhead) {        // (the same trip count for every thread)
     uint4 v[kAhead][kVec];
@@ -232,8 +233,8 @@ __device__ __forceinline__ bool load_queries(uint32_t base, const uint8_t* q, in
       for (int c = 0; c < kVec; ++c) v[u][c] = make_uint4(0, 0, 0, 0);
       if (r < n) {
         const int f = f0 + r, row = int(group.quotient(f));
-        const int64_t i = (q0 + row) * num_heads + int64_t(h) * G + (f - row * G);
-        const uint8_t* src = q + i * (2 * D);
+        const int i = first + f + row * (num_heads - G);     // (below 2^31)
+        const uint8_t* src = q + int64_t(i) * (2 * D);
         ex[u] = extra(i);
 #pragma unroll
         for (int c = 0; c < kVec; ++c) v[u][c] = ld_stream(src + 16 * (sub + 8 * c), true);
