@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bar_item_read[i], kReaders);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bar_q[i], 4);
+      mbar_init(&bar_q[i], 6);                               // the warps of a chain and the two for the queries
       mbar_init(&bar_q_empty[i], 1);
       mbar_init(&bar_s_full[i], 1);
       mbar_init(&bar_p_full[i], 4);                          // one arrival per softmax warp
@@ -845,8 +845,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       done_reading(i);
       if (it.rows == 0) break;
       if (it.two()) {
-        uses.up(0);
-        uses.up(1);
+        // Not ours to fill, but to wait for: a later wait could take an earlier phase that was skipped for its own.  The arrival
+        // keeps the areas' next phases from passing before that.
+        for (int a = 0; a < 2 && ok; ++a) {
+          ok = all(uses[a] == 0 || mbar_wait(&bar_q_empty[a], (uses[a] - 1) & 1u));
+          uses.up(a);
+          if (ok && lane == 0) mbar_arrive(&bar_q[a]);
+        }
+        if (!ok) break;
         continue;
       }
       const int a = int(turn++ & 1u);
@@ -859,9 +865,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       uses.up(a);
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) {                                       // two warps here, four for the blocks of larger items
-        mbar_arrive(&bar_q[a]);
-        mbar_arrive(&bar_q[a]);
+      if (lane == 0) {                                       // (for the chain's warps too)
+        for (int u = 0; u < 3; ++u) mbar_arrive(&bar_q[a]);
       }
     }
     if (!ok && lane == 0) set_error(p.pc.err, PKV_DEVERR_TIMEOUT);

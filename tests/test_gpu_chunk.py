@@ -135,6 +135,21 @@ def test_long_and_short_together(kind):
     _run([600] + [3] * 20 + [0], [300] + [1] * 20 + [200], 4, 2, 128, "f16", kind)
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("rows", [600, 300, 90])
+def test_many_items_for_every_sm(kind, rows):
+    """Blocks of 256 rows and remainders in turn, many for each SM."""
+    c = Case([5] * 40, [rows] * 40, 8, 8, 64, "bf16", kind, pad=1)
+    for _ in range(5):
+        c.out[:c.total] = 5.0
+        c.call()
+        assert c.pkv.pkv_get_device_error() == 0
+        if _ == 0:
+            first = c.out.clone()
+        assert torch.equal(first, c.out)
+    c.check(only=[0, 23] if rows < 600 else [31])
+
+
 def test_without_lse():
     _run([100, 2000], [5, 5], 4, 2, 128, "bf16", "fp4", lse=False)
     _run([100, 2000], [5, 5], 4, 2, 128, "bf16", "same", lse=False)
