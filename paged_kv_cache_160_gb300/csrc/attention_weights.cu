@@ -365,54 +365,60 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
       const int NB = blocks_of(p, it.F);
       const bool stay = NB <= 2;
       ok = each_group(it, [&](int t, int nt, int b0) -> bool {
-        for (int u = 0; u < nt; ++u, ++kc) {
-          if (kWide || (kc & 1u) != uint32_t(par)) continue;
-          const uint32_t st = kc % kSlots, round = kc / kSlots;
-          if (!all(round == 0 || mbar_wait(&bar_k_empty[st], (round - 1) & 1u))) return false;
-          ahead.store(smem_u32(sK) + st * C::kTileBytes, w, lane);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bar_k[st]);
-          if (!load_ahead()) return false;
-        }
-        if (stay && t != it.k0) return true;                 // its blocks are there
-        for (int b = b0; b < NB; ++b, ++qc) {
-          if ((qc & 1u) != uint32_t(par)) continue;
-          const uint32_t use = qc >> 1;
-          float* terms = row_terms[qc & 7u];
-          const int n = min(BR, it.F - b * BR);
-          const float head_scale = !kWide && p.k_scale ? __ldg(p.k_scale + it.h) : 1.f;
-          if (p.tma) {                                       // (a thread per row for its terms)
-            const int f = b * BR + tid, row = int(p.group.quotient(f));
-            float e = 0.f;
-            if (tid < n) e = __ldg(p.lse + (it.q0 + row) * p.num_heads + it.h * G + (f - row * G)) * -1.4426950408889634f;
-            if (!all(use == 0 || mbar_wait(&bar_q_empty[par], (use - 1) & 1u))) return false;
-            if (tid == 0) {
-              mbar_arrive_expect_tx(&bar_q[par], BR * D * 2);
-              for (int d = 0; d < D / 64; ++d)
-                tma_load_3d(sQ + par * C::kTileBytes + d * kHalfBytes, &tmq, &bar_q[par], 64 * d, it.h * G,
-                            it.q0 + int(p.group.quotient(b * BR)), l2_policy_evict_last());
+        // Blocks that stay come before the group's first key tile, others behind it.
+#pragma unroll 1
+        for (int part = 0; part < 2; ++part) {
+          if ((part == 0) != stay) {
+            for (int u = 0; u < nt; ++u, ++kc) {
+              if (kWide || (kc & 1u) != uint32_t(par)) continue;
+              const uint32_t st = kc % kSlots, round = kc / kSlots;
+              if (!all(round == 0 || mbar_wait(&bar_k_empty[st], (round - 1) & 1u))) return false;
+              ahead.store(smem_u32(sK) + st * C::kTileBytes, w, lane);
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&bar_k[st]);
+              if (!load_ahead()) return false;
             }
-            if (tid < n) {
-              terms[(tid >> 1) * 4 + (tid & 1)] = p.scale_log2 * head_scale;
-              terms[(tid >> 1) * 4 + 2 + (tid & 1)] = e;
+          } else if (!stay || t == it.k0) {
+            for (int b = b0; b < NB; ++b, ++qc) {
+              if ((qc & 1u) != uint32_t(par)) continue;
+              const uint32_t use = qc >> 1;
+              float* terms = row_terms[qc & 7u];
+              const int n = min(BR, it.F - b * BR);
+              const float head_scale = !kWide && p.k_scale ? __ldg(p.k_scale + it.h) : 1.f;
+              if (p.tma) {                                       // (a thread per row for its terms)
+                const int f = b * BR + tid, row = int(p.group.quotient(f));
+                float e = 0.f;
+                if (tid < n) e = __ldg(p.lse + (it.q0 + row) * p.num_heads + it.h * G + (f - row * G)) * -1.4426950408889634f;
+                if (!all(use == 0 || mbar_wait(&bar_q_empty[par], (use - 1) & 1u))) return false;
+                if (tid == 0) {
+                  mbar_arrive_expect_tx(&bar_q[par], BR * D * 2);
+                  for (int d = 0; d < D / 64; ++d)
+                    tma_load_3d(sQ + par * C::kTileBytes + d * kHalfBytes, &tmq, &bar_q[par], 64 * d, it.h * G,
+                                it.q0 + int(p.group.quotient(b * BR)), l2_policy_evict_last());
+                }
+                if (tid < n) {
+                  terms[(tid >> 1) * 4 + (tid & 1)] = p.scale_log2 * head_scale;
+                  terms[(tid >> 1) * 4 + 2 + (tid & 1)] = e;
+                }
+                __syncwarp();
+                if (lane == 0 && w > 0) mbar_arrive(&bar_q[par]);
+                continue;
+              }
+              const bool loaded = load_queries<kBF16, !kWide, D, 128, 4>(smem_u32(sQ) + par * C::kTileBytes, p.q, it.q0, p.num_heads, it.h, p.group, b * BR, n, 1,
+                                                  p.scale_log2, head_scale, tid,
+                                                  [&] { return all(use == 0 || mbar_wait(&bar_q_empty[par], (use - 1) & 1u)); },
+                                                  [&](int i) { return __ldg(p.lse + i) * -1.4426950408889634f; },
+                                                  [&](int row, float c, float e) {
+                                                    terms[(row >> 1) * 4 + (row & 1)] = c;
+                                                    terms[(row >> 1) * 4 + 2 + (row & 1)] = e;
+                                                  });
+              if (!loaded) return false;
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&bar_q[par]);
             }
-            __syncwarp();
-            if (lane == 0 && w > 0) mbar_arrive(&bar_q[par]);
-            continue;
           }
-          const bool loaded = load_queries<kBF16, !kWide, D, 128, 4>(smem_u32(sQ) + par * C::kTileBytes, p.q, it.q0, p.num_heads, it.h, p.group, b * BR, n, 1,
-                                              p.scale_log2, head_scale, tid,
-                                              [&] { return all(use == 0 || mbar_wait(&bar_q_empty[par], (use - 1) & 1u)); },
-                                              [&](int i) { return __ldg(p.lse + i) * -1.4426950408889634f; },
-                                              [&](int row, float c, float e) {
-                                                terms[(row >> 1) * 4 + (row & 1)] = c;
-                                                terms[(row >> 1) * 4 + 2 + (row & 1)] = e;
-                                              });
-          if (!loaded) return false;
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bar_q[par]);
         }
         return true;
       });
