@@ -609,6 +609,7 @@ extern "C" pkv_status pkv_attention_weights(float* out, const float* weights, fl
   if (!aligned16(q) || !aligned16(k_cache) || misaligned(out) || misaligned(weights) || misaligned(lse) ||
       misaligned(rows) || misaligned(cu_q_lens) || misaligned(q_start_pos) || misaligned(block_tables))
     return PKV_ERR_INVALID_ARG;
+  if (!on_current_device(q) || !on_current_device(k_cache)) return PKV_ERR_INVALID_ARG;
   unsigned* err = error_word_ptr();
   if (!err) return PKV_ERR_CUDA;
   const bool wide = cache->kv_dtype == PKV_F16 || cache->kv_dtype == PKV_BF16;

@@ -1013,6 +1013,8 @@ extern "C" pkv_status pkv_paged_chunk_attention(void* out, float* lse, const voi
   if (!workspace || !aligned16(workspace) ||
       workspace_bytes < pkv_chunk_workspace_bytes(total_q, num_heads, cache->num_kv_heads, cache->head_dim))
     return PKV_ERR_WORKSPACE;
+  if (!on_current_device(q) || !on_current_device(k_cache) || !on_current_device(v_cache) || !on_current_device(out))
+    return PKV_ERR_INVALID_ARG;
   unsigned* err = error_word_ptr();
   if (!err) return PKV_ERR_CUDA;
   ChunkParams prm = {.group = Divisor(num_heads / cache->num_kv_heads)};

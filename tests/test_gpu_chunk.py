@@ -343,6 +343,33 @@ def test_captured_graphs_and_another_stream():
     a.check()
 
 
+def test_two_streams_at_once():
+    a = Case([9000, 100], [4, 9], 8, 2, 128, "bf16", "fp4")
+    b = Case([700, 3000, 9], [200, 1, 9], 4, 1, 128, "f16", "same")
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(20):
+        for c, st in zip((a, b), streams):
+            c.call(stream=st)
+    torch.cuda.synchronize()
+    assert a.pkv.pkv_get_device_error() == 0
+    a.check()
+    b.check()
+
+
+def test_host_memory_is_refused():
+    import paged_kv_cache_160_gb300 as pkv
+    c = Case([30], [2], 4, 2, 128, "bf16", "same")
+    host = c.cache.k_cache.cpu().pin_memory()
+    import ctypes
+    args = (c.out.data_ptr(), 0, c.q_dev.data_ptr(), 1, c.cu_dev.data_ptr(), c.start_dev.data_ptr(), 1, 2, 4, host.data_ptr(),
+            c.cache.v_cache.data_ptr(), ctypes.byref(c.cache.desc), c.cache.dev_tables.data_ptr(), 2, 0.1, c.ws.data_ptr(),
+            c.ws.numel(), None)
+    assert pkv.lib.pkv_paged_chunk_attention(*args) == 1
+    torch.cuda.synchronize()
+    assert (c.out == 5.0).all()
+
+
 def test_one_row_agrees_with_the_decode():
     import paged_kv_cache_160_gb300 as pkv
     for kind in KINDS:

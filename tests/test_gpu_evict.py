@@ -107,6 +107,28 @@ def test_weights_of_heads(hq, hkv, n):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("hq,hkv,n", [(28, 4, 60), (5, 1, 100), (3, 1, 200), (130, 1, 7), (96, 1, 4)])
+def test_weights_of_many_blocks(kind, dtype, hq, hkv, n):
+    """More than two blocks of rows, of sizes that no power of two divides."""
+    _weights([200, 0], [n, 3], hq, hkv, 64, dtype, kind)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_weights_of_many_items_for_every_sm(kind):
+    """Items of one, two, three and four key tiles, one to five blocks of rows, many for each SM."""
+    c = Weights([5 + 37 * (i % 13) for i in range(120)], [1 + (i * 7) % 90 for i in range(120)], 8, 2, 64, "bf16", kind)
+    c.call_weights()
+    assert c.pkv.pkv_get_device_error() == 0
+    first = c.w.clone()
+    for _ in range(4):
+        c.w.fill_(3.0)
+        c.call_weights()
+        assert c.pkv.pkv_get_device_error() == 0 and torch.equal(first, c.w)
+    c.check_weights()
+
+
+@pytest.mark.parametrize("kind", KINDS)
 def test_weights_of_long_sequences(kind):
     _weights([9000, 40], [3, 200], 4, 2, 128, "bf16", kind, decay=0.5)
 
@@ -365,7 +387,7 @@ def test_compact_worst_orders(kv):
 
 @pytest.mark.parametrize("kv", ["fp4", "e4m3", "bf16"])
 def test_compact_into_other_blocks(kv):
-    _compact([100, 70, 300], [60, 70, 100], kv, fresh=[(0, 0), (0, 2), (1, 1), (2, 0), (2, 5)], dst_rows=[4, 0, 5])
+    _compact([100, 70, 300], [60, 70, 100], kv, fresh=[(0, 0), (0, 2), (1, 1), (2, 0), (2, 5)], dst_rows=[4, 1, 5])
 
 
 @pytest.mark.parametrize("dim", [16, 32, 80, 96, 256])
@@ -420,6 +442,82 @@ def test_compact_errors():
             assert torch.equal(c.k_cache[own], before[own]) and torch.equal(w[0], wb[0])
         if what == "row":
             assert torch.equal(w[0], wb[0])
+
+
+@pytest.mark.parametrize("kv", ["fp4", "bf16"])
+def test_blocks_past_4_gib(kv):
+    """Weights and moves in the last blocks of a pool of more than 2^32 bytes."""
+    import paged_kv_cache_160_gb300 as pkv
+    c = Weights([300], [3], 2, 1, 128, "bf16", kv)
+    cc = c.cache
+    big = (1 << 32) // (cc.k_cache[0].numel() * cc.k_cache.element_size()) + 40
+    pools = []
+    for x in (cc.k_cache, cc.v_cache):
+        p = torch.zeros((big,) + tuple(x.shape[1:]), dtype=x.dtype, device="cuda")
+        p[big - cc.num_blocks:] = x
+        pools.append(p)
+    cc.k_cache, cc.v_cache = pools
+    cc.desc = (pkv.cache_desc_fp4 if kv == "fp4" else pkv.cache_desc)(pools[0], *cc.dev_scales)
+    cc.dev_tables += big - cc.num_blocks
+    c.call_weights()
+    assert pkv.pkv_get_device_error() == 0
+    c.check_weights()
+    kept = _kept(np.random.default_rng(2), [303], [200], 1, 200)
+    pkv.pkv_evict_compact(*pools, cc.desc, torch.from_numpy(kept).cuda(), torch.tensor([200], dtype=torch.int32, device="cuda"),
+                          cc.dev_tables)
+    assert pkv.pkv_get_device_error() == 0
+    for pool, stored in zip(pools, cc.stored):
+        got = pool[big - cc.num_blocks:].view(torch.int16 if kv in DT else torch.uint8).cpu().numpy()
+        assert np.array_equal(_rows_of(cc, got), evict.compact(_rows_of(cc, stored), kept, [200], cc.tables, cc.tables, 16))
+
+
+def test_select_and_compact_in_a_graph():
+    """The captured calls, with other weights and lengths in the captured tensors."""
+    import paged_kv_cache_160_gb300 as pkv
+    i32 = dict(dtype=torch.int32, device="cuda")
+    c = Paged([3000, 500], "e4m3", 2, 64, max_blocks=200)
+    w = torch.rand((2, 2, 3200)).cuda()
+    kept = torch.zeros((2, 2, 900), **i32)
+    lens, keep = torch.tensor([3000, 500], **i32), torch.tensor([900, 100], **i32)
+
+    def call():
+        pkv.pkv_evict_select(kept, w, lens, keep, 3, 10)
+        pkv.pkv_evict_compact(c.k_cache, c.v_cache, c.desc, kept, keep, c.dev_tables, None, w)
+    captured = c.k_cache, c.v_cache, c.desc, c.dev_tables, c.dev_scales     # kept for as long as the graph
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            call()
+    torch.cuda.synchronize()
+    for n, m in (([3000, 500], [900, 100]), ([2900, 480], [77, 300])):
+        c.upload()
+        # the graph works on the tensors that it captured
+        pools = c.k_cache, c.v_cache
+        w.copy_(torch.rand((2, 2, 3200)))
+        lens.copy_(torch.tensor(n))
+        keep.copy_(torch.tensor(m))
+        before = w.cpu().numpy().copy()
+        call()
+        got = [p.clone() for p in pools]
+        after, list_ = w.clone(), kept.cpu().numpy()
+        for i in range(2):
+            for h in range(2):
+                ref = evict.select(before[i, h], n[i], m[i], 3, 10)
+                assert list_[i, h, :m[i]].tolist() == ref
+                assert np.array_equal(after[i, h, :m[i]].cpu().numpy(), before[i, h, ref])
+        assert np.array_equal(got[0].cpu().numpy(), evict.compact(c.stored[0], list_, m, c.tables, c.tables, 16))
+        # the same by the graph
+        w.copy_(torch.from_numpy(before))
+        kept.zero_()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            g.replay()
+        torch.cuda.synchronize()
+        assert np.array_equal(kept.cpu().numpy(), list_) and torch.equal(w, after)
+    assert pkv.pkv_get_device_error() == 0
+    assert captured[0].data_ptr() != c.k_cache.data_ptr()
 
 
 # ---------------------------------------------------------------------------------------
