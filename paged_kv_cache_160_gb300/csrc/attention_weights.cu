@@ -9,8 +9,14 @@
 // key tiles stay in shared memory while the blocks of query rows pass by, each tile's scores in 128 columns of their own: while one
 // tile's products run, the exponentials of the others are taken.  One or two blocks of rows stay too, and the key tiles pass
 // by.  Queries that need no change come by TMA, whole query rows a block; over e4m3 and 4 bits bf16 queries are turned into fp16
-// by the warps that turn the keys.  The list of (chunk, kv head, key tile) is cut over the SMs by the number of blocks that see each tile: no tile's sum is
-// split, so no order of sums depends on the run.
+// by the warps that turn the keys.  The list of (chunk, kv head, key tile) is cut over the SMs by the number of blocks that see
+// each tile: no tile's sum is split, so no order of sums depends on the run.
+//
+// Bound: few rows, HBM (64 sequences of up to 2,048 tokens, one row each, 28 heads over 4, bf16: 19.9 us, 0.57 of the measured
+// copy); many rows, the chain of a slot, products - exponentials - products (2,048 rows over 8,192 keys, 32 heads over 8, f16: 166 us; the
+// products alone take 62, the exponentials 51), where SMs with four key tiles work on for a fifth longer than the mean.  64 rows
+// over up to 16,384 keys of 4 bits: 47 us.  Not faster: the slots in halves of 64 rows (206 us: products of 64 columns read the keys as
+// often), queries through registers only (178).
 #include <algorithm>
 
 #include "paged_tiles.cuh"
@@ -135,7 +141,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
   __shared__ __align__(8) uint64_t bar_q[2], bar_q_empty[2], bar_k[kSlots], bar_k_empty[kSlots], bar_s[kSlots], bar_s_free[kSlots],
       bar_sum, bar_drain;
   __shared__ uint32_t tmem_base_sh;
-  // [block number mod 8]: (factor, factor, -lse, -lse) of row pairs.  Block u + 8 is loaded once the products of u + 6 are done, and
+  // [block number mod 8]: (factor, factor, -lse, -lse) of row pairs; queries by TMA have one factor: only -lse of each row.  Block u + 8 is loaded once the products of u + 6 are done, and
   // those of u + 4 at the latest waited for the sums of u.
   __shared__ __align__(16) float row_terms[8][2 * kTile];
   __shared__ float sums[2][kSlots][kTile];
@@ -252,6 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
       if (it.F == 0) break;
       const int NB = blocks_of(p, it.F);
       const bool stay = NB <= 2;
+      const float slog = p.scale_log2 * (!kWide && p.k_scale ? __ldg(p.k_scale + it.h) : 1.f);           // (queries by TMA)
       ok = each_group(it, [&](int t, int nt, int b0) -> bool {
         const int turns = nt == 1 ? 4 : nt == 2 ? 2 : 1;     // slots of a tile
         const int mine = x < nt * turns ? x % nt : -1, turn = x / nt;        // tile of the group; which of its slots
@@ -272,7 +279,16 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
           for (int cc = 0; cc < chunks; ++cc) {
             uint64_t s[16];
             tmem_ld_pairs(tS + 32 * cc, s);
-            if (whole) {
+            if (whole && p.tma) {
+              const uint64_t sl2 = pack_f32x2(slog, slog);
+#pragma unroll
+              for (int c = 0; c < 8; ++c) {                  // (every read of shared memory takes from what the products read)
+                const float4 f = reinterpret_cast<const float4*>(terms)[8 * cc + c];
+                const uint64_t e0 = fma_f32x2(s[2 * c], sl2, pack_f32x2(f.x, f.y)), e1 = fma_f32x2(s[2 * c + 1], sl2, pack_f32x2(f.z, f.w));
+                acc0 = add_f32x2(acc0, pack_f32x2(fast_exp2(lo_f32(e0)), fast_exp2(hi_f32(e0))));
+                acc1 = add_f32x2(acc1, pack_f32x2(fast_exp2(lo_f32(e1)), fast_exp2(hi_f32(e1))));
+              }
+            } else if (whole) {
 #pragma unroll
               for (int c = 0; c < 16; ++c) {
                 const float4 f = reinterpret_cast<const float4*>(terms)[16 * cc + c];
@@ -284,7 +300,13 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
             } else {
 #pragma unroll
               for (int c = 0; c < 16; ++c) {
-                const float4 f = reinterpret_cast<const float4*>(terms)[16 * cc + c];
+                float4 f;
+                if (p.tma) {
+                  const float2 e = reinterpret_cast<const float2*>(terms)[16 * cc + c];
+                  f = make_float4(slog, slog, e.x, e.y);
+                } else {
+                  f = reinterpret_cast<const float4*>(terms)[16 * cc + c];
+                }
                 const int c0 = 32 * cc + 2 * c;
                 const float e0 = c0 >= lo && c0 < n ? fmaf(lo_f32(s[c]), f.x, f.z) : -INFINITY;
                 const float e1 = c0 + 1 >= lo && c0 + 1 < n ? fmaf(hi_f32(s[c]), f.y, f.w) : -INFINITY;
@@ -397,10 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
                     tma_load_3d(sQ + par * C::kTileBytes + d * kHalfBytes, &tmq, &bar_q[par], 64 * d, it.h * G,
                                 it.q0 + int(p.group.quotient(b * BR)), l2_policy_evict_last());
                 }
-                if (tid < n) {
-                  terms[(tid >> 1) * 4 + (tid & 1)] = p.scale_log2 * head_scale;
-                  terms[(tid >> 1) * 4 + 2 + (tid & 1)] = e;
-                }
+                if (tid < n) terms[tid] = e;
                 __syncwarp();
                 if (lane == 0 && w > 0) mbar_arrive(&bar_q[par]);
                 continue;

