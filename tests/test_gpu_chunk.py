@@ -402,6 +402,41 @@ def test_blocks_past_4_gib(kind):
     c.check()
 
 
+def test_65535_chunks():
+    """As many chunks as a call takes, of zero to two rows over the same few blocks."""
+    import paged_kv_cache_160_gb300 as pkv
+    n = 65535
+    c = Case([40, 7], [1, 1], 2, 1, 64, "bf16", "fp4")
+    cc = c.cache
+    starts = np.arange(n) % 46
+    news = (np.arange(n) * 7 % 13 % 3).astype(int)
+    cu = np.concatenate([[0], np.cumsum(news)]).astype(np.int32)
+    total = int(cu[-1])
+    g = torch.Generator().manual_seed(3)
+    q = torch.randn((total, 2, 64), generator=g).to(torch.bfloat16)
+    tables = torch.from_numpy(np.ascontiguousarray(np.broadcast_to(cc.tables[0], (n, cc.tables.shape[1])))).cuda()
+    out, lse = torch.full_like(q, 5.0, device="cuda"), torch.empty((total, 2), device="cuda")
+    ws = torch.empty(pkv.pkv_chunk_workspace_bytes(total, 2, 1, 64), dtype=torch.uint8, device="cuda")
+    dev = [torch.from_numpy(a).cuda() for a in (cu, starts.astype(np.int32))]
+    pkv.pkv_paged_chunk_attention(out, q.cuda(), *dev, cc.k_cache, cc.v_cache, cc.desc, tables, 0.125, ws, lse=lse)
+    w = torch.full((n, 1, 48), 3.0, device="cuda")
+    pkv.pkv_attention_weights(w, None, 1.0, q.cuda(), lse, *dev, cc.k_cache, cc.desc, tables, 0.125)
+    assert pkv.pkv_get_device_error() == 0
+    j = np.arange(48)
+    k, v = (x[cc.tables[0, j // 16], :, j % 16] for x in (cc.k, cc.v))
+    sums = w.sum(-1)[:, 0].cpu().numpy()
+    for i in list(range(0, n, 4001)) + [n - 1]:
+        a, m, s = cu[i], news[i], int(starts[i])
+        if m == 0:
+            assert (w[i] == 3.0).all()
+            continue
+        ref, ref_lse, size = evict.chunk_attention(q[a:a + m].double().numpy(), k[:s + m], v[:s + m], s, 0.125)
+        err = np.abs(out[a:a + m].double().cpu().numpy() - ref)
+        assert (err <= 2.0 ** -10 * size + 2.0 ** -8 * np.abs(ref) + 2.0 ** -25).all()
+        assert abs(sums[i] - 2 * m - 3.0 * (48 - s - m)) <= 2.0 ** -9 * m
+    assert torch.isfinite(out.float()).all()
+
+
 def test_nothing_to_do():
     import paged_kv_cache_160_gb300 as pkv
     c = Case([5, 9], [0, 0], 4, 2, 64, "bf16", "fp4", pad=4)
