@@ -1,22 +1,26 @@
-// attention_weights: the attention weight that each cached token gets from a chunk's rows, summed over the rows and
-// over the query heads of its kv head, and added to what it had.
+// attention_weights: the attention weight that each cached token gets from a chunk's rows, summed over the
+// rows and over the query heads of its kv head, and added to what it had.
 //
-// Mathematics: with the rows' log-sum-exp known, p = exp(scale q . k - lse) needs no other key: a key's sum is
-// its own, and nothing is exchanged between keys.
+// Mathematics: with the rows' log-sum-exp known, p = exp(scale q . k - lse) needs no other key: a key's sum
+// is its own, and nothing is exchanged between keys.
 //
-// GB300 design: S^T = K Q^T on tcgen05, 128 keys by up to 128 flat query rows (row f is head f mod G of query row f / G), so that
-// a tensor memory lane is a key and its thread adds up a row of exponentials without a word to other threads.  Up to four
-// key tiles stay in shared memory while the blocks of query rows pass by, each tile's scores in 128 columns of their own: while one
-// tile's products run, the exponentials of the others are taken.  One or two blocks of rows stay too, and the key tiles pass
-// by.  Queries that need no change come by TMA, whole query rows a block; over e4m3 and 4 bits bf16 queries are turned into fp16
-// by the warps that turn the keys.  The list of (chunk, kv head, key tile) is cut over the SMs by the number of blocks that see
-// each tile: no tile's sum is split, so no order of sums depends on the run.
+// GB300 design: S^T = K Q^T on tcgen05, 128 keys by up to 128 flat query rows (row f is head f mod G of
+// query row f / G), so that a tensor memory lane is a key and its thread adds up a row of exponentials
+// without a word to other threads.  Up to four key tiles stay in shared memory while the blocks of query
+// rows pass by, each tile's scores in 128 columns of their own: while one tile's products run, the
+// exponentials of the others are taken.  One or two blocks of rows stay too, and the key tiles pass by.
+// Queries that need no change come by TMA, whole query rows a block; over e4m3 and 4 bits bf16 queries are
+// turned into fp16 by the warps that turn the keys.  The list of (chunk, kv head, key tile) is cut over the
+// SMs by the number of blocks that see each tile: no tile's sum is split, so no order of sums depends on
+// the run.
 //
-// Bound: few rows, HBM (64 sequences of up to 2,048 tokens, one row each, 28 heads over 4, bf16: 19.9 us, 0.57 of the measured
-// copy); many rows, the chain of a slot, products - exponentials - products (2,048 rows over 8,192 keys, 32 heads over 8, f16: 137 us; the
-// products alone take 62, the exponentials 51), where SMs with four key tiles work on for a fifth longer than the mean, and shared
-// memory: the products read 8 KB each, and two terms a row beside them instead of one cost 29 us.  64 rows over up to 16,384 keys of 4
-// bits: 47 us.  Not faster: the slots in halves of 64 rows (206 us where whole ones took 166: products of 64 columns read the keys as often).
+// Bound: few rows, HBM (64 sequences of up to 2,048 tokens, one row each, 28 heads over 4, bf16: 19.9 us,
+// 0.57 of the measured copy); many rows, the chain of a slot, products - exponentials - products (2,048
+// rows over 8,192 keys, 32 heads over 8, f16: 137 us; the products alone take 62, the exponentials 51),
+// where SMs with four key tiles work on for a fifth longer than the mean, and shared memory: the products
+// read 8 KB each, and two terms a row beside them instead of one cost 29 us.  64 rows over up to 16,384
+// keys of 4 bits: 47 us.  Not faster: the slots in halves of 64 rows (206 us where whole ones took 166:
+// products of 64 columns read the keys as often).
 #include <algorithm>
 
 #include "paged_tiles.cuh"
@@ -32,7 +36,7 @@ constexpr int kItems = 8;                     // items on their way from the sch
 constexpr int kMaxChunks = 65535;
 constexpr int kSeqChunk = 32;                 // chunks per entry of the table of work
 constexpr int kReaders = 16 + 8 + 1 + 1;      // warps that read the items: exponentials, loaders, MMA, key tiles by TMA
-constexpr int kTileCost = 2;                  // of a key tile beside its blocks: loading it takes about as long as two blocks' products
+constexpr int kTileCost = 2;                  // of a key tile beside its blocks: its load takes as long as about two of them
 
 struct WeightsParams {
   float* out;
@@ -141,8 +145,9 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
   __shared__ __align__(8) uint64_t bar_q[2], bar_q_empty[2], bar_k[kSlots], bar_k_empty[kSlots], bar_s[kSlots], bar_s_free[kSlots],
       bar_sum, bar_drain;
   __shared__ uint32_t tmem_base_sh;
-  // [block number mod 8]: (factor, factor, -lse, -lse) of row pairs; queries by TMA have one factor: only -lse of each row.  Block u + 8 is loaded once the products of u + 6 are done, and
-  // those of u + 4 at the latest waited for the sums of u.
+  // [block number mod 8]: (factor, factor, -lse, -lse) of row pairs; queries by TMA have one factor: only
+  // -lse of each row.  Block u + 8 is loaded once the products of u + 6 are done, and those of u + 4 at
+  // the latest waited for the sums of u.
   __shared__ __align__(16) float row_terms[8][2 * kTile];
   __shared__ float sums[2][kSlots][kTile];
   __shared__ int first_unit[(kMaxChunks + kSeqChunk - 1) / kSeqChunk + 1];
@@ -633,7 +638,8 @@ extern "C" pkv_status pkv_attention_weights(float* out, const float* weights, fl
   if (!err) return PKV_ERR_CUDA;
   const bool wide = cache->kv_dtype == PKV_F16 || cache->kv_dtype == PKV_BF16;
   const int G = num_heads / cache->num_kv_heads;
-  // bf16 queries over e4m3 and 4 bits are changed on the way; of more than 128 heads a kv head, no block holds a query row.
+  // bf16 queries over e4m3 and 4 bits are changed on the way; of more than 128 heads a kv head, no block
+  // holds a query row.
   const bool tma = (wide || q_dtype == PKV_F16) && G <= kTile;
   const int whole = tma ? kTile / G : 1;                     // query rows of a block
   WeightsParams prm = {.group = Divisor(G), .block = Divisor(tma ? whole * G : kTile)};

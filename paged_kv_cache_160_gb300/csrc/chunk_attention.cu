@@ -1,26 +1,31 @@
 // paged_chunk_attention: causal attention of each sequence's new rows over its paged cache of any type.
 //
-// Mathematics: row r of a chunk at positions start .. start + L - 1 attends keys 0 .. start + r, in one pass over
-// tiles of 128 keys with the running maximum m and sum l of the softmax (in units of log2): P = 2^(s c - m),
-// O = O 2^(m_old - m) + P V; out = O / l, lse = (m + log2 l) ln 2.  Parts of a row's keys are merged by their m and l.
+// Mathematics: row r of a chunk at positions start .. start + L - 1 attends keys 0 .. start + r, in one
+// pass over tiles of 128 keys with the running maximum m and sum l of the softmax (in units of log2): P =
+// 2^(s c - m), O = O 2^(m_old - m) + P V; out = O / l, lse = (m + log2 l) ln 2.  Parts of a row's keys are
+// merged by their m and l.
 //
-// GB300 design: the query rows of all heads of a kv head are one list of "flat" rows (row f is head f mod G of query row
-// f / G), cut into items of up to 256.  S = Q K^T and O += P V run on tcgen05 with S, P and O in tensor memory, in
-// two chains A and B so that one chain's softmax overlaps the other's products: of an item's two blocks of 128 rows over
-// the same keys, or, for an item of one block, of every other key tile (merged within the CTA).  The list of (item, key tile)
-// is cut into one equal range per SM, whatever the chunks' lengths: few rows over long histories use every SM, and no SM
-// works on for long after the others.  Items that several SMs work on are merged by a second kernel.
-//   Quantised rows are read from their blocks into registers, turned into fp16 (exact) and stored as operands by 16 warps
-// beside the softmax; 16-bit rows come by TMA.
+// GB300 design: the query rows of all heads of a kv head are one list of "flat" rows (row f is head f mod G
+// of query row f / G), cut into items of up to 256.  S = Q K^T and O += P V run on tcgen05 with S, P and O
+// in tensor memory, in two chains A and B so that one chain's softmax overlaps the other's products: of an
+// item's two blocks of 128 rows over the same keys, or, for an item of one block, of every other key tile
+// (merged within the CTA).  The list of (item, key tile) is cut into one equal range per SM, whatever the
+// chunks' lengths: few rows over long histories use every SM, and no SM works on for long after the others.
+// Items that several SMs work on are merged by a second kernel.
+//   Quantised rows are read from their blocks into registers, turned into fp16 (exact) and stored as
+// operands by 16 warps beside the softmax; 16-bit rows come by TMA.
 //
-// Bound: the chain of a tile, scores - softmax - products, of which two are under way.  A step takes 2,100 to 2,300 cycles, its
-// products 1,170: the issuer looks at four barriers a step at 200 cycles each, and the softmax of a block takes 1,800.  Measured
-// alone: 8 sequences of 32K to 128K tokens, 8 rows each, 32 heads over 8, D 128, 4 bits: 304 us (the bytes take 101); four chunks of 700 to
-// 1,024 rows behind 5K to 9K keys, 32 heads over 8: 454 us over e4m3, 428 over 4 bits, 366 over bf16 (0.61 of the measured bf16 rate);
-// 512 rows behind 3,584, 28 heads over 4, 4 bits: 64 us; 64 sequences of up to 2,048 tokens, 4 rows each: 49 us; 4 of up to 37: 11 us.
-//   Not faster: two softmax threads a row with half the loader warps (578 us over e4m3), an issuer for each chain (489), 64 scores per
-// load from tensor memory, asking L2 for tiles a window ahead.  One code path for all loader warps and loops that stay rolled are
-// what made it four times faster than the first form: unrolled, the warps' instructions came more slowly than they ran.
+// Bound: the chain of a tile, scores - softmax - products, of which two are under way.  A step takes 2,100
+// to 2,300 cycles, its products 1,170: the issuer looks at four barriers a step at 200 cycles each, and the
+// softmax of a block takes 1,800.  Measured alone: 8 sequences of 32K to 128K tokens, 8 rows each, 32 heads
+// over 8, D 128, 4 bits: 304 us (the bytes take 101); four chunks of 700 to 1,024 rows behind 5K to 9K
+// keys, 32 heads over 8: 454 us over e4m3, 428 over 4 bits, 366 over bf16 (0.61 of the measured bf16 rate);
+// 512 rows behind 3,584, 28 heads over 4, 4 bits: 64 us; 64 sequences of up to 2,048 tokens, 4 rows each:
+// 49 us; 4 of up to 37: 11 us.
+//   Not faster: two softmax threads a row with half the loader warps (578 us over e4m3), an issuer for each
+// chain (489), 64 scores per load from tensor memory, asking L2 for tiles a window ahead.  One code path
+// for all loader warps and loops that stay rolled are what made it four times faster than the first form:
+// unrolled, the warps' instructions came more slowly than they ran.
 #include <algorithm>
 
 #include "paged_tiles.cuh"
@@ -126,10 +131,11 @@ __device__ __forceinline__ int units_of(const ChunkParams& p, const Chunk& c) {
   return units;
 }
 
-// Adds to elements d0 .. d1 - 1 of a row that this thread has written (out, of out's type, or o, fp32) the non-finite values
-// among V[j] of keys j0 .. j1 - 1 of chunk seq, times `scale`.
+// Adds to elements d0 .. d1 - 1 of a row that this thread has written (out, of out's type, or o, fp32) the
+// non-finite values among V[j] of keys j0 .. j1 - 1 of chunk seq, times `scale`.
 template <bool kBF16, int D>
-__device__ __noinline__ void give_back(const ChunkParams& p, pkv_dtype kv, int seq, int h, int j0, int j1, int d0, int d1, float scale,
+__device__ __noinline__ void give_back(const ChunkParams& p, pkv_dtype kv, int seq, int h, int j0, int j1, int d0, int d1,
+                                       float scale,
                                        uint8_t* out, float* o) {
   for (int j = j0; j < j1; ++j) {
     const int blk = p.pc.tables[int64_t(seq) * p.pc.max_blocks + (j >> p.pc.block_shift)];
@@ -173,10 +179,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ __align__(16) int items[kItems][12];
   __shared__ __align__(8) uint64_t bar_item[kItems], bar_item_read[kItems];
-  // Q area filled / no product reads it any more; K, V tiles likewise (V: looked at); S_x ready; P_x ready; PV_x done;
-  // O read; both chains' maxima and sums there.
+  // Q area filled / no product reads it any more; K, V tiles likewise (V: looked at); S_x ready; P_x
+  // ready; PV_x done; O read; both chains' maxima and sums there.
   __shared__ __align__(8) uint64_t bar_q[2], bar_q_empty[2], bar_k_full[kStages], bar_k_empty[kStages], bar_v_full[kStages],
-      bar_v_seen[kStages], bar_v_empty[kStages], bar_s_full[2], bar_p_full[2], bar_pv_done[2], bar_o_free, bar_ml, bar_peak[2], bar_drain;
+      bar_v_seen[kStages], bar_v_empty[kStages], bar_s_full[2], bar_p_full[2], bar_pv_done[2], bar_o_free, bar_ml,
+      bar_peak[2], bar_drain;
   __shared__ uint32_t tmem_base_sh;
   __shared__ float factor[2][2][kTile];                      // [query area][use mod 2][row]: products to scores in log2 units
   __shared__ __align__(8) float2 chain_ml[2][2][kTile];      // [item parity][chain][row]
@@ -186,7 +193,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ int first_unit[(kMaxChunks + kSeqChunk - 1) / kSeqChunk + 1];
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // uniform in the warp
 
-  // Weights of few rows come first: as an operand of 128 rows they reach into the queries, whose rows count for nothing.
+  // Weights of few rows come first: as an operand of 128 rows they reach into the queries, whose rows
+  // count for nothing.
   uint8_t* sP = smem;                                        // [chain][64-key half][32 rows]
   uint8_t* sQ = smem + 2 * C::kWeights;                      // [area][64-dim half][128 rows]
   uint8_t* sK = sQ + 2 * C::kTileBytes;                      // [stage][64-dim half][128 rows]
@@ -372,24 +380,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (two) {
               tmem_ld32(tO + 128 * x + 32 * cc, v);
               tmem_wait_ld();
-  #pragma unroll
+#pragma unroll
               for (int c = 0; c < 32; ++c) v[c] = have0 ? v[c] * w0 : 0.f;
             } else {
               float b[32];
               tmem_ld32(tO + 32 * cc, v);
               tmem_ld32(tO + 128 + 32 * cc, b);
               tmem_wait_ld();
-  #pragma unroll
+#pragma unroll
               for (int c = 0; c < 32; ++c) v[c] = (have0 ? v[c] * w0 : 0.f) + (have1 ? b[c] * w1 : 0.f);
             }
             if (r < rows) {
               if (it.slot >= 0) {
-  #pragma unroll
+#pragma unroll
                 for (int c = 0; c < 8; ++c)
                   reinterpret_cast<float4*>(part_o)[8 * cc + c] = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
               } else {
                 uint4* dst = reinterpret_cast<uint4*>(p.out + unit * (2 * D) + 64 * cc);
-  #pragma unroll
+#pragma unroll
                 for (int c = 0; c < 4; ++c)
                   dst[c] = make_uint4(pack2<kBF16>(v[8 * c], v[8 * c + 1]), pack2<kBF16>(v[8 * c + 2], v[8 * c + 3]),
                                       pack2<kBF16>(v[8 * c + 4], v[8 * c + 5]), pack2<kBF16>(v[8 * c + 6], v[8 * c + 7]));
@@ -437,8 +445,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (k == 0) slog = *fac;
         const int lim = keys - tile * kTile;                 // keys 0 .. lim - 1 are attended
         if (few) {
-          // Every quarter of the lanes has a copy of the rows' scores; its warp takes a quarter of the keys.  One warp for
-          // all of a row's keys took 2400 cycles a tile, on one of the SM's four schedulers.
+          // Every quarter of the lanes has a copy of the rows' scores; its warp takes a quarter
+          // of the keys.  One warp for all of a row's keys took 2400 cycles a tile, on one of the
+          // SM's four schedulers.
           float s[32];
           tmem_ld32(tS + 32 * quarter, s);
           tmem_wait_ld();
@@ -626,9 +635,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           (void)mbar_wait(w == 0 ? &bar_k_full[u % kStages] : &bar_v_full[u % kStages], (u / kStages) & 1u);
       }
     } else {
-      // A tile is on its way in registers while the one before it is turned (la: the item of the tile to load, it: of the
-      // tile to store).  Loops that stay small: with two tiles' registers and code in each of 8 warps, instructions were
-      // fetched more slowly than they ran (8 sequences of 32K to 128K tokens: 391 us).
+      // A tile is on its way in registers while the one before it is turned (la: the item of the tile
+      // to load, it: of the tile to store).  Loops that stay small: with two tiles' registers and
+      // code in each of 8 warps, instructions were fetched more slowly than they ran (8 sequences of
+      // 32K to 128K tokens: 391 us).
       StoredTile<KV, D> ahead;
       TableWindow win;
       const uint8_t* cache = is_v ? p.v_cache : p.k_cache;
@@ -854,8 +864,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       done_reading(i);
       if (it.rows == 0) break;
       if (it.two()) {
-        // Not ours to fill, but to wait for: a later wait could take an earlier phase that was skipped for its own.  The arrival
-        // keeps the areas' next phases from passing before that.
+        // Not ours to fill, but to wait for: a later wait could take an earlier phase that was
+        // skipped for its own.  The arrival keeps the areas' next phases from passing before that.
         for (int a = 0; a < 2 && ok; ++a) {
           ok = all(uses[a] == 0 || mbar_wait(&bar_q_empty[a], (uses[a] - 1) & 1u));
           uses.up(a);
@@ -889,8 +899,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Merges the parts of items that several CTAs worked on.  A CTA begins at most one such item, as its last; the other parts
-// are the first ones of the CTAs after it.  blockIdx.x: the CTA that began it; kMergeRows rows each, a warp per row.
+// Merges the parts of items that several CTAs worked on.  A CTA begins at most one such item, as its last;
+// the other parts are the first ones of the CTAs after it.  blockIdx.x: the CTA that began it; kMergeRows
+// rows each, a warp per row.
 constexpr int kMergeRows = 16;
 template <bool kBF16, int D>
 __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const ChunkParams p, int ctas, bool scaled) {
@@ -947,7 +958,8 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const ChunkP
       }
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
-        if (k0 + u >= n || ml[u].x == -INFINITY) continue;   // (a part without keys for the row: its O is 0 or was never written)
+        // A part without keys for the row: its O is 0 or was never written.
+        if (k0 + u >= n || ml[u].x == -INFINITY) continue;
         const float w = fast_exp2(ml[u].x - m);
         l += ml[u].y * w;
 #pragma unroll

@@ -51,16 +51,16 @@ __device__ __forceinline__ void add_to_peer(const void* p, uint32_t rank, uint32
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
-// A cluster of 1 to 8 CTAs per (sequence, kv head).  Every warp has a run of consecutive positions, so that counts
-// and ballots alone give the order of the output.
-//   The rank of the last one kept is found a digit at a time: each CTA counts its own positions' digits and adds the counts
-// that are not zero to every CTA's totals.  (Reading all counts of all CTAs took 4 to 8 thousand cycles a digit.  11 bits: the first digit holds the exponent and two bits of the mantissa, which spreads
-// weights of similar size over several counters.)
-//   kStored: the ranks stay in shared memory, one pass over the weights; else (longer rows) the weights are read again for
-// each digit.
-// Bound: launch, and three rounds of counting, a barrier and a scan.  Measured: 64 sequences of up to 2,048 positions, 4 heads:
-// 7.8 us; 8 of 32K to 128K, 8 heads: 39.6 us (512 CTAs of which 304 run at once; 58 us with the weights read again for each digit
-// and twice the CTAs).
+// A cluster of 1 to 8 CTAs per (sequence, kv head).  Every warp has a run of consecutive positions, so that
+// counts and ballots alone give the order of the output.
+//   The rank of the last one kept is found a digit at a time: each CTA counts its own positions' digits and
+// adds the counts that are not zero to every CTA's totals.  (Reading all counts of all CTAs took 4 to 8
+// thousand cycles a digit.  11 bits: the first digit holds the exponent and two bits of the mantissa, which
+// spreads weights of similar size over several counters.)
+//   kStored: the ranks stay in shared memory, one pass over the weights; else (longer rows) the weights are
+// read again for each digit. Bound: launch, and three rounds of counting, a barrier and a scan.  Measured:
+// 64 sequences of up to 2,048 positions, 4 heads: 7.8 us; 8 of 32K to 128K, 8 heads: 39.6 us (512 CTAs of
+// which 304 run at once; 58 us with the weights read again for each digit and twice the CTAs).
 template <bool kStored>
 __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectParams p, int ctas) {
   extern __shared__ uint32_t ranks[];                        // [warp][run]
@@ -238,12 +238,13 @@ struct CompactParams {
 };
 
 // A cluster of CTAs per (sequence, kv head) and K, V or the weights (blockIdx.y).
-//   In place: kept positions ascend, so a row only ever moves to a lower position, and what a row at position d
-// overwrites is needed by rows up to d alone.  A round reads the sources of consecutive destinations, all CTAs of the
-// cluster meet, and then it writes; rounds ascend.  The next round's reads lie behind everything that this one writes.
-// Bound: HBM, by reads and writes in flight: rows are `pieces` of 16 bytes, eight of them in flight per thread, and the next
-// round's moves are looked up beside them.  Measured: 512 rows of 64 sequences, 4 heads of 128 in bf16: 27.9 us, 0.68 of the
-// measured copy; 8,192 of 3 sequences, 8 heads in e4m3, in clusters of 8: 27.5 us, 0.56.
+//   In place: kept positions ascend, so a row only ever moves to a lower position, and what a row at
+// position d overwrites is needed by rows up to d alone.  A round reads the sources of consecutive
+// destinations, all CTAs of the cluster meet, and then it writes; rounds ascend.  The next round's reads
+// lie behind everything that this one writes. Bound: HBM, by reads and writes in flight: rows are `pieces`
+// of 16 bytes, eight of them in flight per thread, and the next round's moves are looked up beside them.
+// Measured: 512 rows of 64 sequences, 4 heads of 128 in bf16: 27.9 us, 0.68 of the measured copy; 8,192 of
+// 3 sequences, 8 heads in e4m3, in clusters of 8: 27.5 us, 0.56.
 template <bool kFp4, bool kUnit8>
 __global__ void __launch_bounds__(kMoveThreads, kMoveCtas) compact_kernel(const CompactParams p, int ctas) {
   __shared__ int64_t src_at[2][kMoveRows], dst_at[2][kMoveRows];             // rows of the pool; -1: no move

@@ -1,9 +1,9 @@
-// Tiles of 128 keys of a paged cache, and blocks of 128 query rows, as operands of the tensor cores: 16-bit rows
-// in shared memory, [64-element half][128 rows] of 128 bytes each with the 128-byte swizzle.
+// Tiles of 128 keys of a paged cache, and blocks of 128 query rows, as operands of the tensor cores: 16-bit
+// rows in shared memory, [64-element half][128 rows] of 128 bytes each with the 128-byte swizzle.
 //
-// e4m3 and 4-bit rows are turned into fp16, which holds code * scale of their 16 exactly; the kv head's scale is applied
-// to scores and outputs.  Their queries are then fp16 too: bf16 rows are multiplied by a power of two that brings
-// their largest element to 2^14 .. 2^15, taken back with the scale of the scores.
+// e4m3 and 4-bit rows are turned into fp16, which holds code * scale of their 16 exactly; the kv head's
+// scale is applied to scores and outputs.  Their queries are then fp16 too: bf16 rows are multiplied by a
+// power of two that brings their largest element to 2^14 .. 2^15, taken back with the scale of the scores.
 #pragma once
 
 #include "cache_row.cuh"
@@ -208,13 +208,15 @@ __device__ __forceinline__ bool make_row_finite(uint32_t base, int r) {
 // 2^-e as fp64, |e| < 1000.
 __device__ __forceinline__ double exp2_int(int e) { return __hiloint2double((1023 + e) << 20, 0); }
 
-// Flat rows f0 .. f0 + n - 1 (n <= 128) of a chunk whose first row is q0 and of kv head h, flat row f being row f / G
-// of head h G + f mod G, as an operand at `base`, by kThreadsOf threads, 8 for a row.  Quantised caches (kToF16): as fp16, times the
-// sign of the kv head's scale, and for bf16 times a power of two.  put(r, c, e) gets, once for row r, the factor c from
-// products to scores in units of log2 (scale_log2 * head_scale and that power; for 16-bit caches scale_log2) and e = extra(i),
-// i being the row's number among [total_q][num_heads]; it is asked for together with the rows.  kAhead rows of a thread are
-// on their way at a time, and ready() is called when the first of them are: it waits until the operand's place is free, and where
-// it returns false nothing is written.  With copies > 1 (n <= 32) the rows also go to rows 32, 64 .. on.
+// Flat rows f0 .. f0 + n - 1 (n <= 128) of a chunk whose first row is q0 and of kv head h, flat row f being
+// row f / G of head h G + f mod G, as an operand at `base`, by kThreadsOf threads, 8 for a row.  Quantised
+// caches (kToF16): as fp16, times the sign of the kv head's scale, and for bf16 times a power of two.
+// put(r, c, e) gets, once for row r, the factor c from products to scores in units of log2 (scale_log2 *
+// head_scale and that power; for 16-bit caches scale_log2) and e = extra(i), i being the row's number among
+// [total_q][num_heads]; it is asked for together with the rows.  kAhead rows of a thread are on their way
+// at a time, and ready() is called when the first of them are: it waits until the operand's place is free,
+// and where it returns false nothing is written.  With copies > 1 (n <= 32) the rows also go to rows 32, 64
+// .. on.
 template <bool kBF16, bool kToF16, int D, int kThreadsOf, int kAhead, typename Ready, typename Extra, typename Put>
 __device__ __forceinline__ bool load_queries(uint32_t base, const uint8_t* q, int64_t q0, int num_heads, int h,
                                              const Divisor& group, int f0, int n, int copies, float scale_log2, float head_scale, int tid,
