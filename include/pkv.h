@@ -393,8 +393,9 @@ PKV_API size_t pkv_chunk_workspace_bytes(int total_q, int num_heads, int num_kv_
  * ascending from 0 or past total_q, q_start_pos < 0, or positions past its table) sets PKV_DEVERR_CHUNK and its
  * rows stay unwritten.  A block id outside the pool sets PKV_DEVERR_BLOCK_ID; its keys and values count as zeros.
  * Supported: f16, bf16, e4m3 and 4-bit caches, head_dim 64 or 128, block_size 16 or 32, any number of query heads
- * per kv head, scale > 0 and finite, num_chunks up to 65535, total_q * num_heads and max_blocks_per_seq * block_size
- * below 2^31, and (total_q * (num_heads / num_kv_heads) / 64 + 3 num_chunks) * (max_blocks_per_seq * block_size / 128 + 2)
+ * per kv head, scale > 0 and finite, num_chunks up to 65535, total_q * num_heads below 2^31 - 512,
+ * max_blocks_per_seq * block_size up to 2^31 - 128, and
+ * (total_q * (num_heads / num_kv_heads) / 64 + 3 num_chunks) * (max_blocks_per_seq * block_size / 128 + 2)
  * below 2^31.  Sums, maxima and outputs are fp32 until the last rounding; the softmax's exponentials are rounded to
  * the type of their product with V (q_dtype; fp16 over e4m3 and 4 bits).  Over e4m3 and 4 bits, bf16 q is taken as
  * fp16 after a power of two for each row (bits below 2^-25 of the row's largest are lost).  All of it
@@ -447,6 +448,7 @@ PKV_API pkv_status pkv_attention_weights(float* out, const float* weights, float
  *   kept           (device) int32 [num_seqs][num_kv_heads][max_keep]
  *   context_lens, keep_lens (device) int32 [num_seqs]; a context_len outside 0 .. max_len or a keep_len outside
  *                  0 .. max_keep sets PKV_DEVERR_CONTEXT_LEN and gives -1 throughout, as does a sequence without a row
+ * Supported: max_len and max_keep up to 2^30.
  */
 PKV_API pkv_status pkv_evict_select(int32_t* kept, int max_keep, const float* weights, int num_rows, int max_len,
                                     const int32_t* rows, const int32_t* context_lens, const int32_t* keep_lens,
@@ -465,7 +467,8 @@ PKV_API pkv_status pkv_evict_select(int32_t* kept, int max_keep, const float* we
  *   src_tables     (device) int32 [num_seqs][src_max_blocks]; dst_tables [num_seqs][dst_max_blocks]
  *   weights        (device) or NULL: only K and V move
  *   dst_rows       (device) or NULL: rows.  Distinct rows; dst_rows[i] is rows[i] or a row that the call does not read
- * Any cache type, head_dim a multiple of 16 up to 256.  Launch order as pkv_kv_write, for all four calls.
+ * Any cache type, head_dim a multiple of 16 up to 256, max_keep up to 2^30; k_cache is not v_cache.
+ * Launch order as pkv_kv_write, for all four calls.
  */
 PKV_API pkv_status pkv_evict_compact(void* k_cache, void* v_cache, const pkv_cache_desc* cache, const int32_t* kept,
                                      int max_keep, const int32_t* keep_lens, const int32_t* src_tables,

@@ -135,8 +135,7 @@ __device__ __forceinline__ int units_of(const ChunkParams& p, const Chunk& c) {
 // non-finite values among V[j] of keys j0 .. j1 - 1 of chunk seq, times `scale`.
 template <bool kBF16, int D>
 __device__ __noinline__ void give_back(const ChunkParams& p, pkv_dtype kv, int seq, int h, int j0, int j1, int d0, int d1,
-                                       float scale,
-                                       uint8_t* out, float* o) {
+                                       float scale, uint8_t* out, float* o) {
   for (int j = j0; j < j1; ++j) {
     const int blk = p.pc.tables[int64_t(seq) * p.pc.max_blocks + (j >> p.pc.block_shift)];
     if (unsigned(blk) >= unsigned(p.pc.num_blocks)) continue;

@@ -14,6 +14,7 @@ namespace {
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kMaxCluster = 8;
+constexpr int kMostPositions = 1 << 30;       // of a row: loops step past the end of one in 32 bits
 constexpr int kDigits = 3;                    // of 11, 11 and 10 bits, from the top
 constexpr int kBins = 2048;
 
@@ -58,9 +59,10 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 // thousand cycles a digit.  11 bits: the first digit holds the exponent and two bits of the mantissa, which
 // spreads weights of similar size over several counters.)
 //   kStored: the ranks stay in shared memory, one pass over the weights; else (longer rows) the weights are
-// read again for each digit. Bound: launch, and three rounds of counting, a barrier and a scan.  Measured:
-// 64 sequences of up to 2,048 positions, 4 heads: 7.8 us; 8 of 32K to 128K, 8 heads: 39.6 us (512 CTAs of
-// which 304 run at once; 58 us with the weights read again for each digit and twice the CTAs).
+// read again for each digit.
+// Bound: launch, and three rounds of counting, a barrier and a scan.  Measured: 64 sequences of up to 2,048
+// positions, 4 heads: 7.8 us; 8 of 32K to 128K, 8 heads: 39.6 us (512 CTAs of which 304 run at once; 58 us
+// with the weights read again for each digit and twice the CTAs).
 template <bool kStored>
 __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectParams p, int ctas) {
   extern __shared__ uint32_t ranks[];                        // [warp][run]
@@ -241,8 +243,9 @@ struct CompactParams {
 //   In place: kept positions ascend, so a row only ever moves to a lower position, and what a row at
 // position d overwrites is needed by rows up to d alone.  A round reads the sources of consecutive
 // destinations, all CTAs of the cluster meet, and then it writes; rounds ascend.  The next round's reads
-// lie behind everything that this one writes. Bound: HBM, by reads and writes in flight: rows are `pieces`
-// of 16 bytes, eight of them in flight per thread, and the next round's moves are looked up beside them.
+// lie behind everything that this one writes.
+// Bound: HBM, by reads and writes in flight: rows are `pieces` of 16 bytes, eight of them in flight per
+// thread, and the next round's moves are looked up beside them.
 // Measured: 512 rows of 64 sequences, 4 heads of 128 in bf16: 27.9 us, 0.68 of the measured copy; 8,192 of
 // 3 sequences, 8 heads in e4m3, in clusters of 8: 27.5 us, 0.56.
 template <bool kFp4, bool kUnit8>
@@ -428,7 +431,9 @@ pkv_status pkv_evict_select(int32_t* kept, int max_keep, const float* weights, i
                         static_cast<const void*>(rows), static_cast<const void*>(context_lens),
                         static_cast<const void*>(keep_lens)})
     if (reinterpret_cast<uintptr_t>(p) & 3u) return PKV_ERR_INVALID_ARG;
-  if (int64_t(num_seqs) * num_kv_heads >= (int64_t(1) << 31) / kMaxCluster) return PKV_ERR_UNSUPPORTED;
+  if (int64_t(num_seqs) * num_kv_heads >= (int64_t(1) << 31) / kMaxCluster || max_keep > kMostPositions ||
+      max_len > kMostPositions)
+    return PKV_ERR_UNSUPPORTED;
   unsigned* err = error_word_ptr();
   if (!err) return PKV_ERR_CUDA;
   SelectParams prm = {kept, weights, rows, context_lens, keep_lens, max_keep, num_rows, max_len, num_kv_heads, first, recent, err};
@@ -463,13 +468,15 @@ pkv_status pkv_evict_compact(void* k_cache, void* v_cache, const pkv_cache_desc*
   if (!k_cache || !v_cache || !kept || !keep_lens || !src_tables || !dst_tables || src_max_blocks == 0 ||
       dst_max_blocks == 0 || (weights && (num_rows == 0 || max_len == 0)))
     return PKV_ERR_INVALID_ARG;
-  if (!aligned16(k_cache) || !aligned16(v_cache)) return PKV_ERR_INVALID_ARG;
+  // One cache as both would be moved by two CTAs at once.
+  if (!aligned16(k_cache) || !aligned16(v_cache) || k_cache == v_cache) return PKV_ERR_INVALID_ARG;
   for (const void* p : {static_cast<const void*>(kept), static_cast<const void*>(weights),
                         static_cast<const void*>(rows), static_cast<const void*>(dst_rows),
                         static_cast<const void*>(keep_lens), static_cast<const void*>(src_tables),
                         static_cast<const void*>(dst_tables)})
     if (reinterpret_cast<uintptr_t>(p) & 3u) return PKV_ERR_INVALID_ARG;
-  if (int64_t(num_seqs) * cache->num_kv_heads >= (int64_t(1) << 31) / kMaxCluster) return PKV_ERR_UNSUPPORTED;
+  if (int64_t(num_seqs) * cache->num_kv_heads >= (int64_t(1) << 31) / kMaxCluster || max_keep > kMostPositions)
+    return PKV_ERR_UNSUPPORTED;
   unsigned* err = error_word_ptr();
   if (!err) return PKV_ERR_CUDA;
   const bool fp4 = cache->kv_dtype == PKV_FP4_E2M1;

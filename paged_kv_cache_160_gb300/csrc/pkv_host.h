@@ -49,7 +49,7 @@ inline int64_t cache_block_bytes(const pkv_cache_desc* c) {
 inline bool chunk_work_fits(int num_chunks, int total_q, int num_heads, int max_blocks, const pkv_cache_desc* c) {
   const int64_t most = int64_t(1) << 31, keys = int64_t(max_blocks) * c->block_size;
   const int64_t blocks = int64_t(total_q) * (num_heads / c->num_kv_heads) / 64 + 3 * int64_t(num_chunks);
-  return num_chunks <= 65535 && int64_t(total_q) * num_heads < most - 512 && keys < most && blocks < most / (keys / 128 + 2);
+  return num_chunks <= 65535 && int64_t(total_q) * num_heads < most - 512 && keys <= most - 128 && blocks < most / (keys / 128 + 2);
 }
 
 // Shared checks of a cache descriptor; returns PKV_OK or the failing status.

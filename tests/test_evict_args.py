@@ -44,7 +44,8 @@ def test_refusals_of_chunk_calls(call):
     assert call(desc=_desc(kv=1), qd=0) == UNSUPPORTED
     assert call(total=1 << 28, hq=8) == UNSUPPORTED
     assert call(n=70000, total=1 << 20) == UNSUPPORTED
-    # pieces of work numbered in 32 bits
+    # positions, rounded up to a key tile, and pieces of work in 32 bits
+    assert call(width=(1 << 27) - 7) == UNSUPPORTED and call(width=(1 << 27) - 8) != UNSUPPORTED
     assert call(total=1 << 20, hq=1024, width=1 << 20) == UNSUPPORTED
     e4m3 = _desc(kv=2)
     e4m3.k_scale = None
@@ -76,23 +77,24 @@ def test_refusals_of_select_and_compact():
                 dict(n=-1), dict(heads=0), dict(first=-1), dict(recent=-1)):
         assert call(**bad) == INVALID, bad
     assert call(n=1 << 20, heads=1 << 12) == UNSUPPORTED
+    assert call(max_len=(1 << 30) + 1) == UNSUPPORTED and call(max_keep=(1 << 30) + 1) == UNSUPPORTED
     assert call(n=0) == OK and call(max_keep=0) == OK
     names = ("k", "v", "desc", "kept", "max_keep", "keep", "src", "sb", "dst", "db", "w", "num_rows", "max_len", "rows",
              "dst_rows", "n")
-    good = dict(k=16, v=16, desc=_desc(), kept=4, max_keep=8, keep=4, src=4, sb=3, dst=4, db=3, w=4, num_rows=2, max_len=9,
+    good = dict(k=16, v=32, desc=_desc(), kept=4, max_keep=8, keep=4, src=4, sb=3, dst=4, db=3, w=4, num_rows=2, max_len=9,
                 rows=4, dst_rows=4, n=2)
 
     def move(**k):
         a = dict(good, **k)
         a["desc"] = ctypes.byref(a["desc"])
         return pkv.lib.pkv_evict_compact(*[a[x] for x in names], None)
-    for bad in (dict(k=0), dict(k=8), dict(v=0), dict(v=24), dict(kept=0), dict(kept=2), dict(keep=0), dict(keep=2),
+    for bad in (dict(k=0), dict(k=8), dict(v=0), dict(v=24), dict(k=32), dict(kept=0), dict(kept=2), dict(keep=0), dict(keep=2),
                 dict(src=0), dict(src=3), dict(dst=0), dict(dst=2), dict(sb=0), dict(db=0), dict(sb=-1), dict(db=-1),
                 dict(w=2), dict(num_rows=0), dict(max_len=0), dict(rows=1), dict(dst_rows=1), dict(n=-1), dict(max_keep=-1)):
         assert move(**bad) == INVALID, bad
     assert move(desc=_desc(kv=1, dim=40)) == UNSUPPORTED and move(desc=_desc(dim=272)) == UNSUPPORTED
     assert move(desc=_desc(block=8)) == UNSUPPORTED
-    assert move(n=1 << 30) == UNSUPPORTED
+    assert move(n=1 << 30) == UNSUPPORTED and move(max_keep=(1 << 30) + 1) == UNSUPPORTED
     assert move(n=0) == OK and move(max_keep=0) == OK and move(w=0, num_rows=0, max_len=0, n=0) == OK
 
 
