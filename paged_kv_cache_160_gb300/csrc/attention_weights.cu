@@ -14,12 +14,12 @@
 // SMs by the number of blocks that see each tile: no tile's sum is split, so no order of sums depends on
 // the run.
 //
-// Bound: few rows, HBM (64 sequences of up to 2,048 tokens, one row each, 28 heads over 4, bf16: 19.9 us,
-// 0.57 of the measured copy); many rows, the chain of a slot, products - exponentials - products (2,048
-// rows over 8,192 keys, 32 heads over 8, f16: 137 us; the products alone take 62, the exponentials 51),
+// Bound: few rows, HBM (64 sequences of up to 2,048 tokens, one row each, 28 heads over 4, bf16: 20.4 us,
+// 0.55 of the measured copy); many rows, the chain of a slot, products - exponentials - products (2,048
+// rows over 8,192 keys, 32 heads over 8, f16: 138 us; the products alone take 62, the exponentials 51),
 // where SMs with four key tiles work on for a fifth longer than the mean, and shared memory: the products
 // read 8 KB each, and two terms a row beside them instead of one cost 29 us.  64 rows over up to 16,384
-// keys of 4 bits: 47 us.  Not faster: the slots in halves of 64 rows (206 us where whole ones took 166:
+// keys of 4 bits: 48 us.  Not faster: the slots in halves of 64 rows (206 us where whole ones took 166:
 // products of 64 columns read the keys as often).
 #include <algorithm>
 

@@ -18,10 +18,10 @@
 // Bound: the chain of a tile, scores - softmax - products, of which two are under way.  A step takes 2,100
 // to 2,300 cycles, its products 1,170: the issuer looks at four barriers a step at 200 cycles each, and the
 // softmax of a block takes 1,800.  Measured alone: 8 sequences of 32K to 128K tokens, 8 rows each, 32 heads
-// over 8, D 128, 4 bits: 304 us (the bytes take 101); four chunks of 700 to 1,024 rows behind 5K to 9K
-// keys, 32 heads over 8: 454 us over e4m3, 428 over 4 bits, 366 over bf16 (0.61 of the measured bf16 rate);
+// over 8, D 128, 4 bits: 305 us (the bytes take 101); four chunks of 700 to 1,024 rows behind 5K to 9K
+// keys, 32 heads over 8: 459 us over e4m3, 428 over 4 bits, 366 over bf16 (0.61 of the measured bf16 rate);
 // 512 rows behind 3,584, 28 heads over 4, 4 bits: 64 us; 64 sequences of up to 2,048 tokens, 4 rows each:
-// 49 us; 4 of up to 37: 11 us.
+// 49 us; 4 of up to 37: 12 us.
 //   Not faster: two softmax threads a row with half the loader warps (578 us over e4m3), an issuer for each
 // chain (489), 64 scores per load from tensor memory, asking L2 for tiles a window ahead.  One code path
 // for all loader warps and loops that stay rolled are what made it four times faster than the first form:
