@@ -390,7 +390,7 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveCtas) compact_kernel(const 
         *reinterpret_cast<uint4*>(cache + place(d) + 16 * c) = v[u];
       }
     }
-    __syncthreads();                                         // this round's addresses may be overwritten
+    __syncthreads();                                         // the addresses just used may be overwritten
   }
 }
 
