@@ -419,14 +419,14 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
                 if (tid < n) e = __ldg(p.lse + (it.q0 + row) * p.num_heads + it.h * G + (f - row * G)) * -1.4426950408889634f;
                 if (!all(use == 0 || mbar_wait(&bar_q_empty[par], (use - 1) & 1u))) return false;
                 if (tid == 0) {
-                  mbar_arrive_expect_tx(&bar_q[par], BR * D * 2);
+                  mbar_expect_tx(&bar_q[par], BR * D * 2);
                   for (int d = 0; d < D / 64; ++d)
                     tma_load_3d(sQ + par * C::kTileBytes + d * kHalfBytes, &tmq, &bar_q[par], 64 * d, it.h * G,
                                 it.q0 + int(p.group.quotient(b * BR)), l2_policy_evict_last());
                 }
                 if (tid < n) terms[tid] = e;
                 __syncwarp();
-                if (lane == 0 && w > 0) mbar_arrive(&bar_q[par]);
+                if (lane == 0) mbar_arrive(&bar_q[par]);         // every warp's behind its terms: they may come later than the copy
                 continue;
               }
               const bool loaded = load_queries<kBF16, !kWide, D, 128, 4>(smem_u32(sQ) + par * C::kTileBytes, p.q, it.q0, p.num_heads, it.h, p.group, b * BR, n, 1,

@@ -217,6 +217,29 @@ def test_weights_errors():
     c.check_weights()
 
 
+@pytest.mark.parametrize("kind,dtype", [("same", "bf16"), ("same", "f16"), ("e4m3", "f16"), ("fp4", "f16")])
+def test_weights_of_log_sum_exps_that_come_late(kind, dtype):
+    """Queries and keys are in L2, the rows' log-sum-exps are not: no product may run ahead of them.  (The forms whose
+    queries are copied unchanged; the call before leaves other rows' terms in every place.)"""
+    c = Weights([700 + 9 * i for i in range(40)], [1 + i % 5 for i in range(40)], 8, 2, 128, dtype, kind)
+    cold = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")        # more than L2 holds
+    right, wrong = c.lse.clone(), torch.full_like(c.lse, -40.0)
+    for _ in range(20):
+        c.lse.copy_(wrong)
+        c.call_weights()
+        c.lse.copy_(right)
+        cold.fill_(_)
+        c.q_dev.view(torch.uint8).sum()
+        c.cache.k_cache.view(torch.uint8).sum()
+        c.w.fill_(3.0)
+        c.call_weights()
+        assert c.pkv.pkv_get_device_error() == 0
+        if _ == 0:
+            c.check_weights()
+            first = c.w.clone()
+        assert torch.equal(first, c.w)
+
+
 def test_weights_in_a_graph_and_twice_the_same():
     c = Weights([900, 30], [3, 2], 8, 2, 128, "bf16", "fp4")
     c.call_weights()
