@@ -146,8 +146,8 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
       bar_sum, bar_drain;
   __shared__ uint32_t tmem_base_sh;
   // [block number mod 8]: (factor, factor, -lse, -lse) of row pairs; queries by TMA have one factor: only
-  // -lse of each row.  Block u + 8 is loaded once the products of u + 6 are done, and those of u + 4 at
-  // the latest waited for the sums of u.
+  // -lse of each row.  Block u + 8 is loaded once the products of u + 6 are done; by then those of u + 4 at
+  // the latest have waited for the sums of u, or a smaller group has begun, which waits for all.
   __shared__ __align__(16) float row_terms[8][2 * kTile];
   __shared__ float sums[2][kSlots][kTile];
   __shared__ int first_unit[(kMaxChunks + kSeqChunk - 1) / kSeqChunk + 1];
@@ -516,7 +516,12 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
       // ---------------- MMA issuer (the whole warp; see mma_ss) ----------------
       const uint32_t lead = elect_one();
       const uint64_t dK = umma_sdesc_sw128(smem_u32(sK), 16, 1024), dQ = umma_sdesc_sw128(smem_u32(sQ), 16, 1024);
-      uint32_t kc = 0, qc = 0, used = 0, parity = 0;         // key tiles; blocks; by slot: its scores were written, how often mod 2
+      uint32_t kc = 0, qc = 0, parity = 0;                   // key tiles; blocks; by slot: how often its scores were written, mod 2
+      uint32_t open = 0;                                     // by slot: whether these are still to be waited for
+      auto wait_free = [&](uint32_t slot) -> bool {
+        open &= ~(1u << slot);
+        return all(mbar_wait(&bar_s_free[slot], (parity >> slot & 1u) ^ 1u));
+      };
       for (uint32_t i = 0;; ++i) {
         ok = ok && wait_item(i);
         if (!ok) break;
@@ -527,6 +532,12 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
         const bool stay = NB <= 2;
         ok = each_group(it, [&](int t, int nt, int b0) -> bool {
           const int turns = nt == 1 ? 4 : nt == 2 ? 2 : 1;
+          // Every block of a group of four tiles waits for every slot.  A smaller group may leave slots out, whose
+          // warps may still read terms that its blocks would overwrite: they end first.  (64 rows over 16,384 keys
+          // take 1 % longer by it.  Looking at each block for slots that are six behind took 2,048 rows over 8,192
+          // keys from 138 us to 144.)
+          for (uint32_t x = 0; nt < kSlots && x < uint32_t(kSlots); ++x)
+            if ((open >> x & 1u) && !wait_free(x)) return false;
           for (int b = b0; b < NB; ++b) {
             const uint32_t use = qc + (b - (stay ? 0 : b0)), st = use & 1u;
             if (!all(mbar_wait(&bar_q[st], use >> 1 & 1u))) return false;
@@ -534,8 +545,8 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
             for (int u = 0; u < nt; ++u) {
               const uint32_t ks = (kc + u) % kSlots, slot = uint32_t((b - b0) % turns * nt + u);
               if (!all(mbar_wait(&bar_k[ks], (kc + u) / kSlots & 1u))) return false;
-              if ((used >> slot & 1u) && !all(mbar_wait(&bar_s_free[slot], (parity >> slot & 1u) ^ 1u))) return false;
-              used |= 1u << slot;
+              if ((open >> slot & 1u) && !wait_free(slot)) return false;
+              open |= 1u << slot;
               parity ^= 1u << slot;
               tc_fence_after();
               const uint64_t da = dK + uint32_t(ks * C::kTileBytes / 16), db = dQ + uint32_t(st * C::kTileBytes / 16);

@@ -133,6 +133,39 @@ def test_weights_of_long_sequences(kind):
     _weights([9000, 40], [3, 200], 4, 2, 128, "bf16", kind, decay=0.5)
 
 
+@pytest.mark.parametrize("kind,dtype", [("same", "bf16"), ("fp4", "bf16"), ("e4m3", "f16")])
+@pytest.mark.parametrize("keys,rows,chunks", [(896, 34, 1), (896, 34, 3), (640, 12, 3), (1100, 7, 2), (384, 17, 4)])
+def test_weights_of_uneven_groups_and_many_blocks(kind, dtype, keys, rows, chunks):
+    """One to three items for each SM, of seven key tiles (a group of four and one of three), five, nine or three, seen by
+    four to 17 blocks of rows: what a group's idle warps have not read yet is not overwritten."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    n, heads, dim = chunks * sms, 64, 64
+    c = Case([keys - rows] * n, [rows] * n, heads, 1, dim, dtype, kind)
+    c.call()
+    cc = c.cache
+    w = torch.full((n, 1, keys), 3.0, device="cuda")
+    call = lambda: c.pkv.pkv_attention_weights(w, None, 1.0, c.q_dev, c.lse, c.cu_dev, c.start_dev, cc.k_cache, cc.desc,  # noqa: E731
+                                               cc.dev_tables, c.scale)
+    call()
+    assert c.pkv.pkv_get_device_error() == 0
+    first = w.clone()
+    k = torch.from_numpy(cc.k).cuda()                          # float64
+    q = c.q_dev.double().view(n, rows, heads, dim)
+    lse = c.lse.double().view(n, rows, heads)
+    j = torch.arange(keys)
+    seen = j.cuda()[None] <= torch.arange(keys - rows, keys, device="cuda")[:, None]
+    for i in range(n):
+        blocks = torch.from_numpy(cc.tables[i]).long()[j // 16].cuda()
+        s = c.scale * torch.einsum("rhd,jd->rhj", q[i], k[blocks, 0, (j % 16).cuda()]) - lse[i][:, :, None]
+        ref = (s.exp() * seen[:, None]).sum((0, 1))
+        err = (first[i, 0].double() - ref).abs()
+        assert (err <= 2.0 ** -11 * ref + 2.0 ** -30).all(), (i, float((err / ref).max()))
+    for _ in range(10):
+        w.fill_(3.0)
+        call()
+        assert c.pkv.pkv_get_device_error() == 0 and torch.equal(first, w)
+
+
 def test_weights_of_many_sequences():
     rng = np.random.default_rng(6)
     _weights([int(x) for x in rng.integers(0, 300, 400)], [int(x) for x in rng.integers(0, 3, 400)], 3, 1, 64, "bf16", "fp4")
