@@ -397,7 +397,7 @@ PKV_API size_t pkv_chunk_workspace_bytes(int total_q, int num_heads, int num_kv_
  * max_blocks_per_seq * block_size up to 2^31 - 128, and
  * (total_q * (num_heads / num_kv_heads) / 64 + 3 num_chunks) * (max_blocks_per_seq * block_size / 128 + 2)
  * below 2^31.  Sums, maxima and outputs are fp32 until the last rounding; the softmax's exponentials are rounded to
- * the type of their product with V (q_dtype; fp16 over e4m3 and 4 bits: 2^-11 of each, and 2^-25 of a row's largest).
+ * the type of their product with V (q_dtype; fp16 over e4m3 and 4 bits).  As fp16: by 2^-11 of each, or 2^-32 of the row's largest.
  * Over e4m3 and 4 bits, bf16 q is taken as fp16 after a power of two for each row (bits below 2^-25 of the row's
  * largest are lost).  All of it must be memory of the current GPU.  Launch order as pkv_kv_write (waits before touching memory).
  */

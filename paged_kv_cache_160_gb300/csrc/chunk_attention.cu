@@ -37,6 +37,10 @@ namespace {
 constexpr int kThreads = 896;
 constexpr uint32_t kTmemCols = 512;           // S_A | S_B | O_A | O_B, 128 columns each
 constexpr float kRescaleThreshold = 8.f;      // log2 units
+// fp16 exponentials are taken relative to 2^-kHeadroom of the running maximum: up to 2^15, so that their least step, 2^-24,
+// is 2^-31 of a row's largest or less.  (Relative to the maximum itself small weights of many keys vanished: 2^17 keys of
+// e^-18 each.)  bf16 has the exponent of fp32 and needs none.
+constexpr float kHeadroom = 7.f;
 constexpr int kItems = 8;                     // items on their way from the scheduler to the other warps
 constexpr int kItemRows = 2 * kTile;
 constexpr int kFewRows = 32;                  // items of so few rows share each row's keys among four warps
@@ -174,6 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   using C = Cfg<KV, D>;
   constexpr bool kWide = KV == PKV_F16 || KV == PKV_BF16;    // 16-bit caches
   constexpr bool kMmaBF16 = KV == PKV_BF16;
+  constexpr float kBelow = kMmaBF16 ? 0.f : kHeadroom;
   constexpr int kStages = C::kStages;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ __align__(16) int items[kItems][12];
@@ -468,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = all(mbar_wait(&bar_peak[x], peaks & 1u));
           if (!ok) break;
           ++peaks;
-          const float mt = fmaxf(fmaxf(pk[0][lane], pk[1][lane]), fmaxf(pk[2][lane], pk[3][lane])) * slog;
+          const float mt = fmaxf(fmaxf(pk[0][lane], pk[1][lane]), fmaxf(pk[2][lane], pk[3][lane])) * slog - kBelow;
           const bool grow = mt > m + kRescaleThreshold;      // (the same in all four warps)
           const float m_prev = m;
           if (grow) m = mt;
@@ -537,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             mt = fmaxf(mt, fmaxf(fmaxf(c4[0], c4[1]), fmaxf(c4[2], c4[3])));
           }
-          mt *= slog;                                        // (slog > 0)
+          mt = mt * slog - kBelow;                           // (slog > 0)
           const bool grow = mt > m + kRescaleThreshold;      // also true for the first keys
           const float m_prev = m;
           if (grow) m = mt;

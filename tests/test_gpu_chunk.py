@@ -1,8 +1,8 @@
 """GPU parity of pkv_paged_chunk_attention against float64.
 
 With A = sum_j p_j |v_j|, u = finfo.eps / 2 of q's type and w that of the exponentials' type (q's; fp16 over a quantised
-cache): the exponentials are rounded to that type (w A; those below 2^-14 of it, fp16's least normal, by at most 2^-25
-each, 2^-25 N A over N keys for weights relative to a maximum that may trail by 2^8); scores are fp32 sums of at most
+cache): the exponentials are rounded to that type (w A; as fp16, those below its least normal, 2^-14, by at most 2^-25 where
+the row's largest is 2^7 or more: N 2^-32 max |v| over N keys, under 2^-15 for the N here and small beside w A); scores are fp32 sums of at most
 128 exact products, an error of the exponent below 2^-24 * 128 * scale * sum |q k| (under 2^-12 here), and bf16 rows that
 are taken as fp16 lose at most 2^-25 of their largest element; exp2 and the fp32 sums add less than 2^-13.  So
 |err| <= (w + 2^-11) A + u |out| + 2^-25, and |err| <= 2^-11 + 2^-22 |lse| for the log of the sum.
@@ -11,7 +11,7 @@ import numpy as np
 import pytest
 import torch
 
-from oracle import evict
+from oracle import evict, fp4
 from tests.paged import DT, Paged
 
 pytestmark = pytest.mark.gpu
@@ -234,6 +234,47 @@ def test_non_finite_values_reach_those_who_see_them(kind):
     bad = np.isinf if cc.kv in DT else np.isnan
     assert bad(got[4:, :, 48:64]).all()
     assert np.isfinite(got[4:, :, :48]).all() and np.isfinite(got[4:, :, 64:]).all()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("rows", [1, 40, 200])
+def test_many_small_weights_behind_a_large_one(kind, rows):
+    """One key has nearly all of the weight and a value of zero; 2^17 others have e^-18 of it each and values of one.
+
+    As many chunks as SMs over the same blocks, so that no SM sees a part of the keys alone.  An exponential below 2^-14 is
+    rounded to a multiple of 2^-24 as fp16, where that of the row's largest key is 2^7 or more: an error of at most 2^-32 of
+    that one each, N 2^-32 max |v| in all (2^-15 here)."""
+    n, dim, sms = 131072, 64, torch.cuda.get_device_properties(0).multi_processor_count
+    c = Case([n - rows], [rows], 1, 1, dim, "f16", kind, scaled=False)
+    cc = c.cache
+    k, v = np.zeros((cc.num_blocks, 1, 16, dim)), np.ones((cc.num_blocks, 1, 16, dim))
+    b = cc.tables[0, 0]
+    k[b, 0, 0, 0], v[b, 0, 0] = 6.0, 0.0
+    cc.scales = [None, None]
+    if kind == "fp4":
+        cc.stored = [fp4.pack(*fp4.quantise(x)) for x in (k, v)]
+    elif kind == "e4m3":
+        cc.scales = [np.ones(1, np.float32)] * 2
+        cc.stored = [torch.from_numpy(x).to(torch.float8_e4m3fn).view(torch.uint8).numpy() for x in (k, v)]
+    else:
+        cc.stored = [torch.from_numpy(x).to(torch.float16).view(torch.int16).numpy() for x in (k, v)]
+    cc.tables = np.repeat(cc.tables, sms, 0)
+    cc.upload()
+    c.q = torch.zeros((sms * rows, 1, dim), dtype=torch.float16)
+    c.q[:, :, 0] = 24.0
+    c.cu, c.starts, c.total = np.arange(sms + 1, dtype=np.int32) * rows, [n - rows] * sms, sms * rows
+    c.dev()
+    c.call()
+    assert c.pkv.pkv_get_device_error() == 0
+    others = np.arange(n - rows, n) * np.exp(-18.0)
+    one = cc.rows("v", 0, 2)[1, 0, 0]                          # (as stored: 1.03125 in 4 bits)
+    ref = one * (others / (1 + others))[:, None, None]
+    err = np.abs(c.out.double().cpu().numpy().reshape(sms, rows, 1, dim) - ref)
+    bound = 2.0 ** -10 * ref + 2.0 ** -11 * ref + one * n * 2.0 ** -32
+    worst = float((err / bound).max())
+    assert worst <= 1
+    e = np.abs(c.lse.double().cpu().numpy().reshape(sms, rows) - (18.0 + np.log1p(others)))
+    assert (e <= 2.0 ** -11).all()
 
 
 def test_inconsistent_lengths():
