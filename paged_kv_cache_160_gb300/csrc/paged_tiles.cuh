@@ -267,8 +267,13 @@ __device__ __forceinline__ bool load_queries(uint32_t base, const uint8_t* q, in
       }
       if (r < n) {
         if (sub == 0) {
-          const float c = kToF16 ? float(double(scale_log2) * fabs(double(head_scale)) * exp2_int(-shift)) : scale_log2;
-          put(r, c < 1e-35f ? 1e-35f : c, ex[u]);            // (0 * -inf would be NaN)
+          float c = scale_log2;
+          if constexpr (kToF16) {
+            // 0 * -inf would be NaN.  Products are below 2^35 here, so that with 1e-35 scores are as good as 0.
+            c = float(double(scale_log2) * fabs(double(head_scale)) * exp2_int(-shift));
+            c = c < 1e-35f ? 1e-35f : c;
+          }
+          put(r, c, ex[u]);
         }
 #pragma unroll
         for (int c = 0; c < kVec; ++c) {

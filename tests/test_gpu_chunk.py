@@ -169,6 +169,22 @@ def test_bf16_queries_of_any_size(kind, size):
     c.check()
 
 
+@pytest.mark.parametrize("size", [1, 60])
+def test_scales_far_from_one(size):
+    """Scales of 2^123 and 2^-123 between queries and keys of 2^-60 and 2^60 in bf16: the scores are ordinary ones."""
+    for e in (size, -size):
+        c = Case([200, 3], [6, 40], 2, 1, 128, "bf16", "same")
+        k = torch.from_numpy(c.cache.stored[0]).view(torch.bfloat16)
+        c.cache.stored[0] = (k.float() * 2.0 ** e).to(torch.bfloat16).view(torch.int16).numpy()
+        c.cache.upload()
+        c.q = (c.q.float() * 2.0 ** e).to(torch.bfloat16)
+        c.scale = 128 ** -0.5 * 2.0 ** (-2 * e)
+        c.dev()
+        c.call()
+        assert c.pkv.pkv_get_device_error() == 0
+        c.check()
+
+
 @pytest.mark.parametrize("kind", ["fp4", "e4m3"])
 def test_head_scales_of_any_sign(kind):
     c = Case([150], [9], 8, 4, 64, "f16", kind)
