@@ -393,7 +393,7 @@ PKV_API size_t pkv_chunk_workspace_bytes(int total_q, int num_heads, int num_kv_
  * ascending from 0 or past total_q, q_start_pos < 0, or positions past its table) sets PKV_DEVERR_CHUNK and its
  * rows stay unwritten.  A block id outside the pool sets PKV_DEVERR_BLOCK_ID; its keys and values count as zeros.
  * Supported: f16, bf16, e4m3 and 4-bit caches, head_dim 64 or 128, block_size 16 or 32, any number of query heads
- * per kv head, scale > 0 and finite, num_chunks up to 65535, total_q * num_heads below 2^31 - 512,
+ * per kv head, scale > 0 and up to 2^127, num_chunks up to 65535, total_q * num_heads below 2^31 - 512,
  * max_blocks_per_seq * block_size up to 2^31 - 128, and
  * (total_q * (num_heads / num_kv_heads) / 64 + 3 num_chunks) * (max_blocks_per_seq * block_size / 128 + 2)
  * below 2^31.  Sums, maxima and outputs are fp32 until the last rounding; the softmax's exponentials are rounded to

@@ -630,7 +630,7 @@ extern "C" pkv_status pkv_attention_weights(float* out, const float* weights, fl
       num_heads % cache->num_kv_heads)
     return PKV_ERR_INVALID_ARG;
   if (q_dtype != PKV_F16 && q_dtype != PKV_BF16) return PKV_ERR_INVALID_ARG;
-  if (!(scale > 0.f) || scale > 3.4e38f || !(decay >= 0.f) || decay > 3.4e38f) return PKV_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || scale > kMostScale || !(decay >= 0.f) || decay > 3.4e38f) return PKV_ERR_INVALID_ARG;
   if ((cache->kv_dtype == PKV_F16 || cache->kv_dtype == PKV_BF16) && cache->kv_dtype != q_dtype)
     return PKV_ERR_UNSUPPORTED;
   if (cache->head_dim != 64 && cache->head_dim != 128) return PKV_ERR_UNSUPPORTED;

@@ -1022,7 +1022,7 @@ extern "C" pkv_status pkv_paged_chunk_attention(void* out, float* lse, const voi
   if (num_chunks < 0 || total_q < 0 || num_heads <= 0 || max_blocks_per_seq < 0 || num_heads % cache->num_kv_heads)
     return PKV_ERR_INVALID_ARG;
   if (q_dtype != PKV_F16 && q_dtype != PKV_BF16) return PKV_ERR_INVALID_ARG;
-  if (!(scale > 0.f) || scale > 3.4e38f) return PKV_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || scale > kMostScale) return PKV_ERR_INVALID_ARG;
   if ((cache->kv_dtype == PKV_F16 || cache->kv_dtype == PKV_BF16) && cache->kv_dtype != q_dtype)
     return PKV_ERR_UNSUPPORTED;
   if (cache->head_dim != 64 && cache->head_dim != 128) return PKV_ERR_UNSUPPORTED;

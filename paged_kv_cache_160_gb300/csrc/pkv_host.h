@@ -45,6 +45,9 @@ inline int64_t cache_block_bytes(const pkv_cache_desc* c) {
   return c->kv_dtype == PKV_FP4_E2M1 ? elems / 16 * 9 : elems * dtype_bytes(c->kv_dtype);
 }
 
+// The largest scale of chunks (pkv_paged_chunk_attention): times log2(e) it is still finite.
+constexpr float kMostScale = 0x1p127f;
+
 // Whether the row blocks and key tiles of chunks (pkv_paged_chunk_attention) can be numbered in 32 bits.
 inline bool chunk_work_fits(int num_chunks, int total_q, int num_heads, int max_blocks, const pkv_cache_desc* c) {
   const int64_t most = int64_t(1) << 31, keys = int64_t(max_blocks) * c->block_size;

@@ -53,6 +53,14 @@ def test_refusals_of_chunk_calls(call):
     assert call(n=0) == OK and call(total=0) == OK
 
 
+@pytest.mark.parametrize("call", [_chunk, _weights])
+def test_scales_whose_product_with_log2_e_has_no_fp32(call):
+    """scale * 1.4427 has to stay finite: a score of zero times infinity would be NaN."""
+    other = dict(desc=_desc(dim=96))                           # looked at later
+    assert call(scale=2.5e38, **other) == INVALID and call(scale=2.0 ** 127 * 1.01, **other) == INVALID
+    assert call(scale=2.0 ** 127, **other) == UNSUPPORTED and call(scale=1e-40, **other) == UNSUPPORTED
+
+
 def test_refusals_of_the_chunk_attention():
     for bad in (dict(out=8), dict(v=0), dict(v=8)):
         assert _chunk(**bad) == INVALID, bad
