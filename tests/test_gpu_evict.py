@@ -576,6 +576,54 @@ def test_select_and_compact_in_a_graph():
     assert captured[0].data_ptr() != c.k_cache.data_ptr()
 
 
+@pytest.mark.parametrize("kv", ["fp4", "e4m3", "bf16"])
+@pytest.mark.parametrize("fresh", [False, True])
+def test_a_captured_compaction_moves_the_rows(kv, fresh):
+    """Select and compact in a graph, replayed over other rows, weights and lengths: K, V and weights against the oracle."""
+    import paged_kv_cache_160_gb300 as pkv
+    i32 = dict(dtype=torch.int32, device="cuda")
+    c = Paged([3000, 500], kv, 2, 64, max_blocks=200, extra=70)
+    dst = c.tables.copy()
+    if fresh:                                                  # blocks of their own for the first sequence
+        unused = [b for b in range(c.num_blocks) if b not in set(c.tables.flatten().tolist())]
+        dst[0, :60] = unused[:60]
+    dst_dev = torch.from_numpy(dst).cuda()
+    w = torch.rand((2, 2, 3200)).cuda()
+    kept = torch.zeros((2, 2, 900), **i32)
+    lens, keep = torch.tensor([3000, 500], **i32), torch.tensor([900, 100], **i32)
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side), torch.cuda.graph(graph, stream=side):
+        pkv.pkv_evict_select(kept, w, lens, keep, 3, 10)
+        pkv.pkv_evict_compact(c.k_cache, c.v_cache, c.desc, kept, keep, c.dev_tables, dst_dev, w)
+    torch.cuda.synchronize()
+    rng = np.random.default_rng(8)
+    for n, m in (([3000, 500], [900, 100]), ([2900, 480], [77, 300]), ([31, 1], [0, 1]), ([3000, 500], [900, 499])):
+        stored = [rng.permutation(s, axis=0) for s in c.stored]
+        for pool, s in zip((c.k_cache, c.v_cache), stored):
+            pool.view(torch.int16 if kv in DT else torch.uint8).copy_(torch.from_numpy(s))
+        before = rng.random((2, 2, 3200)).astype(np.float32)
+        w.copy_(torch.from_numpy(before))
+        lens.copy_(torch.tensor(n))
+        keep.copy_(torch.tensor(m))
+        kept.fill_(77)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            graph.replay()
+        torch.cuda.synchronize()
+        assert pkv.pkv_get_device_error() == 0
+        list_, after = kept.cpu().numpy(), before.copy()
+        for i in range(2):
+            for h in range(2):
+                ref = evict.select(before[i, h], n[i], m[i], 3, 10)
+                assert list_[i, h].tolist() == ref + [-1] * (900 - len(ref))
+                after[i, h, :m[i]] = before[i, h, ref]
+        assert np.array_equal(w.cpu().numpy(), after)
+        for pool, s in zip((c.k_cache, c.v_cache), stored):
+            got = pool.view(torch.int16 if kv in DT else torch.uint8).cpu().numpy()
+            assert np.array_equal(_rows_of(c, got), evict.compact(_rows_of(c, s), list_, m, c.tables, dst, 16))
+
+
 # ---------------------------------------------------------------------------------------
 # the calls in a row
 # ---------------------------------------------------------------------------------------
