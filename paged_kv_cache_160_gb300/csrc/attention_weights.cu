@@ -18,8 +18,9 @@
 // 0.55 of the measured copy); many rows, the chain of a slot, products - exponentials - products (2,048
 // rows over 8,192 keys, 32 heads over 8, f16: 138 us; the products alone take 62, the exponentials 51),
 // where SMs with four key tiles work on for a fifth longer than the mean, and shared memory: the products
-// read 8 KB each, and two terms a row beside them instead of one cost 29 us.  64 rows over up to 16,384
-// keys of 4 bits: 48 us.  Not faster: the slots in halves of 64 rows (206 us where whole ones took 166:
+// read 8 KB each, and two terms a row beside them instead of one cost 29 us.  Over e4m3 and 4 bits 152 and
+// 144 us with f16 queries, 260 and 252 with bf16 ones, which the loader warps turn into fp16 and which have
+// two terms a row.  64 rows over up to 16,384 keys of 4 bits: 48 us (f16 queries: 38).  Not faster: the slots in halves of 64 rows (206 us where whole ones took 166:
 // products of 64 columns read the keys as often).
 #include <algorithm>
 
@@ -36,7 +37,10 @@ constexpr int kItems = 8;                     // items on their way from the sch
 constexpr int kMaxChunks = 65535;
 constexpr int kSeqChunk = 32;                 // chunks per entry of the table of work
 constexpr int kReaders = 16 + 8 + 1 + 1;      // warps that read the items: exponentials, loaders, MMA, key tiles by TMA
-constexpr int kTileCost = 2;                  // of a key tile beside its blocks: its load takes as long as about two of them
+// Of a key tile beside its blocks: its load takes as long as about two of them.  (With 0, 1, 2, 3 and 4: 20.4, 20.5, 20.3,
+// 20.3 and 20.3 us for one row over 64 sequences, 48.6, 48.6, 48.1, 48.1 and 48.1 for 64 rows over four, 138.7, 138.7, 138.7,
+// 136.7 and 136.7 for 2,048 rows over one, whose cuts fall on whole tiles.)
+constexpr int kTileCost = 2;
 
 struct WeightsParams {
   float* out;

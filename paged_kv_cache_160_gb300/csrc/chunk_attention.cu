@@ -17,15 +17,18 @@
 //
 // Bound: the chain of a tile, scores - softmax - products, of which two are under way.  A step takes 2,100
 // to 2,300 cycles, its products 1,170: the issuer looks at four barriers a step at 200 cycles each, and the
-// softmax of a block takes 1,800.  Measured alone: 8 sequences of 32K to 128K tokens, 8 rows each, 32 heads
-// over 8, D 128, 4 bits: 305 us (the bytes take 101); four chunks of 700 to 1,024 rows behind 5K to 9K
-// keys, 32 heads over 8: 459 us over e4m3, 428 over 4 bits, 366 over bf16 (0.61 of the measured bf16 rate);
-// 512 rows behind 3,584, 28 heads over 4, 4 bits: 64 us; 64 sequences of up to 2,048 tokens, 4 rows each:
-// 49 us; 4 of up to 37: 12 us.
+// softmax of a block takes 1,800.  Measured: 8 sequences of 32K to 128K tokens, 8 rows each, 32 heads
+// over 8, D 128, 4 bits: 303 us (the bytes take 101), bf16 360 (360); four chunks of 700 to 1,024 rows
+// behind 5K to 9K keys, 32 heads over 8: 457 us over e4m3, 428 over 4 bits, 382 over bf16 (0.58 of the
+// measured bf16 rate); 512 rows behind 3,584, 28 heads over 4, 4 bits: 63 us; 64 sequences of up to 2,048
+// tokens, 4 rows each: 49 us; 4 of up to 37: 12 us.  (Rows read back from a quantised cache and attended as
+// plain ones take 356 us in place of 457 and 37 in place of 63, but 82 in place of 49 and 1,091 in place of
+// 303: this kernel is for few rows of many or long sequences, and where there is no room for the rows.)
 //   Not faster: two softmax threads a row with half the loader warps (578 us over e4m3), an issuer for each
-// chain (489), 64 scores per load from tensor memory, asking L2 for tiles a window ahead.  One code path
-// for all loader warps and loops that stay rolled are what made it four times faster than the first form:
-// unrolled, the warps' instructions came more slowly than they ran.
+// chain (489), 64 scores per load from tensor memory, asking L2 for tiles a window ahead.  What made the
+// first form three times faster, on the 8 long sequences: no loads in flight spilled (959 us -> 491), rolled
+// loops in every role (391; unrolled, the warps' instructions came more slowly than they ran), 16 loader
+// warps of one tile each in place of 8 (315), loads without branches (300).
 #include <algorithm>
 
 #include "paged_tiles.cuh"
@@ -43,7 +46,11 @@ constexpr float kRescaleThreshold = 8.f;      // log2 units
 constexpr float kHeadroom = 7.f;
 constexpr int kItems = 8;                     // items on their way from the scheduler to the other warps
 constexpr int kItemRows = 2 * kTile;
-constexpr int kFewRows = 32;                  // items of so few rows share each row's keys among four warps
+// Items of so few rows (a warp's) share each row's keys among four warps: 64 sequences of up to 2,048 tokens, 7 or 28 rows
+// a kv head, over 4 bits 43.2 and 48.6 us (a warp for all keys: 45.6 and 50.1), bf16 38.0 and 41.9 (39.7 and 43.9), 256
+// sequences of 500 to 1,500 over 4 bits 209 (221).  In long walks the four warps' meeting at each tile costs more than it
+// gives: 8 of 32K to 128K tokens, 32 rows, over 4 bits 303 us (291), over e4m3 484 (463), over bf16 359 (359).
+constexpr int kFewRows = 32;
 constexpr int kMaxChunks = 65535;
 constexpr int kSeqChunk = 32;                 // chunks per entry of the table of work
 constexpr int kReaders = 8 + 16 + 1 + 2;      // warps that read the items: softmax, loaders, MMA, queries
@@ -698,202 +705,202 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!ok && lane == 0) set_error(p.pc.err, PKV_DEVERR_TIMEOUT);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-  if (warp == 24) {
-    // ---------------- this CTA's range of the work, item by item ----------------
-    const int64_t total = int64_t(hkv) * first_unit[tables];
-    const int64_t lo = total * blockIdx.x / gridDim.x, hi = total * (blockIdx.x + 1) / gridDim.x;
-    Part parts[2] = {};
-    uint32_t i = 0;
-    auto put = [&](const Item& it) {
-      ok = ok && (i < uint32_t(kItems) || all(mbar_wait(&bar_item_read[i % kItems], (i / kItems - 1) & 1u)));
-      if (!ok) return;
-      if (lane == 0) {
-        int4* w = reinterpret_cast<int4*>(items[i % kItems]);
-        w[0] = make_int4(it.seq, it.h, it.q0, it.start);
-        w[1] = make_int4(it.f0, it.rows, it.t0, it.t1);
-        w[2] = make_int4(it.end, it.masked, it.slot, 0);
-        mbar_arrive(&bar_item[i % kItems]);
-      }
-      __syncwarp();
-      ++i;
-    };
-    if (lo < hi) {
-      int a = 0, b = tables;                                 // hkv first_unit[a] <= lo < hkv first_unit[a + 1]
-      while (b - a > 1) {
-        const int mid = (a + b) >> 1;
-        if (int64_t(hkv) * first_unit[mid] <= lo) a = mid; else b = mid;
-      }
-      const int s0 = a * kSeqChunk + lane;
-      int mine = s0 < p.num_chunks ? units_of(p, Chunk(p, s0)) : 0, sum = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o) sum += v;
-      }
-      const int64_t in_table = lo - int64_t(hkv) * first_unit[a];
-      const unsigned past = __ballot_sync(0xffffffffu, int64_t(hkv) * sum > in_table);
-      const int l = past ? __ffs(past) - 1 : 31;
-      const int64_t before = int64_t(hkv) * __shfl_sync(0xffffffffu, sum - mine, l);
-      const int units = max(1, __shfl_sync(0xffffffffu, mine, l));
-      int seq = a * kSeqChunk + l;
-      int h = int((in_table - before) / units);
-      int64_t pos = lo - (in_table - before) % units;        // of the current item's first unit
-      Chunk ch(p, min(seq, p.num_chunks - 1));
-      int f0 = 0;
-      while (past && seq < p.num_chunks && pos < hi && ok) {
-        const int F = ch.len * G;
-        if (h >= hkv || F == 0) {                            // the next chunk
-          h = 0;
-          f0 = 0;
-          if (++seq < p.num_chunks) ch = Chunk(p, seq);
-          continue;
+    if (warp == 24) {
+      // ---------------- this CTA's range of the work, item by item ----------------
+      const int64_t total = int64_t(hkv) * first_unit[tables];
+      const int64_t lo = total * blockIdx.x / gridDim.x, hi = total * (blockIdx.x + 1) / gridDim.x;
+      Part parts[2] = {};
+      uint32_t i = 0;
+      auto put = [&](const Item& it) {
+        ok = ok && (i < uint32_t(kItems) || all(mbar_wait(&bar_item_read[i % kItems], (i / kItems - 1) & 1u)));
+        if (!ok) return;
+        if (lane == 0) {
+          int4* w = reinterpret_cast<int4*>(items[i % kItems]);
+          w[0] = make_int4(it.seq, it.h, it.q0, it.start);
+          w[1] = make_int4(it.f0, it.rows, it.t0, it.t1);
+          w[2] = make_int4(it.end, it.masked, it.slot, 0);
+          mbar_arrive(&bar_item[i % kItems]);
         }
-        if (f0 >= F) {
-          f0 = 0;
-          ++h;
-          continue;
+        __syncwarp();
+        ++i;
+      };
+      if (lo < hi) {
+        int a = 0, b = tables;                                 // hkv first_unit[a] <= lo < hkv first_unit[a + 1]
+        while (b - a > 1) {
+          const int mid = (a + b) >> 1;
+          if (int64_t(hkv) * first_unit[mid] <= lo) a = mid; else b = mid;
         }
-        Item it;
-        it.seq = seq;
-        it.h = h;
-        it.q0 = ch.q0;
-        it.start = ch.start;
-        it.f0 = f0;
-        it.rows = min(kItemRows, F - f0);
-        it.end = item_end(p.group, ch.start, f0, it.rows);
-        it.masked = (ch.start + int(p.group.quotient(f0)) + 1) / kTile;
-        const int tiles = tiles_of(it.end), cost = it.two() ? 2 : 1;
-        const int64_t next = pos + int64_t(tiles) * cost;
-        if (next > lo) {
-          it.t0 = lo > pos ? int((lo - pos + cost - 1) / cost) : 0;
-          it.t1 = hi < next ? int((hi - pos + cost - 1) / cost) : tiles;
-          if (it.t1 > it.t0) {
-            const int which = pos > lo;
-            it.slot = it.t0 == 0 && it.t1 == tiles ? -1 : int(2 * blockIdx.x + which);
-            if (it.slot >= 0) parts[which] = Part{seq, h, f0, it.rows, it.t0, it.t1, tiles, ch.q0};
-            put(it);
+        const int s0 = a * kSeqChunk + lane;
+        int mine = s0 < p.num_chunks ? units_of(p, Chunk(p, s0)) : 0, sum = mine;
+  #pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, sum, o);
+          if (lane >= o) sum += v;
+        }
+        const int64_t in_table = lo - int64_t(hkv) * first_unit[a];
+        const unsigned past = __ballot_sync(0xffffffffu, int64_t(hkv) * sum > in_table);
+        const int l = past ? __ffs(past) - 1 : 31;
+        const int64_t before = int64_t(hkv) * __shfl_sync(0xffffffffu, sum - mine, l);
+        const int units = max(1, __shfl_sync(0xffffffffu, mine, l));
+        int seq = a * kSeqChunk + l;
+        int h = int((in_table - before) / units);
+        int64_t pos = lo - (in_table - before) % units;        // of the current item's first unit
+        Chunk ch(p, min(seq, p.num_chunks - 1));
+        int f0 = 0;
+        while (past && seq < p.num_chunks && pos < hi && ok) {
+          const int F = ch.len * G;
+          if (h >= hkv || F == 0) {                            // the next chunk
+            h = 0;
+            f0 = 0;
+            if (++seq < p.num_chunks) ch = Chunk(p, seq);
+            continue;
           }
+          if (f0 >= F) {
+            f0 = 0;
+            ++h;
+            continue;
+          }
+          Item it;
+          it.seq = seq;
+          it.h = h;
+          it.q0 = ch.q0;
+          it.start = ch.start;
+          it.f0 = f0;
+          it.rows = min(kItemRows, F - f0);
+          it.end = item_end(p.group, ch.start, f0, it.rows);
+          it.masked = (ch.start + int(p.group.quotient(f0)) + 1) / kTile;
+          const int tiles = tiles_of(it.end), cost = it.two() ? 2 : 1;
+          const int64_t next = pos + int64_t(tiles) * cost;
+          if (next > lo) {
+            it.t0 = lo > pos ? int((lo - pos + cost - 1) / cost) : 0;
+            it.t1 = hi < next ? int((hi - pos + cost - 1) / cost) : tiles;
+            if (it.t1 > it.t0) {
+              const int which = pos > lo;
+              it.slot = it.t0 == 0 && it.t1 == tiles ? -1 : int(2 * blockIdx.x + which);
+              if (it.slot >= 0) parts[which] = Part{seq, h, f0, it.rows, it.t0, it.t1, tiles, ch.q0};
+              put(it);
+            }
+          }
+          pos = next;
+          f0 += kItemRows;
         }
-        pos = next;
-        f0 += kItemRows;
       }
-    }
-    if (lane < 2) reinterpret_cast<Part*>(p.parts)[2 * blockIdx.x + lane] = lane ? parts[1] : parts[0];
-    put(Item{});
-    if (!ok && lane == 0) set_error(p.pc.err, PKV_DEVERR_TIMEOUT);
-  } else if (warp == 25) {
-    // ---------------- MMA issuer (the whole warp; see mma_ss) ----------------
-    const uint32_t lead = elect_one();
-    constexpr uint32_t idesc_s = umma_idesc_f16(kMmaBF16, 128, 128, false, false);
-    constexpr uint32_t idesc_o = umma_idesc_f16(kMmaBF16, 128, D, false, true);
-    const uint64_t dQ = umma_sdesc_sw128(smem_u32(sQ), 16, 1024), dK = umma_sdesc_sw128(smem_u32(sK), 16, 1024);
-    const uint64_t dV = umma_sdesc_sw128(smem_u32(sV), kHalfBytes, 1024), dP = umma_sdesc_sw128(smem_u32(sP), 16, 1024);
-    uint32_t kt = 0, turn = 0, done = 0;                     // tiles; items of one block; items
-    Pair uses, p_of;                                         // of the query areas; steps of A and B
-    for (;; ++done) {
-      ok = ok && wait_item(done);
-      if (!ok) break;
-      const Item it = read_item(done);
-      done_reading(done);
-      if (it.rows == 0) break;
-      const bool two = it.two(), few = it.few();
-      const int N = it.steps();
-      const int area = int(turn & 1u);                       // of an item of one block
-      // S_x(n) = Q K^T into TMEM columns 128x .. 128x + 127.  A descriptor advances by bytes / 16.
-      auto issue_s = [&](int n) -> bool {
-        const int x = n & 1, a = two ? x : area;
-        const uint32_t tile = kt + (two ? n >> 1 : n), st = tile % kStages;
-        if ((two ? n < 2 : n == 0) && !all(mbar_wait(&bar_q[a], uses[a] & 1u))) return false;
-        if (!all(mbar_wait(&bar_k_full[st], (tile / kStages) & 1u))) return false;
-        tc_fence_after();
-        const uint64_t da = dQ + uint32_t(a * C::kTileBytes / 16), db = dK + uint32_t(st * C::kTileBytes / 16);
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          mma_ss(lead, tmem + 128 * x, da + ((kk >> 2) * kHalfBytes + (kk & 3) * 32) / 16,
-                 db + ((kk >> 2) * kHalfBytes + (kk & 3) * 32) / 16, idesc_s, kk > 0);
-        commit(lead, &bar_s_full[x]);
-        if (!two || x == 1) commit(lead, &bar_k_empty[st]);
-        if (two ? n + 2 >= N : n + 1 == N) commit(lead, &bar_q_empty[a]);
-        return true;
-      };
-      // O_x += P_x V, P_x in the first 64 columns of the scores, or of few rows in shared memory.
-      auto issue_pv = [&](int n) -> bool {
-        const int x = n & 1;
-        const uint32_t tile = kt + (two ? n >> 1 : n), st = tile % kStages;
-        if (!all(mbar_wait(&bar_v_seen[st], (tile / kStages) & 1u))) return false;
-        if (n == 0 && done > 0 && !all(mbar_wait(&bar_o_free, (done - 1) & 1u))) return false;
-        if (!all(mbar_wait(&bar_p_full[x], p_of[x] & 1u))) return false;
-        p_of.up(x);
-        tc_fence_after();
-        const uint64_t b = dV + uint32_t(st * C::kTileBytes / 16);
-        if (few) {
-          const uint64_t a = dP + uint32_t(x * C::kWeights / 16);
-#pragma unroll
-          for (int kk = 0; kk < kTile / 16; ++kk)
-            mma_ss(lead, tmem + 256 + 128 * x, a + ((kk >> 2) * C::kWeightHalf + (kk & 3) * 32) / 16, b + kk * 2048 / 16, idesc_o,
-                   n >= 2 || kk > 0);
-        } else {
-#pragma unroll
-          for (int kk = 0; kk < kTile / 16; ++kk)
-            mma_ts(lead, tmem + 256 + 128 * x, tmem + 128 * x + kk * 8, b + kk * 2048 / 16, idesc_o, n >= 2 || kk > 0);
-        }
-        commit(lead, &bar_pv_done[x]);
-        if (!two || x == 1) commit(lead, &bar_v_empty[st]);
-        return true;
-      };
-      ok = issue_s(0) && (N < 2 || issue_s(1));
-      for (int n = 0; ok && n < N; ++n) ok = issue_pv(n) && (n + 2 >= N || issue_s(n + 2));
-      if (!ok) break;
-      kt += it.t1 - it.t0;
-      if (two) {
-        uses.up(0);
-        uses.up(1);
-      } else {
-        uses.up(area);
-        ++turn;
-      }
-    }
-    if (!ok && lane == 0) set_error(p.pc.err, PKV_DEVERR_TIMEOUT);
-    commit(lead, &bar_drain);                                // no product may be under way when the CTA leaves
-    (void)mbar_wait(&bar_drain, 0);
-  } else {
-    // ---------------- queries of items of one block ----------------
-    const int tid = threadIdx.x - 26 * 32;
-    uint32_t turn = 0;
-    Pair uses;
-    for (uint32_t i = 0;; ++i) {
-      ok = ok && wait_item(i);
-      if (!ok) break;
-      const Item it = read_item(i);
-      done_reading(i);
-      if (it.rows == 0) break;
-      if (it.two()) {
-        // Not ours to fill, but to wait for: a later wait could take an earlier phase that was
-        // skipped for its own.  The arrival keeps the areas' next phases from passing before that.
-        for (int a = 0; a < 2 && ok; ++a) {
-          ok = all(uses[a] == 0 || mbar_wait(&bar_q_empty[a], (uses[a] - 1) & 1u));
-          uses.up(a);
-          if (ok && lane == 0) mbar_arrive(&bar_q[a]);
-        }
+      if (lane < 2) reinterpret_cast<Part*>(p.parts)[2 * blockIdx.x + lane] = lane ? parts[1] : parts[0];
+      put(Item{});
+      if (!ok && lane == 0) set_error(p.pc.err, PKV_DEVERR_TIMEOUT);
+    } else if (warp == 25) {
+      // ---------------- MMA issuer (the whole warp; see mma_ss) ----------------
+      const uint32_t lead = elect_one();
+      constexpr uint32_t idesc_s = umma_idesc_f16(kMmaBF16, 128, 128, false, false);
+      constexpr uint32_t idesc_o = umma_idesc_f16(kMmaBF16, 128, D, false, true);
+      const uint64_t dQ = umma_sdesc_sw128(smem_u32(sQ), 16, 1024), dK = umma_sdesc_sw128(smem_u32(sK), 16, 1024);
+      const uint64_t dV = umma_sdesc_sw128(smem_u32(sV), kHalfBytes, 1024), dP = umma_sdesc_sw128(smem_u32(sP), 16, 1024);
+      uint32_t kt = 0, turn = 0, done = 0;                     // tiles; items of one block; items
+      Pair uses, p_of;                                         // of the query areas; steps of A and B
+      for (;; ++done) {
+        ok = ok && wait_item(done);
         if (!ok) break;
-        continue;
+        const Item it = read_item(done);
+        done_reading(done);
+        if (it.rows == 0) break;
+        const bool two = it.two(), few = it.few();
+        const int N = it.steps();
+        const int area = int(turn & 1u);                       // of an item of one block
+        // S_x(n) = Q K^T into TMEM columns 128x .. 128x + 127.  A descriptor advances by bytes / 16.
+        auto issue_s = [&](int n) -> bool {
+          const int x = n & 1, a = two ? x : area;
+          const uint32_t tile = kt + (two ? n >> 1 : n), st = tile % kStages;
+          if ((two ? n < 2 : n == 0) && !all(mbar_wait(&bar_q[a], uses[a] & 1u))) return false;
+          if (!all(mbar_wait(&bar_k_full[st], (tile / kStages) & 1u))) return false;
+          tc_fence_after();
+          const uint64_t da = dQ + uint32_t(a * C::kTileBytes / 16), db = dK + uint32_t(st * C::kTileBytes / 16);
+  #pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_ss(lead, tmem + 128 * x, da + ((kk >> 2) * kHalfBytes + (kk & 3) * 32) / 16,
+                   db + ((kk >> 2) * kHalfBytes + (kk & 3) * 32) / 16, idesc_s, kk > 0);
+          commit(lead, &bar_s_full[x]);
+          if (!two || x == 1) commit(lead, &bar_k_empty[st]);
+          if (two ? n + 2 >= N : n + 1 == N) commit(lead, &bar_q_empty[a]);
+          return true;
+        };
+        // O_x += P_x V, P_x in the first 64 columns of the scores, or of few rows in shared memory.
+        auto issue_pv = [&](int n) -> bool {
+          const int x = n & 1;
+          const uint32_t tile = kt + (two ? n >> 1 : n), st = tile % kStages;
+          if (!all(mbar_wait(&bar_v_seen[st], (tile / kStages) & 1u))) return false;
+          if (n == 0 && done > 0 && !all(mbar_wait(&bar_o_free, (done - 1) & 1u))) return false;
+          if (!all(mbar_wait(&bar_p_full[x], p_of[x] & 1u))) return false;
+          p_of.up(x);
+          tc_fence_after();
+          const uint64_t b = dV + uint32_t(st * C::kTileBytes / 16);
+          if (few) {
+            const uint64_t a = dP + uint32_t(x * C::kWeights / 16);
+  #pragma unroll
+            for (int kk = 0; kk < kTile / 16; ++kk)
+              mma_ss(lead, tmem + 256 + 128 * x, a + ((kk >> 2) * C::kWeightHalf + (kk & 3) * 32) / 16, b + kk * 2048 / 16, idesc_o,
+                     n >= 2 || kk > 0);
+          } else {
+  #pragma unroll
+            for (int kk = 0; kk < kTile / 16; ++kk)
+              mma_ts(lead, tmem + 256 + 128 * x, tmem + 128 * x + kk * 8, b + kk * 2048 / 16, idesc_o, n >= 2 || kk > 0);
+          }
+          commit(lead, &bar_pv_done[x]);
+          if (!two || x == 1) commit(lead, &bar_v_empty[st]);
+          return true;
+        };
+        ok = issue_s(0) && (N < 2 || issue_s(1));
+        for (int n = 0; ok && n < N; ++n) ok = issue_pv(n) && (n + 2 >= N || issue_s(n + 2));
+        if (!ok) break;
+        kt += it.t1 - it.t0;
+        if (two) {
+          uses.up(0);
+          uses.up(1);
+        } else {
+          uses.up(area);
+          ++turn;
+        }
       }
-      const int a = int(turn++ & 1u);
-      float* fac = factor[a][uses[a] & 1u];
-      ok = load_queries<kBF16, !kWide, D, 64, 4>(smem_u32(sQ) + a * C::kTileBytes, p.q, it.q0, p.num_heads, it.h, p.group, it.f0, it.rows,
-                                         it.few() ? kTile / kFewRows : 1, p.scale_log2, !kWide && p.k_scale ? __ldg(p.k_scale + it.h) : 1.f, tid,
-                                         [&] { return all(uses[a] == 0 || mbar_wait(&bar_q_empty[a], (uses[a] - 1) & 1u)); },
-                                         [](int) { return 0.f; }, [&](int row, float c, float) { fac[row] = c; });
-      if (!ok) break;
-      uses.up(a);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {                                       // (for the chain's warps too)
-        for (int u = 0; u < 3; ++u) mbar_arrive(&bar_q[a]);
+      if (!ok && lane == 0) set_error(p.pc.err, PKV_DEVERR_TIMEOUT);
+      commit(lead, &bar_drain);                                // no product may be under way when the CTA leaves
+      (void)mbar_wait(&bar_drain, 0);
+    } else {
+      // ---------------- queries of items of one block ----------------
+      const int tid = threadIdx.x - 26 * 32;
+      uint32_t turn = 0;
+      Pair uses;
+      for (uint32_t i = 0;; ++i) {
+        ok = ok && wait_item(i);
+        if (!ok) break;
+        const Item it = read_item(i);
+        done_reading(i);
+        if (it.rows == 0) break;
+        if (it.two()) {
+          // Not ours to fill, but to wait for: a later wait could take an earlier phase that was
+          // skipped for its own.  The arrival keeps the areas' next phases from passing before that.
+          for (int a = 0; a < 2 && ok; ++a) {
+            ok = all(uses[a] == 0 || mbar_wait(&bar_q_empty[a], (uses[a] - 1) & 1u));
+            uses.up(a);
+            if (ok && lane == 0) mbar_arrive(&bar_q[a]);
+          }
+          if (!ok) break;
+          continue;
+        }
+        const int a = int(turn++ & 1u);
+        float* fac = factor[a][uses[a] & 1u];
+        ok = load_queries<kBF16, !kWide, D, 64, 4>(smem_u32(sQ) + a * C::kTileBytes, p.q, it.q0, p.num_heads, it.h, p.group, it.f0, it.rows,
+                                           it.few() ? kTile / kFewRows : 1, p.scale_log2, !kWide && p.k_scale ? __ldg(p.k_scale + it.h) : 1.f, tid,
+                                           [&] { return all(uses[a] == 0 || mbar_wait(&bar_q_empty[a], (uses[a] - 1) & 1u)); },
+                                           [](int) { return 0.f; }, [&](int row, float c, float) { fac[row] = c; });
+        if (!ok) break;
+        uses.up(a);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {                                       // (for the chain's warps too)
+          for (int u = 0; u < 3; ++u) mbar_arrive(&bar_q[a]);
+        }
       }
+      if (!ok && lane == 0) set_error(p.pc.err, PKV_DEVERR_TIMEOUT);
     }
-    if (!ok && lane == 0) set_error(p.pc.err, PKV_DEVERR_TIMEOUT);
-  }
   }
   tc_fence_before();
   __syncthreads();

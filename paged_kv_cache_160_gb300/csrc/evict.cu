@@ -61,8 +61,9 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 //   kStored: the ranks stay in shared memory, one pass over the weights; else (longer rows) the weights are
 // read again for each digit.
 // Bound: launch, and three rounds of counting, a barrier and a scan.  Measured: 64 sequences of up to 2,048
-// positions, 4 heads: 7.8 us; 8 of 32K to 128K, 8 heads: 39.6 us (512 CTAs of which 304 run at once; 58 us
-// with the weights read again for each digit and twice the CTAs).
+// positions, 4 heads: 7.8 us (in rows of 131,072: 53, clusters of eight for what one CTA could do); 8 of 32K to 128K, 8
+// heads: 39.6 us (512 CTAs of which 304 run at once; 58 us with the weights read again for each digit and
+// twice the CTAs).  All weights equal: 7.9 and 35.7 us; all within a fifth of each other 7.8 and 46.2.
 template <bool kStored>
 __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectParams p, int ctas) {
   extern __shared__ uint32_t ranks[];                        // [warp][run]
@@ -438,7 +439,13 @@ pkv_status pkv_evict_select(int32_t* kept, int max_keep, const float* weights, i
   if (!err) return PKV_ERR_CUDA;
   SelectParams prm = {kept, weights, rows, context_lens, keep_lens, max_keep, num_rows, max_len, num_kv_heads, first, recent, err};
   // One CTA for up to 4096 positions, then up to eight, then more positions for each as far as two CTAs of an SM have
-  // shared memory for their ranks.
+  // shared memory for their ranks.  The positions are those of a row, not of the sequences, which the host does not know.
+  //   64 sequences x 4 heads of 4,096 positions: 9.1 us with one CTA each, 21.1 with two; 8,192: 23.7 with two, 12.4 with
+  // one; 16,384: 43.8 with four, 18.8 with one.  8 x 8 of 16,384: 13.1 with four, 16.0 with two, 18.8 with one; 65,536: 34.8
+  // with eight, 24.8 with four.  So 4,096 is right where the lists are few; many lists of 8K and more would rather have
+  // one CTA each.
+  //   Ranks stored or read again, 16,384 a CTA (8 x 8 of 131,072): 39.7 us and 73; 32,768 a CTA (262,144), where one CTA an
+  // SM would have room: 144 stored, 197 as here.
   constexpr int kFew = 4096, kMost = 16384;
   int ctas = 1;
   while (ctas < kMaxCluster && int64_t(kFew) * ctas < max_len) ctas *= 2;
@@ -504,7 +511,11 @@ pkv_status pkv_evict_compact(void* k_cache, void* v_cache, const pkv_cache_desc*
   prm.head_dim = D;
   prm.round_rows = std::min(kMoveRows, kMoveThreads * kMoveAhead / pieces);
   prm.err = err;
-  // More CTAs for a list while the lists alone do not fill the SMs and each CTA still has rows to move.
+  // More CTAs for a list while the lists alone do not fill the SMs and each CTA still has rows to move: up to half of the
+  // CTAs that can be resident for K, and as many for V.  With one CTA a list 3 x 8 lists of 8,192 e4m3 rows take 112 us in
+  // place of 27.5, 8 x 8 of 4,096 bf16 rows 127 in place of 60.5; 64 x 4 of 512 would take 24.9 in place of 27.8.  Half as
+  // many: 54.0 for the 8 x 8, 24.9 for the 64 x 4, and 28.6 in place of 32.9 for 16 x 8 of 1,024; twice as many 33.1 for
+  // the 64 x 4.
   const int64_t jobs = int64_t(num_seqs) * cache->num_kv_heads;
   int ctas = 1;
   while (ctas < kMaxCluster && 2 * jobs * ctas < int64_t(kMoveCtas) * std::max(1, num_sms()) && max_keep > ctas * prm.round_rows)
