@@ -42,8 +42,11 @@ constexpr uint32_t kTmemCols = 512;           // S_A | S_B | O_A | O_B, 128 colu
 constexpr float kRescaleThreshold = 8.f;      // log2 units
 // fp16 exponentials are taken relative to 2^-kHeadroom of the running maximum: up to 2^15, so that their least step, 2^-24,
 // is 2^-31 of a row's largest or less.  (Relative to the maximum itself small weights of many keys vanished: 2^17 keys of
-// e^-18 each.)  bf16 has the exponent of fp32 and needs none.
+// e^-18 each.)  bf16 has the exponent of fp32 and needs none.  Maxima of kLargeScore and more, in log2 units, are followed
+// at once: their own rounding is not added to the threshold then, and 2^(7 + half a spacing) stays below 65504 for maxima up
+// to 2^28.
 constexpr float kHeadroom = 7.f;
+constexpr float kLargeScore = 2097152.f;
 constexpr int kItems = 8;                     // items on their way from the scheduler to the other warps
 constexpr int kItemRows = 2 * kTile;
 // Items of so few rows (a warp's) share each row's keys among four warps: 64 sequences of up to 2,048 tokens, 7 or 28 rows
@@ -186,6 +189,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr bool kWide = KV == PKV_F16 || KV == PKV_BF16;    // 16-bit caches
   constexpr bool kMmaBF16 = KV == PKV_BF16;
   constexpr float kBelow = kMmaBF16 ? 0.f : kHeadroom;
+  auto grows = [](float mt, float m) -> bool {
+    return mt > m + (kMmaBF16 || fabsf(mt) < kLargeScore ? kRescaleThreshold : 0.f);
+  };
   constexpr int kStages = C::kStages;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ __align__(16) int items[kItems][12];
@@ -481,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           ++peaks;
           const float mt = fmaxf(fmaxf(pk[0][lane], pk[1][lane]), fmaxf(pk[2][lane], pk[3][lane])) * slog - kBelow;
-          const bool grow = mt > m + kRescaleThreshold;      // (the same in all four warps)
+          const bool grow = grows(mt, m);                    // (the same in all four warps)
           const float m_prev = m;
           if (grow) m = mt;
           const float mu = m == -INFINITY ? 0.f : m;
@@ -550,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mt = fmaxf(mt, fmaxf(fmaxf(c4[0], c4[1]), fmaxf(c4[2], c4[3])));
           }
           mt = mt * slog - kBelow;                           // (slog > 0)
-          const bool grow = mt > m + kRescaleThreshold;      // also true for the first keys
+          const bool grow = grows(mt, m);                    // also true for the first keys
           const float m_prev = m;
           if (grow) m = mt;
           // P over S (keys 2e, 2e + 1 in column e).  A row without keys so far has m = -inf and every

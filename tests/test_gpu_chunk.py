@@ -293,6 +293,55 @@ def test_many_small_weights_behind_a_large_one(kind, rows):
     assert (e <= 2.0 ** -11).all()
 
 
+@pytest.mark.parametrize("kind", ["e4m3", "same"])
+@pytest.mark.parametrize("rows", [8, 40, 200])
+@pytest.mark.parametrize("first,apart,steps,alone", [(1024, 6, (2, 5, 5, 3), True), (1024, 6, (2.5, 5, 5, 3.5), True),
+                                                     (1024, 1, (2, 6, 6, 3), False), (1024, 1, (7, 5, 8, 3), False),
+                                                     (1915, 1, (8, 6, 6, 2), False)])
+def test_scores_of_many_millions_that_differ_a_little(kind, rows, first, apart, steps, alone):
+    """Scores of 12.6 to 27 million, where fp32 maxima in units of log2 are multiples of 2 or 4: no exponential may leave
+    fp16's range because of the maximum's own rounding.  (Not alone: as many chunks as SMs, so that an SM sees all of a
+    row's keys.)
+
+    fp32 holds whole numbers up to 2^24 and even ones up to 2^25, as the scores of whole and even steps are: their sums and,
+    a fused product less the maximum, the exponentials' arguments are exact.  Other steps and scores may be rounded to such a
+    number on either side, at most 2 away: a weight that is wrong by a factor of e^2 at most, |err| <= 2 (e^2 - 1) A."""
+    start, dim, n = 700, 64, 1 if alone else torch.cuda.get_device_properties(0).multi_processor_count
+    c = Case([start], [rows], 1, 1, dim, "f16", kind)
+    cc = c.cache
+    h = 32.0 if kind == "e4m3" else 1.0
+    k = np.zeros((cc.num_blocks, 1, 16, dim))
+    k[..., 0] = 12288.0 / h
+    for j, step in zip((300, 450, 460, 600), steps):           # (5 is 7.2 in units of log2)
+        k[cc.tables[0, j // 16], 0, j % 16, 1] = step / h
+    if kind == "e4m3":
+        cc.scales[0] = np.full(1, h, np.float32)
+        cc.stored[0] = torch.from_numpy(k).to(torch.float8_e4m3fn).view(torch.uint8).numpy()
+    else:
+        cc.stored[0] = torch.from_numpy(k).to(torch.float16).view(torch.int16).numpy()
+    cc.upload()
+    assert np.array_equal(cc.k, k * h)
+    c.q[:] = 0
+    c.q[:, 0, 0] = float(first) + apart * torch.arange(rows)
+    c.q[:, 0, 1] = 1.0
+    c.scale = 1.0
+    q = c.q.double().numpy()
+    ref, _, size = evict.chunk_attention(q, cc.rows("k", 0, start + rows), cc.rows("v", 0, start + rows), start, 1.0)
+    c.q, cc.tables = c.q.repeat(n, 1, 1), np.repeat(cc.tables, n, 0)
+    cc.upload()
+    c.cu, c.starts, c.total = np.arange(n + 1, dtype=np.int32) * rows, [start] * n, n * rows
+    c.dev()
+    c.call()
+    assert c.pkv.pkv_get_device_error() == 0
+    got = c.out.double().cpu().numpy().reshape(n, rows, 1, dim)
+    assert np.isfinite(got).all()
+    top = q[:, 0, 0] * 12288 + max(steps)
+    exact = (top <= 2.0 ** 24) & all(x == int(x) for x in steps) | (top <= 2.0 ** 25) & all(x % 2 == 0 for x in steps)
+    slack = np.where(exact, 2.0 ** -10, 2 * (np.exp(2) - 1))[:, None, None]
+    worst = float((np.abs(got - ref) / (slack * size + 2.0 ** -11 * np.abs(ref) + 2.0 ** -25)).max())
+    assert worst <= 1
+
+
 def test_inconsistent_lengths():
     import paged_kv_cache_160_gb300 as pkv
     for what in ("start", "past_table", "descending", "past_total", "first"):
