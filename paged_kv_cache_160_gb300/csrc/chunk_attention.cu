@@ -18,12 +18,12 @@
 // Bound: the chain of a tile, scores - softmax - products, of which two are under way.  A step takes 2,100
 // to 2,300 cycles, its products 1,170: the issuer looks at four barriers a step at 200 cycles each, and the
 // softmax of a block takes 1,800.  Measured: 8 sequences of 32K to 128K tokens, 8 rows each, 32 heads
-// over 8, D 128, 4 bits: 303 us (the bytes take 101), bf16 360 (360); four chunks of 700 to 1,024 rows
-// behind 5K to 9K keys, 32 heads over 8: 457 us over e4m3, 428 over 4 bits, 382 over bf16 (0.58 of the
+// over 8, D 128, 4 bits: 304 us (the bytes take 101), bf16 360 (360); four chunks of 700 to 1,024 rows
+// behind 5K to 9K keys, 32 heads over 8: 459 us over e4m3, 432 over 4 bits, 383 over bf16 (0.58 of the
 // measured bf16 rate); 512 rows behind 3,584, 28 heads over 4, 4 bits: 63 us; 64 sequences of up to 2,048
 // tokens, 4 rows each: 49 us; 4 of up to 37: 12 us.  (Rows read back from a quantised cache and attended as
-// plain ones take 356 us in place of 457 and 37 in place of 63, but 82 in place of 49 and 1,091 in place of
-// 303: this kernel is for few rows of many or long sequences, and where there is no room for the rows.)
+// plain ones take 358 us in place of 459 and 37 in place of 63, but 82 in place of 49 and 1,092 in place of
+// 304: this kernel is for few rows of many or long sequences, and where there is no room for the rows.)
 //   Not faster: two softmax threads a row with half the loader warps (578 us over e4m3), an issuer for each
 // chain (489), 64 scores per load from tensor memory, asking L2 for tiles a window ahead.  What made the
 // first form three times faster, on the 8 long sequences: no loads in flight spilled (959 us -> 491), rolled
